@@ -13,6 +13,11 @@ the C entry points: ``scan`` and ``scan_save`` (forward), ``scan_bwd``
 ``router_pack_weights`` (the weights in the faster kernel's layout),
 ``dict_hardmax`` (index maps from dense matrices), ``decode_step`` (one
 recurrent step), ``select`` and ``compose`` (test exports).
+
+Beside the scan (``include/pdssm_layers.h``): the gated delta rule,
+``delta_rule`` (whole sequences), ``delta_rule_bwd`` (gradients) and
+``delta_step`` (one step), and the norm of queries and keys with the rotation
+by position, ``qk_norm_rope`` and ``qk_norm_rope_bwd``.
 """
 from __future__ import annotations
 
@@ -27,6 +32,7 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIBRARY = os.path.join(HERE, "libpdssm.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "pdssm.h")
+LAYERS_HEADER = os.path.join(os.path.dirname(HERE), "include", "pdssm_layers.h")
 
 # Flag and status values of include/pdssm.h (tests check they agree).
 PDSSM_SEL_I32 = 0x0
@@ -40,6 +46,11 @@ PDSSM_Y_BF16 = 0x10
 PDSSM_DETERMINISTIC = 0x20
 PDSSM_FLAGS_ALL = 0x3F
 PDSSM_ROUTER_W_PACKED = 0x1
+
+# Flags of include/pdssm_layers.h.
+PDSSM_DATA_BF16 = 0x1
+PDSSM_NORM_L2 = 0x2
+PDSSM_ROPE_PAIRS = 0x4
 
 PDSSM_OK = 0
 PDSSM_ERR_NULL = -1
@@ -97,6 +108,23 @@ def _load(path: str) -> ctypes.CDLL:
     lib.pdssm_router_select.restype = ctypes.c_int
     lib.pdssm_router_pack_weights.argtypes = [P, P, I64, I32, I32, P]
     lib.pdssm_router_pack_weights.restype = ctypes.c_int
+    if path == LIBRARY:   # the test builds hold the scan alone
+        F = ctypes.c_float
+        lib.pdssm_delta_fwd.argtypes = [P] * 8 + [I64] * 4 + [I32, I32, F, U32, P, P, SZ, P]
+        lib.pdssm_delta_fwd.restype = ctypes.c_int
+        lib.pdssm_delta_bwd.argtypes = [P] * 14 + [I64] * 4 + [I32, I32, F, U32, P, P, SZ, P]
+        lib.pdssm_delta_bwd.restype = ctypes.c_int
+        lib.pdssm_delta_step.argtypes = [P] * 8 + [I64] * 3 + [I32, I32, F, U32, P, P]
+        lib.pdssm_delta_step.restype = ctypes.c_int
+        for size in (lib.pdssm_delta_workspace_bytes, lib.pdssm_delta_bwd_workspace_bytes):
+            size.argtypes = [I64] * 4 + [I32, I32, U32]
+            size.restype = SZ
+        lib.pdssm_qk_norm_rope_fwd.argtypes = [P] * 9 + [I64] * 4 + [I32, I32, I64, F, U32, P, P]
+        lib.pdssm_qk_norm_rope_fwd.restype = ctypes.c_int
+        lib.pdssm_qk_norm_rope_bwd.argtypes = [P] * 13 + [I64] * 4 + [I32, I32, I64, F, U32, P, P, SZ, P]
+        lib.pdssm_qk_norm_rope_bwd.restype = ctypes.c_int
+        lib.pdssm_qk_norm_rope_bwd_workspace_bytes.argtypes = [I64] * 4 + [I32]
+        lib.pdssm_qk_norm_rope_bwd_workspace_bytes.restype = SZ
     return lib
 
 
@@ -126,9 +154,9 @@ def variant(name: str):
         _LIB = saved
 
 
-def header_functions() -> list:
-    """Names of the functions include/pdssm.h declares."""
-    text = open(HEADER).read()
+def header_functions(header: str = HEADER) -> list:
+    """Names of the functions a header (include/pdssm.h by default) declares."""
+    text = open(header).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return re.findall(r"\b(pdssm_[a-z_]+)\s*\(", text)
 
@@ -448,3 +476,285 @@ def router_select(u: torch.Tensor, w, *, out: Optional[torch.Tensor] = None,
         out = torch.empty((B, H, L), dtype=torch.int16, device=u.device)
     check(pdssm_router_select(u, wt, out, B, L, H, K, D, flags, stream))
     return out
+
+
+# ---------------------------------------------------------------------------
+# Operators beside the scan (include/pdssm_layers.h)
+# ---------------------------------------------------------------------------
+
+class _Strides(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("l", ctypes.c_int64)]
+
+
+def _strides(strides):
+    """The pdssm_strides list of (b, h, l) triples, or None (contiguous)."""
+    if strides is None:
+        return None
+    return (_Strides * len(strides))(*strides)
+
+
+def pdssm_delta_fwd(q, k, v, g, beta, s0, o, s_final, B, Hk, Hv, L, Dk, Dv, scale, flags, strides,
+                    workspace, workspace_bytes, stream=None) -> int:
+    return library().pdssm_delta_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(s0), _ptr(o),
+                                     _ptr(s_final), B, Hk, Hv, L, Dk, Dv, scale, flags,
+                                     _strides(strides), _ptr(workspace), workspace_bytes,
+                                     _stream(stream))
+
+
+def pdssm_delta_workspace_bytes(B, Hk, Hv, L, Dk, Dv, flags) -> int:
+    return library().pdssm_delta_workspace_bytes(B, Hk, Hv, L, Dk, Dv, flags)
+
+
+def pdssm_delta_bwd(q, k, v, g, beta, s0, d_o, ds_final, dq, dk, dv, dg, dbeta, ds0, B, Hk, Hv, L,
+                    Dk, Dv, scale, flags, strides, workspace, workspace_bytes, stream=None) -> int:
+    return library().pdssm_delta_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(s0),
+                                     _ptr(d_o), _ptr(ds_final), _ptr(dq), _ptr(dk), _ptr(dv),
+                                     _ptr(dg), _ptr(dbeta), _ptr(ds0), B, Hk, Hv, L, Dk, Dv, scale,
+                                     flags, _strides(strides), _ptr(workspace), workspace_bytes,
+                                     _stream(stream))
+
+
+def pdssm_delta_bwd_workspace_bytes(B, Hk, Hv, L, Dk, Dv, flags) -> int:
+    return library().pdssm_delta_bwd_workspace_bytes(B, Hk, Hv, L, Dk, Dv, flags)
+
+
+def pdssm_delta_step(q, k, v, g, beta, s, o, s_out, B, Hk, Hv, Dk, Dv, scale, flags, strides,
+                     stream=None) -> int:
+    return library().pdssm_delta_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(s),
+                                      _ptr(o), _ptr(s_out), B, Hk, Hv, Dk, Dv, scale, flags,
+                                      _strides(strides), _stream(stream))
+
+
+def pdssm_qk_norm_rope_fwd(q, k, wq, wk, cos, sin, pos, q_out, k_out, B, Hq, Hk, L, D, R, P, eps,
+                           flags, strides, stream=None) -> int:
+    return library().pdssm_qk_norm_rope_fwd(_ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(cos),
+                                            _ptr(sin), _ptr(pos), _ptr(q_out), _ptr(k_out), B, Hq,
+                                            Hk, L, D, R, P, eps, flags, _strides(strides),
+                                            _stream(stream))
+
+
+def pdssm_qk_norm_rope_bwd(q, k, wq, wk, cos, sin, pos, dq_out, dk_out, dq, dk, dwq, dwk, B, Hq, Hk,
+                           L, D, R, P, eps, flags, strides, workspace, workspace_bytes,
+                           stream=None) -> int:
+    return library().pdssm_qk_norm_rope_bwd(_ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(cos),
+                                            _ptr(sin), _ptr(pos), _ptr(dq_out), _ptr(dk_out),
+                                            _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk), B, Hq, Hk, L,
+                                            D, R, P, eps, flags, _strides(strides),
+                                            _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def pdssm_qk_norm_rope_bwd_workspace_bytes(B, Hq, Hk, L, D) -> int:
+    return library().pdssm_qk_norm_rope_bwd_workspace_bytes(B, Hq, Hk, L, D)
+
+
+def _data_flag(name: str, *tensors) -> int:
+    """The storage flag of tensors that must share one type, bf16 or fp32."""
+    dtype = tensors[0].dtype
+    if dtype not in (torch.bfloat16, torch.float32) or any(t.dtype != dtype for t in tensors):
+        raise ValueError(f"{name} must share one type, bf16 or fp32")
+    return PDSSM_DATA_BF16 if dtype == torch.bfloat16 else 0
+
+
+def _f32(name: str, t, shape) -> None:
+    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be fp32 {list(shape)}")
+
+
+def _state(name: str, t, shape) -> None:
+    _f32(name, t, shape)
+    if t is not None and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _shape(name: str, t, shape, dtype) -> None:
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} {list(shape)}")
+
+
+def _rows(*tensors):
+    """(b, h, l) strides of [B,H,L(,D)] tensors; D must be contiguous."""
+    out = []
+    for t in tensors:
+        s = t.stride()
+        if len(s) == 4 and s[3] != 1 and t.shape[3] > 1:
+            raise ValueError("the last dimension must be contiguous")
+        out.append(s[:3])
+    return out
+
+
+def _delta_sizes(q, k, v, g, beta):
+    flag = _data_flag("q, k and v", q, k, v)
+    B, Hk, L, Dk = q.shape
+    Hv, Dv = v.shape[1], v.shape[3]
+    if k.shape != q.shape or v.shape[0] != B or v.shape[2] != L:
+        raise ValueError("q and k must be [B,Hk,L,Dk] and v [B,Hv,L,Dv]")
+    _f32("g", g, (B, Hv, L))
+    _f32("beta", beta, (B, Hv, L))
+    return flag, B, Hk, Hv, L, Dk, Dv
+
+
+def _workspace(need: int, workspace, device):
+    if need == 0:
+        raise PdssmError(PDSSM_ERR_DIM, "invalid sizes")
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace
+
+
+def delta_rule(q, k, v, g, beta, s0=None, *, scale: Optional[float] = None, want_state: bool = True,
+               o: Optional[torch.Tensor] = None, s_final: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, stream=None):
+    """The gated delta rule over whole sequences: (o [B,Hv,L,Dv], s_final
+    [B,Hv,Dk,Dv] or None).  q, k [B,Hk,L,Dk] and v [B,Hv,L,Dv] bf16 or fp32
+    with any strides of the first three dimensions, g (log decay) and beta
+    fp32 [B,Hv,L], s0 fp32 [B,Hv,Dk,Dv] or None; scale 1/sqrt(Dk) by default.
+    s_final may be s0."""
+    flag, B, Hk, Hv, L, Dk, Dv = _delta_sizes(q, k, v, g, beta)
+    _state("s0", s0, (B, Hv, Dk, Dv))
+    if o is None:
+        o = torch.empty((B, Hv, L, Dv), dtype=v.dtype, device=v.device)
+    else:
+        _shape("o", o, (B, Hv, L, Dv), v.dtype)
+    if s_final is not None:
+        _state("s_final", s_final, (B, Hv, Dk, Dv))
+    elif want_state:
+        s_final = torch.empty((B, Hv, Dk, Dv), dtype=torch.float32, device=v.device)
+    workspace = _workspace(pdssm_delta_workspace_bytes(B, Hk, Hv, L, Dk, Dv, flag), workspace, v.device)
+    check(pdssm_delta_fwd(q, k, v, g, beta, s0, o, s_final, B, Hk, Hv, L, Dk, Dv,
+                          Dk ** -0.5 if scale is None else scale, flag, _rows(q, k, v, g, beta, o),
+                          workspace, workspace.numel(), stream))
+    return o, s_final
+
+
+def delta_rule_bwd(q, k, v, g, beta, do, s0=None, ds_final=None, *, scale: Optional[float] = None,
+                   want_ds0: bool = True, out=None, workspace: Optional[torch.Tensor] = None,
+                   stream=None):
+    """Gradients of delta_rule from its inputs, the gradient ``do`` of o and
+    that of s_final (None: zero): (dq, dk, dv, dg, dbeta, ds0 or None).
+    ``out`` may hold a previous call's result to write into."""
+    flag, B, Hk, Hv, L, Dk, Dv = _delta_sizes(q, k, v, g, beta)
+    _state("s0", s0, (B, Hv, Dk, Dv))
+    _state("ds_final", ds_final, (B, Hv, Dk, Dv))
+    _shape("do", do, v.shape, v.dtype)
+    if out is not None:
+        dq, dk, dv, dg, dbeta, ds0 = out
+        for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v), ("dg", dg, g), ("dbeta", dbeta, g)):
+            _shape(name, t, like.shape, like.dtype)
+        _state("ds0", ds0, (B, Hv, Dk, Dv))
+    else:
+        dq, dk, dv, dg, dbeta = (torch.empty(t.shape, dtype=t.dtype, device=t.device)
+                                 for t in (q, k, v, g, beta))
+        ds0 = torch.empty((B, Hv, Dk, Dv), dtype=torch.float32, device=v.device) if want_ds0 else None
+    workspace = _workspace(pdssm_delta_bwd_workspace_bytes(B, Hk, Hv, L, Dk, Dv, flag), workspace, v.device)
+    check(pdssm_delta_bwd(q, k, v, g, beta, s0, do, ds_final, dq, dk, dv, dg, dbeta, ds0, B, Hk, Hv, L,
+                          Dk, Dv, Dk ** -0.5 if scale is None else scale, flag,
+                          _rows(q, k, v, g, beta, do, dq, dk, dv, dg, dbeta), workspace,
+                          workspace.numel(), stream))
+    return dq, dk, dv, dg, dbeta, ds0
+
+
+def _head_rows(*tensors):
+    """(b, h, 0) strides of [B,H(,D)] tensors; D must be contiguous."""
+    out = []
+    for t in tensors:
+        s = t.stride()
+        if len(s) == 3 and s[2] != 1 and t.shape[2] > 1:
+            raise ValueError("the last dimension must be contiguous")
+        out.append((s[0], s[1], 0))
+    return out
+
+
+def delta_step(q, k, v, g, beta, s, *, s_out: Optional[torch.Tensor] = None,
+               scale: Optional[float] = None, o: Optional[torch.Tensor] = None, stream=None):
+    """One step of the gated delta rule: o [B,Hv,Dv] from q, k [B,Hk,Dk],
+    v [B,Hv,Dv], g, beta fp32 [B,Hv] and the state s fp32 [B,Hv,Dk,Dv], which
+    is updated in place, or into s_out."""
+    flag = _data_flag("q, k and v", q, k, v)
+    B, Hk, Dk = q.shape
+    Hv, Dv = v.shape[1], v.shape[2]
+    if k.shape != q.shape or v.shape[0] != B:
+        raise ValueError("q and k must be [B,Hk,Dk] and v [B,Hv,Dv]")
+    _f32("g", g, (B, Hv))
+    _f32("beta", beta, (B, Hv))
+    _state("s", s, (B, Hv, Dk, Dv))
+    if s_out is None:
+        s_out = s
+    else:
+        _state("s_out", s_out, (B, Hv, Dk, Dv))
+    if o is None:
+        o = torch.empty((B, Hv, Dv), dtype=v.dtype, device=v.device)
+    else:
+        _shape("o", o, (B, Hv, Dv), v.dtype)
+    check(pdssm_delta_step(q, k, v, g, beta, s, o, s_out, B, Hk, Hv, Dk, Dv,
+                           Dk ** -0.5 if scale is None else scale, flag,
+                           _head_rows(q, k, v, g, beta, o), stream))
+    return o
+
+
+_NORM_KIND = {"rms": 0, "l2": PDSSM_NORM_L2}
+_ROPE_PAIRS = {"half": 0, "adjacent": PDSSM_ROPE_PAIRS}
+
+
+def _norm_sizes(q, k, wq, wk, cos, sin, pos, kind, pairs):
+    flags = _data_flag("q and k", q, k) | _NORM_KIND[kind] | _ROPE_PAIRS[pairs]
+    B, Hq, L, D = q.shape
+    if k.shape[0] != B or k.shape[2] != L or k.shape[3] != D:
+        raise ValueError("q must be [B,Hq,L,D] and k [B,Hk,L,D]")
+    for name, w in (("wq", wq), ("wk", wk)):
+        _state(name, w, (D,))
+    P, R = (0, 0) if cos is None else (cos.shape[0], 2 * cos.shape[1])
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    _state("cos", cos, (P, R // 2))
+    _state("sin", sin, (P, R // 2))
+    if pos is not None and (pos.dtype != torch.int32 or tuple(pos.shape) != (B, L) or not pos.is_contiguous()):
+        raise ValueError("pos must be contiguous int32 [B,L]")
+    return flags, B, Hq, k.shape[1], L, D, R, P
+
+
+def qk_norm_rope(q, k, wq=None, wk=None, cos=None, sin=None, pos=None, *, kind: str = "rms",
+                 pairs: str = "half", eps: float = 1e-6, out=None, stream=None):
+    """The norm of every query and key head and the rotation of its first R
+    dimensions: (q_out [B,Hq,L,D], k_out [B,Hk,L,D]).  q [B,Hq,L,D] and k
+    [B,Hk,L,D] bf16 or fp32 with any strides of the first three dimensions;
+    weights fp32 [D] or None; cos, sin fp32 [P,R/2] or None (no rotation); pos
+    int32 [B,L] or None (the place in the sequence).  ``kind``: "rms" or "l2"
+    (unit length); ``pairs``: "half" (i, i + R/2) or "adjacent" (2i, 2i + 1).
+    ``out``: the two results to write into (the inputs, to work in place)."""
+    flags, B, Hq, Hk, L, D, R, P = _norm_sizes(q, k, wq, wk, cos, sin, pos, kind, pairs)
+    if out is None:
+        q_out = torch.empty((B, Hq, L, D), dtype=q.dtype, device=q.device)
+        k_out = torch.empty((B, Hk, L, D), dtype=k.dtype, device=k.device)
+    else:
+        q_out, k_out = out
+        _shape("q_out", q_out, q.shape, q.dtype)
+        _shape("k_out", k_out, k.shape, k.dtype)
+    check(pdssm_qk_norm_rope_fwd(q, k, wq, wk, cos, sin, pos, q_out, k_out, B, Hq, Hk, L, D, R, P, eps,
+                                 flags, _rows(q, k, q_out, k_out), stream))
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(q, k, dq_out, dk_out, wq=None, wk=None, cos=None, sin=None, pos=None, *,
+                     kind: str = "rms", pairs: str = "half", eps: float = 1e-6, out=None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of qk_norm_rope from its inputs and the gradients of its
+    outputs: (dq, dk, dwq, dwk), the last two None where the weight is.
+    ``out``: dq and dk to write into (dq_out and dk_out, to work in place)."""
+    flags, B, Hq, Hk, L, D, R, P = _norm_sizes(q, k, wq, wk, cos, sin, pos, kind, pairs)
+    _shape("dq_out", dq_out, q.shape, q.dtype)
+    _shape("dk_out", dk_out, k.shape, k.dtype)
+    if out is None:
+        dq = torch.empty((B, Hq, L, D), dtype=q.dtype, device=q.device)
+        dk = torch.empty((B, Hk, L, D), dtype=k.dtype, device=k.device)
+    else:
+        dq, dk = out
+        _shape("dq", dq, q.shape, q.dtype)
+        _shape("dk", dk, k.shape, k.dtype)
+    dwq, dwk = (None if w is None else torch.empty((D,), dtype=torch.float32, device=q.device)
+                for w in (wq, wk))
+    if wq is not None or wk is not None:
+        workspace = _workspace(pdssm_qk_norm_rope_bwd_workspace_bytes(B, Hq, Hk, L, D), workspace, q.device)
+    check(pdssm_qk_norm_rope_bwd(q, k, wq, wk, cos, sin, pos, dq_out, dk_out, dq, dk, dwq, dwk, B, Hq,
+                                 Hk, L, D, R, P, eps, flags, _rows(q, k, dq_out, dk_out, dq, dk),
+                                 workspace, 0 if workspace is None else workspace.numel(), stream))
+    return dq, dk, dwq, dwk

@@ -27,6 +27,9 @@ VARIANTS = {
 }
 SOURCES = [os.path.join(CSRC, f) for f in ("pdssm_scan.hip", "pdssm_bwd.hip", "pdssm_aux.hip",
                                             "pdssm_router.hip")]
+# Operators beside the scan (include/pdssm_layers.h): in libpdssm.so only, the
+# test builds change nothing of them.
+LAYER_SOURCES = [os.path.join(CSRC, f) for f in ("pdssm_delta.hip", "pdssm_norm.hip")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",
@@ -44,9 +47,15 @@ def variant_path(name: str) -> str:
     return os.path.join(HERE, f"libpdssm_{name}.so")
 
 
+def _command(hipcc: str, out: str, extra) -> list:
+    sources = SOURCES + (LAYER_SOURCES if out == LIBRARY else [])
+    return [hipcc, *HIPCC_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-parallel-jobs=4", "-o", out + ".tmp",
+            *sources]
+
+
 def build(out: str = LIBRARY, extra=(), verbose: bool = False) -> str:
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-    cmd = [hipcc, *HIPCC_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-o", out + ".tmp", *SOURCES]
+    cmd = _command(hipcc, out, extra)
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
@@ -60,7 +69,7 @@ def build_all(verbose: bool = False) -> None:
     jobs = [(LIBRARY, [])] + [(variant_path(k), v) for k, v in VARIANTS.items()]
     procs = []
     for out, extra in jobs:
-        cmd = [hipcc, *HIPCC_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-o", out + ".tmp", *SOURCES]
+        cmd = _command(hipcc, out, extra)
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         procs.append((out, subprocess.Popen(cmd)))

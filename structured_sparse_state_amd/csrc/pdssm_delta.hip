@@ -1,0 +1,1555 @@
+// The gated delta rule (include/pdssm_layers.h): forward, gradients, step.
+//
+// A chunk of 64 steps at once, from the state S before it.  With G the running
+// sum of g inside the chunk, rise = e^G, left = e^(G_last - G), whole =
+// e^G_last, decay[i,j] = e^(G_i - G_j) for j <= i, and
+//     N = strictly lower part of (K K^T . decay)
+//     P = scale * lower part of (Q K^T . decay)
+// the steps' u solve u = beta (V - rise K S) - beta N u.  With the unscaled
+// u~ = u / beta and Z = (I + N beta)^-1 N, which depends on keys and gates
+// only,
+//     R  = V - rise K S,    u~ = R - Z (beta R),    u = beta u~
+//     O  = scale rise Q S + P u
+//     S <- whole S + K^T (left u).
+// Gradients, from dS of the state after the chunk:
+//     dU = P^T dO + left K dS,   w = dU - Z^T (beta dU),   dV = beta w
+//     dbeta = u~ . w (row by row)
+//     dS <- whole dS + Q^T (scale rise dO) - K^T (rise dV)
+//     X = lower part of (dO u^T . decay) scale,  Y = -strictly lower (dV u^T . decay)
+//     dQ = X K + scale rise dO S^T
+//     dK = X^T Q + (Y + Y^T) K + left u dS^T - rise dV S^T
+//     dg_t = <S_after, dS_after> + sum over the chunk's s >= t of (q_s . dq_s - v_s . dv_s)
+// The last line holds because scaling every later product with the state by
+// e^g_t is the same as scaling S: the gradient of g_t is <S, dS> around it.
+//
+// Kernels: prep_kernel makes Z, P and the gates' vectors of every chunk, all
+// chunks side by side.  chain_kernel walks the chunks of a sequence; a wave
+// owns 16 columns of the state, whose recurrences are independent, and keeps
+// them in registers in the matrix cores' result layout, so states and u feed
+// the next product without leaving the wave.  In the backward chain_kernel
+// runs again to keep the states and u~, reverse_kernel walks the chunks back
+// in the same way, and grad_kernel forms what sums over the columns (dQ, dK,
+// dg, dbeta), all chunks side by side.
+#include <hip/hip_runtime.h>
+
+#include "pdssm_device.h"
+#include "pdssm_host.h"
+#include "pdssm_layers.h"
+#include "pdssm_mma.h"
+
+namespace pdssm {
+namespace {
+
+constexpr int kC = 64;          // steps of a chunk
+constexpr int kThreads = 256;
+constexpr int kMaxDim = 128;
+
+// Lower blocks of 16 x 16 of a chunk's 64 x 64 matrices: block (a,b), b <= a,
+// is number a (a + 1) / 2 + b.
+constexpr int kBlocks = 10;
+constexpr int kBlock = 256;     // values of a block
+__host__ __device__ constexpr int block_of(int a, int b) { return a * (a + 1) / 2 + b; }
+
+// What prep_kernel leaves for a chunk, in floats.  In row format a block's
+// lane (g, i) holds row i, columns 4 g + 0..3; in column format column i,
+// rows 4 g + 0..3.
+enum Vec { kRise, kLeft, kBeta, kWhole, kGhi, kGlo, kResets, kVecs };
+struct Record {
+    // forward: Z and P in row format; backward: Z in both, P in column format
+    static constexpr int kZ = 0;
+    static constexpr int kP = kBlocks * kBlock;
+    static constexpr int kVec = 2 * kBlocks * kBlock;
+    static constexpr int kZt = kVec + 8 * kC;
+    static constexpr int kFwd = kZt;
+    static constexpr int kBwd = kZt + kBlocks * kBlock;
+};
+
+struct Rows {           // rows [B,H,L,(D)] of a call
+    const void *p;
+    pdssm_strides s;
+};
+
+struct DeltaArgs {
+    Rows q, k, v, g, beta, o, d_o;   // o, d_o: what the direction has
+    Rows dq, dk, dv, dg, dbeta;
+    const float *s0;        // NULL for zero
+    float *s_final;         // NULL when not wanted
+    const float *ds_final;
+    float *ds0;
+    float *records;         // [B*Hv][NC][record]
+    float *states;          // [B*Hv][NC][DK][DV] states before the chunks (backward)
+    float *grads;           // same shape: state gradients after the chunks
+    float *ut, *w;          // [B*Hv][NC][64][DV]: u~ and w
+    int64_t heads;          // B*Hv
+    int Hk, Hv, L, NC, Dk, Dv, DV, record;
+    int slices;             // column slices of a head over workgroups
+    float scale;
+    bool vq, vk, vo;        // rows of q, of k, of d_o can be read in 16 bytes
+};
+
+// ---------------------------------------------------------------------------
+// Rows of a chunk from memory into LDS, as bf16 parts.
+// ---------------------------------------------------------------------------
+template <bool BF16>
+struct Unit;            // eight consecutive values of a row
+template <>
+struct Unit<true> {
+    uint4 v;
+};
+template <>
+struct Unit<false> {
+    f32x8 v;
+};
+
+template <bool BF16>
+__device__ __forceinline__ Unit<BF16> load_unit(const void *base, int64_t e, int col, int D, bool inside, bool vec)
+{
+    Unit<BF16> u;
+    if constexpr (BF16) {
+        u.v = make_uint4(0, 0, 0, 0);
+        const uint16_t *p = static_cast<const uint16_t *>(base) + e + col;
+        if (inside && col < D) {
+            if (vec) {
+                u.v = *reinterpret_cast<const uint4 *>(p);
+            } else {
+                uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (col + j < D)
+                        w[j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
+                u.v = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    } else {
+        const float *p = static_cast<const float *>(base) + e + col;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            u.v[j] = 0.f;
+        if (inside && col < D) {
+            if (vec) {
+                const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
+                u.v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (col + j < D)
+                        u.v[j] = p[j];
+            }
+        }
+    }
+    return u;
+}
+
+template <bool BF16>
+__device__ __forceinline__ Frag<BF16 ? 1 : 3> unit_frag(const Unit<BF16> &u)
+{
+    if constexpr (BF16) {
+        Frag<1> f;
+        __builtin_memcpy(&f.p[0], &u.v, 16);
+        return f;
+    } else {
+        return split<3>(u.v);
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ f32x8 unit_values(const Unit<BF16> &u)
+{
+    if constexpr (BF16) {
+        bf16x8 h;
+        __builtin_memcpy(&h, &u.v, 16);
+        return __builtin_convertvector(h, f32x8);
+    } else {
+        return u.v;
+    }
+}
+
+// A tile of 64 rows of KD values in LDS: NK parts, rows of KD + 8 values (the
+// padding spreads the rows over the banks).
+template <int KD, bool BF16, int NT = kThreads>
+struct Tile {
+    static constexpr int NK = BF16 ? 1 : 3;
+    static constexpr int kRow = KD + 8;
+    static constexpr int kPart = kC * kRow;
+    static constexpr int kSize = NK * kPart;                  // uint16_t
+    static constexpr int kUnits = kC * (KD / 8) / NT;         // units of a thread
+
+    Unit<BF16> u[kUnits];
+
+    // Rows t0 .. t0 + 63 of a sequence of L rows that begins at element e0.
+    __device__ __forceinline__ void load(const void *base, int64_t e0, int64_t stride, int t0, int L, int D, bool vec)
+    {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int x = threadIdx.x + i * NT, row = x / (KD / 8), col = x % (KD / 8) * 8;
+            u[i] = load_unit<BF16>(base, e0 + (t0 + row) * stride, col, D, t0 + row < L, vec);
+        }
+    }
+    __device__ __forceinline__ void store(uint16_t *lds) const
+    {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int x = threadIdx.x + i * NT, row = x / (KD / 8), col = x % (KD / 8) * 8;
+            const Frag<NK> f = unit_frag<BF16>(u[i]);
+#pragma unroll
+            for (int n = 0; n < NK; ++n)
+                *reinterpret_cast<bf16x8 *>(lds + n * kPart + row * kRow + col) = f.p[n];
+        }
+    }
+
+    // Row tile `a`, k = 32 s + 8 g + 0..7 (plain order).
+    static __device__ __forceinline__ Frag<NK> rows(const uint16_t *lds, int a, int s, int lane)
+    {
+        Frag<NK> f;
+#pragma unroll
+        for (int n = 0; n < NK; ++n)
+            f.p[n] = lds_row8(lds + n * kPart + (16 * a + (lane & 15)) * kRow + 32 * s + 8 * (lane >> 4));
+        return f;
+    }
+    // Row tile `a`, k = 32 s + (4 g + 0..3, 16 + 4 g + 0..3) (stacked order).
+    static __device__ __forceinline__ Frag<NK> rows_stacked(const uint16_t *lds, int a, int s, int lane)
+    {
+        Frag<NK> f;
+#pragma unroll
+        for (int n = 0; n < NK; ++n) {
+            const uint16_t *p = lds + n * kPart + (16 * a + (lane & 15)) * kRow + 32 * s + 4 * (lane >> 4);
+            f.p[n] = lds_rows4(p, p + 16);
+        }
+        return f;
+    }
+    // Columns 16 m + 0..15, k = rows 32 s + (4 g + 0..3, 16 + 4 g + 0..3).
+    static __device__ __forceinline__ Frag<NK> columns_stacked(const uint16_t *lds, int m, int s, int lane)
+    {
+        Frag<NK> f;
+        const int i = lane & 15, g = lane >> 4;
+#pragma unroll
+        for (int n = 0; n < NK; ++n) {
+            const uint16_t *p = lds + n * kPart + (32 * s + 4 * g + (i >> 2)) * kRow + 16 * m + 4 * (i & 3);
+            f.p[n] = lds_columns4(p, p + 16 * kRow);
+        }
+        return f;
+    }
+    // Columns 16 m + 0..15, k = rows 32 s + 8 g + 0..7.
+    static __device__ __forceinline__ Frag<NK> columns(const uint16_t *lds, int m, int s, int lane)
+    {
+        Frag<NK> f;
+        const int i = lane & 15, g = lane >> 4;
+#pragma unroll
+        for (int n = 0; n < NK; ++n) {
+            const uint16_t *p = lds + n * kPart + (32 * s + 8 * g + (i >> 2)) * kRow + 16 * m + 4 * (i & 3);
+            f.p[n] = lds_columns4(p, p + 4 * kRow);
+        }
+        return f;
+    }
+};
+
+// e^(G_i - G_j), G as a pair of floats, zero across a step that empties the state.
+__device__ __forceinline__ float decay_of(float hi_i, float lo_i, float n_i, float hi_j, float lo_j, float n_j)
+{
+    return n_i == n_j ? expf((hi_i - hi_j) + (lo_i - lo_j)) : 0.f;
+}
+
+__device__ __forceinline__ int64_t kv_head(const DeltaArgs &a, int64_t head, int64_t &b, int &h)
+{
+    b = head / a.Hv;
+    h = (int)(head - b * a.Hv);
+    return h / (a.Hv / a.Hk);
+}
+
+// ---------------------------------------------------------------------------
+// prep_kernel: Z, P and the gates' vectors of one chunk of one value head.
+// Wave a forms row tile a of N and P (bf16 products are exact, fp32 data goes
+// in three parts).  Z = N - N beta Z by forward substitution over 16 x 16
+// blocks: the diagonal blocks row by row with a column in each lane, the
+// others by fp32 matrix instructions, a block column in each wave.
+// ---------------------------------------------------------------------------
+constexpr int kMat = 68;        // row of a 64 x 64 fp32 matrix in LDS
+
+template <int KD, bool BF16, bool BWD>
+__global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
+{
+    using T = Tile<KD, BF16>;
+    constexpr int kQArea = T::kSize * 2 > kC * kMat * 4 ? T::kSize * 2 : kC * kMat * 4;
+    __shared__ __attribute__((aligned(16))) char s_mem[T::kSize * 2 + kQArea + kC * kMat * 4];
+    __shared__ float s_hi[kC], s_lo[kC], s_n[kC], s_beta[kC];
+    uint16_t *s_k = reinterpret_cast<uint16_t *>(s_mem);
+    uint16_t *s_q = reinterpret_cast<uint16_t *>(s_mem + T::kSize * 2);
+    float *s_z = reinterpret_cast<float *>(s_mem + T::kSize * 2);     // after P, in the place of q
+    float *s_N = reinterpret_cast<float *>(s_mem + T::kSize * 2 + kQArea);
+
+    const int64_t head = blockIdx.x / (unsigned)a.NC;
+    const int c = blockIdx.x % (unsigned)a.NC;
+    int64_t b;
+    int h;
+    const int64_t hk = kv_head(a, head, b, h);
+    const int t0 = c * kC, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int g = lane >> 4, i16 = lane & 15;
+    float *rec = a.records + (int64_t)blockIdx.x * a.record;
+
+    {
+        T q, k;
+        k.load(a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk, a.vk);
+        q.load(a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk, a.vq);
+        if (wave == 0) {
+            // G in 64 bits (differences of neighbours stay exact to 32), steps
+            // with g = -inf counted apart.
+            const int t = t0 + lane;
+            float gate = 0.f, bt = 0.f;
+            if (t < a.L) {
+                gate = static_cast<const float *>(a.g.p)[b * a.g.s.b + h * a.g.s.h + t * a.g.s.l];
+                bt = static_cast<const float *>(a.beta.p)[b * a.beta.s.b + h * a.beta.s.h + t * a.beta.s.l];
+            }
+            const bool empty = gate == -__builtin_inff();
+            double G = empty ? 0.0 : (double)gate;
+            float n = empty ? 1.f : 0.f;
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                const double x = __shfl_up(G, m, 64);
+                const float y = __shfl_up(n, m, 64);
+                if (lane >= m) {
+                    G += x;
+                    n += y;
+                }
+            }
+            const float hi = (float)G, lo = (float)(G - (double)hi);
+            const float hi1 = __shfl(hi, 63, 64), lo1 = __shfl(lo, 63, 64), n1 = __shfl(n, 63, 64);
+            s_hi[lane] = hi;
+            s_lo[lane] = lo;
+            s_n[lane] = n;
+            s_beta[lane] = bt;
+            float *vec = rec + Record::kVec;
+            vec[kRise * kC + lane] = n == 0.f ? expf(hi + lo) : 0.f;
+            vec[kLeft * kC + lane] = decay_of(hi1, lo1, n1, hi, lo, n);
+            vec[kBeta * kC + lane] = bt;
+            vec[kWhole * kC + lane] = n1 == 0.f ? expf(hi1 + lo1) : 0.f;
+            vec[kGhi * kC + lane] = hi;
+            vec[kGlo * kC + lane] = lo;
+            vec[kResets * kC + lane] = n;
+        }
+        k.store(s_k);
+        q.store(s_q);
+    }
+    __syncthreads();
+
+    // Row tile `wave` of N and P, results as rows i = lane % 16 (columns in
+    // the registers), P in column format for the backward.
+    {
+        Frag<T::NK> ka[KD / 32], qa[KD / 32];
+#pragma unroll
+        for (int s = 0; s < KD / 32; ++s) {
+            ka[s] = T::rows(s_k, wave, s, lane);
+            qa[s] = T::rows(s_q, wave, s, lane);
+        }
+        const int row = 16 * wave + i16;
+        const float hi = s_hi[row], lo = s_lo[row], n = s_n[row];
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+            if (tb > wave) {
+                *reinterpret_cast<f32x4 *>(s_N + row * kMat + 16 * tb + 4 * g) = f32x4{0.f, 0.f, 0.f, 0.f};
+                continue;
+            }
+            f32x4 kk = {0.f, 0.f, 0.f, 0.f}, qk = kk;
+#pragma unroll
+            for (int s = 0; s < KD / 32; ++s) {
+                const Frag<T::NK> kb = T::rows(s_k, tb, s, lane);
+                kk = mma<3>(kb, ka[s], kk);
+                qk = BWD ? mma<3>(qa[s], kb, qk) : mma<3>(kb, qa[s], qk);
+            }
+            f32x4 nn, pp;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int col = 16 * tb + 4 * g + r;
+                const float d = decay_of(hi, lo, n, s_hi[col], s_lo[col], s_n[col]);
+                nn[r] = col < row ? kk[r] * d : 0.f;
+                if constexpr (BWD) {
+                    const int pi = 16 * wave + 4 * g + r, pj = 16 * tb + i16;
+                    const float e = decay_of(s_hi[pi], s_lo[pi], s_n[pi], s_hi[pj], s_lo[pj], s_n[pj]);
+                    pp[r] = pj <= pi ? a.scale * qk[r] * e : 0.f;
+                } else {
+                    pp[r] = col <= row ? a.scale * qk[r] * d : 0.f;
+                }
+            }
+            *reinterpret_cast<f32x4 *>(s_N + row * kMat + 16 * tb + 4 * g) = nn;
+            *reinterpret_cast<f32x4 *>(rec + Record::kP + block_of(wave, tb) * kBlock + 4 * lane) = pp;
+        }
+    }
+    __syncthreads();    // N whole; q's place is free for Z
+
+    // Diagonal block `wave`: lane's column of Z row by row.
+    {
+        const float *N = s_N + 16 * wave * kMat + 16 * wave;
+        float y[16], z[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float v = N[i * kMat + i16];
+#pragma unroll
+            for (int m = 0; m < i; m += 4) {
+                const f32x4 row = *reinterpret_cast<const f32x4 *>(N + i * kMat + m);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (m + r < i)
+                        v -= row[r] * y[m + r];
+            }
+            z[i] = v;
+            y[i] = v * s_beta[16 * wave + i];
+        }
+        if (g == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                s_z[(16 * wave + i) * kMat + 16 * wave + i16] = z[i];
+        }
+    }
+    __syncthreads();
+
+    // Block column `wave` below the diagonal: Z_aj = X - Z_aa beta X with
+    // X = N_aj - sum over m of N_am (beta Z)_mj.
+    {
+        f32x4 y[4];
+        f32x4 beta[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            beta[m] = *reinterpret_cast<const f32x4 *>(s_beta + 16 * m + 4 * g);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                y[m][r] = m == wave ? s_z[(16 * m + 4 * g + r) * kMat + 16 * m + i16] * beta[m][r] : 0.f;
+        }
+#pragma unroll
+        for (int ta = 1; ta < 4; ++ta) {
+            if (ta <= wave)
+                continue;
+            f32x4 x;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                x[r] = s_N[(16 * ta + 4 * g + r) * kMat + 16 * wave + i16];
+#pragma unroll
+            for (int m = 0; m < ta; ++m)
+                if (m >= wave)
+                    x = mma_f32(-*reinterpret_cast<const f32x4 *>(s_N + (16 * ta + i16) * kMat + 16 * m + 4 * g), y[m], x);
+            const f32x4 zd = *reinterpret_cast<const f32x4 *>(s_z + (16 * ta + i16) * kMat + 16 * ta + 4 * g);
+            x = mma_f32(-zd, x * beta[ta], x);
+            y[ta] = x * beta[ta];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                s_z[(16 * ta + 4 * g + r) * kMat + 16 * wave + i16] = x[r];
+        }
+    }
+    __syncthreads();
+
+    // Z out: row format, and column format for the backward.
+    for (int t = wave; t < kBlocks; t += kThreads / 64) {
+        const int ta = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, tb = t - ta * (ta + 1) / 2;
+        *reinterpret_cast<f32x4 *>(rec + Record::kZ + t * kBlock + 4 * lane) =
+            *reinterpret_cast<const f32x4 *>(s_z + (16 * ta + i16) * kMat + 16 * tb + 4 * g);
+        if constexpr (BWD) {
+            f32x4 v;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                v[r] = s_z[(16 * ta + 4 * g + r) * kMat + 16 * tb + i16];
+            *reinterpret_cast<f32x4 *>(rec + Record::kZt + t * kBlock + 4 * lane) = v;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// A chunk's lower triangular matrix (or its transpose) in LDS as A operands in
+// stacked order: fragment f of row tile a and k step s, part n, at
+// ((f * 3 + n) * 64 + lane) * 8 values.  Six fragments hold the triangle; the
+// halves of them that it leaves out are zero.
+// ---------------------------------------------------------------------------
+template <bool TRANS>
+struct Tri {
+    static constexpr int kFrags = 6;
+    static constexpr int kSize = kFrags * 3 * 64 * 8;    // uint16_t
+    static constexpr int kUnits = (kBlocks * 64 + kThreads - 1) / kThreads;
+    f32x4 u[kUnits];
+
+    // Row tile a of the matrix has k step s (of the transpose: from a / 2 on).
+    static __host__ __device__ constexpr bool has(int a, int s) { return TRANS ? s >= a / 2 : s <= a / 2; }
+    static __host__ __device__ constexpr int frag(int a, int s) { return TRANS ? (a < 2 ? 2 * a + s : a + 2) : (a < 2 ? a : 2 * a - 2 + s); }
+
+    // blocks: row format, or column format for the transpose.
+    __device__ __forceinline__ void load(const float *blocks)
+    {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int x = threadIdx.x + i * kThreads;
+            if (x < kBlocks * 64)
+                u[i] = *reinterpret_cast<const f32x4 *>(blocks + 4 * x);
+        }
+    }
+    __device__ __forceinline__ void store(uint16_t *lds) const
+    {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int x = threadIdx.x + i * kThreads;
+            if (x < kBlocks * 64) {
+                const int t = x >> 6, lane = x & 63;
+                const int ta = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, tb = t - ta * (ta + 1) / 2;
+                const int row = TRANS ? tb : ta, col = TRANS ? ta : tb;
+                uint16_t *p = lds + ((frag(row, col >> 1) * 3) * 64 + lane) * 8 + 4 * (col & 1);
+                f32x4 v = u[i];
+#pragma unroll
+                for (int n = 0; n < 3; ++n) {
+                    const bf16x4 h = __builtin_convertvector(v, bf16x4);
+                    *reinterpret_cast<bf16x4 *>(p + n * 512) = h;
+                    v -= __builtin_convertvector(h, f32x4);
+                }
+            }
+        }
+    }
+    // The halves that no block fills.
+    static __device__ __forceinline__ void clear(uint16_t *lds)
+    {
+        for (int x = threadIdx.x; x < 2 * 3 * 64; x += kThreads) {
+            const int f = TRANS ? (x < 192 ? frag(1, 0) : frag(3, 1)) : (x < 192 ? frag(0, 0) : frag(2, 1));
+            const int half = TRANS ? 0 : 1;
+            *reinterpret_cast<uint2 *>(lds + (f * 192 + x % 192) * 8 + 4 * half) = make_uint2(0, 0);
+        }
+    }
+    template <int N>
+    static __device__ __forceinline__ Frag<N> get(const uint16_t *lds, int a, int s, int lane)
+    {
+        Frag<N> f;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            f.p[n] = lds_row8(lds + ((frag(a, s) * 3 + n) * 64 + lane) * 8);
+        return f;
+    }
+};
+
+// A wave's 16 columns of the 64 rows of a chunk in the C layout (lane: column
+// lane % 16, rows 16 a + 4 g + r).
+template <bool BF16>
+struct Cols {
+    uint32_t raw[4][4];
+
+    __device__ __forceinline__ void load(const void *base, int64_t e0, int64_t stride, int t0, int L, int col, int D,
+                                         int lane)
+    {
+        const int g = lane >> 4;
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = t0 + 16 * a + 4 * g + r;
+                raw[a][r] = 0;
+                if (t < L && col < D) {
+                    const int64_t e = e0 + t * stride + col;
+                    if constexpr (BF16)
+                        raw[a][r] = static_cast<const uint16_t *>(base)[e];
+                    else
+                        raw[a][r] = static_cast<const uint32_t *>(base)[e];
+                }
+            }
+    }
+    __device__ __forceinline__ f32x4 get(int a) const
+    {
+        f32x4 v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            v[r] = BF16 ? bf16_lo(raw[a][r]) : __uint_as_float(raw[a][r]);
+        return v;
+    }
+};
+
+template <bool BF16>
+__device__ __forceinline__ void store_cols(void *base, int64_t e0, int64_t stride, int t0, int L, int col, int D,
+                                           int lane, int a, f32x4 v)
+{
+    const int g = lane >> 4;
+    if (col >= D)
+        return;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int t = t0 + 16 * a + 4 * g + r;
+        if (t < L) {
+            const int64_t e = e0 + t * stride + col;
+            if constexpr (BF16)
+                static_cast<uint16_t *>(base)[e] = f32_to_bf16_rne(v[r]);
+            else
+                static_cast<float *>(base)[e] = v[r];
+        }
+    }
+}
+
+// A state (or its gradient): KD / 16 tiles in the C layout.
+template <int KD>
+struct State {
+    f32x4 s[KD / 16];
+
+    // [Dk][Dv] values from memory; NULL: zero.
+    __device__ __forceinline__ void load(const float *p, int Dk, int Dv, int col, int lane)
+    {
+#pragma unroll
+        for (int m = 0; m < KD / 16; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * m + 4 * (lane >> 4) + r;
+                s[m][r] = (p && row < Dk && col < Dv) ? p[(int64_t)row * Dv + col] : 0.f;
+            }
+    }
+    __device__ __forceinline__ void store(float *p, int Dk, int Dv, int col, int lane) const
+    {
+#pragma unroll
+        for (int m = 0; m < KD / 16; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * m + 4 * (lane >> 4) + r;
+                if (row < Dk && col < Dv)
+                    p[(int64_t)row * Dv + col] = s[m][r];
+            }
+    }
+};
+
+// Four vectors of the record in LDS (rise, left, beta, whole).
+__device__ __forceinline__ f32x4 load_vecs(const float *vec)
+{
+    return threadIdx.x < kC ? *reinterpret_cast<const f32x4 *>(vec + 4 * threadIdx.x) : f32x4{0.f, 0.f, 0.f, 0.f};
+}
+__device__ __forceinline__ f32x4 row_vec(const float *s_vec, int which, int a, int lane)
+{
+    return *reinterpret_cast<const f32x4 *>(s_vec + which * kC + 16 * a + 4 * (lane >> 4));
+}
+
+// ---------------------------------------------------------------------------
+// chain_kernel: the chunks of a head in order.  KEEP: the backward's pass,
+// which keeps the states before the chunks and u~ and forms no outputs.
+// ---------------------------------------------------------------------------
+template <int KD, bool BF16, bool KEEP>
+__global__ void __launch_bounds__(kThreads) chain_kernel(DeltaArgs a)
+{
+    using T = Tile<KD, BF16>;
+    using L_ = Tri<false>;
+    // Parts and order of products that end in an output only: 16 bits are
+    // enough for one that is rounded to 8 (they add 2^-17 to its 2^-9).
+    constexpr int NO = BF16 ? 2 : 3;
+    extern __shared__ __attribute__((aligned(16))) char s_dyn[];
+    uint16_t *s_k = reinterpret_cast<uint16_t *>(s_dyn);
+    uint16_t *s_z = s_k + T::kSize;
+    float *s_vec = reinterpret_cast<float *>(s_z + L_::kSize);
+    uint16_t *s_q = reinterpret_cast<uint16_t *>(s_vec + 4 * kC);     // with outputs only
+    uint16_t *s_p = s_q + T::kSize;
+
+    const int64_t head = blockIdx.x / (unsigned)a.slices;
+    const int slice = blockIdx.x % (unsigned)a.slices;
+    int64_t b;
+    int h;
+    const int64_t hk = kv_head(a, head, b, h);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int col = (slice * (kThreads / 64) + wave) * 16 + (lane & 15);
+    const int64_t ek = b * a.k.s.b + hk * a.k.s.h, eq = b * a.q.s.b + hk * a.q.s.h, ev = b * a.v.s.b + h * a.v.s.h;
+    const float *rec = a.records + head * a.NC * (int64_t)a.record;
+
+    T tk, tq;
+    L_ tz, tp;
+    Cols<BF16> v;
+    f32x4 tv;
+    auto fetch = [&](int c) {
+        const float *r = rec + (int64_t)c * a.record;
+        tk.load(a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk, a.vk);
+        tz.load(r + Record::kZ);
+        tv = load_vecs(r + Record::kVec);
+        v.load(a.v.p, ev, a.v.s.l, c * kC, a.L, col, a.Dv, lane);
+        if constexpr (!KEEP) {
+            tq.load(a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk, a.vq);
+            tp.load(r + Record::kP);
+        }
+    };
+    State<KD> S;
+    S.load(a.s0 ? a.s0 + head * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, col, lane);
+    L_::clear(s_z);
+    if constexpr (!KEEP)
+        L_::clear(s_p);
+    fetch(0);
+    for (int c = 0; c < a.NC; ++c) {
+        tk.store(s_k);
+        tz.store(s_z);
+        if (threadIdx.x < kC)
+            *reinterpret_cast<f32x4 *>(s_vec + 4 * threadIdx.x) = tv;
+        if constexpr (!KEEP) {
+            tq.store(s_q);
+            tp.store(s_p);
+        }
+        f32x4 R[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            R[t] = v.get(t);
+        __syncthreads();
+        if (c + 1 < a.NC)
+            fetch(c + 1);
+
+        if constexpr (KEEP) {
+            S.store(a.states + (head * a.NC + c) * KD * a.DV, KD, a.DV, col, lane);
+        }
+        f32x4 ks[4], qs[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            ks[t] = qs[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < KD / 32; ++s) {
+            const Frag<3> f = split<3>(S.s[2 * s], S.s[2 * s + 1]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                ks[t] = mma<3>(T::rows_stacked(s_k, t, s, lane), f, ks[t]);
+                if constexpr (!KEEP)
+                    qs[t] = mma<NO>(T::rows_stacked(s_q, t, s, lane), f, qs[t]);
+            }
+        }
+        f32x4 x[4], u[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            R[t] -= row_vec(s_vec, kRise, t, lane) * ks[t];
+            x[t] = row_vec(s_vec, kBeta, t, lane) * R[t];
+            u[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const Frag<3> f = split<3>(x[2 * s], x[2 * s + 1]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                if (L_::has(t, s))
+                    u[t] = mma<3>(L_::template get<3>(s_z, t, s, lane), f, u[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            u[t] = R[t] - u[t];      // u~
+            if constexpr (KEEP) {
+                if (col < a.DV) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        a.ut[((head * a.NC + c) * kC + 16 * t + 4 * (lane >> 4) + r) * a.DV + col] = u[t][r];
+                }
+            }
+            u[t] *= row_vec(s_vec, kBeta, t, lane);
+        }
+        if constexpr (!KEEP) {
+            f32x4 o[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                o[t] = a.scale * row_vec(s_vec, kRise, t, lane) * qs[t];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const Frag<NO> f = split<NO>(u[2 * s], u[2 * s + 1]);
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    if (L_::has(t, s))
+                        o[t] = mma<NO>(L_::template get<NO>(s_p, t, s, lane), f, o[t]);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                store_cols<BF16>(const_cast<void *>(a.o.p), b * a.o.s.b + h * a.o.s.h, a.o.s.l, c * kC, a.L, col, a.Dv,
+                                 lane, t, o[t]);
+        }
+        const float whole = s_vec[kWhole * kC];
+#pragma unroll
+        for (int m = 0; m < KD / 16; ++m)
+            S.s[m] *= whole;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const Frag<3> f = split<3>(row_vec(s_vec, kLeft, 2 * s, lane) * u[2 * s],
+                                       row_vec(s_vec, kLeft, 2 * s + 1, lane) * u[2 * s + 1]);
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m)
+                S.s[m] = mma<3>(T::columns_stacked(s_k, m, s, lane), f, S.s[m]);
+        }
+        __syncthreads();
+    }
+    if (!KEEP && a.s_final)
+        S.store(a.s_final + head * a.Dk * a.Dv, a.Dk, a.Dv, col, lane);
+}
+
+// ---------------------------------------------------------------------------
+// reverse_kernel: the chunks of a head from the last to the first, with the
+// gradient of the state in registers.  Writes dV, keeps w and the gradients
+// of the states after the chunks.
+// ---------------------------------------------------------------------------
+template <int KD, bool BF16>
+__global__ void __launch_bounds__(kThreads) reverse_kernel(DeltaArgs a)
+{
+    using T = Tile<KD, BF16>;
+    using U_ = Tri<true>;
+    constexpr int NK = T::NK;
+    extern __shared__ __attribute__((aligned(16))) char s_dyn[];
+    uint16_t *s_k = reinterpret_cast<uint16_t *>(s_dyn);
+    uint16_t *s_z = s_k + T::kSize;
+    float *s_vec = reinterpret_cast<float *>(s_z + U_::kSize);
+    uint16_t *s_q = reinterpret_cast<uint16_t *>(s_vec + 4 * kC);
+    uint16_t *s_p = s_q + T::kSize;
+
+    const int64_t head = blockIdx.x / (unsigned)a.slices;
+    const int slice = blockIdx.x % (unsigned)a.slices;
+    int64_t b;
+    int h;
+    const int64_t hk = kv_head(a, head, b, h);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int col = (slice * (kThreads / 64) + wave) * 16 + (lane & 15);
+    const int64_t ek = b * a.k.s.b + hk * a.k.s.h, eq = b * a.q.s.b + hk * a.q.s.h;
+    const int64_t eo = b * a.d_o.s.b + h * a.d_o.s.h, ev = b * a.dv.s.b + h * a.dv.s.h;
+    const float *rec = a.records + head * a.NC * (int64_t)a.record;
+
+    T tk, tq;
+    U_ tz, tp;
+    Cols<BF16> v;
+    f32x4 tv;
+    auto fetch = [&](int c) {
+        const float *r = rec + (int64_t)c * a.record;
+        tk.load(a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk, a.vk);
+        tq.load(a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk, a.vq);
+        tz.load(r + Record::kZt);
+        tp.load(r + Record::kP);
+        tv = load_vecs(r + Record::kVec);
+        v.load(a.d_o.p, eo, a.d_o.s.l, c * kC, a.L, col, a.Dv, lane);
+    };
+    State<KD> S;
+    S.load(a.ds_final ? a.ds_final + head * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, col, lane);
+    U_::clear(s_z);
+    U_::clear(s_p);
+    fetch(a.NC - 1);
+    for (int c = a.NC - 1; c >= 0; --c) {
+        tk.store(s_k);
+        tq.store(s_q);
+        tz.store(s_z);
+        tp.store(s_p);
+        if (threadIdx.x < kC)
+            *reinterpret_cast<f32x4 *>(s_vec + 4 * threadIdx.x) = tv;
+        f32x4 dO[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            dO[t] = v.get(t);
+        __syncthreads();
+        if (c > 0)
+            fetch(c - 1);
+
+        S.store(a.grads + (head * a.NC + c) * KD * a.DV, KD, a.DV, col, lane);
+        f32x4 dU[4], x[4], w[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            dU[t] = w[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < KD / 32; ++s) {
+            const Frag<3> f = split<3>(S.s[2 * s], S.s[2 * s + 1]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                dU[t] = mma<3>(T::rows_stacked(s_k, t, s, lane), f, dU[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            dU[t] *= row_vec(s_vec, kLeft, t, lane);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const Frag<NK> f = split<NK>(dO[2 * s], dO[2 * s + 1]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                if (U_::has(t, s))
+                    dU[t] = mma<3>(U_::template get<3>(s_p, t, s, lane), f, dU[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            x[t] = row_vec(s_vec, kBeta, t, lane) * dU[t];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const Frag<3> f = split<3>(x[2 * s], x[2 * s + 1]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                if (U_::has(t, s))
+                    w[t] = mma<3>(U_::template get<3>(s_z, t, s, lane), f, w[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            w[t] = dU[t] - w[t];
+            if (col < a.DV) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    a.w[((head * a.NC + c) * kC + 16 * t + 4 * (lane >> 4) + r) * a.DV + col] = w[t][r];
+            }
+            w[t] *= row_vec(s_vec, kBeta, t, lane);     // dV
+            store_cols<BF16>(const_cast<void *>(a.dv.p), ev, a.dv.s.l, c * kC, a.L, col, a.Dv, lane, t, w[t]);
+            w[t] *= -row_vec(s_vec, kRise, t, lane);
+            dO[t] *= a.scale * row_vec(s_vec, kRise, t, lane);
+        }
+        const float whole = s_vec[kWhole * kC];
+#pragma unroll
+        for (int m = 0; m < KD / 16; ++m)
+            S.s[m] *= whole;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const Frag<3> fo = split<3>(dO[2 * s], dO[2 * s + 1]), fw = split<3>(w[2 * s], w[2 * s + 1]);
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m) {
+                S.s[m] = mma<3>(T::columns_stacked(s_q, m, s, lane), fo, S.s[m]);
+                S.s[m] = mma<3>(T::columns_stacked(s_k, m, s, lane), fw, S.s[m]);
+            }
+        }
+        __syncthreads();
+    }
+    if (a.ds0)
+        S.store(a.ds0 + head * a.Dk * a.Dv, a.Dk, a.Dv, col, lane);
+}
+
+// ---------------------------------------------------------------------------
+// grad_kernel: dQ and dK of a chunk of one key head (summed over the value
+// heads of its group), and dg and dbeta of each of those.  Wave w forms row
+// tile w of X and Y (sums over the state's columns), then all rows of the
+// KD / 4 key dimensions that it owns.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float sum16(float v)     // over the lanes of a group of 16
+{
+#pragma unroll
+    for (int m = 8; m >= 1; m >>= 1)
+        v += __shfl_xor(v, m, 64);
+    return v;
+}
+
+__device__ __forceinline__ f32x8 load8(const float *p)
+{
+    const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+__device__ __forceinline__ float dot8(f32x8 a, f32x8 b, float v)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v += a[j] * b[j];
+    return v;
+}
+
+template <int KD, bool BF16>
+__global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
+{
+    using T = Tile<KD, BF16>;
+    using M = Tile<kC, BF16>;           // X and Y: 64 x 64
+    constexpr int NK = T::NK;
+    constexpr int NO = BF16 ? 2 : 3;    // parts for dQ and dK alone (see chain_kernel)
+    constexpr int NM = M::NK;           // parts of X and Y
+    constexpr int NTC = KD / 64;        // 16-column tiles of a wave
+    extern __shared__ __attribute__((aligned(16))) char s_dyn[];
+    uint16_t *s_k = reinterpret_cast<uint16_t *>(s_dyn);
+    uint16_t *s_q = s_k + T::kSize;
+    uint16_t *s_x = s_q + T::kSize;
+    uint16_t *s_y = s_x + M::kSize;
+    float *s_vec = reinterpret_cast<float *>(s_y + M::kSize);         // the record's vectors
+    float *s_rows = s_vec + kVecs * kC;                               // [5][64]: row sums of q . dq by wave, and X's
+    float *s_sum = s_rows + 5 * kC;                                   // [4]: <S, dS> and k . (u dS^T) by wave
+
+    const int64_t chunk = blockIdx.x % (unsigned)a.NC, bk = blockIdx.x / (unsigned)a.NC;
+    const int c = (int)chunk;
+    const int64_t b = bk / a.Hk;
+    const int hk = (int)(bk - b * a.Hk), group = a.Hv / a.Hk;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, i16 = lane & 15;
+    const int t0 = c * kC;
+
+    {
+        T tk, tq;
+        tk.load(a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk, a.vk);
+        tq.load(a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk, a.vq);
+        tk.store(s_k);
+        tq.store(s_q);
+    }
+    f32x4 dq[4][NTC], dk[4][NTC];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int n = 0; n < NTC; ++n)
+            dq[t][n] = dk[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    for (int j = 0; j < group; ++j) {
+        const int h = hk * group + j;
+        const int64_t head = b * a.Hv + h, at = head * a.NC + c;
+        const float *rec = a.records + at * a.record;
+        const float *ut = a.ut + at * kC * a.DV, *w = a.w + at * kC * a.DV;
+        const float *S = a.states + at * KD * a.DV, *dS = a.grads + at * KD * a.DV;
+        const int64_t eo = b * a.d_o.s.b + h * a.d_o.s.h;
+
+        for (int x = threadIdx.x; x < kVecs * kC; x += kThreads)
+            s_vec[x] = rec[Record::kVec + x];
+        __syncthreads();
+
+        // Row tile `wave` of X and Y; rows' sums.
+        {
+            const int row = 16 * wave + i16, t = t0 + row;
+            f32x4 dp[4], dn[4];
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb)
+                dp[tb] = dn[tb] = f32x4{0.f, 0.f, 0.f, 0.f};
+            float uw = 0.f, vw = 0.f;
+            for (int d0 = 0; d0 < a.DV; d0 += 32) {
+                const int col = d0 + 8 * g;
+                const Frag<NK> fo = unit_frag<BF16>(load_unit<BF16>(a.d_o.p, eo + t * a.d_o.s.l, col, a.Dv, t < a.L, a.vo));
+                const f32x8 wv = load8(w + row * a.DV + col);
+                const Frag<NO> fw = split<NO>(wv);
+                const f32x8 vv = unit_values<BF16>(load_unit<BF16>(
+                    a.v.p, b * a.v.s.b + h * a.v.s.h + t * a.v.s.l, col, a.Dv, t < a.L, false));
+                vw = dot8(vv, wv, vw);
+#pragma unroll
+                for (int tb = 0; tb < 4; ++tb) {
+                    if (tb > wave)
+                        continue;
+                    const f32x8 uv = load8(ut + (16 * tb + i16) * a.DV + col);
+                    if (tb == wave)
+                        uw = dot8(uv, wv, uw);
+                    const Frag<3> fu = split<3>(uv);
+                    dp[tb] = mma<3>(fo, fu, dp[tb]);
+                    dn[tb] = mma<NO>(fw, fu, dn[tb]);
+                }
+            }
+            uw += __shfl_xor(uw, 16, 64);
+            uw += __shfl_xor(uw, 32, 64);
+            vw += __shfl_xor(vw, 16, 64);
+            vw += __shfl_xor(vw, 32, 64);
+            if (g == 0 && t < a.L)
+                static_cast<float *>(const_cast<void *>(a.dbeta.p))[b * a.dbeta.s.b + h * a.dbeta.s.h + t * a.dbeta.s.l] = uw;
+            const float v_dv = vw * s_vec[kBeta * kC + row];
+            // X, Y in rows 16 wave + 4 g + r, columns 16 tb + i16
+            f32x4 od = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb) {
+                const int jc = 16 * tb + i16;
+                f32x4 xx = {0.f, 0.f, 0.f, 0.f}, yy = xx;
+                if (tb <= wave) {
+                    const float bj = s_vec[kBeta * kC + jc];
+                    const f32x4 P = *reinterpret_cast<const f32x4 *>(rec + Record::kP + block_of(wave, tb) * kBlock + 4 * lane);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int ic = 16 * wave + 4 * g + r;
+                        const float d = decay_of(s_vec[kGhi * kC + ic], s_vec[kGlo * kC + ic], s_vec[kResets * kC + ic],
+                                                 s_vec[kGhi * kC + jc], s_vec[kGlo * kC + jc], s_vec[kResets * kC + jc]) * bj;
+                        od[r] += dp[tb][r] * bj * P[r];
+                        xx[r] = jc <= ic ? a.scale * dp[tb][r] * d : 0.f;
+                        yy[r] = jc < ic ? -dn[tb][r] * s_vec[kBeta * kC + ic] * d : 0.f;
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NM; ++n) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int p = n * M::kPart + (16 * wave + 4 * g + r) * M::kRow + jc;
+                        const uint16_t hx = f32_to_bf16_rne(xx[r]), hy = f32_to_bf16_rne(yy[r]);
+                        s_x[p] = hx;
+                        s_y[p] = hy;
+                        xx[r] -= bf16_lo(hx);
+                        yy[r] -= bf16_lo(hy);
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float v = sum16(od[r]);
+                if (i16 == 0)
+                    s_rows[4 * kC + 16 * wave + 4 * g + r] = v;
+            }
+            lds_order();
+            if (g == 0)
+                s_rows[4 * kC + row] -= v_dv;
+        }
+        __syncthreads();
+
+        // The wave's key dimensions.
+        f32x4 qdq[4];
+        float ss = 0.f, kds = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            qdq[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int n = 0; n < NTC; ++n) {
+            const int tile = wave * NTC + n, dim = 16 * tile + i16;
+            f32x4 e[4], f[4], k2[4];        // dO S^T, w S^T, u~ dS^T
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                e[t] = f[t] = k2[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int d0 = 0; d0 < a.DV; d0 += 32) {
+                const int col = d0 + 8 * g;
+                const f32x8 sv = load8(S + dim * a.DV + col), dv = load8(dS + dim * a.DV + col);
+                ss = dot8(sv, dv, ss);
+                const Frag<3> fs = split<3>(sv), fd = split<3>(dv);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const int row = 16 * t + i16;
+                    const Frag<NK> fo = unit_frag<BF16>(
+                        load_unit<BF16>(a.d_o.p, eo + (t0 + row) * a.d_o.s.l, col, a.Dv, t0 + row < a.L, a.vo));
+                    e[t] = mma<3>(fo, fs, e[t]);
+                    f[t] = mma<NO>(split<NO>(load8(w + row * a.DV + col)), fs, f[t]);
+                    k2[t] = mma<3>(split<3>(load8(ut + row * a.DV + col)), fd, k2[t]);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const f32x4 rise = row_vec(s_vec, kRise, t, lane), beta = row_vec(s_vec, kBeta, t, lane);
+                e[t] *= a.scale * rise;
+                k2[t] *= beta * row_vec(s_vec, kLeft, t, lane);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int p = (16 * t + 4 * g + r) * T::kRow + dim;
+                    float qv = 0.f, kv = 0.f;
+#pragma unroll
+                    for (int m = NK - 1; m >= 0; --m) {
+                        qv += bf16_lo(s_q[m * T::kPart + p]);
+                        kv += bf16_lo(s_k[m * T::kPart + p]);
+                    }
+                    qdq[t][r] += qv * e[t][r];
+                    kds += kv * k2[t][r];
+                }
+                dq[t][n] += e[t];
+                dk[t][n] += k2[t] - beta * rise * f[t];
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const Frag<NK> fk = T::columns(s_k, tile, s, lane), fq = T::columns(s_q, tile, s, lane);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    if (s <= t / 2) {
+                        dq[t][n] = mma<3>(M::rows(s_x, t, s, lane), fk, dq[t][n]);
+                        dk[t][n] = mma<3>(M::rows(s_y, t, s, lane), fk, dk[t][n]);
+                    }
+                    if (s >= t / 2) {
+                        dk[t][n] = mma<3>(M::columns(s_x, t, s, lane), fq, dk[t][n]);
+                        dk[t][n] = mma<3>(M::columns(s_y, t, s, lane), fk, dk[t][n]);
+                    }
+                }
+            }
+        }
+        ss = ss * s_vec[kWhole * kC] + kds;
+#pragma unroll
+        for (int m = 32; m >= 1; m >>= 1)
+            ss += __shfl_xor(ss, m, 64);
+        if (lane == 0)
+            s_sum[wave] = ss;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float v = sum16(qdq[t][r]);
+                if (i16 == 0)
+                    s_rows[wave * kC + 16 * t + 4 * g + r] = v;
+            }
+        __syncthreads();
+        if (wave == 0) {
+            float v = s_rows[4 * kC + lane];
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                v += s_rows[m * kC + lane];
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                const float x = __shfl_down(v, m, 64);
+                if (lane + m < 64)
+                    v += x;
+            }
+            v += s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+            const bool empty = s_vec[kResets * kC + lane] != (lane ? s_vec[kResets * kC + lane - 1] : 0.f);
+            if (t0 + lane < a.L)
+                static_cast<float *>(const_cast<void *>(a.dg.p))[b * a.dg.s.b + h * a.dg.s.h + (t0 + lane) * a.dg.s.l] =
+                    empty ? 0.f : v;
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int n = 0; n < NTC; ++n)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int dim = 16 * (wave * NTC + n) + i16;
+            store_cols<BF16>(const_cast<void *>(a.dq.p), b * a.dq.s.b + hk * a.dq.s.h, a.dq.s.l, t0, a.L, dim, a.Dk, lane, t, dq[t][n]);
+            store_cols<BF16>(const_cast<void *>(a.dk.p), b * a.dk.s.b + hk * a.dk.s.h, a.dk.s.l, t0, a.L, dim, a.Dk, lane, t, dk[t][n]);
+        }
+}
+
+// ---------------------------------------------------------------------------
+// step_kernel: one step.  A workgroup takes TX x 4 columns of one head's state,
+// each thread four columns of every TY-th row, all rows in registers: the
+// state is read once and written once.  o needs no second pass over the new
+// state: S_new^T q = (e^g S)^T q + (q . k) u, so both products over the rows
+// and q . k are summed across the threads together.
+// ---------------------------------------------------------------------------
+struct StepArgs {
+    Rows q, k, v, g, beta, o;
+    const float *s;
+    float *s_out;
+    int Hk, Hv, Dk, Dv, slices;
+    float scale;
+};
+
+template <bool BF16>
+__device__ __forceinline__ float load_value(const void *p, int64_t e)
+{
+    if constexpr (BF16)
+        return bf16_lo(static_cast<const uint16_t *>(p)[e]);
+    else
+        return static_cast<const float *>(p)[e];
+}
+
+template <bool BF16, int TX, bool VEC>
+__global__ void __launch_bounds__(kThreads) step_kernel(StepArgs a)
+{
+    constexpr int TY = kThreads / TX, RP = kMaxDim / TY, WY = 64 / TX;   // rows of a wave side by side
+    __shared__ float s_part[4][2][TX * 4];
+    __shared__ float s_qk[4];
+    const int64_t head = blockIdx.x / (unsigned)a.slices;
+    const int slice = blockIdx.x % (unsigned)a.slices;
+    const int64_t b = head / a.Hv;
+    const int h = (int)(head - b * a.Hv), hk = h / (a.Hv / a.Hk);
+    const int tx = threadIdx.x % TX, ty = threadIdx.x / TX, wave = threadIdx.x >> 6;
+    const int col = slice * TX * 4 + tx * 4;
+    const float *S = a.s + head * a.Dk * a.Dv;
+    float *So = a.s_out + head * a.Dk * a.Dv;
+
+    f32x4 st[RP];
+    float q[RP], k[RP];
+#pragma unroll
+    for (int i = 0; i < RP; ++i) {
+        const int row = i * TY + ty;
+        st[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        q[i] = k[i] = 0.f;
+        if (row < a.Dk) {
+            if constexpr (VEC) {
+                if (col < a.Dv)
+                    st[i] = *reinterpret_cast<const f32x4 *>(S + row * a.Dv + col);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (col + r < a.Dv)
+                        st[i][r] = S[row * a.Dv + col + r];
+            }
+            q[i] = load_value<BF16>(a.q.p, b * a.q.s.b + hk * a.q.s.h + row);
+            k[i] = load_value<BF16>(a.k.p, b * a.k.s.b + hk * a.k.s.h + row);
+        }
+    }
+    const float decay = expf(static_cast<const float *>(a.g.p)[b * a.g.s.b + h * a.g.s.h]);
+    const float beta = static_cast<const float *>(a.beta.p)[b * a.beta.s.b + h * a.beta.s.h];
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (col + r < a.Dv)
+            v[r] = load_value<BF16>(a.v.p, b * a.v.s.b + h * a.v.s.h + col + r);
+
+    f32x4 ks = {0.f, 0.f, 0.f, 0.f}, qs = ks;
+    float qk = 0.f;
+#pragma unroll
+    for (int i = 0; i < RP; ++i) {
+        st[i] *= decay;
+        ks += k[i] * st[i];
+        qs += q[i] * st[i];
+        qk += q[i] * k[i];
+    }
+#pragma unroll
+    for (int m = TX; m < 64; m <<= 1) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            ks[r] += __shfl_xor(ks[r], m, 64);
+            qs[r] += __shfl_xor(qs[r], m, 64);
+        }
+        qk += __shfl_xor(qk, m, 64);
+    }
+    if (ty % WY == 0) {
+        *reinterpret_cast<f32x4 *>(&s_part[wave][0][tx * 4]) = ks;
+        *reinterpret_cast<f32x4 *>(&s_part[wave][1][tx * 4]) = qs;
+        if (tx == 0)
+            s_qk[wave] = qk;
+    }
+    __syncthreads();
+    ks = qs = f32x4{0.f, 0.f, 0.f, 0.f};
+    qk = 0.f;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        ks += *reinterpret_cast<const f32x4 *>(&s_part[m][0][tx * 4]);
+        qs += *reinterpret_cast<const f32x4 *>(&s_part[m][1][tx * 4]);
+        qk += s_qk[m];
+    }
+    const f32x4 u = beta * (v - ks);
+#pragma unroll
+    for (int i = 0; i < RP; ++i) {
+        const int row = i * TY + ty;
+        st[i] += k[i] * u;
+        if (row < a.Dk) {
+            if constexpr (VEC) {
+                if (col < a.Dv)
+                    *reinterpret_cast<f32x4 *>(So + row * a.Dv + col) = st[i];
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (col + r < a.Dv)
+                        So[row * a.Dv + col + r] = st[i][r];
+            }
+        }
+    }
+    if (ty == 0) {
+        const f32x4 o = a.scale * (qs + qk * u);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (col + r < a.Dv) {
+                const int64_t e = b * a.o.s.b + h * a.o.s.h + col + r;
+                if constexpr (BF16)
+                    static_cast<uint16_t *>(const_cast<void *>(a.o.p))[e] = f32_to_bf16_rne(o[r]);
+                else
+                    static_cast<float *>(const_cast<void *>(a.o.p))[e] = o[r];
+            }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
+constexpr int64_t kMaxL = (int64_t)1 << 30;
+
+int check_delta_dims(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int32_t Dk, int32_t Dv)
+{
+    if (B < 0 || Hk < 0 || Hv < 0 || L < 0 || L > kMaxL || Dk < 1 || Dk > kMaxDim || Dv < 1 || Dv > kMaxDim)
+        return PDSSM_ERR_DIM;
+    if (Hv > 0 && (Hk == 0 || Hv % Hk != 0))
+        return PDSSM_ERR_DIM;
+    if ((double)B * Hv > 5.0e8 || Hv > (1 << 30) || (double)B * Hv * (double)((L + kC - 1) / kC) > 2.0e9)
+        return PDSSM_ERR_DIM;
+    return PDSSM_OK;
+}
+
+
+struct BwdLayout {
+    int64_t records, states, grads, ut, w, total;
+};
+
+int padded_key(int Dk) { return Dk <= 64 ? 64 : 128; }
+int padded_value(int Dv) { return (Dv + 31) / 32 * 32; }
+
+int64_t fwd_bytes(int64_t B, int64_t Hv, int64_t L)
+{
+    const int64_t chunks = B * Hv * ((L + kC - 1) / kC);
+    return (chunks > 0 ? chunks : 1) * Record::kFwd * 4;
+}
+
+BwdLayout bwd_layout(int64_t B, int64_t Hv, int64_t L, int Dk, int Dv)
+{
+    int64_t chunks = B * Hv * ((L + kC - 1) / kC);
+    chunks = chunks > 0 ? chunks : 1;
+    const int64_t state = (int64_t)padded_key(Dk) * padded_value(Dv) * 4, rows = (int64_t)kC * padded_value(Dv) * 4;
+    BwdLayout l;
+    l.records = 0;
+    l.states = chunks * Record::kBwd * 4;
+    l.grads = l.states + chunks * state;
+    l.ut = l.grads + chunks * state;
+    l.w = l.ut + chunks * rows;
+    l.total = l.w + chunks * rows;
+    return l;
+}
+
+// Every row begins on 16 bytes and ends with a whole unit of eight values.
+bool units(const void *p, const pdssm_strides &s, int D, int esize)
+{
+    const int e = 16 / esize;
+    return aligned16(p) && s.b % e == 0 && s.h % e == 0 && s.l % e == 0 && D % 8 == 0;
+}
+
+bool element_aligned(const void *p, int esize) { return ((uintptr_t)p & (uintptr_t)(esize - 1)) == 0; }
+
+template <typename K>
+int launch(K kernel, int64_t grid, size_t lds, const DeltaArgs &a, hipStream_t stream)
+{
+    // More than 64 KB of LDS has to be asked for; the device has 160 KB.
+    if (lds > 65536) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (e != hipSuccess)
+            return hip_status(e);
+    }
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), lds, stream, a);
+    return hip_status(hipGetLastError());
+}
+
+template <int KD, bool BF16>
+constexpr size_t chain_lds(bool outputs)
+{
+    using T = Tile<KD, BF16>;
+    const size_t one = (size_t)(T::kSize + Tri<false>::kSize) * 2;
+    return one * (outputs ? 2 : 1) + 4 * kC * 4;
+}
+
+template <int KD, bool BF16>
+constexpr size_t grad_lds()
+{
+    return (size_t)(2 * Tile<KD, BF16>::kSize + 2 * Tile<kC, BF16>::kSize) * 2 + (kVecs * kC + 5 * kC + 4) * 4;
+}
+
+template <int KD, bool BF16>
+int launch_fwd(const DeltaArgs &a, hipStream_t stream)
+{
+    int rc = launch(prep_kernel<KD, BF16, false>, a.heads * a.NC, 0, a, stream);
+    if (rc == PDSSM_OK)
+        rc = launch(chain_kernel<KD, BF16, false>, a.heads * a.slices, chain_lds<KD, BF16>(true), a, stream);
+    return rc;
+}
+
+template <int KD, bool BF16>
+int launch_bwd(const DeltaArgs &a, hipStream_t stream)
+{
+    int rc = launch(prep_kernel<KD, BF16, true>, a.heads * a.NC, 0, a, stream);
+    if (rc == PDSSM_OK)
+        rc = launch(chain_kernel<KD, BF16, true>, a.heads * a.slices, chain_lds<KD, BF16>(false), a, stream);
+    if (rc == PDSSM_OK)
+        rc = launch(reverse_kernel<KD, BF16>, a.heads * a.slices, chain_lds<KD, BF16>(true), a, stream);
+    if (rc == PDSSM_OK)
+        rc = launch(grad_kernel<KD, BF16>, a.heads / a.Hv * a.Hk * a.NC, grad_lds<KD, BF16>(), a, stream);
+    return rc;
+}
+
+}  // namespace
+}  // namespace pdssm
+
+using namespace pdssm;
+
+extern "C" size_t pdssm_delta_workspace_bytes(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int32_t Dk, int32_t Dv,
+                                              uint32_t flags)
+{
+    if (check_delta_dims(B, Hk, Hv, L, Dk, Dv) != PDSSM_OK || (flags & ~PDSSM_DATA_BF16))
+        return 0;
+    return (size_t)fwd_bytes(B, Hv, L);
+}
+
+extern "C" size_t pdssm_delta_bwd_workspace_bytes(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int32_t Dk,
+                                                  int32_t Dv, uint32_t flags)
+{
+    if (check_delta_dims(B, Hk, Hv, L, Dk, Dv) != PDSSM_OK || (flags & ~PDSSM_DATA_BF16))
+        return 0;
+    return (size_t)bwd_layout(B, Hv, L, Dk, Dv).total;
+}
+
+extern "C" int pdssm_delta_fwd(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                               const float *s0, void *o, float *s_final, int64_t B, int64_t Hk, int64_t Hv, int64_t L,
+                               int32_t Dk, int32_t Dv, float scale, uint32_t flags, const pdssm_strides *strides,
+                               void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    const int rc = check_delta_dims(B, Hk, Hv, L, Dk, Dv);
+    if (rc != PDSSM_OK)
+        return rc;
+    if (flags & ~PDSSM_DATA_BF16)
+        return PDSSM_ERR_FLAGS;
+    if (B == 0 || Hv == 0)
+        return PDSSM_OK;
+    if ((s0 && !aligned16(s0)) || (s_final && !aligned16(s_final)))
+        return PDSSM_ERR_ALIGN;
+    if (L == 0) {
+        if (!s_final || s_final == s0)
+            return PDSSM_OK;
+        return launch_state_fill(s0, s_final, B * Hv * Dk * Dv, stream);
+    }
+    if (!q || !k || !v || !g || !beta || !o || !workspace)
+        return PDSSM_ERR_NULL;
+    const int esize = (flags & PDSSM_DATA_BF16) ? 2 : 4;
+    for (const void *p : {q, k, v, (const void *)o})
+        if (!element_aligned(p, esize))
+            return PDSSM_ERR_ALIGN;
+    for (const float *p : {g, beta})
+        if (!element_aligned(p, 4))
+            return PDSSM_ERR_ALIGN;
+    if (!aligned16(workspace))
+        return PDSSM_ERR_ALIGN;
+    if (workspace_bytes < (size_t)fwd_bytes(B, Hv, L))
+        return PDSSM_ERR_WORKSPACE;
+    DeltaArgs a = {};
+    const pdssm_strides keys = {Hk * L * Dk, L * Dk, Dk}, values = {Hv * L * Dv, L * Dv, Dv}, gates = {Hv * L, L, 1};
+    const pdssm_strides whole[6] = {keys, keys, values, gates, gates, values};
+    const pdssm_strides *s = strides ? strides : whole;
+    a.q = {q, s[0]}, a.k = {k, s[1]}, a.v = {v, s[2]}, a.g = {g, s[3]}, a.beta = {beta, s[4]}, a.o = {o, s[5]};
+    a.s0 = s0, a.s_final = s_final, a.records = static_cast<float *>(workspace), a.record = Record::kFwd;
+    a.heads = B * Hv, a.Hk = (int)Hk, a.Hv = (int)Hv, a.L = (int)L, a.NC = (int)((L + kC - 1) / kC);
+    a.Dk = Dk, a.Dv = Dv, a.DV = padded_value(Dv), a.slices = (Dv + 63) / 64, a.scale = scale;
+    a.vq = units(q, s[0], Dk, esize), a.vk = units(k, s[1], Dk, esize);
+    if (esize == 2)
+        return Dk <= 64 ? launch_fwd<64, true>(a, stream) : launch_fwd<128, true>(a, stream);
+    return Dk <= 64 ? launch_fwd<64, false>(a, stream) : launch_fwd<128, false>(a, stream);
+}
+
+extern "C" int pdssm_delta_bwd(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                               const float *s0, const void *d_o, const float *ds_final, void *dq, void *dk, void *dv,
+                               float *dg, float *dbeta, float *ds0, int64_t B, int64_t Hk, int64_t Hv, int64_t L,
+                               int32_t Dk, int32_t Dv, float scale, uint32_t flags, const pdssm_strides *strides,
+                               void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    const int rc = check_delta_dims(B, Hk, Hv, L, Dk, Dv);
+    if (rc != PDSSM_OK)
+        return rc;
+    if (flags & ~PDSSM_DATA_BF16)
+        return PDSSM_ERR_FLAGS;
+    if (B == 0 || Hv == 0)
+        return PDSSM_OK;
+    for (const float *p : {s0, ds_final, (const float *)ds0})
+        if (p && !aligned16(p))
+            return PDSSM_ERR_ALIGN;
+    if (L == 0) {
+        if (!ds0 || ds0 == ds_final)
+            return PDSSM_OK;
+        return launch_state_fill(ds_final, ds0, B * Hv * Dk * Dv, stream);
+    }
+    if (!q || !k || !v || !g || !beta || !d_o || !dq || !dk || !dv || !dg || !dbeta || !workspace)
+        return PDSSM_ERR_NULL;
+    const int esize = (flags & PDSSM_DATA_BF16) ? 2 : 4;
+    for (const void *p : {q, k, v, d_o, (const void *)dq, (const void *)dk, (const void *)dv})
+        if (!element_aligned(p, esize))
+            return PDSSM_ERR_ALIGN;
+    for (const float *p : {g, beta, (const float *)dg, (const float *)dbeta})
+        if (!element_aligned(p, 4))
+            return PDSSM_ERR_ALIGN;
+    if (!aligned16(workspace))
+        return PDSSM_ERR_ALIGN;
+    const BwdLayout lo = bwd_layout(B, Hv, L, Dk, Dv);
+    if (workspace_bytes < (size_t)lo.total)
+        return PDSSM_ERR_WORKSPACE;
+    DeltaArgs a = {};
+    const pdssm_strides keys = {Hk * L * Dk, L * Dk, Dk}, values = {Hv * L * Dv, L * Dv, Dv}, gates = {Hv * L, L, 1};
+    const pdssm_strides whole[11] = {keys, keys, values, gates, gates, values, keys, keys, values, gates, gates};
+    const pdssm_strides *s = strides ? strides : whole;
+    a.q = {q, s[0]}, a.k = {k, s[1]}, a.v = {v, s[2]}, a.g = {g, s[3]}, a.beta = {beta, s[4]}, a.d_o = {d_o, s[5]};
+    a.dq = {dq, s[6]}, a.dk = {dk, s[7]}, a.dv = {dv, s[8]}, a.dg = {dg, s[9]}, a.dbeta = {dbeta, s[10]};
+    a.s0 = s0, a.ds_final = ds_final, a.ds0 = ds0, a.record = Record::kBwd;
+    char *ws = static_cast<char *>(workspace);
+    a.records = reinterpret_cast<float *>(ws + lo.records);
+    a.states = reinterpret_cast<float *>(ws + lo.states);
+    a.grads = reinterpret_cast<float *>(ws + lo.grads);
+    a.ut = reinterpret_cast<float *>(ws + lo.ut);
+    a.w = reinterpret_cast<float *>(ws + lo.w);
+    a.heads = B * Hv, a.Hk = (int)Hk, a.Hv = (int)Hv, a.L = (int)L, a.NC = (int)((L + kC - 1) / kC);
+    a.Dk = Dk, a.Dv = Dv, a.DV = padded_value(Dv), a.slices = (Dv + 63) / 64, a.scale = scale;
+    a.vq = units(q, s[0], Dk, esize), a.vk = units(k, s[1], Dk, esize), a.vo = units(d_o, s[5], Dv, esize);
+    if (esize == 2)
+        return Dk <= 64 ? launch_bwd<64, true>(a, stream) : launch_bwd<128, true>(a, stream);
+    return Dk <= 64 ? launch_bwd<64, false>(a, stream) : launch_bwd<128, false>(a, stream);
+}
+
+extern "C" int pdssm_delta_step(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                                const float *s, void *o, float *s_out, int64_t B, int64_t Hk, int64_t Hv, int32_t Dk,
+                                int32_t Dv, float scale, uint32_t flags, const pdssm_strides *strides,
+                                hipStream_t stream)
+{
+    const int rc = check_delta_dims(B, Hk, Hv, 1, Dk, Dv);
+    if (rc != PDSSM_OK)
+        return rc;
+    if (flags & ~PDSSM_DATA_BF16)
+        return PDSSM_ERR_FLAGS;
+    if (B == 0 || Hv == 0)
+        return PDSSM_OK;
+    if (!q || !k || !v || !g || !beta || !s || !o || !s_out)
+        return PDSSM_ERR_NULL;
+    const int esize = (flags & PDSSM_DATA_BF16) ? 2 : 4;
+    for (const void *p : {q, k, v, (const void *)o})
+        if (!element_aligned(p, esize))
+            return PDSSM_ERR_ALIGN;
+    if (!element_aligned(g, 4) || !element_aligned(beta, 4) || !aligned16(s) || !aligned16(s_out))
+        return PDSSM_ERR_ALIGN;
+    StepArgs a;
+    const pdssm_strides keys = {Hk * Dk, Dk, 0}, values = {Hv * Dv, Dv, 0}, gates = {Hv, 1, 0};
+    const pdssm_strides whole[6] = {keys, keys, values, gates, gates, values};
+    const pdssm_strides *st = strides ? strides : whole;
+    a.q = {q, st[0]}, a.k = {k, st[1]}, a.v = {v, st[2]}, a.g = {g, st[3]}, a.beta = {beta, st[4]}, a.o = {o, st[5]};
+    a.s = s, a.s_out = s_out, a.Hk = (int)Hk, a.Hv = (int)Hv, a.Dk = Dk, a.Dv = Dv, a.scale = scale;
+    a.slices = (Dv + 31) / 32;
+    const dim3 grid((unsigned)(B * Hv * a.slices)), block(kThreads);
+    const bool vec = Dv % 4 == 0;
+    if (esize == 2) {
+        if (vec)
+            hipLaunchKernelGGL((step_kernel<true, 8, true>), grid, block, 0, stream, a);
+        else
+            hipLaunchKernelGGL((step_kernel<true, 8, false>), grid, block, 0, stream, a);
+    } else {
+        if (vec)
+            hipLaunchKernelGGL((step_kernel<false, 8, true>), grid, block, 0, stream, a);
+        else
+            hipLaunchKernelGGL((step_kernel<false, 8, false>), grid, block, 0, stream, a);
+    }
+    return hip_status(hipGetLastError());
+}
