@@ -34,7 +34,8 @@
  * Layouts: device pointers.  q, k, v, o, g, beta and the like are indexed
  * [B,H,L(,D)] with the last dimension contiguous and the strides of the
  * first three, in elements, in the pdssm_strides of each; a NULL list means
- * contiguous [B,H,L(,D)].  Rows need the alignment of their element only
+ * contiguous [B,H,L(,D)]; for the delta rule the stride along L is in
+ * [0, 2^23).  Rows need the alignment of their element only
  * (rows that all begin on 16 bytes are read faster).  States are contiguous
  * [B,Hv,Dk,Dv], 16-byte aligned.  Outputs overlap neither inputs nor each
  * other, except where said.

@@ -84,7 +84,7 @@ struct DeltaArgs {
     int Hk, Hv, L, NC, Dk, Dv, DV, record;
     int slices;             // column slices of a head over workgroups
     float scale;
-    bool vq, vk, vo;        // rows of q, of k, of d_o can be read in 16 bytes
+    bool vq, vk, vv, vo;    // rows of q, k, v, d_o can be read in 16 bytes
 };
 
 // ---------------------------------------------------------------------------
@@ -101,44 +101,76 @@ struct Unit<false> {
     f32x8 v;
 };
 
+// Rows of one chunk as a buffer: a wave-uniform base and 32-bit offsets inside
+// the chunk (strides along l are below kMaxStride, checked on the host).
+// Places outside the sequence or the row get an offset beyond the buffer, so
+// loads give zero and stores write nothing, without a branch.
+constexpr uint32_t kOutside = 0x80000000u;
+constexpr int64_t kMaxStride = 1 << 23;     // 64 rows of 4-byte values stay below 2^31 bytes
+
 template <bool BF16>
-__device__ __forceinline__ Unit<BF16> load_unit(const void *base, int64_t e, int col, int D, bool inside, bool vec)
-{
-    Unit<BF16> u;
-    if constexpr (BF16) {
-        u.v = make_uint4(0, 0, 0, 0);
-        const uint16_t *p = static_cast<const uint16_t *>(base) + e + col;
-        if (inside && col < D) {
-            if (vec) {
-                u.v = *reinterpret_cast<const uint4 *>(p);
-            } else {
-                uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (col + j < D)
-                        w[j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
-                u.v = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
-    } else {
-        const float *p = static_cast<const float *>(base) + e + col;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            u.v[j] = 0.f;
-        if (inside && col < D) {
-            if (vec) {
-                const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
-                u.v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (col + j < D)
-                        u.v[j] = p[j];
-            }
-        }
+struct Chunk {
+    __amdgpu_buffer_rsrc_t r;
+    uint32_t stride;        // bytes between rows
+    int rows, D;            // rows of the chunk inside the sequence
+    static constexpr uint32_t kSize = BF16 ? 2 : 4;
+
+    // Rows t0 .. of L of the sequence that begins at element e0.
+    __device__ __forceinline__ Chunk(const void *base, int64_t e0, int64_t s, int t0, int L, int D_)
+    {
+        rows = min(L - t0, kC);
+        D = D_;
+        stride = (uint32_t)s * kSize;
+        r = make_rsrc(static_cast<const char *>(base) + (e0 + t0 * s) * kSize, (uint64_t)(rows - 1) * stride + D * kSize);
     }
-    return u;
-}
+    __device__ __forceinline__ uint32_t at(int row, int col) const
+    {
+        return row < rows && col < D ? row * stride + col * kSize : kOutside;
+    }
+    // Values col .. col + 7 of a row; `vec`: rows begin on 16 bytes and hold
+    // whole units.
+    __device__ __forceinline__ Unit<BF16> unit(int row, int col, bool vec) const
+    {
+        Unit<BF16> u;
+        if (vec) {
+            const uint32_t e = at(row, col);
+            if constexpr (BF16) {
+                const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, e, 0, 0);
+                __builtin_memcpy(&u.v, &v, 16);
+            } else {
+                const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, e, 0, 0);
+                const auto w = __builtin_amdgcn_raw_buffer_load_b128(r, e + 16, 0, 0);
+                __builtin_memcpy(&u.v, &v, 16);
+                __builtin_memcpy(reinterpret_cast<char *>(&u.v) + 16, &w, 16);
+            }
+        } else if constexpr (BF16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                w[j] = bload<uint16_t>(r, at(row, col + j), 0);
+            u.v = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                u.v[j] = bload<float>(r, at(row, col + j), 0);
+        }
+        return u;
+    }
+    __device__ __forceinline__ uint32_t raw(int row, int col) const
+    {
+        if constexpr (BF16)
+            return bload<uint16_t>(r, at(row, col), 0);
+        else
+            return bload<uint32_t>(r, at(row, col), 0);
+    }
+    __device__ __forceinline__ void put(int row, int col, float v) const
+    {
+        if constexpr (BF16)
+            __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16_rne(v), r, at(row, col), 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, at(row, col), 0, 0);
+    }
+};
 
 template <bool BF16>
 __device__ __forceinline__ Frag<BF16 ? 1 : 3> unit_frag(const Unit<BF16> &u)
@@ -176,13 +208,12 @@ struct Tile {
 
     Unit<BF16> u[kUnits];
 
-    // Rows t0 .. t0 + 63 of a sequence of L rows that begins at element e0.
-    __device__ __forceinline__ void load(const void *base, int64_t e0, int64_t stride, int t0, int L, int D, bool vec)
+    __device__ __forceinline__ void load(const Chunk<BF16> &c, bool vec)
     {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
-            const int x = threadIdx.x + i * NT, row = x / (KD / 8), col = x % (KD / 8) * 8;
-            u[i] = load_unit<BF16>(base, e0 + (t0 + row) * stride, col, D, t0 + row < L, vec);
+            const int x = threadIdx.x + i * NT;
+            u[i] = c.unit(x / (KD / 8), x % (KD / 8) * 8, vec);
         }
     }
     __device__ __forceinline__ void store(uint16_t *lds) const
@@ -288,8 +319,8 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
 
     {
         T q, k;
-        k.load(a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk, a.vk);
-        q.load(a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk, a.vq);
+        k.load({a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk}, a.vk);
+        q.load({a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk}, a.vq);
         if (wave == 0) {
             // G in 64 bits (differences of neighbours stay exact to 32), steps
             // with g = -inf counted apart.
@@ -487,13 +518,11 @@ struct Tri {
                 const int ta = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, tb = t - ta * (ta + 1) / 2;
                 const int row = TRANS ? tb : ta, col = TRANS ? ta : tb;
                 uint16_t *p = lds + ((frag(row, col >> 1) * 3) * 64 + lane) * 8 + 4 * (col & 1);
-                f32x4 v = u[i];
+                float v[4] = {u[i][0], u[i][1], u[i][2], u[i][3]};
 #pragma unroll
-                for (int n = 0; n < 3; ++n) {
-                    const bf16x4 h = __builtin_convertvector(v, bf16x4);
-                    *reinterpret_cast<bf16x4 *>(p + n * 512) = h;
-                    v -= __builtin_convertvector(h, f32x4);
-                }
+                for (int n = 0; n < 3; ++n)
+                    *reinterpret_cast<uint2 *>(p + n * 512) =
+                        make_uint2(take_part(v[0], v[1], n < 2), take_part(v[2], v[3], n < 2));
             }
         }
     }
@@ -523,24 +552,13 @@ template <bool BF16>
 struct Cols {
     uint32_t raw[4][4];
 
-    __device__ __forceinline__ void load(const void *base, int64_t e0, int64_t stride, int t0, int L, int col, int D,
-                                         int lane)
+    __device__ __forceinline__ void load(const Chunk<BF16> &c, int col, int lane)
     {
-        const int g = lane >> 4;
 #pragma unroll
         for (int a = 0; a < 4; ++a)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = t0 + 16 * a + 4 * g + r;
-                raw[a][r] = 0;
-                if (t < L && col < D) {
-                    const int64_t e = e0 + t * stride + col;
-                    if constexpr (BF16)
-                        raw[a][r] = static_cast<const uint16_t *>(base)[e];
-                    else
-                        raw[a][r] = static_cast<const uint32_t *>(base)[e];
-                }
-            }
+            for (int r = 0; r < 4; ++r)
+                raw[a][r] = c.raw(16 * a + 4 * (lane >> 4) + r, col);
     }
     __device__ __forceinline__ f32x4 get(int a) const
     {
@@ -553,23 +571,11 @@ struct Cols {
 };
 
 template <bool BF16>
-__device__ __forceinline__ void store_cols(void *base, int64_t e0, int64_t stride, int t0, int L, int col, int D,
-                                           int lane, int a, f32x4 v)
+__device__ __forceinline__ void store_cols(const Chunk<BF16> &c, int col, int lane, int a, f32x4 v)
 {
-    const int g = lane >> 4;
-    if (col >= D)
-        return;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int t = t0 + 16 * a + 4 * g + r;
-        if (t < L) {
-            const int64_t e = e0 + t * stride + col;
-            if constexpr (BF16)
-                static_cast<uint16_t *>(base)[e] = f32_to_bf16_rne(v[r]);
-            else
-                static_cast<float *>(base)[e] = v[r];
-        }
-    }
+    for (int r = 0; r < 4; ++r)
+        c.put(16 * a + 4 * (lane >> 4) + r, col, v[r]);
 }
 
 // A state (or its gradient): KD / 16 tiles in the C layout.
@@ -646,12 +652,12 @@ __global__ void __launch_bounds__(kThreads) chain_kernel(DeltaArgs a)
     f32x4 tv;
     auto fetch = [&](int c) {
         const float *r = rec + (int64_t)c * a.record;
-        tk.load(a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk, a.vk);
+        tk.load({a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk}, a.vk);
         tz.load(r + Record::kZ);
         tv = load_vecs(r + Record::kVec);
-        v.load(a.v.p, ev, a.v.s.l, c * kC, a.L, col, a.Dv, lane);
+        v.load({a.v.p, ev, a.v.s.l, c * kC, a.L, a.Dv}, col, lane);
         if constexpr (!KEEP) {
-            tq.load(a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk, a.vq);
+            tq.load({a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk}, a.vq);
             tp.load(r + Record::kP);
         }
     };
@@ -737,8 +743,7 @@ __global__ void __launch_bounds__(kThreads) chain_kernel(DeltaArgs a)
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t)
-                store_cols<BF16>(const_cast<void *>(a.o.p), b * a.o.s.b + h * a.o.s.h, a.o.s.l, c * kC, a.L, col, a.Dv,
-                                 lane, t, o[t]);
+                store_cols<BF16>({a.o.p, b * a.o.s.b + h * a.o.s.h, a.o.s.l, c * kC, a.L, a.Dv}, col, lane, t, o[t]);
         }
         const float whole = s_vec[kWhole * kC];
 #pragma unroll
@@ -793,12 +798,12 @@ __global__ void __launch_bounds__(kThreads) reverse_kernel(DeltaArgs a)
     f32x4 tv;
     auto fetch = [&](int c) {
         const float *r = rec + (int64_t)c * a.record;
-        tk.load(a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk, a.vk);
-        tq.load(a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk, a.vq);
+        tk.load({a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk}, a.vk);
+        tq.load({a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk}, a.vq);
         tz.load(r + Record::kZt);
         tp.load(r + Record::kP);
         tv = load_vecs(r + Record::kVec);
-        v.load(a.d_o.p, eo, a.d_o.s.l, c * kC, a.L, col, a.Dv, lane);
+        v.load({a.d_o.p, eo, a.d_o.s.l, c * kC, a.L, a.Dv}, col, lane);
     };
     State<KD> S;
     S.load(a.ds_final ? a.ds_final + head * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, col, lane);
@@ -863,7 +868,7 @@ __global__ void __launch_bounds__(kThreads) reverse_kernel(DeltaArgs a)
                     a.w[((head * a.NC + c) * kC + 16 * t + 4 * (lane >> 4) + r) * a.DV + col] = w[t][r];
             }
             w[t] *= row_vec(s_vec, kBeta, t, lane);     // dV
-            store_cols<BF16>(const_cast<void *>(a.dv.p), ev, a.dv.s.l, c * kC, a.L, col, a.Dv, lane, t, w[t]);
+            store_cols<BF16>({a.dv.p, ev, a.dv.s.l, c * kC, a.L, a.Dv}, col, lane, t, w[t]);
             w[t] *= -row_vec(s_vec, kRise, t, lane);
             dO[t] *= a.scale * row_vec(s_vec, kRise, t, lane);
         }
@@ -941,8 +946,8 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
 
     {
         T tk, tq;
-        tk.load(a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk, a.vk);
-        tq.load(a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk, a.vq);
+        tk.load({a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk}, a.vk);
+        tq.load({a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk}, a.vq);
         tk.store(s_k);
         tq.store(s_q);
     }
@@ -959,7 +964,8 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
         const float *rec = a.records + at * a.record;
         const float *ut = a.ut + at * kC * a.DV, *w = a.w + at * kC * a.DV;
         const float *S = a.states + at * KD * a.DV, *dS = a.grads + at * KD * a.DV;
-        const int64_t eo = b * a.d_o.s.b + h * a.d_o.s.h;
+        const Chunk<BF16> cdo(a.d_o.p, b * a.d_o.s.b + h * a.d_o.s.h, a.d_o.s.l, t0, a.L, a.Dv);
+        const Chunk<BF16> cv(a.v.p, b * a.v.s.b + h * a.v.s.h, a.v.s.l, t0, a.L, a.Dv);
 
         for (int x = threadIdx.x; x < kVecs * kC; x += kThreads)
             s_vec[x] = rec[Record::kVec + x];
@@ -975,11 +981,10 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
             float uw = 0.f, vw = 0.f;
             for (int d0 = 0; d0 < a.DV; d0 += 32) {
                 const int col = d0 + 8 * g;
-                const Frag<NK> fo = unit_frag<BF16>(load_unit<BF16>(a.d_o.p, eo + t * a.d_o.s.l, col, a.Dv, t < a.L, a.vo));
+                const Frag<NK> fo = unit_frag<BF16>(cdo.unit(row, col, a.vo));
                 const f32x8 wv = load8(w + row * a.DV + col);
                 const Frag<NO> fw = split<NO>(wv);
-                const f32x8 vv = unit_values<BF16>(load_unit<BF16>(
-                    a.v.p, b * a.v.s.b + h * a.v.s.h + t * a.v.s.l, col, a.Dv, t < a.L, false));
+                const f32x8 vv = unit_values<BF16>(cv.unit(row, col, a.vv));
                 vw = dot8(vv, wv, vw);
 #pragma unroll
                 for (int tb = 0; tb < 4; ++tb) {
@@ -1065,8 +1070,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     const int row = 16 * t + i16;
-                    const Frag<NK> fo = unit_frag<BF16>(
-                        load_unit<BF16>(a.d_o.p, eo + (t0 + row) * a.d_o.s.l, col, a.Dv, t0 + row < a.L, a.vo));
+                    const Frag<NK> fo = unit_frag<BF16>(cdo.unit(row, col, a.vo));
                     e[t] = mma<3>(fo, fs, e[t]);
                     f[t] = mma<NO>(split<NO>(load8(w + row * a.DV + col)), fs, f[t]);
                     k2[t] = mma<3>(split<3>(load8(ut + row * a.DV + col)), fd, k2[t]);
@@ -1147,8 +1151,8 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const int dim = 16 * (wave * NTC + n) + i16;
-            store_cols<BF16>(const_cast<void *>(a.dq.p), b * a.dq.s.b + hk * a.dq.s.h, a.dq.s.l, t0, a.L, dim, a.Dk, lane, t, dq[t][n]);
-            store_cols<BF16>(const_cast<void *>(a.dk.p), b * a.dk.s.b + hk * a.dk.s.h, a.dk.s.l, t0, a.L, dim, a.Dk, lane, t, dk[t][n]);
+            store_cols<BF16>({a.dq.p, b * a.dq.s.b + hk * a.dq.s.h, a.dq.s.l, t0, a.L, a.Dk}, dim, lane, t, dq[t][n]);
+            store_cols<BF16>({a.dk.p, b * a.dk.s.b + hk * a.dk.s.h, a.dk.s.l, t0, a.L, a.Dk}, dim, lane, t, dk[t][n]);
         }
 }
 
@@ -1336,6 +1340,15 @@ bool units(const void *p, const pdssm_strides &s, int D, int esize)
     return aligned16(p) && s.b % e == 0 && s.h % e == 0 && s.l % e == 0 && D % 8 == 0;
 }
 
+// Strides along l that a chunk's 32-bit offsets can follow.
+bool strides_ok(const pdssm_strides *s, int n)
+{
+    for (int i = 0; i < n; ++i)
+        if (s[i].l < 0 || s[i].l >= kMaxStride)
+            return false;
+    return true;
+}
+
 bool element_aligned(const void *p, int esize) { return ((uintptr_t)p & (uintptr_t)(esize - 1)) == 0; }
 
 template <typename K>
@@ -1445,6 +1458,8 @@ extern "C" int pdssm_delta_fwd(const void *q, const void *k, const void *v, cons
     const pdssm_strides keys = {Hk * L * Dk, L * Dk, Dk}, values = {Hv * L * Dv, L * Dv, Dv}, gates = {Hv * L, L, 1};
     const pdssm_strides whole[6] = {keys, keys, values, gates, gates, values};
     const pdssm_strides *s = strides ? strides : whole;
+    if (!strides_ok(s, 6))
+        return PDSSM_ERR_DIM;
     a.q = {q, s[0]}, a.k = {k, s[1]}, a.v = {v, s[2]}, a.g = {g, s[3]}, a.beta = {beta, s[4]}, a.o = {o, s[5]};
     a.s0 = s0, a.s_final = s_final, a.records = static_cast<float *>(workspace), a.record = Record::kFwd;
     a.heads = B * Hv, a.Hk = (int)Hk, a.Hv = (int)Hv, a.L = (int)L, a.NC = (int)((L + kC - 1) / kC);
@@ -1495,6 +1510,8 @@ extern "C" int pdssm_delta_bwd(const void *q, const void *k, const void *v, cons
     const pdssm_strides whole[11] = {keys, keys, values, gates, gates, values, keys, keys, values, gates, gates};
     const pdssm_strides *s = strides ? strides : whole;
     a.q = {q, s[0]}, a.k = {k, s[1]}, a.v = {v, s[2]}, a.g = {g, s[3]}, a.beta = {beta, s[4]}, a.d_o = {d_o, s[5]};
+    if (!strides_ok(s, 11))
+        return PDSSM_ERR_DIM;
     a.dq = {dq, s[6]}, a.dk = {dk, s[7]}, a.dv = {dv, s[8]}, a.dg = {dg, s[9]}, a.dbeta = {dbeta, s[10]};
     a.s0 = s0, a.ds_final = ds_final, a.ds0 = ds0, a.record = Record::kBwd;
     char *ws = static_cast<char *>(workspace);
@@ -1505,7 +1522,7 @@ extern "C" int pdssm_delta_bwd(const void *q, const void *k, const void *v, cons
     a.w = reinterpret_cast<float *>(ws + lo.w);
     a.heads = B * Hv, a.Hk = (int)Hk, a.Hv = (int)Hv, a.L = (int)L, a.NC = (int)((L + kC - 1) / kC);
     a.Dk = Dk, a.Dv = Dv, a.DV = padded_value(Dv), a.slices = (Dv + 63) / 64, a.scale = scale;
-    a.vq = units(q, s[0], Dk, esize), a.vk = units(k, s[1], Dk, esize), a.vo = units(d_o, s[5], Dv, esize);
+    a.vq = units(q, s[0], Dk, esize), a.vk = units(k, s[1], Dk, esize), a.vv = units(v, s[2], Dv, esize), a.vo = units(d_o, s[5], Dv, esize);
     if (esize == 2)
         return Dk <= 64 ? launch_bwd<64, true>(a, stream) : launch_bwd<128, true>(a, stream);
     return Dk <= 64 ? launch_bwd<64, false>(a, stream) : launch_bwd<128, false>(a, stream);

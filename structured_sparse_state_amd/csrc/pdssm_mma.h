@@ -19,6 +19,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "pdssm_device.h"
+
 namespace pdssm {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -33,15 +35,34 @@ struct Frag {
     bf16x8 p[N];
 };
 
+// One part of two values as a word, leaving the rest in them (the words are
+// built by the packed conversion; element-wise conversions would be made one
+// by one).
+__device__ __forceinline__ uint32_t take_part(float &a, float &b, bool rest)
+{
+    const uint32_t w = f32x2_to_bf16x2_rne(a, b);
+    if (rest) {
+        a -= bf16_lo(w);
+        b -= bf16_hi(w);
+    }
+    return w;
+}
+
 template <int N>
 __device__ __forceinline__ Frag<N> split(f32x8 v)
 {
     Frag<N> f;
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        x[j] = v[j];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        f.p[n] = __builtin_convertvector(v, bf16x8);
-        if (n + 1 < N)
-            v -= __builtin_convertvector(f.p[n], f32x8);
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = take_part(x[2 * j], x[2 * j + 1], n + 1 < N);
+        __builtin_memcpy(&f.p[n], w, 16);
     }
     return f;
 }
