@@ -81,6 +81,10 @@ struct DeltaArgs {
     float *grads;           // same shape: state gradients after the chunks
     float *ut, *w;          // [B*Hv][NC][64][DV]: u~ and w
     int64_t heads;          // B*Hv
+    // Few heads: the chunks cut in segments of seg_chunks, walked side by side.
+    int segs, seg_chunks;
+    float *seg_states;      // [B*Hv][segs][KD][DV]: states before the segments
+    float *trans;           // [B*Hv][segs][KD][slices*64 + KD]: their ends from zero, and transitions
     int Hk, Hv, L, NC, Dk, Dv, DV, record;
     int slices;             // column slices of a head over workgroups
     float scale;
@@ -123,52 +127,61 @@ struct Chunk {
         stride = (uint32_t)s * kSize;
         r = make_rsrc(static_cast<const char *>(base) + (e0 + t0 * s) * kSize, (uint64_t)(rows - 1) * stride + D * kSize);
     }
-    __device__ __forceinline__ uint32_t at(int row, int col) const
+    // A lane's own part of an offset.  Opaque, so that the offsets of a loop's
+    // many rows are formed where they are used (an addition of a scalar each)
+    // and not held in registers across the loop.
+    __device__ __forceinline__ uint32_t lane_at(int row, int col) const
     {
-        return row < rows && col < D ? row * stride + col * kSize : kOutside;
+        return (uint32_t)opaque((int)(row * stride + col * kSize));
+    }
+    // The offset of lane row + `up`, `up` the same for all lanes.
+    __device__ __forceinline__ uint32_t at(uint32_t lane, int row, int up, int col) const
+    {
+        return row + up < rows && col < D ? lane + up * stride : kOutside;
     }
     // Values col .. col + 7 of a row; `vec`: rows begin on 16 bytes and hold
     // whole units.
-    __device__ __forceinline__ Unit<BF16> unit(int row, int col, bool vec) const
+    __device__ __forceinline__ Unit<BF16> unit(uint32_t lane, int row, int up, int col, bool vec) const
     {
         Unit<BF16> u;
         if (vec) {
-            const uint32_t e = at(row, col);
-            if constexpr (BF16) {
-                const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, e, 0, 0);
-                __builtin_memcpy(&u.v, &v, 16);
-            } else {
-                const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, e, 0, 0);
+            const uint32_t e = at(lane, row, up, col);
+            const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, e, 0, 0);
+            __builtin_memcpy(&u.v, &v, 16);
+            if constexpr (!BF16) {
                 const auto w = __builtin_amdgcn_raw_buffer_load_b128(r, e + 16, 0, 0);
-                __builtin_memcpy(&u.v, &v, 16);
                 __builtin_memcpy(reinterpret_cast<char *>(&u.v) + 16, &w, 16);
             }
         } else if constexpr (BF16) {
             uint32_t w[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                w[j] = bload<uint16_t>(r, at(row, col + j), 0);
+                w[j] = bload<uint16_t>(r, at(lane + j * kSize, row, up, col + j), 0);
             u.v = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                u.v[j] = bload<float>(r, at(row, col + j), 0);
+                u.v[j] = bload<float>(r, at(lane + j * kSize, row, up, col + j), 0);
         }
         return u;
     }
-    __device__ __forceinline__ uint32_t raw(int row, int col) const
+    __device__ __forceinline__ Unit<BF16> unit(int row, int col, bool vec) const
     {
-        if constexpr (BF16)
-            return bload<uint16_t>(r, at(row, col), 0);
-        else
-            return bload<uint32_t>(r, at(row, col), 0);
+        return unit(lane_at(row, col), row, 0, col, vec);
     }
-    __device__ __forceinline__ void put(int row, int col, float v) const
+    __device__ __forceinline__ uint32_t raw(uint32_t lane, int row, int up, int col) const
     {
         if constexpr (BF16)
-            __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16_rne(v), r, at(row, col), 0, 0);
+            return bload<uint16_t>(r, at(lane, row, up, col), 0);
         else
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, at(row, col), 0, 0);
+            return bload<uint32_t>(r, at(lane, row, up, col), 0);
+    }
+    __device__ __forceinline__ void put(uint32_t lane, int row, int up, int col, float v) const
+    {
+        if constexpr (BF16)
+            __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16_rne(v), r, at(lane, row, up, col), 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, at(lane, row, up, col), 0, 0);
     }
 };
 
@@ -208,19 +221,20 @@ struct Tile {
 
     Unit<BF16> u[kUnits];
 
-    __device__ __forceinline__ void load(const Chunk<BF16> &c, bool vec)
+    // `tid`: the thread's number among the NT that share the tile.
+    __device__ __forceinline__ void load(const Chunk<BF16> &c, bool vec, int tid)
     {
+        const int row = tid / (KD / 8), col = tid % (KD / 8) * 8;
+        const uint32_t lane = c.lane_at(row, col);
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            const int x = threadIdx.x + i * NT;
-            u[i] = c.unit(x / (KD / 8), x % (KD / 8) * 8, vec);
-        }
+        for (int i = 0; i < kUnits; ++i)
+            u[i] = c.unit(lane, row, i * (NT * 8 / KD), col, vec);
     }
-    __device__ __forceinline__ void store(uint16_t *lds) const
+    __device__ __forceinline__ void store(uint16_t *lds, int tid) const
     {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
-            const int x = threadIdx.x + i * NT, row = x / (KD / 8), col = x % (KD / 8) * 8;
+            const int x = tid + i * NT, row = x / (KD / 8), col = x % (KD / 8) * 8;
             const Frag<NK> f = unit_frag<BF16>(u[i]);
 #pragma unroll
             for (int n = 0; n < NK; ++n)
@@ -319,8 +333,8 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
 
     {
         T q, k;
-        k.load({a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk}, a.vk);
-        q.load({a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk}, a.vq);
+        k.load({a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk}, a.vk, threadIdx.x);
+        q.load({a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk}, a.vq, threadIdx.x);
         if (wave == 0) {
             // G in 64 bits (differences of neighbours stay exact to 32), steps
             // with g = -inf counted apart.
@@ -357,8 +371,8 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
             vec[kGlo * kC + lane] = lo;
             vec[kResets * kC + lane] = n;
         }
-        k.store(s_k);
-        q.store(s_q);
+        k.store(s_k, threadIdx.x);
+        q.store(s_q, threadIdx.x);
     }
     __syncthreads();
 
@@ -499,20 +513,20 @@ struct Tri {
     static __host__ __device__ constexpr int frag(int a, int s) { return TRANS ? (a < 2 ? 2 * a + s : a + 2) : (a < 2 ? a : 2 * a - 2 + s); }
 
     // blocks: row format, or column format for the transpose.
-    __device__ __forceinline__ void load(const float *blocks)
+    __device__ __forceinline__ void load(const float *blocks, int tid)
     {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
-            const int x = threadIdx.x + i * kThreads;
+            const int x = tid + i * kThreads;
             if (x < kBlocks * 64)
                 u[i] = *reinterpret_cast<const f32x4 *>(blocks + 4 * x);
         }
     }
-    __device__ __forceinline__ void store(uint16_t *lds) const
+    __device__ __forceinline__ void store(uint16_t *lds, int tid) const
     {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
-            const int x = threadIdx.x + i * kThreads;
+            const int x = tid + i * kThreads;
             if (x < kBlocks * 64) {
                 const int t = x >> 6, lane = x & 63;
                 const int ta = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, tb = t - ta * (ta + 1) / 2;
@@ -527,9 +541,9 @@ struct Tri {
         }
     }
     // The halves that no block fills.
-    static __device__ __forceinline__ void clear(uint16_t *lds)
+    static __device__ __forceinline__ void clear(uint16_t *lds, int tid)
     {
-        for (int x = threadIdx.x; x < 2 * 3 * 64; x += kThreads) {
+        for (int x = tid; x < 2 * 3 * 64; x += kThreads) {
             const int f = TRANS ? (x < 192 ? frag(1, 0) : frag(3, 1)) : (x < 192 ? frag(0, 0) : frag(2, 1));
             const int half = TRANS ? 0 : 1;
             *reinterpret_cast<uint2 *>(lds + (f * 192 + x % 192) * 8 + 4 * half) = make_uint2(0, 0);
@@ -554,11 +568,13 @@ struct Cols {
 
     __device__ __forceinline__ void load(const Chunk<BF16> &c, int col, int lane)
     {
+        const int row = 4 * (lane >> 4);
+        const uint32_t e = c.lane_at(row, col);
 #pragma unroll
         for (int a = 0; a < 4; ++a)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                raw[a][r] = c.raw(16 * a + 4 * (lane >> 4) + r, col);
+                raw[a][r] = c.raw(e, row, 16 * a + r, col);
     }
     __device__ __forceinline__ f32x4 get(int a) const
     {
@@ -573,9 +589,11 @@ struct Cols {
 template <bool BF16>
 __device__ __forceinline__ void store_cols(const Chunk<BF16> &c, int col, int lane, int a, f32x4 v)
 {
+    const int row = 4 * (lane >> 4);
+    const uint32_t e = c.lane_at(row, col);
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-        c.put(16 * a + 4 * (lane >> 4) + r, col, v[r]);
+        c.put(e, row, 16 * a + r, col, v[r]);
 }
 
 // A state (or its gradient): KD / 16 tiles in the C layout.
@@ -607,10 +625,29 @@ struct State {
     }
 };
 
+// Values of a wave's 16 columns (lane: column col, rows 4 g + r of a tile) of
+// a [rows][DV] fp32 array of the workspace; columns from DV on are dropped.
+struct Sheet {
+    __amdgpu_buffer_rsrc_t r;
+    uint32_t lane, pitch;
+    __device__ __forceinline__ Sheet(float *p, int rows, int DV, int col, int lane_)
+    {
+        pitch = DV * 4;
+        r = make_rsrc(p, (uint64_t)rows * pitch);
+        lane = col < DV ? (uint32_t)opaque((lane_ >> 4) * 4 * (int)pitch + col * 4) : kOutside;
+    }
+    __device__ __forceinline__ void put(int tile, f32x4 v) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), r, lane + (16 * tile + i) * pitch, 0, 0);
+    }
+};
+
 // Four vectors of the record in LDS (rise, left, beta, whole).
-__device__ __forceinline__ f32x4 load_vecs(const float *vec)
+__device__ __forceinline__ f32x4 load_vecs(const float *vec, int tid)
 {
-    return threadIdx.x < kC ? *reinterpret_cast<const f32x4 *>(vec + 4 * threadIdx.x) : f32x4{0.f, 0.f, 0.f, 0.f};
+    return tid < kC ? *reinterpret_cast<const f32x4 *>(vec + 4 * tid) : f32x4{0.f, 0.f, 0.f, 0.f};
 }
 __device__ __forceinline__ f32x4 row_vec(const float *s_vec, int which, int a, int lane)
 {
@@ -652,29 +689,29 @@ __global__ void __launch_bounds__(kThreads) chain_kernel(DeltaArgs a)
     f32x4 tv;
     auto fetch = [&](int c) {
         const float *r = rec + (int64_t)c * a.record;
-        tk.load({a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk}, a.vk);
-        tz.load(r + Record::kZ);
-        tv = load_vecs(r + Record::kVec);
+        tk.load({a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk}, a.vk, threadIdx.x);
+        tz.load(r + Record::kZ, threadIdx.x);
+        tv = load_vecs(r + Record::kVec, threadIdx.x);
         v.load({a.v.p, ev, a.v.s.l, c * kC, a.L, a.Dv}, col, lane);
         if constexpr (!KEEP) {
-            tq.load({a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk}, a.vq);
-            tp.load(r + Record::kP);
+            tq.load({a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk}, a.vq, threadIdx.x);
+            tp.load(r + Record::kP, threadIdx.x);
         }
     };
     State<KD> S;
     S.load(a.s0 ? a.s0 + head * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, col, lane);
-    L_::clear(s_z);
+    L_::clear(s_z, threadIdx.x);
     if constexpr (!KEEP)
-        L_::clear(s_p);
+        L_::clear(s_p, threadIdx.x);
     fetch(0);
     for (int c = 0; c < a.NC; ++c) {
-        tk.store(s_k);
-        tz.store(s_z);
+        tk.store(s_k, threadIdx.x);
+        tz.store(s_z, threadIdx.x);
         if (threadIdx.x < kC)
             *reinterpret_cast<f32x4 *>(s_vec + 4 * threadIdx.x) = tv;
         if constexpr (!KEEP) {
-            tq.store(s_q);
-            tp.store(s_p);
+            tq.store(s_q, threadIdx.x);
+            tp.store(s_p, threadIdx.x);
         }
         f32x4 R[4];
 #pragma unroll
@@ -685,7 +722,10 @@ __global__ void __launch_bounds__(kThreads) chain_kernel(DeltaArgs a)
             fetch(c + 1);
 
         if constexpr (KEEP) {
-            S.store(a.states + (head * a.NC + c) * KD * a.DV, KD, a.DV, col, lane);
+            const Sheet out(a.states + (head * a.NC + c) * KD * a.DV, KD, a.DV, col, lane);
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m)
+                out.put(m, S.s[m]);
         }
         f32x4 ks[4], qs[4];
 #pragma unroll
@@ -719,13 +759,8 @@ __global__ void __launch_bounds__(kThreads) chain_kernel(DeltaArgs a)
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             u[t] = R[t] - u[t];      // u~
-            if constexpr (KEEP) {
-                if (col < a.DV) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        a.ut[((head * a.NC + c) * kC + 16 * t + 4 * (lane >> 4) + r) * a.DV + col] = u[t][r];
-                }
-            }
+            if constexpr (KEEP)
+                Sheet(a.ut + (head * a.NC + c) * kC * a.DV, kC, a.DV, col, lane).put(t, u[t]);
             u[t] *= row_vec(s_vec, kBeta, t, lane);
         }
         if constexpr (!KEEP) {
@@ -764,6 +799,358 @@ __global__ void __launch_bounds__(kThreads) chain_kernel(DeltaArgs a)
 }
 
 // ---------------------------------------------------------------------------
+// pipe_kernel: chain_kernel's walk for bf16 data, a workgroup of eight waves.
+// Waves 0..3 ("chain") own 16 columns of the state each and do only what the
+// next chunk waits for: u from S, then S.  Waves 4..7 ("help") stage the next
+// chunk's K, V, Z and vectors in the other half of LDS, and form the outputs
+// of the chunk before: each takes the columns of one chain wave, whose S and u
+// it gets in two bf16 parts through LDS.  One barrier a chunk; a flag says
+// when the parts of S are there.
+// ---------------------------------------------------------------------------
+enum Mode { kOut, kKeep, kScan };   // outputs; states and u~ kept; the last state alone
+
+constexpr int kPipeThreads = 512;
+
+template <int KD>
+struct PipeLds {
+    using K = Tile<KD, true>;
+    using V = Tile<kC, true>;
+    static constexpr int kSRow = KD + 8, kURow = kC + 4;
+    static constexpr int kSPart = 16 * kSRow, kUPart = 16 * kURow;
+    // in uint16_t
+    static constexpr int kK = 0;
+    static constexpr int kZ = kK + 2 * K::kSize;
+    static constexpr int kV = kZ + 2 * Tri<false>::kSize;
+    static constexpr int kVec = kV + 2 * V::kSize;
+    static constexpr int kFlag = kVec + 2 * 4 * kC * 2;
+    static constexpr int kS = kFlag + 8;                    // with outputs only
+    static constexpr int kU = kS + 4 * 2 * kSPart;
+    static constexpr size_t bytes(bool out) { return (out ? kU + 2 * 4 * 2 * kUPart : kS) * 2; }
+};
+
+template <int KD, int MODE>
+__global__ void __launch_bounds__(kPipeThreads, 1) pipe_kernel(DeltaArgs a)
+{
+    using LDS = PipeLds<KD>;
+    using TK = typename LDS::K;
+    using TV = typename LDS::V;
+    using L_ = Tri<false>;
+    constexpr int NS = KD / 32;     // k steps over the key dimensions
+    extern __shared__ __attribute__((aligned(16))) char s_dyn[];
+    uint16_t *lds = reinterpret_cast<uint16_t *>(s_dyn);
+    volatile int *s_flag = reinterpret_cast<volatile int *>(lds + LDS::kFlag);
+
+    // What this workgroup walks: chunks c0 .. c1 - 1 of 64 columns of a head's
+    // state, or (kScan) of 64 columns of the segment's transition, the state
+    // that the unit matrix becomes without any v.
+    const int per = MODE == kScan ? a.segs - 1 : a.segs, parts = a.slices + (MODE == kScan ? KD / 64 : 0);
+    const int64_t head = blockIdx.x / (unsigned)(per * parts);
+    const int rest = blockIdx.x % (unsigned)(per * parts), seg = rest / parts, slice = rest % parts;
+    const bool unit = slice >= a.slices;
+    if (unit && seg == 0)
+        return;
+    const int c0 = seg * a.seg_chunks, c1 = min(a.NC, c0 + a.seg_chunks);
+    int64_t b;
+    int h;
+    const int64_t hk = kv_head(a, head, b, h);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, i16 = lane & 15;
+    const int mine = wave & 3;      // the chain wave, or the one that this wave helps
+    const int col = (slice * 4 + mine) * 16 + i16;
+
+    if (wave < 4) {
+        State<KD> S;
+        if (unit) {
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    S.s[m][r] = 16 * m + 4 * g + r == col - a.slices * 64 ? 1.f : 0.f;
+        } else if (seg > 0 && MODE != kScan) {
+            S.load(a.seg_states + (head * a.segs + seg) * KD * a.DV, KD, a.DV, col, lane);
+        } else {
+            S.load(a.s0 && seg == 0 ? a.s0 + head * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, col, lane);
+        }
+        if (lane == 0)
+            s_flag[mine] = c0;
+        Frag<3> sf[NS];
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+            sf[s] = split<3>(S.s[2 * s], S.s[2 * s + 1]);
+        __syncthreads();
+        for (int c = c0; c < c1; ++c) {
+            const int half = (c - c0) & 1;
+            const uint16_t *s_k = lds + LDS::kK + half * TK::kSize, *s_z = lds + LDS::kZ + half * L_::kSize;
+            const uint16_t *s_v = lds + LDS::kV + half * TV::kSize;
+            const float *s_vec = reinterpret_cast<const float *>(lds + LDS::kVec) + half * 4 * kC;
+            Frag<1> kr[NS][4];
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    kr[s][t] = TK::rows_stacked(s_k, t, s, lane);
+            if constexpr (MODE == kOut) {
+                uint16_t *x = lds + LDS::kS + mine * 2 * LDS::kSPart + i16 * LDS::kSRow + 4 * g;
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int s = 0; s < NS; ++s) {
+                        const bf16x8 v = sf[s].p[n];
+                        *reinterpret_cast<bf16x4 *>(x + n * LDS::kSPart + 32 * s) = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+                        *reinterpret_cast<bf16x4 *>(x + n * LDS::kSPart + 32 * s + 16) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+                    }
+                lds_order();
+                if (lane == 0)
+                    s_flag[mine] = c + 1;
+                lds_order();
+            }
+            if constexpr (MODE == kKeep) {
+                const Sheet out(a.states + (head * a.NC + c) * KD * a.DV, KD, a.DV, col, lane);
+#pragma unroll
+                for (int m = 0; m < KD / 16; ++m)
+                    out.put(m, S.s[m]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+
+            // k S, while V and the first half of Z arrive
+            f32x4 R[4];
+            bf16x4 v4[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                R[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+                v4[t] = lds_column4(s_v + (16 * t + 4 * g + (i16 >> 2)) * TV::kRow + 16 * mine + 4 * (i16 & 3));
+            }
+            Frag<3> z0[4], z1[2];
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                if (s == NS / 2) {
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        z0[t] = L_::template get<3>(s_z, t, 0, lane);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+#pragma unroll
+                for (int n = 2; n >= 0; --n)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        R[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kr[s][t].p[0], sf[s].p[n], R[t], 0, 0, 0);
+            }
+            f32x4 x[4], u[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const f32x4 v = unit ? f32x4{0.f, 0.f, 0.f, 0.f} : __builtin_convertvector(v4[t], f32x4);
+                R[t] = v - row_vec(s_vec, kRise, t, lane) * R[t];
+                x[t] = row_vec(s_vec, kBeta, t, lane) * R[t];
+                u[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                z1[t] = L_::template get<3>(s_z, t + 2, 1, lane);
+            Frag<1> kc0[KD / 16], kc1[KD / 16];
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m)
+                kc0[m] = TK::columns_stacked(s_k, m, 0, lane);
+            __builtin_amdgcn_sched_barrier(0);
+            const Frag<3> f0 = split<3>(x[0], x[1]), f1 = split<3>(x[2], x[3]);
+#pragma unroll
+            for (int o = 2; o >= 0; --o)
+#pragma unroll
+                for (int i = 0; i <= o; ++i) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        u[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(z0[t].p[i], f0.p[o - i], u[t], 0, 0, 0);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        u[t + 2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(z1[t].p[i], f1.p[o - i], u[t + 2], 0, 0, 0);
+                }
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m)
+                kc1[m] = TK::columns_stacked(s_k, m, 1, lane);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                u[t] = R[t] - u[t];      // u~
+                if constexpr (MODE == kKeep)
+                    Sheet(a.ut + (head * a.NC + c) * kC * a.DV, kC, a.DV, col, lane).put(t, u[t]);
+                u[t] *= row_vec(s_vec, kBeta, t, lane);
+            }
+            if constexpr (MODE == kOut) {
+                uint16_t *y = lds + LDS::kU + ((half * 4 + mine) * 2) * LDS::kUPart + i16 * LDS::kURow + 4 * g;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    float v[4] = {u[t][0], u[t][1], u[t][2], u[t][3]};
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+                        *reinterpret_cast<uint2 *>(y + n * LDS::kUPart + 16 * t) =
+                            make_uint2(take_part(v[0], v[1], n < 1), take_part(v[2], v[3], n < 1));
+                }
+            }
+            const float whole = s_vec[kWhole * kC];
+            Frag<3> w0, w1;
+            w0 = split<3>(row_vec(s_vec, kLeft, 0, lane) * u[0], row_vec(s_vec, kLeft, 1, lane) * u[1]);
+            w1 = split<3>(row_vec(s_vec, kLeft, 2, lane) * u[2], row_vec(s_vec, kLeft, 3, lane) * u[3]);
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m)
+                S.s[m] *= whole;
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+#pragma unroll
+                for (int n = 2; n >= 0; --n)
+#pragma unroll
+                    for (int m = 2 * s; m < 2 * s + 2; ++m) {
+                        S.s[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc0[m].p[0], w0.p[n], S.s[m], 0, 0, 0);
+                        S.s[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc1[m].p[0], w1.p[n], S.s[m], 0, 0, 0);
+                    }
+                sf[s] = split<3>(S.s[2 * s], S.s[2 * s + 1]);
+            }
+            __syncthreads();
+        }
+        if constexpr (MODE == kScan)
+            S.store(a.trans + (head * a.segs + seg) * KD * (a.slices * 64 + KD), KD, a.slices * 64 + KD, col, lane);
+        else if (a.s_final && c1 == a.NC)
+            S.store(a.s_final + head * a.Dk * a.Dv, a.Dk, a.Dv, col, lane);
+    } else {
+        const int tid = threadIdx.x - 256;
+        const int64_t ek = b * a.k.s.b + hk * a.k.s.h, eq = b * a.q.s.b + hk * a.q.s.h;
+        const int64_t ev = b * a.v.s.b + h * a.v.s.h + (unit ? 0 : slice * 64);
+        const int vcols = unit ? a.Dv : a.Dv - slice * 64;
+        const float *rec = a.records + head * a.NC * (int64_t)a.record;
+        TK tk;
+        TV tv;
+        L_ tz;
+        f32x4 vecs;
+        auto fetch = [&](int c) {
+            const float *r = rec + (int64_t)c * a.record;
+            tk.load({a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk}, a.vk, tid);
+            tz.load(r + Record::kZ, tid);
+            tv.load({a.v.p, ev, a.v.s.l, c * kC, a.L, vcols}, a.vv, tid);
+            vecs = load_vecs(r + Record::kVec, tid);
+        };
+        auto stage = [&](int half) {
+            tk.store(lds + LDS::kK + half * TK::kSize, tid);
+            tz.store(lds + LDS::kZ + half * L_::kSize, tid);
+            tv.store(lds + LDS::kV + half * TV::kSize, tid);
+            if (tid < kC)
+                *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(lds + LDS::kVec) + half * 4 * kC + 4 * tid) = vecs;
+        };
+        L_::clear(lds + LDS::kZ, tid);
+        L_::clear(lds + LDS::kZ + L_::kSize, tid);
+        fetch(c0);
+        Unit<true> qf[MODE == kOut ? NS : 1][4];
+        f32x4 pf[MODE == kOut ? kBlocks : 1], qs[4];
+        auto fetch_q = [&](int c) {
+            const Chunk<true> cq(a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk);
+            const uint32_t e = cq.lane_at(i16, 8 * g);
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    qf[s][t] = cq.unit(e + 64 * s, i16, 16 * t, 32 * s + 8 * g, a.vq);
+        };
+        auto output = [&](int c) {     // from qs, pf and the u of chunk c
+            const uint16_t *y = lds + LDS::kU + ((((c - c0) & 1) * 4 + mine) * 2) * LDS::kUPart + i16 * LDS::kURow + 4 * g;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                Frag<2> f;
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+                    f.p[n] = lds_rows4(y + n * LDS::kUPart + 32 * s, y + n * LDS::kUPart + 32 * s + 16);
+#pragma unroll
+                for (int t = 2 * s; t < 4; ++t) {
+                    const Frag<2> p = split<2>(pf[block_of(t, 2 * s)],
+                                               t > 2 * s ? pf[block_of(t, 2 * s + 1)] : f32x4{0.f, 0.f, 0.f, 0.f});
+                    qs[t] = mma<2>(p, f, qs[t]);
+                }
+            }
+            const Chunk<true> co(a.o.p, b * a.o.s.b + h * a.o.s.h, a.o.s.l, c * kC, a.L, a.Dv);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                store_cols<true>(co, col, lane, t, qs[t]);
+        };
+        stage(0);
+        if (c0 + 1 < c1)
+            fetch(c0 + 1);
+        if constexpr (MODE == kOut)
+            fetch_q(c0);
+        __syncthreads();
+        for (int c = c0; c < c1; ++c) {
+            const int half = (c - c0) & 1;
+            if (c + 1 < c1) {
+                stage(half ^ 1);
+                if (c + 2 < c1)
+                    fetch(c + 2);
+            }
+            if constexpr (MODE == kOut) {
+                if (c > c0)
+                    output(c - 1);
+                const float *P = rec + (int64_t)c * a.record + Record::kP;
+#pragma unroll
+                for (int t = 0; t < kBlocks; ++t)
+                    pf[t] = *reinterpret_cast<const f32x4 *>(P + t * kBlock + 4 * lane);
+                while (s_flag[mine] <= c)
+                    __builtin_amdgcn_s_sleep(1);
+                lds_order();
+                const uint16_t *x = lds + LDS::kS + mine * 2 * LDS::kSPart + i16 * LDS::kSRow + 8 * g;
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    qs[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int s = 0; s < NS; ++s) {
+                    const bf16x8 hi = lds_row8(x + 32 * s), lo = lds_row8(x + LDS::kSPart + 32 * s);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        qs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(unit_frag<true>(qf[s][t]).p[0], lo, qs[t], 0, 0, 0);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        qs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(unit_frag<true>(qf[s][t]).p[0], hi, qs[t], 0, 0, 0);
+                }
+                const float *s_vec = reinterpret_cast<const float *>(lds + LDS::kVec) + half * 4 * kC;
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    qs[t] *= a.scale * row_vec(s_vec, kRise, t, lane);
+                if (c + 1 < c1)
+                    fetch_q(c + 1);
+            }
+            __syncthreads();
+        }
+        if constexpr (MODE == kOut)
+            output(c1 - 1);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// join_kernel: the states before segments 1 .. segs - 1 of a head, from the
+// segments' transitions A and ends B: S <- A S + B.  A wave owns 16 columns.
+// ---------------------------------------------------------------------------
+template <int KD>
+__global__ void __launch_bounds__(kThreads) join_kernel(DeltaArgs a)
+{
+    const int64_t head = blockIdx.x / (unsigned)a.slices;
+    const int slice = blockIdx.x % (unsigned)a.slices;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, i16 = lane & 15;
+    const int col = (slice * 4 + wave) * 16 + i16, pitch = a.slices * 64 + KD;
+    const float *T = a.trans + head * a.segs * KD * (int64_t)pitch;
+    State<KD> S, N;
+    S.load(T, KD, pitch, col, lane);
+    for (int seg = 1;; ++seg) {
+        S.store(a.seg_states + (head * a.segs + seg) * KD * a.DV, KD, a.DV, col, lane);
+        if (seg + 1 >= a.segs)
+            break;
+        const float *t = T + (int64_t)seg * KD * pitch, *A = t + a.slices * 64;
+        N.load(t, KD, pitch, col, lane);
+#pragma unroll
+        for (int s = 0; s < KD / 32; ++s) {
+            const Frag<3> f = split<3>(S.s[2 * s], S.s[2 * s + 1]);
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m) {
+                const float *p = A + (16 * m + i16) * pitch + 32 * s + 4 * g;
+                N.s[m] = mma<3>(split<3>(*reinterpret_cast<const f32x4 *>(p), *reinterpret_cast<const f32x4 *>(p + 16)), f, N.s[m]);
+            }
+        }
+        S = N;
+    }
+}
+
+// ---------------------------------------------------------------------------
 // reverse_kernel: the chunks of a head from the last to the first, with the
 // gradient of the state in registers.  Writes dV, keeps w and the gradients
 // of the states after the chunks.
@@ -798,23 +1185,23 @@ __global__ void __launch_bounds__(kThreads) reverse_kernel(DeltaArgs a)
     f32x4 tv;
     auto fetch = [&](int c) {
         const float *r = rec + (int64_t)c * a.record;
-        tk.load({a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk}, a.vk);
-        tq.load({a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk}, a.vq);
-        tz.load(r + Record::kZt);
-        tp.load(r + Record::kP);
-        tv = load_vecs(r + Record::kVec);
+        tk.load({a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk}, a.vk, threadIdx.x);
+        tq.load({a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk}, a.vq, threadIdx.x);
+        tz.load(r + Record::kZt, threadIdx.x);
+        tp.load(r + Record::kP, threadIdx.x);
+        tv = load_vecs(r + Record::kVec, threadIdx.x);
         v.load({a.d_o.p, eo, a.d_o.s.l, c * kC, a.L, a.Dv}, col, lane);
     };
     State<KD> S;
     S.load(a.ds_final ? a.ds_final + head * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, col, lane);
-    U_::clear(s_z);
-    U_::clear(s_p);
+    U_::clear(s_z, threadIdx.x);
+    U_::clear(s_p, threadIdx.x);
     fetch(a.NC - 1);
     for (int c = a.NC - 1; c >= 0; --c) {
-        tk.store(s_k);
-        tq.store(s_q);
-        tz.store(s_z);
-        tp.store(s_p);
+        tk.store(s_k, threadIdx.x);
+        tq.store(s_q, threadIdx.x);
+        tz.store(s_z, threadIdx.x);
+        tp.store(s_p, threadIdx.x);
         if (threadIdx.x < kC)
             *reinterpret_cast<f32x4 *>(s_vec + 4 * threadIdx.x) = tv;
         f32x4 dO[4];
@@ -825,7 +1212,12 @@ __global__ void __launch_bounds__(kThreads) reverse_kernel(DeltaArgs a)
         if (c > 0)
             fetch(c - 1);
 
-        S.store(a.grads + (head * a.NC + c) * KD * a.DV, KD, a.DV, col, lane);
+        {
+            const Sheet out(a.grads + (head * a.NC + c) * KD * a.DV, KD, a.DV, col, lane);
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m)
+                out.put(m, S.s[m]);
+        }
         f32x4 dU[4], x[4], w[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
@@ -862,11 +1254,7 @@ __global__ void __launch_bounds__(kThreads) reverse_kernel(DeltaArgs a)
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             w[t] = dU[t] - w[t];
-            if (col < a.DV) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    a.w[((head * a.NC + c) * kC + 16 * t + 4 * (lane >> 4) + r) * a.DV + col] = w[t][r];
-            }
+            Sheet(a.w + (head * a.NC + c) * kC * a.DV, kC, a.DV, col, lane).put(t, w[t]);
             w[t] *= row_vec(s_vec, kBeta, t, lane);     // dV
             store_cols<BF16>({a.dv.p, ev, a.dv.s.l, c * kC, a.L, a.Dv}, col, lane, t, w[t]);
             w[t] *= -row_vec(s_vec, kRise, t, lane);
@@ -946,10 +1334,10 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
 
     {
         T tk, tq;
-        tk.load({a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk}, a.vk);
-        tq.load({a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk}, a.vq);
-        tk.store(s_k);
-        tq.store(s_q);
+        tk.load({a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk}, a.vk, threadIdx.x);
+        tq.load({a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk}, a.vq, threadIdx.x);
+        tk.store(s_k, threadIdx.x);
+        tq.store(s_q, threadIdx.x);
     }
     f32x4 dq[4][NTC], dk[4][NTC];
 #pragma unroll
@@ -1305,32 +1693,71 @@ int check_delta_dims(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int32_t Dk, i
 }
 
 
-struct BwdLayout {
-    int64_t records, states, grads, ut, w, total;
-};
-
 int padded_key(int Dk) { return Dk <= 64 ? 64 : 128; }
 int padded_value(int Dv) { return (Dv + 31) / 32 * 32; }
 
-int64_t fwd_bytes(int64_t B, int64_t Hv, int64_t L)
+int slices_of(int Dv) { return (Dv + 63) / 64; }
+
+// How many segments the chunks of a head are cut into.  A walk takes its time
+// by the chunk, whether 16 or all 256 compute units walk, and cutting it adds
+// a walk without outputs and the joining of the segments.
+struct Cut {
+    int segs, chunks;
+};
+
+Cut cut_of(int64_t heads, int64_t L, int Dv, uint32_t flags)
 {
-    const int64_t chunks = B * Hv * ((L + kC - 1) / kC);
-    return (chunks > 0 ? chunks : 1) * Record::kFwd * 4;
+    const int64_t NC = (L + kC - 1) / kC, walks = heads * slices_of(Dv);
+    int64_t segs = 1;
+    if ((flags & PDSSM_DATA_BF16) && walks > 0 && walks * 4 <= 256 && NC >= 32) {
+        segs = 256 / walks;
+        if (segs > NC / 8)
+            segs = NC / 8;
+        if (segs > 32)
+            segs = 32;
+    }
+    Cut c;
+    c.chunks = (int)((NC + segs - 1) / segs);
+    if (c.chunks < 1)
+        c.chunks = 1;
+    c.segs = (int)((NC + c.chunks - 1) / c.chunks);
+    return c;
 }
 
-BwdLayout bwd_layout(int64_t B, int64_t Hv, int64_t L, int Dk, int Dv)
+struct Layout {
+    int64_t records, seg_states, trans, states, grads, ut, w, total;
+    Cut cut;
+};
+
+Layout layout_of(int64_t B, int64_t Hv, int64_t L, int Dk, int Dv, uint32_t flags, bool bwd)
 {
-    int64_t chunks = B * Hv * ((L + kC - 1) / kC);
+    const int64_t heads = B * Hv;
+    int64_t chunks = heads * ((L + kC - 1) / kC);
     chunks = chunks > 0 ? chunks : 1;
     const int64_t state = (int64_t)padded_key(Dk) * padded_value(Dv) * 4, rows = (int64_t)kC * padded_value(Dv) * 4;
-    BwdLayout l;
+    Layout l;
+    l.cut = cut_of(heads, L, Dv, flags);
+    const int64_t cuts = l.cut.segs > 1 ? heads * l.cut.segs : 0;
     l.records = 0;
-    l.states = chunks * Record::kBwd * 4;
-    l.grads = l.states + chunks * state;
-    l.ut = l.grads + chunks * state;
-    l.w = l.ut + chunks * rows;
-    l.total = l.w + chunks * rows;
+    l.seg_states = chunks * (bwd ? Record::kBwd : Record::kFwd) * 4;
+    l.trans = l.seg_states + cuts * state;
+    l.states = l.trans + cuts * padded_key(Dk) * (slices_of(Dv) * 64 + padded_key(Dk)) * 4;
+    l.grads = l.states + (bwd ? chunks * state : 0);
+    l.ut = l.grads + (bwd ? chunks * state : 0);
+    l.w = l.ut + (bwd ? chunks * rows : 0);
+    l.total = l.w + (bwd ? chunks * rows : 0);
     return l;
+}
+
+// The parts of the workspace that both directions have.
+void place_workspace(DeltaArgs &a, const Layout &l, void *workspace)
+{
+    char *ws = static_cast<char *>(workspace);
+    a.records = reinterpret_cast<float *>(ws + l.records);
+    a.seg_states = reinterpret_cast<float *>(ws + l.seg_states);
+    a.trans = reinterpret_cast<float *>(ws + l.trans);
+    a.segs = l.cut.segs;
+    a.seg_chunks = l.cut.chunks;
 }
 
 // Every row begins on 16 bytes and ends with a whole unit of eight values.
@@ -1352,7 +1779,7 @@ bool strides_ok(const pdssm_strides *s, int n)
 bool element_aligned(const void *p, int esize) { return ((uintptr_t)p & (uintptr_t)(esize - 1)) == 0; }
 
 template <typename K>
-int launch(K kernel, int64_t grid, size_t lds, const DeltaArgs &a, hipStream_t stream)
+int launch(K kernel, int64_t grid, size_t lds, const DeltaArgs &a, hipStream_t stream, int threads = kThreads)
 {
     // More than 64 KB of LDS has to be asked for; the device has 160 KB.
     if (lds > 65536) {
@@ -1361,7 +1788,7 @@ int launch(K kernel, int64_t grid, size_t lds, const DeltaArgs &a, hipStream_t s
         if (e != hipSuccess)
             return hip_status(e);
     }
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), lds, stream, a);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3((unsigned)threads), lds, stream, a);
     return hip_status(hipGetLastError());
 }
 
@@ -1379,21 +1806,45 @@ constexpr size_t grad_lds()
     return (size_t)(2 * Tile<KD, BF16>::kSize + 2 * Tile<kC, BF16>::kSize) * 2 + (kVecs * kC + 5 * kC + 4) * 4;
 }
 
+// The states before the segments, where the chunks are cut.
+template <int KD>
+int launch_segments(const DeltaArgs &a, hipStream_t stream)
+{
+    if (a.segs < 2)
+        return PDSSM_OK;
+    const int rc = launch(pipe_kernel<KD, kScan>, a.heads * (a.segs - 1) * (a.slices + KD / 64), PipeLds<KD>::bytes(false), a,
+                          stream, kPipeThreads);
+    return rc != PDSSM_OK ? rc : launch(join_kernel<KD>, a.heads * a.slices, 0, a, stream);
+}
+
 template <int KD, bool BF16>
 int launch_fwd(const DeltaArgs &a, hipStream_t stream)
 {
     int rc = launch(prep_kernel<KD, BF16, false>, a.heads * a.NC, 0, a, stream);
-    if (rc == PDSSM_OK)
-        rc = launch(chain_kernel<KD, BF16, false>, a.heads * a.slices, chain_lds<KD, BF16>(true), a, stream);
-    return rc;
+    if (rc != PDSSM_OK)
+        return rc;
+    if constexpr (BF16) {
+        rc = launch_segments<KD>(a, stream);
+        if (rc == PDSSM_OK)
+            rc = launch(pipe_kernel<KD, kOut>, a.heads * a.slices * a.segs, PipeLds<KD>::bytes(true), a, stream, kPipeThreads);
+        return rc;
+    } else {
+        return launch(chain_kernel<KD, BF16, false>, a.heads * a.slices, chain_lds<KD, BF16>(true), a, stream);
+    }
 }
 
 template <int KD, bool BF16>
 int launch_bwd(const DeltaArgs &a, hipStream_t stream)
 {
     int rc = launch(prep_kernel<KD, BF16, true>, a.heads * a.NC, 0, a, stream);
-    if (rc == PDSSM_OK)
+    if constexpr (BF16) {
+        if (rc == PDSSM_OK)
+            rc = launch_segments<KD>(a, stream);
+        if (rc == PDSSM_OK)
+            rc = launch(pipe_kernel<KD, kKeep>, a.heads * a.slices * a.segs, PipeLds<KD>::bytes(false), a, stream, kPipeThreads);
+    } else if (rc == PDSSM_OK) {
         rc = launch(chain_kernel<KD, BF16, true>, a.heads * a.slices, chain_lds<KD, BF16>(false), a, stream);
+    }
     if (rc == PDSSM_OK)
         rc = launch(reverse_kernel<KD, BF16>, a.heads * a.slices, chain_lds<KD, BF16>(true), a, stream);
     if (rc == PDSSM_OK)
@@ -1411,7 +1862,7 @@ extern "C" size_t pdssm_delta_workspace_bytes(int64_t B, int64_t Hk, int64_t Hv,
 {
     if (check_delta_dims(B, Hk, Hv, L, Dk, Dv) != PDSSM_OK || (flags & ~PDSSM_DATA_BF16))
         return 0;
-    return (size_t)fwd_bytes(B, Hv, L);
+    return (size_t)layout_of(B, Hv, L, Dk, Dv, flags, false).total;
 }
 
 extern "C" size_t pdssm_delta_bwd_workspace_bytes(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int32_t Dk,
@@ -1419,7 +1870,7 @@ extern "C" size_t pdssm_delta_bwd_workspace_bytes(int64_t B, int64_t Hk, int64_t
 {
     if (check_delta_dims(B, Hk, Hv, L, Dk, Dv) != PDSSM_OK || (flags & ~PDSSM_DATA_BF16))
         return 0;
-    return (size_t)bwd_layout(B, Hv, L, Dk, Dv).total;
+    return (size_t)layout_of(B, Hv, L, Dk, Dv, flags, true).total;
 }
 
 extern "C" int pdssm_delta_fwd(const void *q, const void *k, const void *v, const float *g, const float *beta,
@@ -1452,7 +1903,8 @@ extern "C" int pdssm_delta_fwd(const void *q, const void *k, const void *v, cons
             return PDSSM_ERR_ALIGN;
     if (!aligned16(workspace))
         return PDSSM_ERR_ALIGN;
-    if (workspace_bytes < (size_t)fwd_bytes(B, Hv, L))
+    const Layout lo = layout_of(B, Hv, L, Dk, Dv, flags, false);
+    if (workspace_bytes < (size_t)lo.total)
         return PDSSM_ERR_WORKSPACE;
     DeltaArgs a = {};
     const pdssm_strides keys = {Hk * L * Dk, L * Dk, Dk}, values = {Hv * L * Dv, L * Dv, Dv}, gates = {Hv * L, L, 1};
@@ -1461,10 +1913,11 @@ extern "C" int pdssm_delta_fwd(const void *q, const void *k, const void *v, cons
     if (!strides_ok(s, 6))
         return PDSSM_ERR_DIM;
     a.q = {q, s[0]}, a.k = {k, s[1]}, a.v = {v, s[2]}, a.g = {g, s[3]}, a.beta = {beta, s[4]}, a.o = {o, s[5]};
-    a.s0 = s0, a.s_final = s_final, a.records = static_cast<float *>(workspace), a.record = Record::kFwd;
+    a.s0 = s0, a.s_final = s_final, a.record = Record::kFwd;
+    place_workspace(a, lo, workspace);
     a.heads = B * Hv, a.Hk = (int)Hk, a.Hv = (int)Hv, a.L = (int)L, a.NC = (int)((L + kC - 1) / kC);
-    a.Dk = Dk, a.Dv = Dv, a.DV = padded_value(Dv), a.slices = (Dv + 63) / 64, a.scale = scale;
-    a.vq = units(q, s[0], Dk, esize), a.vk = units(k, s[1], Dk, esize);
+    a.Dk = Dk, a.Dv = Dv, a.DV = padded_value(Dv), a.slices = slices_of(Dv), a.scale = scale;
+    a.vq = units(q, s[0], Dk, esize), a.vk = units(k, s[1], Dk, esize), a.vv = units(v, s[2], Dv, esize);
     if (esize == 2)
         return Dk <= 64 ? launch_fwd<64, true>(a, stream) : launch_fwd<128, true>(a, stream);
     return Dk <= 64 ? launch_fwd<64, false>(a, stream) : launch_fwd<128, false>(a, stream);
@@ -1502,7 +1955,7 @@ extern "C" int pdssm_delta_bwd(const void *q, const void *k, const void *v, cons
             return PDSSM_ERR_ALIGN;
     if (!aligned16(workspace))
         return PDSSM_ERR_ALIGN;
-    const BwdLayout lo = bwd_layout(B, Hv, L, Dk, Dv);
+    const Layout lo = layout_of(B, Hv, L, Dk, Dv, flags, true);
     if (workspace_bytes < (size_t)lo.total)
         return PDSSM_ERR_WORKSPACE;
     DeltaArgs a = {};
@@ -1514,14 +1967,14 @@ extern "C" int pdssm_delta_bwd(const void *q, const void *k, const void *v, cons
         return PDSSM_ERR_DIM;
     a.dq = {dq, s[6]}, a.dk = {dk, s[7]}, a.dv = {dv, s[8]}, a.dg = {dg, s[9]}, a.dbeta = {dbeta, s[10]};
     a.s0 = s0, a.ds_final = ds_final, a.ds0 = ds0, a.record = Record::kBwd;
+    place_workspace(a, lo, workspace);
     char *ws = static_cast<char *>(workspace);
-    a.records = reinterpret_cast<float *>(ws + lo.records);
     a.states = reinterpret_cast<float *>(ws + lo.states);
     a.grads = reinterpret_cast<float *>(ws + lo.grads);
     a.ut = reinterpret_cast<float *>(ws + lo.ut);
     a.w = reinterpret_cast<float *>(ws + lo.w);
     a.heads = B * Hv, a.Hk = (int)Hk, a.Hv = (int)Hv, a.L = (int)L, a.NC = (int)((L + kC - 1) / kC);
-    a.Dk = Dk, a.Dv = Dv, a.DV = padded_value(Dv), a.slices = (Dv + 63) / 64, a.scale = scale;
+    a.Dk = Dk, a.Dv = Dv, a.DV = padded_value(Dv), a.slices = slices_of(Dv), a.scale = scale;
     a.vq = units(q, s[0], Dk, esize), a.vk = units(k, s[1], Dk, esize), a.vv = units(v, s[2], Dv, esize), a.vo = units(d_o, s[5], Dv, esize);
     if (esize == 2)
         return Dk <= 64 ? launch_bwd<64, true>(a, stream) : launch_bwd<128, true>(a, stream);
