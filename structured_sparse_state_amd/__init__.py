@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import re
 from typing import NamedTuple, Optional
@@ -547,58 +548,93 @@ def pdssm_qk_norm_rope_bwd_workspace_bytes(B, Hq, Hk, L, D) -> int:
     return library().pdssm_qk_norm_rope_bwd_workspace_bytes(B, Hq, Hk, L, D)
 
 
-def _data_flag(name: str, *tensors) -> int:
+# What a call's tensors must be, worked out once for every set of shapes,
+# strides and types (the plans below) and not again for every call: a decode
+# step's kernel takes about as long as these checks.
+
+def _data_flag(name: str, *dtypes) -> int:
     """The storage flag of tensors that must share one type, bf16 or fp32."""
-    dtype = tensors[0].dtype
-    if dtype not in (torch.bfloat16, torch.float32) or any(t.dtype != dtype for t in tensors):
+    if dtypes[0] not in (torch.bfloat16, torch.float32) or any(t != dtypes[0] for t in dtypes):
         raise ValueError(f"{name} must share one type, bf16 or fp32")
-    return PDSSM_DATA_BF16 if dtype == torch.bfloat16 else 0
+    return PDSSM_DATA_BF16 if dtypes[0] == torch.bfloat16 else 0
 
 
-def _f32(name: str, t, shape) -> None:
-    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name} must be fp32 {list(shape)}")
+def _form(t):
+    """Shape, strides and type of a tensor, or None."""
+    return None if t is None else (t.shape, t.stride(), t.dtype)
 
 
-def _state(name: str, t, shape) -> None:
-    _f32(name, t, shape)
-    if t is not None and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+def _want(name: str, form, shape, dtype, contiguous: bool = False) -> None:
+    if form is None:
+        return
+    if tuple(form[0]) != tuple(shape) or form[2] != dtype:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, not {form[2]} {list(form[0])}")
+    if contiguous:
+        step = 1
+        for n, st in zip(reversed(form[0]), reversed(form[1])):
+            if n > 1 and st != step:
+                raise ValueError(f"{name} must be contiguous")
+            step *= n
 
 
-def _shape(name: str, t, shape, dtype) -> None:
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {dtype} {list(shape)}")
-
-
-def _rows(*tensors):
-    """(b, h, l) strides of [B,H,L(,D)] tensors; D must be contiguous."""
+def _rows(dims: int, *forms):
+    """The pdssm_strides list of [B,H,L(,D)] tensors (dims 3), or of [B,H(,D)]
+    ones (dims 2); D must be contiguous."""
     out = []
-    for t in tensors:
-        s = t.stride()
-        if len(s) == 4 and s[3] != 1 and t.shape[3] > 1:
+    for shape, st, _ in forms:
+        if len(st) > dims and st[dims] != 1 and shape[dims] > 1:
             raise ValueError("the last dimension must be contiguous")
-        out.append(s[:3])
-    return out
+        out.append((*st[:dims], *(0,) * (3 - dims)))
+    return _strides(out)
 
 
-def _delta_sizes(q, k, v, g, beta):
-    flag = _data_flag("q, k and v", q, k, v)
-    B, Hk, L, Dk = q.shape
-    Hv, Dv = v.shape[1], v.shape[3]
-    if k.shape != q.shape or v.shape[0] != B or v.shape[2] != L:
-        raise ValueError("q and k must be [B,Hk,L,Dk] and v [B,Hv,L,Dv]")
-    _f32("g", g, (B, Hv, L))
-    _f32("beta", beta, (B, Hv, L))
-    return flag, B, Hk, Hv, L, Dk, Dv
+def _delta_form(q, k, v, g, beta, dims):
+    """Flag and sizes (B, Hk, Hv, L, Dk, Dv) of a call; L is 1 for a step."""
+    flag = _data_flag("q, k and v", q[2], k[2], v[2])
+    if len(q[0]) != dims + 1 or len(v[0]) != dims + 1:
+        raise ValueError("q, k and v must be [B,H,L,D] (a step: [B,H,D])")
+    B, Hk, *L, Dk = q[0]
+    Hv, Dv = v[0][1], v[0][-1]
+    _want("k", k, q[0], q[2])
+    _want("v", v, (B, Hv, *L, Dv), q[2])
+    _want("g", g, (B, Hv, *L), torch.float32)
+    _want("beta", beta, (B, Hv, *L), torch.float32)
+    return flag, B, Hk, Hv, (L[0] if L else 1), Dk, Dv
 
 
 def _workspace(need: int, workspace, device):
-    if need == 0:
-        raise PdssmError(PDSSM_ERR_DIM, "invalid sizes")
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"the workspace needs {need} bytes")
     return workspace
+
+
+def _need(n: int) -> int:
+    if n == 0:
+        raise PdssmError(PDSSM_ERR_DIM, "invalid sizes")
+    return n
+
+
+def _stream_of(t, stream) -> Optional[int]:
+    """`stream`, or the current stream of the tensor's device."""
+    if stream is not None:
+        return _stream(stream)
+    return _raw_stream(t.get_device()) if _raw_stream is not None and t.is_cuda else _stream(None)
+
+
+# The current stream's handle without building a Stream object, where this
+# torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+@functools.lru_cache(maxsize=1024)
+def _delta_plan(q, k, v, g, beta, o, s0, s_final):
+    flag, B, Hk, Hv, L, Dk, Dv = sizes = _delta_form(q, k, v, g, beta, 3)
+    _want("o", o, v[0], v[2])
+    _want("s0", s0, (B, Hv, Dk, Dv), torch.float32, True)
+    _want("s_final", s_final, (B, Hv, Dk, Dv), torch.float32, True)
+    return sizes, _rows(3, q, k, v, g, beta, o), _need(pdssm_delta_workspace_bytes(B, Hk, Hv, L, Dk, Dv, flag))
 
 
 def delta_rule(q, k, v, g, beta, s0=None, *, scale: Optional[float] = None, want_state: bool = True,
@@ -608,60 +644,67 @@ def delta_rule(q, k, v, g, beta, s0=None, *, scale: Optional[float] = None, want
     [B,Hv,Dk,Dv] or None).  q, k [B,Hk,L,Dk] and v [B,Hv,L,Dv] bf16 or fp32
     with any strides of the first three dimensions, g (log decay) and beta
     fp32 [B,Hv,L], s0 fp32 [B,Hv,Dk,Dv] or None; scale 1/sqrt(Dk) by default.
-    s_final may be s0."""
-    flag, B, Hk, Hv, L, Dk, Dv = _delta_sizes(q, k, v, g, beta)
-    _state("s0", s0, (B, Hv, Dk, Dv))
+    o has the memory order of v; s_final may be s0."""
     if o is None:
-        o = torch.empty((B, Hv, L, Dv), dtype=v.dtype, device=v.device)
-    else:
-        _shape("o", o, (B, Hv, L, Dv), v.dtype)
-    if s_final is not None:
-        _state("s_final", s_final, (B, Hv, Dk, Dv))
-    elif want_state:
-        s_final = torch.empty((B, Hv, Dk, Dv), dtype=torch.float32, device=v.device)
-    workspace = _workspace(pdssm_delta_workspace_bytes(B, Hk, Hv, L, Dk, Dv, flag), workspace, v.device)
-    check(pdssm_delta_fwd(q, k, v, g, beta, s0, o, s_final, B, Hk, Hv, L, Dk, Dv,
-                          Dk ** -0.5 if scale is None else scale, flag, _rows(q, k, v, g, beta, o),
-                          workspace, workspace.numel(), stream))
+        o = torch.empty_like(v)
+    if s_final is None and want_state:
+        s_final = torch.empty((v.shape[0], v.shape[1], q.shape[-1], v.shape[-1]), dtype=torch.float32,
+                              device=v.device)
+    (flag, B, Hk, Hv, L, Dk, Dv), rows, need = _delta_plan(
+        _form(q), _form(k), _form(v), _form(g), _form(beta), _form(o), _form(s0), _form(s_final))
+    workspace = _workspace(need, workspace, v.device)
+    check(library().pdssm_delta_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                    beta.data_ptr(), _ptr(s0), o.data_ptr(), _ptr(s_final), B, Hk, Hv, L,
+                                    Dk, Dv, Dk ** -0.5 if scale is None else scale, flag, rows,
+                                    workspace.data_ptr(), need, _stream_of(v, stream)))
     return o, s_final
+
+
+@functools.lru_cache(maxsize=1024)
+def _delta_bwd_plan(q, k, v, g, beta, s0, do, ds_final, dq, dk, dv, dg, dbeta, ds0):
+    flag, B, Hk, Hv, L, Dk, Dv = sizes = _delta_form(q, k, v, g, beta, 3)
+    for name, form, like in (("do", do, v), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v), ("dg", dg, g),
+                             ("dbeta", dbeta, g)):
+        _want(name, form, like[0], like[2])
+    for name, form in (("s0", s0), ("ds_final", ds_final), ("ds0", ds0)):
+        _want(name, form, (B, Hv, Dk, Dv), torch.float32, True)
+    return (sizes, _rows(3, q, k, v, g, beta, do, dq, dk, dv, dg, dbeta),
+            _need(pdssm_delta_bwd_workspace_bytes(B, Hk, Hv, L, Dk, Dv, flag)))
 
 
 def delta_rule_bwd(q, k, v, g, beta, do, s0=None, ds_final=None, *, scale: Optional[float] = None,
                    want_ds0: bool = True, out=None, workspace: Optional[torch.Tensor] = None,
                    stream=None):
     """Gradients of delta_rule from its inputs, the gradient ``do`` of o and
-    that of s_final (None: zero): (dq, dk, dv, dg, dbeta, ds0 or None).
-    ``out`` may hold a previous call's result to write into."""
-    flag, B, Hk, Hv, L, Dk, Dv = _delta_sizes(q, k, v, g, beta)
-    _state("s0", s0, (B, Hv, Dk, Dv))
-    _state("ds_final", ds_final, (B, Hv, Dk, Dv))
-    _shape("do", do, v.shape, v.dtype)
+    that of s_final (None: zero): (dq, dk, dv, dg, dbeta, ds0 or None), each
+    in the memory order of its input.  ``out`` may hold a previous call's
+    result to write into."""
     if out is not None:
         dq, dk, dv, dg, dbeta, ds0 = out
-        for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v), ("dg", dg, g), ("dbeta", dbeta, g)):
-            _shape(name, t, like.shape, like.dtype)
-        _state("ds0", ds0, (B, Hv, Dk, Dv))
     else:
-        dq, dk, dv, dg, dbeta = (torch.empty(t.shape, dtype=t.dtype, device=t.device)
-                                 for t in (q, k, v, g, beta))
-        ds0 = torch.empty((B, Hv, Dk, Dv), dtype=torch.float32, device=v.device) if want_ds0 else None
-    workspace = _workspace(pdssm_delta_bwd_workspace_bytes(B, Hk, Hv, L, Dk, Dv, flag), workspace, v.device)
-    check(pdssm_delta_bwd(q, k, v, g, beta, s0, do, ds_final, dq, dk, dv, dg, dbeta, ds0, B, Hk, Hv, L,
-                          Dk, Dv, Dk ** -0.5 if scale is None else scale, flag,
-                          _rows(q, k, v, g, beta, do, dq, dk, dv, dg, dbeta), workspace,
-                          workspace.numel(), stream))
+        dq, dk, dv, dg, dbeta = (torch.empty_like(t) for t in (q, k, v, g, beta))
+        ds0 = torch.empty((v.shape[0], v.shape[1], q.shape[-1], v.shape[-1]), dtype=torch.float32,
+                          device=v.device) if want_ds0 else None
+    (flag, B, Hk, Hv, L, Dk, Dv), rows, need = _delta_bwd_plan(
+        _form(q), _form(k), _form(v), _form(g), _form(beta), _form(s0), _form(do), _form(ds_final),
+        _form(dq), _form(dk), _form(dv), _form(dg), _form(dbeta), _form(ds0))
+    workspace = _workspace(need, workspace, v.device)
+    check(library().pdssm_delta_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                    beta.data_ptr(), _ptr(s0), do.data_ptr(), _ptr(ds_final),
+                                    dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(),
+                                    dbeta.data_ptr(), _ptr(ds0), B, Hk, Hv, L, Dk, Dv,
+                                    Dk ** -0.5 if scale is None else scale, flag, rows,
+                                    workspace.data_ptr(), need, _stream_of(v, stream)))
     return dq, dk, dv, dg, dbeta, ds0
 
 
-def _head_rows(*tensors):
-    """(b, h, 0) strides of [B,H(,D)] tensors; D must be contiguous."""
-    out = []
-    for t in tensors:
-        s = t.stride()
-        if len(s) == 3 and s[2] != 1 and t.shape[2] > 1:
-            raise ValueError("the last dimension must be contiguous")
-        out.append((s[0], s[1], 0))
-    return out
+@functools.lru_cache(maxsize=1024)
+def _step_plan(q, k, v, g, beta, o, s, s_out):
+    flag, B, Hk, Hv, _, Dk, Dv = _delta_form(q, k, v, g, beta, 2)
+    _want("o", o, v[0], v[2])
+    _want("s", s, (B, Hv, Dk, Dv), torch.float32, True)
+    _want("s_out", s_out, (B, Hv, Dk, Dv), torch.float32, True)
+    return flag, B, Hk, Hv, Dk, Dv, _rows(2, q, k, v, g, beta, o)
 
 
 def delta_step(q, k, v, g, beta, s, *, s_out: Optional[torch.Tensor] = None,
@@ -669,25 +712,16 @@ def delta_step(q, k, v, g, beta, s, *, s_out: Optional[torch.Tensor] = None,
     """One step of the gated delta rule: o [B,Hv,Dv] from q, k [B,Hk,Dk],
     v [B,Hv,Dv], g, beta fp32 [B,Hv] and the state s fp32 [B,Hv,Dk,Dv], which
     is updated in place, or into s_out."""
-    flag = _data_flag("q, k and v", q, k, v)
-    B, Hk, Dk = q.shape
-    Hv, Dv = v.shape[1], v.shape[2]
-    if k.shape != q.shape or v.shape[0] != B:
-        raise ValueError("q and k must be [B,Hk,Dk] and v [B,Hv,Dv]")
-    _f32("g", g, (B, Hv))
-    _f32("beta", beta, (B, Hv))
-    _state("s", s, (B, Hv, Dk, Dv))
     if s_out is None:
         s_out = s
-    else:
-        _state("s_out", s_out, (B, Hv, Dk, Dv))
     if o is None:
-        o = torch.empty((B, Hv, Dv), dtype=v.dtype, device=v.device)
-    else:
-        _shape("o", o, (B, Hv, Dv), v.dtype)
-    check(pdssm_delta_step(q, k, v, g, beta, s, o, s_out, B, Hk, Hv, Dk, Dv,
-                           Dk ** -0.5 if scale is None else scale, flag,
-                           _head_rows(q, k, v, g, beta, o), stream))
+        o = torch.empty_like(v)
+    flag, B, Hk, Hv, Dk, Dv, rows = _step_plan(_form(q), _form(k), _form(v), _form(g), _form(beta),
+                                               _form(o), _form(s), _form(s_out))
+    check(library().pdssm_delta_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                     beta.data_ptr(), s.data_ptr(), o.data_ptr(), s_out.data_ptr(), B, Hk,
+                                     Hv, Dk, Dv, Dk ** -0.5 if scale is None else scale, flag, rows,
+                                     _stream_of(v, stream)))
     return o
 
 
@@ -695,21 +729,31 @@ _NORM_KIND = {"rms": 0, "l2": PDSSM_NORM_L2}
 _ROPE_PAIRS = {"half": 0, "adjacent": PDSSM_ROPE_PAIRS}
 
 
-def _norm_sizes(q, k, wq, wk, cos, sin, pos, kind, pairs):
-    flags = _data_flag("q and k", q, k) | _NORM_KIND[kind] | _ROPE_PAIRS[pairs]
-    B, Hq, L, D = q.shape
-    if k.shape[0] != B or k.shape[2] != L or k.shape[3] != D:
-        raise ValueError("q must be [B,Hq,L,D] and k [B,Hk,L,D]")
-    for name, w in (("wq", wq), ("wk", wk)):
-        _state(name, w, (D,))
-    P, R = (0, 0) if cos is None else (cos.shape[0], 2 * cos.shape[1])
+def _norm_form(q, k, wq, wk, cos, sin, pos, kind, pairs):
+    """Flags and sizes (B, Hq, Hk, L, D, R, P) of a call."""
+    flags = _data_flag("q and k", q[2], k[2]) | _NORM_KIND[kind] | _ROPE_PAIRS[pairs]
+    if len(q[0]) != 4 or len(k[0]) != 4:
+        raise ValueError("q and k must be [B,H,L,D]")
+    B, Hq, L, D = q[0]
+    Hk = k[0][1]
+    _want("k", k, (B, Hk, L, D), q[2])
+    _want("wq", wq, (D,), torch.float32, True)
+    _want("wk", wk, (D,), torch.float32, True)
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
-    _state("cos", cos, (P, R // 2))
-    _state("sin", sin, (P, R // 2))
-    if pos is not None and (pos.dtype != torch.int32 or tuple(pos.shape) != (B, L) or not pos.is_contiguous()):
-        raise ValueError("pos must be contiguous int32 [B,L]")
-    return flags, B, Hq, k.shape[1], L, D, R, P
+    P, R = (0, 0) if cos is None else (cos[0][0], 2 * cos[0][1])
+    _want("cos", cos, (P, R // 2), torch.float32, True)
+    _want("sin", sin, (P, R // 2), torch.float32, True)
+    _want("pos", pos, (B, L), torch.int32, True)
+    return flags, B, Hq, Hk, L, D, R, P
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_plan(q, k, wq, wk, cos, sin, pos, kind, pairs, q_out, k_out):
+    sizes = _norm_form(q, k, wq, wk, cos, sin, pos, kind, pairs)
+    _want("q_out", q_out, q[0], q[2])
+    _want("k_out", k_out, k[0], k[2])
+    return sizes, _rows(3, q, k, q_out, k_out)
 
 
 def qk_norm_rope(q, k, wq=None, wk=None, cos=None, sin=None, pos=None, *, kind: str = "rms",
@@ -720,41 +764,47 @@ def qk_norm_rope(q, k, wq=None, wk=None, cos=None, sin=None, pos=None, *, kind: 
     weights fp32 [D] or None; cos, sin fp32 [P,R/2] or None (no rotation); pos
     int32 [B,L] or None (the place in the sequence).  ``kind``: "rms" or "l2"
     (unit length); ``pairs``: "half" (i, i + R/2) or "adjacent" (2i, 2i + 1).
-    ``out``: the two results to write into (the inputs, to work in place)."""
-    flags, B, Hq, Hk, L, D, R, P = _norm_sizes(q, k, wq, wk, cos, sin, pos, kind, pairs)
-    if out is None:
-        q_out = torch.empty((B, Hq, L, D), dtype=q.dtype, device=q.device)
-        k_out = torch.empty((B, Hk, L, D), dtype=k.dtype, device=k.device)
-    else:
-        q_out, k_out = out
-        _shape("q_out", q_out, q.shape, q.dtype)
-        _shape("k_out", k_out, k.shape, k.dtype)
-    check(pdssm_qk_norm_rope_fwd(q, k, wq, wk, cos, sin, pos, q_out, k_out, B, Hq, Hk, L, D, R, P, eps,
-                                 flags, _rows(q, k, q_out, k_out), stream))
+    The results have the memory order of q and k; ``out``: two tensors to
+    write into instead (the inputs, to work in place)."""
+    q_out, k_out = (torch.empty_like(q), torch.empty_like(k)) if out is None else out
+    (flags, B, Hq, Hk, L, D, R, P), rows = _norm_plan(
+        _form(q), _form(k), _form(wq), _form(wk), _form(cos), _form(sin), _form(pos), kind, pairs,
+        _form(q_out), _form(k_out))
+    check(library().pdssm_qk_norm_rope_fwd(q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(cos),
+                                           _ptr(sin), _ptr(pos), q_out.data_ptr(), k_out.data_ptr(), B,
+                                           Hq, Hk, L, D, R, P, eps, flags, rows, _stream_of(q, stream)))
     return q_out, k_out
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_bwd_plan(q, k, wq, wk, cos, sin, pos, kind, pairs, dq_out, dk_out, dq, dk):
+    flags, B, Hq, Hk, L, D, R, P = sizes = _norm_form(q, k, wq, wk, cos, sin, pos, kind, pairs)
+    for name, form, like in (("dq_out", dq_out, q), ("dk_out", dk_out, k), ("dq", dq, q), ("dk", dk, k)):
+        _want(name, form, like[0], like[2])
+    need = 0
+    if wq is not None or wk is not None:
+        need = _need(pdssm_qk_norm_rope_bwd_workspace_bytes(B, Hq, Hk, L, D))
+    return sizes, _rows(3, q, k, dq_out, dk_out, dq, dk), need
 
 
 def qk_norm_rope_bwd(q, k, dq_out, dk_out, wq=None, wk=None, cos=None, sin=None, pos=None, *,
                      kind: str = "rms", pairs: str = "half", eps: float = 1e-6, out=None,
                      workspace: Optional[torch.Tensor] = None, stream=None):
     """Gradients of qk_norm_rope from its inputs and the gradients of its
-    outputs: (dq, dk, dwq, dwk), the last two None where the weight is.
-    ``out``: dq and dk to write into (dq_out and dk_out, to work in place)."""
-    flags, B, Hq, Hk, L, D, R, P = _norm_sizes(q, k, wq, wk, cos, sin, pos, kind, pairs)
-    _shape("dq_out", dq_out, q.shape, q.dtype)
-    _shape("dk_out", dk_out, k.shape, k.dtype)
-    if out is None:
-        dq = torch.empty((B, Hq, L, D), dtype=q.dtype, device=q.device)
-        dk = torch.empty((B, Hk, L, D), dtype=k.dtype, device=k.device)
-    else:
-        dq, dk = out
-        _shape("dq", dq, q.shape, q.dtype)
-        _shape("dk", dk, k.shape, k.dtype)
-    dwq, dwk = (None if w is None else torch.empty((D,), dtype=torch.float32, device=q.device)
-                for w in (wq, wk))
-    if wq is not None or wk is not None:
-        workspace = _workspace(pdssm_qk_norm_rope_bwd_workspace_bytes(B, Hq, Hk, L, D), workspace, q.device)
-    check(pdssm_qk_norm_rope_bwd(q, k, wq, wk, cos, sin, pos, dq_out, dk_out, dq, dk, dwq, dwk, B, Hq,
-                                 Hk, L, D, R, P, eps, flags, _rows(q, k, dq_out, dk_out, dq, dk),
-                                 workspace, 0 if workspace is None else workspace.numel(), stream))
+    outputs: (dq, dk, dwq, dwk), the first two in the memory order of q and k,
+    the last two None where the weight is.  ``out``: dq and dk to write into
+    instead (dq_out and dk_out, to work in place)."""
+    dq, dk = (torch.empty_like(q), torch.empty_like(k)) if out is None else out
+    (flags, B, Hq, Hk, L, D, R, P), rows, need = _norm_bwd_plan(
+        _form(q), _form(k), _form(wq), _form(wk), _form(cos), _form(sin), _form(pos), kind, pairs,
+        _form(dq_out), _form(dk_out), _form(dq), _form(dk))
+    dwq, dwk = (None if w is None else torch.empty_like(w) for w in (wq, wk))
+    if need:
+        workspace = _workspace(need, workspace, q.device)
+    check(library().pdssm_qk_norm_rope_bwd(q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(cos),
+                                           _ptr(sin), _ptr(pos), dq_out.data_ptr(), dk_out.data_ptr(),
+                                           dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), B, Hq, Hk,
+                                           L, D, R, P, eps, flags, rows,
+                                           workspace.data_ptr() if need else None, need,
+                                           _stream_of(q, stream)))
     return dq, dk, dwq, dwk

@@ -88,7 +88,6 @@ struct DeltaArgs {
     int Hk, Hv, L, NC, Dk, Dv, DV, record;
     int slices;             // column slices of a head over workgroups
     float scale;
-    bool vq, vk, vv, vo;    // rows of q, k, v, d_o can be read in 16 bytes
 };
 
 // ---------------------------------------------------------------------------
@@ -139,12 +138,13 @@ struct Chunk {
     {
         return row + up < rows && col < D ? lane + up * stride : kOutside;
     }
-    // Values col .. col + 7 of a row; `vec`: rows begin on 16 bytes and hold
+    // Values col .. col + 7 of a row; VEC: rows begin on 16 bytes and hold
     // whole units.
-    __device__ __forceinline__ Unit<BF16> unit(uint32_t lane, int row, int up, int col, bool vec) const
+    template <bool VEC>
+    __device__ __forceinline__ Unit<BF16> unit(uint32_t lane, int row, int up, int col) const
     {
         Unit<BF16> u;
-        if (vec) {
+        if constexpr (VEC) {
             const uint32_t e = at(lane, row, up, col);
             const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, e, 0, 0);
             __builtin_memcpy(&u.v, &v, 16);
@@ -165,9 +165,10 @@ struct Chunk {
         }
         return u;
     }
-    __device__ __forceinline__ Unit<BF16> unit(int row, int col, bool vec) const
+    template <bool VEC>
+    __device__ __forceinline__ Unit<BF16> unit(int row, int col) const
     {
-        return unit(lane_at(row, col), row, 0, col, vec);
+        return unit<VEC>(lane_at(row, col), row, 0, col);
     }
     __device__ __forceinline__ uint32_t raw(uint32_t lane, int row, int up, int col) const
     {
@@ -222,13 +223,14 @@ struct Tile {
     Unit<BF16> u[kUnits];
 
     // `tid`: the thread's number among the NT that share the tile.
-    __device__ __forceinline__ void load(const Chunk<BF16> &c, bool vec, int tid)
+    template <bool VEC>
+    __device__ __forceinline__ void load(const Chunk<BF16> &c, int tid)
     {
         const int row = tid / (KD / 8), col = tid % (KD / 8) * 8;
         const uint32_t lane = c.lane_at(row, col);
 #pragma unroll
         for (int i = 0; i < kUnits; ++i)
-            u[i] = c.unit(lane, row, i * (NT * 8 / KD), col, vec);
+            u[i] = c.template unit<VEC>(lane, row, i * (NT * 8 / KD), col);
     }
     __device__ __forceinline__ void store(uint16_t *lds, int tid) const
     {
@@ -310,7 +312,7 @@ __device__ __forceinline__ int64_t kv_head(const DeltaArgs &a, int64_t head, int
 // ---------------------------------------------------------------------------
 constexpr int kMat = 68;        // row of a 64 x 64 fp32 matrix in LDS
 
-template <int KD, bool BF16, bool BWD>
+template <int KD, bool BF16, bool VEC, bool BWD>
 __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
 {
     using T = Tile<KD, BF16>;
@@ -333,8 +335,8 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
 
     {
         T q, k;
-        k.load({a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk}, a.vk, threadIdx.x);
-        q.load({a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk}, a.vq, threadIdx.x);
+        k.template load<VEC>({a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk}, threadIdx.x);
+        q.template load<VEC>({a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk}, threadIdx.x);
         if (wave == 0) {
             // G in 64 bits (differences of neighbours stay exact to 32), steps
             // with g = -inf counted apart.
@@ -658,7 +660,7 @@ __device__ __forceinline__ f32x4 row_vec(const float *s_vec, int which, int a, i
 // chain_kernel: the chunks of a head in order.  KEEP: the backward's pass,
 // which keeps the states before the chunks and u~ and forms no outputs.
 // ---------------------------------------------------------------------------
-template <int KD, bool BF16, bool KEEP>
+template <int KD, bool BF16, bool VEC, bool KEEP>
 __global__ void __launch_bounds__(kThreads) chain_kernel(DeltaArgs a)
 {
     using T = Tile<KD, BF16>;
@@ -689,12 +691,12 @@ __global__ void __launch_bounds__(kThreads) chain_kernel(DeltaArgs a)
     f32x4 tv;
     auto fetch = [&](int c) {
         const float *r = rec + (int64_t)c * a.record;
-        tk.load({a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk}, a.vk, threadIdx.x);
+        tk.template load<VEC>({a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk}, threadIdx.x);
         tz.load(r + Record::kZ, threadIdx.x);
         tv = load_vecs(r + Record::kVec, threadIdx.x);
         v.load({a.v.p, ev, a.v.s.l, c * kC, a.L, a.Dv}, col, lane);
         if constexpr (!KEEP) {
-            tq.load({a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk}, a.vq, threadIdx.x);
+            tq.template load<VEC>({a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk}, threadIdx.x);
             tp.load(r + Record::kP, threadIdx.x);
         }
     };
@@ -717,7 +719,7 @@ __global__ void __launch_bounds__(kThreads) chain_kernel(DeltaArgs a)
 #pragma unroll
         for (int t = 0; t < 4; ++t)
             R[t] = v.get(t);
-        __syncthreads();
+        lds_barrier();
         if (c + 1 < a.NC)
             fetch(c + 1);
 
@@ -792,7 +794,7 @@ __global__ void __launch_bounds__(kThreads) chain_kernel(DeltaArgs a)
             for (int m = 0; m < KD / 16; ++m)
                 S.s[m] = mma<3>(T::columns_stacked(s_k, m, s, lane), f, S.s[m]);
         }
-        __syncthreads();
+        lds_barrier();
     }
     if (!KEEP && a.s_final)
         S.store(a.s_final + head * a.Dk * a.Dv, a.Dk, a.Dv, col, lane);
@@ -828,7 +830,7 @@ struct PipeLds {
     static constexpr size_t bytes(bool out) { return (out ? kU + 2 * 4 * 2 * kUPart : kS) * 2; }
 };
 
-template <int KD, int MODE>
+template <int KD, bool VEC, int MODE>
 __global__ void __launch_bounds__(kPipeThreads, 1) pipe_kernel(DeltaArgs a)
 {
     using LDS = PipeLds<KD>;
@@ -876,7 +878,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) pipe_kernel(DeltaArgs a)
 #pragma unroll
         for (int s = 0; s < NS; ++s)
             sf[s] = split<3>(S.s[2 * s], S.s[2 * s + 1]);
-        __syncthreads();
+        lds_barrier();
         for (int c = c0; c < c1; ++c) {
             const int half = (c - c0) & 1;
             const uint16_t *s_k = lds + LDS::kK + half * TK::kSize, *s_z = lds + LDS::kZ + half * L_::kSize;
@@ -1002,7 +1004,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) pipe_kernel(DeltaArgs a)
                     }
                 sf[s] = split<3>(S.s[2 * s], S.s[2 * s + 1]);
             }
-            __syncthreads();
+            lds_barrier();
         }
         if constexpr (MODE == kScan)
             S.store(a.trans + (head * a.segs + seg) * KD * (a.slices * 64 + KD), KD, a.slices * 64 + KD, col, lane);
@@ -1020,9 +1022,9 @@ __global__ void __launch_bounds__(kPipeThreads, 1) pipe_kernel(DeltaArgs a)
         f32x4 vecs;
         auto fetch = [&](int c) {
             const float *r = rec + (int64_t)c * a.record;
-            tk.load({a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk}, a.vk, tid);
+            tk.template load<VEC>({a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk}, tid);
             tz.load(r + Record::kZ, tid);
-            tv.load({a.v.p, ev, a.v.s.l, c * kC, a.L, vcols}, a.vv, tid);
+            tv.template load<VEC>({a.v.p, ev, a.v.s.l, c * kC, a.L, vcols}, tid);
             vecs = load_vecs(r + Record::kVec, tid);
         };
         auto stage = [&](int half) {
@@ -1044,7 +1046,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) pipe_kernel(DeltaArgs a)
             for (int s = 0; s < NS; ++s)
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
-                    qf[s][t] = cq.unit(e + 64 * s, i16, 16 * t, 32 * s + 8 * g, a.vq);
+                    qf[s][t] = cq.template unit<VEC>(e + 64 * s, i16, 16 * t, 32 * s + 8 * g);
         };
         auto output = [&](int c) {     // from qs, pf and the u of chunk c
             const uint16_t *y = lds + LDS::kU + ((((c - c0) & 1) * 4 + mine) * 2) * LDS::kUPart + i16 * LDS::kURow + 4 * g;
@@ -1071,7 +1073,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) pipe_kernel(DeltaArgs a)
             fetch(c0 + 1);
         if constexpr (MODE == kOut)
             fetch_q(c0);
-        __syncthreads();
+        lds_barrier();
         for (int c = c0; c < c1; ++c) {
             const int half = (c - c0) & 1;
             if (c + 1 < c1) {
@@ -1110,7 +1112,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) pipe_kernel(DeltaArgs a)
                 if (c + 1 < c1)
                     fetch_q(c + 1);
             }
-            __syncthreads();
+            lds_barrier();
         }
         if constexpr (MODE == kOut)
             output(c1 - 1);
@@ -1155,7 +1157,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(DeltaArgs a)
 // gradient of the state in registers.  Writes dV, keeps w and the gradients
 // of the states after the chunks.
 // ---------------------------------------------------------------------------
-template <int KD, bool BF16>
+template <int KD, bool BF16, bool VEC>
 __global__ void __launch_bounds__(kThreads) reverse_kernel(DeltaArgs a)
 {
     using T = Tile<KD, BF16>;
@@ -1185,8 +1187,8 @@ __global__ void __launch_bounds__(kThreads) reverse_kernel(DeltaArgs a)
     f32x4 tv;
     auto fetch = [&](int c) {
         const float *r = rec + (int64_t)c * a.record;
-        tk.load({a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk}, a.vk, threadIdx.x);
-        tq.load({a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk}, a.vq, threadIdx.x);
+        tk.template load<VEC>({a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk}, threadIdx.x);
+        tq.template load<VEC>({a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk}, threadIdx.x);
         tz.load(r + Record::kZt, threadIdx.x);
         tp.load(r + Record::kP, threadIdx.x);
         tv = load_vecs(r + Record::kVec, threadIdx.x);
@@ -1208,7 +1210,7 @@ __global__ void __launch_bounds__(kThreads) reverse_kernel(DeltaArgs a)
 #pragma unroll
         for (int t = 0; t < 4; ++t)
             dO[t] = v.get(t);
-        __syncthreads();
+        lds_barrier();
         if (c > 0)
             fetch(c - 1);
 
@@ -1273,7 +1275,7 @@ __global__ void __launch_bounds__(kThreads) reverse_kernel(DeltaArgs a)
                 S.s[m] = mma<3>(T::columns_stacked(s_k, m, s, lane), fw, S.s[m]);
             }
         }
-        __syncthreads();
+        lds_barrier();
     }
     if (a.ds0)
         S.store(a.ds0 + head * a.Dk * a.Dv, a.Dk, a.Dv, col, lane);
@@ -1307,7 +1309,7 @@ __device__ __forceinline__ float dot8(f32x8 a, f32x8 b, float v)
     return v;
 }
 
-template <int KD, bool BF16>
+template <int KD, bool BF16, bool VEC>
 __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
 {
     using T = Tile<KD, BF16>;
@@ -1334,8 +1336,8 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
 
     {
         T tk, tq;
-        tk.load({a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk}, a.vk, threadIdx.x);
-        tq.load({a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk}, a.vq, threadIdx.x);
+        tk.template load<VEC>({a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk}, threadIdx.x);
+        tq.template load<VEC>({a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk}, threadIdx.x);
         tk.store(s_k, threadIdx.x);
         tq.store(s_q, threadIdx.x);
     }
@@ -1369,10 +1371,10 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
             float uw = 0.f, vw = 0.f;
             for (int d0 = 0; d0 < a.DV; d0 += 32) {
                 const int col = d0 + 8 * g;
-                const Frag<NK> fo = unit_frag<BF16>(cdo.unit(row, col, a.vo));
+                const Frag<NK> fo = unit_frag<BF16>(cdo.template unit<VEC>(row, col));
                 const f32x8 wv = load8(w + row * a.DV + col);
                 const Frag<NO> fw = split<NO>(wv);
-                const f32x8 vv = unit_values<BF16>(cv.unit(row, col, a.vv));
+                const f32x8 vv = unit_values<BF16>(cv.template unit<VEC>(row, col));
                 vw = dot8(vv, wv, vw);
 #pragma unroll
                 for (int tb = 0; tb < 4; ++tb) {
@@ -1458,7 +1460,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     const int row = 16 * t + i16;
-                    const Frag<NK> fo = unit_frag<BF16>(cdo.unit(row, col, a.vo));
+                    const Frag<NK> fo = unit_frag<BF16>(cdo.template unit<VEC>(row, col));
                     e[t] = mma<3>(fo, fs, e[t]);
                     f[t] = mma<NO>(split<NO>(load8(w + row * a.DV + col)), fs, f[t]);
                     k2[t] = mma<3>(split<3>(load8(ut + row * a.DV + col)), fd, k2[t]);
@@ -1807,49 +1809,70 @@ constexpr size_t grad_lds()
 }
 
 // The states before the segments, where the chunks are cut.
-template <int KD>
+template <int KD, bool VEC>
 int launch_segments(const DeltaArgs &a, hipStream_t stream)
 {
     if (a.segs < 2)
         return PDSSM_OK;
-    const int rc = launch(pipe_kernel<KD, kScan>, a.heads * (a.segs - 1) * (a.slices + KD / 64), PipeLds<KD>::bytes(false), a,
-                          stream, kPipeThreads);
+    const int rc = launch(pipe_kernel<KD, VEC, kScan>, a.heads * (a.segs - 1) * (a.slices + KD / 64),
+                          PipeLds<KD>::bytes(false), a, stream, kPipeThreads);
     return rc != PDSSM_OK ? rc : launch(join_kernel<KD>, a.heads * a.slices, 0, a, stream);
 }
 
-template <int KD, bool BF16>
+template <int KD, bool BF16, bool VEC>
 int launch_fwd(const DeltaArgs &a, hipStream_t stream)
 {
-    int rc = launch(prep_kernel<KD, BF16, false>, a.heads * a.NC, 0, a, stream);
+    int rc = launch(prep_kernel<KD, BF16, VEC, false>, a.heads * a.NC, 0, a, stream);
     if (rc != PDSSM_OK)
         return rc;
     if constexpr (BF16) {
-        rc = launch_segments<KD>(a, stream);
+        rc = launch_segments<KD, VEC>(a, stream);
         if (rc == PDSSM_OK)
-            rc = launch(pipe_kernel<KD, kOut>, a.heads * a.slices * a.segs, PipeLds<KD>::bytes(true), a, stream, kPipeThreads);
+            rc = launch(pipe_kernel<KD, VEC, kOut>, a.heads * a.slices * a.segs, PipeLds<KD>::bytes(true), a, stream,
+                        kPipeThreads);
         return rc;
     } else {
-        return launch(chain_kernel<KD, BF16, false>, a.heads * a.slices, chain_lds<KD, BF16>(true), a, stream);
+        return launch(chain_kernel<KD, BF16, VEC, false>, a.heads * a.slices, chain_lds<KD, BF16>(true), a, stream);
     }
 }
 
-template <int KD, bool BF16>
+template <int KD, bool BF16, bool VEC>
 int launch_bwd(const DeltaArgs &a, hipStream_t stream)
 {
-    int rc = launch(prep_kernel<KD, BF16, true>, a.heads * a.NC, 0, a, stream);
+    int rc = launch(prep_kernel<KD, BF16, VEC, true>, a.heads * a.NC, 0, a, stream);
+    if (rc != PDSSM_OK)
+        return rc;
     if constexpr (BF16) {
+        rc = launch_segments<KD, VEC>(a, stream);
         if (rc == PDSSM_OK)
-            rc = launch_segments<KD>(a, stream);
-        if (rc == PDSSM_OK)
-            rc = launch(pipe_kernel<KD, kKeep>, a.heads * a.slices * a.segs, PipeLds<KD>::bytes(false), a, stream, kPipeThreads);
-    } else if (rc == PDSSM_OK) {
-        rc = launch(chain_kernel<KD, BF16, true>, a.heads * a.slices, chain_lds<KD, BF16>(false), a, stream);
+            rc = launch(pipe_kernel<KD, VEC, kKeep>, a.heads * a.slices * a.segs, PipeLds<KD>::bytes(false), a, stream,
+                        kPipeThreads);
+    } else {
+        rc = launch(chain_kernel<KD, BF16, VEC, true>, a.heads * a.slices, chain_lds<KD, BF16>(false), a, stream);
     }
     if (rc == PDSSM_OK)
-        rc = launch(reverse_kernel<KD, BF16>, a.heads * a.slices, chain_lds<KD, BF16>(true), a, stream);
+        rc = launch(reverse_kernel<KD, BF16, VEC>, a.heads * a.slices, chain_lds<KD, BF16>(true), a, stream);
     if (rc == PDSSM_OK)
-        rc = launch(grad_kernel<KD, BF16>, a.heads / a.Hv * a.Hk * a.NC, grad_lds<KD, BF16>(), a, stream);
+        rc = launch(grad_kernel<KD, BF16, VEC>, a.heads / a.Hv * a.Hk * a.NC, grad_lds<KD, BF16>(), a, stream);
     return rc;
+}
+
+// The variant for these sizes, type and rows (vec: see units()).
+template <bool BWD, int KD, bool BF16>
+int launch_rows(const DeltaArgs &a, bool vec, hipStream_t stream)
+{
+    if constexpr (BWD)
+        return vec ? launch_bwd<KD, BF16, true>(a, stream) : launch_bwd<KD, BF16, false>(a, stream);
+    else
+        return vec ? launch_fwd<KD, BF16, true>(a, stream) : launch_fwd<KD, BF16, false>(a, stream);
+}
+
+template <bool BWD>
+int launch_any(const DeltaArgs &a, bool bf16, bool vec, hipStream_t stream)
+{
+    if (bf16)
+        return a.Dk <= 64 ? launch_rows<BWD, 64, true>(a, vec, stream) : launch_rows<BWD, 128, true>(a, vec, stream);
+    return a.Dk <= 64 ? launch_rows<BWD, 64, false>(a, vec, stream) : launch_rows<BWD, 128, false>(a, vec, stream);
 }
 
 }  // namespace
@@ -1917,10 +1940,8 @@ extern "C" int pdssm_delta_fwd(const void *q, const void *k, const void *v, cons
     place_workspace(a, lo, workspace);
     a.heads = B * Hv, a.Hk = (int)Hk, a.Hv = (int)Hv, a.L = (int)L, a.NC = (int)((L + kC - 1) / kC);
     a.Dk = Dk, a.Dv = Dv, a.DV = padded_value(Dv), a.slices = slices_of(Dv), a.scale = scale;
-    a.vq = units(q, s[0], Dk, esize), a.vk = units(k, s[1], Dk, esize), a.vv = units(v, s[2], Dv, esize);
-    if (esize == 2)
-        return Dk <= 64 ? launch_fwd<64, true>(a, stream) : launch_fwd<128, true>(a, stream);
-    return Dk <= 64 ? launch_fwd<64, false>(a, stream) : launch_fwd<128, false>(a, stream);
+    const bool vec = units(q, s[0], Dk, esize) && units(k, s[1], Dk, esize) && units(v, s[2], Dv, esize);
+    return launch_any<false>(a, esize == 2, vec, stream);
 }
 
 extern "C" int pdssm_delta_bwd(const void *q, const void *k, const void *v, const float *g, const float *beta,
@@ -1975,10 +1996,9 @@ extern "C" int pdssm_delta_bwd(const void *q, const void *k, const void *v, cons
     a.w = reinterpret_cast<float *>(ws + lo.w);
     a.heads = B * Hv, a.Hk = (int)Hk, a.Hv = (int)Hv, a.L = (int)L, a.NC = (int)((L + kC - 1) / kC);
     a.Dk = Dk, a.Dv = Dv, a.DV = padded_value(Dv), a.slices = slices_of(Dv), a.scale = scale;
-    a.vq = units(q, s[0], Dk, esize), a.vk = units(k, s[1], Dk, esize), a.vv = units(v, s[2], Dv, esize), a.vo = units(d_o, s[5], Dv, esize);
-    if (esize == 2)
-        return Dk <= 64 ? launch_bwd<64, true>(a, stream) : launch_bwd<128, true>(a, stream);
-    return Dk <= 64 ? launch_bwd<64, false>(a, stream) : launch_bwd<128, false>(a, stream);
+    const bool vec = units(q, s[0], Dk, esize) && units(k, s[1], Dk, esize) && units(v, s[2], Dv, esize) &&
+                     units(d_o, s[5], Dv, esize);
+    return launch_any<true>(a, esize == 2, vec, stream);
 }
 
 extern "C" int pdssm_delta_step(const void *q, const void *k, const void *v, const float *g, const float *beta,

@@ -129,4 +129,13 @@ __device__ __forceinline__ bf16x8 lds_columns4(const uint16_t *p, const uint16_t
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// A workgroup barrier that orders LDS only: loads from memory stay in flight
+// across it (__syncthreads waits for them).
+__device__ __forceinline__ void lds_barrier()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 }  // namespace pdssm
