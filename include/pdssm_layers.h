@@ -133,7 +133,8 @@ int pdssm_delta_step(const void *q, const void *k, const void *v, const float *g
  *   cos, sin  fp32 [P,R/2] (R = 0: not read)
  *   pos       int32 [B,L] positions, clamped to [0,P), or NULL for pos = l
  *   strides   of q, k, q_out, k_out, or NULL
- * D in [1,256]; R even, in [0,D]; P >= 1 when R > 0; any of B, Hq, Hk, L may
+ * D in [1,256]; R even, in [0,D]; P >= 1 when R > 0; Hq and Hk up to 32768,
+ * B*L*(Hq+Hk) below 2^31; any of B, Hq, Hk, L may
  * be 0.  flags: PDSSM_DATA_BF16, PDSSM_NORM_L2, PDSSM_ROPE_PAIRS.
  */
 int pdssm_qk_norm_rope_fwd(const void *q, const void *k, const float *wq, const float *wk,

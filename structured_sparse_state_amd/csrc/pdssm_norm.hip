@@ -8,11 +8,12 @@
 //
 // Both are bound by HBM: x (and dy) read once, y (or dx) written once, with a
 // few operations per value.  A row of D values belongs to a group of LPH
-// lanes, and a lane holds four of the row's pairs (a, b) whole, so the
+// lanes, and a lane holds eight of the row's pairs (a, b) whole, so the
 // rotation needs nothing from another lane; only the row's sum crosses lanes.
-// A lane takes the same place in HP heads of one token (all their loads are
-// issued before the first is used), with its weights, cosines and sines
-// loaded once for them.
+// In either pairing a lane's values are two runs of eight, one 16-byte load
+// of bf16 each.  A lane takes the same place in HP heads of one token (all
+// their loads are issued before the first is used), with its weights, cosines
+// and sines loaded once for them.
 #include <hip/hip_runtime.h>
 
 #include "pdssm_device.h"
@@ -44,9 +45,9 @@ struct NormArgs {
     const int32_t *pos;
     int64_t P;
     int tokens, L, D, half;   // half = R / 2
-    int segs0;                // head segments (of HP heads) of t[0]; blockIdx.y beyond are t[1]'s
+    int segs0, segs1;         // segments of HP heads of t[0] and of t[1]
     float inv_n, eps;
-    bool pairs;
+    bool pairs, heads_first;
 };
 
 template <typename T>
@@ -67,101 +68,137 @@ __device__ __forceinline__ void store1(T *p, float v)
         *p = v;
 }
 
+// Eight consecutive values as they lie in memory (bf16 ones are unpacked only
+// where they are used: a lane holds several heads' rows).
 template <typename T>
-__device__ __forceinline__ float4 load_quad(const T *p)
-{
-    if constexpr (sizeof(T) == 2) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-        return make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
-    } else {
-        return *reinterpret_cast<const float4 *>(p);
+struct Run;
+template <>
+struct Run<uint16_t> {
+    uint4 w;
+    __device__ __forceinline__ void clear() { w = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void load(const uint16_t *p) { w = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void set(int j, float v)     // of a cleared run
+    {
+        const uint32_t h = (__float_as_uint(v) >> 16) << (16 * (j & 1));
+        j / 2 == 0 ? w.x |= h : j / 2 == 1 ? w.y |= h : j / 2 == 2 ? w.z |= h : w.w |= h;
     }
-}
-
-template <typename T>
-__device__ __forceinline__ void store_quad(T *p, float a, float b, float c, float d)
-{
-    if constexpr (sizeof(T) == 2)
-        *reinterpret_cast<uint2 *>(p) = make_uint2(f32x2_to_bf16x2_rne(a, b), f32x2_to_bf16x2_rne(c, d));
-    else
-        *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
-}
-
-// Where a lane's four pairs lie in a row.  Pair p of the row is (p, p + half)
-// when it turns in half mode, else (2p, 2p + 1); `split`: the lane's first
-// elements are one quad and its second ones another, else the eight are
-// consecutive.  Elements at D and beyond do not exist.
-struct Place {
-    int e0[4], e1[4];
-    int qa, qb;      // first elements of the two quads (VEC)
-    bool split;
+    __device__ __forceinline__ float get(int j) const
+    {
+        const uint32_t u = j / 2 == 0 ? w.x : j / 2 == 1 ? w.y : j / 2 == 2 ? w.z : w.w;
+        return (j & 1) ? bf16_hi(u) : bf16_lo(u);
+    }
+};
+template <>
+struct Run<float> {
+    float4 a, b;
+    __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void load(const float *p)
+    {
+        a = *reinterpret_cast<const float4 *>(p);
+        b = *reinterpret_cast<const float4 *>(p + 4);
+    }
+    __device__ __forceinline__ void set(int j, float v)
+    {
+        float4 &q = j < 4 ? a : b;
+        (j & 3) == 0 ? q.x = v : (j & 3) == 1 ? q.y = v : (j & 3) == 2 ? q.z = v : q.w = v;
+    }
+    __device__ __forceinline__ float get(int j) const
+    {
+        const float4 &q = j < 4 ? a : b;
+        return (j & 3) == 0 ? q.x : (j & 3) == 1 ? q.y : (j & 3) == 2 ? q.z : q.w;
+    }
 };
 
-__device__ __forceinline__ Place place_of(int lane, int half, bool pairs)
+template <typename T>
+__device__ __forceinline__ void store_run(T *p, const float (&v)[8])
 {
-    Place q;
-    q.split = !pairs && 4 * lane < half;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int p = 4 * lane + j;
-        const bool turned = !pairs && p < half;
-        q.e0[j] = turned ? p : 2 * p;
-        q.e1[j] = turned ? p + half : 2 * p + 1;
-    }
-    q.qa = q.e0[0];
-    q.qb = q.split ? q.e1[0] : q.e0[0] + 4;
-    return q;
-}
-
-// The lane's pairs (a[j], b[j]) of one row.  VEC: two quads, each inside the
-// row or outside as a whole.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_pairs(const T *row, const Place &q, int D, float (&a)[4], float (&b)[4])
-{
-    if constexpr (VEC) {
-        float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
-        if (q.qa < D)
-            u = load_quad(row + q.qa);
-        if (q.qb < D)
-            v = load_quad(row + q.qb);
-        if (q.split) {
-            a[0] = u.x, a[1] = u.y, a[2] = u.z, a[3] = u.w;
-            b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
-        } else {
-            a[0] = u.x, b[0] = u.y, a[1] = u.z, b[1] = u.w;
-            a[2] = v.x, b[2] = v.y, a[3] = v.z, b[3] = v.w;
-        }
+    if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(f32x2_to_bf16x2_rne(v[0], v[1]), f32x2_to_bf16x2_rne(v[2], v[3]),
+                                                   f32x2_to_bf16x2_rne(v[4], v[5]), f32x2_to_bf16x2_rne(v[6], v[7]));
     } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            a[j] = q.e0[j] < D ? load1(row + q.e0[j]) : 0.f;
-            b[j] = q.e1[j] < D ? load1(row + q.e1[j]) : 0.f;
-        }
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
     }
 }
 
+constexpr int kPairs = 8;       // pairs of a lane
+
+// Where a lane's pairs lie in a row.  Pair p of the row is (p, p + half) when
+// it turns in half mode, else (2p, 2p + 1); `split`: the lane's first elements
+// are one run of eight and its second ones another, else the sixteen are
+// consecutive.  Elements at D and beyond do not exist.
+struct Place {
+    int first, half;
+    bool split, pairs;
+    __device__ __forceinline__ Place(int lane, int half_, bool pairs_)
+    {
+        first = kPairs * lane, half = half_, pairs = pairs_;
+        split = !pairs && first < half;
+    }
+    __device__ __forceinline__ int e0(int j) const { return !pairs && first + j < half ? first + j : 2 * (first + j); }
+    __device__ __forceinline__ int e1(int j) const
+    {
+        return !pairs && first + j < half ? first + j + half : 2 * (first + j) + 1;
+    }
+    __device__ __forceinline__ int run0() const { return split ? first : 2 * first; }
+    __device__ __forceinline__ int run1() const { return split ? first + half : 2 * first + 8; }
+};
+
+// A lane's pairs of one row.  VEC: two runs, each inside the row or outside
+// as a whole; else the pairs' first and second elements one by one.
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_pairs(T *row, const Place &q, int D, const float (&a)[4], const float (&b)[4])
+struct Pairs {
+    Run<T> u, v;
+    __device__ __forceinline__ void load(const T *row, const Place &q, int D)
+    {
+        u.clear();
+        v.clear();
+        if constexpr (VEC) {
+            if (q.run0() < D)
+                u.load(row + q.run0());
+            if (q.run1() < D)
+                v.load(row + q.run1());
+        } else {
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+                if (q.e0(j) < D)
+                    u.set(j, load1(row + q.e0(j)));
+                if (q.e1(j) < D)
+                    v.set(j, load1(row + q.e1(j)));
+            }
+        }
+    }
+    __device__ __forceinline__ void get(const Place &q, float (&a)[kPairs], float (&b)[kPairs]) const
+    {
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+            a[j] = !VEC || q.split ? u.get(j) : j < 4 ? u.get((2 * j) & 7) : v.get((2 * j) & 7);
+            b[j] = !VEC || q.split ? v.get(j) : j < 4 ? u.get((2 * j + 1) & 7) : v.get((2 * j + 1) & 7);
+        }
+    }
+};
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_pairs(T *row, const Place &q, int D, const float (&a)[kPairs], const float (&b)[kPairs])
 {
     if constexpr (VEC) {
-        if (q.split) {
-            if (q.qa < D)
-                store_quad(row + q.qa, a[0], a[1], a[2], a[3]);
-            if (q.qb < D)
-                store_quad(row + q.qb, b[0], b[1], b[2], b[3]);
-        } else {
-            if (q.qa < D)
-                store_quad(row + q.qa, a[0], b[0], a[1], b[1]);
-            if (q.qb < D)
-                store_quad(row + q.qb, a[2], b[2], a[3], b[3]);
+        float u[8], v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            u[j] = q.split ? a[j] : (j & 1) ? b[j / 2] : a[j / 2];
+            v[j] = q.split ? b[j] : (j & 1) ? b[4 + j / 2] : a[4 + j / 2];
         }
+        if (q.run0() < D)
+            store_run(row + q.run0(), u);
+        if (q.run1() < D)
+            store_run(row + q.run1(), v);
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (q.e0[j] < D)
-                store1(row + q.e0[j], a[j]);
-            if (q.e1[j] < D)
-                store1(row + q.e1[j], b[j]);
+        for (int j = 0; j < kPairs; ++j) {
+            if (q.e0(j) < D)
+                store1(row + q.e0(j), a[j]);
+            if (q.e1(j) < D)
+                store1(row + q.e1(j), b[j]);
         }
     }
 }
@@ -179,92 +216,111 @@ __device__ __forceinline__ float group_sum(float v)
 template <typename T, int LPH, int HP, bool VEC, bool BWD>
 __global__ void __launch_bounds__(kThreads) norm_kernel(NormArgs g)
 {
-    constexpr int kGroups = kThreads / LPH;   // rows of tokens side by side
+    constexpr int kGroups = kThreads / LPH;
     const int lane = threadIdx.x % LPH, grp = threadIdx.x / LPH;
-    const bool second = (int)blockIdx.y >= g.segs0;
-    const NormTensor &t = g.t[second ? 1 : 0];
-    const int64_t h0 = (int64_t)(blockIdx.y - (second ? g.segs0 : 0)) * HP;
     const int D = g.D, half = g.half;
-    const int heads = (int)min((int64_t)HP, t.H - h0);
-    const Place q = place_of(lane, half, g.pairs);
+    const Place q(lane, half, g.pairs);
 
-    float w0[4], w1[4], s0[4], s1[4];   // weights, and the sums of their gradients
+    // A group takes one token and HP of its heads at a time: the backward a
+    // segment of heads (blockIdx.y) and tokens in turn, so that the sums of
+    // the weight's gradient stay in its registers; the forward any pair of the
+    // two, heads first where a token's heads lie together in memory.
+    const int segs = g.segs0 + g.segs1;
+    const uint32_t items = BWD ? (uint32_t)g.tokens : (uint32_t)g.tokens * segs;
+    float s0[kPairs], s1[kPairs];       // sums of the weights' gradients
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        w0[j] = (t.w && q.e0[j] < D) ? t.w[q.e0[j]] : 1.f;
-        w1[j] = (t.w && q.e1[j] < D) ? t.w[q.e1[j]] : 1.f;
+    for (int j = 0; j < kPairs; ++j)
         s0[j] = s1[j] = 0.f;
-    }
 
-    for (int64_t tok = (int64_t)blockIdx.x * kGroups + grp; tok < g.tokens; tok += (int64_t)gridDim.x * kGroups) {
-        const int b = (int)((uint32_t)tok / (uint32_t)g.L), l = (int)((uint32_t)tok % (uint32_t)g.L);
+    for (uint32_t item = blockIdx.x * kGroups + grp; item < items; item += gridDim.x * kGroups) {
+        uint32_t tok, seg;
+        if constexpr (BWD)
+            tok = item, seg = blockIdx.y;
+        else if (g.heads_first)
+            tok = item / segs, seg = item - tok * segs;
+        else
+            seg = item / (uint32_t)g.tokens, tok = item - seg * (uint32_t)g.tokens;
+        const bool second = (int)seg >= g.segs0;
+        const NormTensor &t = g.t[second ? 1 : 0];
+        const int64_t h0 = (int64_t)(second ? seg - g.segs0 : seg) * HP;
+        const int heads = (int)min((int64_t)HP, t.H - h0);
+        const int b = (int)(tok / (uint32_t)g.L), l = (int)(tok - b * (uint32_t)g.L);
         const T *x = static_cast<const T *>(t.x) + b * t.sx.b + h0 * t.sx.h + l * t.sx.l;
-        float xa[HP][4], xb[HP][4];
+        Pairs<T, VEC> px[HP], pd[BWD ? HP : 1];
 #pragma unroll
         for (int i = 0; i < HP; ++i)
-            load_pairs<T, VEC>(x + min(i, heads - 1) * t.sx.h, q, D, xa[i], xb[i]);
-        float da[BWD ? HP : 1][4], db[BWD ? HP : 1][4];
+            px[i].load(x + min(i, heads - 1) * t.sx.h, q, D);
         if constexpr (BWD) {
             const T *dy = static_cast<const T *>(t.dy) + b * t.sdy.b + h0 * t.sdy.h + l * t.sdy.l;
 #pragma unroll
             for (int i = 0; i < HP; ++i)
-                load_pairs<T, VEC>(dy + min(i, heads - 1) * t.sdy.h, q, D, da[i], db[i]);
+                pd[i].load(dy + min(i, heads - 1) * t.sdy.h, q, D);
         }
-        float c[4], s[4];
+        float c[kPairs], s[kPairs], w0[kPairs], w1[kPairs];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            c[j] = 1.f, s[j] = 0.f;
-        if (4 * lane < half) {
+        for (int j = 0; j < kPairs; ++j)
+            c[j] = 1.f, s[j] = 0.f, w0[j] = w1[j] = 1.f;
+        if (q.first < half) {
             int64_t p = g.pos ? (int64_t)g.pos[tok] : (int64_t)l;
             p = p < 0 ? 0 : (p < g.P ? p : g.P - 1);
-            const float *cs = g.cs + p * half + 4 * lane, *sn = g.sn + p * half + 4 * lane;
-            if ((half & 3) == 0) {
-                const float4 u = *reinterpret_cast<const float4 *>(cs), v = *reinterpret_cast<const float4 *>(sn);
-                c[0] = u.x, c[1] = u.y, c[2] = u.z, c[3] = u.w;
-                s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
+            const float *cs = g.cs + p * half + q.first, *sn = g.sn + p * half + q.first;
+            if ((half & 7) == 0) {
+                Run<float> rc, rs;
+                rc.load(cs);
+                rs.load(sn);
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j)
+                    c[j] = rc.get(j), s[j] = rs.get(j);
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (4 * lane + j < half)
+                for (int j = 0; j < kPairs; ++j)
+                    if (q.first + j < half)
                         c[j] = cs[j], s[j] = sn[j];
             }
+        }
+        if (t.w) {
+            Pairs<float, VEC> pw;
+            pw.load(t.w, q, D);
+            pw.get(q, w0, w1);
         }
         T *out = static_cast<T *>(t.out) + b * t.so.b + h0 * t.so.h + l * t.so.l;
 #pragma unroll
         for (int i = 0; i < HP; ++i) {
             if (HP > 1 && i >= heads)
                 break;
-            float ss = 0.f;
+            float xa[kPairs], xb[kPairs], ss = 0.f;
+            px[i].get(q, xa, xb);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                ss += xa[i][j] * xa[i][j] + xb[i][j] * xb[i][j];
-            const float r = 1.f / sqrtf(group_sum<LPH>(ss) * g.inv_n + g.eps);
-            float ya[4], yb[4];
+            for (int j = 0; j < kPairs; ++j)
+                ss += xa[j] * xa[j] + xb[j] * xb[j];
+            const float r = rsqrtf(group_sum<LPH>(ss) * g.inv_n + g.eps);
+            float ya[kPairs], yb[kPairs];
             if constexpr (!BWD) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float a = xa[i][j] * r * w0[j], bb = xb[i][j] * r * w1[j];
+                for (int j = 0; j < kPairs; ++j) {
+                    const float a = xa[j] * r * w0[j], bb = xb[j] * r * w1[j];
                     ya[j] = a * c[j] - bb * s[j];
                     yb[j] = a * s[j] + bb * c[j];
                 }
             } else {
-                float ea[4], eb[4], dot = 0.f;
+                float da[kPairs], db[kPairs], ea[kPairs], eb[kPairs], dot = 0.f;
+                pd[i].get(q, da, db);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float a = da[i][j] * c[j] + db[i][j] * s[j], bb = db[i][j] * c[j] - da[i][j] * s[j];
-                    xa[i][j] *= r;
-                    xb[i][j] *= r;
-                    s0[j] += a * xa[i][j];
-                    s1[j] += bb * xb[i][j];
+                for (int j = 0; j < kPairs; ++j) {
+                    const float a = da[j] * c[j] + db[j] * s[j], bb = db[j] * c[j] - da[j] * s[j];
+                    xa[j] *= r;
+                    xb[j] *= r;
+                    s0[j] += a * xa[j];
+                    s1[j] += bb * xb[j];
                     ea[j] = a * w0[j];
                     eb[j] = bb * w1[j];
-                    dot += ea[j] * xa[i][j] + eb[j] * xb[i][j];
+                    dot += ea[j] * xa[j] + eb[j] * xb[j];
                 }
                 const float m = group_sum<LPH>(dot) * g.inv_n;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    ya[j] = r * (ea[j] - xa[i][j] * m);
-                    yb[j] = r * (eb[j] - xb[i][j] * m);
+                for (int j = 0; j < kPairs; ++j) {
+                    ya[j] = r * (ea[j] - xa[j] * m);
+                    yb[j] = r * (eb[j] - xb[j] * m);
                 }
             }
             store_pairs<T, VEC>(out + i * t.so.h, q, D, ya, yb);
@@ -272,20 +328,22 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(NormArgs g)
     }
 
     if constexpr (BWD) {
+        const bool second = (int)blockIdx.y >= g.segs0;
+        const NormTensor &t = g.t[second ? 1 : 0];
         if (!t.partial)
             return;
         // The workgroup's sums: its groups' rows through LDS, in their order.
-        __shared__ float s_sum[kGroups][LPH * 8];
+        __shared__ float s_sum[kGroups][LPH * 2 * kPairs];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            s_sum[grp][lane * 8 + j] = s0[j];
-            s_sum[grp][lane * 8 + 4 + j] = s1[j];
+        for (int j = 0; j < kPairs; ++j) {
+            s_sum[grp][lane * 2 * kPairs + j] = s0[j];
+            s_sum[grp][lane * 2 * kPairs + kPairs + j] = s1[j];
         }
         __syncthreads();
         const int64_t row = (int64_t)(blockIdx.y - (second ? g.segs0 : 0)) * gridDim.x + blockIdx.x;
-        for (int u = threadIdx.x; u < LPH * 8; u += kThreads) {
-            const Place at = place_of(u / 8, half, g.pairs);
-            const int e = (u & 4) ? at.e1[u & 3] : at.e0[u & 3];
+        for (int u = threadIdx.x; u < LPH * 2 * kPairs; u += kThreads) {
+            const Place at(u / (2 * kPairs), half, g.pairs);
+            const int e = (u & kPairs) ? at.e1(u % kPairs) : at.e0(u % kPairs);
             float v = 0.f;
 #pragma unroll
             for (int i = 0; i < kGroups; ++i)
@@ -338,19 +396,21 @@ int check_norm_dims(int64_t B, int64_t Hq, int64_t Hk, int64_t L, int32_t D, int
     if (B < 0 || Hq < 0 || Hk < 0 || L < 0 || Hq > 32768 || Hk > 32768 || D < 1 || D > kMaxD || R < 0 || R > D ||
         (R & 1) || (R > 0 && P < 1))
         return PDSSM_ERR_DIM;
-    if ((double)B * (double)L > 2147483647.0 || (double)P * D > 9.0e18)
+    // Items (a token and a head) are counted in 32 bits.
+    if ((double)B * (double)L * (double)(Hq + Hk > 1 ? Hq + Hk : 1) > 2147483647.0 || (double)P * D > 9.0e18)
         return PDSSM_ERR_DIM;
     return PDSSM_OK;
 }
 
-// Every row of the tensor can be read in quads of four elements.
-bool quads(const void *p, const pdssm_strides &s, int esize)
+// Every row begins on 16 bytes.
+bool runs(const void *p, const pdssm_strides &s, int esize)
 {
-    return ((uintptr_t)p % (4 * esize)) == 0 && (s.b % 4) == 0 && (s.h % 4) == 0 && (s.l % 4) == 0;
+    const int n = 16 / esize;
+    return aligned16(p) && s.b % n == 0 && s.h % n == 0 && s.l % n == 0;
 }
 
 // Heads a lane takes of one token: four, unless the call has so few rows that
-// more lanes in flight shorten it (2^16 rows are 256 workgroups at D = 128).
+// more lanes in flight shorten it (2^16 rows are 512 workgroups at D = 128).
 int heads_per_lane(int64_t rows) { return rows > (1 << 16) ? 4 : 1; }
 
 struct Plan {
@@ -362,15 +422,14 @@ Plan plan_of(int64_t B, int64_t Hq, int64_t Hk, int64_t L, int32_t D, bool bwd)
 {
     Plan p;
     p.lph = 1;
-    while (p.lph * 8 < D)
+    while (p.lph * 2 * kPairs < D)
         p.lph *= 2;
-    p.lph = p.lph < 8 ? 8 : p.lph;
+    p.lph = p.lph < 4 ? 4 : p.lph;
     p.hp = heads_per_lane(B * L * (Hq + Hk));
     p.segs[0] = (Hq + p.hp - 1) / p.hp;
     p.segs[1] = (Hk + p.hp - 1) / p.hp;
-    const int64_t groups = kThreads / p.lph;
-    p.blocks = (B * L + groups - 1) / groups;
-    const int64_t segs = p.segs[0] + p.segs[1];
+    const int64_t groups = kThreads / p.lph, segs = p.segs[0] + p.segs[1];
+    p.blocks = (B * L * (bwd ? 1 : segs) + groups - 1) / groups;
     if (bwd && segs > 0) {
         const int64_t most = (kBwdGroups + segs - 1) / segs;
         p.blocks = p.blocks < most ? p.blocks : most;
@@ -390,7 +449,7 @@ void launch_vec(const NormArgs &a, bool vec, dim3 grid, hipStream_t stream)
 template <typename T, bool BWD>
 void launch_norm(const NormArgs &a, const Plan &p, bool vec, hipStream_t stream)
 {
-    const dim3 grid((unsigned)p.blocks, (unsigned)(p.segs[0] + p.segs[1]));
+    const dim3 grid((unsigned)p.blocks, (unsigned)(BWD ? p.segs[0] + p.segs[1] : 1));
 #define PDSSM_NORM_CASE(n)                                   \
     case n:                                                  \
         if (p.hp == 4)                                       \
@@ -399,9 +458,9 @@ void launch_norm(const NormArgs &a, const Plan &p, bool vec, hipStream_t stream)
             launch_vec<T, n, 1, BWD>(a, vec, grid, stream);  \
         break
     switch (p.lph) {
+        PDSSM_NORM_CASE(4);
         PDSSM_NORM_CASE(8);
         PDSSM_NORM_CASE(16);
-        PDSSM_NORM_CASE(32);
     }
 #undef PDSSM_NORM_CASE
 }
@@ -441,7 +500,7 @@ int norm_call(const NormCall &c, bool bwd, void *workspace, size_t workspace_byt
     if (any && c.pos && ((uintptr_t)c.pos & 3u))
         return PDSSM_ERR_ALIGN;
     NormArgs a;
-    bool vec = (c.D % 4) == 0 && ((c.flags & PDSSM_ROPE_PAIRS) || (c.R % 8) == 0);
+    bool vec = (c.D % 8) == 0 && ((c.flags & PDSSM_ROPE_PAIRS) || (c.R % 16) == 0);
     for (int i = 0; i < 2; ++i) {
         NormTensor &t = a.t[i];
         t.x = c.x[i], t.dy = c.dy[i], t.out = c.out[i], t.w = c.w[i], t.partial = nullptr, t.H = c.H[i];
@@ -457,7 +516,8 @@ int norm_call(const NormCall &c, bool bwd, void *workspace, size_t workspace_byt
             return PDSSM_ERR_NULL;
         if (((uintptr_t)t.x | (uintptr_t)t.out | (uintptr_t)t.dy) & (uintptr_t)(esize - 1))
             return PDSSM_ERR_ALIGN;
-        vec = vec && quads(t.x, t.sx, esize) && quads(t.out, t.so, esize) && (!bwd || quads(t.dy, t.sdy, esize));
+        vec = vec && runs(t.x, t.sx, esize) && runs(t.out, t.so, esize) && (!bwd || runs(t.dy, t.sdy, esize)) &&
+              aligned16(t.w);
     }
     const bool sums = c.dw[0] || c.dw[1];
     const Plan p = plan_of(c.B, has[0] ? c.H[0] : 0, has[1] ? c.H[1] : 0, c.L, c.D, bwd);
@@ -475,7 +535,9 @@ int norm_call(const NormCall &c, bool bwd, void *workspace, size_t workspace_byt
     if (any) {
         a.cs = c.cs, a.sn = c.sn, a.pos = c.pos, a.P = c.P;
         a.tokens = (int)tokens, a.L = (int)c.L, a.D = c.D, a.half = c.R / 2;
-        a.segs0 = (int)p.segs[0];
+        a.segs0 = (int)p.segs[0], a.segs1 = (int)p.segs[1];
+        const NormTensor &most = a.t[c.H[0] >= c.H[1] ? 0 : 1];
+        a.heads_first = most.sx.h <= most.sx.l;
         a.inv_n = (c.flags & PDSSM_NORM_L2) ? 1.f : 1.f / (float)c.D;
         a.eps = c.eps;
         a.pairs = (c.flags & PDSSM_ROPE_PAIRS) != 0;
