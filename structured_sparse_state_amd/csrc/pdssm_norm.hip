@@ -354,8 +354,9 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(NormArgs g)
     }
 }
 
-// dw[e] = the sum of `rows` partial rows; blockIdx.y picks the tensor.
-constexpr int kSumRows = 16;
+// dw[e] = the sum of `rows` partial rows; blockIdx.y picks the tensor.  A
+// workgroup takes 16 columns, 64 rows at a time.
+constexpr int kSumRows = 64, kSumCols = 16;
 struct SumArgs {
     const float *partial[2];
     float *dw[2];
@@ -363,10 +364,11 @@ struct SumArgs {
     int D;
 };
 
-__global__ void __launch_bounds__(64 * kSumRows) norm_sum_kernel(SumArgs a)
+__global__ void __launch_bounds__(kSumRows *kSumCols) norm_sum_kernel(SumArgs a)
 {
-    __shared__ float s_part[kSumRows][64];
-    const int which = blockIdx.y, col = blockIdx.x * 64 + (threadIdx.x & 63), part = threadIdx.x >> 6;
+    __shared__ float s_part[kSumRows][kSumCols + 1];
+    const int which = blockIdx.y, c = threadIdx.x % kSumCols, part = threadIdx.x / kSumCols;
+    const int col = blockIdx.x * kSumCols + c;
     if (!a.dw[which])
         return;
     float v = 0.f;
@@ -375,12 +377,11 @@ __global__ void __launch_bounds__(64 * kSumRows) norm_sum_kernel(SumArgs a)
         for (int64_t i = part; i < a.rows[which]; i += kSumRows)
             v += a.partial[which][i * a.D + col];
     }
-    s_part[part][threadIdx.x & 63] = v;
+    s_part[part][c] = v;
     __syncthreads();
-    if (part == 0 && col < a.D) {
-#pragma unroll
+    if (threadIdx.x < kSumCols && col < a.D) {
         for (int i = 1; i < kSumRows; ++i)
-            v += s_part[i][threadIdx.x];
+            v += s_part[i][c];
         a.dw[which][col] = v;
     }
 }
@@ -565,7 +566,7 @@ int norm_call(const NormCall &c, bool bwd, void *workspace, size_t workspace_byt
         s.rows[i] = has[i] ? p.segs[i] * p.blocks : 0;
     }
     s.D = c.D;
-    hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((c.D + 63) / 64), 2), dim3(64 * kSumRows), 0, stream, s);
+    hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((c.D + kSumCols - 1) / kSumCols), 2), dim3(kSumRows * kSumCols), 0, stream, s);
     return hip_status(hipGetLastError());
 }
 
