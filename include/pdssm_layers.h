@@ -98,7 +98,8 @@ size_t pdssm_delta_workspace_bytes(int64_t B, int64_t Hk, int64_t Hv, int64_t L,
  *   strides   of q, k, v, g, beta, d_o, dq, dk, dv, dg, dbeta, or NULL
  *   workspace pdssm_delta_bwd_workspace_bytes bytes, 16-byte aligned
  * Sizes, flags and empty shapes as pdssm_delta_fwd; with L = 0,
- * ds0 = ds_final (or zero).  dg is 0 where g = -inf.
+ * ds0 = ds_final (or zero).  dg is 0 where g = -inf, and
+ * for the first step without s0.
  */
 int pdssm_delta_bwd(const void *q, const void *k, const void *v, const float *g,
                     const float *beta, const float *s0, const void *d_o, const float *ds_final,

@@ -1529,7 +1529,9 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
                     v += x;
             }
             v += s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
-            const bool empty = s_vec[kResets * kC + lane] != (lane ? s_vec[kResets * kC + lane - 1] : 0.f);
+            // the decay of an empty state does nothing
+            const bool empty = s_vec[kResets * kC + lane] != (lane ? s_vec[kResets * kC + lane - 1] : 0.f) ||
+                               (t0 + lane == 0 && !a.s0);
             if (t0 + lane < a.L)
                 static_cast<float *>(const_cast<void *>(a.dg.p))[b * a.dg.s.b + h * a.dg.s.h + (t0 + lane) * a.dg.s.l] =
                     empty ? 0.f : v;
@@ -1544,6 +1546,292 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
             store_cols<BF16>({a.dq.p, b * a.dq.s.b + hk * a.dq.s.h, a.dq.s.l, t0, a.L, a.Dk}, dim, lane, t, dq[t][n]);
             store_cols<BF16>({a.dk.p, b * a.dk.s.b + hk * a.dk.s.h, a.dk.s.l, t0, a.L, a.Dk}, dim, lane, t, dk[t][n]);
         }
+}
+
+// ---------------------------------------------------------------------------
+// grads_kernel: grad_kernel for bf16 data, eight waves.  u~, w and dO of the
+// chunk go through LDS once (u~ in three parts, w in two), each row's dot
+// products falling out on the way; a wave forms one or two 16 x 16 blocks of
+// X and Y, then the 16 key dimensions it owns (with 64 of them: half of the
+// rows each), reading the state and its gradient straight into the product's
+// layout.
+// ---------------------------------------------------------------------------
+constexpr int kGradThreads = 512;
+
+template <int KD, int KV>
+struct GradLds {
+    using K = Tile<KD, true, kGradThreads>;
+    using V = Tile<KV, true, kGradThreads>;     // one part of 64 rows of KV values
+    using M = Tile<kC, true, kGradThreads>;
+    static constexpr int kWaves = kGradThreads / 64;
+    // in uint16_t
+    static constexpr int kQ = K::kSize;
+    static constexpr int kU = kQ + K::kSize;
+    static constexpr int kW = kU + 3 * V::kPart;
+    static constexpr int kO = kW + 2 * V::kPart;
+    static constexpr int kX = kO + V::kPart;
+    static constexpr int kY = kX + M::kSize;
+    static constexpr int kVec = kY + M::kSize;
+    static constexpr int kRows = kVec + 2 * kVecs * kC;         // [KD / 16][64]: q . (dO S^T)
+    static constexpr int kBlk = kRows + 2 * (KD / 16) * kC;     // [10][16]: sums of dP . P
+    static constexpr int kVdv = kBlk + 2 * kBlocks * 16;        // [64]: v . dv
+    static constexpr int kSum = kVdv + 2 * kC;                  // [waves]
+    static constexpr size_t kBytes = (kSum + 2 * kWaves) * 2;
+};
+
+// N parts of eight values, part n at p + n * part.
+template <int N>
+__device__ __forceinline__ void put_parts(uint16_t *p, int part, f32x8 v)
+{
+    const Frag<N> f = split<N>(v);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        *reinterpret_cast<bf16x8 *>(p + n * part) = f.p[n];
+}
+
+template <int KD, int KV, bool VEC>
+__global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
+{
+    using LDS = GradLds<KD, KV>;
+    using TK = typename LDS::K;
+    using TV = typename LDS::V;
+    using M = typename LDS::M;
+    constexpr int kTiles = KD / 16, RG = LDS::kWaves / kTiles, NT = 4 / RG;    // row groups, row tiles of a wave
+    constexpr int kUnits = kC * (KV / 8) / kGradThreads;
+    extern __shared__ __attribute__((aligned(16))) char s_dyn[];
+    uint16_t *lds = reinterpret_cast<uint16_t *>(s_dyn);
+    uint16_t *s_k = lds, *s_q = lds + LDS::kQ, *s_u = lds + LDS::kU, *s_w = lds + LDS::kW, *s_o = lds + LDS::kO;
+    uint16_t *s_x = lds + LDS::kX, *s_y = lds + LDS::kY;
+    float *s_vec = reinterpret_cast<float *>(lds + LDS::kVec), *s_rows = reinterpret_cast<float *>(lds + LDS::kRows);
+    float *s_blk = reinterpret_cast<float *>(lds + LDS::kBlk), *s_vdv = reinterpret_cast<float *>(lds + LDS::kVdv);
+    float *s_sum = reinterpret_cast<float *>(lds + LDS::kSum);
+
+    const int c = (int)(blockIdx.x % (unsigned)a.NC);
+    const int64_t bk = blockIdx.x / (unsigned)a.NC, b = bk / a.Hk;
+    const int hk = (int)(bk - b * a.Hk), group = a.Hv / a.Hk, t0 = c * kC;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, i16 = lane & 15;
+    const int tile = wave % kTiles, first = wave / kTiles * NT, dim = 16 * tile + i16;
+
+    {
+        TK tk, tq;
+        tk.template load<VEC>({a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk}, tid);
+        tq.template load<VEC>({a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk}, tid);
+        // the blocks right of the diagonal that share a k step with it
+        if (tid < 128) {
+            const int row = (tid >> 6) * 32 + ((tid >> 2) & 15), col = (tid >> 6) * 32 + 16 + (tid & 3) * 4;
+            *reinterpret_cast<uint2 *>(s_x + row * M::kRow + col) = make_uint2(0, 0);
+            *reinterpret_cast<uint2 *>(s_y + row * M::kRow + col) = make_uint2(0, 0);
+        }
+        tk.store(s_k, tid);
+        tq.store(s_q, tid);
+    }
+    f32x4 dq[NT], dk[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+        dq[t] = dk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    for (int j = 0; j < group; ++j) {
+        const int h = hk * group + j;
+        const int64_t head = b * a.Hv + h, at = head * a.NC + c;
+        const float *rec = a.records + at * a.record;
+        const float *S = a.states + at * KD * a.DV + dim * a.DV, *dS = a.grads + at * KD * a.DV + dim * a.DV;
+        f32x8 sv[KV / 32], dv[KV / 32];
+        {
+            const float *ut = a.ut + at * kC * a.DV, *w = a.w + at * kC * a.DV;
+            const Chunk<true> cdo(a.d_o.p, b * a.d_o.s.b + h * a.d_o.s.h, a.d_o.s.l, t0, a.L, a.Dv);
+            const Chunk<true> cv(a.v.p, b * a.v.s.b + h * a.v.s.h, a.v.s.l, t0, a.L, a.Dv);
+            f32x8 u[kUnits], ww[kUnits];
+            Unit<true> o[kUnits], v[kUnits];
+            float beta[kUnits];
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) {
+                const int x = tid + i * kGradThreads, row = x / (KV / 8), col = x % (KV / 8) * 8;
+                u[i] = ww[i] = f32x8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (col < a.DV) {
+                    u[i] = load8(ut + row * a.DV + col);
+                    ww[i] = load8(w + row * a.DV + col);
+                }
+                o[i] = cdo.template unit<VEC>(row, col);
+                v[i] = cv.template unit<VEC>(row, col);
+                beta[i] = rec[Record::kVec + kBeta * kC + row];
+            }
+            if (tid < kVecs * kC)
+                s_vec[tid] = rec[Record::kVec + tid];
+#pragma unroll
+            for (int s = 0; s < KV / 32; ++s) {
+                sv[s] = dv[s] = f32x8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (32 * s < a.DV) {
+                    sv[s] = load8(S + 32 * s + 8 * g);
+                    dv[s] = load8(dS + 32 * s + 8 * g);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) {
+                const int x = tid + i * kGradThreads, row = x / (KV / 8), col = x % (KV / 8) * 8;
+                const int p = row * TV::kRow + col;
+                put_parts<3>(s_u + p, TV::kPart, u[i]);
+                put_parts<2>(s_w + p, TV::kPart, ww[i]);
+                *reinterpret_cast<uint4 *>(s_o + p) = o[i].v;
+                float uw = dot8(u[i], ww[i], 0.f), vw = dot8(unit_values<true>(v[i]), ww[i], 0.f);
+#pragma unroll
+                for (int m = KV / 16; m >= 1; m >>= 1) {
+                    uw += __shfl_xor(uw, m, 64);
+                    vw += __shfl_xor(vw, m, 64);
+                }
+                if (col == 0) {
+                    s_vdv[row] = vw * beta[i];
+                    if (t0 + row < a.L)
+                        static_cast<float *>(const_cast<void *>(a.dbeta.p))[b * a.dbeta.s.b + h * a.dbeta.s.h +
+                                                                            (t0 + row) * a.dbeta.s.l] = uw;
+                }
+            }
+        }
+        lds_barrier();
+
+        // Blocks of X and Y.
+        for (int t = wave; t < kBlocks; t += LDS::kWaves) {
+            const int ta = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, tb = t - ta * (ta + 1) / 2;
+            const f32x4 P = *reinterpret_cast<const f32x4 *>(rec + Record::kP + t * kBlock + 4 * lane);
+            f32x4 dp = {0.f, 0.f, 0.f, 0.f}, dn = dp;
+#pragma unroll
+            for (int s = 0; s < KV / 32; ++s) {
+                if (32 * s >= a.DV)
+                    break;
+                const int pa = (16 * ta + i16) * TV::kRow + 32 * s + 8 * g, pb = (16 * tb + i16) * TV::kRow + 32 * s + 8 * g;
+                Frag<1> fo;
+                Frag<2> fw;
+                Frag<3> fu;
+                fo.p[0] = lds_row8(s_o + pa);
+#pragma unroll
+                for (int n = 0; n < 3; ++n)
+                    fu.p[n] = lds_row8(s_u + n * TV::kPart + pb);
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+                    fw.p[n] = lds_row8(s_w + n * TV::kPart + pa);
+                dp = mma<3>(fo, fu, dp);
+                dn = mma<2>(fw, fu, dn);
+            }
+            const int jc = 16 * tb + i16;
+            const float bj = s_vec[kBeta * kC + jc];
+            const float hj = s_vec[kGhi * kC + jc], lj = s_vec[kGlo * kC + jc], nj = s_vec[kResets * kC + jc];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int ic = 16 * ta + 4 * g + r;
+                const float d = bj * decay_of(s_vec[kGhi * kC + ic], s_vec[kGlo * kC + ic], s_vec[kResets * kC + ic], hj, lj, nj);
+                const float od = sum16(dp[r] * bj * P[r]);
+                if (i16 == 0)
+                    s_blk[t * 16 + 4 * g + r] = od;
+                // one part each: their 2^-9 beside the results' own
+                s_x[ic * M::kRow + jc] = f32_to_bf16_rne(jc <= ic ? a.scale * dp[r] * d : 0.f);
+                s_y[ic * M::kRow + jc] = f32_to_bf16_rne(jc < ic ? -dn[r] * s_vec[kBeta * kC + ic] * d : 0.f);
+            }
+        }
+
+        // The wave's key dimensions.
+        f32x4 e[NT], f[NT], k2[NT];     // dO S^T, w S^T, u~ dS^T
+        float ss = 0.f, kds = 0.f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            e[t] = f[t] = k2[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < KV / 32; ++s) {
+            if (32 * s >= a.DV)
+                break;
+            if (first == 0)
+                ss = dot8(sv[s], dv[s], ss);
+            const Frag<3> fs = split<3>(sv[s]), fd = split<3>(dv[s]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const int p = (16 * (first + t) + i16) * TV::kRow + 32 * s + 8 * g;
+                Frag<1> fo;
+                Frag<2> fw;
+                Frag<3> fu;
+                fo.p[0] = lds_row8(s_o + p);
+#pragma unroll
+                for (int n = 0; n < 3; ++n)
+                    fu.p[n] = lds_row8(s_u + n * TV::kPart + p);
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+                    fw.p[n] = lds_row8(s_w + n * TV::kPart + p);
+                e[t] = mma<3>(fo, fs, e[t]);
+                f[t] = mma<2>(fw, fs, f[t]);
+                k2[t] = mma<3>(fu, fd, k2[t]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int row = 16 * (first + t) + 4 * g;
+            const f32x4 rise = row_vec(s_vec, kRise, first + t, lane), beta = row_vec(s_vec, kBeta, first + t, lane);
+            e[t] *= a.scale * rise;
+            k2[t] *= beta * row_vec(s_vec, kLeft, first + t, lane);
+            const int p = (row + (i16 >> 2)) * TK::kRow + 16 * tile + 4 * (i16 & 3);
+            const f32x4 qv = __builtin_convertvector(lds_column4(s_q + p), f32x4);
+            const f32x4 kv = __builtin_convertvector(lds_column4(s_k + p), f32x4);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                kds += kv[r] * k2[t][r];
+                const float x = sum16(qv[r] * e[t][r]);
+                if (i16 == 0)
+                    s_rows[tile * kC + row + r] = x;
+            }
+            dq[t] += e[t];
+            dk[t] += k2[t] - beta * rise * f[t];
+        }
+        ss = ss * s_vec[kWhole * kC] + kds;
+#pragma unroll
+        for (int m = 32; m >= 1; m >>= 1)
+            ss += __shfl_xor(ss, m, 64);
+        if (lane == 0)
+            s_sum[wave] = ss;
+        lds_barrier();
+
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const Frag<1> fk = TK::columns(s_k, tile, s, lane), fq = TK::columns(s_q, tile, s, lane);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const int ta = first + t;
+                if (s <= ta / 2) {
+                    dq[t] = mma<1>(M::rows(s_x, ta, s, lane), fk, dq[t]);
+                    dk[t] = mma<1>(M::rows(s_y, ta, s, lane), fk, dk[t]);
+                }
+                if (s >= ta / 2) {
+                    dk[t] = mma<1>(M::columns(s_x, ta, s, lane), fq, dk[t]);
+                    dk[t] = mma<1>(M::columns(s_y, ta, s, lane), fk, dk[t]);
+                }
+            }
+        }
+        if (wave == 0) {
+            float v = -s_vdv[lane];
+            for (int m = 0; m < kTiles; ++m)
+                v += s_rows[m * kC + lane];
+            const int ta = lane >> 4;
+            for (int tb = 0; tb <= ta; ++tb)
+                v += s_blk[block_of(ta, tb) * 16 + (lane & 15)];
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                const float x = __shfl_down(v, m, 64);
+                if (lane + m < 64)
+                    v += x;
+            }
+            for (int m = 0; m < LDS::kWaves; ++m)
+                v += s_sum[m];
+            // the decay of an empty state does nothing
+            const bool empty = s_vec[kResets * kC + lane] != (lane ? s_vec[kResets * kC + lane - 1] : 0.f) ||
+                               (t0 + lane == 0 && !a.s0);
+            if (t0 + lane < a.L)
+                static_cast<float *>(const_cast<void *>(a.dg.p))[b * a.dg.s.b + h * a.dg.s.h + (t0 + lane) * a.dg.s.l] =
+                    empty ? 0.f : v;
+        }
+        lds_barrier();
+    }
+    const Chunk<true> cq(a.dq.p, b * a.dq.s.b + hk * a.dq.s.h, a.dq.s.l, t0, a.L, a.Dk);
+    const Chunk<true> ck(a.dk.p, b * a.dk.s.b + hk * a.dk.s.h, a.dk.s.l, t0, a.L, a.Dk);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        store_cols<true>(cq, dim, lane, first + t, dq[t]);
+        store_cols<true>(ck, dim, lane, first + t, dk[t]);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -1852,9 +2140,15 @@ int launch_bwd(const DeltaArgs &a, hipStream_t stream)
     }
     if (rc == PDSSM_OK)
         rc = launch(reverse_kernel<KD, BF16, VEC>, a.heads * a.slices, chain_lds<KD, BF16>(true), a, stream);
-    if (rc == PDSSM_OK)
-        rc = launch(grad_kernel<KD, BF16, VEC>, a.heads / a.Hv * a.Hk * a.NC, grad_lds<KD, BF16>(), a, stream);
-    return rc;
+    if (rc != PDSSM_OK)
+        return rc;
+    const int64_t chunks = a.heads / a.Hv * a.Hk * a.NC;
+    if constexpr (!BF16)
+        return launch(grad_kernel<KD, BF16, VEC>, chunks, grad_lds<KD, BF16>(), a, stream);
+    else if (a.DV <= 64)
+        return launch(grads_kernel<KD, 64, VEC>, chunks, GradLds<KD, 64>::kBytes, a, stream, kGradThreads);
+    else
+        return launch(grads_kernel<KD, 128, VEC>, chunks, GradLds<KD, 128>::kBytes, a, stream, kGradThreads);
 }
 
 // The variant for these sizes, type and rows (vec: see units()).
