@@ -85,6 +85,9 @@ struct DeltaArgs {
     int segs, seg_chunks;
     float *seg_states;      // [B*Hv][segs][KD][DV]: states before the segments
     float *trans;           // [B*Hv][segs][KD][slices*64 + KD]: their ends from zero, and transitions
+    float *seg_grads;       // [B*Hv][segs][KD][DV]: state gradients after the segments
+    float *rtrans;          // [B*Hv][segs][KD][slices*64]: state gradients before them, from zero
+    unsigned back_blocks;   // workgroups of back_kernel that walk back
     int Hk, Hv, L, NC, Dk, Dv, DV, record;
     int slices;             // column slices of a head over workgroups
     float scale;
@@ -831,7 +834,7 @@ struct PipeLds {
 };
 
 template <int KD, bool VEC, int MODE>
-__global__ void __launch_bounds__(kPipeThreads, 1) pipe_kernel(DeltaArgs a)
+__device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
 {
     using LDS = PipeLds<KD>;
     using TK = typename LDS::K;
@@ -840,16 +843,18 @@ __global__ void __launch_bounds__(kPipeThreads, 1) pipe_kernel(DeltaArgs a)
     constexpr int NS = KD / 32;     // k steps over the key dimensions
     extern __shared__ __attribute__((aligned(16))) char s_dyn[];
     uint16_t *lds = reinterpret_cast<uint16_t *>(s_dyn);
-    volatile int *s_flag = reinterpret_cast<volatile int *>(lds + LDS::kFlag);
+    int *s_flag = reinterpret_cast<int *>(lds + LDS::kFlag);
 
     // What this workgroup walks: chunks c0 .. c1 - 1 of 64 columns of a head's
     // state, or (kScan) of 64 columns of the segment's transition, the state
     // that the unit matrix becomes without any v.
-    const int per = MODE == kScan ? a.segs - 1 : a.segs, parts = a.slices + (MODE == kScan ? KD / 64 : 0);
-    const int64_t head = blockIdx.x / (unsigned)(per * parts);
-    const int rest = blockIdx.x % (unsigned)(per * parts), seg = rest / parts, slice = rest % parts;
+    // A scan leaves out what no joining asks for: the first segment's
+    // transition, the last one's end (and its transition, in the forward).
+    const int parts = a.slices + (MODE == kScan ? KD / 64 : 0);
+    const int64_t head = block / (unsigned)(a.segs * parts);
+    const int rest = block % (unsigned)(a.segs * parts), seg = rest / parts, slice = rest % parts;
     const bool unit = slice >= a.slices;
-    if (unit && seg == 0)
+    if (MODE == kScan && (unit ? seg == 0 || (seg == a.segs - 1 && !a.d_o.p) : seg == a.segs - 1))
         return;
     const int c0 = seg * a.seg_chunks, c1 = min(a.NC, c0 + a.seg_chunks);
     int64_t b;
@@ -900,10 +905,8 @@ __global__ void __launch_bounds__(kPipeThreads, 1) pipe_kernel(DeltaArgs a)
                         *reinterpret_cast<bf16x4 *>(x + n * LDS::kSPart + 32 * s) = __builtin_shufflevector(v, v, 0, 1, 2, 3);
                         *reinterpret_cast<bf16x4 *>(x + n * LDS::kSPart + 32 * s + 16) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
                     }
-                lds_order();
                 if (lane == 0)
-                    s_flag[mine] = c + 1;
-                lds_order();
+                    LdsFlag::set(&s_flag[mine], c + 1);
             }
             if constexpr (MODE == kKeep) {
                 const Sheet out(a.states + (head * a.NC + c) * KD * a.DV, KD, a.DV, col, lane);
@@ -1088,9 +1091,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) pipe_kernel(DeltaArgs a)
 #pragma unroll
                 for (int t = 0; t < kBlocks; ++t)
                     pf[t] = *reinterpret_cast<const f32x4 *>(P + t * kBlock + 4 * lane);
-                while (s_flag[mine] <= c)
-                    __builtin_amdgcn_s_sleep(1);
-                lds_order();
+                LdsFlag::await(&s_flag[mine], c + 1);
                 const uint16_t *x = lds + LDS::kS + mine * 2 * LDS::kSPart + i16 * LDS::kSRow + 8 * g;
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
@@ -1120,32 +1121,372 @@ __global__ void __launch_bounds__(kPipeThreads, 1) pipe_kernel(DeltaArgs a)
 }
 
 // ---------------------------------------------------------------------------
+// The walk back, in the same form: the chain waves carry the gradient of the
+// state through w, the help waves stage and form what does not depend on it,
+// P^T dO before a chunk and Q^T (scale rise dO) during it, handed over as fp32
+// tiles in LDS; the chain leaves w and the new gradient in the same places,
+// from where the help waves write w, dV and the gradient to memory.  SCAN: the
+// gradient before the segment alone, from zero after it.
+// ---------------------------------------------------------------------------
+template <int KD>
+struct BackLds {
+    using K = Tile<KD, true>;
+    // in uint16_t
+    static constexpr int kK = 0;
+    static constexpr int kQ = kK + 2 * K::kSize;
+    static constexpr int kZ = kQ + 2 * K::kSize;
+    static constexpr int kVec = kZ + 2 * Tri<true>::kSize;
+    static constexpr int kFlag = kVec + 4 * 4 * kC * 2;  // four chunks' vectors: the last is still read
+    static constexpr int kD = kFlag + 16;               // [4 waves][4 tiles][64 lanes] of f32x4
+    static constexpr int kE = kD + 4 * 4 * 64 * 8;      // [4 waves][KD / 16 tiles][64 lanes]
+    static constexpr size_t kBytes = (kE + 4 * (KD / 16) * 64 * 8) * 2;
+};
+
+template <int KD, bool VEC, bool SCAN>
+__device__ __forceinline__ void back_walk(const DeltaArgs &a, unsigned block)
+{
+    using LDS = BackLds<KD>;
+    using TK = typename LDS::K;
+    using U_ = Tri<true>;
+    constexpr int NS = KD / 32, NM = KD / 16;
+    extern __shared__ __attribute__((aligned(16))) char s_dyn[];
+    uint16_t *lds = reinterpret_cast<uint16_t *>(s_dyn);
+    int *s_flag = reinterpret_cast<int *>(lds + LDS::kFlag);      // [2][4]: D, E ready
+
+    const int64_t head = block / (unsigned)(a.segs * a.slices);
+    const int rest = block % (unsigned)(a.segs * a.slices), seg = rest / a.slices, slice = rest % a.slices;
+    if (SCAN && seg == 0)
+        return;
+    const int c0 = seg * a.seg_chunks, c1 = min(a.NC, c0 + a.seg_chunks);
+    int64_t b;
+    int h;
+    const int64_t hk = kv_head(a, head, b, h);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i16 = lane & 15;
+    const int mine = wave & 3;
+    const int col = (slice * 4 + mine) * 16 + i16;
+    f32x4 *s_d = reinterpret_cast<f32x4 *>(lds + LDS::kD) + mine * 4 * 64 + lane;
+    f32x4 *s_e = reinterpret_cast<f32x4 *>(lds + LDS::kE) + mine * NM * 64 + lane;
+
+    // Chunk c is step n = c1 - 1 - c of the walk.
+    if (wave < 4) {
+        State<KD> S;
+        if (seg == a.segs - 1)
+            S.load(a.ds_final ? a.ds_final + head * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, col, lane);
+        else
+            S.load(SCAN ? nullptr : a.seg_grads + (head * a.segs + seg) * KD * a.DV, KD, a.DV, col, lane);
+        Frag<3> sf[NS];
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+            sf[s] = split<3>(S.s[2 * s], S.s[2 * s + 1]);
+        if constexpr (!SCAN) {
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+                s_e[m * 64] = S.s[m];
+        }
+        if (lane == 0)
+            s_flag[mine] = s_flag[4 + mine] = 0;
+        lds_barrier();
+        for (int n = 0; n < c1 - c0; ++n) {
+            const int half = n & 1;
+            const uint16_t *s_k = lds + LDS::kK + half * TK::kSize, *s_z = lds + LDS::kZ + half * U_::kSize;
+            const float *s_vec = reinterpret_cast<const float *>(lds + LDS::kVec) + (n & 3) * 4 * kC;
+            Frag<1> kr[NS][4];
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    kr[s][t] = TK::rows_stacked(s_k, t, s, lane);
+            __builtin_amdgcn_sched_barrier(0);
+            f32x4 d[4], x[4], w[4];
+            Frag<3> z0[2], z1[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                d[t] = w[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                if (s == NS / 2) {
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        z1[t] = U_::template get<3>(s_z, t, 1, lane);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+#pragma unroll
+                for (int o = 2; o >= 0; --o)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kr[s][t].p[0], sf[s].p[o], d[t], 0, 0, 0);
+            }
+            LdsFlag::await(&s_flag[mine], n + 1);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                d[t] = s_d[t * 64] + row_vec(s_vec, kLeft, t, lane) * d[t];     // dU
+                x[t] = row_vec(s_vec, kBeta, t, lane) * d[t];
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                z0[t] = U_::template get<3>(s_z, t, 0, lane);
+            Frag<1> kc0[NM], kc1[NM];
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+                kc0[m] = TK::columns_stacked(s_k, m, 0, lane);
+            __builtin_amdgcn_sched_barrier(0);
+            const Frag<3> f0 = split<3>(x[0], x[1]), f1 = split<3>(x[2], x[3]);
+#pragma unroll
+            for (int o = 2; o >= 0; --o)
+#pragma unroll
+                for (int i = 0; i <= o; ++i) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        w[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(z1[t].p[i], f1.p[o - i], w[t], 0, 0, 0);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        w[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(z0[t].p[i], f0.p[o - i], w[t], 0, 0, 0);
+                }
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+                kc1[m] = TK::columns_stacked(s_k, m, 1, lane);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                w[t] = d[t] - w[t];
+                if constexpr (!SCAN)
+                    s_d[t * 64] = w[t];
+                w[t] *= -row_vec(s_vec, kBeta, t, lane) * row_vec(s_vec, kRise, t, lane);
+            }
+            const float whole = s_vec[kWhole * kC];
+            const Frag<3> w0 = split<3>(w[0], w[1]), w1 = split<3>(w[2], w[3]);
+            LdsFlag::await(&s_flag[4 + mine], n + 1);
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+                S.s[m] = S.s[m] * whole + s_e[m * 64];
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+#pragma unroll
+                for (int o = 2; o >= 0; --o)
+#pragma unroll
+                    for (int m = 2 * s; m < 2 * s + 2; ++m) {
+                        S.s[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc0[m].p[0], w0.p[o], S.s[m], 0, 0, 0);
+                        S.s[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc1[m].p[0], w1.p[o], S.s[m], 0, 0, 0);
+                    }
+                sf[s] = split<3>(S.s[2 * s], S.s[2 * s + 1]);
+                if constexpr (!SCAN) {
+#pragma unroll
+                    for (int m = 2 * s; m < 2 * s + 2; ++m)
+                        s_e[m * 64] = S.s[m];
+                }
+            }
+            lds_barrier();
+        }
+        if constexpr (SCAN)
+            S.store(a.rtrans + (head * a.segs + seg) * KD * (a.slices * 64), KD, a.slices * 64, col, lane);
+        else if (a.ds0 && seg == 0)
+            S.store(a.ds0 + head * a.Dk * a.Dv, a.Dk, a.Dv, col, lane);
+    } else {
+        const int tid = threadIdx.x - 256;
+        const int64_t ek = b * a.k.s.b + hk * a.k.s.h, eq = b * a.q.s.b + hk * a.q.s.h;
+        const int64_t eo = b * a.d_o.s.b + h * a.d_o.s.h;
+        const float *rec = a.records + head * a.NC * (int64_t)a.record;
+        TK tk, tq;
+        U_ tz;
+        f32x4 vecs;
+        auto fetch = [&](int c) {
+            const float *r = rec + (int64_t)c * a.record;
+            tk.template load<VEC>({a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk}, tid);
+            tq.template load<VEC>({a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk}, tid);
+            tz.load(r + Record::kZt, tid);
+            vecs = load_vecs(r + Record::kVec, tid);
+        };
+        auto stage = [&](int n) {
+            const int half = n & 1;
+            tk.store(lds + LDS::kK + half * TK::kSize, tid);
+            tq.store(lds + LDS::kQ + half * TK::kSize, tid);
+            tz.store(lds + LDS::kZ + half * U_::kSize, tid);
+            if (tid < kC)
+                *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(lds + LDS::kVec) + (n & 3) * 4 * kC + 4 * tid) = vecs;
+        };
+        // P and dO of a chunk, and P^T dO of it
+        f32x4 pf[kBlocks], pd[4];
+        Cols<true> cols, now;       // dO of the chunk that pf is of, and of the one walked
+        auto fetch_o = [&](int c) {
+            const float *P = rec + (int64_t)c * a.record + Record::kP;
+#pragma unroll
+            for (int t = 0; t < kBlocks; ++t)
+                pf[t] = *reinterpret_cast<const f32x4 *>(P + t * kBlock + 4 * lane);
+            cols.load({a.d_o.p, eo, a.d_o.s.l, c * kC, a.L, a.Dv}, col, lane);
+        };
+        auto product = [&]() {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                pd[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const Frag<1> f = split<1>(cols.get(2 * s), cols.get(2 * s + 1));
+#pragma unroll
+                for (int t = 0; t < 2 * s + 2; ++t) {
+                    const Frag<3> p = split<3>(t <= 2 * s ? pf[block_of(2 * s, t < 2 * s ? t : 2 * s)] : f32x4{0.f, 0.f, 0.f, 0.f},
+                                               pf[block_of(2 * s + 1, t)]);
+                    pd[t] = mma<3>(p, f, pd[t]);
+                }
+            }
+        };
+        // w and dV of chunk c, from the chain's w
+        auto results = [&](int c, const f32x4 (&w)[4]) {
+            const Sheet out(a.w + (head * a.NC + c) * kC * a.DV, kC, a.DV, col, lane);
+            const Chunk<true> cv(a.dv.p, b * a.dv.s.b + h * a.dv.s.h, a.dv.s.l, c * kC, a.L, a.Dv);
+            const float *s_vec = reinterpret_cast<const float *>(lds + LDS::kVec) + ((c1 - 1 - c) & 3) * 4 * kC;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                out.put(t, w[t]);
+                store_cols<true>(cv, col, lane, t, row_vec(s_vec, kBeta, t, lane) * w[t]);
+            }
+        };
+        U_::clear(lds + LDS::kZ, tid);
+        U_::clear(lds + LDS::kZ + U_::kSize, tid);
+        fetch(c1 - 1);
+        fetch_o(c1 - 1);
+        stage(0);
+        if (c1 - 2 >= c0)
+            fetch(c1 - 2);
+        product();
+        now = cols;
+        if (c1 - 2 >= c0)
+            fetch_o(c1 - 2);
+        lds_barrier();
+        for (int n = 0; n < c1 - c0; ++n) {
+            const int c = c1 - 1 - n, half = n & 1;
+            const uint16_t *s_q = lds + LDS::kQ + half * TK::kSize;
+            const float *s_vec = reinterpret_cast<const float *>(lds + LDS::kVec) + (n & 3) * 4 * kC;
+            f32x4 w[4];
+            if constexpr (!SCAN) {
+                if (n > 0) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        w[t] = s_d[t * 64];
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                s_d[t * 64] = pd[t];
+            if (lane == 0)
+                LdsFlag::set(&s_flag[mine], n + 1);
+            if constexpr (!SCAN) {
+                const Sheet out(a.grads + (head * a.NC + c) * KD * a.DV, KD, a.DV, col, lane);
+#pragma unroll
+                for (int m = 0; m < NM; ++m)
+                    out.put(m, s_e[m * 64]);
+            }
+            // Q^T (scale rise dO)
+            f32x4 e[NM];
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+                e[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const Frag<3> f = split<3>(a.scale * row_vec(s_vec, kRise, 2 * s, lane) * now.get(2 * s),
+                                           a.scale * row_vec(s_vec, kRise, 2 * s + 1, lane) * now.get(2 * s + 1));
+#pragma unroll
+                for (int m = 0; m < NM; ++m)
+                    e[m] = mma<3>(TK::columns_stacked(s_q, m, s, lane), f, e[m]);
+            }
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+                s_e[m * 64] = e[m];
+            if (lane == 0)
+                LdsFlag::set(&s_flag[4 + mine], n + 1);
+            // Loads wait for a turn of the walk before their use and come
+            // before its stores: the counter that a load is waited for by
+            // runs in order over both.
+            if (c > c0) {
+                stage(n + 1);
+                if (c - 1 > c0)
+                    fetch(c - 2);
+                product();
+                now = cols;
+                if (c - 1 > c0)
+                    fetch_o(c - 2);
+            }
+            if constexpr (!SCAN) {
+                if (n > 0)
+                    results(c + 1, w);
+            }
+            lds_barrier();
+        }
+        if constexpr (!SCAN) {
+            f32x4 w[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                w[t] = s_d[t * 64];
+            results(c0, w);
+        }
+    }
+}
+
+template <int KD, bool VEC, int MODE>
+__global__ void __launch_bounds__(kPipeThreads, 1) pipe_kernel(DeltaArgs a)
+{
+    pipe_walk<KD, VEC, MODE>(a, blockIdx.x);
+}
+
+// The backward's walks: neither needs the other, so both are one launch, the
+// first `back_blocks` workgroups walking back.
+template <int KD, bool VEC, bool SCAN>
+__global__ void __launch_bounds__(kPipeThreads, 1) back_kernel(DeltaArgs a)
+{
+    if (blockIdx.x < a.back_blocks)
+        back_walk<KD, VEC, SCAN>(a, blockIdx.x);
+    else
+        pipe_walk<KD, VEC, SCAN ? kScan : kKeep>(a, blockIdx.x - a.back_blocks);
+}
+
+// ---------------------------------------------------------------------------
 // join_kernel: the states before segments 1 .. segs - 1 of a head, from the
-// segments' transitions A and ends B: S <- A S + B.  A wave owns 16 columns.
+// segments' transitions A and ends B: S <- A S + B; behind those workgroups
+// (in the backward) the state gradients after segments segs - 2 .. 0:
+// dS <- A^T dS + C.  A wave owns 16 columns.
 // ---------------------------------------------------------------------------
 template <int KD>
 __global__ void __launch_bounds__(kThreads) join_kernel(DeltaArgs a)
 {
-    const int64_t head = blockIdx.x / (unsigned)a.slices;
-    const int slice = blockIdx.x % (unsigned)a.slices;
+    const bool back = blockIdx.x >= a.heads * a.slices;
+    const unsigned block = blockIdx.x - (back ? (unsigned)(a.heads * a.slices) : 0u);
+    const int64_t head = block / (unsigned)a.slices;
+    const int slice = block % (unsigned)a.slices;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, i16 = lane & 15;
     const int col = (slice * 4 + wave) * 16 + i16, pitch = a.slices * 64 + KD;
     const float *T = a.trans + head * a.segs * KD * (int64_t)pitch;
+    const float *C = a.rtrans + head * a.segs * KD * (int64_t)(a.slices * 64);
     State<KD> S, N;
-    S.load(T, KD, pitch, col, lane);
-    for (int seg = 1;; ++seg) {
-        S.store(a.seg_states + (head * a.segs + seg) * KD * a.DV, KD, a.DV, col, lane);
-        if (seg + 1 >= a.segs)
+    if (back)
+        S.load(C + (int64_t)(a.segs - 1) * KD * (a.slices * 64), KD, a.slices * 64, col, lane);
+    else
+        S.load(T, KD, pitch, col, lane);
+    for (int n = 1;; ++n) {
+        const int seg = back ? a.segs - 1 - n : n;
+        S.store((back ? a.seg_grads : a.seg_states) + (head * a.segs + seg) * KD * a.DV, KD, a.DV, col, lane);
+        if (n + 1 >= a.segs)
             break;
-        const float *t = T + (int64_t)seg * KD * pitch, *A = t + a.slices * 64;
-        N.load(t, KD, pitch, col, lane);
+        const float *A = T + (int64_t)seg * KD * pitch + a.slices * 64;
+        if (back)
+            N.load(C + (int64_t)seg * KD * (a.slices * 64), KD, a.slices * 64, col, lane);
+        else
+            N.load(A - a.slices * 64, KD, pitch, col, lane);
 #pragma unroll
         for (int s = 0; s < KD / 32; ++s) {
             const Frag<3> f = split<3>(S.s[2 * s], S.s[2 * s + 1]);
 #pragma unroll
             for (int m = 0; m < KD / 16; ++m) {
-                const float *p = A + (16 * m + i16) * pitch + 32 * s + 4 * g;
-                N.s[m] = mma<3>(split<3>(*reinterpret_cast<const f32x4 *>(p), *reinterpret_cast<const f32x4 *>(p + 16)), f, N.s[m]);
+                f32x4 lo, hi;
+                if (back) {
+                    const float *p = A + (32 * s + 4 * g) * pitch + 16 * m + i16;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        lo[r] = p[r * pitch], hi[r] = p[(16 + r) * pitch];
+                } else {
+                    const float *p = A + (16 * m + i16) * pitch + 32 * s + 4 * g;
+                    lo = *reinterpret_cast<const f32x4 *>(p);
+                    hi = *reinterpret_cast<const f32x4 *>(p + 16);
+                }
+                N.s[m] = mma<3>(split<3>(lo, hi), f, N.s[m]);
             }
         }
         S = N;
@@ -2015,7 +2356,7 @@ Cut cut_of(int64_t heads, int64_t L, int Dv, uint32_t flags)
 }
 
 struct Layout {
-    int64_t records, seg_states, trans, states, grads, ut, w, total;
+    int64_t records, seg_states, trans, seg_grads, rtrans, states, grads, ut, w, total;
     Cut cut;
 };
 
@@ -2031,7 +2372,9 @@ Layout layout_of(int64_t B, int64_t Hv, int64_t L, int Dk, int Dv, uint32_t flag
     l.records = 0;
     l.seg_states = chunks * (bwd ? Record::kBwd : Record::kFwd) * 4;
     l.trans = l.seg_states + cuts * state;
-    l.states = l.trans + cuts * padded_key(Dk) * (slices_of(Dv) * 64 + padded_key(Dk)) * 4;
+    l.seg_grads = l.trans + cuts * padded_key(Dk) * (slices_of(Dv) * 64 + padded_key(Dk)) * 4;
+    l.rtrans = l.seg_grads + (bwd ? cuts * state : 0);
+    l.states = l.rtrans + (bwd ? cuts * padded_key(Dk) * slices_of(Dv) * 64 * 4 : 0);
     l.grads = l.states + (bwd ? chunks * state : 0);
     l.ut = l.grads + (bwd ? chunks * state : 0);
     l.w = l.ut + (bwd ? chunks * rows : 0);
@@ -2046,6 +2389,8 @@ void place_workspace(DeltaArgs &a, const Layout &l, void *workspace)
     a.records = reinterpret_cast<float *>(ws + l.records);
     a.seg_states = reinterpret_cast<float *>(ws + l.seg_states);
     a.trans = reinterpret_cast<float *>(ws + l.trans);
+    a.seg_grads = reinterpret_cast<float *>(ws + l.seg_grads);
+    a.rtrans = reinterpret_cast<float *>(ws + l.rtrans);
     a.segs = l.cut.segs;
     a.seg_chunks = l.cut.chunks;
 }
@@ -2096,59 +2441,58 @@ constexpr size_t grad_lds()
     return (size_t)(2 * Tile<KD, BF16>::kSize + 2 * Tile<kC, BF16>::kSize) * 2 + (kVecs * kC + 5 * kC + 4) * 4;
 }
 
-// The states before the segments, where the chunks are cut.
-template <int KD, bool VEC>
-int launch_segments(const DeltaArgs &a, hipStream_t stream)
-{
-    if (a.segs < 2)
-        return PDSSM_OK;
-    const int rc = launch(pipe_kernel<KD, VEC, kScan>, a.heads * (a.segs - 1) * (a.slices + KD / 64),
-                          PipeLds<KD>::bytes(false), a, stream, kPipeThreads);
-    return rc != PDSSM_OK ? rc : launch(join_kernel<KD>, a.heads * a.slices, 0, a, stream);
-}
-
 template <int KD, bool BF16, bool VEC>
 int launch_fwd(const DeltaArgs &a, hipStream_t stream)
 {
     int rc = launch(prep_kernel<KD, BF16, VEC, false>, a.heads * a.NC, 0, a, stream);
     if (rc != PDSSM_OK)
         return rc;
+    const int64_t walks = a.heads * a.slices;
     if constexpr (BF16) {
-        rc = launch_segments<KD, VEC>(a, stream);
+        if (a.segs > 1) {
+            rc = launch(pipe_kernel<KD, VEC, kScan>, a.heads * a.segs * (a.slices + KD / 64), PipeLds<KD>::bytes(false), a,
+                        stream, kPipeThreads);
+            if (rc == PDSSM_OK)
+                rc = launch(join_kernel<KD>, walks, 0, a, stream);
+        }
         if (rc == PDSSM_OK)
-            rc = launch(pipe_kernel<KD, VEC, kOut>, a.heads * a.slices * a.segs, PipeLds<KD>::bytes(true), a, stream,
-                        kPipeThreads);
+            rc = launch(pipe_kernel<KD, VEC, kOut>, walks * a.segs, PipeLds<KD>::bytes(true), a, stream, kPipeThreads);
         return rc;
     } else {
-        return launch(chain_kernel<KD, BF16, VEC, false>, a.heads * a.slices, chain_lds<KD, BF16>(true), a, stream);
+        return launch(chain_kernel<KD, BF16, VEC, false>, walks, chain_lds<KD, BF16>(true), a, stream);
     }
 }
 
 template <int KD, bool BF16, bool VEC>
-int launch_bwd(const DeltaArgs &a, hipStream_t stream)
+int launch_bwd(DeltaArgs a, hipStream_t stream)
 {
     int rc = launch(prep_kernel<KD, BF16, VEC, true>, a.heads * a.NC, 0, a, stream);
     if (rc != PDSSM_OK)
         return rc;
+    const int64_t walks = a.heads * a.slices, chunks = a.heads / a.Hv * a.Hk * a.NC;
     if constexpr (BF16) {
-        rc = launch_segments<KD, VEC>(a, stream);
+        constexpr size_t lds = BackLds<KD>::kBytes > PipeLds<KD>::bytes(false) ? BackLds<KD>::kBytes : PipeLds<KD>::bytes(false);
+        a.back_blocks = (unsigned)(walks * a.segs);
+        if (a.segs > 1) {
+            rc = launch(back_kernel<KD, VEC, true>, (walks * 2 + a.heads * (KD / 64)) * a.segs, lds, a, stream, kPipeThreads);
+            if (rc == PDSSM_OK)
+                rc = launch(join_kernel<KD>, walks * 2, 0, a, stream);
+        }
         if (rc == PDSSM_OK)
-            rc = launch(pipe_kernel<KD, VEC, kKeep>, a.heads * a.slices * a.segs, PipeLds<KD>::bytes(false), a, stream,
-                        kPipeThreads);
-    } else {
-        rc = launch(chain_kernel<KD, BF16, VEC, true>, a.heads * a.slices, chain_lds<KD, BF16>(false), a, stream);
-    }
-    if (rc == PDSSM_OK)
-        rc = launch(reverse_kernel<KD, BF16, VEC>, a.heads * a.slices, chain_lds<KD, BF16>(true), a, stream);
-    if (rc != PDSSM_OK)
-        return rc;
-    const int64_t chunks = a.heads / a.Hv * a.Hk * a.NC;
-    if constexpr (!BF16)
-        return launch(grad_kernel<KD, BF16, VEC>, chunks, grad_lds<KD, BF16>(), a, stream);
-    else if (a.DV <= 64)
-        return launch(grads_kernel<KD, 64, VEC>, chunks, GradLds<KD, 64>::kBytes, a, stream, kGradThreads);
-    else
+            rc = launch(back_kernel<KD, VEC, false>, walks * 2 * a.segs, lds, a, stream, kPipeThreads);
+        if (rc != PDSSM_OK)
+            return rc;
+        if (a.DV <= 64)
+            return launch(grads_kernel<KD, 64, VEC>, chunks, GradLds<KD, 64>::kBytes, a, stream, kGradThreads);
         return launch(grads_kernel<KD, 128, VEC>, chunks, GradLds<KD, 128>::kBytes, a, stream, kGradThreads);
+    } else {
+        rc = launch(chain_kernel<KD, BF16, VEC, true>, walks, chain_lds<KD, BF16>(false), a, stream);
+        if (rc == PDSSM_OK)
+            rc = launch(reverse_kernel<KD, BF16, VEC>, walks, chain_lds<KD, BF16>(true), a, stream);
+        if (rc == PDSSM_OK)
+            rc = launch(grad_kernel<KD, BF16, VEC>, chunks, grad_lds<KD, BF16>(), a, stream);
+        return rc;
+    }
 }
 
 // The variant for these sizes, type and rows (vec: see units()).

@@ -129,6 +129,26 @@ __device__ __forceinline__ bf16x8 lds_columns4(const uint16_t *p, const uint16_t
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// A flag in LDS: `set` comes after the wave's LDS writes before it, `await`
+// returns once the flag is at least v and before the LDS reads after it.  (LDS
+// instructions of a wave take effect in order; through a generic pointer the
+// flag would also wait for the loads from memory in flight.)
+struct LdsFlag {
+    typedef __attribute__((address_space(3))) int lds_int;
+    static __device__ __forceinline__ void set(int *p, int v)
+    {
+        asm volatile("" ::: "memory");
+        *(volatile lds_int *)(lds_int *)p = v;
+        asm volatile("" ::: "memory");
+    }
+    static __device__ __forceinline__ void await(int *p, int v)
+    {
+        while (*(volatile lds_int *)(lds_int *)p < v)
+            __builtin_amdgcn_s_sleep(1);
+        asm volatile("" ::: "memory");
+    }
+};
+
 // A workgroup barrier that orders LDS only: loads from memory stay in flight
 // across it (__syncthreads waits for them).
 __device__ __forceinline__ void lds_barrier()
