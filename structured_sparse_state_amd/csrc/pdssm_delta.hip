@@ -122,12 +122,15 @@ struct Chunk {
     static constexpr uint32_t kSize = BF16 ? 2 : 4;
 
     // Rows t0 .. of L of the sequence that begins at element e0.
-    __device__ __forceinline__ Chunk(const void *base, int64_t e0, int64_t s, int t0, int L, int D_)
+    // `none`: as if it had no rows.
+    __device__ __forceinline__ Chunk(const void *base, int64_t e0, int64_t s, int t0, int L, int D_, bool none = false)
     {
         rows = min(L - t0, kC);
         D = D_;
         stride = (uint32_t)s * kSize;
         r = make_rsrc(static_cast<const char *>(base) + (e0 + t0 * s) * kSize, (uint64_t)(rows - 1) * stride + D * kSize);
+        if (none)
+            rows = 0;
     }
     // A lane's own part of an offset.  Opaque, so that the offsets of a loop's
     // many rows are formed where they are used (an addition of a scalar each)
@@ -521,11 +524,8 @@ struct Tri {
     __device__ __forceinline__ void load(const float *blocks, int tid)
     {
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            const int x = tid + i * kThreads;
-            if (x < kBlocks * 64)
-                u[i] = *reinterpret_cast<const f32x4 *>(blocks + 4 * x);
-        }
+        for (int i = 0; i < kUnits; ++i)    // (without a branch: see pipe_walk)
+            u[i] = *reinterpret_cast<const f32x4 *>(blocks + 4 * min(tid + i * kThreads, kBlocks * 64 - 1));
     }
     __device__ __forceinline__ void store(uint16_t *lds, int tid) const
     {
@@ -635,11 +635,11 @@ struct State {
 struct Sheet {
     __amdgpu_buffer_rsrc_t r;
     uint32_t lane, pitch;
-    __device__ __forceinline__ Sheet(float *p, int rows, int DV, int col, int lane_)
+    __device__ __forceinline__ Sheet(float *p, int rows, int DV, int col, int lane_, bool none = false)
     {
         pitch = DV * 4;
         r = make_rsrc(p, (uint64_t)rows * pitch);
-        lane = col < DV ? (uint32_t)opaque((lane_ >> 4) * 4 * (int)pitch + col * 4) : kOutside;
+        lane = col < DV && !none ? (uint32_t)opaque((lane_ >> 4) * 4 * (int)pitch + col * 4) : kOutside;
     }
     __device__ __forceinline__ void put(int tile, f32x4 v) const
     {
@@ -652,7 +652,7 @@ struct Sheet {
 // Four vectors of the record in LDS (rise, left, beta, whole).
 __device__ __forceinline__ f32x4 load_vecs(const float *vec, int tid)
 {
-    return tid < kC ? *reinterpret_cast<const f32x4 *>(vec + 4 * tid) : f32x4{0.f, 0.f, 0.f, 0.f};
+    return *reinterpret_cast<const f32x4 *>(vec + 4 * (tid % kC));
 }
 __device__ __forceinline__ f32x4 row_vec(const float *s_vec, int which, int a, int lane)
 {
@@ -1066,27 +1066,32 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
                     qs[t] = mma<2>(p, f, qs[t]);
                 }
             }
-            const Chunk<true> co(a.o.p, b * a.o.s.b + h * a.o.s.h, a.o.s.l, c * kC, a.L, a.Dv);
+            const Chunk<true> co(a.o.p, b * a.o.s.b + h * a.o.s.h, a.o.s.l, max(c, c0) * kC, a.L, a.Dv, c < c0);
 #pragma unroll
             for (int t = 0; t < 4; ++t)
                 store_cols<true>(co, col, lane, t, qs[t]);
         };
         stage(0);
-        if (c0 + 1 < c1)
-            fetch(c0 + 1);
-        if constexpr (MODE == kOut)
+        fetch(min(c0 + 1, c1 - 1));
+        if constexpr (MODE == kOut) {
             fetch_q(c0);
+#pragma unroll
+            for (int t = 0; t < kBlocks; ++t)
+                pf[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                qs[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
         lds_barrier();
         for (int c = c0; c < c1; ++c) {
             const int half = (c - c0) & 1;
-            if (c + 1 < c1) {
-                stage(half ^ 1);
-                if (c + 2 < c1)
-                    fetch(c + 2);
-            }
+            // No branch on the way: where two paths with other loads in flight
+            // meet, a wait for one load becomes a wait for all.  The first turn
+            // writes no outputs, the last ones stage the last chunk again.
+            stage(half ^ 1);
+            fetch(min(c + 2, c1 - 1));
             if constexpr (MODE == kOut) {
-                if (c > c0)
-                    output(c - 1);
+                output(c - 1);
                 const float *P = rec + (int64_t)c * a.record + Record::kP;
 #pragma unroll
                 for (int t = 0; t < kBlocks; ++t)
@@ -1110,8 +1115,7 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
                     qs[t] *= a.scale * row_vec(s_vec, kRise, t, lane);
-                if (c + 1 < c1)
-                    fetch_q(c + 1);
+                fetch_q(min(c + 1, c1 - 1));
             }
             lds_barrier();
         }
@@ -1331,8 +1335,9 @@ __device__ __forceinline__ void back_walk(const DeltaArgs &a, unsigned block)
         };
         // w and dV of chunk c, from the chain's w
         auto results = [&](int c, const f32x4 (&w)[4]) {
-            const Sheet out(a.w + (head * a.NC + c) * kC * a.DV, kC, a.DV, col, lane);
-            const Chunk<true> cv(a.dv.p, b * a.dv.s.b + h * a.dv.s.h, a.dv.s.l, c * kC, a.L, a.Dv);
+            const int at = min(c, c1 - 1);
+            const Sheet out(a.w + (head * a.NC + at) * kC * a.DV, kC, a.DV, col, lane, c >= c1);
+            const Chunk<true> cv(a.dv.p, b * a.dv.s.b + h * a.dv.s.h, a.dv.s.l, at * kC, a.L, a.Dv, c >= c1);
             const float *s_vec = reinterpret_cast<const float *>(lds + LDS::kVec) + ((c1 - 1 - c) & 3) * 4 * kC;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -1345,12 +1350,10 @@ __device__ __forceinline__ void back_walk(const DeltaArgs &a, unsigned block)
         fetch(c1 - 1);
         fetch_o(c1 - 1);
         stage(0);
-        if (c1 - 2 >= c0)
-            fetch(c1 - 2);
+        fetch(max(c1 - 2, c0));
         product();
         now = cols;
-        if (c1 - 2 >= c0)
-            fetch_o(c1 - 2);
+        fetch_o(max(c1 - 2, c0));
         lds_barrier();
         for (int n = 0; n < c1 - c0; ++n) {
             const int c = c1 - 1 - n, half = n & 1;
@@ -1358,11 +1361,9 @@ __device__ __forceinline__ void back_walk(const DeltaArgs &a, unsigned block)
             const float *s_vec = reinterpret_cast<const float *>(lds + LDS::kVec) + (n & 3) * 4 * kC;
             f32x4 w[4];
             if constexpr (!SCAN) {
-                if (n > 0) {
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        w[t] = s_d[t * 64];
-                }
+                for (int t = 0; t < 4; ++t)
+                    w[t] = s_d[t * 64];     // of the chunk before; the first turn has none
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t)
@@ -1396,19 +1397,13 @@ __device__ __forceinline__ void back_walk(const DeltaArgs &a, unsigned block)
             // Loads wait for a turn of the walk before their use and come
             // before its stores: the counter that a load is waited for by
             // runs in order over both.
-            if (c > c0) {
-                stage(n + 1);
-                if (c - 1 > c0)
-                    fetch(c - 2);
-                product();
-                now = cols;
-                if (c - 1 > c0)
-                    fetch_o(c - 2);
-            }
-            if constexpr (!SCAN) {
-                if (n > 0)
-                    results(c + 1, w);
-            }
+            stage(n + 1);
+            fetch(max(c - 2, c0));
+            product();
+            now = cols;
+            fetch_o(max(c - 2, c0));
+            if constexpr (!SCAN)
+                results(c + 1, w);
             lds_barrier();
         }
         if constexpr (!SCAN) {

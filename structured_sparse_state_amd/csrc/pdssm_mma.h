@@ -35,15 +35,25 @@ struct Frag {
     bf16x8 p[N];
 };
 
-// One part of two values as a word, leaving the rest in them (the words are
-// built by the packed conversion; element-wise conversions would be made one
-// by one).
+// One part of two values as a word, leaving the rest in them: one packed
+// conversion, and one two-term dot product for each rest, a + w . (-1, 0),
+// which is exact and spares the unpacking of the word.  The factors are kept
+// from the compiler's sight: as literals it writes them in a 32-bit form whose
+// upper half the instruction takes for both.
 __device__ __forceinline__ uint32_t take_part(float &a, float &b, bool rest)
 {
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
     const uint32_t w = f32x2_to_bf16x2_rne(a, b);
     if (rest) {
-        a -= bf16_lo(w);
-        b -= bf16_hi(w);
+        uint32_t first = 0x0000BF80u, second = 0xBF800000u;
+        asm("" : "+s"(first));
+        asm("" : "+s"(second));
+        bf16x2_t h, f, s;
+        __builtin_memcpy(&h, &w, 4);
+        __builtin_memcpy(&f, &first, 4);
+        __builtin_memcpy(&s, &second, 4);
+        a = __builtin_amdgcn_fdot2_f32_bf16(h, f, a, false);
+        b = __builtin_amdgcn_fdot2_f32_bf16(h, s, b, false);
     }
     return w;
 }
