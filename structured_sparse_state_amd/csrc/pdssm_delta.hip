@@ -114,7 +114,11 @@ struct Unit<false> {
 constexpr uint32_t kOutside = 0x80000000u;
 constexpr int64_t kMaxStride = 1 << 23;     // 64 rows of 4-byte values stay below 2^31 bytes
 
-template <bool BF16>
+//
+// VEC: rows of 16-byte units that do not overlap (see units() on the host).
+// Rows past the sequence then lie past the buffer by themselves, and only the
+// columns need a look.
+template <bool BF16, bool VEC>
 struct Chunk {
     __amdgpu_buffer_rsrc_t r;
     uint32_t stride;        // bytes between rows
@@ -125,28 +129,26 @@ struct Chunk {
     // `none`: as if it had no rows.
     __device__ __forceinline__ Chunk(const void *base, int64_t e0, int64_t s, int t0, int L, int D_, bool none = false)
     {
-        rows = min(L - t0, kC);
+        rows = none ? 0 : min(L - t0, kC);
         D = D_;
         stride = (uint32_t)s * kSize;
-        r = make_rsrc(static_cast<const char *>(base) + (e0 + t0 * s) * kSize, (uint64_t)(rows - 1) * stride + D * kSize);
-        if (none)
-            rows = 0;
+        r = make_rsrc(static_cast<const char *>(base) + (e0 + t0 * s) * kSize,
+                      none ? 0 : (uint64_t)(rows - 1) * stride + D * kSize);
     }
     // A lane's own part of an offset.  Opaque, so that the offsets of a loop's
     // many rows are formed where they are used (an addition of a scalar each)
     // and not held in registers across the loop.
     __device__ __forceinline__ uint32_t lane_at(int row, int col) const
     {
-        return (uint32_t)opaque((int)(row * stride + col * kSize));
+        return (uint32_t)opaque(VEC && col >= D ? (int)kOutside : (int)(row * stride + col * kSize));
     }
     // The offset of lane row + `up`, `up` the same for all lanes.
     __device__ __forceinline__ uint32_t at(uint32_t lane, int row, int up, int col) const
     {
-        return row + up < rows && col < D ? lane + up * stride : kOutside;
+        return VEC || (row + up < rows && col < D) ? lane + up * stride : kOutside;
     }
     // Values col .. col + 7 of a row; VEC: rows begin on 16 bytes and hold
     // whole units.
-    template <bool VEC>
     __device__ __forceinline__ Unit<BF16> unit(uint32_t lane, int row, int up, int col) const
     {
         Unit<BF16> u;
@@ -171,17 +173,21 @@ struct Chunk {
         }
         return u;
     }
-    template <bool VEC>
-    __device__ __forceinline__ Unit<BF16> unit(int row, int col) const
-    {
-        return unit<VEC>(lane_at(row, col), row, 0, col);
-    }
+    __device__ __forceinline__ Unit<BF16> unit(int row, int col) const { return unit(lane_at(row, col), row, 0, col); }
     __device__ __forceinline__ uint32_t raw(uint32_t lane, int row, int up, int col) const
     {
         if constexpr (BF16)
             return bload<uint16_t>(r, at(lane, row, up, col), 0);
         else
             return bload<uint32_t>(r, at(lane, row, up, col), 0);
+    }
+    // Eight values of lane row + up (VEC, bf16).
+    __device__ __forceinline__ void put8(uint32_t lane, int up, bf16x8 v) const
+    {
+        typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+        u32x4 w;
+        __builtin_memcpy(&w, &v, 16);
+        __builtin_amdgcn_raw_buffer_store_b128(w, r, lane + up * stride, 0, 0);
     }
     __device__ __forceinline__ void put(uint32_t lane, int row, int up, int col, float v) const
     {
@@ -230,13 +236,13 @@ struct Tile {
 
     // `tid`: the thread's number among the NT that share the tile.
     template <bool VEC>
-    __device__ __forceinline__ void load(const Chunk<BF16> &c, int tid)
+    __device__ __forceinline__ void load(const Chunk<BF16, VEC> &c, int tid)
     {
         const int row = tid / (KD / 8), col = tid % (KD / 8) * 8;
         const uint32_t lane = c.lane_at(row, col);
 #pragma unroll
         for (int i = 0; i < kUnits; ++i)
-            u[i] = c.template unit<VEC>(lane, row, i * (NT * 8 / KD), col);
+            u[i] = c.unit(lane, row, i * (NT * 8 / KD), col);
     }
     __device__ __forceinline__ void store(uint16_t *lds, int tid) const
     {
@@ -341,8 +347,8 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
 
     {
         T q, k;
-        k.template load<VEC>({a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk}, threadIdx.x);
-        q.template load<VEC>({a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk}, threadIdx.x);
+        k.load(Chunk<BF16, VEC>(a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk), threadIdx.x);
+        q.load(Chunk<BF16, VEC>(a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk), threadIdx.x);
         if (wave == 0) {
             // G in 64 bits (differences of neighbours stay exact to 32), steps
             // with g = -inf counted apart.
@@ -571,7 +577,8 @@ template <bool BF16>
 struct Cols {
     uint32_t raw[4][4];
 
-    __device__ __forceinline__ void load(const Chunk<BF16> &c, int col, int lane)
+    template <bool VEC>
+    __device__ __forceinline__ void load(const Chunk<BF16, VEC> &c, int col, int lane)
     {
         const int row = 4 * (lane >> 4);
         const uint32_t e = c.lane_at(row, col);
@@ -591,8 +598,8 @@ struct Cols {
     }
 };
 
-template <bool BF16>
-__device__ __forceinline__ void store_cols(const Chunk<BF16> &c, int col, int lane, int a, f32x4 v)
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void store_cols(const Chunk<BF16, VEC> &c, int col, int lane, int a, f32x4 v)
 {
     const int row = 4 * (lane >> 4);
     const uint32_t e = c.lane_at(row, col);
@@ -694,12 +701,12 @@ __global__ void __launch_bounds__(kThreads) chain_kernel(DeltaArgs a)
     f32x4 tv;
     auto fetch = [&](int c) {
         const float *r = rec + (int64_t)c * a.record;
-        tk.template load<VEC>({a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk}, threadIdx.x);
+        tk.load(Chunk<BF16, VEC>(a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk), threadIdx.x);
         tz.load(r + Record::kZ, threadIdx.x);
         tv = load_vecs(r + Record::kVec, threadIdx.x);
-        v.load({a.v.p, ev, a.v.s.l, c * kC, a.L, a.Dv}, col, lane);
+        v.load(Chunk<BF16, VEC>(a.v.p, ev, a.v.s.l, c * kC, a.L, a.Dv), col, lane);
         if constexpr (!KEEP) {
-            tq.template load<VEC>({a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk}, threadIdx.x);
+            tq.load(Chunk<BF16, VEC>(a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk), threadIdx.x);
             tp.load(r + Record::kP, threadIdx.x);
         }
     };
@@ -783,7 +790,7 @@ __global__ void __launch_bounds__(kThreads) chain_kernel(DeltaArgs a)
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t)
-                store_cols<BF16>({a.o.p, b * a.o.s.b + h * a.o.s.h, a.o.s.l, c * kC, a.L, a.Dv}, col, lane, t, o[t]);
+                store_cols(Chunk<BF16, VEC>(a.o.p, b * a.o.s.b + h * a.o.s.h, a.o.s.l, c * kC, a.L, a.Dv), col, lane, t, o[t]);
         }
         const float whole = s_vec[kWhole * kC];
 #pragma unroll
@@ -1014,6 +1021,10 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
         else if (a.s_final && c1 == a.NC)
             S.store(a.s_final + head * a.Dk * a.Dv, a.Dk, a.Dv, col, lane);
     } else {
+        // The help waves have more to do than the chain and share its SIMDs:
+        // going first they cut the LM layer's walk from 285 to 236 us (the
+        // chain going first: 279).
+        __builtin_amdgcn_s_setprio(2);
         const int tid = threadIdx.x - 256;
         const int64_t ek = b * a.k.s.b + hk * a.k.s.h, eq = b * a.q.s.b + hk * a.q.s.h;
         const int64_t ev = b * a.v.s.b + h * a.v.s.h + (unit ? 0 : slice * 64);
@@ -1025,9 +1036,9 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
         f32x4 vecs;
         auto fetch = [&](int c) {
             const float *r = rec + (int64_t)c * a.record;
-            tk.template load<VEC>({a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk}, tid);
+            tk.load(Chunk<true, VEC>(a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk), tid);
             tz.load(r + Record::kZ, tid);
-            tv.template load<VEC>({a.v.p, ev, a.v.s.l, c * kC, a.L, vcols}, tid);
+            tv.load(Chunk<true, VEC>(a.v.p, ev, a.v.s.l, c * kC, a.L, vcols), tid);
             vecs = load_vecs(r + Record::kVec, tid);
         };
         auto stage = [&](int half) {
@@ -1043,16 +1054,15 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
         Unit<true> qf[MODE == kOut ? NS : 1][4];
         f32x4 pf[MODE == kOut ? kBlocks : 1], qs[4];
         auto fetch_q = [&](int c) {
-            const Chunk<true> cq(a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk);
-            const uint32_t e = cq.lane_at(i16, 8 * g);
+            const Chunk<true, VEC> cq(a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk);
 #pragma unroll
             for (int s = 0; s < NS; ++s)
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
-                    qf[s][t] = cq.template unit<VEC>(e + 64 * s, i16, 16 * t, 32 * s + 8 * g);
+                    qf[s][t] = cq.unit(cq.lane_at(i16, 32 * s + 8 * g), i16, 16 * t, 32 * s + 8 * g);
         };
         auto output = [&](int c) {     // from qs, pf and the u of chunk c
-            const uint16_t *y = lds + LDS::kU + ((((c - c0) & 1) * 4 + mine) * 2) * LDS::kUPart + i16 * LDS::kURow + 4 * g;
+            uint16_t *y = lds + LDS::kU + ((((c - c0) & 1) * 4 + mine) * 2) * LDS::kUPart + i16 * LDS::kURow + 4 * g;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 Frag<2> f;
@@ -1066,10 +1076,29 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
                     qs[t] = mma<2>(p, f, qs[t]);
                 }
             }
-            const Chunk<true> co(a.o.p, b * a.o.s.b + h * a.o.s.h, a.o.s.l, max(c, c0) * kC, a.L, a.Dv, c < c0);
+            const Chunk<true, VEC> co(a.o.p, b * a.o.s.b + h * a.o.s.h, a.o.s.l, max(c, c0) * kC, a.L, a.Dv, c < c0);
+            if constexpr (VEC) {
+                // Rows of 32 bytes by way of LDS, in the place of the u just
+                // read: two stores of 16 bytes in place of 16 of two.
+                uint16_t *w = lds + LDS::kU + ((((c - c0) & 1) * 4 + mine) * 2) * LDS::kUPart;
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-                store_cols<true>(co, col, lane, t, qs[t]);
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        w[(16 * t + 4 * g + r) * 24 + i16] = f32_to_bf16_rne(qs[t][r]);
+                lds_order();
+                const int row = lane >> 1, at = (lane & 1) * 8;
+                const uint32_t e = co.lane_at(row, col - i16 + at);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const bf16x8 v = lds_row8(w + (row + 32 * n) * 24 + at);
+                    co.put8(e, 32 * n, v);
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    store_cols(co, col, lane, t, qs[t]);
+            }
         };
         stage(0);
         fetch(min(c0 + 1, c1 - 1));
@@ -1286,6 +1315,10 @@ __device__ __forceinline__ void back_walk(const DeltaArgs &a, unsigned block)
         else if (a.ds0 && seg == 0)
             S.store(a.ds0 + head * a.Dk * a.Dv, a.Dk, a.Dv, col, lane);
     } else {
+        // The help waves have more to do than the chain and share its SIMDs:
+        // going first they cut the LM layer's walk from 285 to 236 us (the
+        // chain going first: 279).
+        __builtin_amdgcn_s_setprio(2);
         const int tid = threadIdx.x - 256;
         const int64_t ek = b * a.k.s.b + hk * a.k.s.h, eq = b * a.q.s.b + hk * a.q.s.h;
         const int64_t eo = b * a.d_o.s.b + h * a.d_o.s.h;
@@ -1295,8 +1328,8 @@ __device__ __forceinline__ void back_walk(const DeltaArgs &a, unsigned block)
         f32x4 vecs;
         auto fetch = [&](int c) {
             const float *r = rec + (int64_t)c * a.record;
-            tk.template load<VEC>({a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk}, tid);
-            tq.template load<VEC>({a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk}, tid);
+            tk.load(Chunk<true, VEC>(a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk), tid);
+            tq.load(Chunk<true, VEC>(a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk), tid);
             tz.load(r + Record::kZt, tid);
             vecs = load_vecs(r + Record::kVec, tid);
         };
@@ -1316,7 +1349,7 @@ __device__ __forceinline__ void back_walk(const DeltaArgs &a, unsigned block)
 #pragma unroll
             for (int t = 0; t < kBlocks; ++t)
                 pf[t] = *reinterpret_cast<const f32x4 *>(P + t * kBlock + 4 * lane);
-            cols.load({a.d_o.p, eo, a.d_o.s.l, c * kC, a.L, a.Dv}, col, lane);
+            cols.load(Chunk<true, VEC>(a.d_o.p, eo, a.d_o.s.l, c * kC, a.L, a.Dv), col, lane);
         };
         auto product = [&]() {
 #pragma unroll
@@ -1337,12 +1370,12 @@ __device__ __forceinline__ void back_walk(const DeltaArgs &a, unsigned block)
         auto results = [&](int c, const f32x4 (&w)[4]) {
             const int at = min(c, c1 - 1);
             const Sheet out(a.w + (head * a.NC + at) * kC * a.DV, kC, a.DV, col, lane, c >= c1);
-            const Chunk<true> cv(a.dv.p, b * a.dv.s.b + h * a.dv.s.h, a.dv.s.l, at * kC, a.L, a.Dv, c >= c1);
+            const Chunk<true, VEC> cv(a.dv.p, b * a.dv.s.b + h * a.dv.s.h, a.dv.s.l, at * kC, a.L, a.Dv, c >= c1);
             const float *s_vec = reinterpret_cast<const float *>(lds + LDS::kVec) + ((c1 - 1 - c) & 3) * 4 * kC;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 out.put(t, w[t]);
-                store_cols<true>(cv, col, lane, t, row_vec(s_vec, kBeta, t, lane) * w[t]);
+                store_cols(cv, col, lane, t, row_vec(s_vec, kBeta, t, lane) * w[t]);
             }
         };
         U_::clear(lds + LDS::kZ, tid);
@@ -1523,12 +1556,12 @@ __global__ void __launch_bounds__(kThreads) reverse_kernel(DeltaArgs a)
     f32x4 tv;
     auto fetch = [&](int c) {
         const float *r = rec + (int64_t)c * a.record;
-        tk.template load<VEC>({a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk}, threadIdx.x);
-        tq.template load<VEC>({a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk}, threadIdx.x);
+        tk.load(Chunk<BF16, VEC>(a.k.p, ek, a.k.s.l, c * kC, a.L, a.Dk), threadIdx.x);
+        tq.load(Chunk<BF16, VEC>(a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk), threadIdx.x);
         tz.load(r + Record::kZt, threadIdx.x);
         tp.load(r + Record::kP, threadIdx.x);
         tv = load_vecs(r + Record::kVec, threadIdx.x);
-        v.load({a.d_o.p, eo, a.d_o.s.l, c * kC, a.L, a.Dv}, col, lane);
+        v.load(Chunk<BF16, VEC>(a.d_o.p, eo, a.d_o.s.l, c * kC, a.L, a.Dv), col, lane);
     };
     State<KD> S;
     S.load(a.ds_final ? a.ds_final + head * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, col, lane);
@@ -1594,7 +1627,7 @@ __global__ void __launch_bounds__(kThreads) reverse_kernel(DeltaArgs a)
             w[t] = dU[t] - w[t];
             Sheet(a.w + (head * a.NC + c) * kC * a.DV, kC, a.DV, col, lane).put(t, w[t]);
             w[t] *= row_vec(s_vec, kBeta, t, lane);     // dV
-            store_cols<BF16>({a.dv.p, ev, a.dv.s.l, c * kC, a.L, a.Dv}, col, lane, t, w[t]);
+            store_cols(Chunk<BF16, VEC>(a.dv.p, ev, a.dv.s.l, c * kC, a.L, a.Dv), col, lane, t, w[t]);
             w[t] *= -row_vec(s_vec, kRise, t, lane);
             dO[t] *= a.scale * row_vec(s_vec, kRise, t, lane);
         }
@@ -1672,8 +1705,8 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
 
     {
         T tk, tq;
-        tk.template load<VEC>({a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk}, threadIdx.x);
-        tq.template load<VEC>({a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk}, threadIdx.x);
+        tk.load(Chunk<BF16, VEC>(a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk), threadIdx.x);
+        tq.load(Chunk<BF16, VEC>(a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk), threadIdx.x);
         tk.store(s_k, threadIdx.x);
         tq.store(s_q, threadIdx.x);
     }
@@ -1690,8 +1723,8 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
         const float *rec = a.records + at * a.record;
         const float *ut = a.ut + at * kC * a.DV, *w = a.w + at * kC * a.DV;
         const float *S = a.states + at * KD * a.DV, *dS = a.grads + at * KD * a.DV;
-        const Chunk<BF16> cdo(a.d_o.p, b * a.d_o.s.b + h * a.d_o.s.h, a.d_o.s.l, t0, a.L, a.Dv);
-        const Chunk<BF16> cv(a.v.p, b * a.v.s.b + h * a.v.s.h, a.v.s.l, t0, a.L, a.Dv);
+        const Chunk<BF16, VEC> cdo(a.d_o.p, b * a.d_o.s.b + h * a.d_o.s.h, a.d_o.s.l, t0, a.L, a.Dv);
+        const Chunk<BF16, VEC> cv(a.v.p, b * a.v.s.b + h * a.v.s.h, a.v.s.l, t0, a.L, a.Dv);
 
         for (int x = threadIdx.x; x < kVecs * kC; x += kThreads)
             s_vec[x] = rec[Record::kVec + x];
@@ -1707,10 +1740,10 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
             float uw = 0.f, vw = 0.f;
             for (int d0 = 0; d0 < a.DV; d0 += 32) {
                 const int col = d0 + 8 * g;
-                const Frag<NK> fo = unit_frag<BF16>(cdo.template unit<VEC>(row, col));
+                const Frag<NK> fo = unit_frag<BF16>(cdo.unit(row, col));
                 const f32x8 wv = load8(w + row * a.DV + col);
                 const Frag<NO> fw = split<NO>(wv);
-                const f32x8 vv = unit_values<BF16>(cv.template unit<VEC>(row, col));
+                const f32x8 vv = unit_values<BF16>(cv.unit(row, col));
                 vw = dot8(vv, wv, vw);
 #pragma unroll
                 for (int tb = 0; tb < 4; ++tb) {
@@ -1796,7 +1829,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     const int row = 16 * t + i16;
-                    const Frag<NK> fo = unit_frag<BF16>(cdo.template unit<VEC>(row, col));
+                    const Frag<NK> fo = unit_frag<BF16>(cdo.unit(row, col));
                     e[t] = mma<3>(fo, fs, e[t]);
                     f[t] = mma<NO>(split<NO>(load8(w + row * a.DV + col)), fs, f[t]);
                     k2[t] = mma<3>(split<3>(load8(ut + row * a.DV + col)), fd, k2[t]);
@@ -1879,8 +1912,8 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const int dim = 16 * (wave * NTC + n) + i16;
-            store_cols<BF16>({a.dq.p, b * a.dq.s.b + hk * a.dq.s.h, a.dq.s.l, t0, a.L, a.Dk}, dim, lane, t, dq[t][n]);
-            store_cols<BF16>({a.dk.p, b * a.dk.s.b + hk * a.dk.s.h, a.dk.s.l, t0, a.L, a.Dk}, dim, lane, t, dk[t][n]);
+            store_cols(Chunk<BF16, VEC>(a.dq.p, b * a.dq.s.b + hk * a.dq.s.h, a.dq.s.l, t0, a.L, a.Dk), dim, lane, t, dq[t][n]);
+            store_cols(Chunk<BF16, VEC>(a.dk.p, b * a.dk.s.b + hk * a.dk.s.h, a.dk.s.l, t0, a.L, a.Dk), dim, lane, t, dk[t][n]);
         }
 }
 
@@ -1950,8 +1983,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
 
     {
         TK tk, tq;
-        tk.template load<VEC>({a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk}, tid);
-        tq.template load<VEC>({a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk}, tid);
+        tk.load(Chunk<true, VEC>(a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk), tid);
+        tq.load(Chunk<true, VEC>(a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk), tid);
         // the blocks right of the diagonal that share a k step with it
         if (tid < 128) {
             const int row = (tid >> 6) * 32 + ((tid >> 2) & 15), col = (tid >> 6) * 32 + 16 + (tid & 3) * 4;
@@ -1974,8 +2007,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
         f32x8 sv[KV / 32], dv[KV / 32];
         {
             const float *ut = a.ut + at * kC * a.DV, *w = a.w + at * kC * a.DV;
-            const Chunk<true> cdo(a.d_o.p, b * a.d_o.s.b + h * a.d_o.s.h, a.d_o.s.l, t0, a.L, a.Dv);
-            const Chunk<true> cv(a.v.p, b * a.v.s.b + h * a.v.s.h, a.v.s.l, t0, a.L, a.Dv);
+            const Chunk<true, VEC> cdo(a.d_o.p, b * a.d_o.s.b + h * a.d_o.s.h, a.d_o.s.l, t0, a.L, a.Dv);
+            const Chunk<true, VEC> cv(a.v.p, b * a.v.s.b + h * a.v.s.h, a.v.s.l, t0, a.L, a.Dv);
             f32x8 u[kUnits], ww[kUnits];
             Unit<true> o[kUnits], v[kUnits];
             float beta[kUnits];
@@ -1987,8 +2020,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
                     u[i] = load8(ut + row * a.DV + col);
                     ww[i] = load8(w + row * a.DV + col);
                 }
-                o[i] = cdo.template unit<VEC>(row, col);
-                v[i] = cv.template unit<VEC>(row, col);
+                o[i] = cdo.unit(row, col);
+                v[i] = cv.unit(row, col);
                 beta[i] = rec[Record::kVec + kBeta * kC + row];
             }
             if (tid < kVecs * kC)
@@ -2161,12 +2194,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
         }
         lds_barrier();
     }
-    const Chunk<true> cq(a.dq.p, b * a.dq.s.b + hk * a.dq.s.h, a.dq.s.l, t0, a.L, a.Dk);
-    const Chunk<true> ck(a.dk.p, b * a.dk.s.b + hk * a.dk.s.h, a.dk.s.l, t0, a.L, a.Dk);
+    const Chunk<true, VEC> cq(a.dq.p, b * a.dq.s.b + hk * a.dq.s.h, a.dq.s.l, t0, a.L, a.Dk);
+    const Chunk<true, VEC> ck(a.dk.p, b * a.dk.s.b + hk * a.dk.s.h, a.dk.s.l, t0, a.L, a.Dk);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        store_cols<true>(cq, dim, lane, first + t, dq[t]);
-        store_cols<true>(ck, dim, lane, first + t, dk[t]);
+        store_cols(cq, dim, lane, first + t, dq[t]);
+        store_cols(ck, dim, lane, first + t, dk[t]);
     }
 }
 
@@ -2390,11 +2423,12 @@ void place_workspace(DeltaArgs &a, const Layout &l, void *workspace)
     a.seg_chunks = l.cut.chunks;
 }
 
-// Every row begins on 16 bytes and ends with a whole unit of eight values.
+// Every row begins on 16 bytes, ends with a whole unit of eight values and
+// before the next one.
 bool units(const void *p, const pdssm_strides &s, int D, int esize)
 {
     const int e = 16 / esize;
-    return aligned16(p) && s.b % e == 0 && s.h % e == 0 && s.l % e == 0 && D % 8 == 0;
+    return aligned16(p) && s.b % e == 0 && s.h % e == 0 && s.l % e == 0 && D % 8 == 0 && s.l >= D;
 }
 
 // Strides along l that a chunk's 32-bit offsets can follow.
@@ -2573,7 +2607,8 @@ extern "C" int pdssm_delta_fwd(const void *q, const void *k, const void *v, cons
     place_workspace(a, lo, workspace);
     a.heads = B * Hv, a.Hk = (int)Hk, a.Hv = (int)Hv, a.L = (int)L, a.NC = (int)((L + kC - 1) / kC);
     a.Dk = Dk, a.Dv = Dv, a.DV = padded_value(Dv), a.slices = slices_of(Dv), a.scale = scale;
-    const bool vec = units(q, s[0], Dk, esize) && units(k, s[1], Dk, esize) && units(v, s[2], Dv, esize);
+    const bool vec = units(q, s[0], Dk, esize) && units(k, s[1], Dk, esize) && units(v, s[2], Dv, esize) &&
+                     units(o, s[5], Dv, esize);
     return launch_any<false>(a, esize == 2, vec, stream);
 }
 
@@ -2630,7 +2665,8 @@ extern "C" int pdssm_delta_bwd(const void *q, const void *k, const void *v, cons
     a.heads = B * Hv, a.Hk = (int)Hk, a.Hv = (int)Hv, a.L = (int)L, a.NC = (int)((L + kC - 1) / kC);
     a.Dk = Dk, a.Dv = Dv, a.DV = padded_value(Dv), a.slices = slices_of(Dv), a.scale = scale;
     const bool vec = units(q, s[0], Dk, esize) && units(k, s[1], Dk, esize) && units(v, s[2], Dv, esize) &&
-                     units(d_o, s[5], Dv, esize);
+                     units(d_o, s[5], Dv, esize) && units(dq, s[6], Dk, esize) && units(dk, s[7], Dk, esize) &&
+                     units(dv, s[8], Dv, esize);
     return launch_any<true>(a, esize == 2, vec, stream);
 }
 
