@@ -302,10 +302,21 @@ struct Tile {
     }
 };
 
+// e^x as 2^(x log2 e), with the part of x log2 e that one product rounds away
+// put back as a factor 1 + r ln 2.
+__device__ __forceinline__ float exp_of(float x)
+{
+    const float p = x * 1.44269504f;
+    const float r = __builtin_fmaf(x, 1.44269504f, -p) + x * 1.92596299e-8f;
+    const float e = __builtin_amdgcn_exp2f(p);
+    // an infinite or vanished result stays as it is
+    return __builtin_fabsf(p) < 126.f ? e * __builtin_fmaf(r, 0.693147181f, 1.f) : e;
+}
+
 // e^(G_i - G_j), G as a pair of floats, zero across a step that empties the state.
 __device__ __forceinline__ float decay_of(float hi_i, float lo_i, float n_i, float hi_j, float lo_j, float n_j)
 {
-    return n_i == n_j ? expf((hi_i - hi_j) + (lo_i - lo_j)) : 0.f;
+    return n_i == n_j ? exp_of((hi_i - hi_j) + (lo_i - lo_j)) : 0.f;
 }
 
 __device__ __forceinline__ int64_t kv_head(const DeltaArgs &a, int64_t head, int64_t &b, int &h)
@@ -322,19 +333,21 @@ __device__ __forceinline__ int64_t kv_head(const DeltaArgs &a, int64_t head, int
 // blocks: the diagonal blocks row by row with a column in each lane, the
 // others by fp32 matrix instructions, a block column in each wave.
 // ---------------------------------------------------------------------------
-constexpr int kMat = 68;        // row of a 64 x 64 fp32 matrix in LDS
+constexpr int kMat = 20;        // row of a 16 x 16 fp32 block in LDS
+__device__ __forceinline__ constexpr int lds_block(int a, int b) { return block_of(a, b) * 16 * kMat; }
 
 template <int KD, bool BF16, bool VEC, bool BWD>
 __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
 {
     using T = Tile<KD, BF16>;
-    constexpr int kQArea = T::kSize * 2 > kC * kMat * 4 ? T::kSize * 2 : kC * kMat * 4;
-    __shared__ __attribute__((aligned(16))) char s_mem[T::kSize * 2 + kQArea + kC * kMat * 4];
+    constexpr int kMatrix = kBlocks * 16 * kMat;
+    static_assert(kMatrix * 4 <= T::kSize * 4, "Z takes the place of k and q");
+    __shared__ __attribute__((aligned(16))) char s_mem[T::kSize * 4 + kMatrix * 4];
     __shared__ float s_hi[kC], s_lo[kC], s_n[kC], s_beta[kC];
     uint16_t *s_k = reinterpret_cast<uint16_t *>(s_mem);
     uint16_t *s_q = reinterpret_cast<uint16_t *>(s_mem + T::kSize * 2);
-    float *s_z = reinterpret_cast<float *>(s_mem + T::kSize * 2);     // after P, in the place of q
-    float *s_N = reinterpret_cast<float *>(s_mem + T::kSize * 2 + kQArea);
+    float *s_z = reinterpret_cast<float *>(s_mem);      // after N and P, in the place of k and q
+    float *s_N = reinterpret_cast<float *>(s_mem + T::kSize * 4);
 
     const int64_t head = blockIdx.x / (unsigned)a.NC;
     const int c = blockIdx.x % (unsigned)a.NC;
@@ -403,10 +416,8 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
         const float hi = s_hi[row], lo = s_lo[row], n = s_n[row];
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
-            if (tb > wave) {
-                *reinterpret_cast<f32x4 *>(s_N + row * kMat + 16 * tb + 4 * g) = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (tb > wave)
                 continue;
-            }
             f32x4 kk = {0.f, 0.f, 0.f, 0.f}, qk = kk;
 #pragma unroll
             for (int s = 0; s < KD / 32; ++s) {
@@ -428,34 +439,48 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
                     pp[r] = col <= row ? a.scale * qk[r] * d : 0.f;
                 }
             }
-            *reinterpret_cast<f32x4 *>(s_N + row * kMat + 16 * tb + 4 * g) = nn;
+            *reinterpret_cast<f32x4 *>(s_N + lds_block(wave, tb) + i16 * kMat + 4 * g) = nn;
             *reinterpret_cast<f32x4 *>(rec + Record::kP + block_of(wave, tb) * kBlock + 4 * lane) = pp;
         }
     }
     __syncthreads();    // N whole; q's place is free for Z
 
-    // Diagonal block `wave`: lane's column of Z row by row.
+    // Diagonal block `wave`, a column in each lane, four rows at a time: what
+    // the rows above take from all four, then the four among themselves.
     {
-        const float *N = s_N + 16 * wave * kMat + 16 * wave;
+        const float *N = s_N + lds_block(wave, wave);
         float y[16], z[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float v = N[i * kMat + i16];
+        for (int p = 0; p < 4; ++p) {
+            float v[4];
+            f32x4 tri[4];
 #pragma unroll
-            for (int m = 0; m < i; m += 4) {
-                const f32x4 row = *reinterpret_cast<const f32x4 *>(N + i * kMat + m);
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (m + r < i)
-                        v -= row[r] * y[m + r];
+            for (int i = 0; i < 4; ++i) {
+                v[i] = N[(4 * p + i) * kMat + i16];
+                tri[i] = *reinterpret_cast<const f32x4 *>(N + (4 * p + i) * kMat + 4 * p);
             }
-            z[i] = v;
-            y[i] = v * s_beta[16 * wave + i];
+#pragma unroll
+            for (int m = 0; m < p; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f32x4 row = *reinterpret_cast<const f32x4 *>(N + (4 * p + i) * kMat + 4 * m);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        v[i] -= row[r] * y[4 * m + r];
+                }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int r = 0; r < i; ++r)
+                    v[i] -= tri[i][r] * y[4 * p + r];
+                z[4 * p + i] = v[i];
+                y[4 * p + i] = v[i] * s_beta[16 * wave + 4 * p + i];
+            }
         }
         if (g == 0) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                s_z[(16 * wave + i) * kMat + 16 * wave + i16] = z[i];
+                s_z[lds_block(wave, wave) + i * kMat + i16] = z[i];
         }
     }
     __syncthreads();
@@ -470,7 +495,7 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
             beta[m] = *reinterpret_cast<const f32x4 *>(s_beta + 16 * m + 4 * g);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                y[m][r] = m == wave ? s_z[(16 * m + 4 * g + r) * kMat + 16 * m + i16] * beta[m][r] : 0.f;
+                y[m][r] = m == wave ? s_z[lds_block(m, m) + (4 * g + r) * kMat + i16] * beta[m][r] : 0.f;
         }
 #pragma unroll
         for (int ta = 1; ta < 4; ++ta) {
@@ -479,31 +504,31 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
             f32x4 x;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                x[r] = s_N[(16 * ta + 4 * g + r) * kMat + 16 * wave + i16];
+                x[r] = s_N[lds_block(ta, wave) + (4 * g + r) * kMat + i16];
 #pragma unroll
             for (int m = 0; m < ta; ++m)
                 if (m >= wave)
-                    x = mma_f32(-*reinterpret_cast<const f32x4 *>(s_N + (16 * ta + i16) * kMat + 16 * m + 4 * g), y[m], x);
-            const f32x4 zd = *reinterpret_cast<const f32x4 *>(s_z + (16 * ta + i16) * kMat + 16 * ta + 4 * g);
+                    x = mma_f32(-*reinterpret_cast<const f32x4 *>(s_N + lds_block(ta, m) + i16 * kMat + 4 * g), y[m], x);
+            const f32x4 zd = *reinterpret_cast<const f32x4 *>(s_z + lds_block(ta, ta) + i16 * kMat + 4 * g);
             x = mma_f32(-zd, x * beta[ta], x);
             y[ta] = x * beta[ta];
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                s_z[(16 * ta + 4 * g + r) * kMat + 16 * wave + i16] = x[r];
+                s_z[lds_block(ta, wave) + (4 * g + r) * kMat + i16] = x[r];
         }
     }
     __syncthreads();
 
     // Z out: row format, and column format for the backward.
     for (int t = wave; t < kBlocks; t += kThreads / 64) {
-        const int ta = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, tb = t - ta * (ta + 1) / 2;
+        const float *z = s_z + t * 16 * kMat;
         *reinterpret_cast<f32x4 *>(rec + Record::kZ + t * kBlock + 4 * lane) =
-            *reinterpret_cast<const f32x4 *>(s_z + (16 * ta + i16) * kMat + 16 * tb + 4 * g);
+            *reinterpret_cast<const f32x4 *>(z + i16 * kMat + 4 * g);
         if constexpr (BWD) {
             f32x4 v;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                v[r] = s_z[(16 * ta + 4 * g + r) * kMat + 16 * tb + i16];
+                v[r] = z[(4 * g + r) * kMat + i16];
             *reinterpret_cast<f32x4 *>(rec + Record::kZt + t * kBlock + 4 * lane) = v;
         }
     }
