@@ -569,7 +569,7 @@ def _want(name: str, form, shape, dtype, contiguous: bool = False) -> None:
         return
     if tuple(form[0]) != tuple(shape) or form[2] != dtype:
         raise ValueError(f"{name} must be {dtype} {list(shape)}, not {form[2]} {list(form[0])}")
-    if contiguous:
+    if contiguous and 0 not in form[0]:
         step = 1
         for n, st in zip(reversed(form[0]), reversed(form[1])):
             if n > 1 and st != step:
