@@ -302,6 +302,30 @@ struct Tile {
     }
 };
 
+__device__ __forceinline__ f32x8 load8(const float *p)
+{
+    const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+__device__ __forceinline__ float dot8(f32x8 a, f32x8 b, float v)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v += a[j] * b[j];
+    return v;
+}
+
+// N parts of eight values, part n at p + n * part.
+template <int N>
+__device__ __forceinline__ void put_parts(uint16_t *p, int part, f32x8 v)
+{
+    const Frag<N> f = split<N>(v);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        *reinterpret_cast<bf16x8 *>(p + n * part) = f.p[n];
+}
+
 // e^x as 2^(x log2 e), with the part of x log2 e that one product rounds away
 // put back as a factor 1 + r ln 2.
 __device__ __forceinline__ float exp_of(float x)
@@ -633,6 +657,34 @@ __device__ __forceinline__ void store_cols(const Chunk<BF16, VEC> &c, int col, i
         c.put(e, row, 16 * a + r, col, v[r]);
 }
 
+// Values of a wave's 16 columns (lane: column col, rows 4 g + r of a tile) of
+// a [rows][DV] fp32 array; rows and columns outside it read as zero and are
+// not written.
+struct Sheet {
+    __amdgpu_buffer_rsrc_t r;
+    uint32_t lane, pitch;
+    __device__ __forceinline__ Sheet(const float *p, int rows, int DV, int col, int lane_, bool none = false)
+    {
+        pitch = DV * 4;
+        r = make_rsrc(p, (uint64_t)rows * pitch);
+        lane = col < DV && !none ? (uint32_t)opaque((lane_ >> 4) * 4 * (int)pitch + col * 4) : kOutside;
+    }
+    __device__ __forceinline__ f32x4 get(int tile) const
+    {
+        f32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = bload<float>(r, lane + (16 * tile + i) * pitch, 0);
+        return v;
+    }
+    __device__ __forceinline__ void put(int tile, f32x4 v) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), r, lane + (16 * tile + i) * pitch, 0, 0);
+    }
+};
+
 // A state (or its gradient): KD / 16 tiles in the C layout.
 template <int KD>
 struct State {
@@ -641,43 +693,17 @@ struct State {
     // [Dk][Dv] values from memory; NULL: zero.
     __device__ __forceinline__ void load(const float *p, int Dk, int Dv, int col, int lane)
     {
+        const Sheet from(p, p ? Dk : 0, Dv, col, lane);
 #pragma unroll
         for (int m = 0; m < KD / 16; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * m + 4 * (lane >> 4) + r;
-                s[m][r] = (p && row < Dk && col < Dv) ? p[(int64_t)row * Dv + col] : 0.f;
-            }
+            s[m] = from.get(m);
     }
     __device__ __forceinline__ void store(float *p, int Dk, int Dv, int col, int lane) const
     {
+        const Sheet to(p, Dk, Dv, col, lane);
 #pragma unroll
         for (int m = 0; m < KD / 16; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * m + 4 * (lane >> 4) + r;
-                if (row < Dk && col < Dv)
-                    p[(int64_t)row * Dv + col] = s[m][r];
-            }
-    }
-};
-
-// Values of a wave's 16 columns (lane: column col, rows 4 g + r of a tile) of
-// a [rows][DV] fp32 array of the workspace; columns from DV on are dropped.
-struct Sheet {
-    __amdgpu_buffer_rsrc_t r;
-    uint32_t lane, pitch;
-    __device__ __forceinline__ Sheet(float *p, int rows, int DV, int col, int lane_, bool none = false)
-    {
-        pitch = DV * 4;
-        r = make_rsrc(p, (uint64_t)rows * pitch);
-        lane = col < DV && !none ? (uint32_t)opaque((lane_ >> 4) * 4 * (int)pitch + col * 4) : kOutside;
-    }
-    __device__ __forceinline__ void put(int tile, f32x4 v) const
-    {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), r, lane + (16 * tile + i) * pitch, 0, 0);
+            to.put(m, s[m]);
     }
 };
 
@@ -1495,54 +1521,97 @@ __global__ void __launch_bounds__(kPipeThreads, 1) back_kernel(DeltaArgs a)
 // join_kernel: the states before segments 1 .. segs - 1 of a head, from the
 // segments' transitions A and ends B: S <- A S + B; behind those workgroups
 // (in the backward) the state gradients after segments segs - 2 .. 0:
-// dS <- A^T dS + C.  A wave owns 16 columns.
+// dS <- A^T dS + C.  A wave owns 16 columns; the segment's A goes through LDS
+// in three parts, the next one loading meanwhile (each wave reading and
+// splitting it by itself took five times as long: 219 against 45 us for 16
+// segments of 128 x 128).
 // ---------------------------------------------------------------------------
 template <int KD>
-__global__ void __launch_bounds__(kThreads) join_kernel(DeltaArgs a)
+struct JoinLds {
+    static constexpr int kRow = KD + 8, kPart = KD * kRow;
+    static constexpr size_t kBytes = 3 * kPart * 2;
+};
+
+template <int KD>
+__global__ void __launch_bounds__(kThreads, 1) join_kernel(DeltaArgs a)
 {
+    constexpr int kRow = JoinLds<KD>::kRow, kPart = JoinLds<KD>::kPart, kUnits = KD * KD / 8 / kThreads;
+    extern __shared__ __attribute__((aligned(16))) char s_dyn[];
+    uint16_t *s_a = reinterpret_cast<uint16_t *>(s_dyn);
     const bool back = blockIdx.x >= a.heads * a.slices;
     const unsigned block = blockIdx.x - (back ? (unsigned)(a.heads * a.slices) : 0u);
     const int64_t head = block / (unsigned)a.slices;
     const int slice = block % (unsigned)a.slices;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, i16 = lane & 15;
-    const int col = (slice * 4 + wave) * 16 + i16, pitch = a.slices * 64 + KD;
+    const int col = (slice * 4 + wave) * 16 + i16, ends = a.slices * 64, pitch = ends + KD;
     const float *T = a.trans + head * a.segs * KD * (int64_t)pitch;
-    const float *C = a.rtrans + head * a.segs * KD * (int64_t)(a.slices * 64);
+    const float *C = a.rtrans + head * a.segs * KD * (int64_t)ends;
+
+    f32x8 u[kUnits];
     State<KD> S, N;
+    // The segment's A in units of eight values, and its end B or C.
+    auto fetch = [&](int seg) {
+        const float *A = T + (int64_t)seg * KD * pitch + ends;
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int x = threadIdx.x + i * kThreads;
+            u[i] = load8(A + x / (KD / 8) * pitch + x % (KD / 8) * 8);
+        }
+        if (back)
+            N.load(C + (int64_t)seg * KD * ends, KD, ends, col, lane);
+        else
+            N.load(A - ends, KD, pitch, col, lane);
+    };
+    auto seg_of = [&](int n) { return back ? a.segs - 1 - n : n; };
     if (back)
-        S.load(C + (int64_t)(a.segs - 1) * KD * (a.slices * 64), KD, a.slices * 64, col, lane);
+        S.load(C + (int64_t)(a.segs - 1) * KD * ends, KD, ends, col, lane);
     else
         S.load(T, KD, pitch, col, lane);
+    if (a.segs > 2)
+        fetch(seg_of(1));
     for (int n = 1;; ++n) {
-        const int seg = back ? a.segs - 1 - n : n;
-        S.store((back ? a.seg_grads : a.seg_states) + (head * a.segs + seg) * KD * a.DV, KD, a.DV, col, lane);
+        S.store((back ? a.seg_grads : a.seg_states) + (head * a.segs + seg_of(n)) * KD * a.DV, KD, a.DV, col, lane);
         if (n + 1 >= a.segs)
             break;
-        const float *A = T + (int64_t)seg * KD * pitch + a.slices * 64;
-        if (back)
-            N.load(C + (int64_t)seg * KD * (a.slices * 64), KD, a.slices * 64, col, lane);
-        else
-            N.load(A - a.slices * 64, KD, pitch, col, lane);
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int x = threadIdx.x + i * kThreads;
+            put_parts<3>(s_a + x / (KD / 8) * kRow + x % (KD / 8) * 8, kPart, u[i]);
+        }
+        State<KD> E = N;
+        lds_barrier();
+        if (n + 2 < a.segs)
+            fetch(seg_of(n + 1));
 #pragma unroll
         for (int s = 0; s < KD / 32; ++s) {
             const Frag<3> f = split<3>(S.s[2 * s], S.s[2 * s + 1]);
 #pragma unroll
-            for (int m = 0; m < KD / 16; ++m) {
-                f32x4 lo, hi;
-                if (back) {
-                    const float *p = A + (32 * s + 4 * g) * pitch + 16 * m + i16;
+            for (int m0 = 0; m0 < KD / 16; m0 += 4) {
+                Frag<3> p[4];       // four tiles in turn, so that no product waits for the last
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        lo[r] = p[r * pitch], hi[r] = p[(16 + r) * pitch];
-                } else {
-                    const float *p = A + (16 * m + i16) * pitch + 32 * s + 4 * g;
-                    lo = *reinterpret_cast<const f32x4 *>(p);
-                    hi = *reinterpret_cast<const f32x4 *>(p + 16);
-                }
-                N.s[m] = mma<3>(split<3>(lo, hi), f, N.s[m]);
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) {
+                        const uint16_t *q = s_a + i * kPart;
+                        if (back) {
+                            q += (32 * s + 4 * g + (i16 >> 2)) * kRow + 16 * (m0 + m) + 4 * (i16 & 3);
+                            p[m].p[i] = lds_columns4(q, q + 16 * kRow);
+                        } else {
+                            q += (16 * (m0 + m) + i16) * kRow + 32 * s + 4 * g;
+                            p[m].p[i] = lds_rows4(q, q + 16);
+                        }
+                    }
+#pragma unroll
+                for (int o = 2; o >= 0; --o)
+#pragma unroll
+                    for (int i = 0; i <= o; ++i)
+#pragma unroll
+                        for (int m = 0; m < 4; ++m)
+                            E.s[m0 + m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p[m].p[i], f.p[o - i], E.s[m0 + m], 0, 0, 0);
             }
         }
-        S = N;
+        S = E;
+        lds_barrier();
     }
 }
 
@@ -1686,20 +1755,6 @@ __device__ __forceinline__ float sum16(float v)     // over the lanes of a group
 #pragma unroll
     for (int m = 8; m >= 1; m >>= 1)
         v += __shfl_xor(v, m, 64);
-    return v;
-}
-
-__device__ __forceinline__ f32x8 load8(const float *p)
-{
-    const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
-__device__ __forceinline__ float dot8(f32x8 a, f32x8 b, float v)
-{
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        v += a[j] * b[j];
     return v;
 }
 
@@ -1972,16 +2027,6 @@ struct GradLds {
     static constexpr int kSum = kVdv + 2 * kC;                  // [waves]
     static constexpr size_t kBytes = (kSum + 2 * kWaves) * 2;
 };
-
-// N parts of eight values, part n at p + n * part.
-template <int N>
-__device__ __forceinline__ void put_parts(uint16_t *p, int part, f32x8 v)
-{
-    const Frag<N> f = split<N>(v);
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-        *reinterpret_cast<bf16x8 *>(p + n * part) = f.p[n];
-}
 
 template <int KD, int KV, bool VEC>
 __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
@@ -2507,7 +2552,7 @@ int launch_fwd(const DeltaArgs &a, hipStream_t stream)
             rc = launch(pipe_kernel<KD, VEC, kScan>, a.heads * a.segs * (a.slices + KD / 64), PipeLds<KD>::bytes(false), a,
                         stream, kPipeThreads);
             if (rc == PDSSM_OK)
-                rc = launch(join_kernel<KD>, walks, 0, a, stream);
+                rc = launch(join_kernel<KD>, walks, JoinLds<KD>::kBytes, a, stream);
         }
         if (rc == PDSSM_OK)
             rc = launch(pipe_kernel<KD, VEC, kOut>, walks * a.segs, PipeLds<KD>::bytes(true), a, stream, kPipeThreads);
@@ -2530,7 +2575,7 @@ int launch_bwd(DeltaArgs a, hipStream_t stream)
         if (a.segs > 1) {
             rc = launch(back_kernel<KD, VEC, true>, (walks * 2 + a.heads * (KD / 64)) * a.segs, lds, a, stream, kPipeThreads);
             if (rc == PDSSM_OK)
-                rc = launch(join_kernel<KD>, walks * 2, 0, a, stream);
+                rc = launch(join_kernel<KD>, walks * 2, JoinLds<KD>::kBytes, a, stream);
         }
         if (rc == PDSSM_OK)
             rc = launch(back_kernel<KD, VEC, false>, walks * 2 * a.segs, lds, a, stream, kPipeThreads);
