@@ -564,11 +564,11 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
 // ((f * 3 + n) * 64 + lane) * 8 values.  Six fragments hold the triangle; the
 // halves of them that it leaves out are zero.
 // ---------------------------------------------------------------------------
-template <bool TRANS>
+template <bool TRANS, int NT = kThreads>
 struct Tri {
     static constexpr int kFrags = 6;
     static constexpr int kSize = kFrags * 3 * 64 * 8;    // uint16_t
-    static constexpr int kUnits = (kBlocks * 64 + kThreads - 1) / kThreads;
+    static constexpr int kUnits = (kBlocks * 64 + NT - 1) / NT;
     f32x4 u[kUnits];
 
     // Row tile a of the matrix has k step s (of the transpose: from a / 2 on).
@@ -580,13 +580,13 @@ struct Tri {
     {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i)    // (without a branch: see pipe_walk)
-            u[i] = *reinterpret_cast<const f32x4 *>(blocks + 4 * min(tid + i * kThreads, kBlocks * 64 - 1));
+            u[i] = *reinterpret_cast<const f32x4 *>(blocks + 4 * min(tid + i * NT, kBlocks * 64 - 1));
     }
     __device__ __forceinline__ void store(uint16_t *lds, int tid) const
     {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
-            const int x = tid + i * kThreads;
+            const int x = tid + i * NT;
             if (x < kBlocks * 64) {
                 const int t = x >> 6, lane = x & 63;
                 const int ta = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, tb = t - ta * (ta + 1) / 2;
@@ -603,7 +603,7 @@ struct Tri {
     // The halves that no block fills.
     static __device__ __forceinline__ void clear(uint16_t *lds, int tid)
     {
-        for (int x = tid; x < 2 * 3 * 64; x += kThreads) {
+        for (int x = tid; x < 2 * 3 * 64; x += NT) {
             const int f = TRANS ? (x < 192 ? frag(1, 0) : frag(3, 1)) : (x < 192 ? frag(0, 0) : frag(2, 1));
             const int half = TRANS ? 0 : 1;
             *reinterpret_cast<uint2 *>(lds + (f * 192 + x % 192) * 8 + 4 * half) = make_uint2(0, 0);
@@ -872,18 +872,19 @@ __global__ void __launch_bounds__(kThreads) chain_kernel(DeltaArgs a)
 // ---------------------------------------------------------------------------
 enum Mode { kOut, kKeep, kScan };   // outputs; states and u~ kept; the last state alone
 
-constexpr int kPipeThreads = 512;
+constexpr int kHelpThreads = 512, kPipeThreads = 256 + kHelpThreads;
 
 template <int KD>
 struct PipeLds {
-    using K = Tile<KD, true>;
-    using V = Tile<kC, true>;
+    using K = Tile<KD, true, kHelpThreads>;
+    using V = Tile<kC, true, kHelpThreads>;
+    using Z = Tri<false, kHelpThreads>;
     static constexpr int kSRow = KD + 8, kURow = kC + 4;
     static constexpr int kSPart = 16 * kSRow, kUPart = 16 * kURow;
     // in uint16_t
     static constexpr int kK = 0;
     static constexpr int kZ = kK + 2 * K::kSize;
-    static constexpr int kV = kZ + 2 * Tri<false>::kSize;
+    static constexpr int kV = kZ + 2 * Z::kSize;
     static constexpr int kVec = kV + 2 * V::kSize;
     static constexpr int kFlag = kVec + 2 * 4 * kC * 2;
     static constexpr int kS = kFlag + 8;                    // with outputs only
@@ -897,7 +898,7 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
     using LDS = PipeLds<KD>;
     using TK = typename LDS::K;
     using TV = typename LDS::V;
-    using L_ = Tri<false>;
+    using L_ = typename LDS::Z;
     constexpr int NS = KD / 32;     // k steps over the key dimensions
     extern __shared__ __attribute__((aligned(16))) char s_dyn[];
     uint16_t *lds = reinterpret_cast<uint16_t *>(s_dyn);
@@ -947,9 +948,9 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
             const uint16_t *s_k = lds + LDS::kK + half * TK::kSize, *s_z = lds + LDS::kZ + half * L_::kSize;
             const uint16_t *s_v = lds + LDS::kV + half * TV::kSize;
             const float *s_vec = reinterpret_cast<const float *>(lds + LDS::kVec) + half * 4 * kC;
-            Frag<1> kr[NS][4];
+            Frag<1> kr[2][4];       // two k steps at a time
 #pragma unroll
-            for (int s = 0; s < NS; ++s)
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
                     kr[s][t] = TK::rows_stacked(s_k, t, s, lane);
@@ -985,7 +986,7 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
             Frag<3> z0[4], z1[2];
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
-                if (s == NS / 2) {
+                if (s == NS - 1) {
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                     for (int t = 0; t < 4; ++t)
@@ -996,7 +997,12 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
                 for (int n = 2; n >= 0; --n)
 #pragma unroll
                     for (int t = 0; t < 4; ++t)
-                        R[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kr[s][t].p[0], sf[s].p[n], R[t], 0, 0, 0);
+                        R[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kr[s & 1][t].p[0], sf[s].p[n], R[t], 0, 0, 0);
+                if (s + 2 < NS) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        kr[s & 1][t] = TK::rows_stacked(s_k, t, s + 2, lane);
+                }
             }
             f32x4 x[4], u[4];
 #pragma unroll
@@ -1009,10 +1015,6 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
 #pragma unroll
             for (int t = 0; t < 2; ++t)
                 z1[t] = L_::template get<3>(s_z, t + 2, 1, lane);
-            Frag<1> kc0[KD / 16], kc1[KD / 16];
-#pragma unroll
-            for (int m = 0; m < KD / 16; ++m)
-                kc0[m] = TK::columns_stacked(s_k, m, 0, lane);
             __builtin_amdgcn_sched_barrier(0);
             const Frag<3> f0 = split<3>(x[0], x[1]), f1 = split<3>(x[2], x[3]);
 #pragma unroll
@@ -1026,9 +1028,16 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
                     for (int t = 0; t < 2; ++t)
                         u[t + 2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(z1[t].p[i], f1.p[o - i], u[t + 2], 0, 0, 0);
                 }
+            // two tiles of the state at a time, the next two's k on its way
+            Frag<1> kc[2][2][2];
+            auto load_kc = [&](int s) {
 #pragma unroll
-            for (int m = 0; m < KD / 16; ++m)
-                kc1[m] = TK::columns_stacked(s_k, m, 1, lane);
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        kc[s & 1][m][i] = TK::columns_stacked(s_k, 2 * s + m, i, lane);
+            };
+            load_kc(0);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 u[t] = R[t] - u[t];      // u~
@@ -1056,13 +1065,16 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
                 S.s[m] *= whole;
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
+                if (s + 1 < NS)
+                    load_kc(s + 1);
 #pragma unroll
                 for (int n = 2; n >= 0; --n)
 #pragma unroll
-                    for (int m = 2 * s; m < 2 * s + 2; ++m) {
-                        S.s[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc0[m].p[0], w0.p[n], S.s[m], 0, 0, 0);
-                        S.s[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc1[m].p[0], w1.p[n], S.s[m], 0, 0, 0);
-                    }
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+                            S.s[2 * s + m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                kc[s & 1][m][i].p[0], i ? w1.p[n] : w0.p[n], S.s[2 * s + m], 0, 0, 0);
                 sf[s] = split<3>(S.s[2 * s], S.s[2 * s + 1]);
             }
             lds_barrier();
@@ -1102,65 +1114,53 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
         L_::clear(lds + LDS::kZ, tid);
         L_::clear(lds + LDS::kZ + L_::kSize, tid);
         fetch(c0);
-        Unit<true> qf[MODE == kOut ? NS : 1][4];
-        f32x4 pf[MODE == kOut ? kBlocks : 1], qs[4];
+        // A chain wave's outputs are shared by two help waves: row tiles 0 and
+        // 3, and 1 and 2 (three fragments of P each).
+        const int part = (wave - 4) >> 2, ta = part, tb = part ? 2 : 3;
+        Unit<true> qf[MODE == kOut ? NS : 1][2];
+        f32x4 pf[6], qs[2];
         auto fetch_q = [&](int c) {
             const Chunk<true, VEC> cq(a.q.p, eq, a.q.s.l, c * kC, a.L, a.Dk);
 #pragma unroll
-            for (int s = 0; s < NS; ++s)
+            for (int s = 0; s < NS; ++s) {
+                const uint32_t e = cq.lane_at(i16, 32 * s + 8 * g);
+                qf[s][0] = cq.unit(e, i16, 16 * ta, 32 * s + 8 * g);
+                qf[s][1] = cq.unit(e, i16, 16 * tb, 32 * s + 8 * g);
+            }
+        };
+        // P's blocks (ta, 0), (ta, 1), (tb, 0..3), those right of the diagonal zero
+        auto fetch_p = [&](int c) {
+            const float *P = rec + (int64_t)c * a.record + Record::kP + 4 * lane;
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    qf[s][t] = cq.unit(cq.lane_at(i16, 32 * s + 8 * g), i16, 16 * t, 32 * s + 8 * g);
+            for (int n = 0; n < 6; ++n) {
+                const int row = n < 2 ? ta : tb, cb = n < 2 ? n : n - 2;
+                pf[n] = *reinterpret_cast<const f32x4 *>(P + block_of(row, min(cb, row)) * kBlock);
+            }
         };
         auto output = [&](int c) {     // from qs, pf and the u of chunk c
-            uint16_t *y = lds + LDS::kU + ((((c - c0) & 1) * 4 + mine) * 2) * LDS::kUPart + i16 * LDS::kURow + 4 * g;
+            const uint16_t *y = lds + LDS::kU + ((((c - c0) & 1) * 4 + mine) * 2) * LDS::kUPart + i16 * LDS::kURow + 4 * g;
+            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+            Frag<2> f[2];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                Frag<2> f;
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
-                    f.p[n] = lds_rows4(y + n * LDS::kUPart + 32 * s, y + n * LDS::kUPart + 32 * s + 16);
-#pragma unroll
-                for (int t = 2 * s; t < 4; ++t) {
-                    const Frag<2> p = split<2>(pf[block_of(t, 2 * s)],
-                                               t > 2 * s ? pf[block_of(t, 2 * s + 1)] : f32x4{0.f, 0.f, 0.f, 0.f});
-                    qs[t] = mma<2>(p, f, qs[t]);
-                }
-            }
+                    f[s].p[n] = lds_rows4(y + n * LDS::kUPart + 32 * s, y + n * LDS::kUPart + 32 * s + 16);
+            qs[0] = mma<2>(split<2>(pf[0], part ? pf[1] : zero), f[0], qs[0]);
+            qs[1] = mma<2>(split<2>(pf[2], pf[3]), f[0], qs[1]);
+            qs[1] = mma<2>(split<2>(pf[4], part ? zero : pf[5]), f[1], qs[1]);
             const Chunk<true, VEC> co(a.o.p, b * a.o.s.b + h * a.o.s.h, a.o.s.l, max(c, c0) * kC, a.L, a.Dv, c < c0);
-            if constexpr (VEC) {
-                // Rows of 32 bytes by way of LDS, in the place of the u just
-                // read: two stores of 16 bytes in place of 16 of two.
-                uint16_t *w = lds + LDS::kU + ((((c - c0) & 1) * 4 + mine) * 2) * LDS::kUPart;
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        w[(16 * t + 4 * g + r) * 24 + i16] = f32_to_bf16_rne(qs[t][r]);
-                lds_order();
-                const int row = lane >> 1, at = (lane & 1) * 8;
-                const uint32_t e = co.lane_at(row, col - i16 + at);
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const bf16x8 v = lds_row8(w + (row + 32 * n) * 24 + at);
-                    co.put8(e, 32 * n, v);
-                }
-            } else {
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    store_cols(co, col, lane, t, qs[t]);
-            }
+            store_cols(co, col, lane, ta, qs[0]);
+            store_cols(co, col, lane, tb, qs[1]);
         };
         stage(0);
         fetch(min(c0 + 1, c1 - 1));
         if constexpr (MODE == kOut) {
             fetch_q(c0);
 #pragma unroll
-            for (int t = 0; t < kBlocks; ++t)
-                pf[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-                qs[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int n = 0; n < 6; ++n)
+                pf[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+            qs[0] = qs[1] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
         lds_barrier();
         for (int c = c0; c < c1; ++c) {
@@ -1172,29 +1172,23 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
             fetch(min(c + 2, c1 - 1));
             if constexpr (MODE == kOut) {
                 output(c - 1);
-                const float *P = rec + (int64_t)c * a.record + Record::kP;
-#pragma unroll
-                for (int t = 0; t < kBlocks; ++t)
-                    pf[t] = *reinterpret_cast<const f32x4 *>(P + t * kBlock + 4 * lane);
+                fetch_p(c);
                 LdsFlag::await(&s_flag[mine], c + 1);
                 const uint16_t *x = lds + LDS::kS + mine * 2 * LDS::kSPart + i16 * LDS::kSRow + 8 * g;
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    qs[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+                qs[0] = qs[1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int s = 0; s < NS; ++s) {
                     const bf16x8 hi = lds_row8(x + 32 * s), lo = lds_row8(x + LDS::kSPart + 32 * s);
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
+                    for (int t = 0; t < 2; ++t)
                         qs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(unit_frag<true>(qf[s][t]).p[0], lo, qs[t], 0, 0, 0);
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
+                    for (int t = 0; t < 2; ++t)
                         qs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(unit_frag<true>(qf[s][t]).p[0], hi, qs[t], 0, 0, 0);
                 }
                 const float *s_vec = reinterpret_cast<const float *>(lds + LDS::kVec) + half * 4 * kC;
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    qs[t] *= a.scale * row_vec(s_vec, kRise, t, lane);
+                qs[0] *= a.scale * row_vec(s_vec, kRise, ta, lane);
+                qs[1] *= a.scale * row_vec(s_vec, kRise, tb, lane);
                 fetch_q(min(c + 1, c1 - 1));
             }
             lds_barrier();
@@ -1214,14 +1208,15 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
 // ---------------------------------------------------------------------------
 template <int KD>
 struct BackLds {
-    using K = Tile<KD, true>;
+    using K = Tile<KD, true, kHelpThreads>;
+    using Z = Tri<true, kHelpThreads>;
     // in uint16_t
     static constexpr int kK = 0;
     static constexpr int kQ = kK + 2 * K::kSize;
     static constexpr int kZ = kQ + 2 * K::kSize;
-    static constexpr int kVec = kZ + 2 * Tri<true>::kSize;
+    static constexpr int kVec = kZ + 2 * Z::kSize;
     static constexpr int kFlag = kVec + 4 * 4 * kC * 2;  // four chunks' vectors: the last is still read
-    static constexpr int kD = kFlag + 16;               // [4 waves][4 tiles][64 lanes] of f32x4
+    static constexpr int kD = kFlag + 32;               // [4 waves][4 tiles][64 lanes] of f32x4
     static constexpr int kE = kD + 4 * 4 * 64 * 8;      // [4 waves][KD / 16 tiles][64 lanes]
     static constexpr size_t kBytes = (kE + 4 * (KD / 16) * 64 * 8) * 2;
 };
@@ -1231,11 +1226,11 @@ __device__ __forceinline__ void back_walk(const DeltaArgs &a, unsigned block)
 {
     using LDS = BackLds<KD>;
     using TK = typename LDS::K;
-    using U_ = Tri<true>;
+    using U_ = typename LDS::Z;
     constexpr int NS = KD / 32, NM = KD / 16;
     extern __shared__ __attribute__((aligned(16))) char s_dyn[];
     uint16_t *lds = reinterpret_cast<uint16_t *>(s_dyn);
-    int *s_flag = reinterpret_cast<int *>(lds + LDS::kFlag);      // [2][4]: D, E ready
+    int *s_flag = reinterpret_cast<int *>(lds + LDS::kFlag);      // [2][2][4]: D, E ready, by either help wave
 
     const int64_t head = block / (unsigned)(a.segs * a.slices);
     const int rest = block % (unsigned)(a.segs * a.slices), seg = rest / a.slices, slice = rest % a.slices;
@@ -1268,15 +1263,15 @@ __device__ __forceinline__ void back_walk(const DeltaArgs &a, unsigned block)
                 s_e[m * 64] = S.s[m];
         }
         if (lane == 0)
-            s_flag[mine] = s_flag[4 + mine] = 0;
+            s_flag[mine] = s_flag[4 + mine] = s_flag[8 + mine] = s_flag[12 + mine] = 0;
         lds_barrier();
         for (int n = 0; n < c1 - c0; ++n) {
             const int half = n & 1;
             const uint16_t *s_k = lds + LDS::kK + half * TK::kSize, *s_z = lds + LDS::kZ + half * U_::kSize;
             const float *s_vec = reinterpret_cast<const float *>(lds + LDS::kVec) + (n & 3) * 4 * kC;
-            Frag<1> kr[NS][4];
+            Frag<1> kr[2][4];
 #pragma unroll
-            for (int s = 0; s < NS; ++s)
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
                     kr[s][t] = TK::rows_stacked(s_k, t, s, lane);
@@ -1288,20 +1283,23 @@ __device__ __forceinline__ void back_walk(const DeltaArgs &a, unsigned block)
                 d[t] = w[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
-                if (s == NS / 2) {
-                    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        z1[t] = U_::template get<3>(s_z, t, 1, lane);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
 #pragma unroll
                 for (int o = 2; o >= 0; --o)
 #pragma unroll
                     for (int t = 0; t < 4; ++t)
-                        d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kr[s][t].p[0], sf[s].p[o], d[t], 0, 0, 0);
+                        d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kr[s & 1][t].p[0], sf[s].p[o], d[t], 0, 0, 0);
+                if (s + 2 < NS) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        kr[s & 1][t] = TK::rows_stacked(s_k, t, s + 2, lane);
+                }
             }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                z1[t] = U_::template get<3>(s_z, t, 1, lane);
             LdsFlag::await(&s_flag[mine], n + 1);
+            LdsFlag::await(&s_flag[4 + mine], n + 1);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 d[t] = s_d[t * 64] + row_vec(s_vec, kLeft, t, lane) * d[t];     // dU
@@ -1310,10 +1308,6 @@ __device__ __forceinline__ void back_walk(const DeltaArgs &a, unsigned block)
 #pragma unroll
             for (int t = 0; t < 2; ++t)
                 z0[t] = U_::template get<3>(s_z, t, 0, lane);
-            Frag<1> kc0[NM], kc1[NM];
-#pragma unroll
-            for (int m = 0; m < NM; ++m)
-                kc0[m] = TK::columns_stacked(s_k, m, 0, lane);
             __builtin_amdgcn_sched_barrier(0);
             const Frag<3> f0 = split<3>(x[0], x[1]), f1 = split<3>(x[2], x[3]);
 #pragma unroll
@@ -1327,9 +1321,15 @@ __device__ __forceinline__ void back_walk(const DeltaArgs &a, unsigned block)
                     for (int t = 0; t < 2; ++t)
                         w[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(z0[t].p[i], f0.p[o - i], w[t], 0, 0, 0);
                 }
+            Frag<1> kc[2][2][2];
+            auto load_kc = [&](int s) {
 #pragma unroll
-            for (int m = 0; m < NM; ++m)
-                kc1[m] = TK::columns_stacked(s_k, m, 1, lane);
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        kc[s & 1][m][i] = TK::columns_stacked(s_k, 2 * s + m, i, lane);
+            };
+            load_kc(0);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 w[t] = d[t] - w[t];
@@ -1339,19 +1339,23 @@ __device__ __forceinline__ void back_walk(const DeltaArgs &a, unsigned block)
             }
             const float whole = s_vec[kWhole * kC];
             const Frag<3> w0 = split<3>(w[0], w[1]), w1 = split<3>(w[2], w[3]);
-            LdsFlag::await(&s_flag[4 + mine], n + 1);
+            LdsFlag::await(&s_flag[8 + mine], n + 1);
+            LdsFlag::await(&s_flag[12 + mine], n + 1);
 #pragma unroll
             for (int m = 0; m < NM; ++m)
                 S.s[m] = S.s[m] * whole + s_e[m * 64];
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
+                if (s + 1 < NS)
+                    load_kc(s + 1);
 #pragma unroll
                 for (int o = 2; o >= 0; --o)
 #pragma unroll
-                    for (int m = 2 * s; m < 2 * s + 2; ++m) {
-                        S.s[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc0[m].p[0], w0.p[o], S.s[m], 0, 0, 0);
-                        S.s[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc1[m].p[0], w1.p[o], S.s[m], 0, 0, 0);
-                    }
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+                            S.s[2 * s + m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                kc[s & 1][m][i].p[0], i ? w1.p[o] : w0.p[o], S.s[2 * s + m], 0, 0, 0);
                 sf[s] = split<3>(S.s[2 * s], S.s[2 * s + 1]);
                 if constexpr (!SCAN) {
 #pragma unroll
@@ -1392,41 +1396,40 @@ __device__ __forceinline__ void back_walk(const DeltaArgs &a, unsigned block)
             if (tid < kC)
                 *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(lds + LDS::kVec) + (n & 3) * 4 * kC + 4 * tid) = vecs;
         };
+        // A chain wave has two help waves: of P^T dO and w they take row tiles 0
+        // and 2, and 1 and 3, of the state's tiles the first and second half.
+        const int part = (wave - 4) >> 2, ta = part, tb = 2 + part, m0 = part * (NM / 2);
         // P and dO of a chunk, and P^T dO of it
-        f32x4 pf[kBlocks], pd[4];
-        Cols<true> cols, now;       // dO of the chunk that pf is of, and of the one walked
+        f32x4 pf[6], pd[2];
+        Cols<true> cols;
         auto fetch_o = [&](int c) {
-            const float *P = rec + (int64_t)c * a.record + Record::kP;
+            // blocks (0..3, ta), (2..3, tb), those above the diagonal not used
+            const float *P = rec + (int64_t)c * a.record + Record::kP + 4 * lane;
 #pragma unroll
-            for (int t = 0; t < kBlocks; ++t)
-                pf[t] = *reinterpret_cast<const f32x4 *>(P + t * kBlock + 4 * lane);
+            for (int n = 0; n < 6; ++n) {
+                const int cb = n < 4 ? ta : tb, row = n < 4 ? n : n - 2;
+                pf[n] = *reinterpret_cast<const f32x4 *>(P + block_of(max(row, cb), cb) * kBlock);
+            }
             cols.load(Chunk<true, VEC>(a.d_o.p, eo, a.d_o.s.l, c * kC, a.L, a.Dv), col, lane);
         };
         auto product = [&]() {
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-                pd[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const Frag<1> f = split<1>(cols.get(2 * s), cols.get(2 * s + 1));
-#pragma unroll
-                for (int t = 0; t < 2 * s + 2; ++t) {
-                    const Frag<3> p = split<3>(t <= 2 * s ? pf[block_of(2 * s, t < 2 * s ? t : 2 * s)] : f32x4{0.f, 0.f, 0.f, 0.f},
-                                               pf[block_of(2 * s + 1, t)]);
-                    pd[t] = mma<3>(p, f, pd[t]);
-                }
-            }
+            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+            const Frag<1> f0 = split<1>(cols.get(0), cols.get(1)), f1 = split<1>(cols.get(2), cols.get(3));
+            pd[0] = mma<3>(split<3>(part ? zero : pf[0], pf[1]), f0, zero);
+            pd[0] = mma<3>(split<3>(pf[2], pf[3]), f1, pd[0]);
+            pd[1] = mma<3>(split<3>(part ? zero : pf[4], pf[5]), f1, zero);
         };
         // w and dV of chunk c, from the chain's w
-        auto results = [&](int c, const f32x4 (&w)[4]) {
+        auto results = [&](int c, const f32x4 (&w)[2]) {
             const int at = min(c, c1 - 1);
             const Sheet out(a.w + (head * a.NC + at) * kC * a.DV, kC, a.DV, col, lane, c >= c1);
             const Chunk<true, VEC> cv(a.dv.p, b * a.dv.s.b + h * a.dv.s.h, a.dv.s.l, at * kC, a.L, a.Dv, c >= c1);
             const float *s_vec = reinterpret_cast<const float *>(lds + LDS::kVec) + ((c1 - 1 - c) & 3) * 4 * kC;
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                out.put(t, w[t]);
-                store_cols(cv, col, lane, t, row_vec(s_vec, kBeta, t, lane) * w[t]);
+            for (int t = 0; t < 2; ++t) {
+                const int tile = t ? tb : ta;
+                out.put(tile, w[t]);
+                store_cols(cv, col, lane, tile, row_vec(s_vec, kBeta, tile, lane) * w[t]);
             }
         };
         U_::clear(lds + LDS::kZ, tid);
@@ -1436,65 +1439,63 @@ __device__ __forceinline__ void back_walk(const DeltaArgs &a, unsigned block)
         stage(0);
         fetch(max(c1 - 2, c0));
         product();
-        now = cols;
-        fetch_o(max(c1 - 2, c0));
         lds_barrier();
         for (int n = 0; n < c1 - c0; ++n) {
             const int c = c1 - 1 - n, half = n & 1;
             const uint16_t *s_q = lds + LDS::kQ + half * TK::kSize;
             const float *s_vec = reinterpret_cast<const float *>(lds + LDS::kVec) + (n & 3) * 4 * kC;
-            f32x4 w[4];
+            f32x4 w[2];
             if constexpr (!SCAN) {
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    w[t] = s_d[t * 64];     // of the chunk before; the first turn has none
+                w[0] = s_d[ta * 64];    // of the chunk before; the first turn has none
+                w[1] = s_d[tb * 64];
             }
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-                s_d[t * 64] = pd[t];
+            s_d[ta * 64] = pd[0];
+            s_d[tb * 64] = pd[1];
             if (lane == 0)
-                LdsFlag::set(&s_flag[mine], n + 1);
+                LdsFlag::set(&s_flag[4 * part + mine], n + 1);
             if constexpr (!SCAN) {
                 const Sheet out(a.grads + (head * a.NC + c) * KD * a.DV, KD, a.DV, col, lane);
 #pragma unroll
-                for (int m = 0; m < NM; ++m)
-                    out.put(m, s_e[m * 64]);
+                for (int m = 0; m < NM / 2; ++m)
+                    out.put(m0 + m, s_e[(m0 + m) * 64]);
             }
             // Q^T (scale rise dO)
-            f32x4 e[NM];
+            f32x4 e[NM / 2];
 #pragma unroll
-            for (int m = 0; m < NM; ++m)
+            for (int m = 0; m < NM / 2; ++m)
                 e[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const Frag<3> f = split<3>(a.scale * row_vec(s_vec, kRise, 2 * s, lane) * now.get(2 * s),
-                                           a.scale * row_vec(s_vec, kRise, 2 * s + 1, lane) * now.get(2 * s + 1));
+                const Frag<3> f = split<3>(a.scale * row_vec(s_vec, kRise, 2 * s, lane) * cols.get(2 * s),
+                                           a.scale * row_vec(s_vec, kRise, 2 * s + 1, lane) * cols.get(2 * s + 1));
+                Frag<1> qc[NM / 2];
 #pragma unroll
-                for (int m = 0; m < NM; ++m)
-                    e[m] = mma<3>(TK::columns_stacked(s_q, m, s, lane), f, e[m]);
+                for (int m = 0; m < NM / 2; ++m)
+                    qc[m] = TK::columns_stacked(s_q, m0 + m, s, lane);
+#pragma unroll
+                for (int o = 2; o >= 0; --o)
+#pragma unroll
+                    for (int m = 0; m < NM / 2; ++m)
+                        e[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qc[m].p[0], f.p[o], e[m], 0, 0, 0);
             }
 #pragma unroll
-            for (int m = 0; m < NM; ++m)
-                s_e[m * 64] = e[m];
+            for (int m = 0; m < NM / 2; ++m)
+                s_e[(m0 + m) * 64] = e[m];
             if (lane == 0)
-                LdsFlag::set(&s_flag[4 + mine], n + 1);
+                LdsFlag::set(&s_flag[8 + 4 * part + mine], n + 1);
             // Loads wait for a turn of the walk before their use and come
             // before its stores: the counter that a load is waited for by
             // runs in order over both.
+            fetch_o(max(c - 1, c0));
             stage(n + 1);
-            fetch(max(c - 2, c0));
             product();
-            now = cols;
-            fetch_o(max(c - 2, c0));
+            fetch(max(c - 2, c0));
             if constexpr (!SCAN)
                 results(c + 1, w);
             lds_barrier();
         }
         if constexpr (!SCAN) {
-            f32x4 w[4];
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-                w[t] = s_d[t * 64];
+            const f32x4 w[2] = {s_d[ta * 64], s_d[tb * 64]};
             results(c0, w);
         }
     }
