@@ -326,21 +326,11 @@ __device__ __forceinline__ void put_parts(uint16_t *p, int part, f32x8 v)
         *reinterpret_cast<bf16x8 *>(p + n * part) = f.p[n];
 }
 
-// e^x as 2^(x log2 e), with the part of x log2 e that one product rounds away
-// put back as a factor 1 + r ln 2.
-__device__ __forceinline__ float exp_of(float x)
-{
-    const float p = x * 1.44269504f;
-    const float r = __builtin_fmaf(x, 1.44269504f, -p) + x * 1.92596299e-8f;
-    const float e = __builtin_amdgcn_exp2f(p);
-    // an infinite or vanished result stays as it is
-    return __builtin_fabsf(p) < 126.f ? e * __builtin_fmaf(r, 0.693147181f, 1.f) : e;
-}
-
-// e^(G_i - G_j), G as a pair of floats, zero across a step that empties the state.
+// e^(G_i - G_j) from G log2(e) as a pair of floats, zero across a step that
+// empties the state.
 __device__ __forceinline__ float decay_of(float hi_i, float lo_i, float n_i, float hi_j, float lo_j, float n_j)
 {
-    return n_i == n_j ? exp_of((hi_i - hi_j) + (lo_i - lo_j)) : 0.f;
+    return n_i == n_j ? __builtin_amdgcn_exp2f((hi_i - hi_j) + (lo_i - lo_j)) : 0.f;
 }
 
 __device__ __forceinline__ int64_t kv_head(const DeltaArgs &a, int64_t head, int64_t &b, int &h)
@@ -387,8 +377,8 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
         k.load(Chunk<BF16, VEC>(a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk), threadIdx.x);
         q.load(Chunk<BF16, VEC>(a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk), threadIdx.x);
         if (wave == 0) {
-            // G in 64 bits (differences of neighbours stay exact to 32), steps
-            // with g = -inf counted apart.
+            // G log2(e) in 64 bits (differences of neighbours stay exact to
+            // 32), steps with g = -inf counted apart.
             const int t = t0 + lane;
             float gate = 0.f, bt = 0.f;
             if (t < a.L) {
@@ -396,7 +386,7 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
                 bt = static_cast<const float *>(a.beta.p)[b * a.beta.s.b + h * a.beta.s.h + t * a.beta.s.l];
             }
             const bool empty = gate == -__builtin_inff();
-            double G = empty ? 0.0 : (double)gate;
+            double G = empty ? 0.0 : (double)gate * 1.4426950408889634;
             float n = empty ? 1.f : 0.f;
 #pragma unroll
             for (int m = 1; m < 64; m <<= 1) {
@@ -414,10 +404,10 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
             s_n[lane] = n;
             s_beta[lane] = bt;
             float *vec = rec + Record::kVec;
-            vec[kRise * kC + lane] = n == 0.f ? expf(hi + lo) : 0.f;
+            vec[kRise * kC + lane] = decay_of(hi, lo, n, 0.f, 0.f, 0.f);
             vec[kLeft * kC + lane] = decay_of(hi1, lo1, n1, hi, lo, n);
             vec[kBeta * kC + lane] = bt;
-            vec[kWhole * kC + lane] = n1 == 0.f ? expf(hi1 + lo1) : 0.f;
+            vec[kWhole * kC + lane] = decay_of(hi1, lo1, n1, 0.f, 0.f, 0.f);
             vec[kGhi * kC + lane] = hi;
             vec[kGlo * kC + lane] = lo;
             vec[kResets * kC + lane] = n;
