@@ -1741,12 +1741,16 @@ __global__ void __launch_bounds__(kThreads) reverse_kernel(DeltaArgs a)
 // tile w of X and Y (sums over the state's columns), then all rows of the
 // KD / 4 key dimensions that it owns.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float sum16(float v)     // over the lanes of a group of 16
+// Over the lanes of a group of 16, in all of them: row rotations, which need
+// no trip through LDS.
+template <int N>
+__device__ __forceinline__ float add_rotated(float v)
 {
-#pragma unroll
-    for (int m = 8; m >= 1; m >>= 1)
-        v += __shfl_xor(v, m, 64);
-    return v;
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + N, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float sum16(float v)
+{
+    return add_rotated<1>(add_rotated<2>(add_rotated<4>(add_rotated<8>(v))));
 }
 
 template <int KD, bool BF16, bool VEC>
@@ -2042,6 +2046,37 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, i16 = lane & 15;
     const int tile = wave % kTiles, first = wave / kTiles * NT, dim = 16 * tile + i16;
 
+    // What a value head adds: its units of u~, w, dO, V, and the state and
+    // its gradient in the layout of the products.
+    f32x8 u[kUnits], ww[kUnits], sv[2], dv[2];      // two k steps of the states at a time
+    Unit<true> o[kUnits], v[kUnits];
+    float beta[kUnits], vecs;
+    auto fetch = [&](int j) {
+        const int h = hk * group + j;
+        const int64_t at = (b * a.Hv + h) * a.NC + c;
+        const float *rec = a.records + at * a.record;
+        const float *ut = a.ut + at * kC * a.DV, *w = a.w + at * kC * a.DV;
+        const Chunk<true, VEC> cdo(a.d_o.p, b * a.d_o.s.b + h * a.d_o.s.h, a.d_o.s.l, t0, a.L, a.Dv);
+        const Chunk<true, VEC> cv(a.v.p, b * a.v.s.b + h * a.v.s.h, a.v.s.l, t0, a.L, a.Dv);
+        const f32x8 zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int x = tid + i * kGradThreads, row = x / (KV / 8), col = x % (KV / 8) * 8;
+            const int at8 = row * a.DV + min(col, a.DV - 8);
+            u[i] = col < a.DV ? load8(ut + at8) : zero;
+            ww[i] = col < a.DV ? load8(w + at8) : zero;
+            o[i] = cdo.unit(row, col);
+            v[i] = cv.unit(row, col);
+            beta[i] = rec[Record::kVec + kBeta * kC + row];
+        }
+        vecs = rec[Record::kVec + min(tid, kVecs * kC - 1)];
+    };
+    auto fetch_state = [&](int j, int s) {
+        const int64_t at = (b * a.Hv + hk * group + j) * a.NC + c;
+        const int e = dim * a.DV + min(32 * s, a.DV - 32) + 8 * g;
+        sv[s & 1] = load8(a.states + at * KD * a.DV + e);
+        dv[s & 1] = load8(a.grads + at * KD * a.DV + e);
+    };
     {
         TK tk, tq;
         tk.load(Chunk<true, VEC>(a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk), tid);
@@ -2062,58 +2097,35 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
 
     for (int j = 0; j < group; ++j) {
         const int h = hk * group + j;
-        const int64_t head = b * a.Hv + h, at = head * a.NC + c;
-        const float *rec = a.records + at * a.record;
-        const float *S = a.states + at * KD * a.DV + dim * a.DV, *dS = a.grads + at * KD * a.DV + dim * a.DV;
-        f32x8 sv[KV / 32], dv[KV / 32];
-        {
-            const float *ut = a.ut + at * kC * a.DV, *w = a.w + at * kC * a.DV;
-            const Chunk<true, VEC> cdo(a.d_o.p, b * a.d_o.s.b + h * a.d_o.s.h, a.d_o.s.l, t0, a.L, a.Dv);
-            const Chunk<true, VEC> cv(a.v.p, b * a.v.s.b + h * a.v.s.h, a.v.s.l, t0, a.L, a.Dv);
-            f32x8 u[kUnits], ww[kUnits];
-            Unit<true> o[kUnits], v[kUnits];
-            float beta[kUnits];
+        const float *rec = a.records + ((b * a.Hv + h) * a.NC + c) * a.record;
+        fetch(j);
+        fetch_state(j, 0);
+        fetch_state(j, 1);
+        if (tid < kVecs * kC)
+            s_vec[tid] = vecs;
 #pragma unroll
-            for (int i = 0; i < kUnits; ++i) {
-                const int x = tid + i * kGradThreads, row = x / (KV / 8), col = x % (KV / 8) * 8;
-                u[i] = ww[i] = f32x8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (col < a.DV) {
-                    u[i] = load8(ut + row * a.DV + col);
-                    ww[i] = load8(w + row * a.DV + col);
-                }
-                o[i] = cdo.unit(row, col);
-                v[i] = cv.unit(row, col);
-                beta[i] = rec[Record::kVec + kBeta * kC + row];
-            }
-            if (tid < kVecs * kC)
-                s_vec[tid] = rec[Record::kVec + tid];
+        for (int i = 0; i < kUnits; ++i) {
+            const int x = tid + i * kGradThreads, row = x / (KV / 8), col = x % (KV / 8) * 8;
+            const int p = row * TV::kRow + col;
+            put_parts<3>(s_u + p, TV::kPart, u[i]);
+            put_parts<2>(s_w + p, TV::kPart, ww[i]);
+            *reinterpret_cast<uint4 *>(s_o + p) = o[i].v;
+            float uw = dot8(u[i], ww[i], 0.f), vw = dot8(unit_values<true>(v[i]), ww[i], 0.f);
+            if constexpr (KV == 128) {      // a row's units are a group of 16 lanes, or of 8
+                uw = sum16(uw);
+                vw = sum16(vw);
+            } else {
 #pragma unroll
-            for (int s = 0; s < KV / 32; ++s) {
-                sv[s] = dv[s] = f32x8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (32 * s < a.DV) {
-                    sv[s] = load8(S + 32 * s + 8 * g);
-                    dv[s] = load8(dS + 32 * s + 8 * g);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kUnits; ++i) {
-                const int x = tid + i * kGradThreads, row = x / (KV / 8), col = x % (KV / 8) * 8;
-                const int p = row * TV::kRow + col;
-                put_parts<3>(s_u + p, TV::kPart, u[i]);
-                put_parts<2>(s_w + p, TV::kPart, ww[i]);
-                *reinterpret_cast<uint4 *>(s_o + p) = o[i].v;
-                float uw = dot8(u[i], ww[i], 0.f), vw = dot8(unit_values<true>(v[i]), ww[i], 0.f);
-#pragma unroll
-                for (int m = KV / 16; m >= 1; m >>= 1) {
+                for (int m = 4; m >= 1; m >>= 1) {
                     uw += __shfl_xor(uw, m, 64);
                     vw += __shfl_xor(vw, m, 64);
                 }
-                if (col == 0) {
-                    s_vdv[row] = vw * beta[i];
-                    if (t0 + row < a.L)
-                        static_cast<float *>(const_cast<void *>(a.dbeta.p))[b * a.dbeta.s.b + h * a.dbeta.s.h +
-                                                                            (t0 + row) * a.dbeta.s.l] = uw;
-                }
+            }
+            if (col == 0) {
+                s_vdv[row] = vw * beta[i];
+                if (t0 + row < a.L)
+                    static_cast<float *>(const_cast<void *>(a.dbeta.p))[b * a.dbeta.s.b + h * a.dbeta.s.h +
+                                                                        (t0 + row) * a.dbeta.s.l] = uw;
             }
         }
         lds_barrier();
@@ -2168,8 +2180,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
             if (32 * s >= a.DV)
                 break;
             if (first == 0)
-                ss = dot8(sv[s], dv[s], ss);
-            const Frag<3> fs = split<3>(sv[s]), fd = split<3>(dv[s]);
+                ss = dot8(sv[s & 1], dv[s & 1], ss);
+            const Frag<3> fs = split<3>(sv[s & 1]), fd = split<3>(dv[s & 1]);
+            if (s + 2 < KV / 32)
+                fetch_state(j, s + 2);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const int p = (16 * (first + t) + i16) * TV::kRow + 32 * s + 8 * g;
