@@ -2432,23 +2432,32 @@ int padded_value(int Dv) { return (Dv + 31) / 32 * 32; }
 
 int slices_of(int Dv) { return (Dv + 63) / 64; }
 
-// How many segments the chunks of a head are cut into.  A walk takes its time
-// by the chunk, whether 16 or all 256 compute units walk, and cutting it adds
-// a walk without outputs and the joining of the segments.
+// How many segments the chunks of a head are cut into.  A chunk of a walk
+// takes 2.3 us (keys of 64) or 3.3 us (128) whether one or all 256 compute
+// units walk; G segments divide that time by G, but walk twice (once without
+// outputs) and are joined one after another, 2.2 or 6.5 us each, so G is near
+// the root of NC times the ratio, and no more than fills the device.
+// Forward, in us, as one and cut: 8 heads of 64, 1024 steps 51 and 40, 16384
+// steps 618 and 152; 8 heads of 128, 1024 steps 68 and 60, 16384 steps 879
+// and 280; 32 heads of 128 (64 walks), 4096 steps 244 and 200, 1024 steps 72
+// and 79 (not cut).  The backward, which has two walks for each, gains up to
+// half as many: 16 heads of 128, 4096 steps 359 and 319; 32 heads 498 and 554
+// (not cut).
 struct Cut {
     int segs, chunks;
 };
 
-Cut cut_of(int64_t heads, int64_t L, int Dv, uint32_t flags)
+Cut cut_of(int64_t heads, int64_t L, int Dk, int Dv, uint32_t flags, bool bwd)
 {
-    const int64_t NC = (L + kC - 1) / kC, walks = heads * slices_of(Dv);
+    const int64_t NC = (L + kC - 1) / kC, walks = heads * slices_of(Dv) * (bwd ? 2 : 1);
     int64_t segs = 1;
-    if ((flags & PDSSM_DATA_BF16) && walks > 0 && walks * 4 <= 256 && NC >= 32) {
-        segs = 256 / walks;
-        if (segs > NC / 8)
-            segs = NC / 8;
-        if (segs > 32)
-            segs = 32;
+    if ((flags & PDSSM_DATA_BF16) && walks > 0 && walks <= 64 && NC >= (walks > 32 ? 32 : 16)) {
+        int64_t root = 1;
+        while ((root + 1) * (root + 1) <= NC)
+            ++root;
+        segs = padded_key(Dk) == 64 ? root * 3 / 2 : root;
+        const int64_t most = 256 / (heads * slices_of(Dv));
+        segs = segs < most ? segs : most;
     }
     Cut c;
     c.chunks = (int)((NC + segs - 1) / segs);
@@ -2470,7 +2479,7 @@ Layout layout_of(int64_t B, int64_t Hv, int64_t L, int Dk, int Dv, uint32_t flag
     chunks = chunks > 0 ? chunks : 1;
     const int64_t state = (int64_t)padded_key(Dk) * padded_value(Dv) * 4, rows = (int64_t)kC * padded_value(Dv) * 4;
     Layout l;
-    l.cut = cut_of(heads, L, Dv, flags);
+    l.cut = cut_of(heads, L, Dk, Dv, flags, bwd);
     const int64_t cuts = l.cut.segs > 1 ? heads * l.cut.segs : 0;
     l.records = 0;
     l.seg_states = chunks * (bwd ? Record::kBwd : Record::kFwd) * 4;
