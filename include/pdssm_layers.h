@@ -27,7 +27,8 @@
  * Arithmetic is fp32 or its equal (a product of fp32 values on the matrix
  * cores is taken as the sum of bf16 parts that together hold all 24 bits),
  * with one rounding to nearest even into a bf16 output; terms of bf16
- * outputs alone may carry 16 bits.  Results are bitwise reproducible.
+ * outputs alone may carry 16 bits, and dq and dk of pdssm_delta_bwd one more
+ * rounding to bf16 inside the chunk.  Results are bitwise reproducible.
  * A NaN or an infinity among the inputs of a step spoils that sequence from
  * the first of the step's 64 steps on (in pdssm_delta_bwd up to its end).
  *
@@ -39,6 +40,9 @@
  * (rows that all begin on 16 bytes are read faster).  States are contiguous
  * [B,Hv,Dk,Dv], 16-byte aligned.  Outputs overlap neither inputs nor each
  * other, except where said.
+ *
+ * The delta rule reads rows fastest whose head size is a multiple of 8 values
+ * and that begin on 16 bytes, without overlapping.
  *
  * Ownership, execution and errors as in pdssm.h: the caller owns every buffer
  * and the workspace, which may hold anything on entry; the library allocates
@@ -80,8 +84,10 @@ int pdssm_delta_fwd(const void *q, const void *k, const void *v, const float *g,
                     uint32_t flags, const pdssm_strides *strides, void *workspace,
                     size_t workspace_bytes, hipStream_t stream);
 
-/* Workspace bytes of pdssm_delta_fwd: about 22 KB for every 64 steps of a
- * value head; 0 when the arguments are invalid. */
+/* Workspace bytes of pdssm_delta_fwd: 22 KB for every 64 steps of a value
+ * head, and for long sequences of few heads (cut into at most about 1.5 times
+ * the root of L / 64 segments) some states for each segment; 0 when the
+ * arguments are invalid. */
 size_t pdssm_delta_workspace_bytes(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int32_t Dk,
                                    int32_t Dv, uint32_t flags);
 
@@ -110,7 +116,8 @@ int pdssm_delta_bwd(const void *q, const void *k, const void *v, const float *g,
 
 /* Workspace bytes of pdssm_delta_bwd: for every 64 steps of a value head, the
  * state and its gradient (8 Dk Dv bytes), two vectors of Dv for each step and
- * about 32 KB; 0 when the arguments are invalid. */
+ * 32 KB, and states for each segment as pdssm_delta_fwd; 0 when the arguments
+ * are invalid. */
 size_t pdssm_delta_bwd_workspace_bytes(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int32_t Dk,
                                        int32_t Dv, uint32_t flags);
 

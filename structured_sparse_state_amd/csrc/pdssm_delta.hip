@@ -22,14 +22,23 @@
 // The last line holds because scaling every later product with the state by
 // e^g_t is the same as scaling S: the gradient of g_t is <S, dS> around it.
 //
-// Kernels: prep_kernel makes Z, P and the gates' vectors of every chunk, all
-// chunks side by side.  chain_kernel walks the chunks of a sequence; a wave
+// Kernels.  prep_kernel makes Z, P and the gates' vectors of every chunk, all
+// chunks side by side.  The walks take the chunks of a head in order: a wave
 // owns 16 columns of the state, whose recurrences are independent, and keeps
 // them in registers in the matrix cores' result layout, so states and u feed
-// the next product without leaving the wave.  In the backward chain_kernel
-// runs again to keep the states and u~, reverse_kernel walks the chunks back
-// in the same way, and grad_kernel forms what sums over the columns (dQ, dK,
-// dg, dbeta), all chunks side by side.
+// the next product without leaving the wave.  pipe_kernel walks forward,
+// back_kernel in both directions at once for the gradients (the walk forward
+// then keeps the states and u~, the walk back the states' gradients and w),
+// and grads_kernel forms what sums over the columns (dQ, dK, dg, dbeta), all
+// chunks side by side.  Long sequences of few heads are cut into segments that
+// walk side by side (cut_of, join_kernel).  chain_kernel, reverse_kernel and
+// grad_kernel are the same steps for fp32 data, whose three parts of q, k and
+// dO fill LDS, with all of a workgroup's waves doing the same.
+//
+// What bounds them: a walk takes its chunks one after another, and each is a
+// chain of three products and two splits into parts that no other work of the
+// head can overtake; see cut_of for its time.  The preparation and grads_kernel
+// wait for memory between their phases more than they compute.
 #include <hip/hip_runtime.h>
 
 #include "pdssm_device.h"
@@ -345,7 +354,10 @@ __device__ __forceinline__ int64_t kv_head(const DeltaArgs &a, int64_t head, int
 // Wave a forms row tile a of N and P (bf16 products are exact, fp32 data goes
 // in three parts).  Z = N - N beta Z by forward substitution over 16 x 16
 // blocks: the diagonal blocks row by row with a column in each lane, the
-// others by fp32 matrix instructions, a block column in each wave.
+// others by fp32 matrix instructions, a block column in each wave.  140 to
+// 170 us for the 16384 chunks of the LM layer (8 x 32 heads of 64, 4096 steps),
+// 3.7 to 4.5 TB/s of its 630 MB: five workgroups of 32 KB LDS a compute unit, each waiting at the
+// ends of its phases (without one of them it takes 142 to 179 us).
 // ---------------------------------------------------------------------------
 constexpr int kMat = 20;        // row of a 16 x 16 fp32 block in LDS
 __device__ __forceinline__ constexpr int lds_block(int a, int b) { return block_of(a, b) * 16 * kMat; }
@@ -708,17 +720,19 @@ __device__ __forceinline__ f32x4 row_vec(const float *s_vec, int which, int a, i
 }
 
 // ---------------------------------------------------------------------------
-// chain_kernel: the chunks of a head in order.  KEEP: the backward's pass,
-// which keeps the states before the chunks and u~ and forms no outputs.
+// chain_kernel: the chunks of a head in order, fp32 data.  KEEP: the
+// backward's pass, which keeps the states before the chunks and u~ and forms
+// no outputs.  About 4 us a chunk (keys of 64): the next chunk's rows load
+// while this one's products run, but every wave stages, walks and stores in
+// turn.
 // ---------------------------------------------------------------------------
-template <int KD, bool BF16, bool VEC, bool KEEP>
+template <int KD, bool VEC, bool KEEP>
 __global__ void __launch_bounds__(kThreads) chain_kernel(DeltaArgs a)
 {
+    constexpr bool BF16 = false;
     using T = Tile<KD, BF16>;
     using L_ = Tri<false>;
-    // Parts and order of products that end in an output only: 16 bits are
-    // enough for one that is rounded to 8 (they add 2^-17 to its 2^-9).
-    constexpr int NO = BF16 ? 2 : 3;
+    constexpr int NO = 3;
     extern __shared__ __attribute__((aligned(16))) char s_dyn[];
     uint16_t *s_k = reinterpret_cast<uint16_t *>(s_dyn);
     uint16_t *s_z = s_k + T::kSize;
@@ -852,13 +866,17 @@ __global__ void __launch_bounds__(kThreads) chain_kernel(DeltaArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// pipe_kernel: chain_kernel's walk for bf16 data, a workgroup of eight waves.
-// Waves 0..3 ("chain") own 16 columns of the state each and do only what the
-// next chunk waits for: u from S, then S.  Waves 4..7 ("help") stage the next
-// chunk's K, V, Z and vectors in the other half of LDS, and form the outputs
-// of the chunk before: each takes the columns of one chain wave, whose S and u
-// it gets in two bf16 parts through LDS.  One barrier a chunk; a flag says
-// when the parts of S are there.
+// pipe_walk: the walk for bf16 data, a workgroup of twelve waves.  Waves 0..3
+// ("chain") own 16 columns of the state each and do only what the next chunk
+// waits for: u from S, then S.  Waves 4..11 ("help") stage the next chunk's K,
+// V, Z and vectors in the other half of LDS, and form the outputs of the chunk
+// before: two of them share the columns of a chain wave, whose S and u they
+// get in two bf16 parts through LDS (16 bits: they add 2^-17 to an output's
+// own 2^-9).  One barrier a chunk; a flag says when the parts of S are there.
+// The LM layer's walk takes 205 to 231 us, 3.4 us a chunk on every compute unit: the
+// chain alone needs 2.4 us (84 products of 16 cycles, 370 other instructions,
+// reads from LDS between them), the help waves' loads, products and stores on
+// the same four SIMDs the rest.
 // ---------------------------------------------------------------------------
 enum Mode { kOut, kKeep, kScan };   // outputs; states and u~ kept; the last state alone
 
@@ -1194,7 +1212,9 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
 // P^T dO before a chunk and Q^T (scale rise dO) during it, handed over as fp32
 // tiles in LDS; the chain leaves w and the new gradient in the same places,
 // from where the help waves write w, dV and the gradient to memory.  SCAN: the
-// gradient before the segment alone, from zero after it.
+// gradient before the segment alone, from zero after it.  Both walks of the
+// backward's LM layer (4 x 16 heads of 128, 4096 steps, 1.4 GB to and from
+// memory) take 404 us, 6.3 us a chunk; the chain by itself would take 2.9 us.
 // ---------------------------------------------------------------------------
 template <int KD>
 struct BackLds {
@@ -1611,9 +1631,10 @@ __global__ void __launch_bounds__(kThreads, 1) join_kernel(DeltaArgs a)
 // gradient of the state in registers.  Writes dV, keeps w and the gradients
 // of the states after the chunks.
 // ---------------------------------------------------------------------------
-template <int KD, bool BF16, bool VEC>
+template <int KD, bool VEC>
 __global__ void __launch_bounds__(kThreads) reverse_kernel(DeltaArgs a)
 {
+    constexpr bool BF16 = false;
     using T = Tile<KD, BF16>;
     using U_ = Tri<true>;
     constexpr int NK = T::NK;
@@ -1753,13 +1774,14 @@ __device__ __forceinline__ float sum16(float v)
     return add_rotated<1>(add_rotated<2>(add_rotated<4>(add_rotated<8>(v))));
 }
 
-template <int KD, bool BF16, bool VEC>
+template <int KD, bool VEC>
 __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
 {
+    constexpr bool BF16 = false;
     using T = Tile<KD, BF16>;
     using M = Tile<kC, BF16>;           // X and Y: 64 x 64
     constexpr int NK = T::NK;
-    constexpr int NO = BF16 ? 2 : 3;    // parts for dQ and dK alone (see chain_kernel)
+    constexpr int NO = 3;
     constexpr int NM = M::NK;           // parts of X and Y
     constexpr int NTC = KD / 64;        // 16-column tiles of a wave
     extern __shared__ __attribute__((aligned(16))) char s_dyn[];
@@ -1994,11 +2016,14 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
 
 // ---------------------------------------------------------------------------
 // grads_kernel: grad_kernel for bf16 data, eight waves.  u~, w and dO of the
-// chunk go through LDS once (u~ in three parts, w in two), each row's dot
-// products falling out on the way; a wave forms one or two 16 x 16 blocks of
-// X and Y, then the 16 key dimensions it owns (with 64 of them: half of the
-// rows each), reading the state and its gradient straight into the product's
-// layout.
+// chunk go through LDS once (u~ in three parts, w in two: dg and dbeta need
+// u~'s 24 bits, dQ and dK are rounded to 8), each row's dot products falling
+// out on the way; a wave forms one or two 16 x 16 blocks of X and Y, then the
+// 16 key dimensions it owns (with 64 of them: half of the rows each), reading
+// the state and its gradient straight into the product's layout, two k steps
+// ahead.  330 us for 4096 chunks of 128 x 128 (3.3 TB/s of 1.09 GB): its 160 KB
+// of LDS leave one workgroup to a compute unit, so loads and products of a
+// chunk do not overlap with another's.
 // ---------------------------------------------------------------------------
 constexpr int kGradThreads = 512;
 
@@ -2283,7 +2308,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
 // each thread four columns of every TY-th row, all rows in registers: the
 // state is read once and written once.  o needs no second pass over the new
 // state: S_new^T q = (e^g S)^T q + (q . k) u, so both products over the rows
-// and q . k are summed across the threads together.
+// and q . k are summed across the threads together.  4096 states of 128 x 128
+// (540 MB) take 111 us, 4.9 TB/s, and 16 of them 4.6 us, a launch and a trip to
+// memory and back.
 // ---------------------------------------------------------------------------
 struct StepArgs {
     Rows q, k, v, g, beta, o;
@@ -2540,18 +2567,18 @@ int launch(K kernel, int64_t grid, size_t lds, const DeltaArgs &a, hipStream_t s
     return hip_status(hipGetLastError());
 }
 
-template <int KD, bool BF16>
+template <int KD>
 constexpr size_t chain_lds(bool outputs)
 {
-    using T = Tile<KD, BF16>;
+    using T = Tile<KD, false>;
     const size_t one = (size_t)(T::kSize + Tri<false>::kSize) * 2;
     return one * (outputs ? 2 : 1) + 4 * kC * 4;
 }
 
-template <int KD, bool BF16>
+template <int KD>
 constexpr size_t grad_lds()
 {
-    return (size_t)(2 * Tile<KD, BF16>::kSize + 2 * Tile<kC, BF16>::kSize) * 2 + (kVecs * kC + 5 * kC + 4) * 4;
+    return (size_t)(2 * Tile<KD, false>::kSize + 2 * Tile<kC, false>::kSize) * 2 + (kVecs * kC + 5 * kC + 4) * 4;
 }
 
 template <int KD, bool BF16, bool VEC>
@@ -2572,7 +2599,7 @@ int launch_fwd(const DeltaArgs &a, hipStream_t stream)
             rc = launch(pipe_kernel<KD, VEC, kOut>, walks * a.segs, PipeLds<KD>::bytes(true), a, stream, kPipeThreads);
         return rc;
     } else {
-        return launch(chain_kernel<KD, BF16, VEC, false>, walks, chain_lds<KD, BF16>(true), a, stream);
+        return launch(chain_kernel<KD, VEC, false>, walks, chain_lds<KD>(true), a, stream);
     }
 }
 
@@ -2599,11 +2626,11 @@ int launch_bwd(DeltaArgs a, hipStream_t stream)
             return launch(grads_kernel<KD, 64, VEC>, chunks, GradLds<KD, 64>::kBytes, a, stream, kGradThreads);
         return launch(grads_kernel<KD, 128, VEC>, chunks, GradLds<KD, 128>::kBytes, a, stream, kGradThreads);
     } else {
-        rc = launch(chain_kernel<KD, BF16, VEC, true>, walks, chain_lds<KD, BF16>(false), a, stream);
+        rc = launch(chain_kernel<KD, VEC, true>, walks, chain_lds<KD>(false), a, stream);
         if (rc == PDSSM_OK)
-            rc = launch(reverse_kernel<KD, BF16, VEC>, walks, chain_lds<KD, BF16>(true), a, stream);
+            rc = launch(reverse_kernel<KD, VEC>, walks, chain_lds<KD>(true), a, stream);
         if (rc == PDSSM_OK)
-            rc = launch(grad_kernel<KD, BF16, VEC>, chunks, grad_lds<KD, BF16>(), a, stream);
+            rc = launch(grad_kernel<KD, VEC>, chunks, grad_lds<KD>(), a, stream);
         return rc;
     }
 }
