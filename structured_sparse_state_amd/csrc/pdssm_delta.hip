@@ -1532,98 +1532,126 @@ __global__ void __launch_bounds__(kPipeThreads, 1) back_kernel(DeltaArgs a)
 // join_kernel: the states before segments 1 .. segs - 1 of a head, from the
 // segments' transitions A and ends B: S <- A S + B; behind those workgroups
 // (in the backward) the state gradients after segments segs - 2 .. 0:
-// dS <- A^T dS + C.  A wave owns 16 columns; the segment's A goes through LDS
-// in three parts, the next one loading meanwhile (each wave reading and
-// splitting it by itself took five times as long: 219 against 45 us for 16
-// segments of 128 x 128).
+// dS <- A^T dS + C.  A workgroup owns 16 columns, each of its waves 32 rows:
+// these rows of A go from memory to the wave's registers, the next two
+// segments' while this one's products run, and only the state's parts pass through LDS.
+// Bound by the wait for A: 49 us for 16 segments of 128 x 128 and 8 heads,
+// 3.5 a segment; with one segment under way 57; a workgroup of 64 columns
+// taking all of A through LDS 101.  Every workgroup splits A again, which its
+// waves do side by side.
 // ---------------------------------------------------------------------------
 template <int KD>
 struct JoinLds {
-    static constexpr int kRow = KD + 8, kPart = KD * kRow;
-    static constexpr size_t kBytes = 3 * kPart * 2;
+    static constexpr int kWaves = KD / 32, kThreads = 64 * kWaves;
+    static constexpr size_t kBytes = 2 * kWaves * 3 * 64 * sizeof(bf16x8);     // two turns of the state's parts
+};
+
+template <int N>
+struct Slot {
+    static constexpr int value = N;
 };
 
 template <int KD>
-__global__ void __launch_bounds__(kThreads, 1) join_kernel(DeltaArgs a)
+__global__ void __launch_bounds__(JoinLds<KD>::kThreads, 1) join_kernel(DeltaArgs a)
 {
-    constexpr int kRow = JoinLds<KD>::kRow, kPart = JoinLds<KD>::kPart, kUnits = KD * KD / 8 / kThreads;
+    constexpr int kWaves = JoinLds<KD>::kWaves;
     extern __shared__ __attribute__((aligned(16))) char s_dyn[];
-    uint16_t *s_a = reinterpret_cast<uint16_t *>(s_dyn);
-    const bool back = blockIdx.x >= a.heads * a.slices;
-    const unsigned block = blockIdx.x - (back ? (unsigned)(a.heads * a.slices) : 0u);
-    const int64_t head = block / (unsigned)a.slices;
-    const int slice = block % (unsigned)a.slices;
+    bf16x8 *s_f = reinterpret_cast<bf16x8 *>(s_dyn);
+    const unsigned heads = (unsigned)a.heads, half = heads * (unsigned)((a.DV + 15) / 16);
+    const bool back = blockIdx.x >= half;
+    const unsigned block = blockIdx.x - (back ? half : 0u);
+    // A head's workgroups stand a.heads apart: for a multiple of eight heads
+    // on one XCD, whose L2 then serves all but the first reader of A.
+    const int64_t head = block % heads;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, i16 = lane & 15;
-    const int col = (slice * 4 + wave) * 16 + i16, ends = a.slices * 64, pitch = ends + KD;
+    const int col = (int)(block / heads) * 16 + i16, ends = a.slices * 64, pitch = ends + KD;
     const float *T = a.trans + head * a.segs * KD * (int64_t)pitch;
     const float *C = a.rtrans + head * a.segs * KD * (int64_t)ends;
 
-    f32x8 u[kUnits];
-    State<KD> S, N;
-    // The segment's A in units of eight values, and its end B or C.
-    auto fetch = [&](int seg) {
+    f32x4 u[2][2][kWaves][2], N[2][2], S[2];     // two segments on their way
+    auto get = [&](f32x4 (&to)[2], const float *p, int width) {
+        const Sheet from(p, KD, width, col, lane);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            to[t] = from.get(2 * wave + t);
+    };
+    // The wave's rows of the segment's A (or of its transpose), and its end B or C.
+    auto seg_of = [&](int n) { return back ? a.segs - 1 - n : n; };
+    auto fetch = [&](int n, auto slot) {
+        if (n + 1 >= a.segs)
+            return;
+        const int seg = seg_of(n);
         const float *A = T + (int64_t)seg * KD * pitch + ends;
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            const int x = threadIdx.x + i * kThreads;
-            u[i] = load8(A + x / (KD / 8) * pitch + x % (KD / 8) * 8);
+        for (int t = 0; t < 2; ++t) {
+            const int row = 32 * wave + 16 * t + i16;
+#pragma unroll
+            for (int s = 0; s < kWaves; ++s)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int k = 32 * s + 16 * h + 4 * g;
+                    if (back) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            u[slot.value][t][s][h][j] = A[(k + j) * pitch + row];
+                    } else {
+                        u[slot.value][t][s][h] = *reinterpret_cast<const f32x4 *>(A + row * pitch + k);
+                    }
+                }
         }
         if (back)
-            N.load(C + (int64_t)seg * KD * ends, KD, ends, col, lane);
+            get(N[slot.value], C + (int64_t)seg * KD * ends, ends);
         else
-            N.load(A - ends, KD, pitch, col, lane);
+            get(N[slot.value], A - ends, pitch);
     };
-    auto seg_of = [&](int n) { return back ? a.segs - 1 - n : n; };
     if (back)
-        S.load(C + (int64_t)(a.segs - 1) * KD * ends, KD, ends, col, lane);
+        get(S, C + (int64_t)(a.segs - 1) * KD * ends, ends);
     else
-        S.load(T, KD, pitch, col, lane);
-    if (a.segs > 2)
-        fetch(seg_of(1));
-    for (int n = 1;; ++n) {
-        S.store((back ? a.seg_grads : a.seg_states) + (head * a.segs + seg_of(n)) * KD * a.DV, KD, a.DV, col, lane);
+        get(S, T, pitch);
+    fetch(1, Slot<0>{});
+    fetch(2, Slot<1>{});
+    auto step = [&](int n, auto slot) {
+        const Sheet to((back ? a.seg_grads : a.seg_states) + (head * a.segs + seg_of(n)) * KD * a.DV, KD, a.DV, col, lane);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            to.put(2 * wave + t, S[t]);
         if (n + 1 >= a.segs)
-            break;
+            return false;
+        bf16x8 *turn = s_f + (n & 1) * kWaves * 3 * 64 + lane;
+        const Frag<3> mine = split<3>(S[0], S[1]);
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            const int x = threadIdx.x + i * kThreads;
-            put_parts<3>(s_a + x / (KD / 8) * kRow + x % (KD / 8) * 8, kPart, u[i]);
+        for (int i = 0; i < 3; ++i)
+            turn[(wave * 3 + i) * 64] = mine.p[i];
+        Frag<3> p[2][kWaves];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            S[t] = N[slot.value][t];
+#pragma unroll
+            for (int s = 0; s < kWaves; ++s)
+                p[t][s] = split<3>(u[slot.value][t][s][0], u[slot.value][t][s][1]);
         }
-        State<KD> E = N;
+        fetch(n + 2, slot);
+        // The one barrier of a step: what is written two steps on has been
+        // read by every wave before the next step's.
         lds_barrier();
-        if (n + 2 < a.segs)
-            fetch(seg_of(n + 1));
 #pragma unroll
-        for (int s = 0; s < KD / 32; ++s) {
-            const Frag<3> f = split<3>(S.s[2 * s], S.s[2 * s + 1]);
+        for (int s = 0; s < kWaves; ++s) {
+            Frag<3> f;
 #pragma unroll
-            for (int m0 = 0; m0 < KD / 16; m0 += 4) {
-                Frag<3> p[4];       // four tiles in turn, so that no product waits for the last
+            for (int i = 0; i < 3; ++i)
+                f.p[i] = turn[(s * 3 + i) * 64];
 #pragma unroll
-                for (int m = 0; m < 4; ++m)
+            for (int o = 2; o >= 0; --o)
 #pragma unroll
-                    for (int i = 0; i < 3; ++i) {
-                        const uint16_t *q = s_a + i * kPart;
-                        if (back) {
-                            q += (32 * s + 4 * g + (i16 >> 2)) * kRow + 16 * (m0 + m) + 4 * (i16 & 3);
-                            p[m].p[i] = lds_columns4(q, q + 16 * kRow);
-                        } else {
-                            q += (16 * (m0 + m) + i16) * kRow + 32 * s + 4 * g;
-                            p[m].p[i] = lds_rows4(q, q + 16);
-                        }
-                    }
+                for (int i = 0; i <= o; ++i)
 #pragma unroll
-                for (int o = 2; o >= 0; --o)
-#pragma unroll
-                    for (int i = 0; i <= o; ++i)
-#pragma unroll
-                        for (int m = 0; m < 4; ++m)
-                            E.s[m0 + m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p[m].p[i], f.p[o - i], E.s[m0 + m], 0, 0, 0);
-            }
+                    for (int t = 0; t < 2; ++t)
+                        S[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p[t][s].p[i], f.p[o - i], S[t], 0, 0, 0);
         }
-        S = E;
-        lds_barrier();
-    }
+        return true;
+    };
+    for (int n = 1; step(n, Slot<0>{}) && step(n + 1, Slot<1>{}); n += 2)
+        ;
 }
 
 // ---------------------------------------------------------------------------
@@ -2462,14 +2490,16 @@ int slices_of(int Dv) { return (Dv + 63) / 64; }
 // How many segments the chunks of a head are cut into.  A chunk of a walk
 // takes 2.3 us (keys of 64) or 3.3 us (128) whether one or all 256 compute
 // units walk; G segments divide that time by G, but walk twice (once without
-// outputs) and are joined one after another, 2.2 or 6.5 us each, so G is near
-// the root of NC times the ratio, and no more than fills the device.
-// Forward, in us, as one and cut: 8 heads of 64, 1024 steps 51 and 40, 16384
-// steps 618 and 152; 8 heads of 128, 1024 steps 68 and 60, 16384 steps 879
-// and 280; 32 heads of 128 (64 walks), 4096 steps 244 and 200, 1024 steps 72
-// and 79 (not cut).  The backward, which has two walks for each, gains up to
-// half as many: 16 heads of 128, 4096 steps 359 and 319; 32 heads 498 and 554
-// (not cut).
+// outputs) and are joined one after another, about 1.8 or 3.5 us each, so G is
+// near the root of NC times the ratio, and no more than fills the device.  Keys
+// of 128 with 3/2 of the root measured slower (4 heads, 16384 steps: 195 against
+// 169 us; 8 heads, 4096 steps: 107 against 92).
+// Forward, in us, as one and cut: 8 heads of 64, 1024 steps 51 and 42, 16384
+// steps 618 and 143; 8 heads of 128, 1024 steps 68 and 53, 16384 steps 879
+// and 227; 32 heads of 128 (64 walks), 4096 steps 244 and 196.  Measured with a
+// join of 6.5 us a segment: those 32 heads, 1024 steps 72 and 79 (not cut); the
+// backward, which has two walks for each and gains up to half as many, 16 heads
+// of 128, 4096 steps 359 and 319; 32 heads 498 and 554 (not cut).
 struct Cut {
     int segs, chunks;
 };
@@ -2589,11 +2619,12 @@ int launch_fwd(const DeltaArgs &a, hipStream_t stream)
         return rc;
     const int64_t walks = a.heads * a.slices;
     if constexpr (BF16) {
+        const int64_t joins = a.heads * ((a.DV + 15) / 16);
         if (a.segs > 1) {
             rc = launch(pipe_kernel<KD, VEC, kScan>, a.heads * a.segs * (a.slices + KD / 64), PipeLds<KD>::bytes(false), a,
                         stream, kPipeThreads);
             if (rc == PDSSM_OK)
-                rc = launch(join_kernel<KD>, walks, JoinLds<KD>::kBytes, a, stream);
+                rc = launch(join_kernel<KD>, joins, JoinLds<KD>::kBytes, a, stream, JoinLds<KD>::kThreads);
         }
         if (rc == PDSSM_OK)
             rc = launch(pipe_kernel<KD, VEC, kOut>, walks * a.segs, PipeLds<KD>::bytes(true), a, stream, kPipeThreads);
@@ -2611,12 +2642,13 @@ int launch_bwd(DeltaArgs a, hipStream_t stream)
         return rc;
     const int64_t walks = a.heads * a.slices, chunks = a.heads / a.Hv * a.Hk * a.NC;
     if constexpr (BF16) {
+        const int64_t joins = a.heads * ((a.DV + 15) / 16);
         constexpr size_t lds = BackLds<KD>::kBytes > PipeLds<KD>::bytes(false) ? BackLds<KD>::kBytes : PipeLds<KD>::bytes(false);
         a.back_blocks = (unsigned)(walks * a.segs);
         if (a.segs > 1) {
             rc = launch(back_kernel<KD, VEC, true>, (walks * 2 + a.heads * (KD / 64)) * a.segs, lds, a, stream, kPipeThreads);
             if (rc == PDSSM_OK)
-                rc = launch(join_kernel<KD>, walks * 2, JoinLds<KD>::kBytes, a, stream);
+                rc = launch(join_kernel<KD>, joins * 2, JoinLds<KD>::kBytes, a, stream, JoinLds<KD>::kThreads);
         }
         if (rc == PDSSM_OK)
             rc = launch(back_kernel<KD, VEC, false>, walks * 2 * a.segs, lds, a, stream, kPipeThreads);
