@@ -11,8 +11,9 @@
  *     u    = beta[b,h,t] (v[b,h,t,:] - S^T k[b,hk,t,:])
  *     S   <- S + k[b,hk,t,:] u^T
  *     o[b,h,t,:] = scale S^T q[b,hk,t,:]
- * and s_final is S after the last step.  g is a log decay of any sign, and
- * g = -inf empties the state before the step (a new document begins).
+ * and s_final is S after the last step.  g is a log decay of any sign; one
+ * whose e^g rounds to zero in fp32 (g below -104, -inf and the lowest finite
+ * value among them) empties the state before the step: a new document begins.
  *
  * The norm with rotation.  For every head vector x of q and k (D values):
  *     y = x / sqrt(mean(x^2) + eps) * w       (RMS), or
@@ -104,8 +105,8 @@ size_t pdssm_delta_workspace_bytes(int64_t B, int64_t Hk, int64_t Hv, int64_t L,
  *   strides   of q, k, v, g, beta, d_o, dq, dk, dv, dg, dbeta, or NULL
  *   workspace pdssm_delta_bwd_workspace_bytes bytes, 16-byte aligned
  * Sizes, flags and empty shapes as pdssm_delta_fwd; with L = 0,
- * ds0 = ds_final (or zero).  dg is 0 where g = -inf, and
- * for the first step without s0.
+ * ds0 = ds_final (or zero).  dg is 0 where g empties the state (below
+ * -104), and for the first step without s0.
  */
 int pdssm_delta_bwd(const void *q, const void *k, const void *v, const float *g,
                     const float *beta, const float *s0, const void *d_o, const float *ds_final,

@@ -335,6 +335,11 @@ __device__ __forceinline__ void put_parts(uint16_t *p, int part, f32x8 v)
         *reinterpret_cast<bf16x8 *>(p + n * part) = f.p[n];
 }
 
+// Steps whose e^g rounds to zero in fp32 (half its smallest value is e^-103.97)
+// empty the state.  They are counted and stay out of the running sum, where one
+// of -1e12 would take the bits of every later gate of the chunk.
+constexpr float kEmpties = -104.f;
+
 // e^(G_i - G_j) from G log2(e) as a pair of floats, zero across a step that
 // empties the state.
 __device__ __forceinline__ float decay_of(float hi_i, float lo_i, float n_i, float hi_j, float lo_j, float n_j)
@@ -390,14 +395,14 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
         q.load(Chunk<BF16, VEC>(a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk), threadIdx.x);
         if (wave == 0) {
             // G log2(e) in 64 bits (differences of neighbours stay exact to
-            // 32), steps with g = -inf counted apart.
+            // 32), steps that empty the state counted apart.
             const int t = t0 + lane;
             float gate = 0.f, bt = 0.f;
             if (t < a.L) {
                 gate = static_cast<const float *>(a.g.p)[b * a.g.s.b + h * a.g.s.h + t * a.g.s.l];
                 bt = static_cast<const float *>(a.beta.p)[b * a.beta.s.b + h * a.beta.s.h + t * a.beta.s.l];
             }
-            const bool empty = gate == -__builtin_inff();
+            const bool empty = gate < kEmpties;
             double G = empty ? 0.0 : (double)gate * 1.4426950408889634;
             float n = empty ? 1.f : 0.f;
 #pragma unroll

@@ -1,0 +1,62 @@
+"""The gated delta rule on the GPU at the edges of its range: gates that empty
+the state, whatever value says so.  Inputs and tolerances are those of
+test_gpu_delta; a result that is not a normal fp32 number has no 24 bits, so
+every value may also be off by the smallest normal one, 2^-126."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import structured_sparse_state_amd as pk
+from tests import layers_reference as ref
+from tests.test_gpu_delta import TOL_F32, TOL_KEYS, TOL_OUT, TYPES, inputs, off, say
+
+pytestmark = pytest.mark.gpu
+
+LOWEST = torch.finfo(torch.float32).min
+STEPS = ("q", "k", "v", "g", "beta")
+
+
+def check(x, label):
+    """Forward and gradients against the reference; returns the gradients."""
+    say(f"[case] {label}")
+    args = [x[n] for n in STEPS]
+    want_o, want_s, _ = ref.delta(*args, x["s0"])
+    grads, terms = ref.delta_bwd(*args, x["do"], x["s0"], x["ds"])
+    got = [*pk.delta_rule(*args, x["s0"]), *pk.delta_rule_bwd(*args, x["do"], x["s0"], x["ds"])]
+    torch.cuda.synchronize()
+    f32 = x["q"].dtype == torch.float32
+    tols = [TOL_F32] * 8 if f32 else [TOL_OUT, TOL_F32, TOL_KEYS, TOL_KEYS, TOL_OUT, TOL_F32, TOL_F32, TOL_F32]
+    for name, a, b, tol in zip(("o", "s", "dq", "dk", "dv", "dg", "dbeta", "ds0"), got, (want_o, want_s, *grads), tols):
+        assert a.shape == b.shape and torch.isfinite(a).all(), name
+        size = b.norm() + (8 * terms.norm() if name == "dg" else 0)
+        e = float((a.double().cpu() - b).norm())
+        say(f"  {name} {e:.2e} of {size:.2e}")
+        assert e <= tol * size + 2.0 ** -126 * b.numel() ** 0.5, name
+    return got[2:]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("at", [(0,), (10,), (63, 64), (10, 11, 100), (149,)])
+@pytest.mark.parametrize("gate", [-103.0, -105.0, -1e4, -1e12, -1e30, LOWEST])
+def test_large_negative_gates(dtype, at, gate):
+    """A mask's value among ordinary gates: at the first and the last step, in
+    and at the ends of a chunk, once and several times."""
+    x = inputs(21, 1, 1, 2, 150, 32, 32, TYPES[dtype])
+    x["g"][:, :, list(at)] = gate
+    dg = check(x, f"{dtype} gate {gate:.3g} at {at}")[3]
+    if gate < -104:
+        assert (dg[:, :, list(at)] == 0).all()
+
+
+@pytest.mark.parametrize("gate", [-1e4, -1e15, LOWEST, -float("inf")])
+def test_whole_sequences_and_steps_agree_on_gates(gate):
+    x = inputs(22, 2, 1, 2, 70, 64, 64, torch.bfloat16)
+    x["g"][:, 0, ::7] = gate
+    x["g"][:, 1, 33:] = gate
+    say(f"[case] forward against steps, gate {gate:.3g}")
+    o, s = pk.delta_rule(*(x[n] for n in STEPS), x["s0"])
+    state = x["s0"].clone()
+    steps = [pk.delta_step(*(x[n][:, :, t] for n in STEPS), state) for t in range(70)]
+    torch.cuda.synchronize()
+    assert off(o.float(), torch.stack(steps, 2).float().cpu()) <= 2 * TOL_OUT and off(s, state.cpu()) <= 2 * TOL_F32
