@@ -92,9 +92,9 @@ struct DeltaArgs {
     int64_t heads;          // B*Hv
     // Few heads: the chunks cut in segments of seg_chunks, walked side by side.
     int segs, seg_chunks;
-    float *seg_states;      // [B*Hv][segs][KD][DV]: states before the segments
+    float *seg_states;      // [B*Hv][segs][KD][DV]: states before the segments (s0 among them)
     float *trans;           // [B*Hv][segs][KD][slices*64 + KD]: their ends from zero, and transitions
-    float *seg_grads;       // [B*Hv][segs][KD][DV]: state gradients after the segments
+    float *seg_grads;       // [B*Hv][segs][KD][DV]: state gradients after the segments (ds_final among them)
     float *rtrans;          // [B*Hv][segs][KD][slices*64]: state gradients before them, from zero
     unsigned back_blocks;   // workgroups of back_kernel that walk back
     int Hk, Hv, L, NC, Dk, Dv, DV, record;
@@ -944,7 +944,7 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     S.s[m][r] = 16 * m + 4 * g + r == col - a.slices * 64 ? 1.f : 0.f;
-        } else if (seg > 0 && MODE != kScan) {
+        } else if (a.segs > 1 && MODE != kScan) {
             S.load(a.seg_states + (head * a.segs + seg) * KD * a.DV, KD, a.DV, col, lane);
         } else {
             S.load(a.s0 && seg == 0 ? a.s0 + head * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, col, lane);
@@ -1264,10 +1264,10 @@ __device__ __forceinline__ void back_walk(const DeltaArgs &a, unsigned block)
     // Chunk c is step n = c1 - 1 - c of the walk.
     if (wave < 4) {
         State<KD> S;
-        if (seg == a.segs - 1)
-            S.load(a.ds_final ? a.ds_final + head * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, col, lane);
+        if (a.segs > 1 && !SCAN)
+            S.load(a.seg_grads + (head * a.segs + seg) * KD * a.DV, KD, a.DV, col, lane);
         else
-            S.load(SCAN ? nullptr : a.seg_grads + (head * a.segs + seg) * KD * a.DV, KD, a.DV, col, lane);
+            S.load(a.ds_final && seg == a.segs - 1 ? a.ds_final + head * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, col, lane);
         Frag<3> sf[NS];
 #pragma unroll
         for (int s = 0; s < NS; ++s)
@@ -1534,10 +1534,12 @@ __global__ void __launch_bounds__(kPipeThreads, 1) back_kernel(DeltaArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// join_kernel: the states before segments 1 .. segs - 1 of a head, from the
+// join_kernel: the states before the segments of a head, from s0 and the
 // segments' transitions A and ends B: S <- A S + B; behind those workgroups
-// (in the backward) the state gradients after segments segs - 2 .. 0:
-// dS <- A^T dS + C.  A workgroup owns 16 columns, each of its waves 32 rows:
+// (in the backward) the state gradients after the segments, from the last to
+// the first: dS <- A^T dS + C.  s0 and ds_final are copied too: the last
+// launch writes s_final (or ds0) by other workgroups than those that begin
+// from s0 (ds_final), and the two may be one buffer.  A workgroup owns 16 columns, each of its waves 32 rows:
 // these rows of A go from memory to the wave's registers, the next two
 // segments' while this one's products run, and only the state's parts pass through LDS.
 // Bound by the wait for A: 49 us for 16 segments of 128 x 128 and 8 heads,
@@ -1609,6 +1611,18 @@ __global__ void __launch_bounds__(JoinLds<KD>::kThreads, 1) join_kernel(DeltaArg
         else
             get(N[slot.value], A - ends, pitch);
     };
+    auto put = [&](int n, const f32x4 (&v)[2]) {
+        const Sheet to((back ? a.seg_grads : a.seg_states) + (head * a.segs + seg_of(n)) * KD * a.DV, KD, a.DV, col, lane);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            to.put(2 * wave + t, v[t]);
+    };
+    const float *start = back ? a.ds_final : a.s0;
+    const Sheet first(start ? start + head * a.Dk * a.Dv : nullptr, start ? a.Dk : 0, a.Dv, col, lane);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+        S[t] = first.get(2 * wave + t);
+    put(0, S);
     if (back)
         get(S, C + (int64_t)(a.segs - 1) * KD * ends, ends);
     else
@@ -1616,10 +1630,7 @@ __global__ void __launch_bounds__(JoinLds<KD>::kThreads, 1) join_kernel(DeltaArg
     fetch(1, Slot<0>{});
     fetch(2, Slot<1>{});
     auto step = [&](int n, auto slot) {
-        const Sheet to((back ? a.seg_grads : a.seg_states) + (head * a.segs + seg_of(n)) * KD * a.DV, KD, a.DV, col, lane);
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-            to.put(2 * wave + t, S[t]);
+        put(n, S);
         if (n + 1 >= a.segs)
             return false;
         bf16x8 *turn = s_f + (n & 1) * kWaves * 3 * 64 + lane;

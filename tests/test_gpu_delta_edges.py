@@ -1,7 +1,8 @@
 """The gated delta rule on the GPU at the edges of its range: gates that empty
-the state, whatever value says so.  Inputs and tolerances are those of
-test_gpu_delta; a result that is not a normal fp32 number has no 24 bits, so
-every value may also be off by the smallest normal one, 2^-126."""
+the state, whatever value says so; long sequences of few heads, which are cut
+into segments.  Inputs and tolerances are those of test_gpu_delta; a result that
+is not a normal fp32 number has no 24 bits, so every value may also be off by
+the smallest normal one, 2^-126."""
 from __future__ import annotations
 
 import pytest
@@ -60,3 +61,40 @@ def test_whole_sequences_and_steps_agree_on_gates(gate):
     steps = [pk.delta_step(*(x[n][:, :, t] for n in STEPS), state) for t in range(70)]
     torch.cuda.synchronize()
     assert off(o.float(), torch.stack(steps, 2).float().cpu()) <= 2 * TOL_OUT and off(s, state.cpu()) <= 2 * TOL_F32
+
+
+def cut(B, Hk, Hv, L, Dk, Dv):
+    """Whether a bf16 sequence of these sizes is walked in segments."""
+    chunks = B * Hv * ((L + 63) // 64)
+    return pk.pdssm_delta_workspace_bytes(B, Hk, Hv, L, Dk, Dv, 1) > chunks * (2 * 2560 + 512) * 4
+
+
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (128, 128), (40, 72)])
+def test_states_in_place_of_cut_sequences(Dk, Dv):
+    """s_final over s0 and ds0 over ds_final, bit for bit as elsewhere."""
+    x = inputs(Dk + 1, 1, 1, 2, 2565, Dk, Dv, torch.bfloat16, order="token")
+    assert cut(1, 1, 2, 2565, Dk, Dv)
+    args = [x[n] for n in STEPS]
+    say(f"[case] in place, cut, Dk={Dk} Dv={Dv}")
+    want = [*pk.delta_rule(*args, x["s0"]), *pk.delta_rule_bwd(*args, x["do"], x["s0"], x["ds"])]
+    s, ds = x["s0"].clone(), x["ds"].clone()
+    o, _ = pk.delta_rule(*args, s, s_final=s)
+    out = [torch.empty_like(t) for t in want[2:7]]
+    pk.delta_rule_bwd(*args, x["do"], x["s0"], ds, out=(*out, ds))
+    torch.cuda.synchronize()
+    for a, b in zip((o, s, *out, ds), want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("B,Hk,Hv,L,Dk,Dv,order,gates,s0", [
+    (1, 1, 1, 64 * 16, 128, 128, "head", "plain", False),       # the fewest chunks
+    (2, 1, 3, 64 * 33 + 1, 64, 32, "token", "plain", True),     # shared heads, one step in the last chunk
+    (1, 1, 2, 64 * 41, 64, 64, "token", "empty", True),         # a last segment of one chunk; empty states in all
+    (1, 2, 2, 64 * 37 + 5, 128, 96, "head", "empty", False),
+    (2, 1, 2, 64 * 20 + 9, 50, 70, "apart", "plain", True),     # rows read value by value
+    (3, 1, 1, 64 * 18, 72, 8, "apart", "strong", True),
+])
+def test_cut_sequences(B, Hk, Hv, L, Dk, Dv, order, gates, s0):
+    x = inputs(L, B, Hk, Hv, L, Dk, Dv, torch.bfloat16, order=order, gates=gates, s0=s0)
+    assert cut(B, Hk, Hv, L, Dk, Dv)
+    check(x, f"cut B={B} Hk={Hk} Hv={Hv} L={L} Dk={Dk} Dv={Dv} {order} {gates}")
