@@ -616,10 +616,18 @@ def _need(n: int) -> int:
     return n
 
 
-def _stream_of(t, stream) -> Optional[int]:
-    """`stream`, or the current stream of the tensor's device."""
-    if stream is not None:
-        return _stream(stream)
+def _on_stream(stream, call, *args, **kw):
+    """The call as under torch.cuda.stream(stream): the results and the
+    workspace that it allocates belong to that stream, so memory freed on
+    return is not given to another stream's work while the kernels still run."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, args[0].device)
+    with torch.cuda.stream(stream):
+        return call(*args, **kw)
+
+
+def _stream_of(t) -> Optional[int]:
+    """The current stream of the tensor's device."""
     return _raw_stream(t.get_device()) if _raw_stream is not None and t.is_cuda else _stream(None)
 
 
@@ -644,7 +652,11 @@ def delta_rule(q, k, v, g, beta, s0=None, *, scale: Optional[float] = None, want
     [B,Hv,Dk,Dv] or None).  q, k [B,Hk,L,Dk] and v [B,Hv,L,Dv] bf16 or fp32
     with any strides of the first three dimensions, g (log decay) and beta
     fp32 [B,Hv,L], s0 fp32 [B,Hv,Dk,Dv] or None; scale 1/sqrt(Dk) by default.
-    o has the memory order of v; s_final may be s0."""
+    o has the memory order of v; s_final may be s0.  ``stream`` (here and in
+    the functions below): the call as under torch.cuda.stream(stream)."""
+    if stream is not None:
+        return _on_stream(stream, delta_rule, q, k, v, g, beta, s0, scale=scale, want_state=want_state, o=o,
+                          s_final=s_final, workspace=workspace)
     if o is None:
         o = torch.empty_like(v)
     if s_final is None and want_state:
@@ -656,7 +668,7 @@ def delta_rule(q, k, v, g, beta, s0=None, *, scale: Optional[float] = None, want
     check(library().pdssm_delta_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
                                     beta.data_ptr(), _ptr(s0), o.data_ptr(), _ptr(s_final), B, Hk, Hv, L,
                                     Dk, Dv, Dk ** -0.5 if scale is None else scale, flag, rows,
-                                    workspace.data_ptr(), need, _stream_of(v, stream)))
+                                    workspace.data_ptr(), need, _stream_of(v)))
     return o, s_final
 
 
@@ -679,6 +691,9 @@ def delta_rule_bwd(q, k, v, g, beta, do, s0=None, ds_final=None, *, scale: Optio
     that of s_final (None: zero): (dq, dk, dv, dg, dbeta, ds0 or None), each
     in the memory order of its input.  ``out`` may hold a previous call's
     result to write into."""
+    if stream is not None:
+        return _on_stream(stream, delta_rule_bwd, q, k, v, g, beta, do, s0, ds_final, scale=scale,
+                          want_ds0=want_ds0, out=out, workspace=workspace)
     if out is not None:
         dq, dk, dv, dg, dbeta, ds0 = out
     else:
@@ -694,7 +709,7 @@ def delta_rule_bwd(q, k, v, g, beta, do, s0=None, ds_final=None, *, scale: Optio
                                     dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(),
                                     dbeta.data_ptr(), _ptr(ds0), B, Hk, Hv, L, Dk, Dv,
                                     Dk ** -0.5 if scale is None else scale, flag, rows,
-                                    workspace.data_ptr(), need, _stream_of(v, stream)))
+                                    workspace.data_ptr(), need, _stream_of(v)))
     return dq, dk, dv, dg, dbeta, ds0
 
 
@@ -712,6 +727,8 @@ def delta_step(q, k, v, g, beta, s, *, s_out: Optional[torch.Tensor] = None,
     """One step of the gated delta rule: o [B,Hv,Dv] from q, k [B,Hk,Dk],
     v [B,Hv,Dv], g, beta fp32 [B,Hv] and the state s fp32 [B,Hv,Dk,Dv], which
     is updated in place, or into s_out."""
+    if stream is not None:
+        return _on_stream(stream, delta_step, q, k, v, g, beta, s, s_out=s_out, scale=scale, o=o)
     if s_out is None:
         s_out = s
     if o is None:
@@ -721,7 +738,7 @@ def delta_step(q, k, v, g, beta, s, *, s_out: Optional[torch.Tensor] = None,
     check(library().pdssm_delta_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
                                      beta.data_ptr(), s.data_ptr(), o.data_ptr(), s_out.data_ptr(), B, Hk,
                                      Hv, Dk, Dv, Dk ** -0.5 if scale is None else scale, flag, rows,
-                                     _stream_of(v, stream)))
+                                     _stream_of(v)))
     return o
 
 
@@ -766,13 +783,15 @@ def qk_norm_rope(q, k, wq=None, wk=None, cos=None, sin=None, pos=None, *, kind: 
     (unit length); ``pairs``: "half" (i, i + R/2) or "adjacent" (2i, 2i + 1).
     The results have the memory order of q and k; ``out``: two tensors to
     write into instead (the inputs, to work in place)."""
+    if stream is not None:
+        return _on_stream(stream, qk_norm_rope, q, k, wq, wk, cos, sin, pos, kind=kind, pairs=pairs, eps=eps, out=out)
     q_out, k_out = (torch.empty_like(q), torch.empty_like(k)) if out is None else out
     (flags, B, Hq, Hk, L, D, R, P), rows = _norm_plan(
         _form(q), _form(k), _form(wq), _form(wk), _form(cos), _form(sin), _form(pos), kind, pairs,
         _form(q_out), _form(k_out))
     check(library().pdssm_qk_norm_rope_fwd(q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(cos),
                                            _ptr(sin), _ptr(pos), q_out.data_ptr(), k_out.data_ptr(), B,
-                                           Hq, Hk, L, D, R, P, eps, flags, rows, _stream_of(q, stream)))
+                                           Hq, Hk, L, D, R, P, eps, flags, rows, _stream_of(q)))
     return q_out, k_out
 
 
@@ -794,6 +813,9 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, wq=None, wk=None, cos=None, sin=None,
     outputs: (dq, dk, dwq, dwk), the first two in the memory order of q and k,
     the last two None where the weight is.  ``out``: dq and dk to write into
     instead (dq_out and dk_out, to work in place)."""
+    if stream is not None:
+        return _on_stream(stream, qk_norm_rope_bwd, q, k, dq_out, dk_out, wq, wk, cos, sin, pos, kind=kind,
+                          pairs=pairs, eps=eps, out=out, workspace=workspace)
     dq, dk = (torch.empty_like(q), torch.empty_like(k)) if out is None else out
     (flags, B, Hq, Hk, L, D, R, P), rows, need = _norm_bwd_plan(
         _form(q), _form(k), _form(wq), _form(wk), _form(cos), _form(sin), _form(pos), kind, pairs,
@@ -806,5 +828,5 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, wq=None, wk=None, cos=None, sin=None,
                                            dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), B, Hq, Hk,
                                            L, D, R, P, eps, flags, rows,
                                            workspace.data_ptr() if need else None, need,
-                                           _stream_of(q, stream)))
+                                           _stream_of(q)))
     return dq, dk, dwq, dwk
