@@ -560,8 +560,15 @@ def _data_flag(name: str, *dtypes) -> int:
 
 
 def _form(t):
-    """Shape, strides and type of a tensor, or None."""
-    return None if t is None else (t.shape, t.stride(), t.dtype)
+    """Shape, strides, type and device (-1: not a GPU) of a tensor, or None."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _one_device(*forms) -> None:
+    """The kernels take addresses: a tensor elsewhere would be a fault there."""
+    devices = {form[3] for form in forms if form is not None}
+    if len(devices) > 1 or -1 in devices:
+        raise ValueError("all tensors must be on one GPU")
 
 
 def _want(name: str, form, shape, dtype, contiguous: bool = False) -> None:
@@ -581,7 +588,7 @@ def _rows(dims: int, *forms):
     """The pdssm_strides list of [B,H,L(,D)] tensors (dims 3), or of [B,H(,D)]
     ones (dims 2); D must be contiguous."""
     out = []
-    for shape, st, _ in forms:
+    for shape, st, *_ in forms:
         if len(st) > dims and st[dims] != 1 and shape[dims] > 1:
             raise ValueError("the last dimension must be contiguous")
         out.append((*st[:dims], *(0,) * (3 - dims)))
@@ -605,6 +612,8 @@ def _delta_form(q, k, v, g, beta, dims):
 def _workspace(need: int, workspace, device):
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous and on the tensors' GPU")
     if workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"the workspace needs {need} bytes")
     return workspace
@@ -642,7 +651,9 @@ def _delta_plan(q, k, v, g, beta, o, s0, s_final):
     _want("o", o, v[0], v[2])
     _want("s0", s0, (B, Hv, Dk, Dv), torch.float32, True)
     _want("s_final", s_final, (B, Hv, Dk, Dv), torch.float32, True)
-    return sizes, _rows(3, q, k, v, g, beta, o), _need(pdssm_delta_workspace_bytes(B, Hk, Hv, L, Dk, Dv, flag))
+    need = _need(pdssm_delta_workspace_bytes(B, Hk, Hv, L, Dk, Dv, flag))
+    _one_device(q, k, v, g, beta, o, s0, s_final)
+    return sizes, _rows(3, q, k, v, g, beta, o), need
 
 
 def delta_rule(q, k, v, g, beta, s0=None, *, scale: Optional[float] = None, want_state: bool = True,
@@ -680,8 +691,9 @@ def _delta_bwd_plan(q, k, v, g, beta, s0, do, ds_final, dq, dk, dv, dg, dbeta, d
         _want(name, form, like[0], like[2])
     for name, form in (("s0", s0), ("ds_final", ds_final), ("ds0", ds0)):
         _want(name, form, (B, Hv, Dk, Dv), torch.float32, True)
-    return (sizes, _rows(3, q, k, v, g, beta, do, dq, dk, dv, dg, dbeta),
-            _need(pdssm_delta_bwd_workspace_bytes(B, Hk, Hv, L, Dk, Dv, flag)))
+    need = _need(pdssm_delta_bwd_workspace_bytes(B, Hk, Hv, L, Dk, Dv, flag))
+    _one_device(q, k, v, g, beta, s0, do, ds_final, dq, dk, dv, dg, dbeta, ds0)
+    return sizes, _rows(3, q, k, v, g, beta, do, dq, dk, dv, dg, dbeta), need
 
 
 def delta_rule_bwd(q, k, v, g, beta, do, s0=None, ds_final=None, *, scale: Optional[float] = None,
@@ -719,6 +731,7 @@ def _step_plan(q, k, v, g, beta, o, s, s_out):
     _want("o", o, v[0], v[2])
     _want("s", s, (B, Hv, Dk, Dv), torch.float32, True)
     _want("s_out", s_out, (B, Hv, Dk, Dv), torch.float32, True)
+    _one_device(q, k, v, g, beta, o, s, s_out)
     return flag, B, Hk, Hv, Dk, Dv, _rows(2, q, k, v, g, beta, o)
 
 
@@ -770,6 +783,7 @@ def _norm_plan(q, k, wq, wk, cos, sin, pos, kind, pairs, q_out, k_out):
     sizes = _norm_form(q, k, wq, wk, cos, sin, pos, kind, pairs)
     _want("q_out", q_out, q[0], q[2])
     _want("k_out", k_out, k[0], k[2])
+    _one_device(q, k, wq, wk, cos, sin, pos, q_out, k_out)
     return sizes, _rows(3, q, k, q_out, k_out)
 
 
@@ -803,6 +817,7 @@ def _norm_bwd_plan(q, k, wq, wk, cos, sin, pos, kind, pairs, dq_out, dk_out, dq,
     need = 0
     if wq is not None or wk is not None:
         need = _need(pdssm_qk_norm_rope_bwd_workspace_bytes(B, Hq, Hk, L, D))
+    _one_device(q, k, wq, wk, cos, sin, pos, dq_out, dk_out, dq, dk)
     return sizes, _rows(3, q, k, dq_out, dk_out, dq, dk), need
 
 
