@@ -139,7 +139,8 @@ int pdssm_delta_step(const void *q, const void *k, const void *v, const float *g
  * Norm of every query and key head with the rotation by position (see above).
  *   q, q_out  [B,Hq,L,D]    k, k_out  [B,Hk,L,D]   (an output may be its input)
  *   wq, wk    fp32 [D], or NULL for 1
- *   cos, sin  fp32 [P,R/2] (R = 0: not read)
+ *   cos, sin  fp32 [P,R/2] (R = 0: not read), 16-byte aligned when R is a
+ *             multiple of 16
  *   pos       int32 [B,L] positions, clamped to [0,P), or NULL for pos = l
  *   strides   of q, k, q_out, k_out, or NULL
  * D in [1,256]; R even, in [0,D]; P >= 1 when R > 0; Hq and Hk up to 32768,

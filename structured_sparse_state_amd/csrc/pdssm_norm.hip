@@ -504,7 +504,9 @@ int norm_call(const NormCall &c, bool bwd, void *workspace, size_t workspace_byt
     const bool any = has[0] || has[1];
     if (any && c.R > 0 && (!c.cs || !c.sn))
         return PDSSM_ERR_NULL;
-    if (any && c.R > 0 && (((uintptr_t)c.cs | (uintptr_t)c.sn) & 15u))
+    // Rows of whole runs are read as runs, others value by value: a table's
+    // later rows are then no less aligned than needed.
+    if (any && c.R > 0 && (((uintptr_t)c.cs | (uintptr_t)c.sn) & (c.R % 16 == 0 ? 15u : 3u)))
         return PDSSM_ERR_ALIGN;
     if (any && c.pos && ((uintptr_t)c.pos & 3u))
         return PDSSM_ERR_ALIGN;

@@ -59,3 +59,12 @@ def test_workspaces():
     for bad in (ws[:63], ws[::2], torch.empty(1, dtype=torch.uint8).expand(64), ws.to("meta")):
         with pytest.raises(ValueError):
             pk._workspace(64, bad, ws.device)
+
+
+def test_alignment_of_tables():
+    """Element alignment is asked for where rows are not whole runs, 16 bytes where they are."""
+    fake = 1 << 20      # never dereferenced: both calls are refused
+    call = lambda cos, R: pk.pdssm_qk_norm_rope_fwd(  # noqa: E731
+        fake, fake, None, None, cos, fake, None, fake, fake, 2, 4, 2, 10, 64, R, 10, 1e-6, 1, None, 0)
+    assert call(fake + 2, 20) == pk.PDSSM_ERR_ALIGN
+    assert call(fake + 4, 32) == pk.PDSSM_ERR_ALIGN
