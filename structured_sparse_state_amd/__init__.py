@@ -759,9 +759,21 @@ _NORM_KIND = {"rms": 0, "l2": PDSSM_NORM_L2}
 _ROPE_PAIRS = {"half": 0, "adjacent": PDSSM_ROPE_PAIRS}
 
 
+class UnknownWord(ValueError, KeyError):
+    """A word that an argument does not have (a KeyError too, as callers may
+    have caught it by that name)."""
+    __str__ = Exception.__str__
+
+
+def _word(name: str, words: dict, word) -> int:
+    if word not in words:
+        raise UnknownWord(f"{name} must be one of {', '.join(words)}, not {word!r}")
+    return words[word]
+
+
 def _norm_form(q, k, wq, wk, cos, sin, pos, kind, pairs):
     """Flags and sizes (B, Hq, Hk, L, D, R, P) of a call."""
-    flags = _data_flag("q and k", q[2], k[2]) | _NORM_KIND[kind] | _ROPE_PAIRS[pairs]
+    flags = _data_flag("q and k", q[2], k[2]) | _word("kind", _NORM_KIND, kind) | _word("pairs", _ROPE_PAIRS, pairs)
     if len(q[0]) != 4 or len(k[0]) != 4:
         raise ValueError("q and k must be [B,H,L,D]")
     B, Hq, L, D = q[0]
@@ -771,6 +783,8 @@ def _norm_form(q, k, wq, wk, cos, sin, pos, kind, pairs):
     _want("wk", wk, (D,), torch.float32, True)
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
+    if cos is not None and len(cos[0]) != 2:
+        raise ValueError("cos and sin must be [P,R/2]")
     P, R = (0, 0) if cos is None else (cos[0][0], 2 * cos[0][1])
     _want("cos", cos, (P, R // 2), torch.float32, True)
     _want("sin", sin, (P, R // 2), torch.float32, True)

@@ -68,3 +68,15 @@ def test_alignment_of_tables():
         fake, fake, None, None, cos, fake, None, fake, fake, 2, 4, 2, 10, 64, R, 10, 1e-6, 1, None, 0)
     assert call(fake + 2, 20) == pk.PDSSM_ERR_ALIGN
     assert call(fake + 4, 32) == pk.PDSSM_ERR_ALIGN
+
+
+def test_words_and_tables_of_the_norm():
+    x, t = torch.zeros(2, 3, 5, 8), torch.zeros(9)
+    for kw in (dict(kind="max"), dict(pairs="thirds"), dict(kind=None), dict(cos=t, sin=t),
+               dict(cos=t[:8].view(2, 2, 2), sin=t[:8].view(2, 2, 2))):
+        with pytest.raises(ValueError):
+            pk.qk_norm_rope(x, x, **kw)
+        with pytest.raises(ValueError):
+            pk.qk_norm_rope_bwd(x, x, x, x, **kw)
+    with pytest.raises(ValueError, match="rms, l2"):
+        pk.qk_norm_rope(x, x, kind="max")
