@@ -16,9 +16,15 @@ import sys
 
 import torch
 import torch.nn.functional as F
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import structured_sparse_state_amd as pk  # noqa: E402
+
+
+def rows(grad):
+    """A gradient whose rows lie whole in memory (that of a sum does not)."""
+    return grad if grad.stride(-1) == 1 else grad.contiguous()
 
 
 class QkNormRope(torch.autograd.Function):
@@ -30,9 +36,10 @@ class QkNormRope(torch.autograd.Function):
         return pk.qk_norm_rope(q, k, wq, wk, cos, sin, kind="l2")
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, wq, wk, cos, sin = ctx.saved_tensors
-        return *pk.qk_norm_rope_bwd(q, k, dq_out, dk_out, wq, wk, cos, sin, kind="l2"), None, None
+        return *pk.qk_norm_rope_bwd(q, k, rows(dq_out), rows(dk_out), wq, wk, cos, sin, kind="l2"), None, None
 
 
 class DeltaRule(torch.autograd.Function):
@@ -44,8 +51,9 @@ class DeltaRule(torch.autograd.Function):
         return pk.delta_rule(q, k, v, g, beta, want_state=False)[0]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do):
-        return pk.delta_rule_bwd(*ctx.saved_tensors, do, want_ds0=False)[:5]
+        return pk.delta_rule_bwd(*ctx.saved_tensors, rows(do), want_ds0=False)[:5]
 
 
 class DeltaLayer(torch.nn.Module):
