@@ -920,13 +920,13 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
     // What this workgroup walks: chunks c0 .. c1 - 1 of 64 columns of a head's
     // state, or (kScan) of 64 columns of the segment's transition, the state
     // that the unit matrix becomes without any v.
-    // A scan leaves out what no joining asks for: the first segment's
-    // transition, the last one's end (and its transition, in the forward).
+    // A scan leaves out what no joining asks for: the last segment's end and
+    // transition, and the first one's transition.
     const int parts = a.slices + (MODE == kScan ? KD / 64 : 0);
     const int64_t head = block / (unsigned)(a.segs * parts);
     const int rest = block % (unsigned)(a.segs * parts), seg = rest / parts, slice = rest % parts;
     const bool unit = slice >= a.slices;
-    if (MODE == kScan && (unit ? seg == 0 || (seg == a.segs - 1 && !a.d_o.p) : seg == a.segs - 1))
+    if (MODE == kScan && (seg == a.segs - 1 || (unit && seg == 0)))
         return;
     const int c0 = seg * a.seg_chunks, c1 = min(a.NC, c0 + a.seg_chunks);
     int64_t b;
