@@ -41,6 +41,8 @@
 // wait for memory between their phases more than they compute.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "pdssm_device.h"
 #include "pdssm_host.h"
 #include "pdssm_layers.h"
@@ -2360,6 +2362,7 @@ struct StepArgs {
     Rows q, k, v, g, beta, o;
     const float *s;
     float *s_out;
+    int64_t blocks;         // heads x slices, over both dimensions of the grid
     int Hk, Hv, Dk, Dv, slices;
     float scale;
 };
@@ -2379,8 +2382,11 @@ __global__ void __launch_bounds__(kThreads) step_kernel(StepArgs a)
     constexpr int TY = kThreads / TX, RP = kMaxDim / TY, WY = 64 / TX;   // rows of a wave side by side
     __shared__ float s_part[4][2][TX * 4];
     __shared__ float s_qk[4];
-    const int64_t head = blockIdx.x / (unsigned)a.slices;
-    const int slice = blockIdx.x % (unsigned)a.slices;
+    const unsigned block = blockIdx.y * gridDim.x + blockIdx.x;
+    if (block >= a.blocks)
+        return;
+    const int64_t head = block / (unsigned)a.slices;
+    const int slice = block % (unsigned)a.slices;
     const int64_t b = head / a.Hv;
     const int h = (int)(head - b * a.Hv), hk = h / (a.Hv / a.Hk);
     const int tx = threadIdx.x % TX, ty = threadIdx.x / TX, wave = threadIdx.x >> 6;
@@ -2485,6 +2491,8 @@ __global__ void __launch_bounds__(kThreads) step_kernel(StepArgs a)
 // Host side.
 // ---------------------------------------------------------------------------
 constexpr int64_t kMaxL = (int64_t)1 << 30;
+// Workgroups along x: a launch has fewer than 2^32 threads in a dimension.
+constexpr int64_t kMaxGridX = (int64_t)1 << 23;
 
 int check_delta_dims(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int32_t Dk, int32_t Dv)
 {
@@ -2856,7 +2864,8 @@ extern "C" int pdssm_delta_step(const void *q, const void *k, const void *v, con
     a.q = {q, st[0]}, a.k = {k, st[1]}, a.v = {v, st[2]}, a.g = {g, st[3]}, a.beta = {beta, st[4]}, a.o = {o, st[5]};
     a.s = s, a.s_out = s_out, a.Hk = (int)Hk, a.Hv = (int)Hv, a.Dk = Dk, a.Dv = Dv, a.scale = scale;
     a.slices = (Dv + 31) / 32;
-    const dim3 grid((unsigned)(B * Hv * a.slices)), block(kThreads);
+    a.blocks = B * Hv * a.slices;       // below 2^31, by the limit on B Hv
+    const dim3 grid((unsigned)std::min(a.blocks, kMaxGridX), (unsigned)((a.blocks + kMaxGridX - 1) / kMaxGridX)), block(kThreads);
     const bool vec = Dv % 4 == 0;
     if (esize == 2) {
         if (vec)

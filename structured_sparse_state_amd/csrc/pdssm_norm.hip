@@ -438,7 +438,9 @@ Plan plan_of(int64_t B, int64_t Hq, int64_t Hk, int64_t L, int32_t D, bool bwd)
     p.segs[0] = (Hq + p.hp - 1) / p.hp;
     p.segs[1] = (Hk + p.hp - 1) / p.hp;
     const int64_t groups = kThreads / p.lph, segs = p.segs[0] + p.segs[1];
+    // (a launch has fewer than 2^32 threads; the groups take items in turn)
     p.blocks = (B * L * (bwd ? 1 : segs) + groups - 1) / groups;
+    p.blocks = p.blocks < 1 << 23 ? p.blocks : 1 << 23;
     if (bwd && segs > 0) {
         const int64_t most = (kBwdGroups + segs - 1) / segs;
         p.blocks = p.blocks < most ? p.blocks : most;

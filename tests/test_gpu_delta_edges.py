@@ -98,3 +98,18 @@ def test_cut_sequences(B, Hk, Hv, L, Dk, Dv, order, gates, s0):
     x = inputs(L, B, Hk, Hv, L, Dk, Dv, torch.bfloat16, order=order, gates=gates, s0=s0)
     assert cut(B, Hk, Hv, L, Dk, Dv)
     check(x, f"cut B={B} Hk={Hk} Hv={Hv} L={L} Dk={Dk} Dv={Dv} {order} {gates}")
+
+
+def test_step_of_more_heads_than_one_grid_dimension_holds():
+    """2^24 states and some, more than 2^32 threads in one row of workgroups."""
+    B = (1 << 24) + 70
+    gen = torch.Generator(device="cuda:0").manual_seed(51)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda:0")  # noqa: E731
+    q, k, v, s = r(B, 1, 1), r(B, 1, 1), r(B, 1, 1), r(B, 1, 1, 1)
+    g, beta = -r(B, 1).abs(), torch.sigmoid(r(B, 1))
+    say("[case] step, 2^24 states")
+    S = s.double() * g.double().exp()[..., None, None]
+    S = S + (k * beta[..., None]).double()[..., None] * (v.double() - k.double() * S[..., 0])[..., None]
+    o = pk.delta_step(q, k, v, g, beta, s)
+    torch.cuda.synchronize()
+    assert off(s, S.cpu()) <= TOL_F32 and off(o, (q.double() * S[..., 0]).cpu()) <= TOL_F32
