@@ -60,6 +60,7 @@ constexpr int kMaxDim = 128;
 constexpr int kBlocks = 10;
 constexpr int kBlock = 256;     // values of a block
 __host__ __device__ constexpr int block_of(int a, int b) { return a * (a + 1) / 2 + b; }
+__host__ __device__ constexpr int row_of(int t) { return t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0; }
 
 // What prep_kernel leaves for a chunk, in floats.  In row format a block's
 // lane (g, i) holds row i, columns 4 g + 0..3; in column format column i,
@@ -598,7 +599,7 @@ struct Tri {
             const int x = tid + i * NT;
             if (x < kBlocks * 64) {
                 const int t = x >> 6, lane = x & 63;
-                const int ta = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, tb = t - ta * (ta + 1) / 2;
+                const int ta = row_of(t), tb = t - block_of(ta, 0);
                 const int row = TRANS ? tb : ta, col = TRANS ? ta : tb;
                 uint16_t *p = lds + ((frag(row, col >> 1) * 3) * 64 + lane) * 8 + 4 * (col & 1);
                 float v[4] = {u[i][0], u[i][1], u[i][2], u[i][3]};
@@ -2061,15 +2062,14 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// grads_kernel: grad_kernel for bf16 data, eight waves.  u~, w and dO of the
-// chunk go through LDS once (u~ in three parts, w in two: dg and dbeta need
-// u~'s 24 bits, dQ and dK are rounded to 8), each row's dot products falling
-// out on the way; a wave forms one or two 16 x 16 blocks of X and Y, then the
-// 16 key dimensions it owns (with 64 of them: half of the rows each), reading
-// the state and its gradient straight into the product's layout, two k steps
-// ahead.  330 us for 4096 chunks of 128 x 128 (3.3 TB/s of 1.09 GB): its 160 KB
-// of LDS leave one workgroup to a compute unit, so loads and products of a
-// chunk do not overlap with another's.
+// grads_kernel: grad_kernel for bf16 data, eight waves.  u~, w (three parts
+// each) and dO of the chunk go through LDS once, each row's dot products falling
+// out on the way; a wave takes the 16 key dimensions it owns (with 64 of them:
+// half of the rows each), reading the state and its gradient straight into the
+// product's layout, two k steps ahead, then one or two 16 x 16 blocks of X and
+// Y, whose three parts take the place of u~ and w.  359 to 391 us for 4096 chunks of
+// 128 x 128 (2.8 to 3.0 TB/s of 1.09 GB): its 158 KB of LDS leave one workgroup to a compute
+// unit, so loads and products of a chunk do not overlap with another's.
 // ---------------------------------------------------------------------------
 constexpr int kGradThreads = 512;
 
@@ -2077,22 +2077,38 @@ template <int KD, int KV>
 struct GradLds {
     using K = Tile<KD, true, kGradThreads>;
     using V = Tile<KV, true, kGradThreads>;     // one part of 64 rows of KV values
-    using M = Tile<kC, true, kGradThreads>;
+    using M = Tile<kC, false, kGradThreads>;    // X or Y, three parts
     static constexpr int kWaves = kGradThreads / 64;
     // in uint16_t
     static constexpr int kQ = K::kSize;
     static constexpr int kU = kQ + K::kSize;
     static constexpr int kW = kU + 3 * V::kPart;
-    static constexpr int kO = kW + 2 * V::kPart;
-    static constexpr int kX = kO + V::kPart;
+    static constexpr int kO = kW + 3 * V::kPart;
+    static constexpr int kX = kU;               // once u~ and w have been read
     static constexpr int kY = kX + M::kSize;
-    static constexpr int kVec = kY + M::kSize;
+    static_assert(kY + M::kSize <= kO, "X and Y take the place of u~ and w");
+    static constexpr int kVec = kO + V::kPart;
     static constexpr int kRows = kVec + 2 * kVecs * kC;         // [KD / 16][64]: q . (dO S^T)
     static constexpr int kBlk = kRows + 2 * (KD / 16) * kC;     // [10][16]: sums of dP . P
     static constexpr int kVdv = kBlk + 2 * kBlocks * 16;        // [64]: v . dv
     static constexpr int kSum = kVdv + 2 * kC;                  // [waves]
     static constexpr size_t kBytes = (kSum + 2 * kWaves) * 2;
 };
+
+// Four values of a column, three parts, into rows p, p + M::kRow, ...
+template <typename M>
+__device__ __forceinline__ void put_rows(uint16_t *p, f32x4 v)
+{
+    float x[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int n = 0; n < 3; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; r += 2) {
+            const uint32_t w = take_part(x[r], x[r + 1], n < 2);
+            p[n * M::kPart + r * M::kRow] = (uint16_t)w;
+            p[n * M::kPart + (r + 1) * M::kRow] = (uint16_t)(w >> 16);
+        }
+}
 
 template <int KD, int KV, bool VEC>
 __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
@@ -2152,12 +2168,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
         TK tk, tq;
         tk.load(Chunk<true, VEC>(a.k.p, b * a.k.s.b + hk * a.k.s.h, a.k.s.l, t0, a.L, a.Dk), tid);
         tq.load(Chunk<true, VEC>(a.q.p, b * a.q.s.b + hk * a.q.s.h, a.q.s.l, t0, a.L, a.Dk), tid);
-        // the blocks right of the diagonal that share a k step with it
-        if (tid < 128) {
-            const int row = (tid >> 6) * 32 + ((tid >> 2) & 15), col = (tid >> 6) * 32 + 16 + (tid & 3) * 4;
-            *reinterpret_cast<uint2 *>(s_x + row * M::kRow + col) = make_uint2(0, 0);
-            *reinterpret_cast<uint2 *>(s_y + row * M::kRow + col) = make_uint2(0, 0);
-        }
         tk.store(s_k, tid);
         tq.store(s_q, tid);
     }
@@ -2179,7 +2189,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
             const int x = tid + i * kGradThreads, row = x / (KV / 8), col = x % (KV / 8) * 8;
             const int p = row * TV::kRow + col;
             put_parts<3>(s_u + p, TV::kPart, u[i]);
-            put_parts<2>(s_w + p, TV::kPart, ww[i]);
+            put_parts<3>(s_w + p, TV::kPart, ww[i]);
             *reinterpret_cast<uint4 *>(s_o + p) = o[i].v;
             float uw = dot8(u[i], ww[i], 0.f), vw = dot8(unit_values<true>(v[i]), ww[i], 0.f);
             if constexpr (KV == 128) {      // a row's units are a group of 16 lanes, or of 8
@@ -2201,51 +2211,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
         }
         lds_barrier();
 
-        // Blocks of X and Y.
-        for (int t = wave; t < kBlocks; t += LDS::kWaves) {
-            const int ta = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, tb = t - ta * (ta + 1) / 2;
-            const f32x4 P = *reinterpret_cast<const f32x4 *>(rec + Record::kP + t * kBlock + 4 * lane);
-            f32x4 dp = {0.f, 0.f, 0.f, 0.f}, dn = dp;
-#pragma unroll
-            for (int s = 0; s < KV / 32; ++s) {
-                if (32 * s >= a.DV)
-                    break;
-                const int pa = (16 * ta + i16) * TV::kRow + 32 * s + 8 * g, pb = (16 * tb + i16) * TV::kRow + 32 * s + 8 * g;
-                Frag<1> fo;
-                Frag<2> fw;
-                Frag<3> fu;
-                fo.p[0] = lds_row8(s_o + pa);
-#pragma unroll
-                for (int n = 0; n < 3; ++n)
-                    fu.p[n] = lds_row8(s_u + n * TV::kPart + pb);
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-                    fw.p[n] = lds_row8(s_w + n * TV::kPart + pa);
-                dp = mma<3>(fo, fu, dp);
-                dn = mma<2>(fw, fu, dn);
-            }
-            const int jc = 16 * tb + i16;
-            const float bj = s_vec[kBeta * kC + jc];
-            const float hj = s_vec[kGhi * kC + jc], lj = s_vec[kGlo * kC + jc], nj = s_vec[kResets * kC + jc];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int ic = 16 * ta + 4 * g + r;
-                const float d = bj * decay_of(s_vec[kGhi * kC + ic], s_vec[kGlo * kC + ic], s_vec[kResets * kC + ic], hj, lj, nj);
-                const float od = sum16(dp[r] * bj * P[r]);
-                if (i16 == 0)
-                    s_blk[t * 16 + 4 * g + r] = od;
-                // one part each: their 2^-9 beside the results' own
-                s_x[ic * M::kRow + jc] = f32_to_bf16_rne(jc <= ic ? a.scale * dp[r] * d : 0.f);
-                s_y[ic * M::kRow + jc] = f32_to_bf16_rne(jc < ic ? -dn[r] * s_vec[kBeta * kC + ic] * d : 0.f);
-            }
-        }
-
         // The wave's key dimensions.
         f32x4 e[NT], f[NT], k2[NT];     // dO S^T, w S^T, u~ dS^T
         float ss = 0.f, kds = 0.f;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
             e[t] = f[t] = k2[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        // (Places in LDS from a number of this turn, or those of all phases are
+        // formed ahead of the loop over j and held in registers that spill.)
+        const int at = opaque(i16 * TV::kRow + 8 * g);
+        const int qk_at = opaque((4 * g + (i16 >> 2)) * TK::kRow + 16 * tile + 4 * (i16 & 3));
 #pragma unroll
         for (int s = 0; s < KV / 32; ++s) {
             if (32 * s >= a.DV)
@@ -2257,19 +2232,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
                 fetch_state(j, s + 2);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const int p = (16 * (first + t) + i16) * TV::kRow + 32 * s + 8 * g;
+                const int p = at + 16 * (first + t) * TV::kRow + 32 * s;
                 Frag<1> fo;
-                Frag<2> fw;
+                Frag<3> fw;
                 Frag<3> fu;
                 fo.p[0] = lds_row8(s_o + p);
 #pragma unroll
                 for (int n = 0; n < 3; ++n)
                     fu.p[n] = lds_row8(s_u + n * TV::kPart + p);
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < 3; ++n)
                     fw.p[n] = lds_row8(s_w + n * TV::kPart + p);
                 e[t] = mma<3>(fo, fs, e[t]);
-                f[t] = mma<2>(fw, fs, f[t]);
+                f[t] = mma<3>(fw, fs, f[t]);
                 k2[t] = mma<3>(fu, fd, k2[t]);
             }
         }
@@ -2279,7 +2254,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
             const f32x4 rise = row_vec(s_vec, kRise, first + t, lane), beta = row_vec(s_vec, kBeta, first + t, lane);
             e[t] *= a.scale * rise;
             k2[t] *= beta * row_vec(s_vec, kLeft, first + t, lane);
-            const int p = (row + (i16 >> 2)) * TK::kRow + 16 * tile + 4 * (i16 & 3);
+            const int p = qk_at + 16 * (first + t) * TK::kRow;
             const f32x4 qv = __builtin_convertvector(lds_column4(s_q + p), f32x4);
             const f32x4 kv = __builtin_convertvector(lds_column4(s_k + p), f32x4);
 #pragma unroll
@@ -2298,21 +2273,81 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
             ss += __shfl_xor(ss, m, 64);
         if (lane == 0)
             s_sum[wave] = ss;
+        // Blocks of X and Y: one of the ten for each wave, a second for two of
+        // them; after the key dimensions, whose sums hold more registers.
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4 x[2], y[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int t = wave + n * LDS::kWaves;
+            if (t >= kBlocks)
+                break;
+            const int ta = row_of(t), tb = t - block_of(ta, 0);
+            const f32x4 P = *reinterpret_cast<const f32x4 *>(rec + Record::kP + t * kBlock + 4 * lane);
+            f32x4 dp = {0.f, 0.f, 0.f, 0.f}, dn = dp;
+            for (int d0 = 0; d0 < a.DV; d0 += 32) {
+                const int pa = at + 16 * ta * TV::kRow + d0, pb = at + 16 * tb * TV::kRow + d0;
+                Frag<1> fo;
+                Frag<3> fw, fu;
+                fo.p[0] = lds_row8(s_o + pa);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    fu.p[i] = lds_row8(s_u + i * TV::kPart + pb);
+                    fw.p[i] = lds_row8(s_w + i * TV::kPart + pa);
+                }
+                dp = mma<3>(fo, fu, dp);
+                dn = mma<3>(fw, fu, dn);
+            }
+            const int jc = 16 * tb + i16;
+            const float bj = s_vec[kBeta * kC + jc];
+            const float hj = s_vec[kGhi * kC + jc], lj = s_vec[kGlo * kC + jc], nj = s_vec[kResets * kC + jc];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int ic = 16 * ta + 4 * g + r;
+                const float d = bj * decay_of(s_vec[kGhi * kC + ic], s_vec[kGlo * kC + ic], s_vec[kResets * kC + ic], hj, lj, nj);
+                const float od = sum16(dp[r] * bj * P[r]);
+                if (i16 == 0)
+                    s_blk[t * 16 + 4 * g + r] = od;
+                x[n][r] = jc <= ic ? a.scale * dp[r] * d : 0.f;
+                y[n][r] = jc < ic ? -dn[r] * s_vec[kBeta * kC + ic] * d : 0.f;
+            }
+        }
+        lds_barrier();      // u~, w and dO have been read
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int t = wave + n * LDS::kWaves;
+            if (t >= kBlocks)
+                break;
+            const int ta = row_of(t), tb = t - block_of(ta, 0);
+            const int p = (16 * ta + 4 * g) * M::kRow + 16 * tb + i16;
+            put_rows<M>(s_x + p, x[n]);
+            put_rows<M>(s_y + p, y[n]);
+        }
+        // the blocks right of the diagonal that share a k step with it
+        if (tid < 128) {
+            const int p = ((tid >> 6) * 32 + ((tid >> 2) & 15)) * M::kRow + (tid >> 6) * 32 + 16 + (tid & 3) * 4;
+#pragma unroll
+            for (int n = 0; n < 3; ++n) {
+                *reinterpret_cast<uint2 *>(s_x + n * M::kPart + p) = make_uint2(0, 0);
+                *reinterpret_cast<uint2 *>(s_y + n * M::kPart + p) = make_uint2(0, 0);
+            }
+        }
         lds_barrier();
 
+        const int ln = opaque(lane);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const Frag<1> fk = TK::columns(s_k, tile, s, lane), fq = TK::columns(s_q, tile, s, lane);
+            const Frag<1> fk = TK::columns(s_k, tile, s, ln), fq = TK::columns(s_q, tile, s, ln);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const int ta = first + t;
                 if (s <= ta / 2) {
-                    dq[t] = mma<1>(M::rows(s_x, ta, s, lane), fk, dq[t]);
-                    dk[t] = mma<1>(M::rows(s_y, ta, s, lane), fk, dk[t]);
+                    dq[t] = mma<3>(M::rows(s_x, ta, s, ln), fk, dq[t]);
+                    dk[t] = mma<3>(M::rows(s_y, ta, s, ln), fk, dk[t]);
                 }
                 if (s >= ta / 2) {
-                    dk[t] = mma<1>(M::columns(s_x, ta, s, lane), fq, dk[t]);
-                    dk[t] = mma<1>(M::columns(s_y, ta, s, lane), fk, dk[t]);
+                    dk[t] = mma<3>(M::columns(s_x, ta, s, ln), fq, dk[t]);
+                    dk[t] = mma<3>(M::columns(s_y, ta, s, ln), fk, dk[t]);
                 }
             }
         }

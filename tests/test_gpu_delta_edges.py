@@ -113,3 +113,23 @@ def test_step_of_more_heads_than_one_grid_dimension_holds():
     o = pk.delta_step(q, k, v, g, beta, s)
     torch.cuda.synchronize()
     assert off(s, S.cpu()) <= TOL_F32 and off(o, (q.double() * S[..., 0]).cpu()) <= TOL_F32
+
+
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (128, 128), (40, 72)])
+def test_bf16_results_are_rounded_once(Dk, Dv):
+    """Results of fp32 accuracy rounded to bf16 differ from the reference
+    rounded to bf16 only where a value lies next to the middle of two: an error
+    of d moves a value by an ulp in d / ulp of the cases, so the norm of the
+    difference is about the root of |d| |ulp|, for the 2e-5 of fp32 results
+    and 2^-7 the root of 1.6e-7: 4e-4, below 2^-11."""
+    x = inputs(61, 2, 2, 4, 200, Dk, Dv, torch.bfloat16)
+    say(f"[case] rounded once, Dk={Dk} Dv={Dv}")
+    args = [x[n] for n in STEPS]
+    want_o, _, _ = ref.delta(*args, x["s0"])
+    grads, _ = ref.delta_bwd(*args, x["do"], x["s0"], x["ds"])
+    got = [pk.delta_rule(*args, x["s0"])[0], *pk.delta_rule_bwd(*args, x["do"], x["s0"], x["ds"])[:3]]
+    torch.cuda.synchronize()
+    for name, a, b in zip(("o", "dq", "dk", "dv"), got, (want_o, *grads)):
+        apart = float((a.double().cpu() - b.to(torch.bfloat16).double()).norm() / b.norm())
+        say(f"  {name} {apart:.2e}")
+        assert apart <= 2.0 ** -11, name
