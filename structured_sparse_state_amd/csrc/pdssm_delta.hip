@@ -18,9 +18,14 @@
 //     X = lower part of (dO u^T . decay) scale,  Y = -strictly lower (dV u^T . decay)
 //     dQ = X K + scale rise dO S^T
 //     dK = X^T Q + (Y + Y^T) K + left u dS^T - rise dV S^T
-//     dg_t = <S_after, dS_after> + sum over the chunk's s >= t of (q_s . dq_s - v_s . dv_s)
-// The last line holds because scaling every later product with the state by
-// e^g_t is the same as scaling S: the gradient of g_t is <S, dS> around it.
+//     dg_t = sum over what crosses step t: <whole S, dS>,
+//            q_i . (scale rise dO S^T)_i - k_i . (rise dV S^T)_i   for i >= t,
+//            k_j . (left u dS^T)_j                                 for j < t,
+//            P_ij dP_ij + N_ij dN_ij                               for j < t <= i
+// with dP = dO u^T and dN = -dV u^T: e^g_t is a factor of exactly these terms.
+// (Shorter forms, as sums of q . dq - v . dv from t on, hold the terms that do
+// not cross t twice with unlike signs: under strong decays dg is a small rest
+// of them and loses its bits.)
 //
 // Kernels.  prep_kernel makes Z, P and the gates' vectors of every chunk, all
 // chunks side by side.  The walks take the chunks of a head in order: a wave
@@ -1821,6 +1826,87 @@ __device__ __forceinline__ float sum16(float v)
     return add_rotated<1>(add_rotated<2>(add_rotated<4>(add_rotated<8>(v))));
 }
 
+// The parts of dg that lie inside a chunk, from M = P . dP + N . dN (strictly
+// below the diagonal): its sum over rows i >= t and columns j < t, for every t.
+// Sixteen vectors of 16 values: the row sums and the column sums of the six
+// blocks below the diagonal ones, and the diagonal blocks' own sums.
+struct Cuts {
+    static constexpr int kSize = 16 * 16;
+    static __device__ __forceinline__ int below(int ta, int tb) { return ta * (ta - 1) / 2 + tb; }
+
+    // Block (ta, tb), lane: column lane % 16, rows 4 g + r.
+    static __device__ __forceinline__ void put(float *cuts, int ta, int tb, f32x4 m, int lane)
+    {
+        const int g = lane >> 4, i16 = lane & 15;
+        float col[4];               // sums over the rows from 4 g + r on
+        col[3] = m[3], col[2] = m[2] + col[3], col[1] = m[1] + col[2], col[0] = m[0] + col[1];
+        float rest = col[0];        // over the rows of all lanes from this one on
+#pragma unroll
+        for (int n = 16; n <= 32; n <<= 1) {
+            const float x = __shfl_down(rest, n, 64);
+            rest += lane + n < 64 ? x : 0.f;
+        }
+        if (ta == tb) {
+            float later = __shfl_down(rest, 16, 64);
+            later = g < 3 ? later : 0.f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float v = sum16(i16 < 4 * g + r ? later + col[r] : 0.f);
+                if (i16 == 0)
+                    cuts[(12 + ta) * 16 + 4 * g + r] = v;
+            }
+        } else {
+            if (g == 0)
+                cuts[(6 + below(ta, tb)) * 16 + i16] = rest;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float v = sum16(m[r]);
+                if (i16 == 0)
+                    cuts[below(ta, tb) * 16 + 4 * g + r] = v;
+            }
+        }
+    }
+
+    // Of step t = lane (one wave).
+    static __device__ __forceinline__ float get(const float *cuts, int lane)
+    {
+        const int T = lane >> 4, l = lane & 15;
+        float rows = 0.f, cols = 0.f, far = 0.f;
+#pragma unroll
+        for (int ta = 1; ta < 4; ++ta)
+#pragma unroll
+            for (int tb = 0; tb < ta; ++tb) {
+                const float row = cuts[below(ta, tb) * 16 + l];
+                rows += ta == T ? row : 0.f;
+                cols += tb == T ? cuts[(6 + below(ta, tb)) * 16 + l] : 0.f;
+                far += tb < T && T < ta ? row : 0.f;
+            }
+#pragma unroll
+        for (int n = 1; n < 16; n <<= 1) {
+            const float x = __shfl_down(rows, n, 16), y = __shfl_up(cols, n, 16);
+            rows += l + n < 16 ? x : 0.f;
+            cols += l >= n ? y : 0.f;
+        }
+        const float before = __shfl_up(cols, 1, 16);
+        return cuts[(12 + T) * 16 + l] + rows + (l ? before : 0.f) + sum16(far);
+    }
+};
+
+// dg of step t = lane of a chunk (one wave), from the chunk's whole <S, dS>, what
+// the lane's step adds as a reader of S and as a writer of the state behind
+// the chunk, and the parts inside it.
+__device__ __forceinline__ float crossing(float whole, float reads, float writes, const float *cuts, int lane)
+{
+#pragma unroll
+    for (int n = 1; n < 64; n <<= 1) {
+        const float x = __shfl_down(reads, n, 64), y = __shfl_up(writes, n, 64);
+        reads += lane + n < 64 ? x : 0.f;
+        writes += lane >= n ? y : 0.f;
+    }
+    const float before = __shfl_up(writes, 1, 64);
+    return whole + reads + (lane ? before : 0.f) + Cuts::get(cuts, lane);
+}
+
 template <int KD, bool VEC>
 __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
 {
@@ -1837,8 +1923,11 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
     uint16_t *s_x = s_q + T::kSize;
     uint16_t *s_y = s_x + M::kSize;
     float *s_vec = reinterpret_cast<float *>(s_y + M::kSize);         // the record's vectors
-    float *s_rows = s_vec + kVecs * kC;                               // [5][64]: row sums of q . dq by wave, and X's
-    float *s_sum = s_rows + 5 * kC;                                   // [4]: <S, dS> and k . (u dS^T) by wave
+    float *s_reads = s_vec + kVecs * kC;                              // [4][64]: what the steps read of S, by wave
+    float *s_cuts = s_reads + 4 * kC;
+    float *s_sum = s_cuts + Cuts::kSize;                              // [4]: <S, dS> by wave
+    // [64][4]: what the steps write, by wave, in the padding of k's first part
+    auto s_writes = [&](int row) { return reinterpret_cast<float *>(s_k + row * T::kRow + KD); };
 
     const int64_t chunk = blockIdx.x % (unsigned)a.NC, bk = blockIdx.x / (unsigned)a.NC;
     const int c = (int)chunk;
@@ -1868,27 +1957,27 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
         const float *ut = a.ut + at * kC * a.DV, *w = a.w + at * kC * a.DV;
         const float *S = a.states + at * KD * a.DV, *dS = a.grads + at * KD * a.DV;
         const Chunk<BF16, VEC> cdo(a.d_o.p, b * a.d_o.s.b + h * a.d_o.s.h, a.d_o.s.l, t0, a.L, a.Dv);
-        const Chunk<BF16, VEC> cv(a.v.p, b * a.v.s.b + h * a.v.s.h, a.v.s.l, t0, a.L, a.Dv);
 
         for (int x = threadIdx.x; x < kVecs * kC; x += kThreads)
             s_vec[x] = rec[Record::kVec + x];
         __syncthreads();
 
-        // Row tile `wave` of X and Y; rows' sums.
+        // Row tile `wave` of X and Y; rows' sums.  (Places in LDS from numbers
+        // of this turn, or those of all phases are formed ahead of the loop over
+        // j and held in registers that spill.)
         {
+            const int ln = opaque(lane), x_at = opaque((16 * wave + 4 * g) * M::kRow + i16);
             const int row = 16 * wave + i16, t = t0 + row;
             f32x4 dp[4], dn[4];
 #pragma unroll
             for (int tb = 0; tb < 4; ++tb)
                 dp[tb] = dn[tb] = f32x4{0.f, 0.f, 0.f, 0.f};
-            float uw = 0.f, vw = 0.f;
+            float uw = 0.f;
             for (int d0 = 0; d0 < a.DV; d0 += 32) {
                 const int col = d0 + 8 * g;
                 const Frag<NK> fo = unit_frag<BF16>(cdo.unit(row, col));
                 const f32x8 wv = load8(w + row * a.DV + col);
                 const Frag<NO> fw = split<NO>(wv);
-                const f32x8 vv = unit_values<BF16>(cv.unit(row, col));
-                vw = dot8(vv, wv, vw);
 #pragma unroll
                 for (int tb = 0; tb < 4; ++tb) {
                     if (tb > wave)
@@ -1903,18 +1992,18 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
             }
             uw += __shfl_xor(uw, 16, 64);
             uw += __shfl_xor(uw, 32, 64);
-            vw += __shfl_xor(vw, 16, 64);
-            vw += __shfl_xor(vw, 32, 64);
             if (g == 0 && t < a.L)
                 static_cast<float *>(const_cast<void *>(a.dbeta.p))[b * a.dbeta.s.b + h * a.dbeta.s.h + t * a.dbeta.s.l] = uw;
-            const float v_dv = vw * s_vec[kBeta * kC + row];
             // X, Y in rows 16 wave + 4 g + r, columns 16 tb + i16
-            f32x4 od = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int tb = 0; tb < 4; ++tb) {
                 const int jc = 16 * tb + i16;
                 f32x4 xx = {0.f, 0.f, 0.f, 0.f}, yy = xx;
                 if (tb <= wave) {
+                    f32x4 kk = {0.f, 0.f, 0.f, 0.f}, m = kk;
+#pragma unroll
+                    for (int s = 0; s < KD / 32; ++s)
+                        kk = mma<3>(T::rows(s_k, wave, s, ln), T::rows(s_k, tb, s, ln), kk);
                     const float bj = s_vec[kBeta * kC + jc];
                     const f32x4 P = *reinterpret_cast<const f32x4 *>(rec + Record::kP + block_of(wave, tb) * kBlock + 4 * lane);
 #pragma unroll
@@ -1922,16 +2011,17 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
                         const int ic = 16 * wave + 4 * g + r;
                         const float d = decay_of(s_vec[kGhi * kC + ic], s_vec[kGlo * kC + ic], s_vec[kResets * kC + ic],
                                                  s_vec[kGhi * kC + jc], s_vec[kGlo * kC + jc], s_vec[kResets * kC + jc]) * bj;
-                        od[r] += dp[tb][r] * bj * P[r];
                         xx[r] = jc <= ic ? a.scale * dp[tb][r] * d : 0.f;
                         yy[r] = jc < ic ? -dn[tb][r] * s_vec[kBeta * kC + ic] * d : 0.f;
+                        m[r] = jc < ic ? dp[tb][r] * bj * P[r] + yy[r] * kk[r] : 0.f;
                     }
+                    Cuts::put(s_cuts, wave, tb, m, ln);
                 }
 #pragma unroll
                 for (int n = 0; n < NM; ++n) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int p = n * M::kPart + (16 * wave + 4 * g + r) * M::kRow + jc;
+                        const int p = x_at + n * M::kPart + r * M::kRow + 16 * tb;
                         const uint16_t hx = f32_to_bf16_rne(xx[r]), hy = f32_to_bf16_rne(yy[r]);
                         s_x[p] = hx;
                         s_y[p] = hy;
@@ -1940,24 +2030,16 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
                     }
                 }
             }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float v = sum16(od[r]);
-                if (i16 == 0)
-                    s_rows[4 * kC + 16 * wave + 4 * g + r] = v;
-            }
-            lds_order();
-            if (g == 0)
-                s_rows[4 * kC + row] -= v_dv;
         }
         __syncthreads();
 
         // The wave's key dimensions.
-        f32x4 qdq[4];
-        float ss = 0.f, kds = 0.f;
+        const int ln = opaque(lane), row4 = opaque(4 * g);
+        f32x4 reads[4], writes[4];
+        float ss = 0.f;
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-            qdq[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            reads[t] = writes[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int n = 0; n < NTC; ++n) {
             const int tile = wave * NTC + n, dim = 16 * tile + i16;
@@ -1983,39 +2065,40 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
             for (int t = 0; t < 4; ++t) {
                 const f32x4 rise = row_vec(s_vec, kRise, t, lane), beta = row_vec(s_vec, kBeta, t, lane);
                 e[t] *= a.scale * rise;
+                f[t] *= beta * rise;
                 k2[t] *= beta * row_vec(s_vec, kLeft, t, lane);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int p = (16 * t + 4 * g + r) * T::kRow + dim;
+                    const int p = (16 * t + row4 + r) * T::kRow + dim;
                     float qv = 0.f, kv = 0.f;
 #pragma unroll
                     for (int m = NK - 1; m >= 0; --m) {
                         qv += bf16_lo(s_q[m * T::kPart + p]);
                         kv += bf16_lo(s_k[m * T::kPart + p]);
                     }
-                    qdq[t][r] += qv * e[t][r];
-                    kds += kv * k2[t][r];
+                    reads[t][r] += qv * e[t][r] - kv * f[t][r];
+                    writes[t][r] += kv * k2[t][r];
                 }
                 dq[t][n] += e[t];
-                dk[t][n] += k2[t] - beta * rise * f[t];
+                dk[t][n] += k2[t] - f[t];
             }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const Frag<NK> fk = T::columns(s_k, tile, s, lane), fq = T::columns(s_q, tile, s, lane);
+                const Frag<NK> fk = T::columns(s_k, tile, s, ln), fq = T::columns(s_q, tile, s, ln);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     if (s <= t / 2) {
-                        dq[t][n] = mma<3>(M::rows(s_x, t, s, lane), fk, dq[t][n]);
-                        dk[t][n] = mma<3>(M::rows(s_y, t, s, lane), fk, dk[t][n]);
+                        dq[t][n] = mma<3>(M::rows(s_x, t, s, ln), fk, dq[t][n]);
+                        dk[t][n] = mma<3>(M::rows(s_y, t, s, ln), fk, dk[t][n]);
                     }
                     if (s >= t / 2) {
-                        dk[t][n] = mma<3>(M::columns(s_x, t, s, lane), fq, dk[t][n]);
-                        dk[t][n] = mma<3>(M::columns(s_y, t, s, lane), fk, dk[t][n]);
+                        dk[t][n] = mma<3>(M::columns(s_x, t, s, ln), fq, dk[t][n]);
+                        dk[t][n] = mma<3>(M::columns(s_y, t, s, ln), fk, dk[t][n]);
                     }
                 }
             }
         }
-        ss = ss * s_vec[kWhole * kC] + kds;
+        ss *= s_vec[kWhole * kC];
 #pragma unroll
         for (int m = 32; m >= 1; m >>= 1)
             ss += __shfl_xor(ss, m, 64);
@@ -2025,23 +2108,21 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const float v = sum16(qdq[t][r]);
-                if (i16 == 0)
-                    s_rows[wave * kC + 16 * t + 4 * g + r] = v;
+                const float x = sum16(reads[t][r]), y = sum16(writes[t][r]);
+                const int row = 16 * t + row4 + r;
+                if (i16 == 0) {
+                    s_reads[wave * kC + row] = x;
+                    s_writes(row)[wave] = y;
+                }
             }
         __syncthreads();
         if (wave == 0) {
-            float v = s_rows[4 * kC + lane];
+            const float *w = s_writes(lane);
+            float reads = 0.f;
 #pragma unroll
             for (int m = 0; m < 4; ++m)
-                v += s_rows[m * kC + lane];
-#pragma unroll
-            for (int m = 1; m < 64; m <<= 1) {
-                const float x = __shfl_down(v, m, 64);
-                if (lane + m < 64)
-                    v += x;
-            }
-            v += s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+                reads += s_reads[m * kC + lane];
+            const float v = crossing(s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3], reads, w[0] + w[1] + w[2] + w[3], s_cuts, lane);
             // the decay of an empty state does nothing
             const bool empty = s_vec[kResets * kC + lane] != (lane ? s_vec[kResets * kC + lane - 1] : 0.f) ||
                                (t0 + lane == 0 && !a.s0);
@@ -2068,7 +2149,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
 // half of the rows each), reading the state and its gradient straight into the
 // product's layout, two k steps ahead, then one or two 16 x 16 blocks of X and
 // Y, whose three parts take the place of u~ and w.  359 to 391 us for 4096 chunks of
-// 128 x 128 (2.8 to 3.0 TB/s of 1.09 GB): its 158 KB of LDS leave one workgroup to a compute
+// 128 x 128 (2.8 to 3.0 TB/s of 1.06 GB): its 158 KB of LDS leave one workgroup to a compute
 // unit, so loads and products of a chunk do not overlap with another's.
 // ---------------------------------------------------------------------------
 constexpr int kGradThreads = 512;
@@ -2088,10 +2169,10 @@ struct GradLds {
     static constexpr int kY = kX + M::kSize;
     static_assert(kY + M::kSize <= kO, "X and Y take the place of u~ and w");
     static constexpr int kVec = kO + V::kPart;
-    static constexpr int kRows = kVec + 2 * kVecs * kC;         // [KD / 16][64]: q . (dO S^T)
-    static constexpr int kBlk = kRows + 2 * (KD / 16) * kC;     // [10][16]: sums of dP . P
-    static constexpr int kVdv = kBlk + 2 * kBlocks * 16;        // [64]: v . dv
-    static constexpr int kSum = kVdv + 2 * kC;                  // [waves]
+    static constexpr int kReads = kVec + 2 * kVecs * kC;        // [KD / 16][64]: what the steps read of S
+    static constexpr int kWrites = kReads + 2 * (KD / 16) * kC; // [KD / 16][64]: and write behind the chunk
+    static constexpr int kCuts = kWrites + 2 * (KD / 16) * kC;
+    static constexpr int kSum = kCuts + 2 * Cuts::kSize;        // [waves]: <S, dS>
     static constexpr size_t kBytes = (kSum + 2 * kWaves) * 2;
 };
 
@@ -2123,8 +2204,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
     uint16_t *lds = reinterpret_cast<uint16_t *>(s_dyn);
     uint16_t *s_k = lds, *s_q = lds + LDS::kQ, *s_u = lds + LDS::kU, *s_w = lds + LDS::kW, *s_o = lds + LDS::kO;
     uint16_t *s_x = lds + LDS::kX, *s_y = lds + LDS::kY;
-    float *s_vec = reinterpret_cast<float *>(lds + LDS::kVec), *s_rows = reinterpret_cast<float *>(lds + LDS::kRows);
-    float *s_blk = reinterpret_cast<float *>(lds + LDS::kBlk), *s_vdv = reinterpret_cast<float *>(lds + LDS::kVdv);
+    float *s_vec = reinterpret_cast<float *>(lds + LDS::kVec), *s_cuts = reinterpret_cast<float *>(lds + LDS::kCuts);
+    float *s_reads = reinterpret_cast<float *>(lds + LDS::kReads), *s_writes = reinterpret_cast<float *>(lds + LDS::kWrites);
     float *s_sum = reinterpret_cast<float *>(lds + LDS::kSum);
 
     const int c = (int)(blockIdx.x % (unsigned)a.NC);
@@ -2133,18 +2214,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, i16 = lane & 15;
     const int tile = wave % kTiles, first = wave / kTiles * NT, dim = 16 * tile + i16;
 
-    // What a value head adds: its units of u~, w, dO, V, and the state and
-    // its gradient in the layout of the products.
+    // What a value head adds: its units of u~, w, dO, and the state and its
+    // gradient in the layout of the products.
     f32x8 u[kUnits], ww[kUnits], sv[2], dv[2];      // two k steps of the states at a time
-    Unit<true> o[kUnits], v[kUnits];
-    float beta[kUnits], vecs;
+    Unit<true> o[kUnits];
+    float vecs;
     auto fetch = [&](int j) {
         const int h = hk * group + j;
         const int64_t at = (b * a.Hv + h) * a.NC + c;
         const float *rec = a.records + at * a.record;
         const float *ut = a.ut + at * kC * a.DV, *w = a.w + at * kC * a.DV;
         const Chunk<true, VEC> cdo(a.d_o.p, b * a.d_o.s.b + h * a.d_o.s.h, a.d_o.s.l, t0, a.L, a.Dv);
-        const Chunk<true, VEC> cv(a.v.p, b * a.v.s.b + h * a.v.s.h, a.v.s.l, t0, a.L, a.Dv);
         const f32x8 zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
@@ -2153,8 +2233,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
             u[i] = col < a.DV ? load8(ut + at8) : zero;
             ww[i] = col < a.DV ? load8(w + at8) : zero;
             o[i] = cdo.unit(row, col);
-            v[i] = cv.unit(row, col);
-            beta[i] = rec[Record::kVec + kBeta * kC + row];
         }
         vecs = rec[Record::kVec + min(tid, kVecs * kC - 1)];
     };
@@ -2191,35 +2269,30 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
             put_parts<3>(s_u + p, TV::kPart, u[i]);
             put_parts<3>(s_w + p, TV::kPart, ww[i]);
             *reinterpret_cast<uint4 *>(s_o + p) = o[i].v;
-            float uw = dot8(u[i], ww[i], 0.f), vw = dot8(unit_values<true>(v[i]), ww[i], 0.f);
+            float uw = dot8(u[i], ww[i], 0.f);
             if constexpr (KV == 128) {      // a row's units are a group of 16 lanes, or of 8
                 uw = sum16(uw);
-                vw = sum16(vw);
             } else {
 #pragma unroll
-                for (int m = 4; m >= 1; m >>= 1) {
+                for (int m = 4; m >= 1; m >>= 1)
                     uw += __shfl_xor(uw, m, 64);
-                    vw += __shfl_xor(vw, m, 64);
-                }
             }
-            if (col == 0) {
-                s_vdv[row] = vw * beta[i];
-                if (t0 + row < a.L)
-                    static_cast<float *>(const_cast<void *>(a.dbeta.p))[b * a.dbeta.s.b + h * a.dbeta.s.h +
-                                                                        (t0 + row) * a.dbeta.s.l] = uw;
-            }
+            if (col == 0 && t0 + row < a.L)
+                static_cast<float *>(const_cast<void *>(a.dbeta.p))[b * a.dbeta.s.b + h * a.dbeta.s.h +
+                                                                    (t0 + row) * a.dbeta.s.l] = uw;
         }
         lds_barrier();
 
         // The wave's key dimensions.
         f32x4 e[NT], f[NT], k2[NT];     // dO S^T, w S^T, u~ dS^T
-        float ss = 0.f, kds = 0.f;
+        float ss = 0.f;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
             e[t] = f[t] = k2[t] = f32x4{0.f, 0.f, 0.f, 0.f};
         // (Places in LDS from a number of this turn, or those of all phases are
         // formed ahead of the loop over j and held in registers that spill.)
         const int at = opaque(i16 * TV::kRow + 8 * g);
+        const int row_at = opaque(tile * kC + 16 * first + 4 * g);
         const int qk_at = opaque((4 * g + (i16 >> 2)) * TK::kRow + 16 * tile + 4 * (i16 & 3));
 #pragma unroll
         for (int s = 0; s < KV / 32; ++s) {
@@ -2250,24 +2323,25 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const int row = 16 * (first + t) + 4 * g;
             const f32x4 rise = row_vec(s_vec, kRise, first + t, lane), beta = row_vec(s_vec, kBeta, first + t, lane);
             e[t] *= a.scale * rise;
+            f[t] *= beta * rise;
             k2[t] *= beta * row_vec(s_vec, kLeft, first + t, lane);
             const int p = qk_at + 16 * (first + t) * TK::kRow;
             const f32x4 qv = __builtin_convertvector(lds_column4(s_q + p), f32x4);
             const f32x4 kv = __builtin_convertvector(lds_column4(s_k + p), f32x4);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                kds += kv[r] * k2[t][r];
-                const float x = sum16(qv[r] * e[t][r]);
-                if (i16 == 0)
-                    s_rows[tile * kC + row + r] = x;
+                const float x = sum16(qv[r] * e[t][r] - kv[r] * f[t][r]), y = sum16(kv[r] * k2[t][r]);
+                if (i16 == 0) {
+                    s_reads[row_at + 16 * t + r] = x;
+                    s_writes[row_at + 16 * t + r] = y;
+                }
             }
             dq[t] += e[t];
-            dk[t] += k2[t] - beta * rise * f[t];
+            dk[t] += k2[t] - f[t];
         }
-        ss = ss * s_vec[kWhole * kC] + kds;
+        ss *= s_vec[kWhole * kC];
 #pragma unroll
         for (int m = 32; m >= 1; m >>= 1)
             ss += __shfl_xor(ss, m, 64);
@@ -2276,6 +2350,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
         // Blocks of X and Y: one of the ten for each wave, a second for two of
         // them; after the key dimensions, whose sums hold more registers.
         __builtin_amdgcn_sched_barrier(0);
+        const int ln = opaque(lane);
         f32x4 x[2], y[2];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
@@ -2298,6 +2373,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
                 dp = mma<3>(fo, fu, dp);
                 dn = mma<3>(fw, fu, dn);
             }
+            f32x4 kk = {0.f, 0.f, 0.f, 0.f}, m;
+#pragma unroll
+            for (int s = 0; s < KD / 32; ++s)
+                kk = mma<1>(TK::rows(s_k, ta, s, ln), TK::rows(s_k, tb, s, ln), kk);
             const int jc = 16 * tb + i16;
             const float bj = s_vec[kBeta * kC + jc];
             const float hj = s_vec[kGhi * kC + jc], lj = s_vec[kGlo * kC + jc], nj = s_vec[kResets * kC + jc];
@@ -2305,12 +2384,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
             for (int r = 0; r < 4; ++r) {
                 const int ic = 16 * ta + 4 * g + r;
                 const float d = bj * decay_of(s_vec[kGhi * kC + ic], s_vec[kGlo * kC + ic], s_vec[kResets * kC + ic], hj, lj, nj);
-                const float od = sum16(dp[r] * bj * P[r]);
-                if (i16 == 0)
-                    s_blk[t * 16 + 4 * g + r] = od;
                 x[n][r] = jc <= ic ? a.scale * dp[r] * d : 0.f;
                 y[n][r] = jc < ic ? -dn[r] * s_vec[kBeta * kC + ic] * d : 0.f;
+                m[r] = jc < ic ? dp[r] * bj * P[r] + y[n][r] * kk[r] : 0.f;
             }
+            Cuts::put(s_cuts, ta, tb, m, lane);
         }
         lds_barrier();      // u~, w and dO have been read
 #pragma unroll
@@ -2334,7 +2412,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
         }
         lds_barrier();
 
-        const int ln = opaque(lane);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const Frag<1> fk = TK::columns(s_k, tile, s, ln), fq = TK::columns(s_q, tile, s, ln);
@@ -2352,20 +2429,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(DeltaArgs a)
             }
         }
         if (wave == 0) {
-            float v = -s_vdv[lane];
-            for (int m = 0; m < kTiles; ++m)
-                v += s_rows[m * kC + lane];
-            const int ta = lane >> 4;
-            for (int tb = 0; tb <= ta; ++tb)
-                v += s_blk[block_of(ta, tb) * 16 + (lane & 15)];
-#pragma unroll
-            for (int m = 1; m < 64; m <<= 1) {
-                const float x = __shfl_down(v, m, 64);
-                if (lane + m < 64)
-                    v += x;
+            float reads = 0.f, writes = 0.f, whole = 0.f;
+            for (int m = 0; m < kTiles; ++m) {
+                reads += s_reads[m * kC + lane];
+                writes += s_writes[m * kC + lane];
             }
             for (int m = 0; m < LDS::kWaves; ++m)
-                v += s_sum[m];
+                whole += s_sum[m];
+            const float v = crossing(whole, reads, writes, s_cuts, lane);
             // the decay of an empty state does nothing
             const bool empty = s_vec[kResets * kC + lane] != (lane ? s_vec[kResets * kC + lane - 1] : 0.f) ||
                                (t0 + lane == 0 && !a.s0);
@@ -2667,7 +2738,7 @@ constexpr size_t chain_lds(bool outputs)
 template <int KD>
 constexpr size_t grad_lds()
 {
-    return (size_t)(2 * Tile<KD, false>::kSize + 2 * Tile<kC, false>::kSize) * 2 + (kVecs * kC + 5 * kC + 4) * 4;
+    return (size_t)(2 * Tile<KD, false>::kSize + 2 * Tile<kC, false>::kSize) * 2 + (kVecs * kC + 4 * kC + Cuts::kSize + 4) * 4;
 }
 
 template <int KD, bool BF16, bool VEC>

@@ -133,3 +133,42 @@ def test_bf16_results_are_rounded_once(Dk, Dv):
         apart = float((a.double().cpu() - b.to(torch.bfloat16).double()).norm() / b.norm())
         say(f"  {name} {apart:.2e}")
         assert apart <= 2.0 ** -11, name
+
+
+def sizes_of_dg(x):
+    """|S| |dS| around every step's decay, whose product dg is, in 64 bits."""
+    group = x["v"].shape[1] // x["q"].shape[1]
+    _, _, states = ref.delta(*(x[n] for n in STEPS), x["s0"])
+    q, k = (x[n].double().cpu().repeat_interleave(group, 1) for n in "qk")
+    g, beta, do = (x[n].double().cpu() for n in ("g", "beta", "do"))
+    dS = torch.zeros_like(states[0]) if x["ds"] is None else x["ds"].double().cpu()
+    out = torch.zeros_like(g)
+    for t in reversed(range(q.shape[2])):
+        a, kt = g[:, :, t].exp()[..., None, None], k[:, :, t, :, None]
+        dS = dS + q.shape[-1] ** -0.5 * q[:, :, t, :, None] * do[:, :, t, None, :]
+        dS = dS - kt * (beta[:, :, t, None] * (kt * dS).sum(-2))[..., None, :]
+        out[:, :, t] = (states[t] * a).norm(dim=(-2, -1)) * dS.norm(dim=(-2, -1))
+        dS = dS * a
+    return out
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("Dk,Dv,Hk", [(48, 40, 2), (128, 128, 1), (64, 100, 1)])
+@pytest.mark.parametrize("gates", [-0.2, -2.0, -10.0, -20.0, "mixed"])
+def test_every_gradient_of_a_gate(dtype, gates, Dk, Dv, Hk):
+    """dg step by step.  It is <S, dS>, both known to TOL_F32 of their norms, as
+    a sum over pairs of steps that may cancel among themselves by the root of
+    64: 16 * TOL_F32 of |S| |dS|, which strong decays make small.  (Parts below
+    fp32's normal numbers again have no 24 bits.)"""
+    x = inputs(71, 1, Hk, 2, 150, Dk, Dv, TYPES[dtype])
+    noise = x["g"]      # -0.2 |normal|
+    x["g"] = noise + gates if gates != "mixed" else torch.where(noise < -0.2, 100 * noise, noise)
+    say(f"[case] dg, {dtype}, gates {gates}, Dk={Dk} Dv={Dv}")
+    args = [x[n] for n in STEPS]
+    want = ref.delta_bwd(*args, x["do"], x["s0"], x["ds"])[0][3]
+    got = pk.delta_rule_bwd(*args, x["do"], x["s0"], x["ds"])[3].double().cpu()
+    size = sizes_of_dg(x)
+    torch.cuda.synchronize()
+    e = ((got - want).abs() - 2.0 ** -126) / size
+    say(f"  worst {float(e.max()):.2e} median {float(((got - want).abs() / want.abs()).median()):.2e}")
+    assert (want.abs() <= size * (1 + 1e-9)).all() and (e <= 16 * TOL_F32).all()
