@@ -27,8 +27,7 @@
  * else fp32.  Gates, states, weights, tables, and their gradients are fp32.
  * Arithmetic is fp32 or its equal (a product of fp32 values on the matrix
  * cores is taken as the sum of bf16 parts that together hold all 24 bits),
- * with one rounding to nearest even into a bf16 output; terms of
- * pdssm_delta_fwd's bf16 o alone carry 16 bits.  Results are bitwise
+ * with one rounding to nearest even into a bf16 output.  Results are bitwise
  * reproducible.
  * A NaN or an infinity among the inputs of a step spoils that sequence from
  * the first of the step's 64 steps on (in pdssm_delta_bwd up to its end).

@@ -884,12 +884,13 @@ __global__ void __launch_bounds__(kThreads) chain_kernel(DeltaArgs a)
 // waits for: u from S, then S.  Waves 4..11 ("help") stage the next chunk's K,
 // V, Z and vectors in the other half of LDS, and form the outputs of the chunk
 // before: two of them share the columns of a chain wave, whose S and u they
-// get in two bf16 parts through LDS (16 bits: they add 2^-17 to an output's
-// own 2^-9).  One barrier a chunk; a flag says when the parts of S are there.
-// The LM layer's walk takes 205 to 231 us, 3.4 us a chunk on every compute unit: the
+// get as fp32 through LDS and split again (the chain's own three parts of S do
+// not fit for keys of 128).  One barrier a chunk; a flag says when S is there.
+// The LM layer's walk takes 227 to 288 us, 3.5 us a chunk on every compute unit: the
 // chain alone needs 2.4 us (84 products of 16 cycles, 370 other instructions,
 // reads from LDS between them), the help waves' loads, products and stores on
-// the same four SIMDs the rest.
+// the same four SIMDs the rest.  (S, u and P in two parts for the outputs, whose
+// terms then hold 16 bits: 203 to 247 us.)
 // ---------------------------------------------------------------------------
 enum Mode { kOut, kKeep, kScan };   // outputs; states and u~ kept; the last state alone
 
@@ -900,8 +901,8 @@ struct PipeLds {
     using K = Tile<KD, true, kHelpThreads>;
     using V = Tile<kC, true, kHelpThreads>;
     using Z = Tri<false, kHelpThreads>;
-    static constexpr int kSRow = KD + 8, kURow = kC + 4;
-    static constexpr int kSPart = 16 * kSRow, kUPart = 16 * kURow;
+    static constexpr int kSRow = KD + 4, kURow = kC + 4;    // S and u: fp32, a wave's columns as rows
+    static constexpr int kSWave = 16 * kSRow, kUWave = 16 * kURow;
     // in uint16_t
     static constexpr int kK = 0;
     static constexpr int kZ = kK + 2 * K::kSize;
@@ -909,8 +910,8 @@ struct PipeLds {
     static constexpr int kVec = kV + 2 * V::kSize;
     static constexpr int kFlag = kVec + 2 * 4 * kC * 2;
     static constexpr int kS = kFlag + 8;                    // with outputs only
-    static constexpr int kU = kS + 4 * 2 * kSPart;
-    static constexpr size_t bytes(bool out) { return (out ? kU + 2 * 4 * 2 * kUPart : kS) * 2; }
+    static constexpr int kU = kS + 2 * 4 * kSWave;
+    static constexpr size_t bytes(bool out) { return (out ? kU + 2 * 2 * 4 * kUWave : kS) * 2; }
 };
 
 template <int KD, bool VEC, int MODE>
@@ -976,15 +977,10 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
                 for (int t = 0; t < 4; ++t)
                     kr[s][t] = TK::rows_stacked(s_k, t, s, lane);
             if constexpr (MODE == kOut) {
-                uint16_t *x = lds + LDS::kS + mine * 2 * LDS::kSPart + i16 * LDS::kSRow + 4 * g;
+                float *x = reinterpret_cast<float *>(lds + LDS::kS) + mine * LDS::kSWave + i16 * LDS::kSRow + 4 * g;
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int s = 0; s < NS; ++s) {
-                        const bf16x8 v = sf[s].p[n];
-                        *reinterpret_cast<bf16x4 *>(x + n * LDS::kSPart + 32 * s) = __builtin_shufflevector(v, v, 0, 1, 2, 3);
-                        *reinterpret_cast<bf16x4 *>(x + n * LDS::kSPart + 32 * s + 16) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
-                    }
+                for (int m = 0; m < KD / 16; ++m)
+                    *reinterpret_cast<f32x4 *>(x + 16 * m) = S.s[m];
                 if (lane == 0)
                     LdsFlag::set(&s_flag[mine], c + 1);
             }
@@ -1067,15 +1063,10 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
                 u[t] *= row_vec(s_vec, kBeta, t, lane);
             }
             if constexpr (MODE == kOut) {
-                uint16_t *y = lds + LDS::kU + ((half * 4 + mine) * 2) * LDS::kUPart + i16 * LDS::kURow + 4 * g;
+                float *y = reinterpret_cast<float *>(lds + LDS::kU) + (half * 4 + mine) * LDS::kUWave + i16 * LDS::kURow + 4 * g;
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    float v[4] = {u[t][0], u[t][1], u[t][2], u[t][3]};
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-                        *reinterpret_cast<uint2 *>(y + n * LDS::kUPart + 16 * t) =
-                            make_uint2(take_part(v[0], v[1], n < 1), take_part(v[2], v[3], n < 1));
-                }
+                for (int t = 0; t < 4; ++t)
+                    *reinterpret_cast<f32x4 *>(y + 16 * t) = u[t];
             }
             const float whole = s_vec[kWhole * kC];
             Frag<3> w0, w1;
@@ -1159,17 +1150,16 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
             }
         };
         auto output = [&](int c) {     // from qs, pf and the u of chunk c
-            const uint16_t *y = lds + LDS::kU + ((((c - c0) & 1) * 4 + mine) * 2) * LDS::kUPart + i16 * LDS::kURow + 4 * g;
+            const float *y = reinterpret_cast<const float *>(lds + LDS::kU) + (((c - c0) & 1) * 4 + mine) * LDS::kUWave +
+                             i16 * LDS::kURow + 4 * g;
             const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-            Frag<2> f[2];
+            Frag<3> f[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-                    f[s].p[n] = lds_rows4(y + n * LDS::kUPart + 32 * s, y + n * LDS::kUPart + 32 * s + 16);
-            qs[0] = mma<2>(split<2>(pf[0], part ? pf[1] : zero), f[0], qs[0]);
-            qs[1] = mma<2>(split<2>(pf[2], pf[3]), f[0], qs[1]);
-            qs[1] = mma<2>(split<2>(pf[4], part ? zero : pf[5]), f[1], qs[1]);
+                f[s] = split<3>(*reinterpret_cast<const f32x4 *>(y + 32 * s), *reinterpret_cast<const f32x4 *>(y + 32 * s + 16));
+            qs[0] = mma<3>(split<3>(pf[0], part ? pf[1] : zero), f[0], qs[0]);
+            qs[1] = mma<3>(split<3>(pf[2], pf[3]), f[0], qs[1]);
+            qs[1] = mma<3>(split<3>(pf[4], part ? zero : pf[5]), f[1], qs[1]);
             const Chunk<true, VEC> co(a.o.p, b * a.o.s.b + h * a.o.s.h, a.o.s.l, max(c, c0) * kC, a.L, a.Dv, c < c0);
             store_cols(co, col, lane, ta, qs[0]);
             store_cols(co, col, lane, tb, qs[1]);
@@ -1195,17 +1185,16 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
                 output(c - 1);
                 fetch_p(c);
                 LdsFlag::await(&s_flag[mine], c + 1);
-                const uint16_t *x = lds + LDS::kS + mine * 2 * LDS::kSPart + i16 * LDS::kSRow + 8 * g;
+                const float *x = reinterpret_cast<const float *>(lds + LDS::kS) + mine * LDS::kSWave + i16 * LDS::kSRow + 8 * g;
                 qs[0] = qs[1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int s = 0; s < NS; ++s) {
-                    const bf16x8 hi = lds_row8(x + 32 * s), lo = lds_row8(x + LDS::kSPart + 32 * s);
+                    const Frag<3> f = split<3>(load8(x + 32 * s));
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        qs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(unit_frag<true>(qf[s][t]).p[0], lo, qs[t], 0, 0, 0);
+                    for (int n = 2; n >= 0; --n)
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        qs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(unit_frag<true>(qf[s][t]).p[0], hi, qs[t], 0, 0, 0);
+                        for (int t = 0; t < 2; ++t)
+                            qs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(unit_frag<true>(qf[s][t]).p[0], f.p[n], qs[t], 0, 0, 0);
                 }
                 const float *s_vec = reinterpret_cast<const float *>(lds + LDS::kVec) + half * 4 * kC;
                 qs[0] *= a.scale * row_vec(s_vec, kRise, ta, lane);
