@@ -1097,8 +1097,8 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
             S.store(a.s_final + head * a.Dk * a.Dv, a.Dk, a.Dv, col, lane);
     } else {
         // The help waves have more to do than the chain and share its SIMDs:
-        // going first they cut the LM layer's walk from 285 to 236 us (the
-        // chain going first: 279).
+        // going first they cut the LM layer's forward from 405 to 380 us (the
+        // chain going first: 404).
         __builtin_amdgcn_s_setprio(2);
         const int tid = threadIdx.x - 256;
         const int64_t ek = b * a.k.s.b + hk * a.k.s.h, eq = b * a.q.s.b + hk * a.q.s.h;
@@ -1382,9 +1382,8 @@ __device__ __forceinline__ void back_walk(const DeltaArgs &a, unsigned block)
         else if (a.ds0 && seg == 0)
             S.store(a.ds0 + head * a.Dk * a.Dv, a.Dk, a.Dv, col, lane);
     } else {
-        // The help waves have more to do than the chain and share its SIMDs:
-        // going first they cut the LM layer's walk from 285 to 236 us (the
-        // chain going first: 279).
+        // As in the walk forward, but worth less here: the LM layer's backward
+        // takes 807 us, without it 817, with the chain going first 821.
         __builtin_amdgcn_s_setprio(2);
         const int tid = threadIdx.x - 256;
         const int64_t ek = b * a.k.s.b + hk * a.k.s.h, eq = b * a.q.s.b + hk * a.q.s.h;
@@ -2606,19 +2605,21 @@ int padded_value(int Dv) { return (Dv + 31) / 32 * 32; }
 
 int slices_of(int Dv) { return (Dv + 63) / 64; }
 
-// How many segments the chunks of a head are cut into.  A chunk of a walk
-// takes 2.3 us (keys of 64) or 3.3 us (128) whether one or all 256 compute
-// units walk; G segments divide that time by G, but walk twice (once without
-// outputs) and are joined one after another, about 1.8 or 3.5 us each, so G is
-// near the root of NC times the ratio, and no more than fills the device.  Keys
-// of 128 with 3/2 of the root measured slower (4 heads, 16384 steps: 195 against
-// 169 us; 8 heads, 4096 steps: 107 against 92).
-// Forward, in us, as one and cut: 8 heads of 64, 1024 steps 51 and 42, 16384
-// steps 618 and 143; 8 heads of 128, 1024 steps 68 and 53, 16384 steps 879
-// and 227; 32 heads of 128 (64 walks), 4096 steps 244 and 196.  Measured with a
-// join of 6.5 us a segment: those 32 heads, 1024 steps 72 and 79 (not cut); the
-// backward, which has two walks for each and gains up to half as many, 16 heads
-// of 128, 4096 steps 359 and 319; 32 heads 498 and 554 (not cut).
+// How many segments the chunks of a head are cut into.  A chunk of a forward
+// walk takes 2.7 us (keys of 64) or 4.0 us (128) with few walks, 3.5 and 4.7 us
+// with one on every compute unit; G segments divide that time by G, but walk twice
+// (once without outputs) and are joined one after another, about 1.8 or 3.5 us
+// each, so G is near the root of NC times the ratio, and no more than fills the
+// device.
+// In us, as one and cut.  Forward: 8 heads of 64, 512 steps 34 and 37 (not
+// cut), 1024 steps 57 and 42, 16384 steps 721 and 146; 8 heads of 128, 1024 steps 78
+// and 57, 16384 steps 1046 and 247; 32 heads of 128 (64 walks), 1024 steps 82 and 77
+// to 87 (not cut), 2048 steps 151 and 119, 4096 steps 288 and 200; 64 heads of 128 (128
+// walks), 4096 steps 319 and 369 (not cut).  Backward, two walks for each: 8 heads
+// of 64, 1024 steps 77 and 65; 16 heads of 128 (64 walks), 1024 steps 103 and 104 (not cut),
+// 4096 steps 372 and 336; 32 heads of 128, 4096 steps 553 and 579 (not cut).
+// The factor: 8 heads of 64, 4096 steps with the root 72 us, 3/2 of it 67,
+// twice 68; of 128 with the root 99, 3/2 113.
 struct Cut {
     int segs, chunks;
 };

@@ -17,7 +17,8 @@
 //
 // 8 x 4096 tokens of 40 heads of 128 in bf16: 127 us forward (5.3 TB/s; a copy
 // of the same bytes takes 124 us) and 213 + 7 us backward (4.6 TB/s; the sum of two
-// tensors into a third 168 us), whose registers leave two waves to a SIMD.
+// tensors into a third 168 us), whose registers leave two waves to a SIMD; in
+// fp32 242 us (5.5 TB/s) and 484 us (4.2 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "pdssm_device.h"
@@ -416,10 +417,11 @@ bool runs(const void *p, const pdssm_strides &s, int esize)
 
 // Heads a lane takes of one token.  Four spare the loads of weights, cosines
 // and sines and keep more rows in flight; with few rows, one keeps more of the
-// device busy.  Heads of 128, in us, one head and four: forward 20480 rows 5.0
-// and 5.4, 65520 rows 9.6 and 8.1, 1.3 million rows 164 and 127; backward (more
-// registers) 65520 rows 16.9 and 19.0, 327680 rows 39.7 and 44.8, 1.3 million
-// rows 176 and 169.
+// device busy.  40 heads of 128 a token, bf16, a whole call in us with one head
+// and four: forward (R = 128) 20480 rows 4.7 and 5.1, 65520 rows 9.3 and 7.6,
+// 327680 rows 32.6 and 31.5, 1.3 million rows 165 and 125; backward (R = 64, adjacent
+// pairs, more registers) 65520 rows 18.0 and 20.3, 327680 rows 48.4 and 52.0,
+// 1.3 million rows 235 and 219.  fp32, 1.3 million rows: 246 and 242, 497 and 484.
 int heads_per_lane(int64_t rows, bool bwd) { return rows > (bwd ? 1 << 19 : 1 << 15) ? 4 : 1; }
 
 struct Plan {
