@@ -198,14 +198,6 @@ struct Chunk {
         else
             return bload<uint32_t>(r, at(lane, row, up, col), 0);
     }
-    // Eight values of lane row + up (VEC, bf16).
-    __device__ __forceinline__ void put8(uint32_t lane, int up, bf16x8 v) const
-    {
-        typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-        u32x4 w;
-        __builtin_memcpy(&w, &v, 16);
-        __builtin_amdgcn_raw_buffer_store_b128(w, r, lane + up * stride, 0, 0);
-    }
     __device__ __forceinline__ void put(uint32_t lane, int row, int up, int col, float v) const
     {
         if constexpr (BF16)
@@ -224,18 +216,6 @@ __device__ __forceinline__ Frag<BF16 ? 1 : 3> unit_frag(const Unit<BF16> &u)
         return f;
     } else {
         return split<3>(u.v);
-    }
-}
-
-template <bool BF16>
-__device__ __forceinline__ f32x8 unit_values(const Unit<BF16> &u)
-{
-    if constexpr (BF16) {
-        bf16x8 h;
-        __builtin_memcpy(&h, &u.v, 16);
-        return __builtin_convertvector(h, f32x8);
-    } else {
-        return u.v;
     }
 }
 

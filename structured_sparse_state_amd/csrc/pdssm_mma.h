@@ -4,8 +4,7 @@
 // product of two fp32 matrices is the sum of the products of their parts;
 // the terms of order i + j <= 2 hold it to about 2^-24, and six bf16
 // products (three when one side is bf16 by nature) still run 2.7 times
-// (5.3 times) the rate of the fp32 matrix instruction.  Order <= 1 (two parts
-// each) holds 16 bits, for results that are rounded to bf16 anyway.
+// (5.3 times) the rate of the fp32 matrix instruction.
 //
 // Lane layouts of the 16 x 16 x 32 product (g = lane / 16, i = lane % 16):
 //   A: row i, k = 8 g + 0..7      B: column i, k = 8 g + 0..7
