@@ -29,8 +29,10 @@
  * cores is taken as the sum of bf16 parts that together hold all 24 bits),
  * with one rounding to nearest even into a bf16 output.  Results are bitwise
  * reproducible.
- * A NaN or an infinity among the inputs of a step spoils that sequence from
- * the first of the step's 64 steps on (in pdssm_delta_bwd up to its end).
+ * A NaN or an infinity among the inputs of a step of pdssm_delta_fwd spoils
+ * its heads' outputs from that step on and their state (in v, its column's
+ * alone; in q, that step's outputs alone), and no output before; in
+ * pdssm_delta_bwd it may spoil all gradients of its sequence.
  *
  * Layouts: device pointers.  q, k, v, o, g, beta and the like are indexed
  * [B,H,L(,D)] with the last dimension contiguous and the strides of the

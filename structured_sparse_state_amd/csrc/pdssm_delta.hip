@@ -335,6 +335,48 @@ __device__ __forceinline__ float decay_of(float hi_i, float lo_i, float n_i, flo
     return n_i == n_j ? __builtin_amdgcn_exp2f((hi_i - hi_j) + (lo_i - lo_j)) : 0.f;
 }
 
+__device__ __forceinline__ bool finite(float v) { return __builtin_fabsf(v) <= __FLT_MAX__; }
+
+// A NaN or an infinity in a column of 64 steps (C layout, the column's rows over
+// the lanes of i16): it would reach the steps before it through the zeros of
+// the triangular matrices, so R and beta R of the steps from the first such one
+// on become zero, and their results NaN.
+struct Spoiled {
+    int from = kC;      // the first such step of the lane's column, kC: none
+
+    __device__ __forceinline__ void take_out(f32x4 (&R)[4], f32x4 (&x)[4], int g)
+    {
+        float mark = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                mark = __builtin_fmaf(x[t][r], 0.f, mark);
+        if (__any(mark != 0.f)) {
+#pragma unroll
+            for (int t = 3; t >= 0; --t)
+#pragma unroll
+                for (int r = 3; r >= 0; --r)
+                    from = finite(x[t][r]) ? from : 16 * t + 4 * g + r;
+            from = min(from, __shfl_xor(from, 16, 64));
+            from = min(from, __shfl_xor(from, 32, 64));
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                put(R[t], t, g, from, 0.f);
+                put(x[t], t, g, from, 0.f);
+            }
+        }
+    }
+    // v in the place of a tile's steps from `from` on.
+    static __device__ __forceinline__ void put(f32x4 &x, int tile, int g, int from, float v)
+    {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            x[r] = 16 * tile + 4 * g + r < from ? x[r] : v;
+    }
+    __device__ __forceinline__ float whole(float v) const { return from < kC ? __builtin_nanf("") : v; }
+};
+
 __device__ __forceinline__ int64_t kv_head(const DeltaArgs &a, int64_t head, int64_t &b, int &h)
 {
     b = head / a.Hv;
@@ -363,6 +405,7 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
     static_assert(kMatrix * 4 <= T::kSize * 4, "Z takes the place of k and q");
     __shared__ __attribute__((aligned(16))) char s_mem[T::kSize * 4 + kMatrix * 4];
     __shared__ float s_hi[kC], s_lo[kC], s_n[kC], s_beta[kC];
+    __shared__ int s_odd[kC];
     uint16_t *s_k = reinterpret_cast<uint16_t *>(s_mem);
     uint16_t *s_q = reinterpret_cast<uint16_t *>(s_mem + T::kSize * 2);
     float *s_z = reinterpret_cast<float *>(s_mem);      // after N and P, in the place of k and q
@@ -376,6 +419,7 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
     const int t0 = c * kC, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int g = lane >> 4, i16 = lane & 15;
     float *rec = a.records + (int64_t)blockIdx.x * a.record;
+    float rise = 0.f;   // of step t0 + lane (wave 0)
 
     {
         T q, k;
@@ -407,11 +451,11 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
             s_hi[lane] = hi;
             s_lo[lane] = lo;
             s_n[lane] = n;
-            s_beta[lane] = bt;
+            s_beta[lane] = finite(bt) ? bt : 0.f;
+            rise = finite(bt) ? decay_of(hi, lo, n, 0.f, 0.f, 0.f) : __builtin_nanf("");
             float *vec = rec + Record::kVec;
-            vec[kRise * kC + lane] = decay_of(hi, lo, n, 0.f, 0.f, 0.f);
+            vec[kBeta * kC + lane] = BWD ? bt : s_beta[lane];
             vec[kLeft * kC + lane] = decay_of(hi1, lo1, n1, hi, lo, n);
-            vec[kBeta * kC + lane] = bt;
             vec[kWhole * kC + lane] = decay_of(hi1, lo1, n1, 0.f, 0.f, 0.f);
             vec[kGhi * kC + lane] = hi;
             vec[kGlo * kC + lane] = lo;
@@ -433,6 +477,7 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
         }
         const int row = 16 * wave + i16;
         const float hi = s_hi[row], lo = s_lo[row], n = s_n[row];
+        int odd = 0;
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
             if (tb > wave)
@@ -450,6 +495,8 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
                 const int col = 16 * tb + 4 * g + r;
                 const float d = decay_of(hi, lo, n, s_hi[col], s_lo[col], s_n[col]);
                 nn[r] = col < row ? kk[r] * d : 0.f;
+                odd |= !finite(nn[r]);
+                nn[r] = finite(nn[r]) ? nn[r] : 0.f;
                 if constexpr (BWD) {
                     const int pi = 16 * wave + 4 * g + r, pj = 16 * tb + i16;
                     const float e = decay_of(s_hi[pi], s_lo[pi], s_n[pi], s_hi[pj], s_lo[pj], s_n[pj]);
@@ -461,8 +508,16 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(DeltaArgs a)
             *reinterpret_cast<f32x4 *>(s_N + lds_block(wave, tb) + i16 * kMat + 4 * g) = nn;
             *reinterpret_cast<f32x4 *>(rec + Record::kP + block_of(wave, tb) * kBlock + 4 * lane) = pp;
         }
+        odd |= __shfl_xor(odd, 16, 64);
+        odd |= __shfl_xor(odd, 32, 64);
+        if (g == 0)
+            s_odd[row] = odd;
     }
     __syncthreads();    // N whole; q's place is free for Z
+    // What is not finite stays out of Z, whose products would carry it, times
+    // zero, to the steps before; its own step is spoiled through rise.
+    if (wave == 0)
+        rec[Record::kVec + kRise * kC + lane] = s_odd[lane] ? __builtin_nanf("") : rise;
 
     // Diagonal block `wave`, a column in each lane, four rows at a time: what
     // the rows above take from all four, then the four among themselves.
@@ -808,6 +863,9 @@ __global__ void __launch_bounds__(kThreads) chain_kernel(DeltaArgs a)
             x[t] = row_vec(s_vec, kBeta, t, lane) * R[t];
             u[t] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
+        Spoiled bad;
+        if constexpr (!KEEP)
+            bad.take_out(R, x, lane >> 4);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const Frag<3> f = split<3>(x[2 * s], x[2 * s + 1]);
@@ -837,10 +895,12 @@ __global__ void __launch_bounds__(kThreads) chain_kernel(DeltaArgs a)
                         o[t] = mma<NO>(L_::template get<NO>(s_p, t, s, lane), f, o[t]);
             }
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < 4; ++t) {
+                Spoiled::put(o[t], t, lane >> 4, bad.from, __builtin_nanf(""));
                 store_cols(Chunk<BF16, VEC>(a.o.p, b * a.o.s.b + h * a.o.s.h, a.o.s.l, c * kC, a.L, a.Dv), col, lane, t, o[t]);
+            }
         }
-        const float whole = s_vec[kWhole * kC];
+        const float whole = bad.whole(s_vec[kWhole * kC]);
 #pragma unroll
         for (int m = 0; m < KD / 16; ++m)
             S.s[m] *= whole;
@@ -889,13 +949,14 @@ struct PipeLds {
     static constexpr int kV = kZ + 2 * Z::kSize;
     static constexpr int kVec = kV + 2 * V::kSize;
     static constexpr int kFlag = kVec + 2 * 4 * kC * 2;
-    static constexpr int kS = kFlag + 8;                    // with outputs only
+    static constexpr int kS = kFlag + 16;                   // with outputs only
     static constexpr int kU = kS + 2 * 4 * kSWave;
-    static constexpr size_t bytes(bool out) { return (out ? kU + 2 * 2 * 4 * kUWave : kS) * 2; }
+    static constexpr int kFrom = kU + 2 * 2 * 4 * kUWave;   // [2][4 waves][16 columns]: the first spoiled step
+    static constexpr size_t bytes(bool out) { return (out ? kFrom + 2 * 2 * 4 * 16 : kS) * 2; }
 };
 
-template <int KD, bool VEC, int MODE>
-__device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
+template <int KD, bool VEC, int MODE, bool CAREFUL>
+__device__ __forceinline__ bool pipe_pass(const DeltaArgs &a, unsigned block, int thread)
 {
     using LDS = PipeLds<KD>;
     using TK = typename LDS::K;
@@ -904,7 +965,7 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
     constexpr int NS = KD / 32;     // k steps over the key dimensions
     extern __shared__ __attribute__((aligned(16))) char s_dyn[];
     uint16_t *lds = reinterpret_cast<uint16_t *>(s_dyn);
-    int *s_flag = reinterpret_cast<int *>(lds + LDS::kFlag);
+    int *s_flag = reinterpret_cast<int *>(lds + LDS::kFlag), *s_spoiled = s_flag + 4;
 
     // What this workgroup walks: chunks c0 .. c1 - 1 of 64 columns of a head's
     // state, or (kScan) of 64 columns of the segment's transition, the state
@@ -916,14 +977,15 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
     const int rest = block % (unsigned)(a.segs * parts), seg = rest / parts, slice = rest % parts;
     const bool unit = slice >= a.slices;
     if (MODE == kScan && (seg == a.segs - 1 || (unit && seg == 0)))
-        return;
+        return false;
     const int c0 = seg * a.seg_chunks, c1 = min(a.NC, c0 + a.seg_chunks);
     int64_t b;
     int h;
     const int64_t hk = kv_head(a, head, b, h);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, i16 = lane & 15;
+    const int lane = thread & 63, wave = thread >> 6, g = lane >> 4, i16 = lane & 15;
     const int mine = wave & 3;      // the chain wave, or the one that this wave helps
     const int col = (slice * 4 + mine) * 16 + i16;
+    bool again = false;
 
     if (wave < 4) {
         State<KD> S;
@@ -981,15 +1043,17 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
                 v4[t] = lds_column4(s_v + (16 * t + 4 * g + (i16 >> 2)) * TV::kRow + 16 * mine + 4 * (i16 & 3));
             }
             Frag<3> z0[4], z1[2];
+            auto load_z0 = [&]() {
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    z0[t] = L_::template get<3>(s_z, t, 0, lane);
+                __builtin_amdgcn_sched_barrier(0);
+            };
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
-                if (s == NS - 1) {
-                    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        z0[t] = L_::template get<3>(s_z, t, 0, lane);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
+                if (s == NS - 1 && !CAREFUL)
+                    load_z0();
 #pragma unroll
                 for (int n = 2; n >= 0; --n)
 #pragma unroll
@@ -1008,6 +1072,11 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
                 R[t] = v - row_vec(s_vec, kRise, t, lane) * R[t];
                 x[t] = row_vec(s_vec, kBeta, t, lane) * R[t];
                 u[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+            Spoiled bad;
+            if constexpr (CAREFUL) {
+                bad.take_out(R, x, g);
+                load_z0();      // (before, its registers would spill)
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -1042,13 +1111,17 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
                     Sheet(a.ut + (head * a.NC + c) * kC * a.DV, kC, a.DV, col, lane).put(t, u[t]);
                 u[t] *= row_vec(s_vec, kBeta, t, lane);
             }
+            if constexpr (CAREFUL) {
+                if (g == 0)
+                    reinterpret_cast<int *>(lds + LDS::kFrom)[(half * 4 + mine) * 16 + i16] = bad.from;
+            }
             if constexpr (MODE == kOut) {
                 float *y = reinterpret_cast<float *>(lds + LDS::kU) + (half * 4 + mine) * LDS::kUWave + i16 * LDS::kURow + 4 * g;
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
                     *reinterpret_cast<f32x4 *>(y + 16 * t) = u[t];
             }
-            const float whole = s_vec[kWhole * kC];
+            const float whole = bad.whole(s_vec[kWhole * kC]);
             Frag<3> w0, w1;
             w0 = split<3>(row_vec(s_vec, kLeft, 0, lane) * u[0], row_vec(s_vec, kLeft, 1, lane) * u[1]);
             w1 = split<3>(row_vec(s_vec, kLeft, 2, lane) * u[2], row_vec(s_vec, kLeft, 3, lane) * u[3]);
@@ -1071,16 +1144,30 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
             }
             lds_barrier();
         }
-        if constexpr (MODE == kScan)
+        if constexpr (MODE == kScan) {
             S.store(a.trans + (head * a.segs + seg) * KD * (a.slices * 64 + KD), KD, a.slices * 64 + KD, col, lane);
-        else if (a.s_final && c1 == a.NC)
-            S.store(a.s_final + head * a.Dk * a.Dv, a.Dk, a.Dv, col, lane);
+        } else if constexpr (MODE == kOut) {
+            float mark = 0.f;
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    mark = __builtin_fmaf(S.s[m][r], 0.f, mark);
+            const bool spoiled = !CAREFUL && __any(mark != 0.f);
+            if (lane == 0)
+                s_spoiled[mine] = spoiled;
+            lds_barrier();
+            again = s_spoiled[0] | s_spoiled[1] | s_spoiled[2] | s_spoiled[3];
+            // (s_final may be s0, from which a second pass begins)
+            if (a.s_final && c1 == a.NC && !again)
+                S.store(a.s_final + head * a.Dk * a.Dv, a.Dk, a.Dv, col, lane);
+        }
     } else {
         // The help waves have more to do than the chain and share its SIMDs:
         // going first they cut the LM layer's forward from 405 to 380 us (the
         // chain going first: 404).
         __builtin_amdgcn_s_setprio(2);
-        const int tid = threadIdx.x - 256;
+        const int tid = thread - 256;
         const int64_t ek = b * a.k.s.b + hk * a.k.s.h, eq = b * a.q.s.b + hk * a.q.s.h;
         const int64_t ev = b * a.v.s.b + h * a.v.s.h + (unit ? 0 : slice * 64);
         const int vcols = unit ? a.Dv : a.Dv - slice * 64;
@@ -1140,6 +1227,11 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
             qs[0] = mma<3>(split<3>(pf[0], part ? pf[1] : zero), f[0], qs[0]);
             qs[1] = mma<3>(split<3>(pf[2], pf[3]), f[0], qs[1]);
             qs[1] = mma<3>(split<3>(pf[4], part ? zero : pf[5]), f[1], qs[1]);
+            if constexpr (CAREFUL) {
+                const int from = reinterpret_cast<const int *>(lds + LDS::kFrom)[(((c - c0) & 1) * 4 + mine) * 16 + i16];
+                Spoiled::put(qs[0], ta, g, from, __builtin_nanf(""));
+                Spoiled::put(qs[1], tb, g, from, __builtin_nanf(""));
+            }
             const Chunk<true, VEC> co(a.o.p, b * a.o.s.b + h * a.o.s.h, a.o.s.l, max(c, c0) * kC, a.L, a.Dv, c < c0);
             store_cols(co, col, lane, ta, qs[0]);
             store_cols(co, col, lane, tb, qs[1]);
@@ -1183,8 +1275,25 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
             }
             lds_barrier();
         }
-        if constexpr (MODE == kOut)
+        if constexpr (MODE == kOut) {
             output(c1 - 1);
+            lds_barrier();
+            again = s_spoiled[0] | s_spoiled[1] | s_spoiled[2] | s_spoiled[3];
+        }
+    }
+    return again;
+}
+
+// A state that is not finite at its end: the walk again, with a look at every
+// chunk (which in every walk would cost the LM layer 2 to 13 %, with heads of 128
+// 23 %).
+template <int KD, bool VEC, int MODE>
+__device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
+{
+    if (pipe_pass<KD, VEC, MODE, false>(a, block, threadIdx.x)) {
+        lds_barrier();      // the flags have been read
+        // (opaque: nothing formed for one pass is held through the other)
+        pipe_pass<KD, VEC, MODE, true>(a, opaque_s(block), opaque(threadIdx.x));
     }
 }
 

@@ -1,8 +1,9 @@
 """The gated delta rule on the GPU at the edges of its range: gates that empty
 the state, whatever value says so; long sequences of few heads, which are cut
-into segments.  Inputs and tolerances are those of test_gpu_delta; a result that
-is not a normal fp32 number has no 24 bits, so every value may also be off by
-the smallest normal one, 2^-126."""
+into segments; gates whose gradient strong decays make small; values that are
+not finite; more states than one grid dimension holds.  Inputs and tolerances
+are those of test_gpu_delta; a result that is not a normal fp32 number has no
+24 bits, so every value may also be off by the smallest normal one, 2^-126."""
 from __future__ import annotations
 
 import pytest
@@ -172,3 +173,35 @@ def test_every_gradient_of_a_gate(dtype, gates, Dk, Dv, Hk):
     e = ((got - want).abs() - 2.0 ** -126) / size
     say(f"  worst {float(e.max()):.2e} median {float(((got - want).abs() / want.abs()).median()):.2e}")
     assert (want.abs() <= size * (1 + 1e-9)).all() and (e <= 16 * TOL_F32).all()
+
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("name,value", [("q", NAN), ("q", INF), ("k", NAN), ("k", INF), ("v", NAN), ("v", -INF), ("g", NAN),
+                                        ("g", INF), ("beta", NAN), ("beta", INF)])
+@pytest.mark.parametrize("L,at,Dk,Dv", [(150, 0, 64, 64), (150, 5, 40, 72), (150, 63, 64, 64), (150, 100, 128, 128),
+                                        (150, 149, 64, 33), (2565, 1000, 128, 64), (2565, 2564, 64, 64)])
+def test_what_is_not_finite_leaves_the_steps_before_alone(dtype, name, value, L, at, Dk, Dv):
+    """In the state's columns that it reaches, from its step on, and nowhere else."""
+    x = inputs(81, 2, 1, 2, L, Dk, Dv, TYPES[dtype])
+    say(f"[case] {name} = {value} at {at} of {L}, Dk={Dk} Dv={Dv} {dtype}")
+    o, s = pk.delta_rule(*(x[n] for n in STEPS), x["s0"])
+    y = x[name].clone()
+    y[(1, 0, at) if name in ("g", "beta") else (1, 0, at, 3)] = value
+    bad, bad_s = pk.delta_rule(*({**x, name: y}[n] for n in STEPS), x["s0"])
+    torch.cuda.synchronize()
+    reached = torch.zeros_like(o, dtype=torch.bool)     # both value heads share the query and key head
+    if name == "q":
+        reached[1, :, at] = True
+    elif name == "v":
+        reached[1, 0, at:, 3] = True
+    else:
+        reached[1, :2 if name == "k" else 1, at:] = True
+    assert torch.equal(bad[~reached], o[~reached])
+    assert not torch.isfinite(bad[reached]).any()
+    state = torch.zeros_like(s, dtype=torch.bool)
+    if name != "q":
+        state[:] = reached[:, :, -1, None, :].expand_as(s)
+    assert torch.equal(bad_s[~state], s[~state]) and not torch.isfinite(bad_s[state]).any()
