@@ -628,15 +628,19 @@ def _need(n: int) -> int:
 def _on_stream(stream, call, *args, **kw):
     """The call as under torch.cuda.stream(stream): the results and the
     workspace that it allocates belong to that stream, so memory freed on
-    return is not given to another stream's work while the kernels still run."""
+    return is not given to another stream's work while the kernels still run.
+    (A call that is given all its buffers only takes the stream's handle,
+    which is a few microseconds less.)"""
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, args[0].device)
     with torch.cuda.stream(stream):
         return call(*args, **kw)
 
 
-def _stream_of(t) -> Optional[int]:
-    """The current stream of the tensor's device."""
+def _stream_of(t, stream) -> Optional[int]:
+    """`stream`, or the current stream of the tensor's device."""
+    if stream is not None:
+        return _stream(stream)
     return _raw_stream(t.get_device()) if _raw_stream is not None and t.is_cuda else _stream(None)
 
 
@@ -665,7 +669,7 @@ def delta_rule(q, k, v, g, beta, s0=None, *, scale: Optional[float] = None, want
     fp32 [B,Hv,L], s0 fp32 [B,Hv,Dk,Dv] or None; scale 1/sqrt(Dk) by default.
     o has the memory order of v; s_final may be s0.  ``stream`` (here and in
     the functions below): the call as under torch.cuda.stream(stream)."""
-    if stream is not None:
+    if stream is not None and (o is None or workspace is None or (s_final is None and want_state)):
         return _on_stream(stream, delta_rule, q, k, v, g, beta, s0, scale=scale, want_state=want_state, o=o,
                           s_final=s_final, workspace=workspace)
     if o is None:
@@ -679,7 +683,7 @@ def delta_rule(q, k, v, g, beta, s0=None, *, scale: Optional[float] = None, want
     check(library().pdssm_delta_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
                                     beta.data_ptr(), _ptr(s0), o.data_ptr(), _ptr(s_final), B, Hk, Hv, L,
                                     Dk, Dv, Dk ** -0.5 if scale is None else scale, flag, rows,
-                                    workspace.data_ptr(), need, _stream_of(v)))
+                                    workspace.data_ptr(), need, _stream_of(v, stream)))
     return o, s_final
 
 
@@ -703,7 +707,7 @@ def delta_rule_bwd(q, k, v, g, beta, do, s0=None, ds_final=None, *, scale: Optio
     that of s_final (None: zero): (dq, dk, dv, dg, dbeta, ds0 or None), each
     in the memory order of its input.  ``out`` may hold a previous call's
     result to write into."""
-    if stream is not None:
+    if stream is not None and (out is None or workspace is None):
         return _on_stream(stream, delta_rule_bwd, q, k, v, g, beta, do, s0, ds_final, scale=scale,
                           want_ds0=want_ds0, out=out, workspace=workspace)
     if out is not None:
@@ -721,7 +725,7 @@ def delta_rule_bwd(q, k, v, g, beta, do, s0=None, ds_final=None, *, scale: Optio
                                     dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(),
                                     dbeta.data_ptr(), _ptr(ds0), B, Hk, Hv, L, Dk, Dv,
                                     Dk ** -0.5 if scale is None else scale, flag, rows,
-                                    workspace.data_ptr(), need, _stream_of(v)))
+                                    workspace.data_ptr(), need, _stream_of(v, stream)))
     return dq, dk, dv, dg, dbeta, ds0
 
 
@@ -740,7 +744,7 @@ def delta_step(q, k, v, g, beta, s, *, s_out: Optional[torch.Tensor] = None,
     """One step of the gated delta rule: o [B,Hv,Dv] from q, k [B,Hk,Dk],
     v [B,Hv,Dv], g, beta fp32 [B,Hv] and the state s fp32 [B,Hv,Dk,Dv], which
     is updated in place, or into s_out."""
-    if stream is not None:
+    if stream is not None and o is None:
         return _on_stream(stream, delta_step, q, k, v, g, beta, s, s_out=s_out, scale=scale, o=o)
     if s_out is None:
         s_out = s
@@ -751,7 +755,7 @@ def delta_step(q, k, v, g, beta, s, *, s_out: Optional[torch.Tensor] = None,
     check(library().pdssm_delta_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
                                      beta.data_ptr(), s.data_ptr(), o.data_ptr(), s_out.data_ptr(), B, Hk,
                                      Hv, Dk, Dv, Dk ** -0.5 if scale is None else scale, flag, rows,
-                                     _stream_of(v)))
+                                     _stream_of(v, stream)))
     return o
 
 
@@ -811,7 +815,7 @@ def qk_norm_rope(q, k, wq=None, wk=None, cos=None, sin=None, pos=None, *, kind: 
     (unit length); ``pairs``: "half" (i, i + R/2) or "adjacent" (2i, 2i + 1).
     The results have the memory order of q and k; ``out``: two tensors to
     write into instead (the inputs, to work in place)."""
-    if stream is not None:
+    if stream is not None and out is None:
         return _on_stream(stream, qk_norm_rope, q, k, wq, wk, cos, sin, pos, kind=kind, pairs=pairs, eps=eps, out=out)
     q_out, k_out = (torch.empty_like(q), torch.empty_like(k)) if out is None else out
     (flags, B, Hq, Hk, L, D, R, P), rows = _norm_plan(
@@ -819,7 +823,7 @@ def qk_norm_rope(q, k, wq=None, wk=None, cos=None, sin=None, pos=None, *, kind: 
         _form(q_out), _form(k_out))
     check(library().pdssm_qk_norm_rope_fwd(q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(cos),
                                            _ptr(sin), _ptr(pos), q_out.data_ptr(), k_out.data_ptr(), B,
-                                           Hq, Hk, L, D, R, P, eps, flags, rows, _stream_of(q)))
+                                           Hq, Hk, L, D, R, P, eps, flags, rows, _stream_of(q, stream)))
     return q_out, k_out
 
 
@@ -842,7 +846,7 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, wq=None, wk=None, cos=None, sin=None,
     outputs: (dq, dk, dwq, dwk), the first two in the memory order of q and k,
     the last two None where the weight is.  ``out``: dq and dk to write into
     instead (dq_out and dk_out, to work in place)."""
-    if stream is not None:
+    if stream is not None and (out is None or wq is not None or wk is not None):
         return _on_stream(stream, qk_norm_rope_bwd, q, k, dq_out, dk_out, wq, wk, cos, sin, pos, kind=kind,
                           pairs=pairs, eps=eps, out=out, workspace=workspace)
     dq, dk = (torch.empty_like(q), torch.empty_like(k)) if out is None else out
@@ -857,5 +861,5 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, wq=None, wk=None, cos=None, sin=None,
                                            dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), B, Hq, Hk,
                                            L, D, R, P, eps, flags, rows,
                                            workspace.data_ptr() if need else None, need,
-                                           _stream_of(q)))
+                                           _stream_of(q, stream)))
     return dq, dk, dwq, dwk

@@ -58,3 +58,31 @@ def test_the_default_stream_by_its_handle():
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_given_buffers_and_a_stream():
+    """With every buffer given a call allocates nothing, on any stream."""
+    gen = torch.Generator().manual_seed(32)
+    r = lambda *s: torch.randn(s, generator=gen).to(DEV)  # noqa: E731
+    q, k, v = (r(1, 2, 90, 32) / 6 for _ in range(3))
+    g, beta, s0 = -r(1, 2, 90).abs(), torch.sigmoid(r(1, 2, 90)), r(1, 2, 32, 32)
+    first = [x[:, :, 0].contiguous() for x in (q, k, v, g, beta)]
+    ws = torch.empty(pk.pdssm_delta_bwd_workspace_bytes(1, 2, 2, 90, 32, 32, 0), dtype=torch.uint8, device=DEV)
+    o, s, x = torch.empty_like(v), torch.empty_like(s0), torch.empty_like(first[2])
+    grads = tuple(torch.empty_like(t) for t in (q, k, v, g, beta, s0))
+    nq, nk = torch.empty_like(q), torch.empty_like(k)
+    calls = [lambda **kw: pk.delta_rule(q, k, v, g, beta, s0, o=o, s_final=s, workspace=ws, **kw),
+             lambda **kw: pk.delta_rule_bwd(q, k, v, g, beta, v, s0, s0, out=grads, workspace=ws, **kw),
+             lambda **kw: pk.delta_step(*first, s0, s_out=s, o=x, **kw),
+             lambda **kw: pk.qk_norm_rope(q, k, out=(nq, nk), **kw),
+             lambda **kw: pk.qk_norm_rope_bwd(q, k, v, v, out=(nq, nk), **kw)]
+    side = torch.cuda.Stream()
+    for call in calls:
+        want = [t.clone() for t in call() if t is not None]
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_stats()["allocation.all.allocated"]
+        got = call(stream=side)
+        assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
+        side.synchronize()
+        for a, b in zip((t for t in got if t is not None), want):
+            assert torch.equal(a, b)
