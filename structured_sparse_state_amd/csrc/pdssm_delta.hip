@@ -389,10 +389,10 @@ __device__ __forceinline__ int64_t kv_head(const DeltaArgs &a, int64_t head, int
 // Wave a forms row tile a of N and P (bf16 products are exact, fp32 data goes
 // in three parts).  Z = N - N beta Z by forward substitution over 16 x 16
 // blocks: the diagonal blocks row by row with a column in each lane, the
-// others by fp32 matrix instructions, a block column in each wave.  140 to
-// 170 us for the 16384 chunks of the LM layer (8 x 32 heads of 64, 4096 steps),
-// 3.7 to 4.5 TB/s of its 630 MB: five workgroups of 32 KB LDS a compute unit, each waiting at the
-// ends of its phases (without one of them it takes 142 to 179 us).
+// others by fp32 matrix instructions, a block column in each wave.  138 to
+// 176 us for the 16384 chunks of the LM layer (8 x 32 heads of 64, 4096 steps),
+// 3.7 to 4.7 TB/s of the 642 MB that the counters show: five workgroups of 32 KB
+// LDS a compute unit, each waiting at the ends of its phases.
 // ---------------------------------------------------------------------------
 constexpr int kMat = 20;        // row of a 16 x 16 fp32 block in LDS
 __device__ __forceinline__ constexpr int lds_block(int a, int b) { return block_of(a, b) * 16 * kMat; }
@@ -1304,8 +1304,9 @@ __device__ __forceinline__ void pipe_walk(const DeltaArgs &a, unsigned block)
 // tiles in LDS; the chain leaves w and the new gradient in the same places,
 // from where the help waves write w, dV and the gradient to memory.  SCAN: the
 // gradient before the segment alone, from zero after it.  Both walks of the
-// backward's LM layer (4 x 16 heads of 128, 4096 steps, 1.4 GB to and from
-// memory) take 404 us, 6.3 us a chunk; the chain by itself would take 2.9 us.
+// backward's LM layer (4 x 16 heads of 128, 4096 steps, 1.7 GB to and from
+// memory by the counters, 4.2 TB/s) take 405 us, 6.3 us a chunk; the chain by
+// itself would take 2.9 us.
 // ---------------------------------------------------------------------------
 template <int KD>
 struct BackLds {
@@ -2225,9 +2226,10 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(DeltaArgs a)
 // out on the way; a wave takes the 16 key dimensions it owns (with 64 of them:
 // half of the rows each), reading the state and its gradient straight into the
 // product's layout, two k steps ahead, then one or two 16 x 16 blocks of X and
-// Y, whose three parts take the place of u~ and w.  359 to 391 us for 4096 chunks of
-// 128 x 128 (2.8 to 3.0 TB/s of 1.06 GB): its 158 KB of LDS leave one workgroup to a compute
-// unit, so loads and products of a chunk do not overlap with another's.
+// Y, whose three parts take the place of u~ and w.  357 to 391 us for 4096 chunks
+// of 128 x 128 (2.8 to 3.0 TB/s of the 1.09 GB that the counters show): its 160 KB
+// of LDS leave one workgroup to a compute unit, so loads and products of a chunk
+// do not overlap with another's.
 // ---------------------------------------------------------------------------
 constexpr int kGradThreads = 512;
 
