@@ -34,6 +34,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIBRARY = os.path.join(HERE, "libpdssm.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "pdssm.h")
 LAYERS_HEADER = os.path.join(os.path.dirname(HERE), "include", "pdssm_layers.h")
+BLOCK_HEADER = os.path.join(os.path.dirname(HERE), "include", "pdssm_block.h")
 
 # Flag and status values of include/pdssm.h (tests check they agree).
 PDSSM_SEL_I32 = 0x0
@@ -52,6 +53,10 @@ PDSSM_ROUTER_W_PACKED = 0x1
 PDSSM_DATA_BF16 = 0x1
 PDSSM_NORM_L2 = 0x2
 PDSSM_ROPE_PAIRS = 0x4
+
+# Flags of include/pdssm_block.h.
+PDSSM_NO_DG = 0x2
+PDSSM_DG_HEADS = 0x4
 
 PDSSM_OK = 0
 PDSSM_ERR_NULL = -1
@@ -126,6 +131,15 @@ def _load(path: str) -> ctypes.CDLL:
         lib.pdssm_qk_norm_rope_bwd.restype = ctypes.c_int
         lib.pdssm_qk_norm_rope_bwd_workspace_bytes.argtypes = [I64] * 4 + [I32]
         lib.pdssm_qk_norm_rope_bwd_workspace_bytes.restype = SZ
+        lib.pdssm_linear_fwd.argtypes = [P] * 7 + [I64] * 4 + [I32, I32, F, U32, P, P, SZ, P]
+        lib.pdssm_linear_fwd.restype = ctypes.c_int
+        lib.pdssm_linear_bwd.argtypes = [P] * 12 + [I64] * 4 + [I32, I32, F, U32, P, P, SZ, P]
+        lib.pdssm_linear_bwd.restype = ctypes.c_int
+        lib.pdssm_linear_step.argtypes = [P] * 7 + [I64] * 3 + [I32, I32, F, U32, P, P]
+        lib.pdssm_linear_step.restype = ctypes.c_int
+        for size in (lib.pdssm_linear_workspace_bytes, lib.pdssm_linear_bwd_workspace_bytes):
+            size.argtypes = [I64] * 4 + [I32, I32, U32]
+            size.restype = SZ
     return lib
 
 
@@ -863,3 +877,191 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, wq=None, wk=None, cos=None, sin=None,
                                            workspace.data_ptr() if need else None, need,
                                            _stream_of(q, stream)))
     return dq, dk, dwq, dwk
+
+
+# ---------------------------------------------------------------------------
+# Operators of a layer's block (include/pdssm_block.h)
+# ---------------------------------------------------------------------------
+
+def pdssm_linear_fwd(q, k, v, g, s0, o, s_final, B, Hk, Hv, L, Dk, Dv, scale, flags, strides, workspace,
+                     workspace_bytes, stream=None) -> int:
+    return library().pdssm_linear_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(s0), _ptr(o), _ptr(s_final), B,
+                                      Hk, Hv, L, Dk, Dv, scale, flags, _strides(strides), _ptr(workspace),
+                                      workspace_bytes, _stream(stream))
+
+
+def pdssm_linear_workspace_bytes(B, Hk, Hv, L, Dk, Dv, flags) -> int:
+    return library().pdssm_linear_workspace_bytes(B, Hk, Hv, L, Dk, Dv, flags)
+
+
+def pdssm_linear_bwd(q, k, v, g, s0, d_o, ds_final, dq, dk, dv, dg, ds0, B, Hk, Hv, L, Dk, Dv, scale, flags,
+                     strides, workspace, workspace_bytes, stream=None) -> int:
+    return library().pdssm_linear_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(s0), _ptr(d_o), _ptr(ds_final),
+                                      _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(ds0), B, Hk, Hv, L, Dk, Dv,
+                                      scale, flags, _strides(strides), _ptr(workspace), workspace_bytes,
+                                      _stream(stream))
+
+
+def pdssm_linear_bwd_workspace_bytes(B, Hk, Hv, L, Dk, Dv, flags) -> int:
+    return library().pdssm_linear_bwd_workspace_bytes(B, Hk, Hv, L, Dk, Dv, flags)
+
+
+def pdssm_linear_step(q, k, v, g, s, o, s_out, B, Hk, Hv, Dk, Dv, scale, flags, strides, stream=None) -> int:
+    return library().pdssm_linear_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(s), _ptr(o), _ptr(s_out), B, Hk,
+                                       Hv, Dk, Dv, scale, flags, _strides(strides), _stream(stream))
+
+
+def _linear_form(q, k, v, g, dims):
+    """Flag, sizes (B, Hk, Hv, L, Dk, Dv) and the gates' strides of a call; L is
+    1 for a step."""
+    flag = _data_flag("q, k and v", q[2], k[2], v[2])
+    if len(q[0]) != dims + 1 or len(v[0]) != dims + 1:
+        raise ValueError("q, k and v must be [B,H,L,D] (a step: [B,H,D])")
+    B, Hk, *L, Dk = q[0]
+    Hv, Dv = v[0][1], v[0][-1]
+    _want("k", k, q[0], q[2])
+    _want("v", v, (B, Hv, *L, Dv), q[2])
+    gates = (0, 0, 0)
+    if g is not None and len(g[0]) == 1:
+        _want("g", g, (Hv,), torch.float32)
+        gates = (0, g[1][0], 0)
+    elif g is not None:
+        _want("g", g, (B, Hv, *L), torch.float32)
+        gates = (*g[1], *(0,) * (3 - dims))
+    return (flag, B, Hk, Hv, (L[0] if L else 1), Dk, Dv), gates
+
+
+def _row_strides(dims, *forms):
+    """The triples of _rows, as a list."""
+    out = []
+    for shape, st, *_ in forms:
+        if st[dims] != 1 and shape[dims] > 1:
+            raise ValueError("the last dimension must be contiguous")
+        out.append((*st[:dims], *(0,) * (3 - dims)))
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _linear_plan(q, k, v, g, o, s0, s_final):
+    sizes, gates = _linear_form(q, k, v, g, 3)
+    flag, B, Hk, Hv, L, Dk, Dv = sizes
+    _want("o", o, v[0], v[2])
+    _want("s0", s0, (B, Hv, Dk, Dv), torch.float32, True)
+    _want("s_final", s_final, (B, Hv, Dk, Dv), torch.float32, True)
+    need = _need(pdssm_linear_workspace_bytes(B, Hk, Hv, L, Dk, Dv, flag))
+    _one_device(q, k, v, g, o, s0, s_final)
+    rows = _row_strides(3, q, k, v, o)
+    return sizes, _strides(rows[:3] + [gates] + rows[3:]), need
+
+
+def linear_attention(q, k, v, g=None, s0=None, *, scale: Optional[float] = None, want_state: bool = True,
+                     o: Optional[torch.Tensor] = None, s_final: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """Linear attention with decays over whole sequences: (o [B,Hv,L,Dv],
+    s_final [B,Hv,Dk,Dv] or None).  q, k [B,Hk,L,Dk] and v [B,Hv,L,Dv] bf16 or
+    fp32 with any strides of the first three dimensions; g the log decays, fp32
+    [B,Hv,L], or [Hv] for a fixed one of each head, or None; s0 fp32
+    [B,Hv,Dk,Dv] or None; scale 1/sqrt(Dk) by default.  o has the memory order
+    of v; s_final may be s0.  ``stream`` (here and in the functions below): the
+    call as under torch.cuda.stream(stream)."""
+    if stream is not None and (o is None or workspace is None or (s_final is None and want_state)):
+        return _on_stream(stream, linear_attention, q, k, v, g, s0, scale=scale, want_state=want_state, o=o,
+                          s_final=s_final, workspace=workspace)
+    if o is None:
+        o = torch.empty_like(v)
+    if s_final is None and want_state:
+        s_final = torch.empty((v.shape[0], v.shape[1], q.shape[-1], v.shape[-1]), dtype=torch.float32,
+                              device=v.device)
+    (flag, B, Hk, Hv, L, Dk, Dv), rows, need = _linear_plan(
+        _form(q), _form(k), _form(v), _form(g), _form(o), _form(s0), _form(s_final))
+    workspace = _workspace(need, workspace, v.device)
+    check(library().pdssm_linear_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), _ptr(s0), o.data_ptr(),
+                                     _ptr(s_final), B, Hk, Hv, L, Dk, Dv, Dk ** -0.5 if scale is None else scale,
+                                     flag, rows, workspace.data_ptr(), need, _stream_of(v, stream)))
+    return o, s_final
+
+
+@functools.lru_cache(maxsize=1024)
+def _linear_bwd_plan(q, k, v, g, s0, do, ds_final, dq, dk, dv, dg, ds0):
+    sizes, gates = _linear_form(q, k, v, g, 3)
+    flag, B, Hk, Hv, L, Dk, Dv = sizes
+    for name, form, like in (("do", do, v), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        _want(name, form, like[0], like[2])
+    if dg is not None:
+        _want("dg", dg, g[0], torch.float32)
+    for name, form in (("s0", s0), ("ds_final", ds_final), ("ds0", ds0)):
+        _want(name, form, (B, Hv, Dk, Dv), torch.float32, True)
+    dgates = (0, 0, 0)
+    if dg is None:
+        flag |= PDSSM_NO_DG
+    elif len(dg[0]) == 1:
+        flag |= PDSSM_DG_HEADS
+        dgates = (0, dg[1][0], 0)
+    else:
+        dgates = tuple(dg[1])
+    need = _need(pdssm_linear_bwd_workspace_bytes(B, Hk, Hv, L, Dk, Dv, flag))
+    _one_device(q, k, v, g, s0, do, ds_final, dq, dk, dv, dg, ds0)
+    rows = _row_strides(3, q, k, v, do, dq, dk, dv)
+    return (flag, *sizes[1:]), _strides(rows[:3] + [gates] + rows[3:] + [dgates]), need
+
+
+def linear_attention_bwd(q, k, v, g, do, s0=None, ds_final=None, *, scale: Optional[float] = None,
+                         want_dg: bool = True, want_ds0: bool = True, out=None,
+                         workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of linear_attention from its inputs, the gradient ``do`` of o
+    and that of s_final (None: zero): (dq, dk, dv, dg, ds0), the first four in
+    the memory order of their inputs; dg has the shape of g (for [Hv] the sum
+    over sequences and steps) and is None without g or with want_dg=False, ds0
+    None with want_ds0=False.  ``out`` may hold a previous call's result to
+    write into."""
+    if stream is not None and (out is None or workspace is None):
+        return _on_stream(stream, linear_attention_bwd, q, k, v, g, do, s0, ds_final, scale=scale,
+                          want_dg=want_dg, want_ds0=want_ds0, out=out, workspace=workspace)
+    if out is not None:
+        dq, dk, dv, dg, ds0 = out
+    else:
+        dq, dk, dv = (torch.empty_like(t) for t in (q, k, v))
+        dg = torch.empty_like(g) if g is not None and want_dg else None
+        ds0 = torch.empty((v.shape[0], v.shape[1], q.shape[-1], v.shape[-1]), dtype=torch.float32,
+                          device=v.device) if want_ds0 else None
+    if g is None and dg is not None:
+        raise ValueError("dg without g")
+    (flag, B, Hk, Hv, L, Dk, Dv), rows, need = _linear_bwd_plan(
+        _form(q), _form(k), _form(v), _form(g), _form(s0), _form(do), _form(ds_final), _form(dq), _form(dk),
+        _form(dv), _form(dg), _form(ds0))
+    workspace = _workspace(need, workspace, v.device)
+    check(library().pdssm_linear_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), _ptr(s0), do.data_ptr(),
+                                     _ptr(ds_final), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dg),
+                                     _ptr(ds0), B, Hk, Hv, L, Dk, Dv, Dk ** -0.5 if scale is None else scale, flag,
+                                     rows, workspace.data_ptr(), need, _stream_of(v, stream)))
+    return dq, dk, dv, dg, ds0
+
+
+@functools.lru_cache(maxsize=1024)
+def _linear_step_plan(q, k, v, g, o, s, s_out):
+    (flag, B, Hk, Hv, _, Dk, Dv), gates = _linear_form(q, k, v, g, 2)
+    _want("o", o, v[0], v[2])
+    _want("s", s, (B, Hv, Dk, Dv), torch.float32, True)
+    _want("s_out", s_out, (B, Hv, Dk, Dv), torch.float32, True)
+    _one_device(q, k, v, g, o, s, s_out)
+    rows = _row_strides(2, q, k, v, o)
+    return flag, B, Hk, Hv, Dk, Dv, _strides(rows[:3] + [gates] + rows[3:])
+
+
+def linear_attention_step(q, k, v, g, s, *, s_out: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                          o: Optional[torch.Tensor] = None, stream=None):
+    """One step of linear attention: o [B,Hv,Dv] from q, k [B,Hk,Dk], v
+    [B,Hv,Dv], g fp32 [B,Hv], [Hv] or None, and the state s fp32 [B,Hv,Dk,Dv],
+    which is updated in place, or into s_out."""
+    if stream is not None and o is None:
+        return _on_stream(stream, linear_attention_step, q, k, v, g, s, s_out=s_out, scale=scale, o=o)
+    if s_out is None:
+        s_out = s
+    if o is None:
+        o = torch.empty_like(v)
+    flag, B, Hk, Hv, Dk, Dv, rows = _linear_step_plan(_form(q), _form(k), _form(v), _form(g), _form(o), _form(s),
+                                                      _form(s_out))
+    check(library().pdssm_linear_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), s.data_ptr(),
+                                      o.data_ptr(), s_out.data_ptr(), B, Hk, Hv, Dk, Dv,
+                                      Dk ** -0.5 if scale is None else scale, flag, rows, _stream_of(v, stream)))
+    return o

@@ -27,9 +27,9 @@ VARIANTS = {
 }
 SOURCES = [os.path.join(CSRC, f) for f in ("pdssm_scan.hip", "pdssm_bwd.hip", "pdssm_aux.hip",
                                             "pdssm_router.hip")]
-# Operators beside the scan (include/pdssm_layers.h): in libpdssm.so only, the
-# test builds change nothing of them.
-LAYER_SOURCES = [os.path.join(CSRC, f) for f in ("pdssm_delta.hip", "pdssm_norm.hip")]
+# Operators beside the scan (include/pdssm_layers.h, include/pdssm_block.h): in
+# libpdssm.so only, the test builds change nothing of them.
+LAYER_SOURCES = [os.path.join(CSRC, f) for f in ("pdssm_delta.hip", "pdssm_norm.hip", "pdssm_linear.hip")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -1,0 +1,1257 @@
+// Linear attention with decays (include/pdssm_block.h): forward, gradients, step.
+//
+// A chunk of 64 steps at once, from the state S before it.  With G the running
+// sum of g inside the chunk, rise = e^G, left = e^(G_last - G), whole =
+// e^G_last, decay[i,j] = e^(G_i - G_j) for j <= i,
+//     O  = scale rise Q S + P V,   P = scale * lower part of (Q K^T . decay)
+//     S <- whole S + K^T (left V).
+// The gradients are three walks of the same form, one forward and two back from
+// the gradient dS of the state after the last chunk:
+//     dQ = scale rise dO S^T + X K,   X = scale * lower part of (dO V^T . decay)
+//          S^T <- whole S^T + V^T (left K)
+//     dV = left K dS + P^T dO,        dS   <- whole dS   + Q^T (scale rise dO)
+//     dK = left V dS^T + X^T Q,       dS^T <- whole dS^T + dO^T (scale rise Q).
+// So one walk serves all:
+//     Y = read X1 S + M X3,   M = scale * triangle of (X1 X2^T . decay),
+//     S <- whole S + X2^T (write X3)
+// with (X1, X2, X3) = (q, k, v), (dO, v, k), (k, q, dO), (v, dO, q), the lower
+// triangle going forward and the upper one going back.
+// The gradient of g is the sum of what crosses a step,
+//     dg_t = <whole S, dS> + sum over i >= t of q_i . (scale rise dO S^T)_i
+//            + sum over j < t of k_j . (left V dS^T)_j
+//            + sum over j < t <= i of X_ij q_i . k_j :
+// the walk of dQ keeps the states before the chunks and its share of the rows'
+// products, the walk of dK, whose state has the same shape and the same owner
+// for every value, adds the rest.
+//
+// The walk.  Waves 0..3 ("chain") own 16 columns of the state each, whose
+// recurrences are independent, and keep them in registers in the matrix cores'
+// result layout, from where they feed the products without leaving the wave.
+// Waves 4..7 ("help") bring the next chunk's rows to LDS, sum its gates and
+// form M, all ahead of the chain.  States, M and the weighted X3 enter the
+// products as three bf16 parts (all 24 bits); bf16 rows are one part, fp32 rows
+// three.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "pdssm_block.h"
+#include "pdssm_chunk.h"
+
+namespace pdssm {
+namespace {
+
+constexpr int kMaxDim = 128;
+constexpr int kSlice = 64;          // columns of the state in a workgroup
+constexpr int kHelp = 256, kWalkThreads = 256 + kHelp;
+
+// Vectors of a chunk in LDS: what the rows read of the state and write to it,
+// the state's own decay, G log2(e) as a pair of floats and the steps that
+// empty the state, counted.
+enum LinVec { kRead, kWrite, kWhole, kGhi, kGlo, kResets, kVecs };
+
+struct Walk {
+    Rows x1, x2, x3, y;
+    Rows x4;                // dg: the rows beside y's (q for dQ, k for dK)
+    bool kv1, kv2, kv3, kvy;        // rows of the key heads
+    bool wide;              // y: fp32 [B*Hv][L][pitch] whatever the type of the data
+    int D1, D3, slices;     // contraction, columns
+    const float *start;     // the state before the first chunk of the walk, NULL: zero
+    float *end;             // and after its last, NULL: not wanted
+    int row, col;           // strides of a state's values along contraction and columns
+    float *starts;          // [segs + 1]: states before the segments, see native()
+    float *wholes;          // [segs][heads]: the segments' decays
+};
+
+struct LinArgs {
+    Walk w[3];
+    Rows g;
+    Rows dg;
+    float *kept;            // [NC]: the states before the chunks, see native()
+    float *reads;           // [NC][slices][heads][4][64]: q . what dQ reads of S
+    float *dg_part;         // [slices][heads][L], or NULL: dg itself
+    int64_t heads;          // B*Hv
+    int64_t blocks;         // below 2^32, by the limit on B Hv
+    bool started;           // s0 is given
+    int first, last;        // walks of this launch
+    int segs, seg_chunks;
+    int Hk, Hv, L, NC;
+    float scale;
+};
+
+enum Mode { kOut, kScan };          // outputs; the last state alone
+enum Gate { kNone, kKeep, kGrad };  // what a walk does for dg
+
+// A workgroup's state as its chain waves hold it: state number n of a slice of
+// a head, [4 waves][KD / 16][64 lanes] four values each.
+template <int KD>
+__device__ __forceinline__ float *native(float *p, int64_t n, int slices, int64_t heads, int slice, int64_t head, int wave,
+                                         int lane)
+{
+    return p + ((((n * slices + slice) * heads + head) * 4 + wave) * (KD / 16) * 64 + lane) * 4;
+}
+
+template <int KD, bool BF16>
+struct LinLds {
+    using T1 = Tile<KD, BF16, kHelp>;
+    using T3 = Tile<kSlice, BF16, kHelp>;
+    using M = Tri<false, kHelp>;                    // (both triangles take as much)
+    // bf16: the chain reads one half while the help waves fill the other.  Three
+    // parts of fp32 rows leave no room for that.
+    static constexpr int kHalves = BF16 ? 2 : 1;
+    // in uint16_t
+    static constexpr int kX1 = 0;
+    static constexpr int kX2 = kX1 + kHalves * T1::kSize;
+    static constexpr int kX3 = kX2 + kHalves * T1::kSize;
+    static constexpr int kM = kX3 + kHalves * T3::kSize;
+    // in floats
+    static constexpr int kVec = (kM + kHalves * M::kSize) / 2;
+    static constexpr int kCuts = kVec + kHalves * kVecs * kC;
+    static constexpr int kWrites = kCuts + kHalves * Cuts::kSize;   // [4 waves][64]: k . what dK reads of dS
+    static constexpr int kCross = kWrites + kHalves * 4 * kC;       // [4 waves]: <whole S, dS>
+    static constexpr int kFlag = kCross + kHalves * 4;              // [4] help waves, [4] spoiled
+    static constexpr size_t kBytes = (kFlag + 8) * 4;
+};
+
+// Values of a state in memory, a lane's column and rows 16 m + 4 g + r.
+template <int KD, typename F>
+__device__ __forceinline__ void each_value(const Walk &w, int col, int lane, F f)
+{
+#pragma unroll
+    for (int m = 0; m < KD / 16; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 16 * m + 4 * (lane >> 4) + r;
+            f(m, r, row < w.D1 && col < w.D3, row * w.row + col * w.col);
+        }
+}
+
+// c + A B for four tiles at once, part products of order below 3, the small
+// ones first.
+template <int NA, int NB>
+__device__ __forceinline__ void mma4(const Frag<NA> &a, const Frag<NB> (&b)[4], f32x4 (&c)[4])
+{
+#pragma unroll
+    for (int o = 2; o >= 0; --o)
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            const int j = o - i;
+            if (j >= 0 && j < NB) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    c[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b[t].p[j], c[t], 0, 0, 0);
+            }
+        }
+}
+
+// The values that parts stand for.
+template <int N>
+__device__ __forceinline__ f32x8 joined(const Frag<N> &f)
+{
+    f32x8 v = __builtin_convertvector(f.p[N - 1], f32x8);
+#pragma unroll
+    for (int n = N - 2; n >= 0; --n)
+        v += __builtin_convertvector(f.p[n], f32x8);
+    return v;
+}
+
+__device__ __forceinline__ float sum64(float v)
+{
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1)
+        v += __shfl_xor(v, m, 64);
+    return v;
+}
+
+__device__ __forceinline__ int scalar(unsigned v) { return __builtin_amdgcn_readfirstlane((int)v); }
+
+// One walk over the chunks of a segment.  CAREFUL: looks at every chunk for
+// values of X3 that are not finite, which would reach the steps on the other
+// side of the triangle through its zeros.  Gives true when a state that is not
+// finite at the end asks for such a second pass.
+template <int KD, bool BF16, bool VEC, bool BACK, int MODE, int GATE, bool CAREFUL>
+__device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int seg, int slice, int64_t head, int thread)
+{
+    using LDS = LinLds<KD, BF16>;
+    using T1 = typename LDS::T1;
+    using T3 = typename LDS::T3;
+    using M = Tri<BACK, kHelp>;
+    constexpr int NK = T1::NK, NS = KD / 32;
+    extern __shared__ __attribute__((aligned(16))) char s_dyn[];
+    uint16_t *lds = reinterpret_cast<uint16_t *>(s_dyn);
+    float *ldf = reinterpret_cast<float *>(s_dyn);
+    int *s_help = reinterpret_cast<int *>(ldf + LDS::kFlag), *s_spoiled = s_help + 4;
+
+    const int p0 = seg * a.seg_chunks, p1 = min(a.NC, p0 + a.seg_chunks);
+    const int64_t b = scalar((unsigned)head / (unsigned)a.Hv);
+    const int h = (int)head - (int)b * a.Hv, hk = scalar((unsigned)h / (unsigned)(a.Hv / a.Hk));
+    const int lane = thread & 63, wave = thread >> 6, g = lane >> 4, i16 = lane & 15, mine = wave & 3;
+    auto chunk_of = [&](int p) { return BACK ? a.NC - 1 - p : p; };
+    auto half_of = [&](int p) { return LDS::kHalves == 2 ? (p - p0) & 1 : 0; };
+    auto begin = [&](const Rows &x, bool kv) { return b * x.s.b + (kv ? hk : h) * x.s.h; };
+    auto vecs = [&](int half) { return ldf + LDS::kVec + half * kVecs * kC; };
+
+    if (wave >= 4 && lane == 0)
+        s_help[mine] = 0;
+    lds_barrier();
+    bool again = false;
+
+    if (wave < 4) {
+        const int col = slice * kSlice + mine * 16 + i16;
+        const int col4 = slice * kSlice + mine * 16 + 4 * g;    // of the lane's four values of y
+        f32x4 S[KD / 16];
+        if (a.segs > 1 && MODE != kScan) {
+            const float *from = native<KD>(w.starts, seg, w.slices, a.heads, slice, head, mine, lane);
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m)
+                S[m] = *reinterpret_cast<const f32x4 *>(from + m * 256);
+        } else {
+            const float *from = seg == 0 ? w.start : nullptr;
+            each_value<KD>(w, col, lane, [&](int m, int r, bool in, int at) {
+                S[m][r] = from && in ? from[head * w.D1 * w.D3 + at] : 0.f;
+            });
+        }
+        // The first segment's start is kept too: the last one's end may go to
+        // the same buffer while other workgroups still begin.
+        if (MODE == kScan && seg == 0) {
+            float *to = native<KD>(w.starts, 0, w.slices, a.heads, slice, head, mine, lane);
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m)
+                *reinterpret_cast<f32x4 *>(to + m * 256) = S[m];
+        }
+        Frag<3> sf[NS];
+        float product = 1.f;
+        if constexpr (MODE == kOut) {
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+                sf[s] = split<3>(S[2 * s], S[2 * s + 1]);
+        }
+        f32x4 beside[4];        // dg: the next chunk's values of x4 beside y's
+        f32x4 kept[GATE == kGrad ? KD / 16 : 1];
+        auto fetch = [&](int p) {
+            const int c = chunk_of(p);
+            if constexpr (GATE != kNone) {
+                const Chunk<BF16, VEC> cx(w.x4.p, begin(w.x4, true), w.x4.s.l, c * kC, a.L, w.D3);
+                const uint32_t e = cx.lane_at(i16, col4);
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    beside[t] = cx.four(e, i16, 16 * t, col4);
+            }
+            if constexpr (GATE == kGrad) {
+                const float *from = native<KD>(a.kept, c, w.slices, a.heads, slice, head, mine, lane);
+#pragma unroll
+                for (int m = 0; m < KD / 16; ++m)
+                    kept[m] = *reinterpret_cast<const f32x4 *>(from + m * 256);
+            }
+        };
+        if constexpr (GATE != kNone)
+            fetch(p0);
+        if constexpr (BF16)
+            lds_barrier();
+        for (int p = p0; p < p1; ++p) {
+            if constexpr (!BF16)
+                lds_barrier();
+            const int half = half_of(p), c = chunk_of(p);
+            const uint16_t *s_x1 = lds + LDS::kX1 + half * T1::kSize, *s_x2 = lds + LDS::kX2 + half * T1::kSize;
+            const uint16_t *s_x3 = lds + LDS::kX3 + half * T3::kSize, *s_m = lds + LDS::kM + half * M::kSize;
+            const float *s_vec = vecs(half);
+            Frag<NK> x3[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                x3[s] = T3::columns_stacked(s_x3, mine, s, lane);
+            float gone = 1.f;       // NaN: a column of X3 that is not finite spoils its column of the state
+            int from = kC;          // and its outputs from this step on (in the walk's order)
+            if constexpr (CAREFUL) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int t = 32 * s + 16 * (j >> 2) + 4 * g + (j & 3);
+                        if (!finite((float)x3[s].p[0][j]))
+                            from = min(from, BACK ? kC - 1 - t : t);
+                    }
+                from = min(from, __shfl_xor(from, 16, 64));
+                from = min(from, __shfl_xor(from, 32, 64));
+                gone = from < kC ? __builtin_nanf("") : 1.f;
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int t = 32 * s + 16 * (j >> 2) + 4 * g + (j & 3);
+                        if ((BACK ? kC - 1 - t : t) >= from) {
+#pragma unroll
+                            for (int n = 0; n < NK; ++n)
+                                x3[s].p[n][j] = (__bf16)0.f;
+                        }
+                    }
+            }
+            if constexpr (MODE == kOut) {
+                // Y as tiles of 16 columns (rows of the result) by 16 steps
+                f32x4 Y[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    Y[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int s = 0; s < NS; ++s) {
+                    Frag<NK> x1[4];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        x1[t] = T1::rows_stacked(s_x1, t, s, lane);
+                    mma4(sf[s], x1, Y);
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    Y[t] *= s_vec[kRead * kC + 16 * t + i16];
+                if constexpr (GATE != kNone) {
+                    float *to = GATE == kKeep ? a.reads + ((((int64_t)c * w.slices + slice) * a.heads + head) * 4 + mine) * kC
+                                              : ldf + LDS::kWrites + (half * 4 + mine) * kC;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        float v = Y[t][0] * beside[t][0] + Y[t][1] * beside[t][1] + Y[t][2] * beside[t][2] + Y[t][3] * beside[t][3];
+                        v += __shfl_xor(v, 16, 64);
+                        v += __shfl_xor(v, 32, 64);
+                        if (g == 0)
+                            to[16 * t + i16] = v;
+                    }
+                }
+                if constexpr (GATE == kKeep) {
+                    float *to = native<KD>(a.kept, c, w.slices, a.heads, slice, head, mine, lane);
+#pragma unroll
+                    for (int m = 0; m < KD / 16; ++m)
+                        *reinterpret_cast<f32x4 *>(to + m * 256) = S[m];
+                }
+                if constexpr (GATE == kGrad) {
+                    float v = 0.f;
+#pragma unroll
+                    for (int m = 0; m < KD / 16; ++m)
+                        v += kept[m][0] * S[m][0] + kept[m][1] * S[m][1] + kept[m][2] * S[m][2] + kept[m][3] * S[m][3];
+                    v = sum64(v);
+                    if (lane == 0)
+                        ldf[LDS::kCross + half * 4 + mine] = v * s_vec[kWhole * kC];
+                }
+                if constexpr (GATE != kNone)
+                    fetch(min(p + 1, p1 - 1));
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    Frag<3> m[4];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        if (M::has(t, s))
+                            m[t] = M::template get<3>(s_m, t, s, lane);
+#pragma unroll
+                    for (int o = 2; o >= 0; --o)
+#pragma unroll
+                        for (int i = 0; i < NK; ++i)
+                            if (o - i >= 0) {
+#pragma unroll
+                                for (int t = 0; t < 4; ++t)
+                                    if (M::has(t, s))
+                                        Y[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x3[s].p[i], m[t].p[o - i], Y[t], 0, 0, 0);
+                            }
+                }
+                if constexpr (CAREFUL) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int f = bperm(from, 4 * g + r);
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            const int step = 16 * t + i16;
+                            if ((BACK ? kC - 1 - step : step) >= f)
+                                Y[t][r] = __builtin_nanf("");
+                        }
+                    }
+                }
+                auto store = [&](auto cy) {
+                    const uint32_t e = cy.lane_at(i16, col4);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        cy.put4(e, i16, 16 * t, col4, Y[t]);
+                };
+                if (BF16 && w.wide) {
+                    const int pitch = (w.D3 + 3) / 4 * 4;
+                    store(Chunk<false, VEC>(w.y.p, head * a.L * pitch, pitch, c * kC, a.L, pitch));
+                } else {
+                    store(Chunk<BF16, VEC>(w.y.p, begin(w.y, w.kvy), w.y.s.l, c * kC, a.L, w.D3));
+                }
+            }
+            // the state
+            const float whole = s_vec[kWhole * kC] * gone;
+            product *= whole;
+            Frag<3> wx[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const f32x4 lo = row_vec(s_vec, kWrite, 2 * s, lane), hi = row_vec(s_vec, kWrite, 2 * s + 1, lane);
+                wx[s] = split<3>(joined(x3[s]) * __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+            }
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m)
+                S[m] *= whole;
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                Frag<NK> x2[2][2];
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        x2[m][i] = T1::columns_stacked(s_x2, 2 * s + m, i, lane);
+#pragma unroll
+                for (int o = 2; o >= 0; --o)
+#pragma unroll
+                    for (int n = 0; n < NK; ++n)
+                        if (o - n >= 0) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                                for (int m = 0; m < 2; ++m)
+                                    S[2 * s + m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x2[m][i].p[n], wx[i].p[o - n],
+                                                                                          S[2 * s + m], 0, 0, 0);
+                        }
+                if constexpr (MODE == kOut)
+                    sf[s] = split<3>(S[2 * s], S[2 * s + 1]);
+            }
+            lds_barrier();
+        }
+        if constexpr (MODE == kScan) {
+            float *to = native<KD>(w.starts, seg + 1, w.slices, a.heads, slice, head, mine, lane);
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m)
+                *reinterpret_cast<f32x4 *>(to + m * 256) = S[m];
+            if (thread == 0 && slice == 0)
+                w.wholes[seg * a.heads + head] = product;
+        } else {
+            float mark = 0.f;
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    mark = __builtin_fmaf(S[m][r], 0.f, mark);
+            const bool spoiled = !CAREFUL && __any(mark != 0.f);
+            if (lane == 0)
+                s_spoiled[mine] = spoiled;
+            lds_barrier();
+            again = s_spoiled[0] | s_spoiled[1] | s_spoiled[2] | s_spoiled[3];
+            // (the end may be the start, from which a second pass begins)
+            if (w.end && p1 == a.NC && !again) {
+                each_value<KD>(w, col, lane, [&](int m, int r, bool in, int at) {
+                    if (in)
+                        w.end[head * w.D1 * w.D3 + at] = S[m][r];
+                });
+            }
+        }
+    } else {
+        const int tid = thread - 256;
+        T1 t1, t2;
+        T3 t3;
+        float gate;
+        Unit<BF16> kf[GATE == kGrad ? 2 : 1];       // the wave's rows of k
+        auto fetch = [&](int p) {
+            const int t0 = chunk_of(p) * kC;
+            if constexpr (MODE == kOut)
+                t1.load(Chunk<BF16, VEC>(w.x1.p, begin(w.x1, w.kv1), w.x1.s.l, t0, a.L, w.D1), tid);
+            t2.load(Chunk<BF16, VEC>(w.x2.p, begin(w.x2, w.kv2), w.x2.s.l, t0, a.L, w.D1), tid);
+            t3.load(Chunk<BF16, VEC>(w.x3.p, begin(w.x3, w.kv3) + slice * kSlice, w.x3.s.l, t0, a.L, w.D3 - slice * kSlice), tid);
+            gate = 0.f;
+            if (a.g.p && t0 + lane < a.L)
+                gate = static_cast<const float *>(a.g.p)[b * a.g.s.b + h * a.g.s.h + (t0 + lane) * a.g.s.l];
+            if constexpr (GATE == kGrad) {
+                const Chunk<BF16, VEC> ck(w.x4.p, begin(w.x4, true), w.x4.s.l, t0, a.L, w.D3);
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    kf[s] = ck.unit(16 * mine + i16, slice * kSlice + 32 * s + 8 * g);
+            }
+        };
+        // Rows, gates and M of chunk p into its half of LDS, chunk p + 1 on its way.
+        auto prepare = [&](int p) {
+            const int half = half_of(p);
+            uint16_t *s_x1 = lds + LDS::kX1 + half * T1::kSize, *s_x2 = lds + LDS::kX2 + half * T1::kSize;
+            uint16_t *s_x3 = lds + LDS::kX3 + half * T3::kSize;
+            float *s_vec = vecs(half);
+            if constexpr (MODE == kOut)
+                t1.store(s_x1, tid);
+            t2.store(s_x2, tid);
+            t3.store(s_x3, tid);
+            Frag<NK> kr[GATE == kGrad ? 2 : 1];
+            if constexpr (GATE == kGrad) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    kr[s] = unit_frag<BF16>(kf[s]);
+            }
+            if (mine == 0) {
+                // G log2(e) in 64 bits (differences of neighbours stay exact to
+                // 32), steps that empty the state counted apart.
+                const bool empty = gate < kEmpties;
+                double G = empty ? 0.0 : (double)gate * 1.4426950408889634;
+                float n = empty ? 1.f : 0.f;
+#pragma unroll
+                for (int m = 1; m < 64; m <<= 1) {
+                    const double x = __shfl_up(G, m, 64);
+                    const float y = __shfl_up(n, m, 64);
+                    if (lane >= m) {
+                        G += x;
+                        n += y;
+                    }
+                }
+                const float hi = (float)G, lo = (float)(G - (double)hi);
+                const float hi1 = __shfl(hi, 63, 64), lo1 = __shfl(lo, 63, 64), n1 = __shfl(n, 63, 64);
+                const float rise = a.scale * decay_of(hi, lo, n, 0.f, 0.f, 0.f), left = decay_of(hi1, lo1, n1, hi, lo, n);
+                s_vec[kRead * kC + lane] = BACK ? left : rise;
+                s_vec[kWrite * kC + lane] = BACK ? rise : left;
+                s_vec[kWhole * kC + lane] = decay_of(hi1, lo1, n1, 0.f, 0.f, 0.f);
+                s_vec[kGhi * kC + lane] = hi;
+                s_vec[kGlo * kC + lane] = lo;
+                s_vec[kResets * kC + lane] = n;
+            }
+            fetch(min(p + 1, p1 - 1));
+            if constexpr (MODE == kOut) {
+                // the other help waves' rows
+                if (lane == 0)
+                    LdsFlag::set(&s_help[mine], p - p0 + 1);
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    LdsFlag::await(&s_help[m], p - p0 + 1);
+                uint16_t *s_m = lds + LDS::kM + half * M::kSize;
+                const int row = 16 * mine + i16;
+                const float hi = s_vec[kGhi * kC + row], lo = s_vec[kGlo * kC + row], n = s_vec[kResets * kC + row];
+                Frag<NK> x1[NS];
+#pragma unroll
+                for (int s = 0; s < NS; ++s)
+                    x1[s] = T1::rows(s_x1, mine, s, lane);
+#pragma unroll
+                for (int tb = 0; tb < 4; ++tb) {
+                    if (BACK ? tb < mine : tb > mine)
+                        continue;
+                    f32x4 v = {0.f, 0.f, 0.f, 0.f}, kq = v;
+#pragma unroll
+                    for (int s = 0; s < NS; ++s)
+                        v = mma<3>(T1::rows(s_x2, tb, s, lane), x1[s], v);
+                    if constexpr (GATE == kGrad) {
+#pragma unroll
+                        for (int s = 0; s < 2; ++s)
+                            kq = mma<3>(T3::rows(s_x3, tb, s, lane), kr[s], kq);
+                    }
+                    const f32x4 hj = row_vec(s_vec, kGhi, tb, lane), lj = row_vec(s_vec, kGlo, tb, lane),
+                                nj = row_vec(s_vec, kResets, tb, lane);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int col = 16 * tb + 4 * g + r;
+                        const float d = BACK ? decay_of(hj[r], lj[r], nj[r], hi, lo, n) : decay_of(hi, lo, n, hj[r], lj[r], nj[r]);
+                        v[r] = (BACK ? col >= row : col <= row) ? a.scale * v[r] * d : 0.f;
+                        kq[r] = GATE == kGrad && col > row ? v[r] * kq[r] : 0.f;
+                    }
+                    M::put(s_m, mine, tb, lane, v);
+                    if constexpr (GATE == kGrad)
+                        Cuts::put(ldf + LDS::kCuts + half * Cuts::kSize, tb, mine, kq, lane);
+                }
+            }
+        };
+        // dg of a chunk that the chain has left behind (one wave).
+        auto gates_of = [&](int p) {
+            if constexpr (GATE == kGrad) {
+                if (mine == 0) {
+                    const int half = half_of(p), c = chunk_of(p), t = c * kC + lane;
+                    const float *s_vec = vecs(half), *s_w = ldf + LDS::kWrites + half * 4 * kC, *s_x = ldf + LDS::kCross + half * 4;
+                    const float *r = a.reads + (((int64_t)c * w.slices + slice) * a.heads + head) * 4 * kC + lane;
+                    const float v = crossing(s_x[0] + s_x[1] + s_x[2] + s_x[3], r[0] + r[kC] + r[2 * kC] + r[3 * kC],
+                                             s_w[lane] + s_w[kC + lane] + s_w[2 * kC + lane] + s_w[3 * kC + lane],
+                                             ldf + LDS::kCuts + half * Cuts::kSize, lane);
+                    // the decay of an empty state does nothing
+                    const float *n = s_vec + kResets * kC;
+                    const bool empty = n[lane] != (lane ? n[lane - 1] : 0.f) || (t == 0 && !a.started);
+                    if (t < a.L) {
+                        if (a.dg_part)
+                            a.dg_part[(slice * a.heads + head) * a.L + t] = empty ? 0.f : v;
+                        else
+                            static_cast<float *>(const_cast<void *>(a.dg.p))[b * a.dg.s.b + h * a.dg.s.h + t * a.dg.s.l] =
+                                empty ? 0.f : v;
+                    }
+                }
+            }
+        };
+        if constexpr (MODE == kOut) {
+            for (int n = 0; n < LDS::kHalves; ++n)
+                M::clear(lds + LDS::kM + n * M::kSize, tid);
+        }
+        fetch(p0);
+        if constexpr (BF16) {
+            prepare(p0);
+            lds_barrier();
+        }
+        for (int p = p0; p < p1; ++p) {
+            if (p > p0)
+                gates_of(p - 1);
+            if constexpr (BF16) {
+                if (p + 1 < p1)
+                    prepare(p + 1);
+            } else {
+                prepare(p);
+                lds_barrier();
+            }
+            lds_barrier();
+        }
+        gates_of(p1 - 1);
+        if constexpr (MODE == kOut) {
+            lds_barrier();
+            again = s_spoiled[0] | s_spoiled[1] | s_spoiled[2] | s_spoiled[3];
+        }
+    }
+    return again;
+}
+
+template <int KD, bool BF16, bool VEC, bool BACK, int MODE, int GATE>
+__device__ __forceinline__ void walk(const LinArgs &a, const Walk &w, int seg, int slice, int64_t head)
+{
+    // A state that is not finite at its end: the walk again, with a look at
+    // every chunk.
+    if (walk_pass<KD, BF16, VEC, BACK, MODE, GATE, false>(a, w, seg, slice, head, threadIdx.x)) {
+        lds_barrier();      // the flags have been read
+        // (opaque: nothing formed for one pass is held through the other)
+        walk_pass<KD, BF16, VEC, BACK, MODE, GATE, true>(a, w, seg, opaque_s(slice), head, opaque(threadIdx.x));
+    }
+}
+
+// Workgroups by walk, segment, slice, head, the head first: those that read the
+// same rows are a multiple of the heads apart, with 8 heads and their multiples
+// on one die of the eight, with one L2.
+enum Which { kForward, kBoth, kFirst, kLast };      // the forward's; dQ's, dV's and dK's; with dg: dQ's and dV's; dK's
+
+template <int KD, bool BF16, bool VEC, int MODE, int WHICH>
+__global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(LinArgs a)
+{
+    unsigned rest = blockIdx.y * gridDim.x + blockIdx.x;
+    if (rest >= a.blocks)
+        return;
+    const unsigned heads = (unsigned)a.heads;
+    int n = a.first;
+    if constexpr (WHICH == kBoth || WHICH == kFirst) {
+        while (n < a.last && rest >= heads * a.segs * a.w[n].slices) {
+            rest -= heads * a.segs * a.w[n].slices;
+            ++n;
+        }
+    }
+    const Walk &w = a.w[n];
+    const unsigned of_head = rest / heads;
+    const int64_t head = scalar(rest - of_head * heads);
+    const int seg = scalar(of_head / (unsigned)w.slices), slice = scalar(of_head - seg * w.slices);
+    if (MODE == kScan && seg == a.segs - 1)
+        return;     // nothing asks for the last one's end
+    if constexpr (WHICH == kForward) {
+        walk<KD, BF16, VEC, false, MODE, kNone>(a, w, seg, slice, head);
+    } else if constexpr (WHICH == kLast) {
+        walk<KD, BF16, VEC, true, MODE, kGrad>(a, w, seg, slice, head);
+    } else {
+        if (n == 0)
+            walk<KD, BF16, VEC, false, MODE, WHICH == kFirst ? kKeep : kNone>(a, w, seg, slice, head);
+        else
+            walk<KD, BF16, VEC, true, MODE, kNone>(a, w, seg, slice, head);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// join_kernel: the states before the segments, from the segments' decays and
+// ends: the first segment's end is whole, S_{n+1} = decay_n S_n + end_n.  A
+// thread has four values of one state.
+// ---------------------------------------------------------------------------
+template <int KD>
+__global__ void __launch_bounds__(256) lin_join_kernel(LinArgs a)
+{
+    const Walk &w = a.w[blockIdx.y];
+    const int64_t size = (int64_t)w.slices * a.heads * KD * kSlice;    // values between segments
+    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (at >= size)
+        return;
+    const int64_t head = at / (KD * kSlice) % a.heads;
+    float *p = w.starts + size + at;
+    f32x4 S = *reinterpret_cast<const f32x4 *>(p);
+    for (int n = 1; n + 1 < a.segs; ++n) {
+        p += size;
+        S = w.wholes[n * a.heads + head] * S + *reinterpret_cast<const f32x4 *>(p);
+        *reinterpret_cast<f32x4 *>(p) = S;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// group_kernel: dq and dk as the sums over the value heads of their group, from
+// fp32 [B*Hv][L][pitch].  A thread has four values of a row.
+// ---------------------------------------------------------------------------
+struct GroupArgs {
+    const float *part[2];
+    Rows out[2];
+    int64_t items;          // B*Hk*L*pitch / 4
+    int Hk, group, L, D, pitch;
+};
+
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(256) group_kernel(GroupArgs a)
+{
+    const int units = a.pitch / 4;
+    const float *part = a.part[blockIdx.y];
+    const Rows &out = a.out[blockIdx.y];
+    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < a.items; n += (int64_t)gridDim.x * 256) {
+        const int col = (int)(n % units) * 4;
+        const int64_t row = n / units, t = row % a.L, bk = row / a.L, hk = bk % a.Hk, b = bk / a.Hk;
+        const float *p = part + (bk * a.group * a.L + t) * a.pitch + col;
+        f32x4 v = *reinterpret_cast<const f32x4 *>(p);
+        for (int j = 1; j < a.group; ++j)
+            v += *reinterpret_cast<const f32x4 *>(p + (int64_t)j * a.L * a.pitch);
+        const int64_t e = b * out.s.b + hk * out.s.h + t * out.s.l + col;
+        if constexpr (VEC && BF16) {
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(const_cast<void *>(out.p)) + e) =
+                make_uint2(f32x2_to_bf16x2_rne(v[0], v[1]), f32x2_to_bf16x2_rne(v[2], v[3]));
+        } else if constexpr (VEC) {
+            *reinterpret_cast<f32x4 *>(static_cast<float *>(const_cast<void *>(out.p)) + e) = v;
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (col + r < a.D) {
+                    if constexpr (BF16)
+                        static_cast<uint16_t *>(const_cast<void *>(out.p))[e + r] = f32_to_bf16_rne(v[r]);
+                    else
+                        static_cast<float *>(const_cast<void *>(out.p))[e + r] = v[r];
+                }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dg from the slices' parts: of every step, or (a workgroup for each head) the
+// sum over sequences and steps, in 64 bits.
+// ---------------------------------------------------------------------------
+struct GateArgs {
+    const float *part;      // [slices][B*Hv][L]
+    Rows dg;
+    int64_t heads;
+    int Hv, L, slices;
+};
+
+__global__ void __launch_bounds__(256) gate_steps_kernel(GateArgs a)
+{
+    const int64_t all = a.heads * a.L;
+    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < all; n += (int64_t)gridDim.x * 256) {
+        float v = a.part[n];
+        for (int s = 1; s < a.slices; ++s)
+            v += a.part[s * all + n];
+        const int64_t head = n / a.L, b = head / a.Hv;
+        static_cast<float *>(const_cast<void *>(a.dg.p))[b * a.dg.s.b + (head - b * a.Hv) * a.dg.s.h + n % a.L * a.dg.s.l] = v;
+    }
+}
+
+__global__ void __launch_bounds__(256) gate_heads_kernel(GateArgs a)
+{
+    __shared__ double s_sum[4];
+    const int64_t h = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, B = a.heads / a.Hv;
+    if (h >= a.Hv)
+        return;
+    double v = 0.0;
+    for (int64_t n = 0; n < B * a.slices; ++n) {
+        const int64_t s = n / B, b = n - s * B;
+        const float *p = a.part + (s * a.heads + b * a.Hv + h) * a.L;
+        for (int t = threadIdx.x; t < a.L; t += 256)
+            v += p[t];
+    }
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1)
+        v += __shfl_xor(v, m, 64);
+    if ((threadIdx.x & 63) == 0)
+        s_sum[threadIdx.x >> 6] = v;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        static_cast<float *>(const_cast<void *>(a.dg.p))[h * a.dg.s.h] = (float)(s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]);
+}
+
+// ---------------------------------------------------------------------------
+// lin_step_kernel: one step.  A workgroup takes 32 columns of one head's state,
+// each thread four columns of every 32nd row, all rows in registers: the state
+// is read once and written once, and o falls out on the way.
+// ---------------------------------------------------------------------------
+struct LinStepArgs {
+    Rows q, k, v, g, o;
+    const float *s;
+    float *s_out;
+    int64_t blocks;         // heads x slices, over both dimensions of the grid
+    int Hk, Hv, Dk, Dv, slices;
+    float scale;
+};
+
+template <bool BF16>
+__device__ __forceinline__ float load_value(const void *p, int64_t e)
+{
+    if constexpr (BF16)
+        return bf16_lo(static_cast<const uint16_t *>(p)[e]);
+    else
+        return static_cast<const float *>(p)[e];
+}
+
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(256) lin_step_kernel(LinStepArgs a)
+{
+    constexpr int TX = 8, TY = 256 / TX, RP = kMaxDim / TY;
+    __shared__ float s_part[4][TX * 4];
+    const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (block >= a.blocks)
+        return;
+    const int64_t head = block / a.slices;
+    const int slice = (int)(block % a.slices);
+    const int64_t b = head / a.Hv;
+    const int h = (int)(head - b * a.Hv), hk = h / (a.Hv / a.Hk);
+    const int tx = threadIdx.x % TX, ty = threadIdx.x / TX, wave = threadIdx.x >> 6;
+    const int col = (slice * TX + tx) * 4;
+    const float *S = a.s + head * a.Dk * a.Dv;
+    float *So = a.s_out + head * a.Dk * a.Dv;
+
+    f32x4 st[RP];
+    float q[RP], k[RP];
+#pragma unroll
+    for (int i = 0; i < RP; ++i) {
+        const int row = i * TY + ty;
+        st[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        q[i] = k[i] = 0.f;
+        if (row < a.Dk) {
+            if constexpr (VEC) {
+                if (col < a.Dv)
+                    st[i] = *reinterpret_cast<const f32x4 *>(S + row * a.Dv + col);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (col + r < a.Dv)
+                        st[i][r] = S[row * a.Dv + col + r];
+            }
+            q[i] = load_value<BF16>(a.q.p, b * a.q.s.b + hk * a.q.s.h + row);
+            k[i] = load_value<BF16>(a.k.p, b * a.k.s.b + hk * a.k.s.h + row);
+        }
+    }
+    const float decay = a.g.p ? expf(static_cast<const float *>(a.g.p)[b * a.g.s.b + h * a.g.s.h]) : 1.f;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (col + r < a.Dv)
+            v[r] = load_value<BF16>(a.v.p, b * a.v.s.b + h * a.v.s.h + col + r);
+
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < RP; ++i) {
+        const int row = i * TY + ty;
+        st[i] = st[i] * decay + k[i] * v;
+        if (row < a.Dk) {
+            o += q[i] * st[i];
+            if constexpr (VEC) {
+                if (col < a.Dv)
+                    *reinterpret_cast<f32x4 *>(So + row * a.Dv + col) = st[i];
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (col + r < a.Dv)
+                        So[row * a.Dv + col + r] = st[i][r];
+            }
+        }
+    }
+#pragma unroll
+    for (int m = TX; m < 64; m <<= 1)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            o[r] += __shfl_xor(o[r], m, 64);
+    if ((threadIdx.x & 63) < TX)
+        *reinterpret_cast<f32x4 *>(&s_part[wave][tx * 4]) = o;
+    __syncthreads();
+    if (ty == 0) {
+        o = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            o += *reinterpret_cast<const f32x4 *>(&s_part[m][tx * 4]);
+        o *= a.scale;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (col + r < a.Dv) {
+                const int64_t e = b * a.o.s.b + h * a.o.s.h + col + r;
+                if constexpr (BF16)
+                    static_cast<uint16_t *>(const_cast<void *>(a.o.p))[e] = f32_to_bf16_rne(o[r]);
+                else
+                    static_cast<float *>(const_cast<void *>(a.o.p))[e] = o[r];
+            }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
+constexpr int64_t kMaxL = (int64_t)1 << 30;
+// Workgroups along x: a launch has fewer than 2^32 threads in a dimension.
+constexpr int64_t kMaxGridX = (int64_t)1 << 22;
+
+int check_linear_dims(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int32_t Dk, int32_t Dv)
+{
+    if (B < 0 || Hk < 0 || Hv < 0 || L < 0 || L > kMaxL || Dk < 1 || Dk > kMaxDim || Dv < 1 || Dv > kMaxDim)
+        return PDSSM_ERR_DIM;
+    if (Hv > 0 && (Hk == 0 || Hv % Hk != 0))
+        return PDSSM_ERR_DIM;
+    if ((double)B * Hv > 5.0e8 || Hv > (1 << 30) || (double)B * Hv * (double)((L + kC - 1) / kC) > 2.0e9)
+        return PDSSM_ERR_DIM;
+    return PDSSM_OK;
+}
+
+int slices_of(int D) { return (D + kSlice - 1) / kSlice; }
+int padded(int D) { return D <= 64 ? 64 : 128; }
+
+// How many segments the chunks of a head are cut into, walked side by side: they
+// are walked twice (once without outputs) and joined, so a walk is cut only
+// where the workgroups do not fill the device, and no finer than fills it.
+struct Cut {
+    int segs, chunks;
+};
+
+Cut cut_of(int64_t walks, int64_t L)
+{
+    const int64_t NC = (L + kC - 1) / kC;
+    int64_t segs = 1;
+    if (walks > 0 && walks <= 128 && NC >= 16)
+        segs = std::min<int64_t>(256 / walks, NC / 4);
+    Cut c;
+    c.chunks = (int)std::max<int64_t>(1, (NC + segs - 1) / segs);
+    c.segs = (int)std::max<int64_t>(1, (NC + c.chunks - 1) / c.chunks);
+    return c;
+}
+
+// Places in the workspace.
+struct Space {
+    int64_t total = 0;
+    int64_t take(int64_t bytes)
+    {
+        const int64_t at = total;
+        total += (bytes + 255) / 256 * 256;
+        return at;
+    }
+};
+
+struct LinLayout {
+    Space space;
+    Cut cut;
+    int64_t starts[3], wholes[3], kept, reads, dg_part, dq_part, dk_part, ds;
+};
+
+LinLayout layout_of(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int Dk, int Dv, bool bwd, bool grad, bool dg_heads)
+{
+    LinLayout l = {};
+    const int64_t heads = B * Hv, NC = (L + kC - 1) / kC;
+    const int sk = slices_of(Dk), sv = slices_of(Dv), pitch = (Dk + 3) / 4 * 4;
+    const int64_t state = (int64_t)std::max(padded(Dk), padded(Dv)) * kSlice * 4;
+    l.space.take(256);
+    l.cut = cut_of(heads * (bwd ? std::max(sk, sv) : sv), L);
+    for (int n = 0; n < (bwd ? 3 : 1); ++n) {
+        const int64_t slices = bwd && n != 1 ? sk : sv;
+        if (l.cut.segs > 1) {
+            l.starts[n] = l.space.take((l.cut.segs + 1) * heads * slices * state);
+            l.wholes[n] = l.space.take(l.cut.segs * heads * 4);
+        }
+    }
+    if (bwd) {
+        l.ds = l.space.take(heads * Dk * Dv * 4);
+        if (grad) {
+            l.kept = l.space.take(NC * heads * sk * state);
+            l.reads = l.space.take(NC * heads * sk * 4 * kC * 4);
+            if (sk > 1 || dg_heads)
+                l.dg_part = l.space.take(heads * sk * L * 4);
+        }
+        if (Hv > Hk) {
+            l.dq_part = l.space.take(heads * L * pitch * 4);
+            l.dk_part = l.space.take(heads * L * pitch * 4);
+        }
+    }
+    return l;
+}
+
+template <typename K, typename A>
+int lin_launch(K kernel, dim3 grid, int threads, size_t lds, const A &a, hipStream_t stream)
+{
+    // More than 64 KB of LDS has to be asked for; the device has 160 KB.
+    if (lds > 65536) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (e != hipSuccess)
+            return hip_status(e);
+    }
+    hipLaunchKernelGGL(kernel, grid, dim3((unsigned)threads), lds, stream, a);
+    return hip_status(hipGetLastError());
+}
+
+dim3 grid_of(int64_t blocks)
+{
+    return dim3((unsigned)std::min(blocks, kMaxGridX), (unsigned)((blocks + kMaxGridX - 1) / kMaxGridX));
+}
+
+// A call's walks; of cut sequences all scans first, and the join.
+template <int KD, bool BF16, bool VEC, bool BWD>
+int launch_walks(LinArgs a, bool grad, hipStream_t stream)
+{
+    constexpr size_t lds = LinLds<KD, BF16>::kBytes;
+    static_assert(lds <= 163840, "LDS of a compute unit");
+    auto launch = [&](auto kernel, int first, int last) {
+        a.first = first, a.last = last, a.blocks = 0;
+        for (int n = first; n <= last; ++n)
+            a.blocks += a.heads * a.segs * a.w[n].slices;
+        return lin_launch(kernel, grid_of(a.blocks), kWalkThreads, lds, a, stream);
+    };
+    int rc = PDSSM_OK;
+    if (a.segs > 1) {
+        rc = launch(walk_kernel<KD, BF16, VEC, kScan, BWD ? kBoth : kForward>, 0, BWD ? 2 : 0);
+        if (rc == PDSSM_OK) {
+            const int64_t slices = BWD ? std::max(a.w[0].slices, a.w[1].slices) : a.w[0].slices;
+            rc = lin_launch(lin_join_kernel<KD>, dim3((unsigned)(a.heads * slices * (KD * kSlice / 1024)), BWD ? 3 : 1), 256, 0, a, stream);
+        }
+    }
+    if (rc != PDSSM_OK)
+        return rc;
+    if constexpr (!BWD) {
+        return launch(walk_kernel<KD, BF16, VEC, kOut, kForward>, 0, 0);
+    } else {
+        if (!grad)
+            return launch(walk_kernel<KD, BF16, VEC, kOut, kBoth>, 0, 2);
+        // dK's walk adds up dg from what dQ's keeps
+        rc = launch(walk_kernel<KD, BF16, VEC, kOut, kFirst>, 0, 1);
+        return rc == PDSSM_OK ? launch(walk_kernel<KD, BF16, VEC, kOut, kLast>, 2, 2) : rc;
+    }
+}
+
+template <int KD, bool BF16, bool VEC>
+int launch_direction(const LinArgs &a, bool bwd, bool grad, hipStream_t stream)
+{
+    return bwd ? launch_walks<KD, BF16, VEC, true>(a, grad, stream) : launch_walks<KD, BF16, VEC, false>(a, false, stream);
+}
+
+template <bool BF16>
+int launch_sizes(const LinArgs &a, bool wide, bool vec, bool bwd, bool grad, hipStream_t stream)
+{
+    if (wide)
+        return vec ? launch_direction<128, BF16, true>(a, bwd, grad, stream) : launch_direction<128, BF16, false>(a, bwd, grad, stream);
+    return vec ? launch_direction<64, BF16, true>(a, bwd, grad, stream) : launch_direction<64, BF16, false>(a, bwd, grad, stream);
+}
+
+}  // namespace
+}  // namespace pdssm
+
+using namespace pdssm;
+
+namespace {
+
+constexpr uint32_t kBwdFlags = PDSSM_DATA_BF16 | PDSSM_NO_DG | PDSSM_DG_HEADS;
+
+bool bwd_flags_ok(uint32_t flags)
+{
+    return !(flags & ~kBwdFlags) && (flags & (PDSSM_NO_DG | PDSSM_DG_HEADS)) != (PDSSM_NO_DG | PDSSM_DG_HEADS);
+}
+
+}  // namespace
+
+extern "C" size_t pdssm_linear_workspace_bytes(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int32_t Dk, int32_t Dv,
+                                               uint32_t flags)
+{
+    if (check_linear_dims(B, Hk, Hv, L, Dk, Dv) != PDSSM_OK || (flags & ~PDSSM_DATA_BF16))
+        return 0;
+    return (size_t)layout_of(B, Hk, Hv, L, Dk, Dv, false, false, false).space.total;
+}
+
+extern "C" size_t pdssm_linear_bwd_workspace_bytes(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int32_t Dk,
+                                                   int32_t Dv, uint32_t flags)
+{
+    if (check_linear_dims(B, Hk, Hv, L, Dk, Dv) != PDSSM_OK || !bwd_flags_ok(flags))
+        return 0;
+    return (size_t)layout_of(B, Hk, Hv, L, Dk, Dv, true, !(flags & PDSSM_NO_DG), flags & PDSSM_DG_HEADS).space.total;
+}
+
+extern "C" int pdssm_linear_fwd(const void *q, const void *k, const void *v, const float *g, const float *s0, void *o,
+                                float *s_final, int64_t B, int64_t Hk, int64_t Hv, int64_t L, int32_t Dk, int32_t Dv,
+                                float scale, uint32_t flags, const pdssm_strides *strides, void *workspace,
+                                size_t workspace_bytes, hipStream_t stream)
+{
+    const int rc = check_linear_dims(B, Hk, Hv, L, Dk, Dv);
+    if (rc != PDSSM_OK)
+        return rc;
+    if (flags & ~PDSSM_DATA_BF16)
+        return PDSSM_ERR_FLAGS;
+    if (B == 0 || Hv == 0)
+        return PDSSM_OK;
+    if ((s0 && !aligned16(s0)) || (s_final && !aligned16(s_final)))
+        return PDSSM_ERR_ALIGN;
+    if (L == 0) {
+        if (!s_final || s_final == s0)
+            return PDSSM_OK;
+        return launch_state_fill(s0, s_final, B * Hv * Dk * Dv, stream);
+    }
+    if (!q || !k || !v || !o || !workspace)
+        return PDSSM_ERR_NULL;
+    const int esize = (flags & PDSSM_DATA_BF16) ? 2 : 4;
+    for (const void *p : {q, k, v, (const void *)o})
+        if (!element_aligned(p, esize))
+            return PDSSM_ERR_ALIGN;
+    if (!element_aligned(g, 4) || !aligned16(workspace))
+        return PDSSM_ERR_ALIGN;
+    const LinLayout lo = layout_of(B, Hk, Hv, L, Dk, Dv, false, false, false);
+    if (workspace_bytes < (size_t)lo.space.total)
+        return PDSSM_ERR_WORKSPACE;
+    const pdssm_strides keys = {Hk * L * Dk, L * Dk, Dk}, values = {Hv * L * Dv, L * Dv, Dv}, gates = {Hv * L, L, 1};
+    const pdssm_strides contiguous[5] = {keys, keys, values, gates, values};
+    const pdssm_strides *s = strides ? strides : contiguous;
+    if (!strides_ok(s, 3) || (g && !strides_ok(s + 3, 1)) || !strides_ok(s + 4, 1))
+        return PDSSM_ERR_DIM;
+    char *ws = static_cast<char *>(workspace);
+    LinArgs a = {};
+    Walk &w = a.w[0];
+    w.x1 = {q, s[0]}, w.x2 = {k, s[1]}, w.x3 = {v, s[2]}, w.y = {o, s[4]};
+    w.kv1 = w.kv2 = true;
+    w.D1 = Dk, w.D3 = Dv, w.slices = slices_of(Dv), w.start = s0, w.end = s_final, w.row = Dv, w.col = 1;
+    w.starts = reinterpret_cast<float *>(ws + lo.starts[0]), w.wholes = reinterpret_cast<float *>(ws + lo.wholes[0]);
+    a.g = {g, s[3]};
+    a.heads = B * Hv, a.segs = lo.cut.segs, a.seg_chunks = lo.cut.chunks;
+    a.Hk = (int)Hk, a.Hv = (int)Hv, a.L = (int)L, a.NC = (int)((L + kC - 1) / kC), a.scale = scale;
+    const bool vec = units(q, s[0], Dk, esize) && units(k, s[1], Dk, esize) && units(v, s[2], Dv, esize) &&
+                     units(o, s[4], Dv, esize);
+    return esize == 2 ? launch_sizes<true>(a, Dk > 64, vec, false, false, stream)
+                      : launch_sizes<false>(a, Dk > 64, vec, false, false, stream);
+}
+
+extern "C" int pdssm_linear_bwd(const void *q, const void *k, const void *v, const float *g, const float *s0,
+                                const void *d_o, const float *ds_final, void *dq, void *dk, void *dv, float *dg,
+                                float *ds0, int64_t B, int64_t Hk, int64_t Hv, int64_t L, int32_t Dk, int32_t Dv,
+                                float scale, uint32_t flags, const pdssm_strides *strides, void *workspace,
+                                size_t workspace_bytes, hipStream_t stream)
+{
+    int rc = check_linear_dims(B, Hk, Hv, L, Dk, Dv);
+    if (rc != PDSSM_OK)
+        return rc;
+    if (!bwd_flags_ok(flags))
+        return PDSSM_ERR_FLAGS;
+    const bool grad = !(flags & PDSSM_NO_DG), dg_heads = flags & PDSSM_DG_HEADS;
+    if (Hv == 0 || (B == 0 && !dg_heads))
+        return PDSSM_OK;
+    const pdssm_strides keys = {Hk * L * Dk, L * Dk, Dk}, values = {Hv * L * Dv, L * Dv, Dv}, gates = {Hv * L, L, 1};
+    const pdssm_strides contiguous[9] = {keys, keys, values, gates, values, keys, keys, values, dg_heads ? pdssm_strides{0, 1, 0} : gates};
+    const pdssm_strides *s = strides ? strides : contiguous;
+    GateArgs ga = {};
+    ga.dg = {dg, s[8]}, ga.heads = B * Hv, ga.Hv = (int)Hv, ga.L = (int)L, ga.slices = slices_of(Dk);
+    if (B == 0 || L == 0) {
+        for (const float *p : {ds_final, (const float *)ds0})
+            if (p && !aligned16(p))
+                return PDSSM_ERR_ALIGN;
+        if (dg_heads) {
+            if (!dg)
+                return PDSSM_ERR_NULL;
+            if (!element_aligned(dg, 4))
+                return PDSSM_ERR_ALIGN;
+            rc = lin_launch(gate_heads_kernel, grid_of(Hv), 256, 0, ga, stream);
+        }
+        if (rc == PDSSM_OK && B > 0 && ds0 && ds0 != ds_final)
+            rc = launch_state_fill(ds_final, ds0, B * Hv * Dk * Dv, stream);
+        return rc;
+    }
+    for (const float *p : {s0, ds_final, (const float *)ds0})
+        if (p && !aligned16(p))
+            return PDSSM_ERR_ALIGN;
+    if (!q || !k || !v || !d_o || !dq || !dk || !dv || (grad && !dg) || !workspace)
+        return PDSSM_ERR_NULL;
+    const int esize = (flags & PDSSM_DATA_BF16) ? 2 : 4;
+    for (const void *p : {q, k, v, d_o, (const void *)dq, (const void *)dk, (const void *)dv})
+        if (!element_aligned(p, esize))
+            return PDSSM_ERR_ALIGN;
+    if (!element_aligned(g, 4) || (grad && !element_aligned(dg, 4)) || !aligned16(workspace))
+        return PDSSM_ERR_ALIGN;
+    const LinLayout lo = layout_of(B, Hk, Hv, L, Dk, Dv, true, grad, dg_heads);
+    if (workspace_bytes < (size_t)lo.space.total)
+        return PDSSM_ERR_WORKSPACE;
+    for (int n = 0; n < 9; ++n)
+        if (!(n == 3 && !g) && !(n == 8 && (!grad || dg_heads)) && !strides_ok(s + n, 1))
+            return PDSSM_ERR_DIM;
+    char *ws = static_cast<char *>(workspace);
+    auto place = [&](int64_t at) { return reinterpret_cast<float *>(ws + at); };
+    // dV's walk writes ds0 while dK's may still begin from ds_final
+    if (ds0 && ds0 == ds_final) {
+        rc = launch_state_fill(ds_final, place(lo.ds), B * Hv * Dk * Dv, stream);
+        if (rc != PDSSM_OK)
+            return rc;
+        ds_final = place(lo.ds);
+    }
+    const bool shared = Hv > Hk;
+    const int pitch = (Dk + 3) / 4 * 4;
+    LinArgs a = {};
+    Walk &wq = a.w[0], &wv = a.w[1], &wk = a.w[2];
+    wq.x1 = {d_o, s[4]}, wq.x2 = {v, s[2]}, wq.x3 = {k, s[1]}, wq.x4 = {q, s[0]}, wq.y = {dq, s[5]};
+    wv.x1 = {k, s[1]}, wv.x2 = {q, s[0]}, wv.x3 = {d_o, s[4]}, wv.y = {dv, s[7]};
+    wk.x1 = {v, s[2]}, wk.x2 = {d_o, s[4]}, wk.x3 = {q, s[0]}, wk.x4 = {k, s[1]}, wk.y = {dk, s[6]};
+    wq.kv3 = wk.kv3 = wv.kv1 = wv.kv2 = true;
+    wq.D1 = wk.D1 = wv.D3 = Dv, wq.D3 = wk.D3 = wv.D1 = Dk;
+    wq.row = wk.row = wv.col = 1, wq.col = wk.col = wv.row = Dv;
+    wq.start = s0, wv.start = wk.start = ds_final, wv.end = ds0;
+    for (Walk *w : {&wq, &wk})
+        w->kvy = true;
+    if (shared) {
+        const pdssm_strides part = {Hv * L * pitch, L * pitch, pitch};
+        for (Walk *w : {&wq, &wk})
+            w->wide = true, w->kvy = false;
+        wq.y = {place(lo.dq_part), part}, wk.y = {place(lo.dk_part), part};
+    }
+    for (int n = 0; n < 3; ++n) {
+        Walk &w = a.w[n];
+        w.slices = slices_of(w.D3), w.starts = place(lo.starts[n]), w.wholes = place(lo.wholes[n]);
+    }
+    a.g = {g, s[3]}, a.dg = ga.dg, a.started = s0 != nullptr;
+    a.kept = place(lo.kept), a.reads = place(lo.reads);
+    a.dg_part = grad && (ga.slices > 1 || dg_heads) ? place(lo.dg_part) : nullptr;
+    a.heads = B * Hv, a.segs = lo.cut.segs, a.seg_chunks = lo.cut.chunks;
+    a.Hk = (int)Hk, a.Hv = (int)Hv, a.L = (int)L, a.NC = (int)((L + kC - 1) / kC), a.scale = scale;
+    const bool vec_keys = units(dq, s[5], Dk, esize) && units(dk, s[6], Dk, esize);
+    const bool vec = units(q, s[0], Dk, esize) && units(k, s[1], Dk, esize) && units(v, s[2], Dv, esize) &&
+                     units(d_o, s[4], Dv, esize) && vec_keys && units(dv, s[7], Dv, esize);
+    const bool wide = Dk > 64 || Dv > 64;
+    rc = esize == 2 ? launch_sizes<true>(a, wide, vec, true, grad, stream) : launch_sizes<false>(a, wide, vec, true, grad, stream);
+    if (rc == PDSSM_OK && a.dg_part) {
+        ga.part = a.dg_part;
+        if (dg_heads)
+            rc = lin_launch(gate_heads_kernel, grid_of(Hv), 256, 0, ga, stream);
+        else
+            rc = lin_launch(gate_steps_kernel, dim3((unsigned)std::min<int64_t>((a.heads * L + 255) / 256, 4096)), 256, 0, ga, stream);
+    }
+    if (rc == PDSSM_OK && shared) {
+        GroupArgs gr = {{place(lo.dq_part), place(lo.dk_part)}, {{dq, s[5]}, {dk, s[6]}}, B * Hk * L * (pitch / 4),
+                        (int)Hk, (int)(Hv / Hk), (int)L, Dk, pitch};
+        const dim3 grid((unsigned)std::min<int64_t>((gr.items + 255) / 256, 8192), 2);
+        if (esize == 2)
+            rc = vec_keys ? lin_launch(group_kernel<true, true>, grid, 256, 0, gr, stream)
+                          : lin_launch(group_kernel<true, false>, grid, 256, 0, gr, stream);
+        else
+            rc = vec_keys ? lin_launch(group_kernel<false, true>, grid, 256, 0, gr, stream)
+                          : lin_launch(group_kernel<false, false>, grid, 256, 0, gr, stream);
+    }
+    return rc;
+}
+
+extern "C" int pdssm_linear_step(const void *q, const void *k, const void *v, const float *g, const float *s, void *o,
+                                 float *s_out, int64_t B, int64_t Hk, int64_t Hv, int32_t Dk, int32_t Dv, float scale,
+                                 uint32_t flags, const pdssm_strides *strides, hipStream_t stream)
+{
+    const int rc = check_linear_dims(B, Hk, Hv, 1, Dk, Dv);
+    if (rc != PDSSM_OK)
+        return rc;
+    if (flags & ~PDSSM_DATA_BF16)
+        return PDSSM_ERR_FLAGS;
+    if (B == 0 || Hv == 0)
+        return PDSSM_OK;
+    if (!q || !k || !v || !s || !o || !s_out)
+        return PDSSM_ERR_NULL;
+    const int esize = (flags & PDSSM_DATA_BF16) ? 2 : 4;
+    for (const void *p : {q, k, v, (const void *)o})
+        if (!element_aligned(p, esize))
+            return PDSSM_ERR_ALIGN;
+    if (!element_aligned(g, 4) || !aligned16(s) || !aligned16(s_out))
+        return PDSSM_ERR_ALIGN;
+    LinStepArgs a = {};
+    const pdssm_strides keys = {Hk * Dk, Dk, 0}, values = {Hv * Dv, Dv, 0}, gates = {Hv, 1, 0};
+    const pdssm_strides contiguous[5] = {keys, keys, values, gates, values};
+    const pdssm_strides *st = strides ? strides : contiguous;
+    a.q = {q, st[0]}, a.k = {k, st[1]}, a.v = {v, st[2]}, a.g = {g, st[3]}, a.o = {o, st[4]};
+    a.s = s, a.s_out = s_out, a.Hk = (int)Hk, a.Hv = (int)Hv, a.Dk = Dk, a.Dv = Dv, a.scale = scale;
+    a.slices = (Dv + 31) / 32;
+    a.blocks = B * Hv * a.slices;
+    const dim3 grid = grid_of(a.blocks);
+    if (esize == 2)
+        return Dv % 4 == 0 ? lin_launch(lin_step_kernel<true, true>, grid, 256, 0, a, stream)
+                           : lin_launch(lin_step_kernel<true, false>, grid, 256, 0, a, stream);
+    return Dv % 4 == 0 ? lin_launch(lin_step_kernel<false, true>, grid, 256, 0, a, stream)
+                       : lin_launch(lin_step_kernel<false, false>, grid, 256, 0, a, stream);
+}
