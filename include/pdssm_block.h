@@ -136,6 +136,58 @@ int pdssm_linear_step(const void *q, const void *k, const void *v, const float *
                       int32_t Dv, float scale, uint32_t flags, const pdssm_strides *strides,
                       hipStream_t stream);
 
+/*
+ * The layer norm of h = residual + dropout(x) (see above).
+ *   x, residual, y, h  [B,H,L,D]; residual NULL for zero, h NULL when not
+ *             wanted; y or h may be x or residual
+ *   w, b      fp32 [D], or NULL for 1 and 0
+ *   p, seed, offset, rng   the dropout (p = 0: none); rng NULL, or two values
+ *             in device memory, 8-byte aligned, in place of seed and offset
+ *   strides   of x, residual, y, h, or NULL
+ * D in [1,16384]; B*H*L below 2^31; any of B, H, L may be 0.
+ * flags: PDSSM_DATA_BF16.
+ */
+int pdssm_layer_norm_fwd(const void *x, const void *residual, const float *w, const float *b,
+                         void *y, void *h, int64_t B, int64_t H, int64_t L, int32_t D, float eps,
+                         double p, uint64_t seed, uint64_t offset, const uint64_t *rng,
+                         uint32_t flags, const pdssm_strides *strides, hipStream_t stream);
+
+/*
+ * Gradients of pdssm_layer_norm_fwd from h (as stored) and dy, the gradient
+ * of y.
+ *   dh        the gradient that h has from elsewhere, or NULL for zero
+ *   dr        the gradient of h (of the residual, and without dropout of x),
+ *             or NULL when not wanted; may be dy, dh or h
+ *   dx        the gradient of x, or NULL when not wanted; may be dy, dh or h,
+ *             not dr
+ *   dw, db    fp32 [D] gradients of w and b, or NULL when not wanted (a w of
+ *             NULL counts as ones)
+ *   strides   of h, dy, dh, dr, dx, or NULL
+ *   workspace pdssm_layer_norm_bwd_workspace_bytes bytes, 16-byte aligned; NULL
+ *             when neither dw nor db is wanted
+ * With no rows, dw and db are zero.
+ */
+int pdssm_layer_norm_bwd(const void *h, const void *dy, const void *dh, const float *w, void *dr,
+                         void *dx, float *dw, float *db, int64_t B, int64_t H, int64_t L,
+                         int32_t D, float eps, double p, uint64_t seed, uint64_t offset,
+                         const uint64_t *rng, uint32_t flags, const pdssm_strides *strides,
+                         void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of pdssm_layer_norm_bwd with dw or db (512 rows of sums at
+ * most); 0 when the arguments are invalid. */
+size_t pdssm_layer_norm_bwd_workspace_bytes(int64_t B, int64_t H, int64_t L, int32_t D);
+
+/*
+ * y = residual + dropout(x) (see above); the gradient of x is dropout of y's
+ * with the same seed and offset.
+ *   x, residual, y  [B,H,L,D]; residual NULL for zero; y may be x or residual
+ *   strides   of x, residual, y, or NULL
+ * Sizes and flags as pdssm_layer_norm_fwd.
+ */
+int pdssm_dropout(const void *x, const void *residual, void *y, int64_t B, int64_t H, int64_t L,
+                  int32_t D, double p, uint64_t seed, uint64_t offset, const uint64_t *rng,
+                  uint32_t flags, const pdssm_strides *strides, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

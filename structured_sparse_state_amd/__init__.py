@@ -140,6 +140,15 @@ def _load(path: str) -> ctypes.CDLL:
         for size in (lib.pdssm_linear_workspace_bytes, lib.pdssm_linear_bwd_workspace_bytes):
             size.argtypes = [I64] * 4 + [I32, I32, U32]
             size.restype = SZ
+        U64, DB = ctypes.c_uint64, ctypes.c_double
+        lib.pdssm_layer_norm_fwd.argtypes = [P] * 6 + [I64] * 3 + [I32, F, DB, U64, U64, P, U32, P, P]
+        lib.pdssm_layer_norm_fwd.restype = ctypes.c_int
+        lib.pdssm_layer_norm_bwd.argtypes = [P] * 8 + [I64] * 3 + [I32, F, DB, U64, U64, P, U32, P, P, SZ, P]
+        lib.pdssm_layer_norm_bwd.restype = ctypes.c_int
+        lib.pdssm_layer_norm_bwd_workspace_bytes.argtypes = [I64] * 3 + [I32]
+        lib.pdssm_layer_norm_bwd_workspace_bytes.restype = SZ
+        lib.pdssm_dropout.argtypes = [P] * 3 + [I64] * 3 + [I32, DB, U64, U64, P, U32, P, P]
+        lib.pdssm_dropout.restype = ctypes.c_int
     return lib
 
 
@@ -1065,3 +1074,161 @@ def linear_attention_step(q, k, v, g, s, *, s_out: Optional[torch.Tensor] = None
                                       o.data_ptr(), s_out.data_ptr(), B, Hk, Hv, Dk, Dv,
                                       Dk ** -0.5 if scale is None else scale, flag, rows, _stream_of(v, stream)))
     return o
+
+
+def pdssm_layer_norm_fwd(x, residual, w, b, y, h, B, H, L, D, eps, p, seed, offset, rng, flags, strides,
+                         stream=None) -> int:
+    return library().pdssm_layer_norm_fwd(_ptr(x), _ptr(residual), _ptr(w), _ptr(b), _ptr(y), _ptr(h), B, H, L, D,
+                                          eps, p, seed, offset, _ptr(rng), flags, _strides(strides),
+                                          _stream(stream))
+
+
+def pdssm_layer_norm_bwd(h, dy, dh, w, dr, dx, dw, db, B, H, L, D, eps, p, seed, offset, rng, flags, strides,
+                         workspace, workspace_bytes, stream=None) -> int:
+    return library().pdssm_layer_norm_bwd(_ptr(h), _ptr(dy), _ptr(dh), _ptr(w), _ptr(dr), _ptr(dx), _ptr(dw),
+                                          _ptr(db), B, H, L, D, eps, p, seed, offset, _ptr(rng), flags,
+                                          _strides(strides), _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def pdssm_layer_norm_bwd_workspace_bytes(B, H, L, D) -> int:
+    return library().pdssm_layer_norm_bwd_workspace_bytes(B, H, L, D)
+
+
+def pdssm_dropout(x, residual, y, B, H, L, D, p, seed, offset, rng, flags, strides, stream=None) -> int:
+    return library().pdssm_dropout(_ptr(x), _ptr(residual), _ptr(y), B, H, L, D, p, seed, offset, _ptr(rng), flags,
+                                   _strides(strides), _stream(stream))
+
+
+def _block_rows(*forms):
+    """The (b, h, l) triples of row tensors [D] to [B,H,L,D] (None: zeros)."""
+    out = []
+    for form in forms:
+        if form is None:
+            out.append((0, 0, 0))
+            continue
+        shape, st = form[:2]
+        if st[-1] != 1 and shape[-1] > 1:
+            raise ValueError("the last dimension must be contiguous")
+        out.append((*(0,) * (4 - len(shape)), *st[:-1]))
+    return _strides(out)
+
+
+def _block_form(name, x, rng, w, b, others):
+    """Flag and sizes (B, H, L, D) of a call on rows like x."""
+    if not 1 <= len(x[0]) <= 4:
+        raise ValueError(f"{name} must have one to four dimensions")
+    flag = _data_flag("row tensors", *(f[2] for f in (x, *others.values()) if f is not None))
+    for other, form in others.items():
+        _want(other, form, x[0], x[2])
+    D = x[0][-1]
+    _want("w", w, (D,), torch.float32, True)
+    _want("b", b, (D,), torch.float32, True)
+    _want("seed", rng, (2,), torch.int64, True)
+    _one_device(x, rng, w, b, *others.values())
+    return (flag, *(1,) * (4 - len(x[0])), *x[0])
+
+
+def _seed(seed, offset):
+    """(seed, offset, the tensor that holds both or None) of a call."""
+    if isinstance(seed, torch.Tensor):
+        if offset:
+            raise ValueError("a seed tensor holds the offset too")
+        return 0, 0, seed
+    return seed & 0xFFFFFFFFFFFFFFFF, offset & 0xFFFFFFFFFFFFFFFF, None
+
+
+def _drops(p: float) -> bool:
+    """Whether dropout with p drops anything (its 16-bit threshold is above 0)."""
+    return p * 65536 + 0.5 >= 1
+
+
+@functools.lru_cache(maxsize=1024)
+def _layer_norm_plan(x, w, b, residual, y, h, rng):
+    sizes = _block_form("x", x, rng, w, b, {"residual": residual, "y": y, "h": h})
+    return sizes, _block_rows(x, residual, y, h)
+
+
+def layer_norm(x, w=None, b=None, *, residual=None, eps: float = 1e-5, p: float = 0.0, seed=0, offset: int = 0,
+               out: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None, stream=None):
+    """The layer norm over the last dimension of h = residual + dropout(x):
+    (y, h).  x and residual bf16 or fp32 of one to four dimensions, any strides
+    but the last; w, b fp32 [D] or None (1 and 0).  Without residual and dropout
+    h is x itself, unless a place for it is given.  ``p``: the part of x that is
+    dropped; ``seed`` and ``offset`` pick the mask, or an int64 GPU tensor [2] in
+    place of seed holds both.  The results have the memory order of x; ``out``
+    and ``h``: tensors to write into instead (x or residual among them)."""
+    if stream is not None and (out is None or (h is None and (residual is not None or _drops(p)))):
+        return _on_stream(stream, layer_norm, x, w, b, residual=residual, eps=eps, p=p, seed=seed, offset=offset,
+                          out=out, h=h)
+    y = torch.empty_like(x) if out is None else out
+    to = h
+    if h is None and (residual is not None or _drops(p)):
+        h = to = torch.empty_like(x)
+    seed, offset, rng = _seed(seed, offset)
+    (flag, B, H, L, D), rows = _layer_norm_plan(_form(x), _form(w), _form(b), _form(residual), _form(y), _form(to),
+                                                _form(rng))
+    check(library().pdssm_layer_norm_fwd(x.data_ptr(), _ptr(residual), _ptr(w), _ptr(b), y.data_ptr(), _ptr(to), B,
+                                         H, L, D, eps, p, seed, offset, _ptr(rng), flag, rows,
+                                         _stream_of(x, stream)))
+    return y, x if h is None else h
+
+
+@functools.lru_cache(maxsize=1024)
+def _layer_norm_bwd_plan(h, w, dy, dh, dr, dx, rng, sums):
+    sizes = _block_form("h", h, rng, w, None, {"dy": dy, "dh": dh, "dr": dr, "dx": dx})
+    need = _need(pdssm_layer_norm_bwd_workspace_bytes(*sizes[1:])) if sums else 0
+    return sizes, _block_rows(h, dy, dh, dr, dx), need
+
+
+def layer_norm_bwd(h, dy, w=None, *, dh=None, want_db: bool = False, eps: float = 1e-5, p: float = 0.0, seed=0,
+                   offset: int = 0, out=None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of layer_norm from h, the gradient dy of y and the one dh that h
+    has from elsewhere (None: zero): (dr, dx, dw, db), of h (and the residual), of
+    x (without dropout dr itself), of w (None without it) and of b (with
+    want_db).  p, seed and offset as in the forward.  ``out``: dr and dx to write
+    into instead (of dy, dh and h; one tensor twice without dropout)."""
+    if stream is not None and (out is None or w is not None or want_db):
+        return _on_stream(stream, layer_norm_bwd, h, dy, w, dh=dh, want_db=want_db, eps=eps, p=p, seed=seed,
+                          offset=offset, out=out, workspace=workspace)
+    drops = _drops(p)
+    dr, dx = (torch.empty_like(h), torch.empty_like(h) if drops else None) if out is None else out
+    if dx is None:
+        dx = dr
+    if drops and dx is dr:
+        raise ValueError("with dropout dr and dx are two tensors")
+    seed, offset, rng = _seed(seed, offset)
+    sums = w is not None or want_db
+    to = None if dx is dr else dx
+    (flag, B, H, L, D), rows, need = _layer_norm_bwd_plan(_form(h), _form(w), _form(dy), _form(dh), _form(dr),
+                                                          _form(to), _form(rng), sums)
+    dw = None if w is None else torch.empty_like(w)
+    db = torch.empty(D, dtype=torch.float32, device=h.device) if want_db else None
+    if need:
+        workspace = _workspace(need, workspace, h.device)
+    check(library().pdssm_layer_norm_bwd(h.data_ptr(), dy.data_ptr(), _ptr(dh), _ptr(w), dr.data_ptr(), _ptr(to),
+                                         _ptr(dw), _ptr(db), B, H, L, D, eps, p, seed, offset, _ptr(rng), flag,
+                                         rows, workspace.data_ptr() if need else None, need,
+                                         _stream_of(h, stream)))
+    return dr, dx, dw, db
+
+
+@functools.lru_cache(maxsize=1024)
+def _dropout_plan(x, residual, y, rng):
+    sizes = _block_form("x", x, rng, None, None, {"residual": residual, "y": y})
+    return sizes, _block_rows(x, residual, y)
+
+
+def dropout(x, p: float, seed, offset: int = 0, *, residual=None, out: Optional[torch.Tensor] = None, stream=None):
+    """residual + dropout(x), the mask from ``seed`` and ``offset`` (or an int64
+    GPU tensor [2] of both as seed) by value and place, never stored.  The
+    gradient of x is dropout of the result's with the same seed and offset.  x
+    bf16 or fp32 of one to four dimensions, any strides but the last; ``out``: a
+    tensor to write into (x or residual among them)."""
+    if stream is not None and out is None:
+        return _on_stream(stream, dropout, x, p, seed, offset, residual=residual)
+    y = torch.empty_like(x) if out is None else out
+    seed, offset, rng = _seed(seed, offset)
+    (flag, B, H, L, D), rows = _dropout_plan(_form(x), _form(residual), _form(y), _form(rng))
+    check(library().pdssm_dropout(x.data_ptr(), _ptr(residual), y.data_ptr(), B, H, L, D, p, seed, offset,
+                                  _ptr(rng), flag, rows, _stream_of(x, stream)))
+    return y

@@ -29,7 +29,8 @@ SOURCES = [os.path.join(CSRC, f) for f in ("pdssm_scan.hip", "pdssm_bwd.hip", "p
                                             "pdssm_router.hip")]
 # Operators beside the scan (include/pdssm_layers.h, include/pdssm_block.h): in
 # libpdssm.so only, the test builds change nothing of them.
-LAYER_SOURCES = [os.path.join(CSRC, f) for f in ("pdssm_delta.hip", "pdssm_norm.hip", "pdssm_linear.hip")]
+LAYER_SOURCES = [os.path.join(CSRC, f) for f in ("pdssm_delta.hip", "pdssm_norm.hip", "pdssm_linear.hip",
+                                                 "pdssm_layer_norm.hip")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",
