@@ -67,6 +67,10 @@ struct Chunk {
         r = make_rsrc(static_cast<const char *>(base) + (e0 + t0 * s) * kSize,
                       none ? 0 : (uint64_t)(rows - 1) * stride + D * kSize);
     }
+    __device__ __forceinline__ Chunk(__amdgpu_buffer_rsrc_t r_, uint32_t stride_, int rows_, int D_)
+        : r(r_), stride(stride_), rows(rows_), D(D_)
+    {
+    }
     // A lane's own part of an offset.  Opaque, so that the offsets of a loop's
     // many rows are formed where they are used (an addition of a scalar each)
     // and not held in registers across the loop.
@@ -156,6 +160,32 @@ struct Chunk {
         else
             __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, at(lane, row, up, col), 0, 0);
     }
+};
+
+// The chunks of a sequence one after another: the place of the next one and the
+// way to the one behind it, formed once (the address of a chunk from its number
+// costs scalar loads and products that a walk waits for).
+struct Stream {
+    const char *at;
+    int64_t step;           // bytes
+    uint32_t stride, width; // bytes between rows, of a row
+
+    __device__ __forceinline__ Stream(const void *base, int64_t e0, int64_t s, int c, bool back, int D, int size)
+    {
+        at = static_cast<const char *>(base) + (e0 + (int64_t)c * kC * s) * size;
+        step = (back ? -kC : kC) * s * size;
+        stride = (uint32_t)s * (uint32_t)size;
+        width = (uint32_t)(D * size);
+    }
+    // The chunk here, of `rows` rows (none: 0).
+    template <bool BF16, bool VEC>
+    __device__ __forceinline__ Chunk<BF16, VEC> chunk(int rows, int D) const
+    {
+        const uint32_t bytes = rows > 0 ? (uint32_t)(rows - 1) * stride + width : 0;
+        return Chunk<BF16, VEC>(__builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(at), (short)0, (int)bytes, 0x00020000), stride,
+                                rows, D);
+    }
+    __device__ __forceinline__ void next(bool move) { at += move ? step : 0; }
 };
 
 template <bool BF16>

@@ -43,12 +43,14 @@ namespace {
 
 constexpr int kMaxDim = 128;
 constexpr int kSlice = 64;          // columns of the state in a workgroup
-constexpr int kHelp = 256, kWalkThreads = 256 + kHelp;
+constexpr int kChain = 4;           // chain waves
+constexpr int kHelp = 256;          // help threads
+constexpr int kWalkThreads = kChain * 64 + kHelp;
 
 // Vectors of a chunk in LDS: what the rows read of the state and write to it,
 // the state's own decay, G log2(e) as a pair of floats and the steps that
-// empty the state, counted.
-enum LinVec { kRead, kWrite, kWhole, kGhi, kGlo, kResets, kVecs };
+// empty the state, counted; for dg what dQ's walk left in `reads`.
+enum LinVec { kRead, kWrite, kWhole, kGhi, kGlo, kResets, kReads, kVecs };
 
 struct Walk {
     Rows x1, x2, x3, y;
@@ -106,7 +108,7 @@ struct LinLds {
     static constexpr int kM = kX3 + kHalves * T3::kSize;
     // in floats
     static constexpr int kVec = (kM + kHalves * M::kSize) / 2;
-    static constexpr int kCuts = kVec + kHalves * kVecs * kC;
+    static constexpr int kCuts = kVec + 4 * kVecs * kC;             // (the gates' vectors are a chunk further ahead)
     static constexpr int kWrites = kCuts + kHalves * Cuts::kSize;   // [4 waves][64]: k . what dK reads of dS
     static constexpr int kCross = kWrites + kHalves * 4 * kC;       // [4 waves]: <whole S, dS>
     static constexpr int kFlag = kCross + kHalves * 4;              // [4] help waves, [4] spoiled
@@ -126,10 +128,10 @@ __device__ __forceinline__ void each_value(const Walk &w, int col, int lane, F f
         }
 }
 
-// c + A B for four tiles at once, part products of order below 3, the small
-// ones first.
-template <int NA, int NB>
-__device__ __forceinline__ void mma4(const Frag<NA> &a, const Frag<NB> (&b)[4], f32x4 (&c)[4])
+// c + A B for the tiles FIRST .. LAST side by side, part products of order
+// below 3, the small ones first.
+template <int FIRST, int LAST, int N, int NA, int NB>
+__device__ __forceinline__ void mma_tiles(const Frag<NA> &a, const Frag<NB> (&b)[N], f32x4 (&c)[N])
 {
 #pragma unroll
     for (int o = 2; o >= 0; --o)
@@ -138,7 +140,7 @@ __device__ __forceinline__ void mma4(const Frag<NA> &a, const Frag<NB> (&b)[4], 
             const int j = o - i;
             if (j >= 0 && j < NB) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
+                for (int t = FIRST; t <= LAST; ++t)
                     c[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b[t].p[j], c[t], 0, 0, 0);
             }
         }
@@ -155,12 +157,68 @@ __device__ __forceinline__ f32x8 joined(const Frag<N> &f)
     return v;
 }
 
+// Three parts of what meets rows of NK parts in a product.
+template <int NK>
+__device__ __forceinline__ Frag<3> parts(f32x8 v)
+{
+    if constexpr (NK == 1)
+        return split_cut(v);
+    else
+        return split<3>(v);
+}
+template <int NK>
+__device__ __forceinline__ Frag<3> parts(f32x4 a, f32x4 b)
+{
+    return parts<NK>(__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
 __device__ __forceinline__ float sum64(float v)
 {
 #pragma unroll
     for (int m = 32; m >= 1; m >>= 1)
         v += __shfl_xor(v, m, 64);
     return v;
+}
+
+// The running sum over the wave's lanes: shifts inside rows of 16, then the rows'
+// last values on, without a trip through LDS.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float shifted(float v)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double shifted(double v)
+{
+    return __hiloint2double(__builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, ROWS, 0xF, false),
+                            __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, ROWS, 0xF, false));
+}
+template <typename T>
+__device__ __forceinline__ T running_sum(T v)
+{
+    v += shifted<0x111, 0xF>(v);    // row_shr 1, 2, 4, 8
+    v += shifted<0x112, 0xF>(v);
+    v += shifted<0x114, 0xF>(v);
+    v += shifted<0x118, 0xF>(v);
+    v += shifted<0x142, 0xA>(v);    // row_bcast 15 to rows 1 and 3
+    v += shifted<0x143, 0xC>(v);    // row_bcast 31 to rows 2 and 3
+    return v;
+}
+__device__ __forceinline__ float first_lane(float v) { return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v))); }
+__device__ __forceinline__ float last_lane(float v) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63)); }
+
+// Returns once all four flags are at least v (see LdsFlag).
+__device__ __forceinline__ void await_all(int *flags, int v)
+{
+    typedef int i32x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) i32x4 lds_i32x4;
+    for (;;) {
+        const i32x4 f = *(volatile lds_i32x4 *)(lds_i32x4 *)flags;
+        if (min(min(f[0], f[1]), min(f[2], f[3])) >= v)
+            break;
+        __builtin_amdgcn_s_sleep(1);
+    }
+    asm volatile("" ::: "memory");
 }
 
 __device__ __forceinline__ int scalar(unsigned v) { return __builtin_amdgcn_readfirstlane((int)v); }
@@ -185,18 +243,20 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
     const int p0 = seg * a.seg_chunks, p1 = min(a.NC, p0 + a.seg_chunks);
     const int64_t b = scalar((unsigned)head / (unsigned)a.Hv);
     const int h = (int)head - (int)b * a.Hv, hk = scalar((unsigned)h / (unsigned)(a.Hv / a.Hk));
-    const int lane = thread & 63, wave = thread >> 6, g = lane >> 4, i16 = lane & 15, mine = wave & 3;
+    const int lane = thread & 63, wave = scalar(thread >> 6), g = lane >> 4, i16 = lane & 15, mine = wave & 3;
     auto chunk_of = [&](int p) { return BACK ? a.NC - 1 - p : p; };
     auto half_of = [&](int p) { return LDS::kHalves == 2 ? (p - p0) & 1 : 0; };
     auto begin = [&](const Rows &x, bool kv) { return b * x.s.b + (kv ? hk : h) * x.s.h; };
-    auto vecs = [&](int half) { return ldf + LDS::kVec + half * kVecs * kC; };
+    auto vecs = [&](int p) { return ldf + LDS::kVec + ((p - p0) & 3) * (kVecs * kC); };
+    auto rows_of = [&](int p) { return min(kC, a.L - chunk_of(p) * kC); };
+    constexpr int kSize = BF16 ? 2 : 4;
 
-    if (wave >= 4 && lane == 0)
+    if (wave >= kChain && lane == 0)
         s_help[mine] = 0;
     lds_barrier();
     bool again = false;
 
-    if (wave < 4) {
+    if (wave < kChain) {
         const int col = slice * kSlice + mine * 16 + i16;
         const int col4 = slice * kSlice + mine * 16 + 4 * g;    // of the lane's four values of y
         f32x4 S[KD / 16];
@@ -224,14 +284,20 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
         if constexpr (MODE == kOut) {
 #pragma unroll
             for (int s = 0; s < NS; ++s)
-                sf[s] = split<3>(S[2 * s], S[2 * s + 1]);
+                sf[s] = parts<NK>(S[2 * s], S[2 * s + 1]);
         }
-        f32x4 beside[4];        // dg: the next chunk's values of x4 beside y's
+        f32x4 beside[4];       // dg: the next chunk's values of x4 beside y's
         f32x4 kept[GATE == kGrad ? KD / 16 : 1];
+        const int pitch = (w.D3 + 3) / 4 * 4;
+        const bool wide = BF16 && w.wide;
+        Stream out(w.y.p, wide ? head * a.L * pitch : begin(w.y, w.kvy), wide ? pitch : w.y.s.l, chunk_of(p0), BACK,
+                   wide ? pitch : w.D3, wide ? 4 : kSize);
+        Stream x4(w.x4.p, begin(w.x4, true), w.x4.s.l, chunk_of(p0), BACK, w.D3, kSize);
         auto fetch = [&](int p) {
             const int c = chunk_of(p);
             if constexpr (GATE != kNone) {
-                const Chunk<BF16, VEC> cx(w.x4.p, begin(w.x4, true), w.x4.s.l, c * kC, a.L, w.D3);
+                const Chunk<BF16, VEC> cx = x4.chunk<BF16, VEC>(rows_of(p), w.D3);
+                x4.next(p + 1 < p1);
                 const uint32_t e = cx.lane_at(i16, col4);
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
@@ -254,7 +320,7 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
             const int half = half_of(p), c = chunk_of(p);
             const uint16_t *s_x1 = lds + LDS::kX1 + half * T1::kSize, *s_x2 = lds + LDS::kX2 + half * T1::kSize;
             const uint16_t *s_x3 = lds + LDS::kX3 + half * T3::kSize, *s_m = lds + LDS::kM + half * M::kSize;
-            const float *s_vec = vecs(half);
+            const float *s_vec = vecs(p);
             Frag<NK> x3[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s)
@@ -285,9 +351,8 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
                         }
                     }
             }
+            f32x4 Y[4];    // tiles of 16 columns (rows of the result) by 16 steps
             if constexpr (MODE == kOut) {
-                // Y as tiles of 16 columns (rows of the result) by 16 steps
-                f32x4 Y[4];
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
                     Y[t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -297,7 +362,7 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
 #pragma unroll
                     for (int t = 0; t < 4; ++t)
                         x1[t] = T1::rows_stacked(s_x1, t, s, lane);
-                    mma4(sf[s], x1, Y);
+                    mma_tiles<0, 3>(sf[s], x1, Y);
                 }
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
@@ -310,8 +375,7 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
                         float v = Y[t][0] * beside[t][0] + Y[t][1] * beside[t][1] + Y[t][2] * beside[t][2] + Y[t][3] * beside[t][3];
                         v += __shfl_xor(v, 16, 64);
                         v += __shfl_xor(v, 32, 64);
-                        if (g == 0)
-                            to[16 * t + i16] = v;
+                        to[16 * t + i16] = v;     // (the four lanes of a step all write it)
                     }
                 }
                 if constexpr (GATE == kKeep) {
@@ -326,8 +390,7 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
                     for (int m = 0; m < KD / 16; ++m)
                         v += kept[m][0] * S[m][0] + kept[m][1] * S[m][1] + kept[m][2] * S[m][2] + kept[m][3] * S[m][3];
                     v = sum64(v);
-                    if (lane == 0)
-                        ldf[LDS::kCross + half * 4 + mine] = v * s_vec[kWhole * kC];
+                    ldf[LDS::kCross + half * 4 + wave] = v * s_vec[kWhole * kC];
                 }
                 if constexpr (GATE != kNone)
                     fetch(min(p + 1, p1 - 1));
@@ -338,16 +401,13 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
                     for (int t = 0; t < 4; ++t)
                         if (M::has(t, s))
                             m[t] = M::template get<3>(s_m, t, s, lane);
-#pragma unroll
-                    for (int o = 2; o >= 0; --o)
-#pragma unroll
-                        for (int i = 0; i < NK; ++i)
-                            if (o - i >= 0) {
-#pragma unroll
-                                for (int t = 0; t < 4; ++t)
-                                    if (M::has(t, s))
-                                        Y[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x3[s].p[i], m[t].p[o - i], Y[t], 0, 0, 0);
-                            }
+                    // (the triangle has all tiles of one k step, half of the other's)
+                    if (s == (BACK ? 1 : 0))
+                        mma_tiles<0, 3>(x3[s], m, Y);
+                    else if (BACK)
+                        mma_tiles<0, 1>(x3[s], m, Y);
+                    else
+                        mma_tiles<2, 3>(x3[s], m, Y);
                 }
                 if constexpr (CAREFUL) {
 #pragma unroll
@@ -361,18 +421,6 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
                         }
                     }
                 }
-                auto store = [&](auto cy) {
-                    const uint32_t e = cy.lane_at(i16, col4);
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        cy.put4(e, i16, 16 * t, col4, Y[t]);
-                };
-                if (BF16 && w.wide) {
-                    const int pitch = (w.D3 + 3) / 4 * 4;
-                    store(Chunk<false, VEC>(w.y.p, head * a.L * pitch, pitch, c * kC, a.L, pitch));
-                } else {
-                    store(Chunk<BF16, VEC>(w.y.p, begin(w.y, w.kvy), w.y.s.l, c * kC, a.L, w.D3));
-                }
             }
             // the state
             const float whole = s_vec[kWhole * kC] * gone;
@@ -381,7 +429,7 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const f32x4 lo = row_vec(s_vec, kWrite, 2 * s, lane), hi = row_vec(s_vec, kWrite, 2 * s + 1, lane);
-                wx[s] = split<3>(joined(x3[s]) * __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                wx[s] = parts<NK>(joined(x3[s]) * __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
             }
 #pragma unroll
             for (int m = 0; m < KD / 16; ++m)
@@ -407,7 +455,20 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
                                                                                           S[2 * s + m], 0, 0, 0);
                         }
                 if constexpr (MODE == kOut)
-                    sf[s] = split<3>(S[2 * s], S[2 * s + 1]);
+                    sf[s] = parts<NK>(S[2 * s], S[2 * s + 1]);
+            }
+            if constexpr (MODE == kOut) {
+                auto store = [&](auto cy) {
+                    const uint32_t e = cy.lane_at(i16, col4);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        cy.put4(e, i16, 16 * t, col4, Y[t]);
+                };
+                if (wide)
+                    store(out.chunk<false, VEC>(rows_of(p), pitch));
+                else
+                    store(out.chunk<BF16, VEC>(rows_of(p), w.D3));
+                out.next(true);
             }
             lds_barrier();
         }
@@ -439,119 +500,169 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
             }
         }
     } else {
-        const int tid = thread - 256;
-        T1 t1, t2;
-        T3 t3;
-        float gate;
-        Unit<BF16> kf[GATE == kGrad ? 2 : 1];       // the wave's rows of k
-        auto fetch = [&](int p) {
-            const int t0 = chunk_of(p) * kC;
-            if constexpr (MODE == kOut)
-                t1.load(Chunk<BF16, VEC>(w.x1.p, begin(w.x1, w.kv1), w.x1.s.l, t0, a.L, w.D1), tid);
-            t2.load(Chunk<BF16, VEC>(w.x2.p, begin(w.x2, w.kv2), w.x2.s.l, t0, a.L, w.D1), tid);
-            t3.load(Chunk<BF16, VEC>(w.x3.p, begin(w.x3, w.kv3) + slice * kSlice, w.x3.s.l, t0, a.L, w.D3 - slice * kSlice), tid);
-            gate = 0.f;
-            if (a.g.p && t0 + lane < a.L)
-                gate = static_cast<const float *>(a.g.p)[b * a.g.s.b + h * a.g.s.h + (t0 + lane) * a.g.s.l];
+        const int tid = thread - kChain * 64;
+        constexpr int kGateWave = 1;    // (with two blocks of M where others have three)
+        struct Incoming {
+            T1 t1, t2;
+            T3 t3;
+            Unit<BF16> k[GATE == kGrad ? 4 : 1];    // the wave's rows of k
+        };
+        float gate, reads;
+        const int c0 = chunk_of(p0);
+        Stream x1(w.x1.p, begin(w.x1, w.kv1), w.x1.s.l, c0, BACK, w.D1, kSize);
+        Stream x2(w.x2.p, begin(w.x2, w.kv2), w.x2.s.l, c0, BACK, w.D1, kSize);
+        const int cols = w.D3 - slice * kSlice;
+        Stream x3(w.x3.p, begin(w.x3, w.kv3) + slice * kSlice, w.x3.s.l, c0, BACK, cols, kSize);
+        Stream x4(w.x4.p, begin(w.x4, true) + slice * kSlice, w.x4.s.l, c0, BACK, cols, kSize);
+        Stream gates(a.g.p, b * a.g.s.b + h * a.g.s.h, a.g.s.l, c0, BACK, 1, 4);
+        const bool has_gates = a.g.p != nullptr, has_steps = has_gates && a.g.s.l != 0;
+        // (no branches on the way of the loads: where two paths with other loads
+        // in flight meet, a wait for one becomes a wait for all)
+        auto fetch = [&](Incoming &in, int p) {
+            const int rows = rows_of(p);
+            const bool move = p + 1 < p1;
+            if constexpr (MODE == kOut) {
+                in.t1.load(x1.chunk<BF16, VEC>(rows, w.D1), tid);
+                x1.next(move);
+            }
+            in.t2.load(x2.chunk<BF16, VEC>(rows, w.D1), tid);
+            x2.next(move);
+            in.t3.load(x3.chunk<BF16, VEC>(rows, cols), tid);
+            x3.next(move);
             if constexpr (GATE == kGrad) {
-                const Chunk<BF16, VEC> ck(w.x4.p, begin(w.x4, true), w.x4.s.l, t0, a.L, w.D3);
+                const Chunk<BF16, VEC> ck = x4.chunk<BF16, VEC>(rows, cols);
+                x4.next(move);
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
-                    kf[s] = ck.unit(16 * mine + i16, slice * kSlice + 32 * s + 8 * g);
+                for (int s = 0; s < 4; ++s)
+                    in.k[s] = ck.unit(16 * (s >= 2 && mine == 0 ? 0 : 3 - mine) + i16, 32 * (s & 1) + 8 * g);
             }
         };
-        // Rows, gates and M of chunk p into its half of LDS, chunk p + 1 on its way.
-        auto prepare = [&](int p) {
+        auto fetch_gate = [&](int p) {
+            const Chunk<false, false> cg = gates.chunk<false, false>(has_gates ? rows_of(p) : 0, 1);
+            gates.next(p + 1 < p1);
+            gate = __uint_as_float(cg.raw(cg.lane_at(lane, 0), lane, 0, 0));
+            if constexpr (GATE == kGrad) {
+                const float *r = a.reads + (((int64_t)chunk_of(p) * w.slices + slice) * a.heads + head) * 4 * kC + lane;
+                reads = (r[0] + r[kC]) + (r[2 * kC] + r[3 * kC]);
+            }
+        };
+        // The gates' vectors of chunk p (one wave), from the values fetched, those
+        // of chunk p + 1 on their way.
+        auto sum_gates = [&](int p) {
+            // (the same for every whole chunk where the gates do not change from
+            // step to step)
+            if (mine != kGateWave || !(GATE == kGrad || has_steps || p - p0 < 4 || rows_of(p) != rows_of(p - 4)))
+                return;
+            // G log2(e) in 64 bits (differences of neighbours stay exact to 32),
+            // steps that empty the state counted apart.
+            float *s_vec = vecs(p);
+            const float now = has_steps ? gate : lane < rows_of(p) ? first_lane(gate) : 0.f;
+            const bool empty = now < kEmpties;
+            const double G = running_sum(empty ? 0.0 : (double)now * 1.4426950408889634);
+            const float n = running_sum(empty ? 1.f : 0.f);
+            const float hi = (float)G, lo = (float)(G - (double)hi);
+            const float hi1 = last_lane(hi), lo1 = last_lane(lo), n1 = last_lane(n);
+            const float rise = a.scale * decay_of(hi, lo, n, 0.f, 0.f, 0.f), left = decay_of(hi1, lo1, n1, hi, lo, n);
+            s_vec[kRead * kC + lane] = BACK ? left : rise;
+            s_vec[kWrite * kC + lane] = BACK ? rise : left;
+            s_vec[kWhole * kC + lane] = decay_of(hi1, lo1, n1, 0.f, 0.f, 0.f);
+            s_vec[kGhi * kC + lane] = hi;
+            s_vec[kGlo * kC + lane] = lo;
+            s_vec[kResets * kC + lane] = n;
+            if constexpr (GATE == kGrad)
+                s_vec[kReads * kC + lane] = reads;
+            fetch_gate(min(p + 1, p1 - 1));
+        };
+        // Rows and M of chunk p into its half of LDS, the rows of chunk p + 1 on
+        // their way, and the gates of chunk p + 1.
+        auto prepare = [&](Incoming &in, int p) {
             const int half = half_of(p);
             uint16_t *s_x1 = lds + LDS::kX1 + half * T1::kSize, *s_x2 = lds + LDS::kX2 + half * T1::kSize;
             uint16_t *s_x3 = lds + LDS::kX3 + half * T3::kSize;
-            float *s_vec = vecs(half);
+            const float *s_vec = vecs(p);
             if constexpr (MODE == kOut)
-                t1.store(s_x1, tid);
-            t2.store(s_x2, tid);
-            t3.store(s_x3, tid);
-            Frag<NK> kr[GATE == kGrad ? 2 : 1];
+                in.t1.store(s_x1, tid);
+            in.t2.store(s_x2, tid);
+            in.t3.store(s_x3, tid);
+            Frag<NK> kr[4];
             if constexpr (GATE == kGrad) {
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
-                    kr[s] = unit_frag<BF16>(kf[s]);
+                for (int s = 0; s < 4; ++s)
+                    kr[s] = unit_frag<BF16>(in.k[s]);
             }
-            if (mine == 0) {
-                // G log2(e) in 64 bits (differences of neighbours stay exact to
-                // 32), steps that empty the state counted apart.
-                const bool empty = gate < kEmpties;
-                double G = empty ? 0.0 : (double)gate * 1.4426950408889634;
-                float n = empty ? 1.f : 0.f;
-#pragma unroll
-                for (int m = 1; m < 64; m <<= 1) {
-                    const double x = __shfl_up(G, m, 64);
-                    const float y = __shfl_up(n, m, 64);
-                    if (lane >= m) {
-                        G += x;
-                        n += y;
-                    }
-                }
-                const float hi = (float)G, lo = (float)(G - (double)hi);
-                const float hi1 = __shfl(hi, 63, 64), lo1 = __shfl(lo, 63, 64), n1 = __shfl(n, 63, 64);
-                const float rise = a.scale * decay_of(hi, lo, n, 0.f, 0.f, 0.f), left = decay_of(hi1, lo1, n1, hi, lo, n);
-                s_vec[kRead * kC + lane] = BACK ? left : rise;
-                s_vec[kWrite * kC + lane] = BACK ? rise : left;
-                s_vec[kWhole * kC + lane] = decay_of(hi1, lo1, n1, 0.f, 0.f, 0.f);
-                s_vec[kGhi * kC + lane] = hi;
-                s_vec[kGlo * kC + lane] = lo;
-                s_vec[kResets * kC + lane] = n;
-            }
-            fetch(min(p + 1, p1 - 1));
+            fetch(in, min(p + 1, p1 - 1));
             if constexpr (MODE == kOut) {
-                // the other help waves' rows
+                // the other help waves' rows (and the gates, summed a turn before)
                 if (lane == 0)
                     LdsFlag::set(&s_help[mine], p - p0 + 1);
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-                    LdsFlag::await(&s_help[m], p - p0 + 1);
+                await_all(s_help, p - p0 + 1);
                 uint16_t *s_m = lds + LDS::kM + half * M::kSize;
-                const int row = 16 * mine + i16;
-                const float hi = s_vec[kGhi * kC + row], lo = s_vec[kGlo * kC + row], n = s_vec[kResets * kC + row];
-                Frag<NK> x1[NS];
+                // Three blocks for each wave in one run of code, whose waits
+                // overlap: of the lower triangle (0,0) and (3,3); (1,0) and (1,1);
+                // (2,0) to (2,2); (3,0) to (3,2), two of them twice; mirrored going
+                // back.
+                int ta[3], tb[3];
 #pragma unroll
-                for (int s = 0; s < NS; ++s)
-                    x1[s] = T1::rows(s_x1, mine, s, lane);
-#pragma unroll
-                for (int tb = 0; tb < 4; ++tb) {
-                    if (BACK ? tb < mine : tb > mine)
-                        continue;
-                    f32x4 v = {0.f, 0.f, 0.f, 0.f}, kq = v;
-#pragma unroll
-                    for (int s = 0; s < NS; ++s)
-                        v = mma<3>(T1::rows(s_x2, tb, s, lane), x1[s], v);
-                    if constexpr (GATE == kGrad) {
-#pragma unroll
-                        for (int s = 0; s < 2; ++s)
-                            kq = mma<3>(T3::rows(s_x3, tb, s, lane), kr[s], kq);
+                for (int n = 0; n < 3; ++n) {
+                    ta[n] = n && mine == 0 ? 3 : mine;
+                    tb[n] = n && mine == 0 ? 3 : min(n, mine);
+                    if constexpr (BACK) {
+                        ta[n] = 3 - ta[n];
+                        tb[n] = 3 - tb[n];
                     }
-                    const f32x4 hj = row_vec(s_vec, kGhi, tb, lane), lj = row_vec(s_vec, kGlo, tb, lane),
-                                nj = row_vec(s_vec, kResets, tb, lane);
+                }
+                f32x4 v[3], kq[3];
+#pragma unroll
+                for (int n = 0; n < 3; ++n)
+                    v[n] = kq[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int s = 0; s < NS; ++s) {
+                    const Frag<NK> x1[2] = {T1::rows(s_x1, ta[0], s, lane), T1::rows(s_x1, ta[1], s, lane)};
+#pragma unroll
+                    for (int n = 0; n < 3; ++n)
+                        v[n] = mma<3>(T1::rows(s_x2, tb[n], s, lane), x1[n > 0], v[n]);
+                }
+                if constexpr (GATE == kGrad) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int n = 0; n < 3; ++n)
+                            kq[n] = mma<3>(T3::rows(s_x3, tb[n], s, lane), kr[2 * (n > 0) + s], kq[n]);
+                }
+#pragma unroll
+                for (int n = 0; n < 3; ++n) {
+                    const int row = 16 * ta[n] + i16;
+                    const float hi = s_vec[kGhi * kC + row], lo = s_vec[kGlo * kC + row], resets = s_vec[kResets * kC + row];
+                    const f32x4 hj = row_vec(s_vec, kGhi, tb[n], lane), lj = row_vec(s_vec, kGlo, tb[n], lane),
+                                nj = row_vec(s_vec, kResets, tb[n], lane);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int col = 16 * tb + 4 * g + r;
-                        const float d = BACK ? decay_of(hj[r], lj[r], nj[r], hi, lo, n) : decay_of(hi, lo, n, hj[r], lj[r], nj[r]);
-                        v[r] = (BACK ? col >= row : col <= row) ? a.scale * v[r] * d : 0.f;
-                        kq[r] = GATE == kGrad && col > row ? v[r] * kq[r] : 0.f;
+                        const int col = 16 * tb[n] + 4 * g + r;
+                        const float d = BACK ? decay_of(hj[r], lj[r], nj[r], hi, lo, resets) : decay_of(hi, lo, resets, hj[r], lj[r], nj[r]);
+                        v[n][r] = (BACK ? col >= row : col <= row) ? a.scale * v[n][r] * d : 0.f;
+                        kq[n][r] = GATE == kGrad && col > row ? v[n][r] * kq[n][r] : 0.f;
                     }
-                    M::put(s_m, mine, tb, lane, v);
-                    if constexpr (GATE == kGrad)
-                        Cuts::put(ldf + LDS::kCuts + half * Cuts::kSize, tb, mine, kq, lane);
+                    M::put(s_m, ta[n], tb[n], lane, v[n]);
+                }
+                if constexpr (GATE == kGrad) {
+#pragma unroll
+                    for (int n = 0; n < 3; ++n)
+                        Cuts::put(ldf + LDS::kCuts + half * Cuts::kSize, tb[n], ta[n], kq[n], lane);
                 }
             }
+            sum_gates(p + 1);
         };
         // dg of a chunk that the chain has left behind (one wave).
         auto gates_of = [&](int p) {
             if constexpr (GATE == kGrad) {
-                if (mine == 0) {
-                    const int half = half_of(p), c = chunk_of(p), t = c * kC + lane;
-                    const float *s_vec = vecs(half), *s_w = ldf + LDS::kWrites + half * 4 * kC, *s_x = ldf + LDS::kCross + half * 4;
-                    const float *r = a.reads + (((int64_t)c * w.slices + slice) * a.heads + head) * 4 * kC + lane;
-                    const float v = crossing(s_x[0] + s_x[1] + s_x[2] + s_x[3], r[0] + r[kC] + r[2 * kC] + r[3 * kC],
+                if (mine == kGateWave) {
+                    const int half = half_of(p), t = chunk_of(p) * kC + lane;
+                    const float *s_vec = vecs(p), *s_w = ldf + LDS::kWrites + half * 4 * kC, *s_x = ldf + LDS::kCross + half * 4;
+                    float whole = s_x[0];
+#pragma unroll
+                    for (int n = 1; n < kChain; ++n)
+                        whole += s_x[n];
+                    const float v = crossing(whole, s_vec[kReads * kC + lane],
                                              s_w[lane] + s_w[kC + lane] + s_w[2 * kC + lane] + s_w[3 * kC + lane],
                                              ldf + LDS::kCuts + half * Cuts::kSize, lane);
                     // the decay of an empty state does nothing
@@ -571,22 +682,31 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
             for (int n = 0; n < LDS::kHalves; ++n)
                 M::clear(lds + LDS::kM + n * M::kSize, tid);
         }
-        fetch(p0);
-        if constexpr (BF16) {
-            prepare(p0);
-            lds_barrier();
-        }
-        for (int p = p0; p < p1; ++p) {
+        auto behind = [&](int p) {      // the chain has left chunk p - 1
             if (p > p0)
                 gates_of(p - 1);
-            if constexpr (BF16) {
-                if (p + 1 < p1)
-                    prepare(p + 1);
-            } else {
-                prepare(p);
+        };
+        Incoming in;
+        fetch_gate(p0);
+        fetch(in, p0);
+        sum_gates(p0);
+        if constexpr (BF16) {
+            prepare(in, p0);
+            lds_barrier();
+            for (int p = p0; p + 1 < p1; ++p) {
+                behind(p);
+                prepare(in, p + 1);
                 lds_barrier();
             }
+            behind(p1 - 1);
             lds_barrier();
+        } else {
+            for (int p = p0; p < p1; ++p) {
+                behind(p);
+                prepare(in, p);
+                lds_barrier();
+                lds_barrier();
+            }
         }
         gates_of(p1 - 1);
         if constexpr (MODE == kOut) {

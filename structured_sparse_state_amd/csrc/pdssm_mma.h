@@ -76,6 +76,42 @@ __device__ __forceinline__ Frag<N> split(f32x8 v)
     return f;
 }
 
+// Three parts of eight values that go into products with a single part: cut off
+// and not rounded (eight bits each, again all 24), which spares the conversions:
+// the upper halves of two values are one word, and their rests one two-term dot
+// product each.
+__device__ __forceinline__ Frag<3> split_cut(f32x8 v)
+{
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    Frag<3> f;
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        x[j] = v[j];
+    uint32_t first = 0x0000BF80u, second = 0xBF800000u;
+    asm("" : "+s"(first));
+    asm("" : "+s"(second));
+    bf16x2_t ff, ss;
+    __builtin_memcpy(&ff, &first, 4);
+    __builtin_memcpy(&ss, &second, 4);
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            w[j] = __builtin_amdgcn_perm(__float_as_uint(x[2 * j + 1]), __float_as_uint(x[2 * j]), 0x07060302u);
+            if (n < 2) {
+                bf16x2_t h;
+                __builtin_memcpy(&h, &w[j], 4);
+                x[2 * j] = __builtin_amdgcn_fdot2_f32_bf16(h, ff, x[2 * j], false);
+                x[2 * j + 1] = __builtin_amdgcn_fdot2_f32_bf16(h, ss, x[2 * j + 1], false);
+            }
+        }
+        __builtin_memcpy(&f.p[n], w, 16);
+    }
+    return f;
+}
+
 // The B operand of two stacked C tiles.
 template <int N>
 __device__ __forceinline__ Frag<N> split(f32x4 a, f32x4 b)
