@@ -42,10 +42,9 @@ namespace pdssm {
 namespace {
 
 constexpr int kMaxDim = 128;
-constexpr int kSlice = 64;          // columns of the state in a workgroup
-constexpr int kChain = 4;           // chain waves
 constexpr int kHelp = 256;          // help threads
-constexpr int kWalkThreads = kChain * 64 + kHelp;
+// A workgroup's columns SL of the state are 64 or 128, a chain wave for each 16.
+constexpr int walk_threads(int SL) { return SL / 16 * 64 + kHelp; }
 
 // Vectors of a chunk in LDS: what the rows read of the state and write to it,
 // the state's own decay, G log2(e) as a pair of floats and the steps that
@@ -57,12 +56,13 @@ struct Walk {
     Rows x4;                // dg: the rows beside y's (q for dQ, k for dK)
     bool kv1, kv2, kv3, kvy;        // rows of the key heads
     bool wide;              // y: fp32 [B*Hv][L][pitch] whatever the type of the data
-    int D1, D3, slices;     // contraction, columns
+    int D1, D3, groups;     // contraction, columns, groups of 16 columns that are kept
     const float *start;     // the state before the first chunk of the walk, NULL: zero
     float *end;             // and after its last, NULL: not wanted
     int row, col;           // strides of a state's values along contraction and columns
     float *starts;          // [segs + 1]: states before the segments, see native()
     float *wholes;          // [segs][heads]: the segments' decays
+    int segs, seg_chunks;
 };
 
 struct LinArgs {
@@ -70,13 +70,12 @@ struct LinArgs {
     Rows g;
     Rows dg;
     float *kept;            // [NC]: the states before the chunks, see native()
-    float *reads;           // [NC][slices][heads][4][64]: q . what dQ reads of S
+    float *reads;           // [NC][heads][groups][64]: q . what dQ reads of S
     float *dg_part;         // [slices][heads][L], or NULL: dg itself
     int64_t heads;          // B*Hv
     int64_t blocks;         // below 2^32, by the limit on B Hv
     bool started;           // s0 is given
     int first, last;        // walks of this launch
-    int segs, seg_chunks;
     int Hk, Hv, L, NC;
     float scale;
 };
@@ -84,19 +83,19 @@ struct LinArgs {
 enum Mode { kOut, kScan };          // outputs; the last state alone
 enum Gate { kNone, kKeep, kGrad };  // what a walk does for dg
 
-// A workgroup's state as its chain waves hold it: state number n of a slice of
-// a head, [4 waves][KD / 16][64 lanes] four values each.
+// 16 columns of a state as a chain wave holds them: group `group` of state
+// number n of a head, [KD / 16][64 lanes] four values each.
 template <int KD>
-__device__ __forceinline__ float *native(float *p, int64_t n, int slices, int64_t heads, int slice, int64_t head, int wave,
-                                         int lane)
+__device__ __forceinline__ float *native(float *p, int64_t n, int64_t heads, int groups, int64_t head, int group, int lane)
 {
-    return p + ((((n * slices + slice) * heads + head) * 4 + wave) * (KD / 16) * 64 + lane) * 4;
+    return p + (((n * heads + head) * groups + group) * (KD / 16) * 64 + lane) * 4;
 }
 
-template <int KD, bool BF16>
+template <int KD, bool BF16, int SL>
 struct LinLds {
+    static constexpr int kChain = SL / 16;
     using T1 = Tile<KD, BF16, kHelp>;
-    using T3 = Tile<kSlice, BF16, kHelp>;
+    using T3 = Tile<SL, BF16, kHelp>;
     using M = Tri<false, kHelp>;                    // (both triangles take as much)
     // bf16: the chain reads one half while the help waves fill the other.  Three
     // parts of fp32 rows leave no room for that.
@@ -109,10 +108,10 @@ struct LinLds {
     // in floats
     static constexpr int kVec = (kM + kHalves * M::kSize) / 2;
     static constexpr int kCuts = kVec + 4 * kVecs * kC;             // (the gates' vectors are a chunk further ahead)
-    static constexpr int kWrites = kCuts + kHalves * Cuts::kSize;   // [4 waves][64]: k . what dK reads of dS
-    static constexpr int kCross = kWrites + kHalves * 4 * kC;       // [4 waves]: <whole S, dS>
-    static constexpr int kFlag = kCross + kHalves * 4;              // [4] help waves, [4] spoiled
-    static constexpr size_t kBytes = (kFlag + 8) * 4;
+    static constexpr int kWrites = kCuts + kHalves * Cuts::kSize;   // [chain waves][64]: k . what dK reads of dS
+    static constexpr int kCross = kWrites + kHalves * kChain * kC;  // [chain waves]: <whole S, dS>
+    static constexpr int kFlag = kCross + kHalves * kChain;         // [4] help waves, [chain waves] spoiled
+    static constexpr size_t kBytes = (kFlag + 4 + kChain) * 4;
 };
 
 // Values of a state in memory, a lane's column and rows 16 m + 4 g + r.
@@ -227,23 +226,24 @@ __device__ __forceinline__ int scalar(unsigned v) { return __builtin_amdgcn_read
 // values of X3 that are not finite, which would reach the steps on the other
 // side of the triangle through its zeros.  Gives true when a state that is not
 // finite at the end asks for such a second pass.
-template <int KD, bool BF16, bool VEC, bool BACK, int MODE, int GATE, bool CAREFUL>
+template <int KD, bool BF16, bool VEC, int SL, bool BACK, int MODE, int GATE, bool CAREFUL>
 __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int seg, int slice, int64_t head, int thread)
 {
-    using LDS = LinLds<KD, BF16>;
+    using LDS = LinLds<KD, BF16, SL>;
     using T1 = typename LDS::T1;
     using T3 = typename LDS::T3;
     using M = Tri<BACK, kHelp>;
-    constexpr int NK = T1::NK, NS = KD / 32;
+    constexpr int NK = T1::NK, NS = KD / 32, kChain = LDS::kChain;
     extern __shared__ __attribute__((aligned(16))) char s_dyn[];
     uint16_t *lds = reinterpret_cast<uint16_t *>(s_dyn);
     float *ldf = reinterpret_cast<float *>(s_dyn);
     int *s_help = reinterpret_cast<int *>(ldf + LDS::kFlag), *s_spoiled = s_help + 4;
 
-    const int p0 = seg * a.seg_chunks, p1 = min(a.NC, p0 + a.seg_chunks);
+    const int p0 = seg * w.seg_chunks, p1 = min(a.NC, p0 + w.seg_chunks);
     const int64_t b = scalar((unsigned)head / (unsigned)a.Hv);
     const int h = (int)head - (int)b * a.Hv, hk = scalar((unsigned)h / (unsigned)(a.Hv / a.Hk));
-    const int lane = thread & 63, wave = scalar(thread >> 6), g = lane >> 4, i16 = lane & 15, mine = wave & 3;
+    const int lane = thread & 63, wave = scalar(thread >> 6), g = lane >> 4, i16 = lane & 15;
+    const int mine = wave < kChain ? wave : wave - kChain, group = slice * kChain + mine;
     auto chunk_of = [&](int p) { return BACK ? a.NC - 1 - p : p; };
     auto half_of = [&](int p) { return LDS::kHalves == 2 ? (p - p0) & 1 : 0; };
     auto begin = [&](const Rows &x, bool kv) { return b * x.s.b + (kv ? hk : h) * x.s.h; };
@@ -257,11 +257,11 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
     bool again = false;
 
     if (wave < kChain) {
-        const int col = slice * kSlice + mine * 16 + i16;
-        const int col4 = slice * kSlice + mine * 16 + 4 * g;    // of the lane's four values of y
+        const int col = group * 16 + i16;
+        const int col4 = group * 16 + 4 * g;    // of the lane's four values of y
         f32x4 S[KD / 16];
-        if (a.segs > 1 && MODE != kScan) {
-            const float *from = native<KD>(w.starts, seg, w.slices, a.heads, slice, head, mine, lane);
+        if (w.segs > 1 && MODE != kScan) {
+            const float *from = native<KD>(w.starts, seg, a.heads, w.groups, head, group, lane);
 #pragma unroll
             for (int m = 0; m < KD / 16; ++m)
                 S[m] = *reinterpret_cast<const f32x4 *>(from + m * 256);
@@ -274,7 +274,7 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
         // The first segment's start is kept too: the last one's end may go to
         // the same buffer while other workgroups still begin.
         if (MODE == kScan && seg == 0) {
-            float *to = native<KD>(w.starts, 0, w.slices, a.heads, slice, head, mine, lane);
+            float *to = native<KD>(w.starts, 0, a.heads, w.groups, head, group, lane);
 #pragma unroll
             for (int m = 0; m < KD / 16; ++m)
                 *reinterpret_cast<f32x4 *>(to + m * 256) = S[m];
@@ -304,7 +304,7 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
                     beside[t] = cx.four(e, i16, 16 * t, col4);
             }
             if constexpr (GATE == kGrad) {
-                const float *from = native<KD>(a.kept, c, w.slices, a.heads, slice, head, mine, lane);
+                const float *from = native<KD>(a.kept, c, a.heads, w.groups, head, group, lane);
 #pragma unroll
                 for (int m = 0; m < KD / 16; ++m)
                     kept[m] = *reinterpret_cast<const f32x4 *>(from + m * 256);
@@ -368,8 +368,8 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
                 for (int t = 0; t < 4; ++t)
                     Y[t] *= s_vec[kRead * kC + 16 * t + i16];
                 if constexpr (GATE != kNone) {
-                    float *to = GATE == kKeep ? a.reads + ((((int64_t)c * w.slices + slice) * a.heads + head) * 4 + mine) * kC
-                                              : ldf + LDS::kWrites + (half * 4 + mine) * kC;
+                    float *to = GATE == kKeep ? a.reads + (((int64_t)c * a.heads + head) * w.groups + group) * kC
+                                              : ldf + LDS::kWrites + (half * kChain + mine) * kC;
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
                         float v = Y[t][0] * beside[t][0] + Y[t][1] * beside[t][1] + Y[t][2] * beside[t][2] + Y[t][3] * beside[t][3];
@@ -379,7 +379,7 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
                     }
                 }
                 if constexpr (GATE == kKeep) {
-                    float *to = native<KD>(a.kept, c, w.slices, a.heads, slice, head, mine, lane);
+                    float *to = native<KD>(a.kept, c, a.heads, w.groups, head, group, lane);
 #pragma unroll
                     for (int m = 0; m < KD / 16; ++m)
                         *reinterpret_cast<f32x4 *>(to + m * 256) = S[m];
@@ -390,7 +390,7 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
                     for (int m = 0; m < KD / 16; ++m)
                         v += kept[m][0] * S[m][0] + kept[m][1] * S[m][1] + kept[m][2] * S[m][2] + kept[m][3] * S[m][3];
                     v = sum64(v);
-                    ldf[LDS::kCross + half * 4 + wave] = v * s_vec[kWhole * kC];
+                    ldf[LDS::kCross + half * kChain + wave] = v * s_vec[kWhole * kC];
                 }
                 if constexpr (GATE != kNone)
                     fetch(min(p + 1, p1 - 1));
@@ -473,7 +473,7 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
             lds_barrier();
         }
         if constexpr (MODE == kScan) {
-            float *to = native<KD>(w.starts, seg + 1, w.slices, a.heads, slice, head, mine, lane);
+            float *to = native<KD>(w.starts, seg + 1, a.heads, w.groups, head, group, lane);
 #pragma unroll
             for (int m = 0; m < KD / 16; ++m)
                 *reinterpret_cast<f32x4 *>(to + m * 256) = S[m];
@@ -490,7 +490,8 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
             if (lane == 0)
                 s_spoiled[mine] = spoiled;
             lds_barrier();
-            again = s_spoiled[0] | s_spoiled[1] | s_spoiled[2] | s_spoiled[3];
+            for (int n = 0; n < kChain; ++n)
+                again |= s_spoiled[n] != 0;
             // (the end may be the start, from which a second pass begins)
             if (w.end && p1 == a.NC && !again) {
                 each_value<KD>(w, col, lane, [&](int m, int r, bool in, int at) {
@@ -511,9 +512,9 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
         const int c0 = chunk_of(p0);
         Stream x1(w.x1.p, begin(w.x1, w.kv1), w.x1.s.l, c0, BACK, w.D1, kSize);
         Stream x2(w.x2.p, begin(w.x2, w.kv2), w.x2.s.l, c0, BACK, w.D1, kSize);
-        const int cols = w.D3 - slice * kSlice;
-        Stream x3(w.x3.p, begin(w.x3, w.kv3) + slice * kSlice, w.x3.s.l, c0, BACK, cols, kSize);
-        Stream x4(w.x4.p, begin(w.x4, true) + slice * kSlice, w.x4.s.l, c0, BACK, cols, kSize);
+        const int cols = w.D3 - slice * SL;
+        Stream x3(w.x3.p, begin(w.x3, w.kv3) + slice * SL, w.x3.s.l, c0, BACK, cols, kSize);
+        Stream x4(w.x4.p, begin(w.x4, true) + slice * SL, w.x4.s.l, c0, BACK, cols, kSize);
         Stream gates(a.g.p, b * a.g.s.b + h * a.g.s.h, a.g.s.l, c0, BACK, 1, 4);
         const bool has_gates = a.g.p != nullptr, has_steps = has_gates && a.g.s.l != 0;
         // (no branches on the way of the loads: where two paths with other loads
@@ -542,8 +543,11 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
             gates.next(p + 1 < p1);
             gate = __uint_as_float(cg.raw(cg.lane_at(lane, 0), lane, 0, 0));
             if constexpr (GATE == kGrad) {
-                const float *r = a.reads + (((int64_t)chunk_of(p) * w.slices + slice) * a.heads + head) * 4 * kC + lane;
-                reads = (r[0] + r[kC]) + (r[2 * kC] + r[3 * kC]);
+                const float *r = a.reads + (((int64_t)chunk_of(p) * a.heads + head) * w.groups + slice * kChain) * kC + lane;
+                reads = r[0];
+#pragma unroll
+                for (int n = 1; n < kChain; ++n)
+                    reads += r[n * kC];
             }
         };
         // The gates' vectors of chunk p (one wave), from the values fetched, those
@@ -657,14 +661,14 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
             if constexpr (GATE == kGrad) {
                 if (mine == kGateWave) {
                     const int half = half_of(p), t = chunk_of(p) * kC + lane;
-                    const float *s_vec = vecs(p), *s_w = ldf + LDS::kWrites + half * 4 * kC, *s_x = ldf + LDS::kCross + half * 4;
-                    float whole = s_x[0];
+                    const float *s_vec = vecs(p), *s_w = ldf + LDS::kWrites + half * kChain * kC, *s_x = ldf + LDS::kCross + half * kChain;
+                    float whole = s_x[0], writes = s_w[lane];
 #pragma unroll
-                    for (int n = 1; n < kChain; ++n)
+                    for (int n = 1; n < kChain; ++n) {
                         whole += s_x[n];
-                    const float v = crossing(whole, s_vec[kReads * kC + lane],
-                                             s_w[lane] + s_w[kC + lane] + s_w[2 * kC + lane] + s_w[3 * kC + lane],
-                                             ldf + LDS::kCuts + half * Cuts::kSize, lane);
+                        writes += s_w[n * kC + lane];
+                    }
+                    const float v = crossing(whole, s_vec[kReads * kC + lane], writes, ldf + LDS::kCuts + half * Cuts::kSize, lane);
                     // the decay of an empty state does nothing
                     const float *n = s_vec + kResets * kC;
                     const bool empty = n[lane] != (lane ? n[lane - 1] : 0.f) || (t == 0 && !a.started);
@@ -711,21 +715,22 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
         gates_of(p1 - 1);
         if constexpr (MODE == kOut) {
             lds_barrier();
-            again = s_spoiled[0] | s_spoiled[1] | s_spoiled[2] | s_spoiled[3];
+            for (int n = 0; n < kChain; ++n)
+                again |= s_spoiled[n] != 0;
         }
     }
     return again;
 }
 
-template <int KD, bool BF16, bool VEC, bool BACK, int MODE, int GATE>
+template <int KD, bool BF16, bool VEC, int SL, bool BACK, int MODE, int GATE>
 __device__ __forceinline__ void walk(const LinArgs &a, const Walk &w, int seg, int slice, int64_t head)
 {
     // A state that is not finite at its end: the walk again, with a look at
     // every chunk.
-    if (walk_pass<KD, BF16, VEC, BACK, MODE, GATE, false>(a, w, seg, slice, head, threadIdx.x)) {
+    if (walk_pass<KD, BF16, VEC, SL, BACK, MODE, GATE, false>(a, w, seg, slice, head, threadIdx.x)) {
         lds_barrier();      // the flags have been read
         // (opaque: nothing formed for one pass is held through the other)
-        walk_pass<KD, BF16, VEC, BACK, MODE, GATE, true>(a, w, seg, opaque_s(slice), head, opaque(threadIdx.x));
+        walk_pass<KD, BF16, VEC, SL, BACK, MODE, GATE, true>(a, w, seg, opaque_s(slice), head, opaque(threadIdx.x));
     }
 }
 
@@ -734,35 +739,36 @@ __device__ __forceinline__ void walk(const LinArgs &a, const Walk &w, int seg, i
 // on one die of the eight, with one L2.
 enum Which { kForward, kBoth, kFirst, kLast };      // the forward's; dQ's, dV's and dK's; with dg: dQ's and dV's; dK's
 
-template <int KD, bool BF16, bool VEC, int MODE, int WHICH>
-__global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(LinArgs a)
+template <int KD, bool BF16, bool VEC, int SL, int MODE, int WHICH>
+__global__ void __launch_bounds__(walk_threads(SL), 1) walk_kernel(LinArgs a)
 {
     unsigned rest = blockIdx.y * gridDim.x + blockIdx.x;
     if (rest >= a.blocks)
         return;
     const unsigned heads = (unsigned)a.heads;
+    // (nothing asks for the last segment's end)
+    auto slices = [&](int n) { return (unsigned)(a.w[n].D3 + SL - 1) / SL; };
+    auto blocks = [&](int n) { return heads * (a.w[n].segs - (MODE == kScan)) * slices(n); };
     int n = a.first;
-    if constexpr (WHICH == kBoth || WHICH == kFirst) {
-        while (n < a.last && rest >= heads * a.segs * a.w[n].slices) {
-            rest -= heads * a.segs * a.w[n].slices;
+    if constexpr (WHICH != kForward) {
+        while (n < a.last && rest >= blocks(n)) {
+            rest -= blocks(n);
             ++n;
         }
     }
     const Walk &w = a.w[n];
-    const unsigned of_head = rest / heads;
+    const unsigned of_head = rest / heads, count = slices(n);
     const int64_t head = scalar(rest - of_head * heads);
-    const int seg = scalar(of_head / (unsigned)w.slices), slice = scalar(of_head - seg * w.slices);
-    if (MODE == kScan && seg == a.segs - 1)
-        return;     // nothing asks for the last one's end
+    const int seg = scalar(of_head / count), slice = scalar(of_head - seg * count);
     if constexpr (WHICH == kForward) {
-        walk<KD, BF16, VEC, false, MODE, kNone>(a, w, seg, slice, head);
+        walk<KD, BF16, VEC, SL, false, MODE, kNone>(a, w, seg, slice, head);
     } else if constexpr (WHICH == kLast) {
-        walk<KD, BF16, VEC, true, MODE, kGrad>(a, w, seg, slice, head);
+        walk<KD, BF16, VEC, SL, true, MODE, kGrad>(a, w, seg, slice, head);
     } else {
         if (n == 0)
-            walk<KD, BF16, VEC, false, MODE, WHICH == kFirst ? kKeep : kNone>(a, w, seg, slice, head);
+            walk<KD, BF16, VEC, SL, false, MODE, WHICH == kFirst ? kKeep : kNone>(a, w, seg, slice, head);
         else
-            walk<KD, BF16, VEC, true, MODE, kNone>(a, w, seg, slice, head);
+            walk<KD, BF16, VEC, SL, true, MODE, kNone>(a, w, seg, slice, head);
     }
 }
 
@@ -775,14 +781,14 @@ template <int KD>
 __global__ void __launch_bounds__(256) lin_join_kernel(LinArgs a)
 {
     const Walk &w = a.w[blockIdx.y];
-    const int64_t size = (int64_t)w.slices * a.heads * KD * kSlice;    // values between segments
+    const int64_t one = (int64_t)w.groups * KD * 16, size = a.heads * one;      // values of a state, and between segments
     const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (at >= size)
+    if (at >= size || w.segs == 1)
         return;
-    const int64_t head = at / (KD * kSlice) % a.heads;
+    const int64_t head = at / one;
     float *p = w.starts + size + at;
     f32x4 S = *reinterpret_cast<const f32x4 *>(p);
-    for (int n = 1; n + 1 < a.segs; ++n) {
+    for (int n = 1; n + 1 < w.segs; ++n) {
         p += size;
         S = w.wholes[n * a.heads + head] * S + *reinterpret_cast<const f32x4 *>(p);
         *reinterpret_cast<f32x4 *>(p) = S;
@@ -1008,12 +1014,14 @@ int check_linear_dims(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int32_t Dk, 
     return PDSSM_OK;
 }
 
-int slices_of(int D) { return (D + kSlice - 1) / kSlice; }
+int slices_of(int D, int SL) { return (D + SL - 1) / SL; }
 int padded(int D) { return D <= 64 ? 64 : 128; }
+// Columns of a workgroup: three parts of fp32 rows leave no room for 128.
+int slice_for(int D3, uint32_t flags) { return (flags & PDSSM_DATA_BF16) ? padded(D3) : 64; }
 
 // How many segments the chunks of a head are cut into, walked side by side: they
-// are walked twice (once without outputs) and joined, so a walk is cut only
-// where the workgroups do not fill the device, and no finer than fills it.
+// are walked twice (once without outputs) and joined, so walks are cut only
+// where a launch's workgroups do not fill the device, and no finer than fills it.
 struct Cut {
     int segs, chunks;
 };
@@ -1043,32 +1051,43 @@ struct Space {
 
 struct LinLayout {
     Space space;
-    Cut cut;
+    Cut cut[3];
+    int groups[3];
     int64_t starts[3], wholes[3], kept, reads, dg_part, dq_part, dk_part, ds;
 };
 
-LinLayout layout_of(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int Dk, int Dv, bool bwd, bool grad, bool dg_heads)
+// Of the forward, or of dQ's, dV's and dK's walks.
+LinLayout layout_of(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int Dk, int Dv, uint32_t flags, bool bwd)
 {
     LinLayout l = {};
     const int64_t heads = B * Hv, NC = (L + kC - 1) / kC;
-    const int sk = slices_of(Dk), sv = slices_of(Dv), pitch = (Dk + 3) / 4 * 4;
-    const int64_t state = (int64_t)std::max(padded(Dk), padded(Dv)) * kSlice * 4;
+    const int pitch = (Dk + 3) / 4 * 4;
+    const bool grad = bwd && !(flags & PDSSM_NO_DG);
     l.space.take(256);
-    l.cut = cut_of(heads * (bwd ? std::max(sk, sv) : sv), L);
+    if (bwd) {
+        const int SL = slice_for(std::max(Dk, Dv), flags), sk = slices_of(Dk, SL), sv = slices_of(Dv, SL);
+        // with dg dK's walk comes after the others, its columns 64 at a time
+        const Cut first = cut_of(heads * (sk + sv + (grad ? 0 : sk)), L);
+        l.cut[0] = l.cut[1] = first;
+        l.cut[2] = grad ? cut_of(heads * slices_of(Dk, 64), L) : first;
+    } else {
+        l.cut[0] = cut_of(heads * slices_of(Dv, slice_for(Dv, flags)), L);
+    }
+    const int64_t rows = std::max(padded(Dk), padded(Dv));
     for (int n = 0; n < (bwd ? 3 : 1); ++n) {
-        const int64_t slices = bwd && n != 1 ? sk : sv;
-        if (l.cut.segs > 1) {
-            l.starts[n] = l.space.take((l.cut.segs + 1) * heads * slices * state);
-            l.wholes[n] = l.space.take(l.cut.segs * heads * 4);
+        l.groups[n] = (bwd ? (int)rows : padded(Dv)) / 16;
+        if (l.cut[n].segs > 1) {
+            l.starts[n] = l.space.take((l.cut[n].segs + 1) * heads * l.groups[n] * rows * 64);
+            l.wholes[n] = l.space.take(l.cut[n].segs * heads * 4);
         }
     }
     if (bwd) {
         l.ds = l.space.take(heads * Dk * Dv * 4);
         if (grad) {
-            l.kept = l.space.take(NC * heads * sk * state);
-            l.reads = l.space.take(NC * heads * sk * 4 * kC * 4);
-            if (sk > 1 || dg_heads)
-                l.dg_part = l.space.take(heads * sk * L * 4);
+            l.kept = l.space.take(NC * heads * l.groups[0] * rows * 64);
+            l.reads = l.space.take(NC * heads * l.groups[0] * kC * 4);
+            if (Dk > 64 || (flags & PDSSM_DG_HEADS))
+                l.dg_part = l.space.take(heads * slices_of(Dk, 64) * L * 4);
         }
         if (Hv > Hk) {
             l.dq_part = l.space.take(heads * L * pitch * 4);
@@ -1098,50 +1117,61 @@ dim3 grid_of(int64_t blocks)
 }
 
 // A call's walks; of cut sequences all scans first, and the join.
-template <int KD, bool BF16, bool VEC, bool BWD>
+template <int KD, bool BF16, bool VEC, int SL, bool BWD>
 int launch_walks(LinArgs a, bool grad, hipStream_t stream)
 {
-    constexpr size_t lds = LinLds<KD, BF16>::kBytes;
-    static_assert(lds <= 163840, "LDS of a compute unit");
-    auto launch = [&](auto kernel, int first, int last) {
+    auto launch = [&](auto kernel, int sl, size_t lds, int first, int last, bool scan) {
         a.first = first, a.last = last, a.blocks = 0;
         for (int n = first; n <= last; ++n)
-            a.blocks += a.heads * a.segs * a.w[n].slices;
-        return lin_launch(kernel, grid_of(a.blocks), kWalkThreads, lds, a, stream);
+            a.blocks += a.heads * (a.w[n].segs - scan) * slices_of(a.w[n].D3, sl);
+        return lin_launch(kernel, grid_of(a.blocks), walk_threads(sl), lds, a, stream);
     };
+    constexpr size_t lds = LinLds<KD, BF16, SL>::kBytes;
+    static_assert(lds <= 163840, "LDS of a compute unit");
+    constexpr int kLastWalk = BWD ? 2 : 0;
     int rc = PDSSM_OK;
-    if (a.segs > 1) {
-        rc = launch(walk_kernel<KD, BF16, VEC, kScan, BWD ? kBoth : kForward>, 0, BWD ? 2 : 0);
-        if (rc == PDSSM_OK) {
-            const int64_t slices = BWD ? std::max(a.w[0].slices, a.w[1].slices) : a.w[0].slices;
-            rc = lin_launch(lin_join_kernel<KD>, dim3((unsigned)(a.heads * slices * (KD * kSlice / 1024)), BWD ? 3 : 1), 256, 0, a, stream);
-        }
+    int64_t states = 0;
+    for (int n = 0; n <= kLastWalk; ++n)
+        if (a.w[n].segs > 1)
+            states = std::max(states, a.heads * a.w[n].groups);
+    if (states > 0) {
+        rc = launch(walk_kernel<KD, BF16, VEC, SL, kScan, BWD ? kBoth : kForward>, SL, lds, 0, kLastWalk, true);
+        if (rc == PDSSM_OK)
+            rc = lin_launch(lin_join_kernel<KD>, dim3((unsigned)(states * KD / 64), kLastWalk + 1), 256, 0, a, stream);
     }
     if (rc != PDSSM_OK)
         return rc;
     if constexpr (!BWD) {
-        return launch(walk_kernel<KD, BF16, VEC, kOut, kForward>, 0, 0);
+        return launch(walk_kernel<KD, BF16, VEC, SL, kOut, kForward>, SL, lds, 0, 0, false);
     } else {
         if (!grad)
-            return launch(walk_kernel<KD, BF16, VEC, kOut, kBoth>, 0, 2);
+            return launch(walk_kernel<KD, BF16, VEC, SL, kOut, kBoth>, SL, lds, 0, 2, false);
         // dK's walk adds up dg from what dQ's keeps
-        rc = launch(walk_kernel<KD, BF16, VEC, kOut, kFirst>, 0, 1);
-        return rc == PDSSM_OK ? launch(walk_kernel<KD, BF16, VEC, kOut, kLast>, 2, 2) : rc;
+        rc = launch(walk_kernel<KD, BF16, VEC, SL, kOut, kFirst>, SL, lds, 0, 1, false);
+        return rc == PDSSM_OK ? launch(walk_kernel<KD, BF16, VEC, 64, kOut, kLast>, 64, LinLds<KD, BF16, 64>::kBytes, 2, 2, false) : rc;
     }
 }
 
-template <int KD, bool BF16, bool VEC>
-int launch_direction(const LinArgs &a, bool bwd, bool grad, hipStream_t stream)
+// The variant for these sizes, type and rows: D1 and D3 the largest contraction
+// and columns of the walks.
+template <bool BF16, bool VEC>
+int launch_sizes(const LinArgs &a, int D1, int D3, bool bwd, bool grad, hipStream_t stream)
 {
-    return bwd ? launch_walks<KD, BF16, VEC, true>(a, grad, stream) : launch_walks<KD, BF16, VEC, false>(a, false, stream);
+    constexpr int wide = BF16 ? 128 : 64;
+    if (bwd)
+        return D1 > 64 ? launch_walks<128, BF16, VEC, wide, true>(a, grad, stream) : launch_walks<64, BF16, VEC, 64, true>(a, grad, stream);
+    if constexpr (BF16) {
+        if (D3 > 64)
+            return D1 > 64 ? launch_walks<128, BF16, VEC, 128, false>(a, false, stream) : launch_walks<64, BF16, VEC, 128, false>(a, false, stream);
+    }
+    return D1 > 64 ? launch_walks<128, BF16, VEC, 64, false>(a, false, stream) : launch_walks<64, BF16, VEC, 64, false>(a, false, stream);
 }
 
-template <bool BF16>
-int launch_sizes(const LinArgs &a, bool wide, bool vec, bool bwd, bool grad, hipStream_t stream)
+int launch_any(const LinArgs &a, bool bf16, bool vec, int D1, int D3, bool bwd, bool grad, hipStream_t stream)
 {
-    if (wide)
-        return vec ? launch_direction<128, BF16, true>(a, bwd, grad, stream) : launch_direction<128, BF16, false>(a, bwd, grad, stream);
-    return vec ? launch_direction<64, BF16, true>(a, bwd, grad, stream) : launch_direction<64, BF16, false>(a, bwd, grad, stream);
+    if (bf16)
+        return vec ? launch_sizes<true, true>(a, D1, D3, bwd, grad, stream) : launch_sizes<true, false>(a, D1, D3, bwd, grad, stream);
+    return vec ? launch_sizes<false, true>(a, D1, D3, bwd, grad, stream) : launch_sizes<false, false>(a, D1, D3, bwd, grad, stream);
 }
 
 }  // namespace
@@ -1165,7 +1195,7 @@ extern "C" size_t pdssm_linear_workspace_bytes(int64_t B, int64_t Hk, int64_t Hv
 {
     if (check_linear_dims(B, Hk, Hv, L, Dk, Dv) != PDSSM_OK || (flags & ~PDSSM_DATA_BF16))
         return 0;
-    return (size_t)layout_of(B, Hk, Hv, L, Dk, Dv, false, false, false).space.total;
+    return (size_t)layout_of(B, Hk, Hv, L, Dk, Dv, flags, false).space.total;
 }
 
 extern "C" size_t pdssm_linear_bwd_workspace_bytes(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int32_t Dk,
@@ -1173,7 +1203,7 @@ extern "C" size_t pdssm_linear_bwd_workspace_bytes(int64_t B, int64_t Hk, int64_
 {
     if (check_linear_dims(B, Hk, Hv, L, Dk, Dv) != PDSSM_OK || !bwd_flags_ok(flags))
         return 0;
-    return (size_t)layout_of(B, Hk, Hv, L, Dk, Dv, true, !(flags & PDSSM_NO_DG), flags & PDSSM_DG_HEADS).space.total;
+    return (size_t)layout_of(B, Hk, Hv, L, Dk, Dv, flags, true).space.total;
 }
 
 extern "C" int pdssm_linear_fwd(const void *q, const void *k, const void *v, const float *g, const float *s0, void *o,
@@ -1203,7 +1233,7 @@ extern "C" int pdssm_linear_fwd(const void *q, const void *k, const void *v, con
             return PDSSM_ERR_ALIGN;
     if (!element_aligned(g, 4) || !aligned16(workspace))
         return PDSSM_ERR_ALIGN;
-    const LinLayout lo = layout_of(B, Hk, Hv, L, Dk, Dv, false, false, false);
+    const LinLayout lo = layout_of(B, Hk, Hv, L, Dk, Dv, flags, false);
     if (workspace_bytes < (size_t)lo.space.total)
         return PDSSM_ERR_WORKSPACE;
     const pdssm_strides keys = {Hk * L * Dk, L * Dk, Dk}, values = {Hv * L * Dv, L * Dv, Dv}, gates = {Hv * L, L, 1};
@@ -1216,15 +1246,15 @@ extern "C" int pdssm_linear_fwd(const void *q, const void *k, const void *v, con
     Walk &w = a.w[0];
     w.x1 = {q, s[0]}, w.x2 = {k, s[1]}, w.x3 = {v, s[2]}, w.y = {o, s[4]};
     w.kv1 = w.kv2 = true;
-    w.D1 = Dk, w.D3 = Dv, w.slices = slices_of(Dv), w.start = s0, w.end = s_final, w.row = Dv, w.col = 1;
+    w.D1 = Dk, w.D3 = Dv, w.groups = lo.groups[0], w.start = s0, w.end = s_final, w.row = Dv, w.col = 1;
     w.starts = reinterpret_cast<float *>(ws + lo.starts[0]), w.wholes = reinterpret_cast<float *>(ws + lo.wholes[0]);
+    w.segs = lo.cut[0].segs, w.seg_chunks = lo.cut[0].chunks;
     a.g = {g, s[3]};
-    a.heads = B * Hv, a.segs = lo.cut.segs, a.seg_chunks = lo.cut.chunks;
+    a.heads = B * Hv;
     a.Hk = (int)Hk, a.Hv = (int)Hv, a.L = (int)L, a.NC = (int)((L + kC - 1) / kC), a.scale = scale;
     const bool vec = units(q, s[0], Dk, esize) && units(k, s[1], Dk, esize) && units(v, s[2], Dv, esize) &&
                      units(o, s[4], Dv, esize);
-    return esize == 2 ? launch_sizes<true>(a, Dk > 64, vec, false, false, stream)
-                      : launch_sizes<false>(a, Dk > 64, vec, false, false, stream);
+    return launch_any(a, esize == 2, vec, Dk, Dv, false, false, stream);
 }
 
 extern "C" int pdssm_linear_bwd(const void *q, const void *k, const void *v, const float *g, const float *s0,
@@ -1245,7 +1275,7 @@ extern "C" int pdssm_linear_bwd(const void *q, const void *k, const void *v, con
     const pdssm_strides contiguous[9] = {keys, keys, values, gates, values, keys, keys, values, dg_heads ? pdssm_strides{0, 1, 0} : gates};
     const pdssm_strides *s = strides ? strides : contiguous;
     GateArgs ga = {};
-    ga.dg = {dg, s[8]}, ga.heads = B * Hv, ga.Hv = (int)Hv, ga.L = (int)L, ga.slices = slices_of(Dk);
+    ga.dg = {dg, s[8]}, ga.heads = B * Hv, ga.Hv = (int)Hv, ga.L = (int)L, ga.slices = slices_of(Dk, 64);
     if (B == 0 || L == 0) {
         for (const float *p : {ds_final, (const float *)ds0})
             if (p && !aligned16(p))
@@ -1272,7 +1302,7 @@ extern "C" int pdssm_linear_bwd(const void *q, const void *k, const void *v, con
             return PDSSM_ERR_ALIGN;
     if (!element_aligned(g, 4) || (grad && !element_aligned(dg, 4)) || !aligned16(workspace))
         return PDSSM_ERR_ALIGN;
-    const LinLayout lo = layout_of(B, Hk, Hv, L, Dk, Dv, true, grad, dg_heads);
+    const LinLayout lo = layout_of(B, Hk, Hv, L, Dk, Dv, flags, true);
     if (workspace_bytes < (size_t)lo.space.total)
         return PDSSM_ERR_WORKSPACE;
     for (int n = 0; n < 9; ++n)
@@ -1308,18 +1338,18 @@ extern "C" int pdssm_linear_bwd(const void *q, const void *k, const void *v, con
     }
     for (int n = 0; n < 3; ++n) {
         Walk &w = a.w[n];
-        w.slices = slices_of(w.D3), w.starts = place(lo.starts[n]), w.wholes = place(lo.wholes[n]);
+        w.groups = lo.groups[n], w.starts = place(lo.starts[n]), w.wholes = place(lo.wholes[n]);
+        w.segs = lo.cut[n].segs, w.seg_chunks = lo.cut[n].chunks;
     }
     a.g = {g, s[3]}, a.dg = ga.dg, a.started = s0 != nullptr;
     a.kept = place(lo.kept), a.reads = place(lo.reads);
     a.dg_part = grad && (ga.slices > 1 || dg_heads) ? place(lo.dg_part) : nullptr;
-    a.heads = B * Hv, a.segs = lo.cut.segs, a.seg_chunks = lo.cut.chunks;
+    a.heads = B * Hv;
     a.Hk = (int)Hk, a.Hv = (int)Hv, a.L = (int)L, a.NC = (int)((L + kC - 1) / kC), a.scale = scale;
     const bool vec_keys = units(dq, s[5], Dk, esize) && units(dk, s[6], Dk, esize);
     const bool vec = units(q, s[0], Dk, esize) && units(k, s[1], Dk, esize) && units(v, s[2], Dv, esize) &&
                      units(d_o, s[4], Dv, esize) && vec_keys && units(dv, s[7], Dv, esize);
-    const bool wide = Dk > 64 || Dv > 64;
-    rc = esize == 2 ? launch_sizes<true>(a, wide, vec, true, grad, stream) : launch_sizes<false>(a, wide, vec, true, grad, stream);
+    rc = launch_any(a, esize == 2, vec, std::max(Dk, Dv), std::max(Dk, Dv), true, grad, stream);
     if (rc == PDSSM_OK && a.dg_part) {
         ga.part = a.dg_part;
         if (dg_heads)
