@@ -108,9 +108,9 @@ struct LinLds {
     // in floats
     static constexpr int kVec = (kM + kHalves * M::kSize) / 2;
     static constexpr int kCuts = kVec + 4 * kVecs * kC;             // (the gates' vectors are a chunk further ahead)
-    static constexpr int kWrites = kCuts + kHalves * Cuts::kSize;   // [chain waves][64]: k . what dK reads of dS
-    static constexpr int kCross = kWrites + kHalves * kChain * kC;  // [chain waves]: <whole S, dS>
-    static constexpr int kFlag = kCross + kHalves * kChain;         // [4] help waves, [chain waves] spoiled
+    static constexpr int kWrites = kCuts + 2 * Cuts::kSize;       // [chain waves][64]: k . what dK reads of dS
+    static constexpr int kCross = kWrites + 2 * kChain * kC;        // [chain waves]: <whole S, dS>
+    static constexpr int kFlag = kCross + 2 * kChain;               // [4] help waves, [chain waves] spoiled
     static constexpr size_t kBytes = (kFlag + 4 + kChain) * 4;
 };
 
@@ -245,6 +245,7 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
     const int lane = thread & 63, wave = scalar(thread >> 6), g = lane >> 4, i16 = lane & 15;
     const int mine = wave < kChain ? wave : wave - kChain, group = slice * kChain + mine;
     auto chunk_of = [&](int p) { return BACK ? a.NC - 1 - p : p; };
+    auto turn_of = [&](int p) { return (p - p0) & 1; };     // what goes to dg is kept for a turn
     auto half_of = [&](int p) { return LDS::kHalves == 2 ? (p - p0) & 1 : 0; };
     auto begin = [&](const Rows &x, bool kv) { return b * x.s.b + (kv ? hk : h) * x.s.h; };
     auto vecs = [&](int p) { return ldf + LDS::kVec + ((p - p0) & 3) * (kVecs * kC); };
@@ -369,7 +370,7 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
                     Y[t] *= s_vec[kRead * kC + 16 * t + i16];
                 if constexpr (GATE != kNone) {
                     float *to = GATE == kKeep ? a.reads + (((int64_t)c * a.heads + head) * w.groups + group) * kC
-                                              : ldf + LDS::kWrites + (half * kChain + mine) * kC;
+                                              : ldf + LDS::kWrites + (turn_of(p) * kChain + mine) * kC;
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
                         float v = Y[t][0] * beside[t][0] + Y[t][1] * beside[t][1] + Y[t][2] * beside[t][2] + Y[t][3] * beside[t][3];
@@ -390,7 +391,7 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
                     for (int m = 0; m < KD / 16; ++m)
                         v += kept[m][0] * S[m][0] + kept[m][1] * S[m][1] + kept[m][2] * S[m][2] + kept[m][3] * S[m][3];
                     v = sum64(v);
-                    ldf[LDS::kCross + half * kChain + wave] = v * s_vec[kWhole * kC];
+                    ldf[LDS::kCross + turn_of(p) * kChain + wave] = v * s_vec[kWhole * kC];
                 }
                 if constexpr (GATE != kNone)
                     fetch(min(p + 1, p1 - 1));
@@ -651,24 +652,23 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
                 if constexpr (GATE == kGrad) {
 #pragma unroll
                     for (int n = 0; n < 3; ++n)
-                        Cuts::put(ldf + LDS::kCuts + half * Cuts::kSize, tb[n], ta[n], kq[n], lane);
+                        Cuts::put(ldf + LDS::kCuts + turn_of(p) * Cuts::kSize, tb[n], ta[n], kq[n], lane);
                 }
             }
-            sum_gates(p + 1);
         };
         // dg of a chunk that the chain has left behind (one wave).
         auto gates_of = [&](int p) {
             if constexpr (GATE == kGrad) {
                 if (mine == kGateWave) {
-                    const int half = half_of(p), t = chunk_of(p) * kC + lane;
-                    const float *s_vec = vecs(p), *s_w = ldf + LDS::kWrites + half * kChain * kC, *s_x = ldf + LDS::kCross + half * kChain;
+                    const int turn = turn_of(p), t = chunk_of(p) * kC + lane;
+                    const float *s_vec = vecs(p), *s_w = ldf + LDS::kWrites + turn * kChain * kC, *s_x = ldf + LDS::kCross + turn * kChain;
                     float whole = s_x[0], writes = s_w[lane];
 #pragma unroll
                     for (int n = 1; n < kChain; ++n) {
                         whole += s_x[n];
                         writes += s_w[n * kC + lane];
                     }
-                    const float v = crossing(whole, s_vec[kReads * kC + lane], writes, ldf + LDS::kCuts + half * Cuts::kSize, lane);
+                    const float v = crossing(whole, s_vec[kReads * kC + lane], writes, ldf + LDS::kCuts + turn * Cuts::kSize, lane);
                     // the decay of an empty state does nothing
                     const float *n = s_vec + kResets * kC;
                     const bool empty = n[lane] != (lane ? n[lane - 1] : 0.f) || (t == 0 && !a.started);
@@ -696,19 +696,23 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
         sum_gates(p0);
         if constexpr (BF16) {
             prepare(in, p0);
+            sum_gates(p0 + 1);
             lds_barrier();
             for (int p = p0; p + 1 < p1; ++p) {
                 behind(p);
                 prepare(in, p + 1);
+                sum_gates(p + 2);
                 lds_barrier();
             }
             behind(p1 - 1);
             lds_barrier();
         } else {
             for (int p = p0; p < p1; ++p) {
-                behind(p);
                 prepare(in, p);
                 lds_barrier();
+                // while the chain is at chunk p
+                sum_gates(p + 1);
+                behind(p);
                 lds_barrier();
             }
         }
