@@ -40,9 +40,9 @@
  * bits), with one rounding to nearest even into a bf16 output.  Results are
  * bitwise reproducible.
  * A NaN or an infinity among the inputs of a step of pdssm_linear_fwd spoils
- * its heads' outputs from that step on and their state (in v, its column's; in
- * q, its step's outputs alone); in pdssm_linear_bwd it may spoil all gradients
- * of its sequence.
+ * its heads' outputs from that step on and their state (in v its column of
+ * both, in k its row of the state; in q its step's outputs alone); in
+ * pdssm_linear_bwd it may spoil all gradients of its sequence.
  *
  * Layouts: device pointers.  Row tensors are indexed [B,H,L,D] (gates [B,H,L])
  * with the last dimension contiguous and the strides of the first three, in

@@ -202,7 +202,8 @@ __device__ __forceinline__ Frag<BF16 ? 1 : 3> unit_frag(const Unit<BF16> &u)
 
 // A tile of 64 rows of KD values in LDS: NK parts, rows of KD + 8 values (the
 // padding spreads the rows over the banks).
-template <int KD, bool BF16, int NT = 256>
+// APART: what is not finite in fp32 rows stays in its place.
+template <int KD, bool BF16, int NT = 256, bool APART = false>
 struct Tile {
     static constexpr int NK = BF16 ? 1 : 3;
     static constexpr int kRow = KD + 8;
@@ -227,7 +228,11 @@ struct Tile {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
             const int x = tid + i * NT, row = x / (KD / 8), col = x % (KD / 8) * 8;
-            const Frag<NK> f = unit_frag<BF16>(u[i]);
+            Frag<NK> f;
+            if constexpr (APART && !BF16)
+                f = split_apart(u[i].v);
+            else
+                f = unit_frag<BF16>(u[i]);
 #pragma unroll
             for (int n = 0; n < NK; ++n)
                 *reinterpret_cast<bf16x8 *>(lds + n * kPart + row * kRow + col) = f.p[n];

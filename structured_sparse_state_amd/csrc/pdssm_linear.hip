@@ -94,8 +94,8 @@ __device__ __forceinline__ float *native(float *p, int64_t n, int64_t heads, int
 template <int KD, bool BF16, int SL>
 struct LinLds {
     static constexpr int kChain = SL / 16;
-    using T1 = Tile<KD, BF16, kHelp>;
-    using T3 = Tile<SL, BF16, kHelp>;
+    using T1 = Tile<KD, BF16, kHelp, true>;
+    using T3 = Tile<SL, BF16, kHelp, true>;
     using M = Tri<false, kHelp>;                    // (both triangles take as much)
     // bf16: the chain reads one half while the help waves fill the other.  Three
     // parts of fp32 rows leave no room for that.

@@ -76,6 +76,25 @@ __device__ __forceinline__ Frag<N> split(f32x8 v)
     return f;
 }
 
+// The same with a subtraction for each rest: the dot products take the other
+// value of a word times zero, so what is not finite would spoil its neighbour.
+__device__ __forceinline__ Frag<3> split_apart(f32x8 v)
+{
+    Frag<3> f;
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            w[j] = f32x2_to_bf16x2_rne(v[2 * j], v[2 * j + 1]);
+            v[2 * j] -= bf16_lo(w[j]);
+            v[2 * j + 1] -= bf16_hi(w[j]);
+        }
+        __builtin_memcpy(&f.p[n], w, 16);
+    }
+    return f;
+}
+
 // Three parts of eight values that go into products with a single part: cut off
 // and not rounded (eight bits each, again all 24), which spares the conversions:
 // the upper halves of two values are one word, and their rests one two-term dot
