@@ -187,7 +187,7 @@ __device__ __forceinline__ void team_sum(float (&v)[N], float (*s_sum)[16])
     }
     if constexpr (TEAM > 64) {
         constexpr int kWaves = TEAM / 64;
-        const int wave = threadIdx.x >> 6;
+        const int wave = threadIdx.x >> 6, first = wave / kWaves * kWaves;      // of the team
         __syncthreads();        // the sums before have been read
         if ((threadIdx.x & 63) == 0) {
 #pragma unroll
@@ -200,7 +200,7 @@ __device__ __forceinline__ void team_sum(float (&v)[N], float (*s_sum)[16])
             v[n] = 0.f;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w)
-                v[n] += s_sum[n][w];
+                v[n] += s_sum[n][first + w];
         }
     }
 }
@@ -556,24 +556,35 @@ int take_rows(RowsOf &r, const void *p, const pdssm_strides *s, int n, const pds
     return PDSSM_OK;
 }
 
-// Workgroups: as many rows a team as fill the device several times over, so that
-// a team's weights serve many rows.
-int64_t teams_of(int team) { return (team > 256 ? team : 256) / team; }
-
-int team_of(int D) { return D <= 128 ? 16 : D <= 2048 ? 64 : D <= 8192 ? 256 : 1024; }
-
-int64_t groups_of(int64_t rows, int D, bool bwd)
+// Teams, so that a lane has at most four units of a row forward and two backward
+// (whose sums of dw and db take as many registers again).  8 x 4096 rows of 2048,
+// bf16: forward 114 us with 64 lanes of four units, 114 with 128 of two, 117 with 256
+// of one; backward 165, 146 and 150 (one, two and five waves to a SIMD).
+int team_of(int D, bool bwd)
 {
-    const int team = team_of(D);
-    const int64_t groups = (rows + teams_of(team) - 1) / teams_of(team);
-    return std::min<int64_t>(groups, bwd ? 512 : 2048);
+    if (D <= 128)
+        return 16;
+    if (D <= (bwd ? 1024 : 2048))
+        return 64;
+    if (bwd)
+        return D <= 2048 ? 128 : D <= 4096 ? 256 : D <= 8192 ? 512 : 1024;
+    return D <= 8192 ? 256 : 1024;
 }
 
-template <typename T, int TEAM, int UNITS, bool WHOLE>
-void launch_norm(const NormArgs &a, bool bwd, int64_t groups, hipStream_t stream)
+// Workgroups: no more than fill the device a few times over, so that a team's
+// weights (and sums) serve many rows.  The backward above with 512, 768, 1024 and
+// 1536 of them: 147, 158, 153 and 158 us.
+int64_t groups_of(int64_t rows, int D, bool bwd)
+{
+    const int64_t teams = std::max(256 / team_of(D, bwd), 1);
+    return std::min<int64_t>((rows + teams - 1) / teams, bwd ? 512 : 2048);
+}
+
+template <typename T, int TEAM, int UNITS, bool WHOLE, bool BWD>
+void launch_norm(const NormArgs &a, int64_t groups, hipStream_t stream)
 {
     const dim3 grid((unsigned)groups), block((unsigned)threads_of<TEAM>());
-    if (bwd)
+    if constexpr (BWD)
         hipLaunchKernelGGL((layer_norm_bwd_kernel<T, TEAM, UNITS, WHOLE>), grid, block, 0, stream, a);
     else
         hipLaunchKernelGGL((layer_norm_kernel<T, TEAM, UNITS, WHOLE>), grid, block, 0, stream, a);
@@ -582,20 +593,25 @@ void launch_norm(const NormArgs &a, bool bwd, int64_t groups, hipStream_t stream
 template <typename T, bool WHOLE>
 void launch_width(const NormArgs &a, bool bwd, int64_t groups, hipStream_t stream)
 {
-    if (a.D <= 128)
-        launch_norm<T, 16, 1, WHOLE>(a, bwd, groups, stream);
-    else if (a.D <= 512)
-        launch_norm<T, 64, 1, WHOLE>(a, bwd, groups, stream);
-    else if (a.D <= 1024)
-        launch_norm<T, 64, 2, WHOLE>(a, bwd, groups, stream);
-    else if (a.D <= 2048)
-        launch_norm<T, 64, 4, WHOLE>(a, bwd, groups, stream);
-    else if (a.D <= 4096)
-        launch_norm<T, 256, 2, WHOLE>(a, bwd, groups, stream);
-    else if (a.D <= 8192)
-        launch_norm<T, 256, 4, WHOLE>(a, bwd, groups, stream);
-    else
-        launch_norm<T, 1024, 2, WHOLE>(a, bwd, groups, stream);
+    const int units = (a.D + kUnit - 1) / kUnit, team = team_of(a.D, bwd), each = (units + team - 1) / team;
+#define PDSSM_TEAM(n, u, back)                                        \
+    if (team == n && each <= u && bwd == back)                        \
+        return launch_norm<T, n, u, WHOLE, back>(a, groups, stream)
+    PDSSM_TEAM(16, 1, false);
+    PDSSM_TEAM(64, 1, false);
+    PDSSM_TEAM(64, 2, false);
+    PDSSM_TEAM(64, 4, false);
+    PDSSM_TEAM(256, 2, false);
+    PDSSM_TEAM(256, 4, false);
+    PDSSM_TEAM(1024, 2, false);
+    PDSSM_TEAM(16, 1, true);
+    PDSSM_TEAM(64, 1, true);
+    PDSSM_TEAM(64, 2, true);
+    PDSSM_TEAM(128, 2, true);
+    PDSSM_TEAM(256, 2, true);
+    PDSSM_TEAM(512, 2, true);
+    PDSSM_TEAM(1024, 2, true);
+#undef PDSSM_TEAM
 }
 
 int launch_rows(const NormArgs &a, bool bf16, bool whole, bool bwd, int64_t groups, hipStream_t stream)
