@@ -15,6 +15,13 @@
 // so a mask costs a lane one block for each 16-byte load, and is made again in
 // the backward.  A team takes many rows with its weights (and the backward's sums
 // of dw and db) held in registers.
+//
+// Bytes bound all of them at the LM layer's 8 x 4096 rows of 2048, bf16, p = 0.1:
+// forward 114 us, 537 MB at 4.7 TB/s (x and the residual in, y and h out);
+// backward 143 us with its 4 us of layer_norm_sum_kernel, 671 MB at 4.7 TB/s (three
+// rows in, two out), of which the generator's second pass costs 6; dropout
+// alone 47 us, 268 MB at 5.7 TB/s.  A copy reaches 4.9 TB/s here, and 6.0
+// with two rows in for one out.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -453,7 +460,7 @@ __global__ void __launch_bounds__(threads_of<TEAM>()) layer_norm_bwd_kernel(Norm
 }
 
 // dw and db from the workgroups' sums.  A workgroup takes 16 columns, 64 rows at a
-// time.
+// time (512 rows of 2 x 2048: 4.4 us, mostly the launch's latency).
 constexpr int kSumRows = 64, kSumCols = 16;
 struct SumArgs {
     const float *partial;   // [rows][2][D]

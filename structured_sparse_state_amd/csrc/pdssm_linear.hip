@@ -24,13 +24,23 @@
 // products, the walk of dK, whose state has the same shape and the same owner
 // for every value, adds the rest.
 //
-// The walk.  Waves 0..3 ("chain") own 16 columns of the state each, whose
+// The walk.  A workgroup takes SL = 64 or 128 columns of one head's state over the
+// chunks of a segment.  Its first SL / 16 waves ("chain") own 16 columns each, whose
 // recurrences are independent, and keep them in registers in the matrix cores'
-// result layout, from where they feed the products without leaving the wave.
-// Waves 4..7 ("help") bring the next chunk's rows to LDS, sum its gates and
-// form M, all ahead of the chain.  States, M and the weighted X3 enter the
-// products as three bf16 parts (all 24 bits); bf16 rows are one part, fp32 rows
-// three.
+// result layout, from where they feed the products without leaving the wave.  The
+// four waves behind them ("help") bring the next chunk's rows to LDS, sum its gates
+// and form M, all ahead of the chain; a barrier ends each chunk.  States, M and the
+// weighted X3 enter the products as three bf16 parts (all 24 bits); bf16 rows are
+// one part, fp32 rows three.  Parts that meet bf16 rows are cut off (24 bits in three
+// parts, nothing left out); three parts against three leave out the products of
+// order 3 and more, so those are rounded, which keeps them smaller.
+//
+// What bounds it: in every chunk the chain's products, one after another on the
+// state (about 3400 to 4000 clocks; 284 matrix instructions of 16 clocks each over
+// the workgroup at 64 x 64), and the help waves' way from loads through LDS to M
+// (about 3500), between the same barriers.  8 x 32 heads of 64, 4096 steps, forward,
+// one decay a head: 138 us, 541 MB at 3.9 TB/s (the rows alone, staged and nothing
+// else, 75 us); 150 with gates of every step.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -784,7 +794,8 @@ __global__ void __launch_bounds__(walk_threads(SL), 1) walk_kernel(LinArgs a)
 // ---------------------------------------------------------------------------
 // join_kernel: the states before the segments, from the segments' decays and
 // ends: the first segment's end is whole, S_{n+1} = decay_n S_n + end_n.  A
-// thread has four values of one state.
+// thread has four values of one state; the segments follow each other (4.3 us for
+// 8 states of 128 x 128 and 32 segments, 14 for the three walks of 64 heads in two).
 // ---------------------------------------------------------------------------
 template <int KD>
 __global__ void __launch_bounds__(256) lin_join_kernel(LinArgs a)
@@ -806,7 +817,9 @@ __global__ void __launch_bounds__(256) lin_join_kernel(LinArgs a)
 
 // ---------------------------------------------------------------------------
 // group_kernel: dq and dk as the sums over the value heads of their group, from
-// fp32 [B*Hv][L][pitch].  A thread has four values of a row.
+// fp32 [B*Hv][L][pitch].  A thread has four values of a row, and nothing else to do
+// than move them: 59 us for 2 x 16 heads of 4 sequences of 4096 rows of 128 into 8,
+// 336 MB at 5.7 TB/s.
 // ---------------------------------------------------------------------------
 struct GroupArgs {
     const float *part[2];
@@ -849,7 +862,8 @@ __global__ void __launch_bounds__(256) group_kernel(GroupArgs a)
 
 // ---------------------------------------------------------------------------
 // dg from the slices' parts: of every step, or (a workgroup for each head) the
-// sum over sequences and steps, in 64 bits.
+// sum over sequences and steps, in 64 bits: 5 and 4 us at 64 heads and 4096 steps
+// and at 6 and 333, a launch's latency.
 // ---------------------------------------------------------------------------
 struct GateArgs {
     const float *part;      // [slices][B*Hv][L]
@@ -896,7 +910,9 @@ __global__ void __launch_bounds__(256) gate_heads_kernel(GateArgs a)
 // ---------------------------------------------------------------------------
 // lin_step_kernel: one step.  A workgroup takes 32 columns of one head's state,
 // each thread four columns of every 32nd row, all rows in registers: the state
-// is read once and written once, and o falls out on the way.
+// is read once and written once, and o falls out on the way.  Its bytes bound it:
+// 128 x 32 states of 128 x 64 take 55 us, 270 MB at 4.9 TB/s (a copy's rate); 16
+// states of 128 x 128 4.4 us, a launch's latency.
 // ---------------------------------------------------------------------------
 struct LinStepArgs {
     Rows q, k, v, g, o;
@@ -1025,25 +1041,45 @@ int check_linear_dims(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int32_t Dk, 
 
 int slices_of(int D, int SL) { return (D + SL - 1) / SL; }
 int padded(int D) { return D <= 64 ? 64 : 128; }
-// Columns of a workgroup: three parts of fp32 rows leave no room for 128.
-int slice_for(int D3, uint32_t flags) { return (flags & PDSSM_DATA_BF16) ? padded(D3) : 64; }
+// Columns of a workgroup, from the walks of a launch at 64 columns each.  128 take
+// the rows through LDS and form M once in place of twice: 318 against 414 us for
+// 8 x 32 heads of 128 and 4096 steps, 83 against 90 for 8 heads and 18000.  Of 64 a
+// chunk is done sooner, which counts while the device is not filled: 22 against 39 us
+// for 8 heads and 512 steps, 37 against 44 and 4096.  (Three parts of fp32 rows leave
+// no room for 128.)
+int slice_for(int D3, int64_t walks, int64_t L, uint32_t flags)
+{
+    const int64_t NC = (L + kC - 1) / kC;
+    return !(flags & PDSSM_DATA_BF16) || D3 <= 64 || walks * std::max<int64_t>(1, NC / 4) <= 256 ? 64 : 128;
+}
 
 // How many segments the chunks of a head are cut into, walked side by side: they
-// are walked twice (once without outputs) and joined, so walks are cut only
-// where a launch's workgroups do not fill the device, and no finer than fills it.
+// are walked twice (once without outputs, at half the cost) and joined, so walks are
+// cut only where a launch's workgroups do not fill the device, no finer than fills
+// it, and where the chunks saved are worth the two launches more: about three chunks
+// of a bf16 forward, whose walks begin with a chunk's wait, fewer of the others.
+// Heads of 128 (fp32: 64 and 100), one sequence, us cut and whole:
+//     bf16 forward, 8 heads    256 steps 19, 18      512: 22, 28     4096: 37, 173    18000: 83, 1098
+//     fp32 forward, 8 heads    128: 18, 15           256: 19, 24     2048: 30, 154
+//     bf16 backward, 8 heads   128: 33, 32           256: 38, 47     512: 47, 78      4096: 97, 598
+//     fp32 backward, 6 heads   128: 79, 96           333: 87, 217    2048: 187, 1120
+// and one chunk a segment in place of two: 28 against 25 us forward, bf16, 1024 steps;
+// 19 against 24, fp32, 333; backward 87 against 119, fp32, 333.
 struct Cut {
     int segs, chunks;
 };
 
-Cut cut_of(int64_t walks, int64_t L)
+Cut cut_of(int64_t walks, int64_t L, uint32_t flags, bool bwd)
 {
-    const int64_t NC = (L + kC - 1) / kC;
-    int64_t segs = 1;
-    if (walks > 0 && walks <= 128 && NC >= 16)
-        segs = std::min<int64_t>(256 / walks, NC / 4);
-    Cut c;
-    c.chunks = (int)std::max<int64_t>(1, (NC + segs - 1) / segs);
-    c.segs = (int)std::max<int64_t>(1, (NC + c.chunks - 1) / c.chunks);
+    const bool bf16 = flags & PDSSM_DATA_BF16;
+    const int64_t NC = (L + kC - 1) / kC, launches = bwd ? bf16 : bf16 ? 3 : 1;
+    const int64_t segs = walks > 0 ? std::min(256 / walks, bf16 && !bwd ? NC / 2 : NC) : 0;
+    Cut c = {1, (int)std::max<int64_t>(1, NC)};
+    if (segs > 1) {
+        const int64_t chunks = (NC + segs - 1) / segs;
+        if (3 * chunks + 2 * launches <= 2 * NC)
+            c = {(int)((NC + chunks - 1) / chunks), (int)chunks};
+    }
     return c;
 }
 
@@ -1060,6 +1096,7 @@ struct Space {
 
 struct LinLayout {
     Space space;
+    int SL;                 // columns of a workgroup (dK's with dg: 64)
     Cut cut[3];
     int groups[3];
     int64_t starts[3], wholes[3], kept, reads, dg_part, dq_part, dk_part, ds;
@@ -1074,13 +1111,17 @@ LinLayout layout_of(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int Dk, int Dv
     const bool grad = bwd && !(flags & PDSSM_NO_DG);
     l.space.take(256);
     if (bwd) {
-        const int SL = slice_for(std::max(Dk, Dv), flags), sk = slices_of(Dk, SL), sv = slices_of(Dv, SL);
-        // with dg dK's walk comes after the others, its columns 64 at a time
-        const Cut first = cut_of(heads * (sk + sv + (grad ? 0 : sk)), L);
-        l.cut[0] = l.cut[1] = first;
-        l.cut[2] = grad ? cut_of(heads * slices_of(Dk, 64), L) : first;
+        // With dg dK's walk comes after the others, its columns 64 at a time.  Cut for
+        // that without dg too, so that the other gradients' bits do not depend on it
+        // (432 us with dg and 304 without for 4 x 16 heads of 128, 4096 steps; cut for
+        // three walks at once 656 and 263).
+        auto walks = [&](int SL) { return heads * (slices_of(Dk, SL) + slices_of(Dv, SL)); };
+        l.SL = slice_for(std::max(Dk, Dv), walks(64), L, flags);
+        l.cut[0] = l.cut[1] = cut_of(walks(l.SL), L, flags, true);
+        l.cut[2] = cut_of(heads * slices_of(Dk, 64), L, flags, true);
     } else {
-        l.cut[0] = cut_of(heads * slices_of(Dv, slice_for(Dv, flags)), L);
+        l.SL = slice_for(Dv, heads * slices_of(Dv, 64), L, flags);
+        l.cut[0] = cut_of(heads * slices_of(Dv, l.SL), L, flags, false);
     }
     const int64_t rows = std::max(padded(Dk), padded(Dv));
     for (int n = 0; n < (bwd ? 3 : 1); ++n) {
@@ -1153,34 +1194,47 @@ int launch_walks(LinArgs a, bool grad, hipStream_t stream)
     if constexpr (!BWD) {
         return launch(walk_kernel<KD, BF16, VEC, SL, kOut, kForward>, SL, lds, 0, 0, false);
     } else {
-        if (!grad)
-            return launch(walk_kernel<KD, BF16, VEC, SL, kOut, kBoth>, SL, lds, 0, 2, false);
+        constexpr size_t lds64 = LinLds<KD, BF16, 64>::kBytes;
+        if (!grad) {
+            // Cut walks fill the device more than once: dK's then go behind the others
+            // with columns of 64 (304 against 320 us for 4 x 16 heads of 128, 4096 steps).
+            if (SL == 64 || a.w[2].segs == 1)
+                return launch(walk_kernel<KD, BF16, VEC, SL, kOut, kBoth>, SL, lds, 0, 2, false);
+            rc = launch(walk_kernel<KD, BF16, VEC, SL, kOut, kBoth>, SL, lds, 0, 1, false);
+            return rc == PDSSM_OK ? launch(walk_kernel<KD, BF16, VEC, 64, kOut, kBoth>, 64, lds64, 2, 2, false) : rc;
+        }
         // dK's walk adds up dg from what dQ's keeps
         rc = launch(walk_kernel<KD, BF16, VEC, SL, kOut, kFirst>, SL, lds, 0, 1, false);
-        return rc == PDSSM_OK ? launch(walk_kernel<KD, BF16, VEC, 64, kOut, kLast>, 64, LinLds<KD, BF16, 64>::kBytes, 2, 2, false) : rc;
+        return rc == PDSSM_OK ? launch(walk_kernel<KD, BF16, VEC, 64, kOut, kLast>, 64, lds64, 2, 2, false) : rc;
     }
 }
 
-// The variant for these sizes, type and rows: D1 and D3 the largest contraction
-// and columns of the walks.
-template <bool BF16, bool VEC>
-int launch_sizes(const LinArgs &a, int D1, int D3, bool bwd, bool grad, hipStream_t stream)
+// The variant for these sizes, type and rows: D1 the largest contraction of the
+// walks.
+template <int KD, bool BF16, bool VEC>
+int launch_width(const LinArgs &a, int SL, bool bwd, bool grad, hipStream_t stream)
 {
-    constexpr int wide = BF16 ? 128 : 64;
-    if (bwd)
-        return D1 > 64 ? launch_walks<128, BF16, VEC, wide, true>(a, grad, stream) : launch_walks<64, BF16, VEC, 64, true>(a, grad, stream);
     if constexpr (BF16) {
-        if (D3 > 64)
-            return D1 > 64 ? launch_walks<128, BF16, VEC, 128, false>(a, false, stream) : launch_walks<64, BF16, VEC, 128, false>(a, false, stream);
+        if (SL == 128 && !bwd)
+            return launch_walks<KD, BF16, VEC, 128, false>(a, false, stream);
+        if constexpr (KD == 128)        // (backward, columns and contraction change places)
+            if (SL == 128)
+                return launch_walks<KD, BF16, VEC, 128, true>(a, grad, stream);
     }
-    return D1 > 64 ? launch_walks<128, BF16, VEC, 64, false>(a, false, stream) : launch_walks<64, BF16, VEC, 64, false>(a, false, stream);
+    return bwd ? launch_walks<KD, BF16, VEC, 64, true>(a, grad, stream) : launch_walks<KD, BF16, VEC, 64, false>(a, grad, stream);
 }
 
-int launch_any(const LinArgs &a, bool bf16, bool vec, int D1, int D3, bool bwd, bool grad, hipStream_t stream)
+template <bool BF16, bool VEC>
+int launch_sizes(const LinArgs &a, int D1, int SL, bool bwd, bool grad, hipStream_t stream)
+{
+    return D1 > 64 ? launch_width<128, BF16, VEC>(a, SL, bwd, grad, stream) : launch_width<64, BF16, VEC>(a, SL, bwd, grad, stream);
+}
+
+int launch_any(const LinArgs &a, bool bf16, bool vec, int D1, int SL, bool bwd, bool grad, hipStream_t stream)
 {
     if (bf16)
-        return vec ? launch_sizes<true, true>(a, D1, D3, bwd, grad, stream) : launch_sizes<true, false>(a, D1, D3, bwd, grad, stream);
-    return vec ? launch_sizes<false, true>(a, D1, D3, bwd, grad, stream) : launch_sizes<false, false>(a, D1, D3, bwd, grad, stream);
+        return vec ? launch_sizes<true, true>(a, D1, SL, bwd, grad, stream) : launch_sizes<true, false>(a, D1, SL, bwd, grad, stream);
+    return vec ? launch_sizes<false, true>(a, D1, SL, bwd, grad, stream) : launch_sizes<false, false>(a, D1, SL, bwd, grad, stream);
 }
 
 }  // namespace
@@ -1263,7 +1317,7 @@ extern "C" int pdssm_linear_fwd(const void *q, const void *k, const void *v, con
     a.Hk = (int)Hk, a.Hv = (int)Hv, a.L = (int)L, a.NC = (int)((L + kC - 1) / kC), a.scale = scale;
     const bool vec = units(q, s[0], Dk, esize) && units(k, s[1], Dk, esize) && units(v, s[2], Dv, esize) &&
                      units(o, s[4], Dv, esize);
-    return launch_any(a, esize == 2, vec, Dk, Dv, false, false, stream);
+    return launch_any(a, esize == 2, vec, Dk, lo.SL, false, false, stream);
 }
 
 extern "C" int pdssm_linear_bwd(const void *q, const void *k, const void *v, const float *g, const float *s0,
@@ -1358,7 +1412,7 @@ extern "C" int pdssm_linear_bwd(const void *q, const void *k, const void *v, con
     const bool vec_keys = units(dq, s[5], Dk, esize) && units(dk, s[6], Dk, esize);
     const bool vec = units(q, s[0], Dk, esize) && units(k, s[1], Dk, esize) && units(v, s[2], Dv, esize) &&
                      units(d_o, s[4], Dv, esize) && vec_keys && units(dv, s[7], Dv, esize);
-    rc = launch_any(a, esize == 2, vec, std::max(Dk, Dv), std::max(Dk, Dv), true, grad, stream);
+    rc = launch_any(a, esize == 2, vec, std::max(Dk, Dv), lo.SL, true, grad, stream);
     if (rc == PDSSM_OK && a.dg_part) {
         ga.part = a.dg_part;
         if (dg_heads)
