@@ -18,6 +18,11 @@ Beside the scan (``include/pdssm_layers.h``): the gated delta rule,
 ``delta_rule`` (whole sequences), ``delta_rule_bwd`` (gradients) and
 ``delta_step`` (one step), and the norm of queries and keys with the rotation
 by position, ``qk_norm_rope`` and ``qk_norm_rope_bwd``.
+
+For a layer's block (``include/pdssm_block.h``): linear attention with decays,
+``linear_attention``, ``linear_attention_bwd`` and ``linear_attention_step``;
+the layer norm of a residual and a dropped-out branch, ``layer_norm`` and
+``layer_norm_bwd``; and ``dropout``.
 """
 from __future__ import annotations
 
