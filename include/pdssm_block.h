@@ -86,8 +86,9 @@ int pdssm_linear_fwd(const void *q, const void *k, const void *v, const float *g
                      const pdssm_strides *strides, void *workspace, size_t workspace_bytes,
                      hipStream_t stream);
 
-/* Workspace bytes of pdssm_linear_fwd: 256, and for long sequences of few
- * heads a state for each segment; 0 when the arguments are invalid. */
+/* Workspace bytes of pdssm_linear_fwd: 256, and for few heads, whose sequences
+ * are cut into at most 256 segments together, a state for each segment; 0 when
+ * the arguments are invalid. */
 size_t pdssm_linear_workspace_bytes(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int32_t Dk,
                                     int32_t Dv, uint32_t flags);
 
@@ -107,7 +108,8 @@ size_t pdssm_linear_workspace_bytes(int64_t B, int64_t Hk, int64_t Hv, int64_t L
  * Sizes and empty shapes as pdssm_linear_fwd; with L = 0, ds0 = ds_final (or
  * zero), and dg [Hv] is zero (with B = 0 too).  flags: PDSSM_DATA_BF16 and one
  * of PDSSM_NO_DG, PDSSM_DG_HEADS.  dg is 0 where g empties the state (below
- * -104), and for the first step without s0.
+ * -104), and for the first step without s0.  The other gradients are the same
+ * bits whether dg is wanted or not.
  */
 int pdssm_linear_bwd(const void *q, const void *k, const void *v, const float *g, const float *s0,
                      const void *d_o, const float *ds_final, void *dq, void *dk, void *dv,
@@ -118,8 +120,8 @@ int pdssm_linear_bwd(const void *q, const void *k, const void *v, const float *g
 
 /* Workspace bytes of pdssm_linear_bwd: with dg the state of every 64 steps of
  * a value head, with shared heads (Hv > Hk) dq and dk of every value head in
- * fp32, one state for each value head, and for long sequences of few heads
- * three for each segment; 0 when the arguments are invalid. */
+ * fp32, one state for each value head, and for few heads three for each segment
+ * as pdssm_linear_fwd; 0 when the arguments are invalid. */
 size_t pdssm_linear_bwd_workspace_bytes(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int32_t Dk,
                                         int32_t Dv, uint32_t flags);
 

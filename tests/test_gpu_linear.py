@@ -243,6 +243,23 @@ def test_cut_sequences(dtype, B, Hk, Hv, L, Dk, Dv, order, gates, s0):
     check_bwd(x, f"cut L={L} Dk={Dk} Dv={Dv} {order} {gates}")
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("B,Hk,Hv,L,Dk,Dv,order,gates,s0", [
+    (1, 1, 1, 64 * 2, 64, 64, "token", "plain", True),          # two chunks: a segment each, where that pays
+    (1, 1, 2, 64 * 3 + 1, 100, 40, "head", "heads", True),      # segments of one chunk, one step in the last
+    (2, 1, 2, 64 * 4, 128, 128, "token", "empty", True),
+    (1, 2, 4, 64 * 6, 128, 72, "apart", "strong", True),        # the fewest chunks of a bf16 forward that are cut
+    (1, 2, 2, 64 * 7 + 9, 64, 128, "head", "none", False),
+    (2, 40, 80, 130, 24, 72, "token", "plain", True),           # so many heads that a workgroup takes 128 columns
+    (2, 64, 64, 64, 8, 128, "head", "heads", False),            # and just not
+    (1, 100, 100, 64 * 16 + 1, 16, 16, "token", "plain", True), # two segments
+])
+def test_columns_and_segments_of_short_sequences(dtype, B, Hk, Hv, L, Dk, Dv, order, gates, s0):
+    x = inputs(L + Dv, B, Hk, Hv, L, Dk, Dv, TYPES[dtype], order=order, gates=gates, s0=s0)
+    check_fwd(x, f"short L={L} Hv={Hv} Dk={Dk} Dv={Dv} {order} {gates}")
+    check_bwd(x, f"short L={L} Hv={Hv} Dk={Dk} Dv={Dv} {order} {gates}")
+
+
 @pytest.mark.parametrize("Dk,Dv", [(64, 64), (128, 128), (40, 72)])
 def test_states_in_place_of_cut_sequences(Dk, Dv):
     """s_final over s0 and ds0 over ds_final, bit for bit as elsewhere."""
