@@ -239,6 +239,24 @@ struct Tile {
         }
     }
 
+    // Values col .. col + 3 of a row (col a multiple of 4), and one value.
+    static __device__ __forceinline__ f32x4 four(const uint16_t *lds, int row, int col)
+    {
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int n = NK - 1; n >= 0; --n)
+            v += __builtin_convertvector(*reinterpret_cast<const bf16x4 *>(lds + n * kPart + row * kRow + col), f32x4);
+        return v;
+    }
+    static __device__ __forceinline__ float one(const uint16_t *lds, int row, int col)
+    {
+        float v = 0.f;
+#pragma unroll
+        for (int n = NK - 1; n >= 0; --n)
+            v += bf16_lo(lds[n * kPart + row * kRow + col]);
+        return v;
+    }
+
     // Row tile `a`, k = 32 s + 8 g + 0..7 (plain order).
     static __device__ __forceinline__ Frag<NK> rows(const uint16_t *lds, int a, int s, int lane)
     {

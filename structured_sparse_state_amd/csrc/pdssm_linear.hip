@@ -35,6 +35,12 @@
 // parts, nothing left out); three parts against three leave out the products of
 // order 3 and more, so those are rounded, which keeps them smaller.
 //
+// Growth.  Decays inside a chunk are e^(sum of g): sums above 88 are more than fp32
+// holds, and infinity times a state, a key or a value that is zero would be NaN where
+// the definition gives zero.  Where the positive gates of some chunk add up to more
+// than 22 the walk is done a second time, step by step, with factors of any size as a
+// float and a power of two.
+//
 // What bounds it: in every chunk the chain's products, one after another on the
 // state (about 3400 to 4000 clocks; 284 matrix instructions of 16 clocks each over
 // the workgroup at 64 x 64), and the help waves' way from loads through LDS to M
@@ -71,7 +77,7 @@ struct Walk {
     float *end;             // and after its last, NULL: not wanted
     int row, col;           // strides of a state's values along contraction and columns
     float *starts;          // [segs + 1]: states before the segments, see native()
-    float *wholes;          // [segs][heads]: the segments' decays
+    float2 *wholes;         // [segs][heads]: the segments' decays, as a float and a power of two
     int segs, seg_chunks;
 };
 
@@ -92,6 +98,7 @@ struct LinArgs {
 
 enum Mode { kOut, kScan };          // outputs; the last state alone
 enum Gate { kNone, kKeep, kGrad };  // what a walk does for dg
+enum Pass { kFast, kCareful, kSteps };      // see walk_pass
 
 // 16 columns of a state as a chain wave holds them: group `group` of state
 // number n of a head, [KD / 16][64 lanes] four values each.
@@ -230,14 +237,88 @@ __device__ __forceinline__ void await_all(int *flags, int v)
     asm volatile("" ::: "memory");
 }
 
+// Walks with a chunk whose positive gates add up to more (2^32 together) are done step
+// by step.
+constexpr float kGrows = 22.f;
+// e^g of more leaves no number of fp32 but zero finite.
+constexpr float kMostGate = 1e4f;
+
+// e^x as a float and a power of two, of any size.
+struct Growth {
+    float f;
+    int n;
+    __device__ __forceinline__ float of(float v) const { return n ? ldexpf(v * f, n) : v * f; }
+    __device__ __forceinline__ f32x4 of(f32x4 v) const { return f32x4{of(v[0]), of(v[1]), of(v[2]), of(v[3])}; }
+};
+
+// As decay_of, with the same bits where it is below 2^64.
+__device__ __forceinline__ Growth growth_of(float hi_i, float lo_i, float n_i, float hi_j, float lo_j, float n_j)
+{
+    const float e = (hi_i - hi_j) + (lo_i - lo_j);
+    if (n_i != n_j)
+        return {0.f, 0};
+    const float n = e > 64.f && finite(e) ? rintf(e) : 0.f;     // (below 2^20, by kMostGate)
+    return {__builtin_amdgcn_exp2f(e - n), (int)n};
+}
+
 __device__ __forceinline__ int scalar(unsigned v) { return __builtin_amdgcn_readfirstlane((int)v); }
 
-// One walk over the chunks of a segment.  CAREFUL: looks at every chunk for
-// values of X3 that are not finite, which would reach the steps on the other
-// side of the triangle through its zeros.  Gives true when a state that is not
-// finite at the end asks for such a second pass.
-template <int KD, bool BF16, bool VEC, int SL, bool BACK, int MODE, int GATE, bool CAREFUL>
-__device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int seg, int slice, int64_t head, int thread)
+// A chunk step by step, from its rows in LDS: the wave's columns of the state and of
+// the result.  Lane (g, i16) has rows 16 m + 4 g + r of column i16 of the state, so a
+// value of Y is a sum over the four g.
+template <int KD, bool BF16, int SL, bool BACK, int MODE>
+__device__ __forceinline__ void walk_steps(const uint16_t *s_x1, const uint16_t *s_x2, const uint16_t *s_x3, int mine, int lane,
+                                           Growth own, float scale, f32x4 (&S)[KD / 16], f32x4 (&Y)[4])
+{
+    using T1 = typename LinLds<KD, BF16, SL>::T1;
+    using T3 = typename LinLds<KD, BF16, SL>::T3;
+    const int g = lane >> 4, i16 = lane & 15;
+#pragma unroll
+    for (int tile = 0; tile < 4; ++tile) {
+        const int at = BACK ? 3 - tile : tile;
+        if constexpr (MODE == kOut)
+            Y[at] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int n = 0; n < 16; ++n) {
+            const int step = BACK ? 15 - n : n, t = 16 * at + step;
+            const Growth now = {__int_as_float(__builtin_amdgcn_readlane(__float_as_int(own.f), t)),
+                                __builtin_amdgcn_readlane(own.n, t)};
+            const float value = (BACK ? scale : 1.f) * T3::one(s_x3, t, 16 * mine + i16);
+            float y = 0.f;
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m) {
+                const f32x4 key = T1::four(s_x2, t, 16 * m + 4 * g);
+                if constexpr (!BACK)
+                    S[m] = now.of(S[m]);
+                S[m] += key * value;
+                if constexpr (MODE == kOut) {
+                    const f32x4 query = T1::four(s_x1, t, 16 * m + 4 * g);
+                    y += query[0] * S[m][0] + query[1] * S[m][1] + query[2] * S[m][2] + query[3] * S[m][3];
+                }
+                if constexpr (BACK)
+                    S[m] = now.of(S[m]);
+            }
+            if constexpr (MODE == kOut) {
+                y += __shfl_xor(y, 16, 64);
+                y += __shfl_xor(y, 32, 64);
+                y *= BACK ? 1.f : scale;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float v = bperm(y, 4 * g + r);
+                    Y[at][r] = i16 == step ? v : Y[at][r];
+                }
+            }
+        }
+    }
+}
+
+// One walk over the chunks of a segment.  kFast gives the pass that is to follow:
+// kSteps, every chunk step by step, where one grows by more than kGrows; kCareful,
+// with a look at every chunk for values of X3 that are not finite, which would reach
+// the steps on the other side of the triangle through its zeros, where the state at
+// the end is not finite; or none (kFast).
+template <int KD, bool BF16, bool VEC, int SL, bool BACK, int MODE, int GATE, int PASS>
+__device__ __forceinline__ int walk_pass(const LinArgs &a, const Walk &w, int seg, int slice, int64_t head, int thread)
 {
     using LDS = LinLds<KD, BF16, SL>;
     using T1 = typename LDS::T1;
@@ -261,11 +342,25 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
     auto vecs = [&](int p) { return ldf + LDS::kVec + ((p - p0) & 3) * (kVecs * kC); };
     auto rows_of = [&](int p) { return min(kC, a.L - chunk_of(p) * kC); };
     constexpr int kSize = BF16 ? 2 : 4;
+    constexpr bool CAREFUL = PASS == kCareful, STEPS = PASS == kSteps;
+    constexpr int kGateWave = 1;        // (a help wave with two blocks of M where others have three)
 
     if (wave >= kChain && lane == 0)
         s_help[mine] = 0;
     lds_barrier();
-    bool again = false;
+    int again = kFast;
+    auto follows = [&]() {      // (behind the pass's last barrier)
+        if (PASS != kFast)
+            return kFast;
+        if (s_help[kGateWave] < 0)
+            return kSteps;
+        int spoiled = 0;
+        if constexpr (MODE == kOut) {
+            for (int n = 0; n < kChain; ++n)
+                spoiled |= s_spoiled[n];
+        }
+        return spoiled ? kCareful : kFast;
+    };
 
     if (wave < kChain) {
         const int col = group * 16 + i16;
@@ -291,8 +386,8 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
                 *reinterpret_cast<f32x4 *>(to + m * 256) = S[m];
         }
         Frag<3> sf[NS];
-        float product = 1.f;
-        if constexpr (MODE == kOut) {
+        Growth product = {1.f, 0};
+        if constexpr (MODE == kOut && !STEPS) {
 #pragma unroll
             for (int s = 0; s < NS; ++s)
                 sf[s] = parts<NK>(S[2 * s], S[2 * s + 1]);
@@ -332,10 +427,17 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
             const uint16_t *s_x1 = lds + LDS::kX1 + half * T1::kSize, *s_x2 = lds + LDS::kX2 + half * T1::kSize;
             const uint16_t *s_x3 = lds + LDS::kX3 + half * T3::kSize, *s_m = lds + LDS::kM + half * M::kSize;
             const float *s_vec = vecs(p);
+            // e^g summed from a step behind `from` to `to` (-1: before the first)
+            auto grown = [&](int from, int to) {
+                auto at = [&](int which, int t) { return t < 0 ? 0.f : s_vec[which * kC + t]; };
+                return growth_of(at(kGhi, to), at(kGlo, to), at(kResets, to), at(kGhi, from), at(kGlo, from), at(kResets, from));
+            };
             Frag<NK> x3[2];
+            if constexpr (!STEPS) {
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-                x3[s] = T3::columns_stacked(s_x3, mine, s, lane);
+                for (int s = 0; s < 2; ++s)
+                    x3[s] = T3::columns_stacked(s_x3, mine, s, lane);
+            }
             float gone = 1.f;       // NaN: a column of X3 that is not finite spoils its column of the state
             int from = kC;          // and its outputs from this step on (in the walk's order)
             if constexpr (CAREFUL) {
@@ -363,21 +465,25 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
                     }
             }
             f32x4 Y[4];    // tiles of 16 columns (rows of the result) by 16 steps
-            if constexpr (MODE == kOut) {
+            if constexpr (MODE == kOut && !(STEPS && GATE == kNone)) {
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
                     Y[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int s = 0; s < NS; ++s) {
+                    if constexpr (STEPS)
+                        sf[s] = parts<NK>(S[2 * s], S[2 * s + 1]);
                     Frag<NK> x1[4];
 #pragma unroll
                     for (int t = 0; t < 4; ++t)
                         x1[t] = T1::rows_stacked(s_x1, t, s, lane);
                     mma_tiles<0, 3>(sf[s], x1, Y);
                 }
+                if constexpr (!STEPS) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    Y[t] *= s_vec[kRead * kC + 16 * t + i16];
+                    for (int t = 0; t < 4; ++t)
+                        Y[t] *= s_vec[kRead * kC + 16 * t + i16];
+                }
                 if constexpr (GATE != kNone) {
                     float *to = GATE == kKeep ? a.reads + (((int64_t)c * a.heads + head) * w.groups + group) * kC
                                               : ldf + LDS::kWrites + (turn_of(p) * kChain + mine) * kC;
@@ -386,6 +492,8 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
                         float v = Y[t][0] * beside[t][0] + Y[t][1] * beside[t][1] + Y[t][2] * beside[t][2] + Y[t][3] * beside[t][3];
                         v += __shfl_xor(v, 16, 64);
                         v += __shfl_xor(v, 32, 64);
+                        if constexpr (STEPS)
+                            v = BACK ? grown(16 * t + i16, kC - 1).of(v) : grown(-1, 16 * t + i16).of(a.scale * v);
                         to[16 * t + i16] = v;     // (the four lanes of a step all write it)
                     }
                 }
@@ -401,72 +509,86 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
                     for (int m = 0; m < KD / 16; ++m)
                         v += kept[m][0] * S[m][0] + kept[m][1] * S[m][1] + kept[m][2] * S[m][2] + kept[m][3] * S[m][3];
                     v = sum64(v);
-                    ldf[LDS::kCross + turn_of(p) * kChain + wave] = v * s_vec[kWhole * kC];
+                    ldf[LDS::kCross + turn_of(p) * kChain + wave] = STEPS ? grown(-1, kC - 1).of(v) : v * s_vec[kWhole * kC];
                 }
                 if constexpr (GATE != kNone)
                     fetch(min(p + 1, p1 - 1));
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    Frag<3> m[4];
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        if (M::has(t, s))
-                            m[t] = M::template get<3>(s_m, t, s, lane);
-                    // (the triangle has all tiles of one k step, half of the other's)
-                    if (s == (BACK ? 1 : 0))
-                        mma_tiles<0, 3>(x3[s], m, Y);
-                    else if (BACK)
-                        mma_tiles<0, 1>(x3[s], m, Y);
-                    else
-                        mma_tiles<2, 3>(x3[s], m, Y);
+            }
+            const float whole = s_vec[kWhole * kC] * gone;
+            if constexpr (MODE == kScan) {
+                const Growth now = STEPS ? grown(-1, kC - 1) : Growth{whole, 0};
+                product.f *= now.f;
+                product.n = min(product.n + now.n, 1 << 20);
+                if (product.f > 0x1p32f) {
+                    product.f *= 0x1p-64f;
+                    product.n += 64;
                 }
-                if constexpr (CAREFUL) {
+            }
+            if constexpr (STEPS) {
+                walk_steps<KD, BF16, SL, BACK, MODE>(s_x1, s_x2, s_x3, mine, lane, grown(lane - 1, lane), a.scale, S, Y);
+            } else {
+                if constexpr (MODE == kOut) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int f = bperm(from, 4 * g + r);
+                    for (int s = 0; s < 2; ++s) {
+                        Frag<3> m[4];
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            const int step = 16 * t + i16;
-                            if ((BACK ? kC - 1 - step : step) >= f)
-                                Y[t][r] = __builtin_nanf("");
+                        for (int t = 0; t < 4; ++t)
+                            if (M::has(t, s))
+                                m[t] = M::template get<3>(s_m, t, s, lane);
+                        // (the triangle has all tiles of one k step, half of the other's)
+                        if (s == (BACK ? 1 : 0))
+                            mma_tiles<0, 3>(x3[s], m, Y);
+                        else if (BACK)
+                            mma_tiles<0, 1>(x3[s], m, Y);
+                        else
+                            mma_tiles<2, 3>(x3[s], m, Y);
+                    }
+                    if constexpr (CAREFUL) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int f = bperm(from, 4 * g + r);
+#pragma unroll
+                            for (int t = 0; t < 4; ++t) {
+                                const int step = 16 * t + i16;
+                                if ((BACK ? kC - 1 - step : step) >= f)
+                                    Y[t][r] = __builtin_nanf("");
+                            }
                         }
                     }
                 }
-            }
-            // the state
-            const float whole = s_vec[kWhole * kC] * gone;
-            product *= whole;
-            Frag<3> wx[2];
+                // the state
+                Frag<3> wx[2];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const f32x4 lo = row_vec(s_vec, kWrite, 2 * s, lane), hi = row_vec(s_vec, kWrite, 2 * s + 1, lane);
-                wx[s] = parts<NK>(joined(x3[s]) * __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-            }
+                for (int s = 0; s < 2; ++s) {
+                    const f32x4 lo = row_vec(s_vec, kWrite, 2 * s, lane), hi = row_vec(s_vec, kWrite, 2 * s + 1, lane);
+                    wx[s] = parts<NK>(joined(x3[s]) * __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                }
 #pragma unroll
-            for (int m = 0; m < KD / 16; ++m)
-                S[m] *= whole;
+                for (int m = 0; m < KD / 16; ++m)
+                    S[m] *= whole;
 #pragma unroll
-            for (int s = 0; s < NS; ++s) {
-                Frag<NK> x2[2][2];
+                for (int s = 0; s < NS; ++s) {
+                    Frag<NK> x2[2][2];
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        x2[m][i] = T1::columns_stacked(s_x2, 2 * s + m, i, lane);
+                        for (int i = 0; i < 2; ++i)
+                            x2[m][i] = T1::columns_stacked(s_x2, 2 * s + m, i, lane);
 #pragma unroll
-                for (int o = 2; o >= 0; --o)
+                    for (int o = 2; o >= 0; --o)
 #pragma unroll
-                    for (int n = 0; n < NK; ++n)
-                        if (o - n >= 0) {
+                        for (int n = 0; n < NK; ++n)
+                            if (o - n >= 0) {
 #pragma unroll
-                            for (int i = 0; i < 2; ++i)
+                                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                                for (int m = 0; m < 2; ++m)
-                                    S[2 * s + m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x2[m][i].p[n], wx[i].p[o - n],
-                                                                                          S[2 * s + m], 0, 0, 0);
-                        }
-                if constexpr (MODE == kOut)
-                    sf[s] = parts<NK>(S[2 * s], S[2 * s + 1]);
+                                    for (int m = 0; m < 2; ++m)
+                                        S[2 * s + m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x2[m][i].p[n], wx[i].p[o - n],
+                                                                                              S[2 * s + m], 0, 0, 0);
+                            }
+                    if constexpr (MODE == kOut)
+                        sf[s] = parts<NK>(S[2 * s], S[2 * s + 1]);
+                }
             }
             if constexpr (MODE == kOut) {
                 auto store = [&](auto cy) {
@@ -489,7 +611,9 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
             for (int m = 0; m < KD / 16; ++m)
                 *reinterpret_cast<f32x4 *>(to + m * 256) = S[m];
             if (thread == 0 && slice == 0)
-                w.wholes[seg * a.heads + head] = product;
+                w.wholes[seg * a.heads + head] = make_float2(product.f, (float)product.n);
+            lds_barrier();
+            again = follows();
         } else {
             float mark = 0.f;
 #pragma unroll
@@ -497,14 +621,13 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     mark = __builtin_fmaf(S[m][r], 0.f, mark);
-            const bool spoiled = !CAREFUL && __any(mark != 0.f);
+            const bool spoiled = PASS == kFast && __any(mark != 0.f);
             if (lane == 0)
                 s_spoiled[mine] = spoiled;
             lds_barrier();
-            for (int n = 0; n < kChain; ++n)
-                again |= s_spoiled[n] != 0;
+            again = follows();
             // (the end may be the start, from which a second pass begins)
-            if (w.end && p1 == a.NC && !again) {
+            if (w.end && p1 == a.NC && again == kFast) {
                 each_value<KD>(w, col, lane, [&](int m, int r, bool in, int at) {
                     if (in)
                         w.end[head * w.D1 * w.D3 + at] = S[m][r];
@@ -518,7 +641,7 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
         if constexpr (GATE != kNone)
             __builtin_amdgcn_s_setprio(2);
         const int tid = thread - kChain * 64;
-        constexpr int kGateWave = 1;    // (with two blocks of M where others have three)
+        float most = 0.f;       // (the gates' wave) the largest gate of a lane
         struct Incoming {
             T1 t1, t2;
             T3 t3;
@@ -576,7 +699,11 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
             // G log2(e) in 64 bits (differences of neighbours stay exact to 32),
             // steps that empty the state counted apart.
             float *s_vec = vecs(p);
-            const float now = has_steps ? gate : lane < rows_of(p) ? first_lane(gate) : 0.f;
+            float now = has_steps ? gate : lane < rows_of(p) ? first_lane(gate) : 0.f;
+            if constexpr (PASS == kFast)
+                most = fmaxf(most, now);
+            if constexpr (STEPS)
+                now = finite(now) ? fminf(now, kMostGate) : now;
             const bool empty = now < kEmpties;
             const double G = running_sum(empty ? 0.0 : (double)now * 1.4426950408889634);
             const float n = running_sum(empty ? 1.f : 0.f);
@@ -658,11 +785,19 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int col = 16 * tb[n] + 4 * g + r;
-                        const float d = BACK ? decay_of(hj[r], lj[r], nj[r], hi, lo, resets) : decay_of(hi, lo, resets, hj[r], lj[r], nj[r]);
-                        v[n][r] = (BACK ? col >= row : col <= row) ? a.scale * v[n][r] * d : 0.f;
-                        kq[n][r] = GATE == kGrad && col > row ? v[n][r] * kq[n][r] : 0.f;
+                        const bool inside = BACK ? col >= row : col <= row;
+                        if constexpr (STEPS) {
+                            // (the growth last: a product that is zero stays zero)
+                            const Growth d = BACK ? growth_of(hj[r], lj[r], nj[r], hi, lo, resets) : growth_of(hi, lo, resets, hj[r], lj[r], nj[r]);
+                            kq[n][r] = GATE == kGrad && col > row ? Growth{kq[n][r], d.n}.of(a.scale * v[n][r] * d.f) : 0.f;
+                        } else {
+                            const float d = BACK ? decay_of(hj[r], lj[r], nj[r], hi, lo, resets) : decay_of(hi, lo, resets, hj[r], lj[r], nj[r]);
+                            v[n][r] = inside ? a.scale * v[n][r] * d : 0.f;
+                            kq[n][r] = GATE == kGrad && col > row ? v[n][r] * kq[n][r] : 0.f;
+                        }
                     }
-                    M::put(s_m, ta[n], tb[n], lane, v[n]);
+                    if constexpr (!STEPS)
+                        M::put(s_m, ta[n], tb[n], lane, v[n]);
                 }
                 if constexpr (GATE == kGrad) {
 #pragma unroll
@@ -697,7 +832,7 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
                 }
             }
         };
-        if constexpr (MODE == kOut) {
+        if constexpr (MODE == kOut && !STEPS) {
             for (int n = 0; n < LDS::kHalves; ++n)
                 M::clear(lds + LDS::kM + n * M::kSize, tid);
         }
@@ -732,11 +867,26 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
             }
         }
         gates_of(p1 - 1);
-        if constexpr (MODE == kOut) {
-            lds_barrier();
-            for (int n = 0; n < kChain; ++n)
-                again |= s_spoiled[n] != 0;
+        // A chunk that grows has a gate above the mean of what it grows by: only then are
+        // the gates read again and summed (a branch in the loop, whatever it holds, costs
+        // the backward 2 %).
+        if constexpr (PASS == kFast) {
+            if (mine == kGateWave && __any(most > kGrows / kC)) {
+                bool grows = false;
+                Stream again(a.g.p, b * a.g.s.b + h * a.g.s.h, a.g.s.l, c0, BACK, 1, 4);
+                for (int p = p0; p < p1; ++p) {
+                    const Chunk<false, false> cg = again.chunk<false, false>(rows_of(p), 1);
+                    again.next(true);
+                    const float g = __uint_as_float(cg.raw(cg.lane_at(lane, 0), lane, 0, 0));
+                    grows |= sum64(finite(g) ? fmaxf(g, 0.f) : 0.f) > kGrows;
+                }
+                // (behind the last chunk's barrier: nobody waits for the flag any more)
+                if (grows && lane == 0)
+                    s_help[kGateWave] = -1;
+            }
         }
+        lds_barrier();
+        again = follows();
     }
     return again;
 }
@@ -744,13 +894,15 @@ __device__ __forceinline__ bool walk_pass(const LinArgs &a, const Walk &w, int s
 template <int KD, bool BF16, bool VEC, int SL, bool BACK, int MODE, int GATE>
 __device__ __forceinline__ void walk(const LinArgs &a, const Walk &w, int seg, int slice, int64_t head)
 {
-    // A state that is not finite at its end: the walk again, with a look at
-    // every chunk.
-    if (walk_pass<KD, BF16, VEC, SL, BACK, MODE, GATE, false>(a, w, seg, slice, head, threadIdx.x)) {
-        lds_barrier();      // the flags have been read
-        // (opaque: nothing formed for one pass is held through the other)
-        walk_pass<KD, BF16, VEC, SL, BACK, MODE, GATE, true>(a, w, seg, opaque_s(slice), head, opaque(threadIdx.x));
-    }
+    const int again = walk_pass<KD, BF16, VEC, SL, BACK, MODE, GATE, kFast>(a, w, seg, slice, head, threadIdx.x);
+    if (again == kFast)
+        return;
+    lds_barrier();      // the flags have been read
+    // (opaque: nothing formed for one pass is held through the other)
+    if (MODE == kOut && again == kCareful)
+        walk_pass<KD, BF16, VEC, SL, BACK, MODE, GATE, kCareful>(a, w, seg, opaque_s(slice), head, opaque(threadIdx.x));
+    else
+        walk_pass<KD, BF16, VEC, SL, BACK, MODE, GATE, kSteps>(a, w, seg, opaque_s(slice), head, opaque(threadIdx.x));
 }
 
 // Workgroups by walk, segment, slice, head, the head first: those that read the
@@ -759,8 +911,11 @@ __device__ __forceinline__ void walk(const LinArgs &a, const Walk &w, int seg, i
 enum Which { kForward, kBoth, kFirst, kLast };      // the forward's; dQ's, dV's and dK's; with dg: dQ's and dV's; dK's
 
 template <int KD, bool BF16, bool VEC, int SL, int MODE, int WHICH>
-__global__ void __launch_bounds__(walk_threads(SL), 1) walk_kernel(LinArgs a)
+__global__ void __launch_bounds__(walk_threads(SL), 1) walk_kernel(LinArgs)
 {
+    // (the arguments where they lie: of a parameter with this many uses the compiler
+    // makes a copy in scratch)
+    const LinArgs &a = *reinterpret_cast<const LinArgs *>((const void *)__builtin_amdgcn_kernarg_segment_ptr());
     unsigned rest = blockIdx.y * gridDim.x + blockIdx.x;
     if (rest >= a.blocks)
         return;
@@ -785,7 +940,9 @@ __global__ void __launch_bounds__(walk_threads(SL), 1) walk_kernel(LinArgs a)
         walk<KD, BF16, VEC, SL, true, MODE, kGrad>(a, w, seg, slice, head);
     } else {
         if (n == 0)
-            walk<KD, BF16, VEC, SL, false, MODE, WHICH == kFirst ? kKeep : kNone>(a, w, seg, slice, head);
+            walk<KD, BF16, VEC, SL, false, MODE, WHICH == kFirst ? kKeep : kNone>(a, a.w[0], seg, slice, head);
+        else if constexpr (WHICH == kFirst)
+            walk<KD, BF16, VEC, SL, true, MODE, kNone>(a, a.w[1], seg, slice, head);
         else
             walk<KD, BF16, VEC, SL, true, MODE, kNone>(a, w, seg, slice, head);
     }
@@ -810,7 +967,12 @@ __global__ void __launch_bounds__(256) lin_join_kernel(LinArgs a)
     f32x4 S = *reinterpret_cast<const f32x4 *>(p);
     for (int n = 1; n + 1 < w.segs; ++n) {
         p += size;
-        S = w.wholes[n * a.heads + head] * S + *reinterpret_cast<const f32x4 *>(p);
+        const float2 whole = w.wholes[n * a.heads + head];
+        const f32x4 end = *reinterpret_cast<const f32x4 *>(p);
+        const Growth by = {whole.x, (int)whole.y};
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            S[r] = by.n ? by.of(S[r]) + end[r] : __builtin_fmaf(by.f, S[r], end[r]);
         *reinterpret_cast<f32x4 *>(p) = S;
     }
 }
@@ -970,7 +1132,16 @@ __global__ void __launch_bounds__(256) lin_step_kernel(LinStepArgs a)
             k[i] = load_value<BF16>(a.k.p, b * a.k.s.b + hk * a.k.s.h + row);
         }
     }
-    const float decay = a.g.p ? expf(static_cast<const float *>(a.g.p)[b * a.g.s.b + h * a.g.s.h]) : 1.f;
+    // e^g may be more than fp32 holds, and the state zero: then as a power of two
+    // (rounded down, so that it leaves no finite result behind it) and the rest.
+    float decay = 1.f;
+    int shift = 0;
+    if (a.g.p) {
+        const float gate = static_cast<const float *>(a.g.p)[b * a.g.s.b + h * a.g.s.h];
+        const double e = finite(gate) ? (double)fminf(gate, kMostGate) * 1.4426950408889634 : 0.0;
+        shift = gate > 64.f ? (int)floor(e) : 0;
+        decay = shift ? __builtin_amdgcn_exp2f((float)(e - shift)) : expf(gate);
+    }
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int r = 0; r < 4; ++r)
@@ -981,7 +1152,9 @@ __global__ void __launch_bounds__(256) lin_step_kernel(LinStepArgs a)
 #pragma unroll
     for (int i = 0; i < RP; ++i) {
         const int row = i * TY + ty;
-        st[i] = st[i] * decay + k[i] * v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            st[i][r] = ldexpf(st[i][r], shift) * decay + k[i] * v[r];
         if (row < a.Dk) {
             o += q[i] * st[i];
             if constexpr (VEC) {
@@ -1128,7 +1301,7 @@ LinLayout layout_of(int64_t B, int64_t Hk, int64_t Hv, int64_t L, int Dk, int Dv
         l.groups[n] = (bwd ? (int)rows : padded(Dv)) / 16;
         if (l.cut[n].segs > 1) {
             l.starts[n] = l.space.take((l.cut[n].segs + 1) * heads * l.groups[n] * rows * 64);
-            l.wholes[n] = l.space.take(l.cut[n].segs * heads * 4);
+            l.wholes[n] = l.space.take(l.cut[n].segs * heads * 8);
         }
     }
     if (bwd) {
@@ -1310,7 +1483,7 @@ extern "C" int pdssm_linear_fwd(const void *q, const void *k, const void *v, con
     w.x1 = {q, s[0]}, w.x2 = {k, s[1]}, w.x3 = {v, s[2]}, w.y = {o, s[4]};
     w.kv1 = w.kv2 = true;
     w.D1 = Dk, w.D3 = Dv, w.groups = lo.groups[0], w.start = s0, w.end = s_final, w.row = Dv, w.col = 1;
-    w.starts = reinterpret_cast<float *>(ws + lo.starts[0]), w.wholes = reinterpret_cast<float *>(ws + lo.wholes[0]);
+    w.starts = reinterpret_cast<float *>(ws + lo.starts[0]), w.wholes = reinterpret_cast<float2 *>(ws + lo.wholes[0]);
     w.segs = lo.cut[0].segs, w.seg_chunks = lo.cut[0].chunks;
     a.g = {g, s[3]};
     a.heads = B * Hv;
@@ -1401,7 +1574,7 @@ extern "C" int pdssm_linear_bwd(const void *q, const void *k, const void *v, con
     }
     for (int n = 0; n < 3; ++n) {
         Walk &w = a.w[n];
-        w.groups = lo.groups[n], w.starts = place(lo.starts[n]), w.wholes = place(lo.wholes[n]);
+        w.groups = lo.groups[n], w.starts = place(lo.starts[n]), w.wholes = reinterpret_cast<float2 *>(place(lo.wholes[n]));
         w.segs = lo.cut[n].segs, w.seg_chunks = lo.cut[n].chunks;
     }
     a.g = {g, s[3]}, a.dg = ga.dg, a.started = s0 != nullptr;
