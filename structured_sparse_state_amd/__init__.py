@@ -1147,6 +1147,10 @@ def _drops(p: float) -> bool:
     return p * 65536 + 0.5 >= 1
 
 
+def _same_place(a, b) -> bool:
+    return a is not None and b is not None and (a is b or a.data_ptr() == b.data_ptr() != 0)
+
+
 @functools.lru_cache(maxsize=1024)
 def _layer_norm_plan(x, w, b, residual, y, h, rng):
     sizes = _block_form("x", x, rng, w, b, {"residual": residual, "y": y, "h": h})
@@ -1158,16 +1162,18 @@ def layer_norm(x, w=None, b=None, *, residual=None, eps: float = 1e-5, p: float 
     """The layer norm over the last dimension of h = residual + dropout(x):
     (y, h).  x and residual bf16 or fp32 of one to four dimensions, any strides
     but the last; w, b fp32 [D] or None (1 and 0).  Without residual and dropout
-    h is x itself, unless a place for it is given.  ``p``: the part of x that is
-    dropped; ``seed`` and ``offset`` pick the mask, or an int64 GPU tensor [2] in
-    place of seed holds both.  The results have the memory order of x; ``out``
-    and ``h``: tensors to write into instead (x or residual among them)."""
-    if stream is not None and (out is None or (h is None and (residual is not None or _drops(p)))):
+    h is x itself, unless y takes its place or a place for h is given.  ``p``: the
+    part of x that is dropped; ``seed`` and ``offset`` pick the mask, or an int64
+    GPU tensor [2] in place of seed holds both.  The results have the memory order
+    of x; ``out`` and ``h``: tensors to write into instead (x or residual among
+    them)."""
+    new = h is None and (residual is not None or _drops(p) or _same_place(out, x))
+    if stream is not None and (out is None or new):
         return _on_stream(stream, layer_norm, x, w, b, residual=residual, eps=eps, p=p, seed=seed, offset=offset,
                           out=out, h=h)
     y = torch.empty_like(x) if out is None else out
     to = h
-    if h is None and (residual is not None or _drops(p)):
+    if new:
         h = to = torch.empty_like(x)
     seed, offset, rng = _seed(seed, offset)
     (flag, B, H, L, D), rows = _layer_norm_plan(_form(x), _form(w), _form(b), _form(residual), _form(y), _form(to),
