@@ -1165,8 +1165,10 @@ def layer_norm(x, w=None, b=None, *, residual=None, eps: float = 1e-5, p: float 
     h is x itself, unless y takes its place or a place for h is given.  ``p``: the
     part of x that is dropped; ``seed`` and ``offset`` pick the mask, or an int64
     GPU tensor [2] in place of seed holds both.  The results have the memory order
-    of x; ``out`` and ``h``: tensors to write into instead (x or residual among
+    of x; ``out`` and ``h``: two tensors to write into instead (x or residual among
     them)."""
+    if _same_place(out, h):
+        raise ValueError("y and h are two tensors")
     new = h is None and (residual is not None or _drops(p) or _same_place(out, x))
     if stream is not None and (out is None or new):
         return _on_stream(stream, layer_norm, x, w, b, residual=residual, eps=eps, p=p, seed=seed, offset=offset,
@@ -1205,7 +1207,7 @@ def layer_norm_bwd(h, dy, w=None, *, dh=None, want_db: bool = False, eps: float 
     dr, dx = (torch.empty_like(h), torch.empty_like(h) if drops else None) if out is None else out
     if dx is None:
         dx = dr
-    if drops and dx is dr:
+    if drops and _same_place(dr, dx):
         raise ValueError("with dropout dr and dx are two tensors")
     seed, offset, rng = _seed(seed, offset)
     sums = w is not None or want_db

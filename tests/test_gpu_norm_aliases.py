@@ -32,3 +32,13 @@ def test_h_when_y_goes_over_x(dtype, given):
     over, place = x.clone(), torch.empty_like(x)
     assert pk.layer_norm(over, w, b, out=over, h=place)[1] is place and torch.equal(place, x)
     assert pk.layer_norm(x, w, b, out=torch.empty_like(x))[1] is x
+
+
+def test_two_results_are_two_tensors():
+    x, t = torch.zeros(2, 5, 8), torch.zeros(2, 5, 8)
+    for same in (t, t[:]):
+        for kw in (dict(), dict(residual=x), dict(residual=x, p=0.5, seed=1)):
+            with pytest.raises(ValueError, match="two tensors"):
+                pk.layer_norm(x, out=t, h=same, **kw)
+        with pytest.raises(ValueError, match="two tensors"):
+            pk.layer_norm_bwd(x, x, out=(t, same), p=0.5, seed=1)
