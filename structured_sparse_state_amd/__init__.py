@@ -665,16 +665,23 @@ def _on_stream(stream, call, *args, **kw):
         return call(*args, **kw)
 
 
-def _stream_of(t, stream) -> Optional[int]:
-    """`stream`, or the current stream of the tensor's device."""
-    if stream is not None:
-        return _stream(stream)
-    return _raw_stream(t.get_device()) if _raw_stream is not None and t.is_cuda else _stream(None)
-
-
 # The current stream's handle without building a Stream object, where this
 # torch has it.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _run(entry, t, stream, *args) -> None:
+    """The call on `stream`, or the current stream of the tensor's device, with
+    that device the current one: a default stream is the current device's."""
+    device = t.get_device()
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return _run(entry, t, stream, *args)
+    status = entry(*args, _raw_stream(device) if stream is None else _stream(stream))
+    if status != PDSSM_OK:
+        check(status)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -708,10 +715,9 @@ def delta_rule(q, k, v, g, beta, s0=None, *, scale: Optional[float] = None, want
     (flag, B, Hk, Hv, L, Dk, Dv), rows, need = _delta_plan(
         _form(q), _form(k), _form(v), _form(g), _form(beta), _form(o), _form(s0), _form(s_final))
     workspace = _workspace(need, workspace, v.device)
-    check(library().pdssm_delta_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-                                    beta.data_ptr(), _ptr(s0), o.data_ptr(), _ptr(s_final), B, Hk, Hv, L,
-                                    Dk, Dv, Dk ** -0.5 if scale is None else scale, flag, rows,
-                                    workspace.data_ptr(), need, _stream_of(v, stream)))
+    _run(library().pdssm_delta_fwd, v, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+         _ptr(s0), o.data_ptr(), _ptr(s_final), B, Hk, Hv, L, Dk, Dv, Dk ** -0.5 if scale is None else scale, flag,
+         rows, workspace.data_ptr(), need)
     return o, s_final
 
 
@@ -748,12 +754,10 @@ def delta_rule_bwd(q, k, v, g, beta, do, s0=None, ds_final=None, *, scale: Optio
         _form(q), _form(k), _form(v), _form(g), _form(beta), _form(s0), _form(do), _form(ds_final),
         _form(dq), _form(dk), _form(dv), _form(dg), _form(dbeta), _form(ds0))
     workspace = _workspace(need, workspace, v.device)
-    check(library().pdssm_delta_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-                                    beta.data_ptr(), _ptr(s0), do.data_ptr(), _ptr(ds_final),
-                                    dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(),
-                                    dbeta.data_ptr(), _ptr(ds0), B, Hk, Hv, L, Dk, Dv,
-                                    Dk ** -0.5 if scale is None else scale, flag, rows,
-                                    workspace.data_ptr(), need, _stream_of(v, stream)))
+    _run(library().pdssm_delta_bwd, v, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+         _ptr(s0), do.data_ptr(), _ptr(ds_final), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(),
+         dbeta.data_ptr(), _ptr(ds0), B, Hk, Hv, L, Dk, Dv, Dk ** -0.5 if scale is None else scale, flag, rows,
+         workspace.data_ptr(), need)
     return dq, dk, dv, dg, dbeta, ds0
 
 
@@ -780,10 +784,9 @@ def delta_step(q, k, v, g, beta, s, *, s_out: Optional[torch.Tensor] = None,
         o = torch.empty_like(v)
     flag, B, Hk, Hv, Dk, Dv, rows = _step_plan(_form(q), _form(k), _form(v), _form(g), _form(beta),
                                                _form(o), _form(s), _form(s_out))
-    check(library().pdssm_delta_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-                                     beta.data_ptr(), s.data_ptr(), o.data_ptr(), s_out.data_ptr(), B, Hk,
-                                     Hv, Dk, Dv, Dk ** -0.5 if scale is None else scale, flag, rows,
-                                     _stream_of(v, stream)))
+    _run(library().pdssm_delta_step, v, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+         beta.data_ptr(), s.data_ptr(), o.data_ptr(), s_out.data_ptr(), B, Hk, Hv, Dk, Dv,
+         Dk ** -0.5 if scale is None else scale, flag, rows)
     return o
 
 
@@ -849,9 +852,8 @@ def qk_norm_rope(q, k, wq=None, wk=None, cos=None, sin=None, pos=None, *, kind: 
     (flags, B, Hq, Hk, L, D, R, P), rows = _norm_plan(
         _form(q), _form(k), _form(wq), _form(wk), _form(cos), _form(sin), _form(pos), kind, pairs,
         _form(q_out), _form(k_out))
-    check(library().pdssm_qk_norm_rope_fwd(q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(cos),
-                                           _ptr(sin), _ptr(pos), q_out.data_ptr(), k_out.data_ptr(), B,
-                                           Hq, Hk, L, D, R, P, eps, flags, rows, _stream_of(q, stream)))
+    _run(library().pdssm_qk_norm_rope_fwd, q, stream, q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(cos),
+         _ptr(sin), _ptr(pos), q_out.data_ptr(), k_out.data_ptr(), B, Hq, Hk, L, D, R, P, eps, flags, rows)
     return q_out, k_out
 
 
@@ -884,12 +886,9 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, wq=None, wk=None, cos=None, sin=None,
     dwq, dwk = (None if w is None else torch.empty_like(w) for w in (wq, wk))
     if need:
         workspace = _workspace(need, workspace, q.device)
-    check(library().pdssm_qk_norm_rope_bwd(q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(cos),
-                                           _ptr(sin), _ptr(pos), dq_out.data_ptr(), dk_out.data_ptr(),
-                                           dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), B, Hq, Hk,
-                                           L, D, R, P, eps, flags, rows,
-                                           workspace.data_ptr() if need else None, need,
-                                           _stream_of(q, stream)))
+    _run(library().pdssm_qk_norm_rope_bwd, q, stream, q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(cos),
+         _ptr(sin), _ptr(pos), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _ptr(dwq),
+         _ptr(dwk), B, Hq, Hk, L, D, R, P, eps, flags, rows, workspace.data_ptr() if need else None, need)
     return dq, dk, dwq, dwk
 
 
@@ -989,9 +988,9 @@ def linear_attention(q, k, v, g=None, s0=None, *, scale: Optional[float] = None,
     (flag, B, Hk, Hv, L, Dk, Dv), rows, need = _linear_plan(
         _form(q), _form(k), _form(v), _form(g), _form(o), _form(s0), _form(s_final))
     workspace = _workspace(need, workspace, v.device)
-    check(library().pdssm_linear_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), _ptr(s0), o.data_ptr(),
-                                     _ptr(s_final), B, Hk, Hv, L, Dk, Dv, Dk ** -0.5 if scale is None else scale,
-                                     flag, rows, workspace.data_ptr(), need, _stream_of(v, stream)))
+    _run(library().pdssm_linear_fwd, v, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), _ptr(s0),
+         o.data_ptr(), _ptr(s_final), B, Hk, Hv, L, Dk, Dv, Dk ** -0.5 if scale is None else scale, flag, rows,
+         workspace.data_ptr(), need)
     return o, s_final
 
 
@@ -1044,10 +1043,9 @@ def linear_attention_bwd(q, k, v, g, do, s0=None, ds_final=None, *, scale: Optio
         _form(q), _form(k), _form(v), _form(g), _form(s0), _form(do), _form(ds_final), _form(dq), _form(dk),
         _form(dv), _form(dg), _form(ds0))
     workspace = _workspace(need, workspace, v.device)
-    check(library().pdssm_linear_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), _ptr(s0), do.data_ptr(),
-                                     _ptr(ds_final), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dg),
-                                     _ptr(ds0), B, Hk, Hv, L, Dk, Dv, Dk ** -0.5 if scale is None else scale, flag,
-                                     rows, workspace.data_ptr(), need, _stream_of(v, stream)))
+    _run(library().pdssm_linear_bwd, v, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), _ptr(s0),
+         do.data_ptr(), _ptr(ds_final), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dg), _ptr(ds0), B, Hk, Hv, L,
+         Dk, Dv, Dk ** -0.5 if scale is None else scale, flag, rows, workspace.data_ptr(), need)
     return dq, dk, dv, dg, ds0
 
 
@@ -1075,9 +1073,8 @@ def linear_attention_step(q, k, v, g, s, *, s_out: Optional[torch.Tensor] = None
         o = torch.empty_like(v)
     flag, B, Hk, Hv, Dk, Dv, rows = _linear_step_plan(_form(q), _form(k), _form(v), _form(g), _form(o), _form(s),
                                                       _form(s_out))
-    check(library().pdssm_linear_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), s.data_ptr(),
-                                      o.data_ptr(), s_out.data_ptr(), B, Hk, Hv, Dk, Dv,
-                                      Dk ** -0.5 if scale is None else scale, flag, rows, _stream_of(v, stream)))
+    _run(library().pdssm_linear_step, v, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), s.data_ptr(),
+         o.data_ptr(), s_out.data_ptr(), B, Hk, Hv, Dk, Dv, Dk ** -0.5 if scale is None else scale, flag, rows)
     return o
 
 
@@ -1180,9 +1177,8 @@ def layer_norm(x, w=None, b=None, *, residual=None, eps: float = 1e-5, p: float 
     seed, offset, rng = _seed(seed, offset)
     (flag, B, H, L, D), rows = _layer_norm_plan(_form(x), _form(w), _form(b), _form(residual), _form(y), _form(to),
                                                 _form(rng))
-    check(library().pdssm_layer_norm_fwd(x.data_ptr(), _ptr(residual), _ptr(w), _ptr(b), y.data_ptr(), _ptr(to), B,
-                                         H, L, D, eps, p, seed, offset, _ptr(rng), flag, rows,
-                                         _stream_of(x, stream)))
+    _run(library().pdssm_layer_norm_fwd, x, stream, x.data_ptr(), _ptr(residual), _ptr(w), _ptr(b), y.data_ptr(),
+         _ptr(to), B, H, L, D, eps, p, seed, offset, _ptr(rng), flag, rows)
     return y, x if h is None else h
 
 
@@ -1218,10 +1214,9 @@ def layer_norm_bwd(h, dy, w=None, *, dh=None, want_db: bool = False, eps: float 
     db = torch.empty(D, dtype=torch.float32, device=h.device) if want_db else None
     if need:
         workspace = _workspace(need, workspace, h.device)
-    check(library().pdssm_layer_norm_bwd(h.data_ptr(), dy.data_ptr(), _ptr(dh), _ptr(w), dr.data_ptr(), _ptr(to),
-                                         _ptr(dw), _ptr(db), B, H, L, D, eps, p, seed, offset, _ptr(rng), flag,
-                                         rows, workspace.data_ptr() if need else None, need,
-                                         _stream_of(h, stream)))
+    _run(library().pdssm_layer_norm_bwd, h, stream, h.data_ptr(), dy.data_ptr(), _ptr(dh), _ptr(w), dr.data_ptr(),
+         _ptr(to), _ptr(dw), _ptr(db), B, H, L, D, eps, p, seed, offset, _ptr(rng), flag, rows,
+         workspace.data_ptr() if need else None, need)
     return dr, dx, dw, db
 
 
@@ -1242,6 +1237,6 @@ def dropout(x, p: float, seed, offset: int = 0, *, residual=None, out: Optional[
     y = torch.empty_like(x) if out is None else out
     seed, offset, rng = _seed(seed, offset)
     (flag, B, H, L, D), rows = _dropout_plan(_form(x), _form(residual), _form(y), _form(rng))
-    check(library().pdssm_dropout(x.data_ptr(), _ptr(residual), y.data_ptr(), B, H, L, D, p, seed, offset,
-                                  _ptr(rng), flag, rows, _stream_of(x, stream)))
+    _run(library().pdssm_dropout, x, stream, x.data_ptr(), _ptr(residual), y.data_ptr(), B, H, L, D, p, seed, offset,
+         _ptr(rng), flag, rows)
     return y
