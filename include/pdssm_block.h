@@ -14,9 +14,11 @@
  * strides (0 among them: a fixed decay for each head), or NULL for none; one
  * whose e^g rounds to zero in fp32 (g below -104, -inf and the lowest finite
  * value among them) empties the state before the step: a new document begins.
- * Where g is positive, states and results have to be numbers that fp32 holds, e^g
- * and the products of several need not (a state of zeros stays zero); sequences
- * whose positive gates add up to more than 22 in a run of 64 steps are slower.
+ * Where g is positive, states and results (before their scale too; for the gradient
+ * of g the product of the norms of the state and its gradient) have to be numbers
+ * that fp32 holds, e^g and the products of several need not (a state of zeros stays
+ * zero); sequences whose positive gates add up to more than 60 in a run of 64 steps
+ * are slower.
  *
  * The layer norm.  For every row of D values
  *     h = residual + dropout(x)                    (residual 0 when NULL)

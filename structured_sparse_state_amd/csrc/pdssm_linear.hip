@@ -38,8 +38,9 @@
 // Growth.  Decays inside a chunk are e^(sum of g): sums above 88 are more than fp32
 // holds, and infinity times a state, a key or a value that is zero would be NaN where
 // the definition gives zero.  Where the positive gates of some chunk add up to more
-// than 22 the walk is done a second time, step by step, with factors of any size as a
-// float and a power of two.
+// than 60 the walk is done a second time, step by step, with factors of any size as a
+// float and a power of two (8 x 32 heads of 64, 4096 steps: 1.9 ms forward, 6.1 back,
+// where the others take 0.14 and 0.6).
 //
 // What bounds it: in every chunk the chain's products, one after another on the
 // state (about 3400 to 4000 clocks; 284 matrix instructions of 16 clocks each over
@@ -237,9 +238,9 @@ __device__ __forceinline__ void await_all(int *flags, int v)
     asm volatile("" ::: "memory");
 }
 
-// Walks with a chunk whose positive gates add up to more (2^32 together) are done step
-// by step.
-constexpr float kGrows = 22.f;
+// Walks with a chunk whose positive gates add up to more are done step by step.  Below
+// it, e^60 = 2^87 leaves 2^41 to what it multiplies.
+constexpr float kGrows = 60.f;
 // e^g of more leaves no number of fp32 but zero finite.
 constexpr float kMostGate = 1e4f;
 
@@ -247,29 +248,27 @@ constexpr float kMostGate = 1e4f;
 struct Growth {
     float f;
     int n;
-    __device__ __forceinline__ float of(float v) const { return n ? ldexpf(v * f, n) : v * f; }
-    __device__ __forceinline__ f32x4 of(f32x4 v) const { return f32x4{of(v[0]), of(v[1]), of(v[2]), of(v[3])}; }
+    __device__ __forceinline__ float of(float v) const { return ldexpf(v * f, n); }
 };
 
-// As decay_of, with the same bits where it is below 2^64.
+// As decay_of, of any size, to 2^-23 of itself.
 __device__ __forceinline__ Growth growth_of(float hi_i, float lo_i, float n_i, float hi_j, float lo_j, float n_j)
 {
-    const float e = (hi_i - hi_j) + (lo_i - lo_j);
-    if (n_i != n_j)
-        return {0.f, 0};
-    const float n = e > 64.f && finite(e) ? rintf(e) : 0.f;     // (below 2^20, by kMostGate)
-    return {__builtin_amdgcn_exp2f(e - n), (int)n};
+    const float e = hi_i - hi_j, n = finite(e) ? rintf(e) : 0.f;       // (below 2^20, by kMostGate)
+    return n_i == n_j ? Growth{__builtin_amdgcn_exp2f((e - n) + (lo_i - lo_j)), (int)n} : Growth{0.f, 0};
 }
 
 __device__ __forceinline__ int scalar(unsigned v) { return __builtin_amdgcn_readfirstlane((int)v); }
 
 // A chunk step by step, from its rows in LDS: the wave's columns of the state and of
 // the result.  Lane (g, i16) has rows 16 m + 4 g + r of column i16 of the state, so a
-// value of Y is a sum over the four g.
+// value of Y is a sum over the four g.  The roundings are written out: the walks with
+// and without dg have to give the same bits.
 template <int KD, bool BF16, int SL, bool BACK, int MODE>
 __device__ __forceinline__ void walk_steps(const uint16_t *s_x1, const uint16_t *s_x2, const uint16_t *s_x3, int mine, int lane,
                                            Growth own, float scale, f32x4 (&S)[KD / 16], f32x4 (&Y)[4])
 {
+#pragma clang fp contract(off)
     using T1 = typename LinLds<KD, BF16, SL>::T1;
     using T3 = typename LinLds<KD, BF16, SL>::T3;
     const int g = lane >> 4, i16 = lane & 15;
@@ -288,20 +287,20 @@ __device__ __forceinline__ void walk_steps(const uint16_t *s_x1, const uint16_t 
 #pragma unroll
             for (int m = 0; m < KD / 16; ++m) {
                 const f32x4 key = T1::four(s_x2, t, 16 * m + 4 * g);
-                if constexpr (!BACK)
-                    S[m] = now.of(S[m]);
-                S[m] += key * value;
-                if constexpr (MODE == kOut) {
-                    const f32x4 query = T1::four(s_x1, t, 16 * m + 4 * g);
-                    y += query[0] * S[m][0] + query[1] * S[m][1] + query[2] * S[m][2] + query[3] * S[m][3];
+                f32x4 query = {0.f, 0.f, 0.f, 0.f};
+                if constexpr (MODE == kOut)
+                    query = T1::four(s_x1, t, 16 * m + 4 * g);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    S[m][r] = __builtin_fmaf(key[r], value, BACK ? S[m][r] : now.of(S[m][r]));
+                    y = __builtin_fmaf(BACK ? query[r] : scale * query[r], S[m][r], y);
+                    if constexpr (BACK)
+                        S[m][r] = now.of(S[m][r]);
                 }
-                if constexpr (BACK)
-                    S[m] = now.of(S[m]);
             }
             if constexpr (MODE == kOut) {
                 y += __shfl_xor(y, 16, 64);
                 y += __shfl_xor(y, 32, 64);
-                y *= BACK ? 1.f : scale;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float v = bperm(y, 4 * g + r);
@@ -471,8 +470,10 @@ __device__ __forceinline__ int walk_pass(const LinArgs &a, const Walk &w, int se
                     Y[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int s = 0; s < NS; ++s) {
-                    if constexpr (STEPS)
-                        sf[s] = parts<NK>(S[2 * s], S[2 * s + 1]);
+                    if constexpr (STEPS) {      // (the scale first: what fp32 holds may be no more than the result)
+                        const float first = BACK ? 1.f : a.scale;
+                        sf[s] = parts<NK>(first * S[2 * s], first * S[2 * s + 1]);
+                    }
                     Frag<NK> x1[4];
 #pragma unroll
                     for (int t = 0; t < 4; ++t)
@@ -493,7 +494,7 @@ __device__ __forceinline__ int walk_pass(const LinArgs &a, const Walk &w, int se
                         v += __shfl_xor(v, 16, 64);
                         v += __shfl_xor(v, 32, 64);
                         if constexpr (STEPS)
-                            v = BACK ? grown(16 * t + i16, kC - 1).of(v) : grown(-1, 16 * t + i16).of(a.scale * v);
+                            v = (BACK ? grown(16 * t + i16, kC - 1) : grown(-1, 16 * t + i16)).of(v);
                         to[16 * t + i16] = v;     // (the four lanes of a step all write it)
                     }
                 }
@@ -518,10 +519,14 @@ __device__ __forceinline__ int walk_pass(const LinArgs &a, const Walk &w, int se
             if constexpr (MODE == kScan) {
                 const Growth now = STEPS ? grown(-1, kC - 1) : Growth{whole, 0};
                 product.f *= now.f;
-                product.n = min(product.n + now.n, 1 << 20);
+                product.n = max(min(product.n + now.n, 1 << 20), -(1 << 20));
                 if (product.f > 0x1p32f) {
                     product.f *= 0x1p-64f;
                     product.n += 64;
+                }
+                if (STEPS && product.f < 0x1p-32f) {
+                    product.f *= 0x1p64f;
+                    product.n -= 64;
                 }
             }
             if constexpr (STEPS) {
@@ -641,7 +646,7 @@ __device__ __forceinline__ int walk_pass(const LinArgs &a, const Walk &w, int se
         if constexpr (GATE != kNone)
             __builtin_amdgcn_s_setprio(2);
         const int tid = thread - kChain * 64;
-        float most = 0.f;       // (the gates' wave) the largest gate of a lane
+        float most = 0.f;       // (the gates' wave) the most that the positive gates of a chunk add up to
         struct Incoming {
             T1 t1, t2;
             T3 t3;
@@ -700,13 +705,13 @@ __device__ __forceinline__ int walk_pass(const LinArgs &a, const Walk &w, int se
             // steps that empty the state counted apart.
             float *s_vec = vecs(p);
             float now = has_steps ? gate : lane < rows_of(p) ? first_lane(gate) : 0.f;
-            if constexpr (PASS == kFast)
-                most = fmaxf(most, now);
             if constexpr (STEPS)
                 now = finite(now) ? fminf(now, kMostGate) : now;
             const bool empty = now < kEmpties;
             const double G = running_sum(empty ? 0.0 : (double)now * 1.4426950408889634);
             const float n = running_sum(empty ? 1.f : 0.f);
+            if constexpr (PASS == kFast)
+                most = fmaxf(most, running_sum(now <= __FLT_MAX__ ? fmaxf(now, 0.f) : 0.f));
             const float hi = (float)G, lo = (float)(G - (double)hi);
             const float hi1 = last_lane(hi), lo1 = last_lane(lo), n1 = last_lane(n);
             const float rise = a.scale * decay_of(hi, lo, n, 0.f, 0.f, 0.f), left = decay_of(hi1, lo1, n1, hi, lo, n);
@@ -867,23 +872,11 @@ __device__ __forceinline__ int walk_pass(const LinArgs &a, const Walk &w, int se
             }
         }
         gates_of(p1 - 1);
-        // A chunk that grows has a gate above the mean of what it grows by: only then are
-        // the gates read again and summed (a branch in the loop, whatever it holds, costs
-        // the backward 2 %).
+        // (behind the last chunk's barrier: nobody waits for the flag any more)
         if constexpr (PASS == kFast) {
-            if (mine == kGateWave && __any(most > kGrows / kC)) {
-                bool grows = false;
-                Stream again(a.g.p, b * a.g.s.b + h * a.g.s.h, a.g.s.l, c0, BACK, 1, 4);
-                for (int p = p0; p < p1; ++p) {
-                    const Chunk<false, false> cg = again.chunk<false, false>(rows_of(p), 1);
-                    again.next(true);
-                    const float g = __uint_as_float(cg.raw(cg.lane_at(lane, 0), lane, 0, 0));
-                    grows |= sum64(finite(g) ? fmaxf(g, 0.f) : 0.f) > kGrows;
-                }
-                // (behind the last chunk's barrier: nobody waits for the flag any more)
-                if (grows && lane == 0)
-                    s_help[kGateWave] = -1;
-            }
+            const bool grows = last_lane(most) > kGrows;    // (with all lanes here)
+            if (grows && lane == 0)
+                s_help[kGateWave] = -1;
         }
         lds_barrier();
         again = follows();

@@ -139,10 +139,12 @@ def test_a_tiny_state(dtype, Dk, Dv):
 
 @pytest.mark.parametrize("dtype", TYPES)
 def test_heads_that_grow(dtype):
-    """A fixed growth of every step: 0.9 a step to e^72, and beside it a decay."""
-    x = inputs(5, 2, 1, 2, 80, 64, 48, TYPES[dtype], s0=False, gates="heads")
-    x["g"] = torch.tensor([0.9, -0.1], device=DEV)
-    check(x, "heads of 0.9 and -0.1")
+    """A fixed growth of every step, 0.9 over 80 steps and 1 over 70, and beside it a
+    decay."""
+    for L, g in ((80, 0.9), (70, 1.0)):
+        x = inputs(5, 2, 1, 2, L, 64, 48, TYPES[dtype], s0=False, gates="heads")
+        x["g"] = torch.tensor([g, -0.1], device=DEV)
+        check(x, f"heads that grow by {g}")
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -164,11 +166,11 @@ def test_growth_over_segments(dtype, gate, Dk, Dv):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("spread", [0.5, 1.0, 2.0])
-@pytest.mark.parametrize("L", [150, 64 * 24 + 5])
+@pytest.mark.parametrize("L,spread", [(150, 0.5), (150, 1.0), (150, 2.0), (150, 3.0), (1541, 0.5), (1541, 1.0), (1541, 2.0)])
 def test_gates_of_both_signs(dtype, spread, L):
-    """Positive gates of a chunk add up to 13, 25 and 50 about a sum of zero; a
-    drift down keeps the longer sequence where it is."""
+    """Positive gates of a chunk add up to about 13, 25, 50 and 75 and the negative
+    ones to as much; a drift down keeps the longer sequence where it is.  (Of 3.0
+    over 1541 steps |S| |dS| reaches 3.5e39, which dg needs below 3.4e38.)"""
     x = inputs(10, 1, 1, 2, L, 64, 40, TYPES[dtype])
     gen = torch.Generator().manual_seed(11)
     x["g"] = (spread * torch.randn(1, 2, L, generator=gen) - (0.0 if L < 200 else 0.1)).to(DEV)
@@ -177,8 +179,8 @@ def test_gates_of_both_signs(dtype, spread, L):
 
 @pytest.mark.parametrize("dtype", TYPES)
 def test_growth_over_the_chunks_of_a_segment(dtype):
-    """Segments of many chunks (there are many heads), each chunk below e^22 and
-    the segment above what fp32 holds."""
+    """Segments of many chunks (there are many heads), each chunk of e^19 and the
+    segment above what fp32 holds."""
     L, H = 64 * 40, 40
     x = inputs(9, 1, H, H, L, 16, 8, TYPES[dtype])
     assert pk.pdssm_linear_workspace_bytes(1, H, H, L, 16, 8, int(dtype == "bf16")) > 256
@@ -189,6 +191,20 @@ def test_growth_over_the_chunks_of_a_segment(dtype):
     for name in ("k", "do"):
         x[name][:, :, first:last + 1] = 0
     check(x, "gates 0.3 over many chunks")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_gates_of_both_signs_over_segments(dtype):
+    """Segments of many chunks of which some grow, with states that live on: the
+    segments' decays as products of both."""
+    L, H = 64 * 40, 40
+    x = inputs(12, 1, H, H, L, 16, 24, TYPES[dtype])
+    assert pk.pdssm_linear_workspace_bytes(1, H, H, L, 16, 24, int(dtype == "bf16")) > 256
+    gen = torch.Generator().manual_seed(13)
+    g = 3.0 * torch.randn(1, H, L, generator=gen) - 1.2
+    assert (g.clamp_min(0).unflatten(2, (-1, 64)).sum(-1) > 60).float().mean() > 0.02
+    x["g"] = g.to(DEV)
+    check(x, "gates of both signs over segments")
 
 
 @pytest.mark.parametrize("dtype", TYPES)
