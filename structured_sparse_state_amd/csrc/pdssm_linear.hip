@@ -515,9 +515,7 @@ __device__ __forceinline__ int walk_pass(const LinArgs &a, const Walk &w, int se
                 if constexpr (GATE != kNone)
                     fetch(min(p + 1, p1 - 1));
             }
-            const float whole = s_vec[kWhole * kC] * gone;
-            if constexpr (MODE == kScan) {
-                const Growth now = STEPS ? grown(-1, kC - 1) : Growth{whole, 0};
+            auto decays = [&](Growth now) {
                 product.f *= now.f;
                 product.n = max(min(product.n + now.n, 1 << 20), -(1 << 20));
                 if (product.f > 0x1p32f) {
@@ -528,8 +526,10 @@ __device__ __forceinline__ int walk_pass(const LinArgs &a, const Walk &w, int se
                     product.f *= 0x1p64f;
                     product.n -= 64;
                 }
-            }
+            };
             if constexpr (STEPS) {
+                if constexpr (MODE == kScan)
+                    decays(grown(-1, kC - 1));
                 walk_steps<KD, BF16, SL, BACK, MODE>(s_x1, s_x2, s_x3, mine, lane, grown(lane - 1, lane), a.scale, S, Y);
             } else {
                 if constexpr (MODE == kOut) {
@@ -562,6 +562,9 @@ __device__ __forceinline__ int walk_pass(const LinArgs &a, const Walk &w, int se
                     }
                 }
                 // the state
+                const float whole = s_vec[kWhole * kC] * gone;
+                if constexpr (MODE == kScan)
+                    decays({whole, 0});
                 Frag<3> wx[2];
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
@@ -1131,9 +1134,13 @@ __global__ void __launch_bounds__(256) lin_step_kernel(LinStepArgs a)
     int shift = 0;
     if (a.g.p) {
         const float gate = static_cast<const float *>(a.g.p)[b * a.g.s.b + h * a.g.s.h];
-        const double e = finite(gate) ? (double)fminf(gate, kMostGate) * 1.4426950408889634 : 0.0;
-        shift = gate > 64.f ? (int)floor(e) : 0;
-        decay = shift ? __builtin_amdgcn_exp2f((float)(e - shift)) : expf(gate);
+        if (gate > 64.f && finite(gate)) {
+            const double e = (double)fminf(gate, kMostGate) * 1.4426950408889634;
+            shift = (int)e;
+            decay = __builtin_amdgcn_exp2f((float)(e - shift));
+        } else {
+            decay = expf(gate);
+        }
     }
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
