@@ -24,7 +24,8 @@
  *     h = residual + dropout(x)                    (residual 0 when NULL)
  *     y = (h - mean(h)) / sqrt(var(h) + eps) * w + b
  * with var the mean of squares about the mean, w = 1 and b = 0 when NULL.  y is
- * of h before its rounding to the storage type.
+ * of h before its rounding to the storage type.  A row's squares about its mean
+ * have to add up to a number that fp32 holds (values up to 1e17 always do).
  *
  * Dropout.  With T = round(65536 p), a value is kept, and multiplied by
  * 65536 / (65536 - T), when its 16 random bits are T or more; the others become

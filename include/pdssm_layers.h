@@ -14,6 +14,8 @@
  * and s_final is S after the last step.  g is a log decay of any sign; one
  * whose e^g rounds to zero in fp32 (g below -104, -inf and the lowest finite
  * value among them) empties the state before the step: a new document begins.
+ * Positive gates of up to 64 steps in a row have to add up to less than 88: e^g
+ * of more is infinity in fp32, and infinity times a zero NaN.
  *
  * The norm with rotation.  For every head vector x of q and k (D values):
  *     y = x / sqrt(mean(x^2) + eps) * w       (RMS), or

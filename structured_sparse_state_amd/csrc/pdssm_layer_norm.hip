@@ -16,12 +16,16 @@
 // the backward.  A team takes many rows with its weights (and the backward's sums
 // of dw and db) held in registers.
 //
-// Bytes bound all of them at the LM layer's 8 x 4096 rows of 2048, bf16, p = 0.1:
-// forward 114 us, 537 MB at 4.7 TB/s (x and the residual in, y and h out);
-// backward 143 us with its 4 us of layer_norm_sum_kernel, 671 MB at 4.7 TB/s (three
-// rows in, two out), of which the generator's second pass costs 6; dropout
-// alone 47 us, 268 MB at 5.7 TB/s.  A copy reaches 4.9 TB/s here, and 6.0
-// with two rows in for one out.
+// Bytes bound all of them at the LM layer's 8 x 4096 rows of 2048, bf16, p = 0.1, in
+// calls one behind the other: forward 115 us, 537 MB at 4.7 TB/s (x and the residual
+// in, y and h out); backward 144 us, layer_norm_sum_kernel's part in it, 671 MB at
+// 4.6 TB/s (three rows in, two out), of which the generator's second pass costs 6 (a
+// kernel trace has 152 to 161 us for the backward's and 4.5 for the sums'); dropout
+// alone 47 us, 268 MB at 5.7 TB/s.  A copy reaches 4.9 TB/s here, and 6.0 with two
+// rows in for one out.
+// Few rows leave most of the device idle, as teams are chosen by the width alone: 32
+// rows of 2048, forward, 8 workgroups, 10 us (9 without weights, 7 without residual
+// too).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -566,7 +570,7 @@ int take_rows(RowsOf &r, const void *p, const pdssm_strides *s, int n, const pds
 // Teams, so that a lane has at most four units of a row forward and two backward
 // (whose sums of dw and db take as many registers again).  8 x 4096 rows of 2048,
 // bf16: forward 114 us with 64 lanes of four units, 114 with 128 of two, 117 with 256
-// of one; backward 165, 146 and 150 (one, two and five waves to a SIMD).
+// of one; backward (with its sums) 165, 146 and 150 (one, two and five waves to a SIMD).
 int team_of(int D, bool bwd)
 {
     if (D <= 128)

@@ -39,15 +39,21 @@
 // holds, and infinity times a state, a key or a value that is zero would be NaN where
 // the definition gives zero.  Where the positive gates of some chunk add up to more
 // than 60 the walk is done a second time, step by step, with factors of any size as a
-// float and a power of two (8 x 32 heads of 64, 4096 steps: 1.9 ms forward, 6.1 back,
-// where the others take 0.14 and 0.6).
+// float and a power of two (8 x 32 heads of 64, 4096 steps: 1.9 ms forward, 5.7 back,
+// where the others take 0.15 and 0.6).
 //
-// What bounds it: in every chunk the chain's products, one after another on the
-// state (about 3400 to 4000 clocks; 284 matrix instructions of 16 clocks each over
-// the workgroup at 64 x 64), and the help waves' way from loads through LDS to M
-// (about 3500), between the same barriers.  8 x 32 heads of 64, 4096 steps, forward,
-// one decay a head: 138 us, 541 MB at 3.9 TB/s (the rows alone, staged and nothing
-// else, 75 us); 150 with gates of every step.
+// What bounds it, at 64 x 64: in every chunk the chain's products, one after another
+// on the state (about 3400 to 4000 clocks; 284 matrix instructions of 16 clocks each
+// over the workgroup), and the help waves' way from loads through LDS to M (about
+// 3500), between the same barriers.  8 x 32 heads of 64, 4096 steps, forward, one decay
+// a head: 136 to 148 us by the machine, 541 MB at 3.7 to 4.0 TB/s (the rows alone,
+// staged and nothing else, 75 us); 150 to 158 with gates of every step.
+// At 128 x 128 a chunk takes 5.8 to 6.3 us (walks of 9 chunks 52 to 57 us).  Of that
+// its matrix instructions are 1.6 us; the eight chain waves read X1, X2 and M each for
+// itself, 128, 128 and 147 KB, which at the rates of such reads alone (152, 303 and 520
+// bytes a ns) is 1.6 us more; the rest has not been taken apart.  The walk moves
+// 170 MB at 3.0 to 3.2 TB/s meanwhile; those of dQ and dV in the backward, which keep
+// the states, 979 MB at 4.5 TB/s, nearly a copy's rate.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -947,8 +953,9 @@ __global__ void __launch_bounds__(walk_threads(SL), 1) walk_kernel(LinArgs)
 // ---------------------------------------------------------------------------
 // join_kernel: the states before the segments, from the segments' decays and
 // ends: the first segment's end is whole, S_{n+1} = decay_n S_n + end_n.  A
-// thread has four values of one state; the segments follow each other (4.3 us for
-// 8 states of 128 x 128 and 32 segments, 14 for the three walks of 64 heads in two).
+// thread has four values of one state; the segments follow each other (14 us for
+// 8 states of 128 x 128 and 32 segments, 4.5 for the three walks of 64 heads in two;
+// each segment's values fetched a turn ahead 16).
 // ---------------------------------------------------------------------------
 template <int KD>
 __global__ void __launch_bounds__(256) lin_join_kernel(LinArgs a)
@@ -976,7 +983,7 @@ __global__ void __launch_bounds__(256) lin_join_kernel(LinArgs a)
 // ---------------------------------------------------------------------------
 // group_kernel: dq and dk as the sums over the value heads of their group, from
 // fp32 [B*Hv][L][pitch].  A thread has four values of a row, and nothing else to do
-// than move them: 59 us for 2 x 16 heads of 4 sequences of 4096 rows of 128 into 8,
+// than move them: 58 us for 2 x 16 heads of 4 sequences of 4096 rows of 128 into 8,
 // 336 MB at 5.7 TB/s.
 // ---------------------------------------------------------------------------
 struct GroupArgs {
@@ -1019,9 +1026,10 @@ __global__ void __launch_bounds__(256) group_kernel(GroupArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// dg from the slices' parts: of every step, or (a workgroup for each head) the
-// sum over sequences and steps, in 64 bits: 5 and 4 us at 64 heads and 4096 steps
-// and at 6 and 333, a launch's latency.
+// dg from the slices' parts: of every step (5 us for 64 heads of 4096, a launch's
+// latency), or the sum over sequences and steps, in 64 bits, by a workgroup for each
+// head, 256 values after 256: 4 us for 999 values a head, but 66 for 65536 and 710
+// for 524288, where few heads of many steps leave the device idle.
 // ---------------------------------------------------------------------------
 struct GateArgs {
     const float *part;      // [slices][B*Hv][L]
@@ -1069,7 +1077,7 @@ __global__ void __launch_bounds__(256) gate_heads_kernel(GateArgs a)
 // lin_step_kernel: one step.  A workgroup takes 32 columns of one head's state,
 // each thread four columns of every 32nd row, all rows in registers: the state
 // is read once and written once, and o falls out on the way.  Its bytes bound it:
-// 128 x 32 states of 128 x 64 take 55 us, 270 MB at 4.9 TB/s (a copy's rate); 16
+// 128 x 32 states of 128 x 64 take 56 us, 270 MB at 4.8 TB/s (a copy's rate); 16
 // states of 128 x 128 4.4 us, a launch's latency.
 // ---------------------------------------------------------------------------
 struct LinStepArgs {
@@ -1229,7 +1237,7 @@ int slice_for(int D3, int64_t walks, int64_t L, uint32_t flags)
 // How many segments the chunks of a head are cut into, walked side by side: they
 // are walked twice (once without outputs, at half the cost) and joined, so walks are
 // cut only where a launch's workgroups do not fill the device, no finer than fills
-// it, and where the chunks saved are worth the two launches more: about three chunks
+// it (129 to 255 workgroups stay whole, and up to half of the device idle), and where the chunks saved are worth the two launches more: about three chunks
 // of a bf16 forward, whose walks begin with a chunk's wait, fewer of the others.
 // Heads of 128 (fp32: 64 and 100), one sequence, us cut and whole:
 //     bf16 forward, 8 heads    256 steps 19, 18      512: 22, 28     4096: 37, 173    18000: 83, 1098
