@@ -227,6 +227,37 @@ def test_growing_steps(dtype):
         near(state, want_s, size[..., None, None], name + "'s state")
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("name,value", [("q", float("nan")), ("k", float("nan")), ("v", float("inf")), ("g", float("nan")),
+                                        ("g", float("inf"))])
+@pytest.mark.parametrize("L,at", [(200, 5), (200, 130), (64 * 24 + 5, 700)])
+def test_what_is_not_finite_beside_growth(dtype, name, value, L, at):
+    """In walks that are done step by step: from its step on, in the rows and
+    columns of the state that it reaches, and nowhere else."""
+    x = inputs(14, 2, 1, 2, L, 64, 48, TYPES[dtype])
+    x["g"][:, :, 80:84] = 40.0
+    x["g"][:, :, 80] = x["g"][:, :, 84] = NONE
+    x["k"][:, :, 80:84] = 0
+    say(f"[case] {name} = {value} at {at} of {L}")
+    o, s = pk.linear_attention(*(x[n] for n in STEPS), x["s0"])
+    y = x[name].clone()
+    y[(1, 0, at) if name == "g" else (1, 0, at, 3)] = value
+    bad, bad_s = pk.linear_attention(*({**x, name: y}[n] for n in STEPS), x["s0"])
+    torch.cuda.synchronize()
+    assert torch.isfinite(o).all() and torch.isfinite(s).all()
+    reached, state = torch.zeros_like(o, dtype=torch.bool), torch.zeros_like(s, dtype=torch.bool)
+    if name == "q":
+        reached[1, :, at] = True
+    elif name == "v":
+        reached[1, 0, at:, 3] = state[1, 0, :, 3] = True
+    else:
+        both = slice(0, 2 if name == "k" else 1)
+        reached[1, both, at:] = True
+        state[1, both, 3 if name == "k" else slice(None)] = True
+    assert torch.equal(bad[~reached], o[~reached]) and not torch.isfinite(bad[reached]).any()
+    assert torch.equal(bad_s[~state], s[~state]) and not torch.isfinite(bad_s[state]).any()
+
+
 def test_growth_in_place_reproducible_and_on_a_stream():
     """Growth with states in place, from whatever the workspace holds, on a given
     stream, captured and replayed: the same bits."""

@@ -73,3 +73,24 @@ def test_more_than_2_to_the_32_units():
     for at in (0, 1 << 20, rows - 4):
         assert torch.equal(x[at:at + 4].cpu() != 0, kept(range(at, at + 4), D, 0.5))
         assert ((x[at:at + 4] == 0) | (x[at:at + 4] == 2)).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D", [5, 1000, 16384])
+def test_rows_of_large_values(dtype, D):
+    """Values of up to 1e17, whose squares fp32 still holds the sum of."""
+    gen = torch.Generator().manual_seed(3)
+    x = (1e17 * (2 * torch.rand(7, D, generator=gen) - 1)).to(DEV, dtype)
+    x[0, 0], x[0, 1:] = 1e17, -1e17
+    dy = torch.randn(7, D, generator=gen).to(DEV, dtype)
+    say(f"[case] values of 1e17, D={D}")
+    y, _ = pk.layer_norm(x)
+    dr, _, _, _ = pk.layer_norm_bwd(x, dy)
+    torch.cuda.synchronize()
+    want, h = ref.layer_norm(x)
+    spread = (h - h.mean(-1, keepdim=True)).square().mean(-1, keepdim=True).sqrt()
+    ratio = 1 + rms(h) / spread
+    near(y, want, ratio * ratio, "y")
+    want = ref.layer_norm_bwd(x, dy)[0]
+    size = ratio * ratio * rms(dy.double().cpu()) / spread * (1 + (h - h.mean(-1, keepdim=True)).abs() / spread)
+    near(dr, want, size, "dr")
